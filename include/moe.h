@@ -15,6 +15,14 @@
  *   moe_lora_gather_bgmv     the same fold on unsorted slot-major rows (decode)
  *   moe_combine              weighted top-k combine
  *
+ * and, for serving, the operators that stand around it in a decoder's
+ * feed-forward half:
+ *
+ *   moe_add_rmsnorm_quant    residual addition and RMS norm, with E4M3 output
+ *   moe_block_fp8_gemm       E4M3 matrix product with block scales
+ *   moe_silu_mul_quant       SiLU-mul of a gate/up product, with E4M3 output
+ *   moe_few_tokens           the whole layer for at most 32 tokens, two kernels
+ *
  * Sources the semantics are restated from (cited per call below):
  *   [lora]    spark_model/layers/ops/moe_lora_grouped.rs (Atlas inference docs)
  *   [ferrum]  ferrum-kernels 0.7.7, src/backend/cuda/moe.rs
@@ -81,6 +89,9 @@ extern "C" {
 #define MOE_SPLITK_BYTES ((size_t)MOE_SPLITK_CTAS * (131072 + 16))
 #define MOE_MAX_TOPK 16
 #define MOE_MAX_LORA_RANK 64
+#define MOE_MAX_NORM_H 32768   /* widest row of moe_add_rmsnorm_quant */
+#define MOE_MAX_FEW_TOKENS 32  /* most tokens of moe_few_tokens */
+#define MOE_QUANT_GROUP 128    /* columns per E4M3 scale (and weight rows per block scale) */
 
 /* ---- element types ----------------------------------------------------------- */
 #define MOE_ACT_BF16 0
@@ -414,6 +425,99 @@ int moe_lora_gather_bgmv(const MoeExpertRoute* route, const void* x, void* base_
 int moe_combine(const void* y, int32_t act, const int32_t* pair_to_row,
                 const float* topk_weights, void* out, int32_t T, int32_t H, int32_t top_k,
                 int32_t max_padded, int32_t* err_word, void* stream);
+
+/* ---- operators around the layer (serving) -------------------------------------- */
+
+/*
+ * E4M3 codes with scales, as the next two calls write and moe_block_fp8_gemm
+ * reads them: codes uint8 [T, N] (OCP FP8: bias 7, no infinity, 0x7f / 0xff
+ * NaN), scales f32 [T, ceil(N / 128)], one per row and 128 columns (the last
+ * group may be shorter); a code stands for e4m3(code) * scale.
+ *     scale = max(max |v| / 448, 2^-126) over the group,  code = e4m3(v / scale)
+ * rounded to nearest even. A group that holds a NaN has a NaN scale and NaN
+ * codes; one that holds an infinity has an infinite scale, NaN codes where the
+ * infinities were and zeros elsewhere. v is the f32 result, not rounded to the
+ * activation type first.
+ */
+
+/*
+ * Residual addition and root-mean-square norm:
+ *     r = x + residual,   y = r / sqrt(mean_h(r^2) + eps) * weight
+ * in f32 throughout (the norm is that of the unrounded r).
+ *   x             device act [T, H]
+ *   residual      device act [T, H] or NULL (r = x)
+ *   weight        device act [H]
+ *   residual_out  device act [T, H] out or NULL: r; may be x or residual
+ *   y             device act [T, H] out or NULL: the normed rows (not x,
+ *                 residual or residual_out)
+ *   q, q_scales   device uint8 [T, H] and f32 [T, ceil(H / 128)] out, or both
+ *                 NULL: the normed rows in E4M3
+ * Requirements: y or q given; H % 8 == 0, H <= MOE_MAX_NORM_H; tensors 16-byte
+ * aligned; eps >= 0.
+ */
+int moe_add_rmsnorm_quant(const void* x, const void* residual, int32_t act, const void* weight,
+                          float eps, int32_t T, int32_t H, void* residual_out, void* y, void* q,
+                          float* q_scales, void* stream);
+
+/*
+ * SiLU-mul of a stacked gate/up product, in E4M3:
+ *     v[t, i] = g / (1 + exp(-g)) * u,   g = gate_up[t, i], u = gate_up[t, I + i]
+ *   gate_up       device act [T, 2 I]
+ *   q, q_scales   device uint8 [T, I] and f32 [T, ceil(I / 128)] out
+ * Requirements: I % 8 == 0; gate_up and q 16-byte aligned.
+ */
+int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, int32_t I, void* q,
+                       float* q_scales, void* stream);
+
+/*
+ * E4M3 matrix product with block scales:
+ *     out[m, n] = act( sum_b a_scales[m, b] * w_scales[n / 128, b]
+ *                      * sum_{k in block b} e4m3(a[m, k]) * e4m3(w[n, k])  (+ addend[m, n]) )
+ * over the blocks b of 128 contraction indices, f32 accumulation; scales are
+ * any f32 values.
+ *   a, a_scales   device uint8 [M, K] and f32 [M, ceil(K / 128)]
+ *   w, w_scales   device uint8 [N, K] and f32 [ceil(N / 128), ceil(K / 128)]
+ *   addend        device act [M, N] or NULL; may be out
+ *   out           device act [M, N] out
+ *   err_word      device i32 or NULL (MOE_DEV_ERR_TIMEOUT)
+ * Requirements: K % 16 == 0, N % 8 == 0, tensors 16-byte aligned.
+ */
+int moe_block_fp8_gemm(const void* a, const float* a_scales, const void* w, const float* w_scales,
+                       const void* addend, void* out, int32_t act, int32_t M, int32_t N, int32_t K,
+                       int32_t* err_word, void* stream);
+
+/* Bytes of device workspace moe_few_tokens needs (the SiLU-mul rows). */
+size_t moe_few_tokens_workspace_size(int32_t T, int32_t top_k, int32_t I);
+
+/*
+ * The whole expert layer for a few tokens, T <= MOE_MAX_FEW_TOKENS, in two
+ * kernels (no sort, no gather, no padding):
+ *     out[t] = act( sum_j w[t, j] * (h_tj . Wd_e),  e = ids[t, j] )
+ *     h_tj[i] = act( silu(x[t] . Wg_e[i]) * (x[t] . Wu_e[i]) )
+ * Weights stream from HBM once per touched expert; sums are f32 and the only
+ * roundings are h and out (each once).
+ *   x             device act [T, H]
+ *   logits        device f32 [T, E]: routed as by moe_route_topk_softmax (same
+ *                 ids and weights, written to topk_ids / topk_weights); or
+ *                 NULL: topk_ids / topk_weights are inputs
+ *   topk_ids      device i32 [T, top_k]; topk_weights device f32 [T, top_k].
+ *                 As inputs: an id outside [0, E) drops its pair and sets
+ *                 MOE_DEV_ERR_EXPERT_ID; an expert named twice by one token
+ *                 adds both weights
+ *   w_gate_up, w_down   host pointers to MoeWeight, as for moe_grouped_gate_up
+ *                 and moe_grouped_down
+ *   renormalize   as for moe_route_topk_softmax (with logits only)
+ *   out           device act [T, H] out (not x)
+ *   workspace     device, >= moe_few_tokens_workspace_size bytes, 16-byte
+ *                 aligned; contents need not be initialised
+ * Requirements: those of moe_grouped_gate_up and moe_grouped_down on H, I, E
+ * and the formats, and 2 I H < 2^30 weights per expert.
+ */
+int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* topk_ids,
+                   float* topk_weights, const MoeWeight* w_gate_up, const MoeWeight* w_down,
+                   int32_t T, int32_t top_k, int32_t H, int32_t I, int32_t E, int32_t renormalize,
+                   void* out, int32_t* err_word, void* workspace, size_t workspace_bytes,
+                   void* stream);
 
 /* ---- host helper ------------------------------------------------------------- */
 

@@ -1,0 +1,11 @@
+// The few-token layer on GPTQ int4 weights (few.cuh).
+#include "few.cuh"
+
+namespace moe {
+
+cudaError_t launch_few_gptq(const FewParams& p, int act, int sms, cudaStream_t st) {
+    return act == MOE_ACT_BF16 ? launch_few<MOE_W_GPTQ_INT4, MOE_ACT_BF16>(p, sms, st)
+                               : launch_few<MOE_W_GPTQ_INT4, MOE_ACT_F16>(p, sms, st);
+}
+
+}  // namespace moe

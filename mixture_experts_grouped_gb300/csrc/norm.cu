@@ -1,0 +1,243 @@
+// Row operators of the serving path that end in E4M3 codes: residual addition
+// with the root-mean-square norm, and SiLU-mul.
+#include "quant.cuh"
+
+namespace moe {
+namespace {
+
+// ---- residual addition + RMS norm (+ E4M3 output) -------------------------------
+//
+//   r = x + residual,  y = r * (1 / sqrt(mean(r^2) + eps)) * weight,
+//   per 128 columns: s = max(amax |y| / 448, 2^-126), q = e4m3(y / s)
+//
+// Everything between the loads and the stores is f32 (r is not rounded before
+// it is normed, y not before it is quantised). HBM-bound: a row is read once
+// into registers (VPT 16-byte vectors a thread), its sum of squares reduced,
+// and every output written from there. A group of 128 columns is half a warp,
+// so its maximum takes four shuffles and no shared memory.
+
+template <int ACT, int VPT>
+struct NormRow {
+    float v[VPT][8];
+    // r = x + residual of this thread's vectors; writes r; returns its sum of squares
+    __device__ __forceinline__ float load(const uint4* x, const uint4* res, uint4* res_out, int V, int first,
+                                          int step) {
+        float ss = 0.0f;
+        uint4 a[VPT], b[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * step;
+            a[j] = i < V ? x[i] : make_uint4(0u, 0u, 0u, 0u);
+            b[j] = (i < V && res) ? res[i] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * step;
+            unpack8<ACT>(a[j], v[j]);
+            if (res) {
+                float f[8];
+                unpack8<ACT>(b[j], f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[j][q] = __fadd_rn(v[j][q], f[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) ss = fmaf(v[j][q], v[j][q], ss);
+            if (res_out && i < V) res_out[i] = pack8<ACT>(v[j]);
+        }
+        return ss;
+    }
+    __device__ __forceinline__ void store(float rstd, const uint4* w, uint4* y, uint2* q, float* s, int V, int first,
+                                          int step, int lane) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = first + j * step;
+            float wv[8];
+            unpack8<ACT>(i < V ? w[i] : make_uint4(0u, 0u, 0u, 0u), wv);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * rstd * wv[k];
+            if (y && i < V) y[i] = pack8<ACT>(v[j]);
+            if (q) {
+                // lanes past the row hold NaN or 0 (0 * rstd * 0): they stay out of the maximum
+                const float sc = group_scale(amax_half_warp(i < V ? amax_bits(v[j]) : 0u));
+                if (i < V) {
+                    q[i] = e4m3x8(v[j], sc);
+                    if ((lane & (kQuantLanes - 1)) == 0) s[i / kQuantLanes] = sc;
+                }
+            }
+        }
+    }
+};
+
+struct NormParams {
+    const uint4* x;
+    const uint4* res;
+    const uint4* w;
+    uint4* res_out;
+    uint4* y;
+    uint2* q;
+    float* s;
+    float eps;
+    int T, H;
+};
+
+__device__ __forceinline__ float rms_rstd(float ss, int H, float eps) {
+    return rsqrtf(__fdiv_rn(ss, static_cast<float>(H)) + eps);
+}
+
+constexpr int kNormWarpRows = 4;
+
+// rows of up to 256 VPT columns: a warp each
+template <int ACT, int VPT>
+__global__ void __launch_bounds__(32 * kNormWarpRows) add_rmsnorm_warp_kernel(const NormParams p) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kNormWarpRows + (threadIdx.x >> 5);
+    if (t >= p.T) return;
+    const int V = p.H / 8;
+    const size_t row = static_cast<size_t>(t) * V;
+    NormRow<ACT, VPT> r;
+    float ss = r.load(p.x + row, p.res ? p.res + row : nullptr, p.res_out ? p.res_out + row : nullptr, V, lane, 32);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const int groups = (p.H + kQuantGroup - 1) / kQuantGroup;
+    r.store(rms_rstd(ss, p.H, p.eps), p.w, p.y ? p.y + row : nullptr, p.q ? p.q + row : nullptr,
+            p.q ? p.s + static_cast<size_t>(t) * groups : nullptr, V, lane, 32, lane);
+}
+
+// longer rows: a block each
+template <int ACT, int VPT>
+__global__ void __launch_bounds__(1024) add_rmsnorm_block_kernel(const NormParams p) {
+    pdl_wait();
+    __shared__ float part[32];
+    const int tid = threadIdx.x, lane = tid & 31, n = blockDim.x;
+    const int t = blockIdx.x;
+    const int V = p.H / 8;
+    const size_t row = static_cast<size_t>(t) * V;
+    NormRow<ACT, VPT> r;
+    float ss = r.load(p.x + row, p.res ? p.res + row : nullptr, p.res_out ? p.res_out + row : nullptr, V, tid, n);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    if (lane == 0) part[tid >> 5] = ss;
+    __syncthreads();
+    ss = lane < (n >> 5) ? part[lane] : 0.0f;  // every warp adds the warps' sums in the same order
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    const int groups = (p.H + kQuantGroup - 1) / kQuantGroup;
+    r.store(rms_rstd(ss, p.H, p.eps), p.w, p.y ? p.y + row : nullptr, p.q ? p.q + row : nullptr,
+            p.q ? p.s + static_cast<size_t>(t) * groups : nullptr, V, tid, n, lane);
+}
+
+template <int ACT>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
+    const int V = p.H / 8;
+    const int blocks = (p.T + kNormWarpRows - 1) / kNormWarpRows;
+    if (V <= 32) return launch_pdl(add_rmsnorm_warp_kernel<ACT, 1>, blocks, 32 * kNormWarpRows, 0, st, p);
+    if (V <= 64) return launch_pdl(add_rmsnorm_warp_kernel<ACT, 2>, blocks, 32 * kNormWarpRows, 0, st, p);
+    const int vpt = V <= 1024 ? 1 : (V <= 2048 ? 2 : 4);
+    const int threads = ((V + vpt - 1) / vpt + 31) / 32 * 32;
+    if (vpt == 1) return launch_pdl(add_rmsnorm_block_kernel<ACT, 1>, p.T, threads, 0, st, p);
+    if (vpt == 2) return launch_pdl(add_rmsnorm_block_kernel<ACT, 2>, p.T, threads, 0, st, p);
+    return launch_pdl(add_rmsnorm_block_kernel<ACT, 4>, p.T, threads, 0, st, p);
+}
+
+// ---- SiLU-mul with E4M3 output -----------------------------------------------------
+//
+//   v = g / (1 + exp(-g)) * u,  s = max(amax |v| / 448, 2^-126),  q = e4m3(v / s)
+//
+// of a [T, 2I] gate/up product (gate columns, then up). HBM-bound: 4 bytes in
+// and 1 byte out per element of [T, I]. Each thread takes 8 columns, a half
+// warp one group of 128; rows are padded to whole groups in the thread index.
+constexpr int kSiluThreads = 256;
+
+template <int ACT>
+__global__ void __launch_bounds__(kSiluThreads)
+silu_mul_quant_kernel(const uint4* __restrict__ gu, uint2* __restrict__ q, float* __restrict__ s, int T, int I) {
+    pdl_wait();
+    const int V = I / 8;                                        // vectors per row
+    const int groups = (I + kQuantGroup - 1) / kQuantGroup;
+    const int64_t group = (static_cast<int64_t>(blockIdx.x) * kSiluThreads + threadIdx.x) / kQuantLanes;
+    if (group >= static_cast<int64_t>(T) * groups) return;      // a half warp together
+    const int64_t t = group / groups;
+    const int v = static_cast<int>(group - t * groups) * kQuantLanes + (threadIdx.x & (kQuantLanes - 1));
+    float o[8];
+    uint32_t m = 0;
+    if (v < V) {
+        const uint4* row = gu + t * 2 * V;
+        float g[8], u[8];
+        unpack8<ACT>(__ldg(row + v), g);
+        unpack8<ACT>(__ldg(row + V + v), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
+        m = amax_bits(o);
+    }
+    // the two halves of a warp may part above: each reduces under its own mask
+    const uint32_t mask = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+    for (int off = kQuantLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(mask, m, off));
+    if (v < V) {
+        const float sc = group_scale(m);
+        q[t * V + v] = e4m3x8(o, sc);
+        if ((threadIdx.x & (kQuantLanes - 1)) == 0) s[group] = sc;
+    }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_add_rmsnorm_quant(const void* x, const void* residual, int32_t act, const void* weight, float eps,
+                                     int32_t T, int32_t H, void* residual_out, void* y, void* q, float* q_scales,
+                                     void* stream) {
+    const char* who = "moe_add_rmsnorm_quant";
+    MOE_REQUIRE(act == MOE_ACT_BF16 || act == MOE_ACT_F16, "%s: act=%d is neither bf16 nor fp16", who, act);
+    MOE_REQUIRE(T >= 0, "%s: T=%d is negative", who, T);
+    MOE_REQUIRE(H > 0 && H % 8 == 0, "%s: H=%d must be a positive multiple of 8", who, H);
+    MOE_REQUIRE(eps >= 0.0f, "%s: eps=%g must not be negative", who, static_cast<double>(eps));
+    if (H > MOE_MAX_NORM_H)
+        return moe::fail(MOE_ERR_UNSUPPORTED, "%s: H=%d above %d", who, H, MOE_MAX_NORM_H);
+    MOE_REQUIRE(y || q, "%s: neither y nor q is given", who);
+    MOE_REQUIRE((q == nullptr) == (q_scales == nullptr), "%s: q and q_scales go together", who);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(x && weight, "%s: NULL pointer", who);
+    MOE_REQUIRE(moe::aligned16(x) && moe::aligned16(residual) && moe::aligned16(weight) &&
+                    moe::aligned16(residual_out) && moe::aligned16(y) && moe::aligned16(q),
+                "%s: tensors must be 16-byte aligned", who);
+    MOE_REQUIRE((reinterpret_cast<uintptr_t>(q_scales) & 3u) == 0, "%s: q_scales must be 4-byte aligned", who);
+    const moe::NormParams p{static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+                            static_cast<const uint4*>(weight), static_cast<uint4*>(residual_out),
+                            static_cast<uint4*>(y), static_cast<uint2*>(q), q_scales, eps, T, H};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        act == MOE_ACT_BF16 ? moe::launch_norm<MOE_ACT_BF16>(p, st) : moe::launch_norm<MOE_ACT_F16>(p, st);
+    if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    moe::count_launch();
+    return moe::check_launch(who);
+}
+
+extern "C" int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, int32_t I, void* q, float* q_scales,
+                                  void* stream) {
+    const char* who = "moe_silu_mul_quant";
+    MOE_REQUIRE(act == MOE_ACT_BF16 || act == MOE_ACT_F16, "%s: act=%d is neither bf16 nor fp16", who, act);
+    MOE_REQUIRE(T >= 0, "%s: T=%d is negative", who, T);
+    MOE_REQUIRE(I > 0 && I % 8 == 0, "%s: I=%d must be a positive multiple of 8", who, I);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(gate_up && q && q_scales, "%s: NULL pointer", who);
+    MOE_REQUIRE(moe::aligned16(gate_up) && moe::aligned16(q), "%s: gate_up / q must be 16-byte aligned", who);
+    MOE_REQUIRE((reinterpret_cast<uintptr_t>(q_scales) & 3u) == 0, "%s: q_scales must be 4-byte aligned", who);
+    const int64_t groups = static_cast<int64_t>(T) * ((I + moe::kQuantGroup - 1) / moe::kQuantGroup);
+    constexpr int kPerBlock = moe::kSiluThreads / moe::kQuantLanes;
+    const int64_t blocks = (groups + kPerBlock - 1) / kPerBlock;
+    if (blocks > 0x7fffffff) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: T=%d x I=%d is too large", who, T, I);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const uint4* gu = static_cast<const uint4*>(gate_up);
+    uint2* qv = static_cast<uint2*>(q);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const cudaError_t e =
+        act == MOE_ACT_BF16
+            ? moe::launch_pdl(moe::silu_mul_quant_kernel<MOE_ACT_BF16>, grid, moe::kSiluThreads, 0, st, gu, qv,
+                              q_scales, T, I)
+            : moe::launch_pdl(moe::silu_mul_quant_kernel<MOE_ACT_F16>, grid, moe::kSiluThreads, 0, st, gu, qv,
+                              q_scales, T, I);
+    if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
+    moe::count_launch();
+    return moe::check_launch(who);
+}

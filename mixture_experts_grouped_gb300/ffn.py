@@ -1,0 +1,127 @@
+"""Serving-side feed-forward pieces around the expert layer.
+
+:class:`FewTokensLayer` is the expert layer for at most 32 tokens (buffers and
+one call); :class:`SharedExpert` a dense SwiGLU expert on E4M3 weights with
+block scales; :class:`FeedForward` the feed-forward half of a decoder layer
+from them: residual addition and norm, the routed experts, the shared expert
+added to them. As in :mod:`layer`, PyTorch only provides device memory and the
+stream, every step runs in libmoe.so, nothing synchronises with the host, and
+buffers are allocated once.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import layer as L
+from . import moe as M
+
+
+class FewTokensLayer:
+    """Buffers for the whole expert layer at one (T, H, I, E, k) shape, T <= 32, and its one call."""
+
+    def __init__(self, T, H, I, E, k, act, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight, device="cuda",
+                 renormalize: bool = True):
+        self.T, self.H, self.I, self.E, self.k = T, H, I, E, k
+        self.act, self.act_code = act, M.ACT_CODES[act]
+        self.w_gate_up, self.w_down, self.renormalize = w_gate_up, w_down, renormalize
+        self.topk_ids = torch.empty((T, k), dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((T, k), dtype=torch.float32, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.ws_bytes = M.moe_few_tokens_workspace_size(T, k, I)
+        self.ws = torch.empty(max(1, self.ws_bytes), dtype=torch.uint8, device=device)
+        self.out = torch.empty((T, H), dtype=L.act_dtype(act), device=device)
+
+    def forward(self, x, logits=None, stream=None):
+        """The layer on x [T, H]; returns its output buffer. Without logits the
+        routing already in ``topk_ids`` / ``topk_weights`` is used."""
+        M.moe_few_tokens(x, self.act_code, logits, self.topk_ids, self.topk_weights, self.w_gate_up.desc,
+                         self.w_down.desc, self.T, self.k, self.H, self.I, self.E, self.renormalize, self.out,
+                         self.err, self.ws, self.ws_bytes, stream)
+        return self.out
+
+
+def quant_buffers(rows: int, cols: int, device):
+    """Codes and scales of a quantised [rows, cols] tensor."""
+    g = -(-cols // M.MOE_QUANT_GROUP)
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty((rows, g), dtype=torch.float32, device=device))
+
+
+@dataclass
+class BlockFp8Weight:
+    """E4M3 codes uint8 [N, K] with f32 scales [ceil(N / 128), ceil(K / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+class SharedExpert:
+    """A dense SwiGLU expert on block-scaled E4M3 weights: gate/up product,
+    SiLU-mul, down product, optionally added to another output."""
+
+    def __init__(self, T, H, I, act, w_gate_up: BlockFp8Weight, w_down: BlockFp8Weight, device="cuda"):
+        self.T, self.H, self.I = T, H, I
+        self.act_code = M.ACT_CODES[act]
+        self.w_gate_up, self.w_down = w_gate_up, w_down
+        dt = L.act_dtype(act)
+        self.gate_up = torch.empty((T, 2 * I), dtype=dt, device=device)
+        self.q, self.q_scales = quant_buffers(T, I, device)
+        self.out = torch.empty((T, H), dtype=dt, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def forward(self, xq, xq_scales, addend=None, stream=None):
+        """The expert on quantised rows [T, H], plus ``addend`` [T, H]; returns its output buffer."""
+        M.moe_block_fp8_gemm(xq, xq_scales, self.w_gate_up.codes, self.w_gate_up.scales, None, self.gate_up,
+                             self.act_code, self.T, 2 * self.I, self.H, self.err, stream)
+        M.moe_silu_mul_quant(self.gate_up, self.act_code, self.T, self.I, self.q, self.q_scales, stream)
+        M.moe_block_fp8_gemm(self.q, self.q_scales, self.w_down.codes, self.w_down.scales, addend, self.out,
+                             self.act_code, self.T, self.H, self.I, self.err, stream)
+        return self.out
+
+
+class FeedForward:
+    """The feed-forward half of a decoder layer at one shape:
+
+        r = x + residual,  y = norm(r),  out = experts(y) + shared(e4m3(y))
+
+    ``forward`` returns (out, r), what the next layer takes. The routed experts
+    run as :class:`FewTokensLayer` up to 32 tokens and as
+    :class:`layer.MoeLayer` above; the router weight is f32 [H, E].
+    """
+
+    def __init__(self, T, H, I, E, k, act, norm_weight, w_router, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight,
+                 shared: Optional[SharedExpert] = None, eps: float = 1e-6, bs: int = 16, device="cuda",
+                 renormalize: bool = True):
+        self.T, self.H, self.E, self.k, self.eps, self.renormalize = T, H, E, k, eps, renormalize
+        self.act_code = M.ACT_CODES[act]
+        self.norm_weight, self.w_router, self.shared = norm_weight, w_router, shared
+        dt = L.act_dtype(act)
+        self.residual = torch.empty((T, H), dtype=dt, device=device)
+        self.y = torch.empty((T, H), dtype=dt, device=device)
+        self.q, self.q_scales = quant_buffers(T, H, device) if shared is not None else (None, None)
+        self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
+        if T <= M.MOE_MAX_FEW_TOKENS:
+            self.experts = FewTokensLayer(T, H, I, E, k, act, w_gate_up, w_down, device, renormalize)
+        else:
+            self.experts = L.MoeLayer(T, H, I, E, k, bs, act, w_gate_up, w_down, device, renormalize=renormalize)
+
+    def forward(self, x, residual=None, stream=None):
+        M.moe_add_rmsnorm_quant(x, residual, self.act_code, self.norm_weight, self.eps, self.T, self.H, self.residual,
+                                self.y, self.q, self.q_scales, stream)
+        ex = self.experts
+        M.moe_router_topk_softmax(self.y, self.act_code, self.w_router, self.T, self.H, self.E, self.k,
+                                  self.renormalize, self.logits, ex.topk_ids, ex.topk_weights, stream)
+        if isinstance(ex, FewTokensLayer):
+            out = ex.forward(self.y, None, stream)
+        else:
+            ex.align(stream)
+            ex.gate_up(self.y, stream)
+            ex.down(stream)
+            ex.combine(stream)
+            out = ex.out
+        if self.shared is not None:
+            out = self.shared.forward(self.q, self.q_scales, out, stream)
+        return out, self.residual

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from ctypes import c_char_p, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p, POINTER
+from ctypes import c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p, POINTER
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
@@ -19,6 +19,7 @@ MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA = 0, 1, 2, 3
 MOE_DEV_ERR_EXPERT_ID, MOE_DEV_ERR_CAPACITY, MOE_DEV_ERR_OFFSETS, MOE_DEV_ERR_PAIR_ID, MOE_DEV_ERR_TIMEOUT = (
     0x1, 0x2, 0x4, 0x8, 0x10)
 MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_LORA_RANK = 256, 16, 64
+MOE_MAX_NORM_H, MOE_MAX_FEW_TOKENS, MOE_QUANT_GROUP = 32768, 32, 128
 MOE_ACT_BF16, MOE_ACT_F16 = 0, 1
 MOE_W_BF16, MOE_W_GPTQ_INT4, MOE_W_NVFP4, MOE_W_FP8_E4M3 = 0, 1, 2, 3
 
@@ -71,6 +72,15 @@ _SIGNATURES = {
                                        c_uint32, c_uint32, c_uint32, c_void_p]),
     "moe_combine": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
                               c_void_p, c_void_p]),
+    "moe_add_rmsnorm_quant": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_float, c_int32, c_int32, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_silu_mul_quant": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+    "moe_block_fp8_gemm": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                     c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_few_tokens_workspace_size": (c_size_t, [c_int32, c_int32, c_int32]),
+    "moe_few_tokens": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, POINTER(MoeWeight),
+                                 POINTER(MoeWeight), c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p,
+                                 c_void_p, c_void_p, c_size_t, c_void_p]),
     "moe_validate_group_arrays": (c_int32, [c_char_p, c_int32, POINTER(c_int32), c_int32, POINTER(c_char_p),
                                             POINTER(c_int32), c_int32]),
 }
@@ -219,6 +229,36 @@ def moe_combine(y, act, pair_to_row, topk_weights, out, T, H, top_k, max_padded,
     _check("moe_combine", lib().moe_combine(
         _ptr(y), act, _ptr(pair_to_row), _ptr(topk_weights), _ptr(out), T, H, top_k, max_padded, _ptr(err_word),
         _stream(stream)))
+
+
+def moe_add_rmsnorm_quant(x, residual, act, weight, eps, T, H, residual_out=None, y=None, q=None, q_scales=None,
+                          stream=None):
+    _check("moe_add_rmsnorm_quant", lib().moe_add_rmsnorm_quant(
+        _ptr(x), _ptr(residual), act, _ptr(weight), eps, T, H, _ptr(residual_out), _ptr(y), _ptr(q), _ptr(q_scales),
+        _stream(stream)))
+
+
+def moe_silu_mul_quant(gate_up, act, T, I, q, q_scales, stream=None):
+    _check("moe_silu_mul_quant", lib().moe_silu_mul_quant(
+        _ptr(gate_up), act, T, I, _ptr(q), _ptr(q_scales), _stream(stream)))
+
+
+def moe_block_fp8_gemm(a, a_scales, w, w_scales, addend, out, act, M, N, K, err_word=None, stream=None):
+    _check("moe_block_fp8_gemm", lib().moe_block_fp8_gemm(
+        _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(addend), _ptr(out), act, M, N, K, _ptr(err_word),
+        _stream(stream)))
+
+
+def moe_few_tokens_workspace_size(T, top_k, I) -> int:
+    return int(lib().moe_few_tokens_workspace_size(T, top_k, I))
+
+
+def moe_few_tokens(x, act, logits, topk_ids, topk_weights, w_gate_up: MoeWeight, w_down: MoeWeight, T, top_k, H, I, E,
+                   renormalize, out, err_word, workspace, workspace_bytes, stream=None):
+    _check("moe_few_tokens", lib().moe_few_tokens(
+        _ptr(x), act, _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(w_gate_up),
+        ctypes.byref(w_down), T, top_k, H, I, E, 1 if renormalize else 0, _ptr(out), _ptr(err_word),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def moe_validate_group_arrays(who: str, num_experts: int, offsets, per_expert) -> None:
