@@ -17,8 +17,8 @@ namespace moe {
 namespace {
 
 constexpr int kBfThreads = 256, kBfWarps = kBfThreads / 32;
-constexpr int kBfRing = 8;
-constexpr int kBfSpan = 64;
+constexpr int kBfSpan = 64;   // contraction indices per unit
+constexpr int kBfRing = 8;    // stages of a warp's ring
 
 struct BfParams {
     const uint8_t* a;
@@ -30,13 +30,15 @@ struct BfParams {
     int M, N, K, kb;  // kb: scales per row
 };
 
-struct BfUnit {
-    uint4 r[2];
-    float s[2];
+// A stage: 1 KB of weights, NT tiles of tokens, the tokens' scales, two weight scales.
+template <int NT> struct BfStage {
+    static constexpr int X_AT = 1024, SA_AT = X_AT + 512 * NT, SB_AT = SA_AT + 32 * NT, BYTES = SB_AT + 16;
 };
 
 template <int ACT, int NT>
-__global__ void __launch_bounds__(kBfThreads, 2) block_fp8_rows_kernel(const BfParams p) {
+__global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfParams p) {
+    using S = BfStage<NT>;
+    extern __shared__ uint8_t bf_smem[];
     __shared__ float4 red[kBfWarps * NT * 32];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -46,111 +48,131 @@ __global__ void __launch_bounds__(kBfThreads, 2) block_fp8_rows_kernel(const BfP
     const int ms = min(8 * NT, p.M - m0);
     const int nt = (ms + 7) / 8;
     const int ntiles = (n1 - n0 + 15) / 16;
-    const int K = p.K, nk = ((K + kBfSpan - 1) / kBfSpan + kBfWarps - 1) / kBfWarps;  // steps per warp and tile
+    const int K = p.K, nks = (K + kBfSpan - 1) / kBfSpan;
+    uint8_t* ring = bf_smem + warp * kBfRing * S::BYTES;
 
-    const uint8_t* xp[NT];
+    // the warp's units: tile by tile, steps warp, warp + 8, ... of each
+    int ltile = warp < nks ? 0 : ntiles, lks = warp;
+    auto fetch = [&](int stage) {
+        if (ltile < ntiles) {
+            uint8_t* st = ring + stage * S::BYTES;
+            const int k0 = lks * kBfSpan, k = k0 + 16 * c, b = k0 / kQuantGroup;
+            const bool in = k < K;
+            const int kk = in ? k : 0;
+            const int ra = n0 + 16 * ltile + g, rb = ra + 8;
+            if (ra < n1) cp_async16_zfill(st + 16 * lane, p.w + static_cast<size_t>(ra) * K + kk, in);
+            if (rb < n1) cp_async16_zfill(st + 512 + 16 * lane, p.w + static_cast<size_t>(rb) * K + kk, in);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xp[t] = 8 * t + g < ms ? p.a + static_cast<size_t>(m0 + 8 * t + g) * K : nullptr;
-
-    BfUnit ring[kBfRing];
-    int ltile = 0, lj = 0;
-    auto fetch = [&](BfUnit& u) {
-        if (ltile >= ntiles) return;
-        const int k0 = (lj * kBfWarps + warp) * kBfSpan, k = k0 + 16 * c;
-        const int ra = n0 + 16 * ltile + g, rb = ra + 8;
-        u.r[0] = u.r[1] = make_uint4(0u, 0u, 0u, 0u);
-        u.s[0] = u.s[1] = 0.0f;
-        if (k < K && ra < n1) u.r[0] = ldg_stream16(p.w + static_cast<size_t>(ra) * K + k);
-        if (k < K && rb < n1) u.r[1] = ldg_stream16(p.w + static_cast<size_t>(rb) * K + k);
-        if (k0 < K && ra < n1) u.s[0] = __ldg(p.sb + static_cast<size_t>(ra / kQuantGroup) * p.kb + k0 / kQuantGroup);
-        if (k0 < K && rb < n1) u.s[1] = __ldg(p.sb + static_cast<size_t>(rb / kQuantGroup) * p.kb + k0 / kQuantGroup);
-        if (++lj == nk) {
-            lj = 0;
-            ++ltile;
+            for (int t = 0; t < NT; ++t)
+                if (8 * t + g < ms)
+                    cp_async16_l1(st + S::X_AT + 512 * t + 16 * lane,
+                                  p.a + static_cast<size_t>(m0 + 8 * t + g) * K + kk, in);
+            if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(m0 + lane) * p.kb + b);
+            // 16 consecutive rows lie in at most two blocks of 128
+            if (lane < 2) {
+                const int n = min(n0 + 16 * ltile + 15 * lane, n1 - 1);
+                cp_async4(st + S::SB_AT + 4 * lane, p.sb + static_cast<size_t>(n / kQuantGroup) * p.kb + b);
+            }
+            lks += kBfWarps;
+            if (lks >= nks) {
+                lks = warp;
+                ++ltile;
+            }
         }
+        cp_async_commit();
     };
-#pragma unroll
-    for (int d = 0; d < kBfRing; ++d) fetch(ring[d]);
+    for (int d = 0; d < kBfRing - 1; ++d) fetch(d);
 
-    float acc[NT][4];
+    int stage = 0;
+    for (int tile = 0; tile < ntiles; ++tile) {
+        float acc[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-    int tile = 0, j = 0;
-    while (tile < ntiles) {
+        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+        const int first_block = (n0 + 16 * tile) / kQuantGroup;
+        const bool a2 = (n0 + 16 * tile + g) / kQuantGroup != first_block;      // row g lies in the second block
+        const bool b2 = (n0 + 16 * tile + 8 + g) / kQuantGroup != first_block;  // row g + 8
+        for (int ks = warp; ks < nks; ks += kBfWarps) {
+            __syncwarp();  // every lane is done with the stage refilled now
+            fetch(stage == 0 ? kBfRing - 1 : stage - 1);
+            cp_async_wait_group<kBfRing - 1>();
+            __syncwarp();  // scales were copied by other lanes
+            const uint8_t* st = ring + stage * S::BYTES;
+            const uint4 ua = *reinterpret_cast<const uint4*>(st + 16 * lane);
+            const uint4 ub = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
+            const float* sb = reinterpret_cast<const float*>(st + S::SB_AT);
+            const float s0 = sb[a2], s1 = sb[b2];
+            uint32_t fa[8], fb[8];
+            const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
 #pragma unroll
-        for (int d = 0; d < kBfRing; ++d) {
-            if (tile >= ntiles) break;
-            const int k0 = (j * kBfWarps + warp) * kBfSpan, k = k0 + 16 * c;
-            if (k0 < K) {
-                const BfUnit& u = ring[d];
-                uint32_t fa[8], fb[8];
-                const uint32_t wa[4] = {u.r[0].x, u.r[0].y, u.r[0].z, u.r[0].w};
-                const uint32_t wb[4] = {u.r[1].x, u.r[1].y, u.r[1].z, u.r[1].w};
+            for (int i = 0; i < 4; ++i) {
+                e4m3x4_to_act<MOE_ACT_F16>(wa[i], fa[2 * i], fa[2 * i + 1]);
+                e4m3x4_to_act<MOE_ACT_F16>(wb[i], fb[2 * i], fb[2 * i + 1]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t >= nt) continue;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * t + g < ms) x = *reinterpret_cast<const uint4*>(st + S::X_AT + 512 * t + 16 * lane);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    e4m3x4_to_act<MOE_ACT_F16>(wa[i], fa[2 * i], fa[2 * i + 1]);
-                    e4m3x4_to_act<MOE_ACT_F16>(wb[i], fb[2 * i], fb[2 * i + 1]);
+                    uint32_t x0, x1;
+                    e4m3x4_to_act<MOE_ACT_F16>(xw[i], x0, x1);
+                    mma_16816<MOE_ACT_F16>(part, fa[2 * i], fb[2 * i], fa[2 * i + 1], fb[2 * i + 1], x0, x1);
                 }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t >= nt) continue;
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (xp[t] && k < K) x = __ldg(reinterpret_cast<const uint4*>(xp[t] + k));
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_act<MOE_ACT_F16>(xw[i], b0, b1);
-                        mma_16816<MOE_ACT_F16>(part, fa[2 * i], fb[2 * i], fa[2 * i + 1], fb[2 * i + 1], b0, b1);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int m = 8 * t + 2 * c + q;
-                        const float sm =
-                            m < ms ? __ldg(p.sa + static_cast<size_t>(m0 + m) * p.kb + k0 / kQuantGroup) : 0.0f;
-                        acc[t][q] = fmaf(sm * u.s[0], part[q], acc[t][q]);
-                        acc[t][2 + q] = fmaf(sm * u.s[1], part[2 + q], acc[t][2 + q]);
-                    }
-                }
+                // sums of tokens past the batch are never read, so their stale scales do no harm
+                const float2 sm = *reinterpret_cast<const float2*>(st + S::SA_AT + 32 * t + 8 * c);
+                acc[t][0] = fmaf(sm.x * s0, part[0], acc[t][0]);
+                acc[t][1] = fmaf(sm.y * s0, part[1], acc[t][1]);
+                acc[t][2] = fmaf(sm.x * s1, part[2], acc[t][2]);
+                acc[t][3] = fmaf(sm.y * s1, part[3], acc[t][3]);
             }
-            if (++j == nk) {  // the tile's contraction is complete: add the warps' sums
-                j = 0;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-                    acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-                }
-                __syncthreads();
-                for (int i = tid; i < ms * 16; i += kBfThreads) {
-                    const int m = i >> 4, r = i & 15, n = n0 + 16 * tile + r;
-                    // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8) + (m & 1)
-                    const float* src = reinterpret_cast<const float*>(red + (m >> 3) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) +
-                                       2 * (r >> 3) + (m & 1);
-                    float v = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
-                    if (n < n1) {
-                        const size_t at = static_cast<size_t>(m0 + m) * p.N + n;
-                        if (p.addend)
-                            v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
-                        reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
-                    }
-                }
-                __syncthreads();
-                ++tile;
-            }
-            fetch(ring[d]);
+            if (++stage == kBfRing) stage = 0;
         }
+        // the tile's contraction is complete: add the warps' sums
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        __syncthreads();
+        for (int i = tid; i < ms * 16; i += kBfThreads) {
+            const int m = i >> 4, r = i & 15, n = n0 + 16 * tile + r;
+            // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8) + (m & 1)
+            const float* src = reinterpret_cast<const float*>(red + (m >> 3) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) +
+                               2 * (r >> 3) + (m & 1);
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
+            if (n < n1) {
+                const size_t at = static_cast<size_t>(m0 + m) * p.N + n;
+                if (p.addend) v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
+                reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
+            }
+        }
+        __syncthreads();
     }
+}
+
+template <int ACT, int NT>
+cudaError_t launch_rows_nt(const BfParams& p, dim3 grid, cudaStream_t st) {
+    constexpr int smem = kBfWarps * kBfRing * BfStage<NT>::BYTES;
+    static int configured_for = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_for != dev) {
+        if (set_smem_limit(reinterpret_cast<const void*>(block_fp8_rows_kernel<ACT, NT>), smem) != MOE_OK)
+            return cudaGetLastError();
+        configured_for = dev;
+    }
+    return launch_pdl(block_fp8_rows_kernel<ACT, NT>, grid, kBfThreads, smem, st, p);
 }
 
 template <int ACT>
 cudaError_t launch_rows(const BfParams& p, int sms, cudaStream_t st) {
     const int gx = sms < p.N ? sms : p.N;
-    if (p.M <= 8) return launch_pdl(block_fp8_rows_kernel<ACT, 1>, dim3(gx), kBfThreads, 0, st, p);
-    if (p.M <= 16) return launch_pdl(block_fp8_rows_kernel<ACT, 2>, dim3(gx), kBfThreads, 0, st, p);
-    return launch_pdl(block_fp8_rows_kernel<ACT, 4>, dim3(gx, (p.M + 31) / 32), kBfThreads, 0, st, p);
+    if (p.M <= 8) return launch_rows_nt<ACT, 1>(p, dim3(gx), st);
+    if (p.M <= 16) return launch_rows_nt<ACT, 2>(p, dim3(gx), st);
+    return launch_rows_nt<ACT, 4>(p, dim3(gx, (p.M + 31) / 32), st);
 }
 
 }  // namespace

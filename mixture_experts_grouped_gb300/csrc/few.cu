@@ -29,6 +29,7 @@ int check_weight(const MoeWeight* w, int act, int N, int K, const char* what, co
             return MOE_OK;
         case MOE_W_NVFP4:
             MOE_REQUIRE(w->scales && w->scale2, "%s: NVFP4 needs scales and scale2", who);
+            MOE_REQUIRE(aligned16(w->scales), "%s: NVFP4 scales must be 16-byte aligned", who);
             MOE_REQUIRE(K % 32 == 0 && N % 16 == 0, "%s: NVFP4 needs K=%d %% 32 == 0 and N=%d %% 16 == 0", who, K, N);
             return MOE_OK;
         case MOE_W_FP8_E4M3:

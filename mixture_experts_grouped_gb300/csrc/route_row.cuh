@@ -15,6 +15,40 @@ __device__ __forceinline__ bool better(float va, int ia, float vb, int ib) {
     return va > vb || (va == vb && ia < ib);
 }
 
+// The weights of a row whose selection is known: lane r < k holds the r-th
+// expert si and its logit sv, m is the largest logit. Writes the row's ids and
+// weights (lanes < top_k).
+__device__ __forceinline__ void finish_row(const float (&v)[kPerLane], int lane, int E, int k, int renorm, float m,
+                                           float sv, int si, int32_t* __restrict__ ids_row,
+                                           float* __restrict__ w_row) {
+    // lane r < k holds the exponential of its selected expert: the fp64 exp is
+    // evaluated once per selected expert, in parallel across the lanes
+    const float e_mine = (lane < k) ? __double2float_rn(exp(static_cast<double>(__fsub_rn(sv, m)))) : 0.0f;
+    float denom;
+    if (renorm) {
+        denom = 0.0f;  // e_0 + e_1 + ... in rank order
+#pragma unroll
+        for (int r = 0; r < MOE_MAX_TOPK; ++r) {
+            const float er = __shfl_sync(0xffffffffu, e_mine, r);
+            if (r < k) denom = __fadd_rn(denom, er);
+        }
+    } else {
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            if (lane + 32 * j < E)
+                part = __fadd_rn(part, __double2float_rn(exp(static_cast<double>(__fsub_rn(v[j], m)))));
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) part = __fadd_rn(part, __shfl_xor_sync(0xffffffffu, part, off));
+        denom = part;
+    }
+    if (lane < k) {
+        ids_row[lane] = si;
+        w_row[lane] = __fdiv_rn(e_mine, denom);
+    }
+}
+
 // Top-k softmax of one row whose logits sit in registers: lane l holds
 // v[j] = logit of expert l + 32 j (E <= 256). Writes the row's top_k ids and
 // weights (lanes < top_k).
@@ -56,9 +90,7 @@ __device__ __forceinline__ void route_row(const float (&v)[kPerLane], int lane, 
         sel_v[r] = bv;
     }
 
-    const float m = sel_v[0];
-    // lane r < k holds the exponential of its selected expert: the fp64 exp is
-    // evaluated once per selected expert, in parallel across the lanes
+    // lane r takes the r-th selection
     float sv = 0.0f;
     int si = 0;
 #pragma unroll
@@ -67,30 +99,49 @@ __device__ __forceinline__ void route_row(const float (&v)[kPerLane], int lane, 
             sv = sel_v[q];
             si = sel_i[q];
         }
-    const float e_mine = (lane < k) ? __double2float_rn(exp(static_cast<double>(__fsub_rn(sv, m)))) : 0.0f;
-    float denom;
-    if (renorm) {
-        denom = 0.0f;  // e_0 + e_1 + ... in rank order
+    finish_row(v, lane, E, k, renorm, sel_v[0], sv, si, ids_row, w_row);
+}
+
+// The selection of route_row by integer reductions: lane r < k gets the r-th
+// expert si and its logit sv. Each round takes the largest remaining logit as
+// an order-preserving integer with one warp reduction, and the lowest index
+// that holds it with a second. Returns false, with nothing selected, for a row
+// that holds a NaN: route_row's comparisons are not an order then. (route_row
+// itself took about 8 us of a one-token layer when every CTA ran it: its 16
+// unrolled rounds of shuffles, and the fp64 exponential, which runs on few
+// units per SM.)
+__device__ __forceinline__ bool select_row(const float (&v)[kPerLane], int lane, int E, int k, float& sv, int& si) {
+    bool nan = false;
+    uint32_t key[kPerLane];
 #pragma unroll
-        for (int r = 0; r < MOE_MAX_TOPK; ++r) {
-            const float er = __shfl_sync(0xffffffffu, e_mine, r);
-            if (r < k) denom = __fadd_rn(denom, er);
-        }
-    } else {
-        float part = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) {
-            if (lane + 32 * j < E)
-                part = __fadd_rn(part, __double2float_rn(exp(static_cast<double>(__fsub_rn(v[j], m)))));
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) part = __fadd_rn(part, __shfl_xor_sync(0xffffffffu, part, off));
-        denom = part;
+    for (int j = 0; j < kPerLane; ++j) {
+        nan |= lane + 32 * j < E && v[j] != v[j];
+        const uint32_t b = __float_as_uint(__fadd_rn(v[j], 0.0f));  // -0 counts as 0
+        key[j] = lane + 32 * j < E ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;  // 0: absent or taken
     }
-    if (lane < k) {
-        ids_row[lane] = si;
-        w_row[lane] = __fdiv_rn(e_mine, denom);
+    if (__any_sync(0xffffffffu, nan)) return false;
+    sv = 0.0f;
+    si = 0;
+    for (int r = 0; r < k; ++r) {
+        uint32_t bk = 0;
+        int bi = 0;
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j)
+            if (key[j] > bk) {
+                bk = key[j];
+                bi = lane + 32 * j;
+            }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+        const int at = static_cast<int>(__reduce_min_sync(0xffffffffu, bk == top ? static_cast<uint32_t>(bi) : ~0u));
+        if (lane == r) {
+            si = at;
+            sv = __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
+        }
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j)
+            if (lane + 32 * j == at) key[j] = 0u;
     }
+    return true;
 }
 
 }  // namespace moe
