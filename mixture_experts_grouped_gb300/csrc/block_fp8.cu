@@ -9,8 +9,9 @@
 //   * Each CTA takes an equal share of the weight rows, in tiles of 16; the
 //     contraction steps of a tile are dealt to its 8 warps in turn, and the
 //     warps' sums are added through shared memory in warp order.
-//   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a; more
-//     rows than 8 NT take further blocks (grid.y), which find the weights in L2.
+//   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a.
+// More rows run on the 5th-generation tensor cores (block_fp8_tc.cu).
+#include "block_fp8.cuh"
 #include "stream.cuh"
 
 namespace moe {
@@ -19,16 +20,7 @@ namespace {
 constexpr int kBfThreads = 256, kBfWarps = kBfThreads / 32;
 constexpr int kBfSpan = 64;   // contraction indices per unit
 constexpr int kBfRing = 8;    // stages of a warp's ring
-
-struct BfParams {
-    const uint8_t* a;
-    const float* sa;
-    const uint8_t* w;
-    const float* sb;
-    const uint16_t* addend;
-    uint16_t* out;
-    int M, N, K, kb;  // kb: scales per row
-};
+constexpr int kBfRowsMost = 32;  // rows up to which this form is used
 
 // A stage: 1 KB of weights, NT tiles of tokens, the tokens' scales, two weight scales.
 template <int NT> struct BfStage {
@@ -44,8 +36,7 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n0 = static_cast<int>(static_cast<int64_t>(p.N) * blockIdx.x / gridDim.x);
     const int n1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
-    const int m0 = blockIdx.y * 8 * NT;
-    const int ms = min(8 * NT, p.M - m0);
+    const int ms = p.M;  // <= 8 NT
     const int nt = (ms + 7) / 8;
     const int ntiles = (n1 - n0 + 15) / 16;
     const int K = p.K, nks = (K + kBfSpan - 1) / kBfSpan;
@@ -66,8 +57,8 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
             for (int t = 0; t < NT; ++t)
                 if (8 * t + g < ms)
                     cp_async16_l1(st + S::X_AT + 512 * t + 16 * lane,
-                                  p.a + static_cast<size_t>(m0 + 8 * t + g) * K + kk, in);
-            if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(m0 + lane) * p.kb + b);
+                                  p.a + static_cast<size_t>(8 * t + g) * K + kk, in);
+            if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(lane) * p.kb + b);
             // 16 consecutive rows lie in at most two blocks of 128
             if (lane < 2) {
                 const int n = min(n0 + 16 * ltile + 15 * lane, n1 - 1);
@@ -144,7 +135,7 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
 #pragma unroll
             for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
             if (n < n1) {
-                const size_t at = static_cast<size_t>(m0 + m) * p.N + n;
+                const size_t at = static_cast<size_t>(m) * p.N + n;
                 if (p.addend) v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
                 reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
             }
@@ -172,7 +163,7 @@ cudaError_t launch_rows(const BfParams& p, int sms, cudaStream_t st) {
     const int gx = sms < p.N ? sms : p.N;
     if (p.M <= 8) return launch_rows_nt<ACT, 1>(p, dim3(gx), st);
     if (p.M <= 16) return launch_rows_nt<ACT, 2>(p, dim3(gx), st);
-    return launch_rows_nt<ACT, 4>(p, dim3(gx, (p.M + 31) / 32), st);
+    return launch_rows_nt<ACT, 4>(p, dim3(gx), st);
 }
 
 }  // namespace
@@ -186,20 +177,19 @@ extern "C" int moe_block_fp8_gemm(const void* a, const float* a_scales, const vo
     MOE_REQUIRE(M >= 0, "%s: M=%d is negative", who, M);
     MOE_REQUIRE(N > 0 && N % 8 == 0, "%s: N=%d must be a positive multiple of 8", who, N);
     MOE_REQUIRE(K > 0 && K % 16 == 0, "%s: K=%d must be a positive multiple of 16", who, K);
-    if (M > 65535 * 32) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: M=%d is too large", who, M);
     if (M == 0) return MOE_OK;
     MOE_REQUIRE(a && a_scales && w && w_scales && out, "%s: NULL pointer", who);
     MOE_REQUIRE(moe::aligned16(a) && moe::aligned16(w) && moe::aligned16(addend) && moe::aligned16(out),
                 "%s: a / w / addend / out must be 16-byte aligned", who);
     MOE_REQUIRE(((reinterpret_cast<uintptr_t>(a_scales) | reinterpret_cast<uintptr_t>(w_scales)) & 3u) == 0,
                 "%s: scales must be 4-byte aligned", who);
-    (void)err_word;
     const int sms = moe::sm_count();
     if (sms <= 0) return moe::fail(MOE_ERR_CUDA, "%s: no CUDA device", who);
     const moe::BfParams p{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(w), w_scales,
                           static_cast<const uint16_t*>(addend), static_cast<uint16_t*>(out), M, N, K,
                           (K + moe::kQuantGroup - 1) / moe::kQuantGroup};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M > moe::kBfRowsMost) return moe::launch_block_fp8_tc(p, act, sms, err_word, st, who);
     const cudaError_t e = act == MOE_ACT_BF16 ? moe::launch_rows<MOE_ACT_BF16>(p, sms, st)
                                               : moe::launch_rows<MOE_ACT_F16>(p, sms, st);
     if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
