@@ -258,7 +258,8 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if (CG == 2) mbar_arrive_cluster(tempty0 + buf * 8);
+                            // the reads are complete (tcgen05.wait::ld), so there is nothing to release
+                            if (CG == 2) mbar_arrive_cluster_relaxed(tempty0 + buf * 8);
                             else mbar_arrive(&s.tempty[buf]);
                         }
                     }
