@@ -46,6 +46,10 @@ int make_tmap_2d_raw(CUtensorMap* map, const void* base, CUtensorMapDataType dt,
 // Encode a 2-D map of bytes with the 128-byte swizzle: rows x cols (cols a
 // multiple of 16), box box_rows x 128.
 int make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Encode a 2-D map of 16-bit outputs for TMA stores: rows x cols, box box_rows
+// x box_cols (64 or 32), swizzled over the box's 128 or 64 bytes.
+int make_tmap_2d_out(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+                     int act);
 // Encode a plain 3-D tensor map: dims d0 (contiguous) x d1 x d2 elements,
 // byte strides s1 (between d1 steps) and s2 (between d2 steps), box
 // b0 x b1 x b2. Used to fetch two separated halves of a weight tile with one
