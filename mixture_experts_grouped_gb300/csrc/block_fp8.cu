@@ -3,13 +3,18 @@
 //     out[m, n] = sum_b sa[m, b] sb[n / 128, b] sum_{k in b} a[m, k] w[n, k]  (+ addend[m, n])
 //
 // Few rows: bound by the weight bytes, so the weights stream straight into the
-// fragments of warp-level tensor-core products (stream.cuh). E4M3 values are
-// exact in f16 and their products exact in f32; the sums of each unit of 64
-// contraction indices are scaled in f32 before they are added.
-//   * Each CTA takes an equal share of the weight rows, in tiles of 16; the
-//     contraction steps of a tile are dealt to its 8 warps in turn, and the
-//     warps' sums are added through shared memory in warp order.
-//   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a.
+// fragments of warp-level tensor-core products (see stream.cuh for the ring
+// and the free choice of k order). The products take the E4M3 codes as they
+// are (m16n8k32, f32 accumulation: exact products, and a sum of 448^2 and 31
+// terms of 2^-6 comes out exact), so nothing is converted; the f16 form of the
+// same product costs eight times as much per contraction index here, and took
+// 38 us at M = 17, N = 4096, K = 14336.
+//   * Each CTA takes an equal share of the weight rows, 32 at a time; a unit
+//     is 32 rows x one block of 128 contraction indices, whose sums are scaled
+//     in f32 before they are added. The blocks are dealt to the CTA's 8 warps
+//     in turn, and the warps' sums added through shared memory in warp order.
+//   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a, read
+//     once per unit for all its 32 weight rows.
 // More rows run on the 5th-generation tensor cores (block_fp8_tc.cu).
 #include "block_fp8.cuh"
 #include "stream.cuh"
@@ -18,122 +23,149 @@ namespace moe {
 namespace {
 
 constexpr int kBfThreads = 256, kBfWarps = kBfThreads / 32;
-constexpr int kBfSpan = 64;   // contraction indices per unit
-constexpr int kBfRing = 8;    // stages of a warp's ring
 constexpr int kBfRowsMost = 32;  // rows up to which this form is used
 
-// A stage: 1 KB of weights, NT tiles of tokens, the tokens' scales, two weight scales.
+// A stage: 4 KB of weights (32 rows x 128), NT tiles of 8 tokens, the tokens'
+// scales, two weight scales. The ring has what fits 200 KB, at most 6 stages.
 template <int NT> struct BfStage {
-    static constexpr int X_AT = 1024, SA_AT = X_AT + 512 * NT, SB_AT = SA_AT + 32 * NT, BYTES = SB_AT + 16;
+    static constexpr int X_AT = 4096, SA_AT = X_AT + 1024 * NT, SB_AT = SA_AT + 32 * NT, BYTES = SB_AT + 16;
+    static constexpr int FIT = 204800 / (kBfWarps * BYTES), RING = FIT < 6 ? FIT : 6;
 };
+
+__device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
 template <int ACT, int NT>
 __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfParams p) {
     using S = BfStage<NT>;
+    constexpr int RING = S::RING;
     extern __shared__ uint8_t bf_smem[];
-    __shared__ float4 red[kBfWarps * NT * 32];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int n0 = static_cast<int>(static_cast<int64_t>(p.N) * blockIdx.x / gridDim.x);
     const int n1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
     const int ms = p.M;  // <= 8 NT
     const int nt = (ms + 7) / 8;
-    const int ntiles = (n1 - n0 + 15) / 16;
-    const int K = p.K, nks = (K + kBfSpan - 1) / kBfSpan;
-    uint8_t* ring = bf_smem + warp * kBfRing * S::BYTES;
+    const int ntiles = (n1 - n0 + 31) / 32;
+    const int K = p.K;
+    uint8_t* ring = bf_smem + warp * RING * S::BYTES;
+    float4* red = reinterpret_cast<float4*>(bf_smem);  // [warps][2][NT][32], over the ring of a finished tile
 
-    // the warp's units: tile by tile, steps warp, warp + 8, ... of each
-    int ltile = warp < nks ? 0 : ntiles, lks = warp;
-    auto fetch = [&](int stage) {
-        if (ltile < ntiles) {
-            uint8_t* st = ring + stage * S::BYTES;
-            const int k0 = lks * kBfSpan, k = k0 + 16 * c, b = k0 / kQuantGroup;
-            const bool in = k < K;
-            const int kk = in ? k : 0;
-            const int ra = n0 + 16 * ltile + g, rb = ra + 8;
-            if (ra < n1) cp_async16_zfill(st + 16 * lane, p.w + static_cast<size_t>(ra) * K + kk, in);
-            if (rb < n1) cp_async16_zfill(st + 512 + 16 * lane, p.w + static_cast<size_t>(rb) * K + kk, in);
+    // Lane (g, c) copies and uses, of rows g, g + 8, g + 16, g + 24 and of token
+    // g of each tile, the 16-byte pieces c and c + 4 of a block's 128 codes.
+    auto fetch = [&](int stage, int tile, int b) {
+        uint8_t* st = ring + stage * S::BYTES;
+        const int k = b * kQuantGroup + 16 * c;
+        const bool in0 = k < K, in1 = k + 64 < K;
+        const int k0 = in0 ? k : 0, k1 = in1 ? k + 64 : 0;
+        const int first = n0 + 32 * tile;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (8 * t + g < ms)
-                    cp_async16_l1(st + S::X_AT + 512 * t + 16 * lane,
-                                  p.a + static_cast<size_t>(8 * t + g) * K + kk, in);
-            if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(lane) * p.kb + b);
-            // 16 consecutive rows lie in at most two blocks of 128
-            if (lane < 2) {
-                const int n = min(n0 + 16 * ltile + 15 * lane, n1 - 1);
-                cp_async4(st + S::SB_AT + 4 * lane, p.sb + static_cast<size_t>(n / kQuantGroup) * p.kb + b);
-            }
-            lks += kBfWarps;
-            if (lks >= nks) {
-                lks = warp;
-                ++ltile;
+        for (int r = 0; r < 4; ++r) {
+            const int n = first + 8 * r + g;
+            if (n < n1) {
+                const uint8_t* w = p.w + static_cast<size_t>(n) * K;
+                cp_async16_zfill(st + 1024 * r + 16 * lane, w + k0, in0);
+                cp_async16_zfill(st + 1024 * r + 512 + 16 * lane, w + k1, in1);
             }
         }
-        cp_async_commit();
-    };
-    for (int d = 0; d < kBfRing - 1; ++d) fetch(d);
-
-    int stage = 0;
-    for (int tile = 0; tile < ntiles; ++tile) {
-        float acc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-        const int first_block = (n0 + 16 * tile) / kQuantGroup;
-        const bool a2 = (n0 + 16 * tile + g) / kQuantGroup != first_block;      // row g lies in the second block
-        const bool b2 = (n0 + 16 * tile + 8 + g) / kQuantGroup != first_block;  // row g + 8
-        for (int ks = warp; ks < nks; ks += kBfWarps) {
+        for (int t = 0; t < NT; ++t) {
+            if (8 * t + g < ms) {
+                const uint8_t* a = p.a + static_cast<size_t>(8 * t + g) * K;
+                cp_async16_l1(st + S::X_AT + 1024 * t + 16 * lane, a + k0, in0);
+                cp_async16_l1(st + S::X_AT + 1024 * t + 512 + 16 * lane, a + k1, in1);
+            }
+        }
+        if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(lane) * p.kb + b);
+        // 32 consecutive rows lie in at most two blocks of 128
+        if (lane < 2) {
+            const int n = min(first + 31 * lane, n1 - 1);
+            cp_async4(st + S::SB_AT + 4 * lane, p.sb + static_cast<size_t>(n / kQuantGroup) * p.kb + b);
+        }
+    };
+
+    for (int tile = 0; tile < ntiles; ++tile) {
+        const int first = n0 + 32 * tile;
+        int lb = warp;  // the block copied next
+        for (int d = 0; d < RING - 1; ++d) {
+            if (lb < p.kb) fetch(d, tile, lb);
+            lb += kBfWarps;
+            cp_async_commit();
+        }
+        float acc[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+        // which of the two weight scales each of the lane's rows takes
+        const int border = (first / kQuantGroup + 1) * kQuantGroup - first;  // rows before the second block
+        int stage = 0;
+        for (int b = warp; b < p.kb; b += kBfWarps) {
             __syncwarp();  // every lane is done with the stage refilled now
-            fetch(stage == 0 ? kBfRing - 1 : stage - 1);
-            cp_async_wait_group<kBfRing - 1>();
+            if (lb < p.kb) fetch(stage == 0 ? RING - 1 : stage - 1, tile, lb);
+            lb += kBfWarps;
+            cp_async_commit();
+            cp_async_wait_group<RING - 1>();
             __syncwarp();  // scales were copied by other lanes
             const uint8_t* st = ring + stage * S::BYTES;
-            const uint4 ua = *reinterpret_cast<const uint4*>(st + 16 * lane);
-            const uint4 ub = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
-            const float* sb = reinterpret_cast<const float*>(st + S::SB_AT);
-            const float s0 = sb[a2], s1 = sb[b2];
-            uint32_t fa[8], fb[8];
-            const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
+            if (++stage == RING) stage = 0;
+            uint4 w[4][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e4m3x4_to_act<MOE_ACT_F16>(wa[i], fa[2 * i], fa[2 * i + 1]);
-                e4m3x4_to_act<MOE_ACT_F16>(wb[i], fb[2 * i], fb[2 * i + 1]);
-            }
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[r][i] = *reinterpret_cast<const uint4*>(st + 1024 * r + 512 * i + 16 * lane);
+            const float2 sb = *reinterpret_cast<const float2*>(st + S::SB_AT);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (t >= nt) continue;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * t + g < ms) x = *reinterpret_cast<const uint4*>(st + S::X_AT + 512 * t + 16 * lane);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (t >= nt) break;
+                uint4 x[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t x0, x1;
-                    e4m3x4_to_act<MOE_ACT_F16>(xw[i], x0, x1);
-                    mma_16816<MOE_ACT_F16>(part, fa[2 * i], fb[2 * i], fa[2 * i + 1], fb[2 * i + 1], x0, x1);
-                }
+                for (int i = 0; i < 2; ++i)
+                    x[i] = 8 * t + g < ms ? *reinterpret_cast<const uint4*>(st + S::X_AT + 1024 * t + 512 * i + 16 * lane)
+                                          : make_uint4(0u, 0u, 0u, 0u);
                 // sums of tokens past the batch are never read, so their stale scales do no harm
                 const float2 sm = *reinterpret_cast<const float2*>(st + S::SA_AT + 32 * t + 8 * c);
-                acc[t][0] = fmaf(sm.x * s0, part[0], acc[t][0]);
-                acc[t][1] = fmaf(sm.y * s0, part[1], acc[t][1]);
-                acc[t][2] = fmaf(sm.x * s1, part[2], acc[t][2]);
-                acc[t][3] = fmaf(sm.y * s1, part[3], acc[t][3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mma_e4m3_16832(part, w[2 * h][i].x, w[2 * h + 1][i].x, w[2 * h][i].y, w[2 * h + 1][i].y, x[i].x,
+                                       x[i].y);
+                        mma_e4m3_16832(part, w[2 * h][i].z, w[2 * h + 1][i].z, w[2 * h][i].w, w[2 * h + 1][i].w, x[i].z,
+                                       x[i].w);
+                    }
+                    const float s0 = 16 * h + g < border ? sb.x : sb.y, s1 = 16 * h + 8 + g < border ? sb.x : sb.y;
+                    acc[h][t][0] = fmaf(sm.x * s0, part[0], acc[h][t][0]);
+                    acc[h][t][1] = fmaf(sm.y * s0, part[1], acc[h][t][1]);
+                    acc[h][t][2] = fmaf(sm.x * s1, part[2], acc[h][t][2]);
+                    acc[h][t][3] = fmaf(sm.y * s1, part[3], acc[h][t][3]);
+                }
             }
-            if (++stage == kBfRing) stage = 0;
         }
         // the tile's contraction is complete: add the warps' sums
+        cp_async_wait_all();
+        __syncthreads();  // every warp is done with its ring
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            red[(warp * NT + t) * 32 + lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (t < nt)
+                    red[((warp * 2 + h) * NT + t) * 32 + lane] =
+                        make_float4(acc[h][t][0], acc[h][t][1], acc[h][t][2], acc[h][t][3]);
         __syncthreads();
-        for (int i = tid; i < ms * 16; i += kBfThreads) {
-            const int m = i >> 4, r = i & 15, n = n0 + 16 * tile + r;
-            // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8) + (m & 1)
-            const float* src = reinterpret_cast<const float*>(red + (m >> 3) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) +
-                               2 * (r >> 3) + (m & 1);
+        for (int i = tid; i < ms * 32; i += kBfThreads) {
+            const int m = i >> 5, r = i & 31, n = first + r;
+            // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8 & 1) + (m & 1)
+            const float* src = reinterpret_cast<const float*>(red + ((r >> 4) * NT + (m >> 3)) * 32 + 4 * (r & 7) +
+                                                              ((m & 7) >> 1)) + 2 * ((r >> 3) & 1) + (m & 1);
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
+            for (int w = 0; w < kBfWarps; ++w) v += src[w * 2 * NT * 128];
             if (n < n1) {
                 const size_t at = static_cast<size_t>(m) * p.N + n;
                 if (p.addend) v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
@@ -146,7 +178,7 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
 
 template <int ACT, int NT>
 cudaError_t launch_rows_nt(const BfParams& p, dim3 grid, cudaStream_t st) {
-    constexpr int smem = kBfWarps * kBfRing * BfStage<NT>::BYTES;
+    constexpr int smem = kBfWarps * BfStage<NT>::RING * BfStage<NT>::BYTES;
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);
