@@ -53,49 +53,80 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
     const int ntiles = (n1 - n0 + 31) / 32;
     const int K = p.K;
     uint8_t* ring = bf_smem + warp * RING * S::BYTES;
-    float4* red = reinterpret_cast<float4*>(bf_smem);  // [warps][2][NT][32], over the ring of a finished tile
+    float4* red = reinterpret_cast<float4*>(bf_smem + kBfWarps * RING * S::BYTES);  // [warps][NT][32], 16 rows' sums
 
     // Lane (g, c) copies and uses, of rows g, g + 8, g + 16, g + 24 and of token
     // g of each tile, the 16-byte pieces c and c + 4 of a block's 128 codes.
-    auto fetch = [&](int stage, int tile, int b) {
-        uint8_t* st = ring + stage * S::BYTES;
-        const int k = b * kQuantGroup + 16 * c;
-        const bool in0 = k < K, in1 = k + 64 < K;
-        const int k0 = in0 ? k : 0, k1 = in1 ? k + 64 : 0;
-        const int first = n0 + 32 * tile;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int n = first + 8 * r + g;
-            if (n < n1) {
-                const uint8_t* w = p.w + static_cast<size_t>(n) * K;
-                cp_async16_zfill(st + 1024 * r + 16 * lane, w + k0, in0);
-                cp_async16_zfill(st + 1024 * r + 512 + 16 * lane, w + k1, in1);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (8 * t + g < ms) {
-                const uint8_t* a = p.a + static_cast<size_t>(8 * t + g) * K;
-                cp_async16_l1(st + S::X_AT + 1024 * t + 16 * lane, a + k0, in0);
-                cp_async16_l1(st + S::X_AT + 1024 * t + 512 + 16 * lane, a + k1, in1);
-            }
-        }
-        if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, p.sa + static_cast<size_t>(lane) * p.kb + b);
+    const int row8 = 8 * K;  // bytes from a row to the one 8 below
+    const uint8_t* const pa = p.a + static_cast<size_t>(g) * K + 16 * c;
+    const float* const psa = p.sa + static_cast<size_t>(lane < ms ? lane : 0) * p.kb;
+    const int tiles_mine = (ms - g + 7) / 8;  // token tiles in which this lane has a token (may be 0)
+    const uint8_t* pw = nullptr;              // row g of the current tile
+    const float* psb = nullptr;               // lanes 0 and 1: the tile's first and last block scales
+    int rows_mine = 0;                        // of the lane's four rows
+    auto aim = [&](int first) {
+        pw = p.w + static_cast<size_t>(first + g) * K + 16 * c;
+        rows_mine = (n1 - first - g + 7) / 8;
         // 32 consecutive rows lie in at most two blocks of 128
-        if (lane < 2) {
-            const int n = min(first + 31 * lane, n1 - 1);
-            cp_async4(st + S::SB_AT + 4 * lane, p.sb + static_cast<size_t>(n / kQuantGroup) * p.kb + b);
+        psb = p.sb + static_cast<size_t>(min(first + 31 * (lane & 1), n1 - 1) / kQuantGroup) * p.kb;
+    };
+    auto fetch = [&](int stage, int b) {
+        uint8_t* st = ring + stage * S::BYTES;
+        const int k0 = b * kQuantGroup;
+        if (k0 + kQuantGroup <= K) {
+            uint8_t* d = st + 16 * lane;
+            const uint8_t* w = pw + k0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (r < rows_mine) {
+                    cp_async16(d + 1024 * r, w);
+                    cp_async16(d + 1024 * r + 512, w + 64);
+                }
+                w += row8;
+            }
+            const uint8_t* a = pa + k0;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t < tiles_mine) {
+                    cp_async16_l1(d + S::X_AT + 1024 * t, a, true);
+                    cp_async16_l1(d + S::X_AT + 1024 * t + 512, a + 64, true);
+                }
+                a += row8;
+            }
+        } else {  // the last block of a K that 128 does not divide: zeros past its end
+            const bool in0 = k0 + 16 * c < K, in1 = k0 + 64 + 16 * c < K;
+            const int o0 = in0 ? k0 : 0, o1 = in1 ? k0 + 64 : 0;
+            for (int r = 0; r < min(4, rows_mine); ++r) {
+                cp_async16_zfill(st + 1024 * r + 16 * lane, pw + static_cast<size_t>(r) * row8 + o0, in0);
+                cp_async16_zfill(st + 1024 * r + 512 + 16 * lane, pw + static_cast<size_t>(r) * row8 + o1, in1);
+            }
+            for (int t = 0; t < min(NT, tiles_mine); ++t) {
+                cp_async16_l1(st + S::X_AT + 1024 * t + 16 * lane, pa + static_cast<size_t>(t) * row8 + o0, in0);
+                cp_async16_l1(st + S::X_AT + 1024 * t + 512 + 16 * lane, pa + static_cast<size_t>(t) * row8 + o1, in1);
+            }
         }
+        if (lane < ms) cp_async4(st + S::SA_AT + 4 * lane, psa + b);
+        if (lane < 2) cp_async4(st + S::SB_AT + 4 * lane, psb + b);
     };
 
+    // the warp's units: blocks warp, warp + 8, ... of each tile; the copies run on into the next tile
+    int ltile = warp < p.kb ? 0 : ntiles, lb = warp;
+    if (ltile < ntiles) aim(n0);
+    auto copy_next = [&](int stage) {
+        if (ltile < ntiles) {
+            fetch(stage, lb);
+            lb += kBfWarps;
+            if (lb >= p.kb) {
+                lb = warp;
+                if (++ltile < ntiles) aim(n0 + 32 * ltile);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int d = 0; d < RING - 1; ++d) copy_next(d);
+    int stage = 0;
     for (int tile = 0; tile < ntiles; ++tile) {
         const int first = n0 + 32 * tile;
-        int lb = warp;  // the block copied next
-        for (int d = 0; d < RING - 1; ++d) {
-            if (lb < p.kb) fetch(d, tile, lb);
-            lb += kBfWarps;
-            cp_async_commit();
-        }
         float acc[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -103,12 +134,9 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
             for (int t = 0; t < NT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
         // which of the two weight scales each of the lane's rows takes
         const int border = (first / kQuantGroup + 1) * kQuantGroup - first;  // rows before the second block
-        int stage = 0;
         for (int b = warp; b < p.kb; b += kBfWarps) {
             __syncwarp();  // every lane is done with the stage refilled now
-            if (lb < p.kb) fetch(stage == 0 ? RING - 1 : stage - 1, tile, lb);
-            lb += kBfWarps;
-            cp_async_commit();
+            copy_next(stage == 0 ? RING - 1 : stage - 1);
             cp_async_wait_group<RING - 1>();
             __syncwarp();  // scales were copied by other lanes
             const uint8_t* st = ring + stage * S::BYTES;
@@ -147,38 +175,38 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                 }
             }
         }
-        // the tile's contraction is complete: add the warps' sums
-        cp_async_wait_all();
-        __syncthreads();  // every warp is done with its ring
+        // the tile's contraction is complete: add the warps' sums, 16 rows at a time
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            if (first + 16 * h >= n1) break;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 if (t < nt)
-                    red[((warp * 2 + h) * NT + t) * 32 + lane] =
+                    red[(warp * NT + t) * 32 + lane] =
                         make_float4(acc[h][t][0], acc[h][t][1], acc[h][t][2], acc[h][t][3]);
-        __syncthreads();
-        for (int i = tid; i < ms * 32; i += kBfThreads) {
-            const int m = i >> 5, r = i & 31, n = first + r;
-            // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8 & 1) + (m & 1)
-            const float* src = reinterpret_cast<const float*>(red + ((r >> 4) * NT + (m >> 3)) * 32 + 4 * (r & 7) +
-                                                              ((m & 7) >> 1)) + 2 * ((r >> 3) & 1) + (m & 1);
-            float v = 0.0f;
+            __syncthreads();
+            for (int i = tid; i < ms * 16; i += kBfThreads) {
+                const int m = i >> 4, r = i & 15, n = first + 16 * h + r;
+                // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8) + (m & 1)
+                const float* src = reinterpret_cast<const float*>(red + (m >> 3) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) +
+                                   2 * (r >> 3) + (m & 1);
+                float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kBfWarps; ++w) v += src[w * 2 * NT * 128];
-            if (n < n1) {
-                const size_t at = static_cast<size_t>(m) * p.N + n;
-                if (p.addend) v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
-                reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
+                for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
+                if (n < n1) {
+                    const size_t at = static_cast<size_t>(m) * p.N + n;
+                    if (p.addend) v += Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.addend)[at]);
+                    reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
 template <int ACT, int NT>
 cudaError_t launch_rows_nt(const BfParams& p, dim3 grid, cudaStream_t st) {
-    constexpr int smem = kBfWarps * BfStage<NT>::RING * BfStage<NT>::BYTES;
+    constexpr int smem = kBfWarps * (BfStage<NT>::RING * BfStage<NT>::BYTES + 512 * NT);
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);

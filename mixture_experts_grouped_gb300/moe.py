@@ -119,10 +119,27 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's handle of a device's current stream, looked up on first use
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream. The raw getter takes 0.3 us where building
+    torch's Stream object takes 3, a third of a small call."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+        else:
+            torch.cuda.init()
+            _raw_stream = lambda: raw(torch._C._cuda_getDevice())
+    return _raw_stream()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
