@@ -9,13 +9,15 @@
 // separate combine. Both kernels rebuild the same small plan in shared memory
 // from the ids (selecting the experts themselves when given logits): a bit
 // mask of tokens per expert (T <= 32 bits), the touched experts in ascending
-// order and, per expert, its "slots" (distinct tokens, ascending). Each CTA
-// takes an equal share of the weight rows, and each of its warps an equal,
+// order and, per expert, its "slots" (distinct tokens, ascending). An expert
+// with more slots than a unit's product takes (8 or 16) is listed again for
+// the rest, and its weights read again. Each CTA takes an equal share of the weight rows, and each of its warps an equal,
 // contiguous share of the CTA's units (stream.cuh):
-//   gate/up  rows (touched expert, i): 8 gate and the 8 up rows of the same i
+//   gate/up  rows (touched expert, i): gate rows and the up rows of the same i
 //            to a unit, so one lane holds both sums of an h element. A warp
-//            finishes an item (8 rows, the whole contraction) by itself; items
-//            cut between warps are added once, at the end, in warp order.
+//            finishes an item (16 or 32 such rows, the whole contraction) by
+//            itself; items cut between warps are added once, at the end, in
+//            warp order.
 //   down     columns [n0, n1) of every touched expert, so the weighted sum
 //            over the experts stays inside the CTA: each warp keeps its own
 //            f32 sums per token in shared memory and adds an expert's products,
@@ -37,17 +39,21 @@ constexpr int kFewPairs = MOE_MAX_FEW_TOKENS * MOE_MAX_TOPK;
 // Warps per CTA and ring stages per warp. bf16 has next to nothing to convert:
 // 8 warps keep up, and a CTA of each kernel fits an SM, so the down kernel's
 // start hides behind the gate/up kernel's end. The quantised formats are bound
-// by the instructions of their conversion and want all the warps of an SM.
+// by the instructions of their conversion and want all the warps of an SM
+// (GPTQ's wide gate/up items want registers more than warps: 11).
 template <int FMT> struct FewShape {
-    static constexpr int WARPS = FMT == MOE_W_BF16 ? 8 : 15;
-    static constexpr int RING = FMT == MOE_W_BF16 ? 7 : (FMT == MOE_W_GPTQ_INT4 ? 8 : 6);
-    static constexpr int RESIDENT = FMT == MOE_W_BF16 ? 2 : 1;  // CTAs per SM the registers must allow
+    static constexpr bool DENSE = FMT == MOE_W_BF16, GPTQ = FMT == MOE_W_GPTQ_INT4;
+    static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
+    static constexpr int GU_RING = DENSE || GPTQ ? 4 : (FMT == MOE_W_FP8_E4M3 ? 5 : 4);
+    static constexpr int DN_RING = DENSE ? 4 : (FMT == MOE_W_FP8_E4M3 ? 5 : 8);
+    static constexpr int RESIDENT = DENSE ? 2 : 1;  // CTAs per SM the registers must allow
 };
+constexpr int kFewEntries = MOE_MAX_EXPERTS + kFewPairs / 8;
 
 struct FewPlan {
-    int n;                              // touched experts
-    int te[MOE_MAX_EXPERTS];            // touched experts, ascending
-    int start[MOE_MAX_EXPERTS + 1];     // first slot of each
+    int n;                              // entries: touched experts, ascending, split
+    int te[kFewEntries];                // expert of each
+    int start[kFewEntries + 1];         // first slot of each
     uint32_t mask[MOE_MAX_EXPERTS];     // by expert id: tokens routed to it
     int first[MOE_MAX_EXPERTS];         // by expert id: first slot
     int ids[kFewPairs];
@@ -64,9 +70,9 @@ static __device__ __noinline__ void route_row_nan(const float* lrow, int lane, i
     route_row(v, lane, E, k, renorm, ids, w);
 }
 
-// Everything of the plan but the weights; THREADS threads, all of them here.
-// `publish`: this CTA reports bad ids.
-template <int THREADS>
+// Everything of the plan but the weights; THREADS threads, all of them here;
+// at most SLOTS slots an entry. `publish`: this CTA reports bad ids.
+template <int THREADS, int SLOTS>
 __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool publish) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.T * p.k;
@@ -95,11 +101,11 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
         else if (publish) set_err(p.err, MOE_DEV_ERR_EXPERT_ID);
     }
     __syncthreads();
-    // prefix sums over the experts: touched experts in the high half, slots in the low
+    // prefix sums over the experts: entries in the high half, slots in the low
     uint32_t m = 0, mine = 0, inc = 0;
     if (tid < MOE_MAX_EXPERTS) {
         m = s.mask[tid];
-        inc = mine = (m ? 1u << 16 : 0u) + __popc(m);
+        inc = mine = ((__popc(m) + SLOTS - 1) / SLOTS << 16) + __popc(m);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
@@ -111,10 +117,10 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
     if (tid < MOE_MAX_EXPERTS) {
         uint32_t before = inc - mine;
         for (int w = 0; w < warp; ++w) before += s.scan[w];
-        if (m) {
-            s.te[before >> 16] = tid;
-            s.start[before >> 16] = before & 0xffffu;
-            s.first[tid] = before & 0xffffu;
+        s.first[tid] = before & 0xffffu;
+        for (int j = 0; j < __popc(m); j += SLOTS) {
+            s.te[(before >> 16) + j / SLOTS] = tid;
+            s.start[(before >> 16) + j / SLOTS] = (before & 0xffffu) + j;
         }
         if (tid == MOE_MAX_EXPERTS - 1) {
             const uint32_t all = before + mine;
@@ -167,17 +173,17 @@ __device__ __forceinline__ void publish_routing(const FewParams& p, int t, int s
 // ---- gate/up ----------------------------------------------------------------------
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__((FewShape<FMT>::WARPS + 1) * 32, FewShape<FMT>::RESIDENT)
+__global__ void __launch_bounds__((FewShape<FMT>::GU_WARPS + 1) * 32, FewShape<FMT>::RESIDENT)
 few_gate_up_kernel(const FewParams p) {
-    using U = Unit<FMT, ACT>;
+    using U = Unit<FMT, ACT, true>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT>::RING, W = FewShape<FMT>::WARPS;
+    constexpr int RING = FewShape<FMT>::GU_RING, W = FewShape<FMT>::GU_WARPS, MT = U::MT, ROWS = U::ROWS;
     extern __shared__ uint8_t few_smem[];
-    float4* cut = reinterpret_cast<float4*>(few_smem + W * RING * S::BYTES);  // [W][2][NT][32]: sums of cut items
+    float4* cut = reinterpret_cast<float4*>(few_smem + W * RING * S::BYTES);  // [W][2][MT][NT][32]: sums of cut items
     __shared__ FewPlan s;
     pdl_wait();
     pdl_launch_next();
-    build_plan<(W + 1) * 32>(s, p, blockIdx.x == 0);
+    build_plan<(W + 1) * 32, 8 * NT>(s, p, blockIdx.x == 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (warp == W) {  // beside the products: the routing outputs, one row per CTA
         if (p.logits) publish_routing(p, blockIdx.x, gridDim.x, lane);
@@ -185,148 +191,163 @@ few_gate_up_kernel(const FewParams p) {
         return;
     }
     const int I = p.I, K = p.H;
-    const int64_t rows = static_cast<int64_t>(s.n) * I;  // row = touched index * I + i
-    const int r0 = static_cast<int>(rows * blockIdx.x / gridDim.x);
-    const int r1 = static_cast<int>(rows * (blockIdx.x + 1) / gridDim.x);
+    const int64_t shares = static_cast<int64_t>(s.n) * (I / U::ALIGN);  // row = entry * I + i
+    const int r0 = static_cast<int>(shares * blockIdx.x / gridDim.x) * U::ALIGN;
+    const int r1 = static_cast<int>(shares * (blockIdx.x + 1) / gridDim.x) * U::ALIGN;
     const int nk = (K + U::SPAN - 1) / U::SPAN;
-    // items: up to 8 consecutive rows of one expert
-    const int ti0 = r0 / I, i0 = r0 - ti0 * I, per = (I + 7) / 8;
-    const int f_rows = min(r1 - r0, I - i0), f_items = (f_rows + 7) / 8;
-    const int rest = r1 - r0 - f_rows, last = rest % I;
-    const int64_t units = static_cast<int64_t>(f_items + rest / I * per + (last + 7) / 8) * nk;
+    // items: up to ROWS consecutive rows of one entry
+    const int ti0 = r0 / I, i0 = r0 - ti0 * I, per = (I + ROWS - 1) / ROWS;
+    const int f_rows = min(r1 - r0, I - i0), f_items = (f_rows + ROWS - 1) / ROWS;
+    const int rest = r1 - r0 - f_rows;
+    const int64_t units = static_cast<int64_t>(f_items + rest / I * per + (rest % I + ROWS - 1) / ROWS) * nk;
     auto first_unit = [&](int w) { return static_cast<int>(units * w / W); };
     auto locate = [&](int q, int& ti, int& i) {  // item q of the CTA
         if (q < f_items) {
             ti = ti0;
-            i = i0 + 8 * q;
+            i = i0 + ROWS * q;
         } else {
             ti = ti0 + 1 + (q - f_items) / per;
-            i = 8 * ((q - f_items) % per);
+            i = ROWS * ((q - f_items) % per);
         }
     };
     auto row_end = [&](int ti) { return min(I, r1 - ti * I); };
+    auto next_item = [&](int& ti, int& i) {
+        i += ROWS;
+        if (i >= row_end(ti)) {
+            i = 0;
+            ++ti;
+        }
+    };
     const int u0 = first_unit(warp), u1 = first_unit(warp + 1);
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
 
-    // where the copies are
-    int lleft = u1 - u0, lks = u0 % nk, lti, li;
-    bool laim = true;
+    // The copies: units left in the warp's share and in the item, contraction
+    // indices to its end
+    int l_left = u1 - u0, l_item = 0, l_k = (u0 % nk) * U::SPAN, l_kleft = 0, lti, li;
     locate(u0 / nk, lti, li);
     typename U::Src src;
     const uint16_t* lx = nullptr;
+    bool l_has = false;
     auto fetch = [&](int stage) {
-        if (lleft > 0) {
-            if (laim) {
+        if (l_left > 0) {
+            if (l_item == 0) {
                 const WBase b = expert_base<FMT>(p.gu.w, p.gu.scales, p.gu.zeros, 2 * I, K, p.gu.group_size, s.te[lti]);
-                const int cnt = min(8, row_end(lti) - li);
-                src.aim(b, UnitRows{li, cnt, I + li, cnt}, lane);
+                const int cnt = min(ROWS, row_end(lti) - li);
+                src.aim(b, li, cnt, I + li, cnt, l_k, lane);
+                l_kleft = K - l_k;
+                l_item = (l_kleft + U::SPAN - 1) / U::SPAN;
                 if (U::X_RING) {
                     const int slot = s.start[lti] + g;
-                    lx = slot < s.start[lti + 1] ? p.x + static_cast<size_t>(s.slot_tok[slot]) * K + U::k_of(0, c)
-                                                 : nullptr;
+                    l_has = slot < s.start[lti + 1];
+                    if (l_has) lx = p.x + static_cast<size_t>(s.slot_tok[slot]) * K + l_k + U::k_of(0, c);
                 }
-                laim = false;
+                l_k = 0;
+                next_item(lti, li);
             }
             uint8_t* st = ring + stage * S::BYTES;
-            const int k0 = lks * U::SPAN;
-            const bool tail = k0 + U::SPAN > K;
-            src.load(st, k0, K, tail, lane);
-            if (U::X_RING) Tokens<U>::copy(st + S::X_AT, lx, k0, K, tail, lane);
-            --lleft;
-            if (++lks == nk) {
-                lks = 0;
-                laim = true;
-                li += 8;
-                if (li >= row_end(lti)) {
-                    li = 0;
-                    ++lti;
-                }
+            if (l_kleft >= U::SPAN) src.load(st, lane);
+            else src.load_tail(st, l_kleft, lane);
+            src.step();
+            if (U::X_RING) {
+                Tokens<U>::copy(st + S::X_AT, lx, l_has, l_kleft, lane);
+                lx += U::SPAN;
             }
+            l_kleft -= U::SPAN;
+            --l_item;
+            --l_left;
         }
         cp_async_commit();
     };
     for (int d = 0; d < RING - 1; ++d) fetch(d);
 
     // writes the h elements of an item's finished sums
-    auto finish = [&](const float (&acc)[NT][4], int ti, int i) {
-        const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, e = s.te[ti];
-        if (i + g >= row_end(ti)) return;
-        const float gs2 = FMT == MOE_W_NVFP4 ? __ldg(p.gu.scale2 + e) : 1.0f;
-        const float us2 = FMT == MOE_W_NVFP4 ? __ldg(p.gu.scale2 + p.E + e) : 1.0f;
+    auto finish = [&](const float (&acc)[MT][NT][4], int ti, int i) {
+        const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, e = s.te[ti], end = row_end(ti);
+        const float gs2 = FMT == MOE_W_NVFP4 ? U::SCALE_UP * __ldg(p.gu.scale2 + e) : 1.0f;
+        const float us2 = FMT == MOE_W_NVFP4 ? U::SCALE_UP * __ldg(p.gu.scale2 + p.E + e) : 1.0f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < MT; ++m) {
+            const int row = i + U::row_a(m, g);
+            if (row >= end) continue;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int slot = 8 * t + 2 * c + q;
-                if (slot < ns) {
-                    const float gs = gs2 * acc[t][q], us = us2 * acc[t][2 + q];
-                    const float v = __fdividef(gs, 1.0f + __expf(-gs)) * us;
-                    reinterpret_cast<typename Act<ACT>::T*>(p.h)[static_cast<size_t>(s0 + slot) * I + i + g] =
-                        Act<ACT>::from_f(v);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int slot = 8 * t + 2 * c + q;
+                    if (slot < ns) {
+                        const float gs = gs2 * acc[m][t][q], us = us2 * acc[m][t][2 + q];
+                        const float v = __fdividef(gs, 1.0f + __expf(-gs)) * us;
+                        reinterpret_cast<typename Act<ACT>::T*>(p.h)[static_cast<size_t>(s0 + slot) * I + row] =
+                            Act<ACT>::from_f(v);
+                    }
                 }
-            }
+        }
     };
 
-    float acc[NT][4];
+    float acc[MT][NT][4];
     int left = u1 - u0, ks = u0 % nk, stage = 0, ti, i;
     locate(u0 / nk, ti, i);
     while (left > 0) {
-        const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = (ns + 7) / 8;
-        const int cnt = min(8, row_end(ti) - i), begin = ks, end = min(nk, ks + left);
-        const UnitRows rows_u{i, cnt, I + i, cnt};
-        const uint16_t* xp[NT];
+        const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = NT > 1 && ns > 8 ? 2 : 1;
+        const int end = row_end(ti), begin = ks, stop = min(nk, ks + left);
+        const bool has = g < ns, has1 = NT > 1 && 8 + g < ns;
+        const uint16_t* x0 = p.x + ks * U::SPAN + U::k_of(0, c);
+        const uint16_t* x1 = has1 ? x0 + static_cast<size_t>(s.slot_tok[s0 + 8 + g]) * K : x0;
+        if (has) x0 += static_cast<size_t>(s.slot_tok[s0 + g]) * K;
+        Tokens<U> x;
+        x.clear();
+        float f[MT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int q = 8 * t + g;
-            xp[t] = q < ns ? p.x + static_cast<size_t>(s.slot_tok[s0 + q]) * K + U::k_of(0, c) : nullptr;
-            acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+        for (int m = 0; m < MT; ++m) {
+            f[m][0] = f[m][1] = 1.0f;
+            if (U::ROW_SCALE && i + U::row_a(m, g) < end) {
+                const float* sc =
+                    static_cast<const float*>(p.gu.scales) + static_cast<size_t>(2 * I) * s.te[ti] + i + U::row_a(m, g);
+                f[m][0] = __ldg(sc);
+                f[m][1] = __ldg(sc + I);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t][0] = acc[m][t][1] = acc[m][t][2] = acc[m][t][3] = 0.0f;
         }
-        float f0 = 1.0f, f1 = 1.0f;
-        if (U::ROW_SCALE && g < cnt) {
-            const float* sc = static_cast<const float*>(p.gu.scales) + static_cast<size_t>(2 * I) * s.te[ti] + i + g;
-            f0 = __ldg(sc);
-            f1 = __ldg(sc + I);
-        }
-        for (; ks < end; ++ks) {
-            const int k0 = ks * U::SPAN;
-            const bool tail = k0 + U::SPAN > K;
-            Tokens<U> x;
-            if (!U::X_RING) x.fetch(xp[0], k0, K, tail, lane);
+        int kleft = K - ks * U::SPAN;
+        for (; ks < stop; ++ks) {
+            if (!U::X_RING) x.fetch(x0, has, kleft, lane);
             __syncwarp();  // every lane is done with the stage refilled now
             fetch(stage == 0 ? RING - 1 : stage - 1);
             cp_async_wait_group<RING - 1>();
             __syncwarp();  // scales were copied by other lanes
             const uint8_t* st = ring + stage * S::BYTES;
-            U u;
-            u.open(st, rows_u, lane);
-            if (U::X_RING) x.open(st + S::X_AT, xp[0], lane);
-            unit_mma<U, ACT, NT>(u, x, xp, nt, k0, K, tail, lane, acc);
             if (++stage == RING) stage = 0;
+            U u;
+            u.open(st, i, I + i, lane);
+            if (U::X_RING) x.open(st + S::X_AT, has, lane);
+            unit_mma<U, ACT, NT>(u, x, x1, has1, nt, kleft, lane, acc);
+            x0 += U::SPAN;
+            x1 += U::SPAN;
+            kleft -= U::SPAN;
         }
-        left -= end - begin;
+        left -= stop - begin;
         if (U::ROW_SCALE) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                acc[t][0] *= f0;
-                acc[t][1] *= f0;
-                acc[t][2] *= f1;
-                acc[t][3] *= f1;
-            }
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[m][t][q] *= f[m][q >> 1];
         }
-        if (begin == 0 && end == nk) {
+        if (begin == 0 && stop == nk) {
             finish(acc, ti, i);
         } else {
-            float4* dst = cut + (warp * 2 + (begin == 0)) * NT * 32 + lane;
+            float4* dst = cut + (warp * 2 + (begin == 0)) * MT * NT * 32 + lane;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (t < nt) dst[t * 32] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t < nt)
+                        dst[(m * NT + t) * 32] = make_float4(acc[m][t][0], acc[m][t][1], acc[m][t][2], acc[m][t][3]);
         }
         ks = 0;
-        i += 8;
-        if (i >= row_end(ti)) {
-            i = 0;
-            ++ti;
-        }
+        next_item(ti, i);
     }
     __syncthreads();
     // The items cut between warps: the first warp that starts inside an item adds
@@ -334,30 +355,27 @@ few_gate_up_kernel(const FewParams p) {
     if (warp == 0 || u0 >= units || u0 % nk == 0 || first_unit(warp - 1) > u0 / nk * nk) return;
     const int q = u0 / nk, q_end = (q + 1) * nk;
     locate(q, ti, i);
-    const int nt = (s.start[ti + 1] - s.start[ti] + 7) / 8;
-    const float4* src0 = cut + ((warp - 1) * 2 + 1) * NT * 32 + lane;
+    const int nt = NT > 1 && s.start[ti + 1] - s.start[ti] > 8 ? 2 : 1;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const float4 v = t < nt ? src0[t * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        acc[t][0] = v.x;
-        acc[t][1] = v.y;
-        acc[t][2] = v.z;
-        acc[t][3] = v.w;
-    }
-    for (int w = warp; w < W; ++w) {
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t][0] = acc[m][t][1] = acc[m][t][2] = acc[m][t][3] = 0.0f;
+    for (int w = warp - 1; w < W; ++w) {
         const int from = first_unit(w), to = first_unit(w + 1);
         if (from >= q_end) break;
         if (from == to) continue;
-        const float4* more = cut + w * 2 * NT * 32 + lane;
+        const float4* part = cut + (w * 2 + (w < warp)) * MT * NT * 32 + lane;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (t < nt) {
-                const float4 v = more[t * 32];
-                acc[t][0] += v.x;
-                acc[t][1] += v.y;
-                acc[t][2] += v.z;
-                acc[t][3] += v.w;
-            }
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (t < nt) {
+                    const float4 v = part[(m * NT + t) * 32];
+                    acc[m][t][0] += v.x;
+                    acc[m][t][1] += v.y;
+                    acc[m][t][2] += v.z;
+                    acc[m][t][3] += v.w;
+                }
     }
     finish(acc, ti, i);
 }
@@ -386,155 +404,166 @@ __device__ __noinline__ void few_tile_end(float* sums, uint16_t* out, int T, int
 }
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__(FewShape<FMT>::WARPS * 32, FewShape<FMT>::RESIDENT)
+__global__ void __launch_bounds__(FewShape<FMT>::DN_WARPS * 32, FewShape<FMT>::RESIDENT)
 few_down_kernel(const FewParams p) {
-    using U = Unit<FMT, ACT>;
+    using U = Unit<FMT, ACT, false>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT>::RING, W = FewShape<FMT>::WARPS;
+    constexpr int RING = FewShape<FMT>::DN_RING, W = FewShape<FMT>::DN_WARPS;
     extern __shared__ uint8_t few_smem[];
     float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][17]: sums of 16 columns
     __shared__ FewPlan s;
     // before the wait: only what was complete before the gate/up kernel started
     // (logits, or ids given as inputs) and the weights
-    build_plan<W * 32>(s, p, false);
+    build_plan<W * 32, 8 * NT>(s, p, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
-    const int n0 = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
-    const int n1 = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
+    const int64_t shares = p.H / U::ALIGN;
+    const int n0 = static_cast<int>(shares * blockIdx.x / gridDim.x) * U::ALIGN;
+    const int n1 = static_cast<int>(shares * (blockIdx.x + 1) / gridDim.x) * U::ALIGN;
     const int ntiles = (n1 - n0 + 15) / 16;
     const int nks = (K + U::SPAN - 1) / U::SPAN;
     float* mine = sums + warp * p.T * 17;
     for (int i = tid; i < W * p.T * 17; i += W * 32) sums[i] = 0.0f;
 
-    // A tile's units (touched expert, contraction step): this warp's share is the same in every tile
+    // A tile's units (entry, contraction step): this warp's share is the same in every tile
     const int64_t units = static_cast<int64_t>(n) * nks;
     const int u0 = static_cast<int>(units * warp / W), count = static_cast<int>(units * (warp + 1) / W) - u0;
     const int ti_first = u0 / nks, ks_first = u0 - ti_first * nks;
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
 
-    // where the copies are
-    int ltile = count > 0 ? 0 : ntiles, lti = ti_first, lks = ks_first, lleft = count;
-    bool laim = true;
+    // The copies: where they are, units left in the tile's share and of the
+    // entry, contraction indices to its end
+    struct Pos {
+        int tile, ti, k, left, of_entry, kleft;
+    };
+    const Pos start{count > 0 ? 0 : ntiles, ti_first, ks_first * U::SPAN, count, 0, 0};
+    Pos l = start;
     typename U::Src src;
-    auto fetch_w = [&](int stage) {
-        if (laim) {
-            const WBase b = expert_base<FMT>(p.down.w, p.down.scales, p.down.zeros, p.H, K, p.down.group_size, s.te[lti]);
-            const int a = n0 + 16 * ltile;
-            src.aim(b, UnitRows{a, n1 - a, a + 8, n1 - a - 8}, lane);
-            laim = false;
-        }
-        const int k0 = lks * U::SPAN;
-        src.load(ring + stage * S::BYTES, k0, K, k0 + U::SPAN > K, lane);
+    const uint16_t* lx = nullptr;
+    bool l_has = false;
+    // moves on by a unit; true where a new entry begins
+    auto enter = [&](Pos& q) {
+        if (q.of_entry > 0) return false;
+        q.kleft = K - q.k;
+        q.of_entry = (q.kleft + U::SPAN - 1) / U::SPAN;
+        return true;
     };
-    auto fetch_h = [&](int stage, int ti, int ks) {
-        const int slot = s.start[ti] + g, k0 = ks * U::SPAN;
-        Tokens<U>::copy(ring + stage * S::BYTES + S::X_AT,
-                        slot < s.start[ti + 1] ? p.h + static_cast<size_t>(slot) * K + U::k_of(0, c) : nullptr, k0, K,
-                        k0 + U::SPAN > K, lane);
-    };
-    auto advance = [&]() {
-        if (++lks == nks) {
-            lks = 0;
-            ++lti;
-            laim = true;
+    auto advance = [&](Pos& q) {
+        q.kleft -= U::SPAN;
+        if (--q.of_entry == 0) {
+            q.k = 0;
+            ++q.ti;
         }
-        if (--lleft == 0) {
-            ++ltile;
-            lti = ti_first;
-            lks = ks_first;
-            lleft = count;
-            laim = true;
+        if (--q.left == 0) {
+            q.left = count;
+            q.ti = ti_first;
+            q.k = ks_first * U::SPAN;
+            q.of_entry = 0;
+            ++q.tile;
         }
     };
-    for (int d = 0; d < RING - 1 && ltile < ntiles; ++d) {
-        fetch_w(d);
-        advance();
+    auto fetch_w = [&](uint8_t* st, Pos& q) {
+        if (enter(q)) {
+            const WBase b = expert_base<FMT>(p.down.w, p.down.scales, p.down.zeros, p.H, K, p.down.group_size, s.te[q.ti]);
+            const int a = n0 + 16 * q.tile;
+            src.aim(b, a, n1 - a, a + 8, n1 - a - 8, q.k, lane);
+        }
+        if (q.kleft >= U::SPAN) src.load(st, lane);
+        else src.load_tail(st, q.kleft, lane);
+        src.step();
+    };
+    auto fetch_h = [&](uint8_t* st, int ti, int kleft, bool entered) {
+        if (entered) {
+            const int slot = s.start[ti] + g;
+            l_has = slot < s.start[ti + 1];
+            if (l_has) lx = p.h + static_cast<size_t>(slot) * K + (K - kleft) + U::k_of(0, c);
+        }
+        Tokens<U>::copy(st + S::X_AT, lx, l_has, kleft, lane);
+        lx += U::SPAN;
+    };
+    for (int d = 0; d < RING - 1 && l.tile < ntiles; ++d) {
+        fetch_w(ring + d * S::BYTES, l);
+        advance(l);
     }
     pdl_wait();  // h and the routing outputs are complete
     slot_weights<W * 32>(s, p);
     {
-        int tile = count > 0 ? 0 : ntiles, ti = ti_first, ks = ks_first, left = count;
+        Pos q = start;
         for (int d = 0; d < RING - 1; ++d) {
-            if (U::X_RING && tile < ntiles) {
-                fetch_h(d, ti, ks);
-                if (++ks == nks) {
-                    ks = 0;
-                    ++ti;
-                }
-                if (--left == 0) {
-                    ++tile;
-                    ti = ti_first;
-                    ks = ks_first;
-                    left = count;
-                }
+            if (U::X_RING && q.tile < ntiles) {
+                const bool entered = enter(q);
+                fetch_h(ring + d * S::BYTES, q.ti, q.kleft, entered);
+                advance(q);
             }
             cp_async_commit();
         }
     }
     __syncthreads();  // the slots' weights, and the sums are zero
 
-    float acc[NT][4];
+    float acc[1][NT][4];
     int stage = 0;
     for (int tile = 0; tile < ntiles; ++tile) {
         const int a = n0 + 16 * tile;
-        const UnitRows rows_u{a, n1 - a, a + 8, n1 - a - 8};
         int left = count, ti = ti_first, ks = ks_first;
-        while (left > 0) {  // one expert's units
-            const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = (ns + 7) / 8, e = s.te[ti];
-            const int end = min(nks, ks + left);
-            left -= end - ks;
-            const uint16_t* xp[NT];
+        while (left > 0) {  // one entry's units
+            const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = NT > 1 && ns > 8 ? 2 : 1, e = s.te[ti];
+            const int stop = min(nks, ks + left);
+            left -= stop - ks;
+            const bool has = g < ns, has1 = NT > 1 && 8 + g < ns;
+            const uint16_t* x0 = p.h + static_cast<size_t>(s0 + (has ? g : 0)) * K + ks * U::SPAN + U::k_of(0, c);
+            const uint16_t* x1 = has1 ? x0 + static_cast<size_t>(8) * K : x0;
+            Tokens<U> x;
+            x.clear();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int q = 8 * t + g;
-                xp[t] = q < ns ? p.h + static_cast<size_t>(s0 + q) * K + U::k_of(0, c) : nullptr;
-                acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-            }
-            float f0 = 1.0f, f1 = 1.0f;
+            for (int t = 0; t < NT; ++t) acc[0][t][0] = acc[0][t][1] = acc[0][t][2] = acc[0][t][3] = 0.0f;
+            const int ra = U::row_a(0, g), rb = U::row_b(g);
+            float f0 = U::SCALE_UP, f1 = U::SCALE_UP;
             if (U::ROW_SCALE) {
-                const float* sc = static_cast<const float*>(p.down.scales) + static_cast<size_t>(p.H) * e + a + g;
-                f0 = a + g < n1 ? __ldg(sc) : 0.0f;
-                f1 = a + 8 + g < n1 ? __ldg(sc + 8) : 0.0f;
+                const float* sc = static_cast<const float*>(p.down.scales) + static_cast<size_t>(p.H) * e + a;
+                f0 = a + ra < n1 ? __ldg(sc + ra) : 0.0f;
+                f1 = a + rb < n1 ? __ldg(sc + rb) : 0.0f;
             }
-            if (FMT == MOE_W_NVFP4) f0 = f1 = __ldg(p.down.scale2 + e);
-            for (; ks < end; ++ks) {
-                const int k0 = ks * U::SPAN;
-                const bool tail = k0 + U::SPAN > K;
-                Tokens<U> x;
-                if (!U::X_RING) x.fetch(xp[0], k0, K, tail, lane);
+            if (FMT == MOE_W_NVFP4) f0 = f1 = U::SCALE_UP * __ldg(p.down.scale2 + e);
+            int kleft = K - ks * U::SPAN;
+            for (; ks < stop; ++ks) {
+                if (!U::X_RING) x.fetch(x0, has, kleft, lane);
                 __syncwarp();  // every lane is done with the stage refilled now
-                if (ltile < ntiles) {
-                    const int st = stage == 0 ? RING - 1 : stage - 1;
-                    fetch_w(st);
-                    if (U::X_RING) fetch_h(st, lti, lks);
-                    advance();
+                if (l.tile < ntiles) {
+                    uint8_t* st = ring + (stage == 0 ? RING - 1 : stage - 1) * S::BYTES;
+                    const bool entered = l.of_entry == 0;
+                    fetch_w(st, l);
+                    if (U::X_RING) fetch_h(st, l.ti, l.kleft, entered);
+                    advance(l);
                 }
                 cp_async_commit();
                 cp_async_wait_group<RING - 1>();
                 __syncwarp();  // scales were copied by other lanes
                 const uint8_t* st = ring + stage * S::BYTES;
-                U u;
-                u.open(st, rows_u, lane);
-                if (U::X_RING) x.open(st + S::X_AT, xp[0], lane);
-                unit_mma<U, ACT, NT>(u, x, xp, nt, k0, K, tail, lane, acc);
                 if (++stage == RING) stage = 0;
+                U u;
+                u.open(st, a, a + 8, lane);
+                if (U::X_RING) x.open(st + S::X_AT, has, lane);
+                unit_mma<U, ACT, NT>(u, x, x1, has1, nt, kleft, lane, acc);
+                x0 += U::SPAN;
+                x1 += U::SPAN;
+                kleft -= U::SPAN;
             }
-            // leave the expert: add its products, times the weights, to the tokens' sums
+            // leave the entry: add its products, times the weights, to the tokens' sums
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (t > 0 && t >= nt) break;
+                if (t > 0 && nt <= t) break;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int slot = 8 * t + 2 * c + q;
                     if (slot < ns) {
-                        float* dst = mine + s.slot_tok[s0 + slot] * 17 + g;
+                        float* dst = mine + s.slot_tok[s0 + slot] * 17;
                         const float w = s.slot_w[s0 + slot];
-                        dst[0] = fmaf(w, f0 * acc[t][q], dst[0]);
-                        dst[8] = fmaf(w, f1 * acc[t][2 + q], dst[8]);
+                        dst[ra] = fmaf(w, f0 * acc[0][t][q], dst[ra]);
+                        dst[rb] = fmaf(w, f1 * acc[0][t][2 + q], dst[rb]);
                     }
                 }
             }
-            __syncwarp();  // another lane adds to the same token's sums for the next expert
+            __syncwarp();  // another lane adds to the same token's sums for the next entry
             ks = 0;
             ++ti;
         }
@@ -544,10 +573,14 @@ few_down_kernel(const FewParams p) {
 
 template <int FMT, int ACT, int NT>
 cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
-    constexpr int W = FewShape<FMT>::WARPS;
-    constexpr int ring = W * FewShape<FMT>::RING * Stage<Unit<FMT, ACT>>::BYTES;
-    constexpr int gu_smem = ring + static_cast<int>(sizeof(float4)) * 2 * W * NT * 32;
-    constexpr int dn_most = ring + static_cast<int>(sizeof(float)) * W * 8 * NT * 17;
+    using F = FewShape<FMT>;
+    using GU = Unit<FMT, ACT, true>;
+    using DN = Unit<FMT, ACT, false>;
+    constexpr int gu_smem =
+        F::GU_WARPS * (F::GU_RING * Stage<GU>::BYTES + static_cast<int>(sizeof(float4)) * 2 * GU::MT * NT * 32);
+    constexpr int dn_ring = F::DN_WARPS * F::DN_RING * Stage<DN>::BYTES;
+    constexpr int dn_most = dn_ring + static_cast<int>(sizeof(float)) * F::DN_WARPS * (NT == 1 ? 8 : 32) * 17;
+    static_assert(gu_smem + sizeof(FewPlan) <= 232448 && dn_most + sizeof(FewPlan) <= 232448, "shared memory");
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -557,17 +590,17 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
             return cudaGetLastError();
         configured_for = dev;
     }
-    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (W + 1) * 32, gu_smem, st, p);
+    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::GU_WARPS + 1) * 32, gu_smem, st, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(few_down_kernel<FMT, ACT, NT>, sms < p.H ? sms : p.H, W * 32,
-                      ring + sizeof(float) * W * p.T * 17, st, p);
+    const int cols = p.H / DN::ALIGN;
+    return launch_pdl(few_down_kernel<FMT, ACT, NT>, sms < cols ? sms : cols, F::DN_WARPS * 32,
+                      dn_ring + sizeof(float) * F::DN_WARPS * p.T * 17, st, p);
 }
 
+// up to 8 tokens: one token tile; more: two, and experts of over 16 tokens are listed twice
 template <int FMT, int ACT>
 cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t st) {
-    if (p.T <= 8) return launch_few_nt<FMT, ACT, 1>(p, sms, st);
-    if (p.T <= 16) return launch_few_nt<FMT, ACT, 2>(p, sms, st);
-    return launch_few_nt<FMT, ACT, 4>(p, sms, st);
+    return p.T <= 8 ? launch_few_nt<FMT, ACT, 1>(p, sms, st) : launch_few_nt<FMT, ACT, 2>(p, sms, st);
 }
 
 }  // namespace moe

@@ -12,13 +12,13 @@
 // g + 8, and the products use them as their (2c, 2c + 1) and (2c + 8, 2c + 9)
 // slots; the token operand takes the same k range of token g.
 //
-// A "unit" is what a warp takes at a time: 16 rows x SPAN contraction indices.
-// Units arrive by cp.async in a ring of shared-memory stages private to the
-// warp. Each lane copies what it will itself read (only scales cross lanes),
-// so a stage needs no barrier beyond the warp's own, and what is in flight
-// takes no registers. (The same ring in registers ran at a fifth of HBM's
-// rate: loads and conversions kept the ring's registers from staying in
-// flight.)
+// A "unit" is what a warp takes at a time: one or several 16-row tiles x SPAN
+// contraction indices, 1 to 2 KB of weights. Units arrive by cp.async in a
+// ring of shared-memory stages private to the warp. Each lane copies what it
+// will itself read (only scales cross lanes), so a stage needs no barrier
+// beyond the warp's own, and what is in flight takes no registers. (The same
+// ring in registers ran at a fifth of HBM's rate: loads and conversions kept
+// the ring's registers from staying in flight.)
 #pragma once
 
 #include "gemm_dequant.cuh"
@@ -96,151 +96,212 @@ __device__ __forceinline__ WBase expert_base(const void* w, const void* sc, cons
     return b;
 }
 
-// Two sets of up to 8 weight rows: a, a + 1, ... (lane groups g < na) and b, ... (g < nb).
-struct UnitRows {
-    int a, na, b, nb;
-};
-
-// Unit<FMT, ACT>: one format's stage layout and fragments.
-//   SPAN       contraction indices per unit
-//   CHUNKS     pieces of 8 contraction indices a lane holds per row
+// Unit<FMT, ACT, GU>: one format's stage layout and fragments, for the gate/up
+// kernel (GU: set a holds gate rows, set b the up rows of the same columns) or
+// the down kernel (both sets are rows of one 16-row tile).
+//   MT         16-row tiles per unit; SPAN contraction indices; CHUNKS pieces
+//              of 8 contraction indices a lane holds per row
+//   ROWS       rows per set a and item (GU), rows of a tile (down)
+//   ALIGN      first rows are multiples of it
+//   row_a / row_b   which rows lane group g has in tile m (row_b: down only)
 //   BYTES      weights and scales of a unit in a stage
 //   X_RING     the first token tile's values ride in the stage too (formats
 //              whose conversion is too short to hide their latency)
 //   X_PERM     the token operand's 8 values go in the order 0,4,1,5,2,6,3,7
-//   GROUPED    a unit's sums are scaled (row_scale) before they are added
-//   Src        where a lane copies from: set to an expert's rows by aim(), then
-//              load() copies the unit at contraction index k0
+//   GROUPED    sums of 64 contraction indices are scaled (scale) before they
+//              are added to the others
+//   SCALE_UP   the sums come out divided by it
+//   Src        where a lane copies from: aim() sets it to an expert's rows at
+//              a contraction index, load() copies a unit, step() moves on
 //   open       reads a stage's words and scales into registers
-//   frag(i)    piece i of both rows as the A operands of two products
+//   frag(i, m) piece i of both sets of tile m as A operands of two products
 // Copies past the contraction's end are filled with zeros (the token operand
 // too); a row past the unit's rows is not copied: it only feeds sums that
 // nobody reads.
-template <int FMT, int ACT> struct Unit;
+template <int FMT, int ACT, bool GU> struct Unit;
 
-// rows of K contiguous elements of EB bits, 16 bytes of each row and lane
-template <int EB> struct RowSrc {
+// Rows of K contiguous elements of EB bits: per lane and row KT times 16 bytes.
+template <int EB, int MT, int KT> struct RowSrc {
+    static constexpr int STEP = 512 / EB;  // contraction indices of one 16-byte piece of the four lanes
     const uint8_t* pa;
     const uint8_t* pb;
-    bool va, vb;
-    int kc;  // the lane's first contraction index within a unit
-    __device__ __forceinline__ void aim(const WBase& b, const UnitRows& u, int lane) {
-        const int g = lane >> 2;
-        kc = (lane & 3) * (128 / EB);
-        va = g < u.na;
-        vb = g < u.nb;
-        pa = b.w + (static_cast<size_t>(u.a + g) * b.K + kc) * EB / 8;
-        pb = b.w + (static_cast<size_t>(u.b + g) * b.K + kc) * EB / 8;
+    int na, nb, row8;  // tiles in which the lane's rows exist; bytes from a row to the 8th below it
+    __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
+        const int g = lane >> 2, k = k0 + (lane & 3) * (128 / EB);
+        na = (n_a - g + 7) >> 3;
+        nb = (n_b - g + 7) >> 3;
+        row8 = b.K * EB;
+        pa = b.w + (static_cast<size_t>(a + g) * b.K + k) * EB / 8;
+        pb = b.w + (static_cast<size_t>(bb + g) * b.K + k) * EB / 8;
     }
-    __device__ __forceinline__ void load(uint8_t* st, int k0, int K, bool tail, int lane) const {
-        const int off = k0 * EB / 8;
-        if (!tail) {
-            if (va) cp_async16(st + 16 * lane, pa + off);
-            if (vb) cp_async16(st + 512 + 16 * lane, pb + off);
-        } else {
-            const bool in = k0 + kc < K;  // a skipped copy reads nothing, but its address stays the row's own
-            if (va) cp_async16_zfill(st + 16 * lane, pa + (in ? off : 0), in);
-            if (vb) cp_async16_zfill(st + 512 + 16 * lane, pb + (in ? off : 0), in);
+    __device__ __forceinline__ void load(uint8_t* st, int lane) const {
+        uint8_t* d = st + 16 * lane;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (m < na)
+#pragma unroll
+                for (int t = 0; t < KT; ++t) cp_async16(d + (2 * m * KT + t) * 512, pa + m * row8 + t * 64);
+            if (m < nb)
+#pragma unroll
+                for (int t = 0; t < KT; ++t) cp_async16(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + t * 64);
         }
+    }
+    __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const {  // `left` indices to K's end
+        uint8_t* d = st + 16 * lane;
+        for (int t = 0; t < KT; ++t) {
+            const bool in = t * STEP + (lane & 3) * (128 / EB) < left;
+            const int o = in ? t * 64 : -16 * (lane & 3);  // a skipped copy reads nothing: the unit's first piece stands in
+            for (int m = 0; m < MT; ++m) {
+                if (m < na) cp_async16_zfill(d + (2 * m * KT + t) * 512, pa + m * row8 + o, in);
+                if (m < nb) cp_async16_zfill(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + o, in);
+            }
+        }
+    }
+    __device__ __forceinline__ void step() {
+        pa += 64 * KT;
+        pb += 64 * KT;
     }
 };
 
-template <int ACT> struct Unit<MOE_W_BF16, ACT> {
-    static constexpr int SPAN = 32, CHUNKS = 1, BYTES = 1024;
+template <int ACT, bool GU> struct Unit<MOE_W_BF16, ACT, GU> {
+    static constexpr int MT = GU ? 2 : 1, KT = GU ? 1 : 2, SPAN = 32 * KT, CHUNKS = KT, BYTES = 2048;
+    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
     static constexpr bool X_RING = true, X_PERM = false, GROUPED = false, ROW_SCALE = false;
-    struct Src : RowSrc<16> {};
-    uint4 r[2];
-    __device__ __forceinline__ void open(const uint8_t* st, const UnitRows&, int lane) {
-        r[0] = *reinterpret_cast<const uint4*>(st + 16 * lane);
-        r[1] = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
-    }
-    static __device__ __forceinline__ int k_of(int, int c) { return 8 * c; }
-    __device__ __forceinline__ void frag(int, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        a[0] = r[0].x; a[1] = r[0].y; a[2] = r[0].z; a[3] = r[0].w;
-        b[0] = r[1].x; b[1] = r[1].y; b[2] = r[1].z; b[3] = r[1].w;
-    }
-    __device__ __forceinline__ float row_scale(int) const { return 1.0f; }
-};
-
-template <int ACT> struct Unit<MOE_W_FP8_E4M3, ACT> {
-    static constexpr int SPAN = 64, CHUNKS = 2, BYTES = 1024;
-    static constexpr bool X_RING = false, X_PERM = false, GROUPED = false, ROW_SCALE = true;
-    struct Src : RowSrc<8> {};
-    uint4 r[2];
-    __device__ __forceinline__ void open(const uint8_t* st, const UnitRows&, int lane) {
-        r[0] = *reinterpret_cast<const uint4*>(st + 16 * lane);
-        r[1] = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
-    }
-    static __device__ __forceinline__ int k_of(int i, int c) { return 16 * c + 8 * i; }
-    __device__ __forceinline__ void frag(int i, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        e4m3x4_to_act<ACT>(i ? r[0].z : r[0].x, a[0], a[1]);
-        e4m3x4_to_act<ACT>(i ? r[0].w : r[0].y, a[2], a[3]);
-        e4m3x4_to_act<ACT>(i ? r[1].z : r[1].x, b[0], b[1]);
-        e4m3x4_to_act<ACT>(i ? r[1].w : r[1].y, b[2], b[3]);
-    }
-    __device__ __forceinline__ float row_scale(int) const { return 1.0f; }
-};
-
-// NVFP4: the block scales lie along n, one byte each: a stage holds, for each
-// row set and each of the unit's 8 blocks, the three aligned words around its
-// 8 rows (48 words: one per lane, and a second for half the lanes).
-template <int ACT> struct Unit<MOE_W_NVFP4, ACT> {
-    static constexpr int SPAN = 128, CHUNKS = 4, BYTES = 1024 + 192;
-    static constexpr bool X_RING = false, X_PERM = false, GROUPED = false, ROW_SCALE = false;
-    struct Src : RowSrc<4> {
-        const uint8_t* ps[2];
-        int kb[2];  // block within the unit
-        bool vs[2];
-        int N;
-        __device__ __forceinline__ void aim(const WBase& b, const UnitRows& u, int lane) {
-            RowSrc<4>::aim(b, u, lane);
-            N = b.N;
+    static constexpr float SCALE_UP = 1.0f;
+    struct Src : RowSrc<16, MT, KT> {};
+    uint4 r[MT][2][KT];
+    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
+    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    __device__ __forceinline__ void open(const uint8_t* st, int, int, int lane) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int p = lane + 32 * h, set = p / 24, q = p - 24 * set;
-                const int n = ((set ? u.b : u.a) & ~3) + 4 * (q % 3);
-                kb[h] = q / 3;
-                vs[h] = p < 48 && n < b.N;
-                ps[h] = b.sc + static_cast<size_t>(kb[h]) * b.N + n;
+        for (int q = 0; q < 2 * MT * KT; ++q)
+            r[q / (2 * KT)][q / KT % 2][q % KT] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
+    }
+    static __device__ __forceinline__ int k_of(int i, int c) { return 8 * c + 32 * i; }
+    __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+        a[0] = r[m][0][i].x; a[1] = r[m][0][i].y; a[2] = r[m][0][i].z; a[3] = r[m][0][i].w;
+        b[0] = r[m][1][i].x; b[1] = r[m][1][i].y; b[2] = r[m][1][i].z; b[3] = r[m][1][i].w;
+    }
+    __device__ __forceinline__ float scale(int, int, int) const { return 1.0f; }
+};
+
+template <int ACT, bool GU> struct Unit<MOE_W_FP8_E4M3, ACT, GU> {
+    static constexpr int MT = GU ? 2 : 1, KT = GU ? 1 : 2, SPAN = 64 * KT, CHUNKS = 2 * KT, BYTES = 2048;
+    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
+    static constexpr bool X_RING = false, X_PERM = false, GROUPED = false, ROW_SCALE = true;
+    static constexpr float SCALE_UP = 1.0f;
+    struct Src : RowSrc<8, MT, KT> {};
+    uint4 r[MT][2][KT];
+    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
+    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    __device__ __forceinline__ void open(const uint8_t* st, int, int, int lane) {
+#pragma unroll
+        for (int q = 0; q < 2 * MT * KT; ++q)
+            r[q / (2 * KT)][q / KT % 2][q % KT] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
+    }
+    static __device__ __forceinline__ int k_of(int i, int c) { return 16 * c + 8 * (i & 1) + 64 * (i >> 1); }
+    __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+        const uint4 &u = r[m][0][i >> 1], &v = r[m][1][i >> 1];
+        e4m3x4_to_act<ACT>(i & 1 ? u.z : u.x, a[0], a[1]);
+        e4m3x4_to_act<ACT>(i & 1 ? u.w : u.y, a[2], a[3]);
+        e4m3x4_to_act<ACT>(i & 1 ? v.z : v.x, b[0], b[1]);
+        e4m3x4_to_act<ACT>(i & 1 ? v.w : v.y, b[2], b[3]);
+    }
+    __device__ __forceinline__ float scale(int, int, int) const { return 1.0f; }
+};
+
+// NVFP4: the block scales lie along n, one byte each. For each of the unit's 8
+// blocks a stage holds the aligned words around the rows of set a and of set b:
+// WS words a set, 16 WS words in all, two per lane (half of the lanes, where WS
+// is 3).
+//
+// To bf16, a pair of codes takes two shifts and two logic operations: sign to
+// bit 15, exponent and mantissa to bits 8..6, which is the code's value times
+// 2^-126 (subnormals included). The block scale carries 2^118 of that back
+// (448 * 2^118 is the most that fits) and the finished sums the other 2^8; the
+// product is exact, as 6 significant bits are.
+template <int ACT, bool GU> struct Unit<MOE_W_NVFP4, ACT, GU> {
+    static constexpr int MT = GU ? 2 : 1, SPAN = 128, CHUNKS = 4;
+    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
+    static constexpr int WS = GU ? 5 : 3;  // words around 8 MT unaligned bytes
+    static constexpr int SC_AT = 1024 * MT, BYTES = SC_AT + 16 * WS * 4;
+    static constexpr bool X_RING = false, X_PERM = ACT == MOE_ACT_BF16, GROUPED = false, ROW_SCALE = false;
+    static constexpr float SCALE_UP = ACT == MOE_ACT_BF16 ? 256.0f : 1.0f;
+    static constexpr int PIECES = (16 * WS + 31) / 32;
+    struct Src : RowSrc<4, MT, 1> {
+        const uint8_t* ps[PIECES];
+        uint32_t ok;  // bit h: piece h exists
+        int row_step;
+        __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
+            RowSrc<4, MT, 1>::aim(b, a, n_a, bb, n_b, k0, lane);
+            row_step = 8 * b.N;
+            ok = 0;
+#pragma unroll
+            for (int h = 0; h < PIECES; ++h) {
+                const int p = lane + 32 * h, set = p / (8 * WS), q = p - 8 * WS * set;
+                const int n = ((set ? bb : a) & ~3) + 4 * (q % WS);
+                if (p < 16 * WS && n < b.N) ok |= 1u << h;
+                ps[h] = b.sc + static_cast<size_t>(k0 / 16 + q / WS) * b.N + n;
             }
         }
-        __device__ __forceinline__ void load(uint8_t* st, int k0, int K, bool tail, int lane) const {
-            RowSrc<4>::load(st, k0, K, tail, lane);
-            const int off = (k0 >> 4) * N;
+        __device__ __forceinline__ void load(uint8_t* st, int lane) const {
+            RowSrc<4, MT, 1>::load(st, lane);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!vs[h]) continue;
-                uint8_t* d = st + 1024 + 4 * lane + 128 * h;
-                if (!tail) {
-                    cp_async4(d, ps[h] + off);
-                } else {  // a scale past the end meets zero codes, but must not be a NaN
-                    const bool in = k0 + 16 * kb[h] < K;
-                    cp_async4_zfill(d, ps[h] + (in ? off : -kb[h] * N), in);
-                }
+            for (int h = 0; h < PIECES; ++h)
+                if (ok >> h & 1) cp_async4(st + SC_AT + 128 * h + 4 * lane, ps[h]);
+        }
+        __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const {
+            RowSrc<4, MT, 1>::load_tail(st, left, lane);
+            for (int h = 0; h < PIECES; ++h) {
+                // a scale past the end meets zero codes, but must not be a NaN
+                const int kb = (lane + 32 * h) % (8 * WS) / WS;
+                const bool in = 16 * kb < left;
+                if (ok >> h & 1)
+                    cp_async4_zfill(st + SC_AT + 128 * h + 4 * lane, in ? ps[h] : ps[h] - kb * (row_step / 8), in);
             }
+        }
+        __device__ __forceinline__ void step() {
+            RowSrc<4, MT, 1>::step();
+#pragma unroll
+            for (int h = 0; h < PIECES; ++h) ps[h] += row_step;
         }
     };
-    uint4 r[2];
-    uint32_t sc[2];  // the two block scales of the lane's 32 codes, low byte first
-    __device__ __forceinline__ void open(const uint8_t* st, const UnitRows& u, int lane) {
+    uint4 r[MT][2];
+    uint32_t s2[MT][2][2];  // the two block scales of the lane's 32 codes, each twice in a word
+    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
+    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    __device__ __forceinline__ void open(const uint8_t* st, int a, int b, int lane) {
         const int g = lane >> 2, c = lane & 3;
-        r[0] = *reinterpret_cast<const uint4*>(st + 16 * lane);
-        r[1] = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
-        const uint8_t* s0 = st + 1024 + 24 * c + (u.a & 3) + g;
-        const uint8_t* s1 = st + 1024 + 96 + 24 * c + (u.b & 3) + g;
-        sc[0] = s0[0] | (static_cast<uint32_t>(s0[12]) << 8);
-        sc[1] = s1[0] | (static_cast<uint32_t>(s1[12]) << 8);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                r[m][h] = *reinterpret_cast<const uint4*>(st + 512 * (2 * m + h) + 16 * lane);
+                const uint8_t* s = st + SC_AT + (h * 8 + 2 * c) * WS * 4 + ((h ? b : a) & 3) + 8 * m + g;
+                uint32_t f;
+                asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+                    : "=r"(f)
+                    : "r"(s[0] | (static_cast<uint32_t>(s[WS * 4]) << 8)));
+                if (ACT == MOE_ACT_F16) {
+                    s2[m][h][0] = gemm::prmt(f, f, 0x1010u);
+                    s2[m][h][1] = gemm::prmt(f, f, 0x3232u);
+                } else {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                    const float lo = v.x * 0x1p118f, hi = v.y * 0x1p118f;
+                    s2[m][h][0] = Act<MOE_ACT_BF16>::pack2(lo, lo);
+                    s2[m][h][1] = Act<MOE_ACT_BF16>::pack2(hi, hi);
+                }
+            }
     }
     static __device__ __forceinline__ int k_of(int i, int c) { return 32 * c + 8 * i; }
-    static __device__ __forceinline__ void row(const uint4& w, uint32_t sc, int i, uint32_t (&o)[4]) {
+    static __device__ __forceinline__ void row(const uint4& w, uint32_t m, int i, uint32_t (&o)[4]) {
         const uint32_t word = i == 0 ? w.x : (i == 1 ? w.y : (i == 2 ? w.z : w.w));
-        uint32_t s2[2];
-        const uint32_t s[2] = {sc & 0xffu, sc >> 8};
-        gemm::e4m3_scale_pairs<ACT, 2>(s, s2);
-        const uint32_t m = s2[i >> 1];
         if (ACT == MOE_ACT_BF16) {
-            gemm::e2m1x4_to_bf16x4(word, o[0], o[1]);
-            gemm::e2m1x4_to_bf16x4(word >> 16, o[2], o[3]);
+            // (k_j, k_{j+4})
+            o[0] = gemm::and_or(word << 6, 0x01C001C0u, (word << 12) & 0x80008000u);
+            o[1] = gemm::and_or(word << 2, 0x01C001C0u, (word << 8) & 0x80008000u);
+            o[2] = gemm::and_or(word >> 2, 0x01C001C0u, (word << 4) & 0x80008000u);
+            o[3] = gemm::and_or(word >> 6, 0x01C001C0u, word & 0x80008000u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]),
@@ -256,183 +317,270 @@ template <int ACT> struct Unit<MOE_W_NVFP4, ACT> {
             }
         }
     }
-    __device__ __forceinline__ void frag(int i, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        row(r[0], sc[0], i, a);
-        row(r[1], sc[1], i, b);
+    __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+        row(r[m][0], s2[m][0][i >> 1], i, a);
+        row(r[m][1], s2[m][1][i >> 1], i, b);
     }
-    __device__ __forceinline__ float row_scale(int) const { return 1.0f; }
+    __device__ __forceinline__ float scale(int, int, int) const { return 1.0f; }
 };
 
-// GPTQ: the words of 8 k values lie along n, so a lane copies single words. The
-// fragments hold the integers q - z (exact), and the group's f16 scale
-// multiplies the f32 sums of each unit: SPAN = 64 divides every group. Per row
-// set a stage holds the five aligned words around its 8 scales and the two
-// zero-point words its 8 rows can touch (lanes 0-13, one word each).
-template <int ACT> struct Unit<MOE_W_GPTQ_INT4, ACT> {
-    static constexpr int SPAN = 64, CHUNKS = 2, BYTES = 512 + 64;
+// GPTQ: the words of 8 k values lie along n, so a lane copies V neighbouring
+// columns' words at once and they go to V different rows of its fragments.
+//   gate/up  V = 4 (16 bytes): lane group g has columns 4g .. 4g + 3, one in
+//            each of four tiles; an item is 32 columns, a 128-byte line per
+//            k word (with 8 columns an item, DRAM read 3.3 times the weights)
+//   down     V = 2 (8 bytes): columns 2g and 2g + 1 are rows g and g + 8
+// The fragments hold the integers q - z (exact), and the group's f16 scale
+// multiplies the f32 sums of each 64 contraction indices (a divisor of every
+// group). Per 64 indices a lane group's V scales and its zero-point word are
+// copied by one lane each: lane c = 0 / 1 scales of set a / b, 2 / 3 zeros.
+template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
+    static constexpr int V = GU ? 4 : 2, SETS = GU ? 2 : 1, KT = GU ? 1 : 2;  // KT: pieces of 64 indices
+    static constexpr int MT = GU ? 4 : 1, SPAN = 64 * KT, CHUNKS = 2 * KT;
+    static constexpr int ROWS = GU ? 32 : 16, ALIGN = V;
+    static constexpr int PIECE = 32 * 4 * V;                    // bytes of one k word of all lanes
+    static constexpr int SC_AT = 2 * KT * SETS * PIECE;         // then, per 64 indices and set: scales, zeros
+    static constexpr int SC_SET = 8 * (2 * V + 4), BYTES = SC_AT + KT * SETS * SC_SET;
     static constexpr bool X_RING = false, X_PERM = true, GROUPED = true, ROW_SCALE = false;
+    static constexpr float SCALE_UP = 1.0f;
     struct Src {
-        const uint8_t* p;   // row a + g, k piece c
-        const uint8_t* pg;  // the lane's scale or zero-point word, group 0
-        int db;             // bytes from row set a to row set b
-        int N, G, gstep;    // gstep: bytes from group to group
+        const uint8_t* p;   // set a, k word c
+        const uint8_t* pg;  // the lane's scales or zero-point word, group 0
+        int N, G, k, db, gstep;
         bool va, vb, vg;
-        __device__ __forceinline__ void aim(const WBase& b, const UnitRows& u, int lane) {
-            const int g = lane >> 2, c = lane & 3;
+        __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
+            const int g = lane >> 2, c = lane & 3, set = GU ? c & 1 : 0, n = (set ? bb : a) + V * g;
             N = b.N;
             G = b.G;
-            va = g < u.na;
-            vb = g < u.nb;
-            p = b.w + (static_cast<size_t>(c) * N + u.a + g) * 4;
-            db = (u.b - u.a) * 4;
-            if (lane < 10) {
-                const int set = lane / 5, n = ((set ? u.b : u.a) & ~1) + 2 * (lane - 5 * set);
-                vg = n < N;
+            k = k0;
+            va = V * g < n_a;
+            vb = V * g < n_b;
+            db = (bb - a) * 4;
+            p = b.w + (static_cast<size_t>(k0 / 8 + c) * N + a + V * g) * 4;
+            vg = (set ? vb : va) && (GU || c == 0 || c == 2);
+            if (c < 2) {
                 pg = b.sc + static_cast<size_t>(n) * 2;
                 gstep = 2 * N;
             } else {
-                const int set = ((lane - 10) >> 1) & 1, n8 = (set ? u.b : u.a) / 8 + (lane & 1);
-                vg = lane < 14 && n8 < N / 8;
-                pg = b.z + static_cast<size_t>(n8) * 4;
+                pg = b.z + static_cast<size_t>(n / 8) * 4;
                 gstep = N / 2;
             }
         }
-        __device__ __forceinline__ void load(uint8_t* st, int k0, int K, bool, int lane) const {
-            const uint8_t* w = p + (k0 >> 1) * N;  // k0 / 8 words of 4 bytes
-            const int half = 16 * N;
-            if (va) {
-                cp_async4(st + 4 * lane, w);
-                cp_async4(st + 128 + 4 * lane, w + half);
+        static __device__ __forceinline__ void copy(void* d, const uint8_t* s, bool in) {
+            if (V == 4) cp_async16_zfill(d, s, in);
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(d)), "l"(s), "r"(in ? 8 : 0)
+                             : "memory");
+        }
+        __device__ __forceinline__ void load_n(uint8_t* st, int left, int lane) const {
+            uint8_t* d = st + 4 * V * lane;
+            const int half = 16 * N;  // 4 k words on
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                const bool in = 64 * t < left;
+                const uint8_t* w = in ? p + 2 * t * half : p;
+                if (va) {
+                    copy(d + 2 * t * PIECE, w, in);
+                    copy(d + (2 * t + 1) * PIECE, w + half, in);
+                }
+                if (GU && vb) {
+                    copy(d + 2 * PIECE, w + db, in);
+                    copy(d + 3 * PIECE, w + db + half, in);
+                }
+                if (vg) {
+                    const int g = lane >> 2, c = lane & 3;
+                    uint8_t* s = st + SC_AT + (t * SETS + (GU ? c & 1 : 0)) * SC_SET;
+                    const uint8_t* src = pg + static_cast<size_t>(in ? (k + 64 * t) / G : 0) * gstep;
+                    if (c >= 2) cp_async4_zfill(s + 16 * V + 4 * g, src, in);
+                    else if (V == 4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(s + 8 * g)), "l"(src),
+                                     "r"(in ? 8 : 0)
+                                     : "memory");
+                    else cp_async4_zfill(s + 4 * g, src, in);
+                }
             }
-            if (vb) {
-                cp_async4(st + 256 + 4 * lane, w + db);
-                cp_async4(st + 384 + 4 * lane, w + db + half);
-            }
-            if (vg) cp_async4(st + 512 + 4 * lane, pg + static_cast<size_t>(k0 / G) * gstep);
+        }
+        __device__ __forceinline__ void load(uint8_t* st, int lane) const { load_n(st, SPAN, lane); }
+        __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const { load_n(st, left, lane); }
+        __device__ __forceinline__ void step() {
+            p += static_cast<size_t>(KT) * 32 * N;
+            k += SPAN;
         }
     };
-    uint32_t w[2][2];  // [row][piece]
-    uint32_t z[2];
-    float s[2];
-    __device__ __forceinline__ void open(const uint8_t* st, const UnitRows& u, int lane) {
+    uint32_t w[KT][2][SETS][V];
+    uint32_t z[KT][SETS];  // the V zero points, 4 bits each
+    uint2 s[KT][SETS];     // the V scales
+    static __device__ __forceinline__ int row_a(int m, int g) { return GU ? 4 * g + m : 2 * g; }
+    static __device__ __forceinline__ int row_b(int g) { return 2 * g + 1; }
+    __device__ __forceinline__ void open(const uint8_t* st, int a, int b, int lane) {
         const int g = lane >> 2;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int n = (q ? u.b : u.a), r = n + g;
-            w[q][0] = *reinterpret_cast<const uint32_t*>(st + 256 * q + 4 * lane);
-            w[q][1] = *reinterpret_cast<const uint32_t*>(st + 256 * q + 128 + 4 * lane);
-            s[q] = __half2float(*reinterpret_cast<const __half*>(st + 512 + 20 * q + 2 * ((n & 1) + g)));
-            const uint32_t zw = *reinterpret_cast<const uint32_t*>(st + 512 + 40 + 8 * q + 4 * (r / 8 - n / 8));
-            z[q] = (zw >> (4 * (r & 7))) & 15u;
-        }
-    }
-    static __device__ __forceinline__ int k_of(int i, int c) { return 8 * (c + 4 * i); }
-    __device__ __forceinline__ void row(int q, int i, uint32_t (&o)[4]) const {
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // (k_j, k_{j+4})
-            if (ACT == MOE_ACT_F16) {
-                const uint32_t v = gemm::and_or(w[q][i] >> (4 * j), 0x000F000Fu, 0x64006400u);  // 1024 + q
-                const __half2 zz = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6400u | z[q])));
-                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), zz);
+            for (int q = 0; q < SETS; ++q) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* d = st + (2 * (t * SETS + q) + i) * PIECE + 4 * V * lane;
+                    if (V == 4) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(d);
+                        w[t][i][q][0] = u.x;
+                        w[t][i][q][1] = u.y;
+                        w[t][i][q][V - 2] = u.z;
+                        w[t][i][q][V - 1] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(d);
+                        w[t][i][q][0] = u.x;
+                        w[t][i][q][1] = u.y;
+                    }
+                }
+                const uint8_t* sc = st + SC_AT + (t * SETS + q) * SC_SET;
+                if (V == 4) s[t][q] = *reinterpret_cast<const uint2*>(sc + 8 * g);
+                else s[t][q].x = *reinterpret_cast<const uint32_t*>(sc + 4 * g);
+                z[t][q] = *reinterpret_cast<const uint32_t*>(sc + 16 * V + 4 * g) >> (4 * (((q ? b : a) + V * g) & 7));
+            }
+    }
+    static __device__ __forceinline__ int k_of(int i, int c) { return 8 * c + 32 * i; }
+    static __device__ __forceinline__ void row(uint32_t w, uint32_t z, uint32_t (&o)[4]) {  // (k_j, k_{j+4})
+        if (ACT == MOE_ACT_F16) {
+            // 1024 + q, or 1024 + 16 q (divided by 16 again); both differences are exact
+            const __half2 z1 = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x6400u | z)));
+            const __half2 nz = __half2half2(__ushort_as_half(static_cast<unsigned short>(0xD400u | (z << 4))));  // -(64 + z)
+            const __half2 c16 = __half2half2(__ushort_as_half(static_cast<unsigned short>(0x2C00u)));
+            const uint32_t w8 = w >> 8;
+            const uint32_t q[4] = {gemm::and_or(w, 0x000F000Fu, 0x64006400u), gemm::and_or(w, 0x00F000F0u, 0x64006400u),
+                                   gemm::and_or(w8, 0x000F000Fu, 0x64006400u),
+                                   gemm::and_or(w8, 0x00F000F0u, 0x64006400u)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 h = *reinterpret_cast<const __half2*>(&q[j]);
+                const __half2 d = (j & 1) ? __hfma2(h, c16, nz) : __hsub2(h, z1);
                 o[j] = *reinterpret_cast<const uint32_t*>(&d);
-            } else {
-                const uint32_t v = gemm::and_or(w[q][i] >> (4 * j), 0x000F000Fu, 0x43004300u);  // 128 + q
-                const __nv_bfloat162 zz =
-                    __bfloat162bfloat162(__ushort_as_bfloat16(static_cast<unsigned short>(0x4300u | z[q])));
+            }
+        } else {
+            const __nv_bfloat162 zz = __bfloat162bfloat162(__ushort_as_bfloat16(static_cast<unsigned short>(0x4300u | z)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t v = gemm::and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u);  // 128 + q
                 const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), zz);
                 o[j] = *reinterpret_cast<const uint32_t*>(&d);
             }
         }
     }
-    __device__ __forceinline__ void frag(int i, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        row(0, i, a);
-        row(1, i, b);
+    __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+        const int t = i >> 1;
+        if (GU) {
+            row(w[t][i & 1][0][m], (z[t][0] >> (4 * m)) & 15u, a);
+            row(w[t][i & 1][SETS - 1][m], (z[t][SETS - 1] >> (4 * m)) & 15u, b);
+        } else {
+            row(w[t][i & 1][0][0], z[t][0] & 15u, a);
+            row(w[t][i & 1][0][1], (z[t][0] >> 4) & 15u, b);
+        }
     }
-    __device__ __forceinline__ float row_scale(int q) const { return s[q]; }
+    // of piece i's group: row a (h = 0) or b of tile m
+    __device__ __forceinline__ float scale(int i, int m, int h) const {
+        const int t = i >> 1, v = GU ? m : h;
+        const uint2& u = s[t][GU ? h * (SETS - 1) : 0];
+        const uint32_t word = v < 2 ? u.x : u.y;
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(v & 1 ? word >> 16 : word & 0xffffu)));
+    }
 };
 
 // A stage of a warp's ring
 template <class U> struct Stage {
-    static constexpr int X_AT = U::BYTES, BYTES = (U::BYTES + (U::X_RING ? 512 * U::CHUNKS : 0) + 15) / 16 * 16;
+    static constexpr int X_AT = (U::BYTES + 15) / 16 * 16, BYTES = X_AT + (U::X_RING ? 512 * U::CHUNKS : 0);
 };
 
 __device__ __forceinline__ uint4 perm_0415(const uint4& x) {
     return make_uint4(gemm::prmt(x.x, x.z, 0x5410), gemm::prmt(x.x, x.z, 0x7632), gemm::prmt(x.y, x.w, 0x5410),
                       gemm::prmt(x.y, x.w, 0x7632));
 }
+// 16 bytes where `ok`, else v as it was
+__device__ __forceinline__ void ld16_if(uint4& v, const void* p, bool ok) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"(static_cast<int>(ok))
+        : "memory");
+}
 
-// The first token tile's values of one unit. x: the lane's token row (token g),
-// already at its piece 0 of contraction index 0, or NULL (no token: zeros).
+// The first token tile's values of one unit. x: the lane's token row (token g)
+// at the unit's first contraction index, already moved to the lane's piece 0;
+// `has`: whether there is such a token (else zeros).
 template <class U> struct Tokens {
     uint4 v[U::CHUNKS];
-    // into the stage (X_RING)
-    static __device__ __forceinline__ void copy(uint8_t* st, const uint16_t* x, int k0, int K, bool tail, int lane) {
-        if (!x) return;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < U::CHUNKS; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // into the stage (X_RING); `left`: contraction indices to the end, SPAN or more if none are missing
+    static __device__ __forceinline__ void copy(uint8_t* st, const uint16_t* x, bool has, int left, int lane) {
+        if (!has) return;
 #pragma unroll
         for (int i = 0; i < U::CHUNKS; ++i) {
-            const int o = U::k_of(i, 0);
-            const bool in = !tail || k0 + U::k_of(i, lane & 3) < K;
-            cp_async16_l1(st + 512 * i + 16 * lane, x + (in ? k0 + o : 0), in);
+            const bool in = U::k_of(i, lane & 3) < left;
+            cp_async16_l1(st + 512 * i + 16 * lane, x + (in ? U::k_of(i, 0) : -U::k_of(0, lane & 3)), in);
         }
     }
-    __device__ __forceinline__ void open(const uint8_t* st, const uint16_t* x, int lane) {
+    // from the stage; lanes without a token keep what clear() left
+    __device__ __forceinline__ void open(const uint8_t* st, bool has, int lane) {
+        if (has)
 #pragma unroll
-        for (int i = 0; i < U::CHUNKS; ++i)
-            v[i] = x ? *reinterpret_cast<const uint4*>(st + 512 * i + 16 * lane) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < U::CHUNKS; ++i) v[i] = *reinterpret_cast<const uint4*>(st + 512 * i + 16 * lane);
     }
     // straight into registers
-    __device__ __forceinline__ void fetch(const uint16_t* x, int k0, int K, bool tail, int lane) {
+    __device__ __forceinline__ void fetch(const uint16_t* x, bool has, int left, int lane) {
+        if (left < U::SPAN) clear();
 #pragma unroll
-        for (int i = 0; i < U::CHUNKS; ++i) {
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (x && (!tail || k0 + U::k_of(i, lane & 3) < K))
-                v[i] = *reinterpret_cast<const uint4*>(x + k0 + U::k_of(i, 0));
-        }
+        for (int i = 0; i < U::CHUNKS; ++i) ld16_if(v[i], x + U::k_of(i, 0), has && U::k_of(i, lane & 3) < left);
     }
 };
 
-// acc[tile] += unit x tokens, for nt tiles of 8 tokens; xp[tile], for tile >= 1, as Tokens' x.
+// acc[tile][token tile] += unit x tokens, for nt token tiles of 8. x1, has1: the
+// lane's token of the second tile, as in Tokens.
 template <class U, int ACT, int NT>
-__device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const uint16_t* const (&xp)[NT], int nt,
-                                         int k0, int K, bool tail, int lane, float (&acc)[NT][4]) {
-    float part[NT][4];
-    if (U::GROUPED) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) part[t][0] = part[t][1] = part[t][2] = part[t][3] = 0.0f;
-    }
+__device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const uint16_t* x1, bool has1, int nt,
+                                         int left, int lane, float (&acc)[U::MT][NT][4]) {
+    float part[U::MT][NT][4];
 #pragma unroll
     for (int i = 0; i < U::CHUNKS; ++i) {
-        uint32_t a[4], b[4];
-        u.frag(i, a, b);
-        {
-            const uint4 x = U::X_PERM ? perm_0415(x0.v[i]) : x0.v[i];
-            float (&d)[4] = U::GROUPED ? part[0] : acc[0];
-            mma_16816<ACT>(d, a[0], b[0], a[1], b[1], x.x, x.y);
-            mma_16816<ACT>(d, a[2], b[2], a[3], b[3], x.z, x.w);
-        }
-        if (NT > 1 && nt > 1) {
+        if (U::GROUPED && (i & 1) == 0) {
 #pragma unroll
-            for (int t = 1; t < NT; ++t) {
-                if (t >= nt) break;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (xp[t] && (!tail || k0 + U::k_of(i, lane & 3) < K))
-                    x = *reinterpret_cast<const uint4*>(xp[t] + k0 + U::k_of(i, 0));
-                if (U::X_PERM) x = perm_0415(x);
-                float (&d)[4] = U::GROUPED ? part[t] : acc[t];
-                mma_16816<ACT>(d, a[0], b[0], a[1], b[1], x.x, x.y);
-                mma_16816<ACT>(d, a[2], b[2], a[3], b[3], x.z, x.w);
+            for (int m = 0; m < U::MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) part[m][t][0] = part[m][t][1] = part[m][t][2] = part[m][t][3] = 0.0f;
+        }
+        uint4 x[NT];
+        x[0] = U::X_PERM ? perm_0415(x0.v[i]) : x0.v[i];
+        if (NT > 1 && nt > 1) {
+            x[NT - 1] = make_uint4(0u, 0u, 0u, 0u);
+            ld16_if(x[NT - 1], x1 + U::k_of(i, 0), has1 && U::k_of(i, lane & 3) < left);
+            if (U::X_PERM) x[NT - 1] = perm_0415(x[NT - 1]);
+        }
+#pragma unroll
+        for (int m = 0; m < U::MT; ++m) {
+            uint32_t a[4], b[4];
+            u.frag(i, m, a, b);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t > 0 && nt <= t) break;
+                float (&d)[4] = U::GROUPED ? part[m][t] : acc[m][t];
+                mma_16816<ACT>(d, a[0], b[0], a[1], b[1], x[t].x, x[t].y);
+                mma_16816<ACT>(d, a[2], b[2], a[3], b[3], x[t].z, x[t].w);
             }
         }
-    }
-    if (U::GROUPED) {
-        const float s0 = u.row_scale(0), s1 = u.row_scale(1);
+        if (U::GROUPED && (i & 1) == 1) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t > 0 && t >= nt) break;
-            acc[t][0] = fmaf(s0, part[t][0], acc[t][0]);
-            acc[t][1] = fmaf(s0, part[t][1], acc[t][1]);
-            acc[t][2] = fmaf(s1, part[t][2], acc[t][2]);
-            acc[t][3] = fmaf(s1, part[t][3], acc[t][3]);
+            for (int m = 0; m < U::MT; ++m) {
+                const float s0 = u.scale(i, m, 0), s1 = u.scale(i, m, 1);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t > 0 && nt <= t) break;
+                    acc[m][t][0] = fmaf(s0, part[m][t][0], acc[m][t][0]);
+                    acc[m][t][1] = fmaf(s0, part[m][t][1], acc[m][t][1]);
+                    acc[m][t][2] = fmaf(s1, part[m][t][2], acc[m][t][2]);
+                    acc[m][t][3] = fmaf(s1, part[m][t][3], acc[m][t][3]);
+                }
+            }
         }
     }
 }
