@@ -44,7 +44,7 @@ constexpr int kFewPairs = MOE_MAX_FEW_TOKENS * MOE_MAX_TOPK;
 template <int FMT> struct FewShape {
     static constexpr bool DENSE = FMT == MOE_W_BF16, GPTQ = FMT == MOE_W_GPTQ_INT4;
     static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
-    static constexpr int GU_RING = DENSE || GPTQ ? 4 : (FMT == MOE_W_FP8_E4M3 ? 5 : 4);
+    static constexpr int GU_RING = FMT == MOE_W_FP8_E4M3 ? 5 : 4;
     static constexpr int DN_RING = DENSE ? 4 : (FMT == MOE_W_FP8_E4M3 ? 5 : 8);
     static constexpr int RESIDENT = DENSE ? 2 : 1;  // CTAs per SM the registers must allow
 };
@@ -71,14 +71,15 @@ static __device__ __noinline__ void route_row_nan(const float* lrow, int lane, i
 }
 
 // Everything of the plan but the weights; THREADS threads, all of them here;
-// at most SLOTS slots an entry. `publish`: this CTA reports bad ids.
+// at most SLOTS slots an entry. `select`: route from the logits (else the ids
+// are there); `publish`: this CTA reports bad ids.
 template <int THREADS, int SLOTS>
-__device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool publish) {
+__device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool select, bool publish) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = p.T * p.k;
     static_assert(THREADS >= MOE_MAX_EXPERTS, "one thread per expert");
     if (tid < MOE_MAX_EXPERTS) s.mask[tid] = 0;
-    if (p.logits) {
+    if (select) {
         for (int t = warp; t < p.T; t += THREADS / 32) {
             const float* lrow = p.logits + t * p.E;
             float v[kPerLane], sv;
@@ -183,7 +184,7 @@ few_gate_up_kernel(const FewParams p) {
     __shared__ FewPlan s;
     pdl_wait();
     pdl_launch_next();
-    build_plan<(W + 1) * 32, 8 * NT>(s, p, blockIdx.x == 0);
+    build_plan<(W + 1) * 32, 8 * NT>(s, p, p.logits != nullptr, blockIdx.x == 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (warp == W) {  // beside the products: the routing outputs, one row per CTA
         if (p.logits) publish_routing(p, blockIdx.x, gridDim.x, lane);
@@ -412,9 +413,13 @@ few_down_kernel(const FewParams p) {
     extern __shared__ uint8_t few_smem[];
     float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][17]: sums of 16 columns
     __shared__ FewPlan s;
-    // before the wait: only what was complete before the gate/up kernel started
-    // (logits, or ids given as inputs) and the weights
-    build_plan<W * 32, 8 * NT>(s, p, false);
+    // Beside the gate/up kernel: only what was complete before that started
+    // (logits, or ids given as inputs) and the weights are read before the wait.
+    // Otherwise this CTA starts when that kernel is all but done, and takes the
+    // ids it left.
+    constexpr bool BESIDE = FewShape<FMT>::RESIDENT > 1;
+    if (!BESIDE) pdl_wait();
+    build_plan<W * 32, 8 * NT>(s, p, BESIDE && p.logits != nullptr, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
     const int64_t shares = p.H / U::ALIGN;
@@ -485,7 +490,7 @@ few_down_kernel(const FewParams p) {
         fetch_w(ring + d * S::BYTES, l);
         advance(l);
     }
-    pdl_wait();  // h and the routing outputs are complete
+    if (BESIDE) pdl_wait();  // h and the routing outputs are complete
     slot_weights<W * 32>(s, p);
     {
         Pos q = start;

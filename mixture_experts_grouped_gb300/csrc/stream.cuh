@@ -30,6 +30,10 @@ __device__ __forceinline__ void cp_async4_zfill(void* dst, const void* src, bool
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(full ? 4 : 0)
                  : "memory");
 }
+// 16 bytes of a weight row, which is read on from there: L2 fetches the 256 bytes around them
+__device__ __forceinline__ void cp_async16_row(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 // 16 bytes through L1 (token operands: neighbouring warps and later tiles read them again)
 __device__ __forceinline__ void cp_async16_l1(void* dst, const void* src, bool full) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(full ? 16 : 0)
@@ -140,10 +144,10 @@ template <int EB, int MT, int KT> struct RowSrc {
         for (int m = 0; m < MT; ++m) {
             if (m < na)
 #pragma unroll
-                for (int t = 0; t < KT; ++t) cp_async16(d + (2 * m * KT + t) * 512, pa + m * row8 + t * 64);
+                for (int t = 0; t < KT; ++t) cp_async16_row(d + (2 * m * KT + t) * 512, pa + m * row8 + t * 64);
             if (m < nb)
 #pragma unroll
-                for (int t = 0; t < KT; ++t) cp_async16(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + t * 64);
+                for (int t = 0; t < KT; ++t) cp_async16_row(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + t * 64);
         }
     }
     __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const {  // `left` indices to K's end
@@ -345,14 +349,16 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
     static constexpr float SCALE_UP = 1.0f;
     struct Src {
         const uint8_t* p;   // set a, k word c
-        const uint8_t* pg;  // the lane's scales or zero-point word, group 0
-        int N, G, k, db, gstep;
+        const uint8_t* pg;  // the lane's scales or zero-point word of the group
+        int N, db, gstep;   // gstep: bytes from group to group
+        int per, rest;      // 64s of contraction indices in a group, and left of this one
         bool va, vb, vg;
         __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
             const int g = lane >> 2, c = lane & 3, set = GU ? c & 1 : 0, n = (set ? bb : a) + V * g;
             N = b.N;
-            G = b.G;
-            k = k0;
+            per = b.G / 64;
+            const int group = k0 / b.G;
+            rest = per - (k0 - group * b.G) / 64;
             va = V * g < n_a;
             vb = V * g < n_b;
             db = (bb - a) * 4;
@@ -365,6 +371,7 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
                 pg = b.z + static_cast<size_t>(n / 8) * 4;
                 gstep = N / 2;
             }
+            pg += static_cast<size_t>(group) * gstep;
         }
         static __device__ __forceinline__ void copy(void* d, const uint8_t* s, bool in) {
             if (V == 4) cp_async16_zfill(d, s, in);
@@ -372,7 +379,7 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(d)), "l"(s), "r"(in ? 8 : 0)
                              : "memory");
         }
-        __device__ __forceinline__ void load_n(uint8_t* st, int left, int lane) const {
+        __device__ __forceinline__ void load_n(uint8_t* st, int left, int lane) {
             uint8_t* d = st + 4 * V * lane;
             const int half = 16 * N;  // 4 k words on
 #pragma unroll
@@ -390,22 +397,23 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
                 if (vg) {
                     const int g = lane >> 2, c = lane & 3;
                     uint8_t* s = st + SC_AT + (t * SETS + (GU ? c & 1 : 0)) * SC_SET;
-                    const uint8_t* src = pg + static_cast<size_t>(in ? (k + 64 * t) / G : 0) * gstep;
-                    if (c >= 2) cp_async4_zfill(s + 16 * V + 4 * g, src, in);
+                    if (c >= 2) cp_async4_zfill(s + 16 * V + 4 * g, pg, in);
                     else if (V == 4)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(s + 8 * g)), "l"(src),
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(s + 8 * g)), "l"(pg),
                                      "r"(in ? 8 : 0)
                                      : "memory");
-                    else cp_async4_zfill(s + 4 * g, src, in);
+                    else cp_async4_zfill(s + 4 * g, pg, in);
+                }
+                // on by 64 indices; not past the end, where the last group stands in for a copy of nothing
+                if (--rest == 0) {
+                    rest = per;
+                    if (64 * (t + 1) < left) pg += gstep;
                 }
             }
         }
-        __device__ __forceinline__ void load(uint8_t* st, int lane) const { load_n(st, SPAN, lane); }
-        __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const { load_n(st, left, lane); }
-        __device__ __forceinline__ void step() {
-            p += static_cast<size_t>(KT) * 32 * N;
-            k += SPAN;
-        }
+        __device__ __forceinline__ void load(uint8_t* st, int lane) { load_n(st, 1 << 30, lane); }
+        __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) { load_n(st, left, lane); }
+        __device__ __forceinline__ void step() { p += static_cast<size_t>(KT) * 32 * N; }
     };
     uint32_t w[KT][2][SETS][V];
     uint32_t z[KT][SETS];  // the V zero points, 4 bits each
@@ -529,17 +537,22 @@ template <class U> struct Tokens {
     }
     // straight into registers
     __device__ __forceinline__ void fetch(const uint16_t* x, bool has, int left, int lane) {
-        if (left < U::SPAN) clear();
+        if (left >= U::SPAN) {
 #pragma unroll
-        for (int i = 0; i < U::CHUNKS; ++i) ld16_if(v[i], x + U::k_of(i, 0), has && U::k_of(i, lane & 3) < left);
+            for (int i = 0; i < U::CHUNKS; ++i) ld16_if(v[i], x + U::k_of(i, 0), has);
+        } else {
+            clear();
+#pragma unroll
+            for (int i = 0; i < U::CHUNKS; ++i) ld16_if(v[i], x + U::k_of(i, 0), has && U::k_of(i, lane & 3) < left);
+        }
     }
 };
 
-// acc[tile][token tile] += unit x tokens, for nt token tiles of 8. x1, has1: the
-// lane's token of the second tile, as in Tokens.
-template <class U, int ACT, int NT>
-__device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const uint16_t* x1, bool has1, int nt,
-                                         int left, int lane, float (&acc)[U::MT][NT][4]) {
+// acc[tile][token tile] += unit x tokens, for the first NT of NTA token tiles of
+// 8. x1, has1: the lane's token of the second tile, as in Tokens.
+template <class U, int ACT, int NT, int NTA>
+__device__ __forceinline__ void unit_mma_n(const U& u, const Tokens<U>& x0, const uint16_t* x1, bool has1, int left,
+                                           int lane, float (&acc)[U::MT][NTA][4]) {
     float part[U::MT][NT][4];
 #pragma unroll
     for (int i = 0; i < U::CHUNKS; ++i) {
@@ -551,7 +564,7 @@ __device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const 
         }
         uint4 x[NT];
         x[0] = U::X_PERM ? perm_0415(x0.v[i]) : x0.v[i];
-        if (NT > 1 && nt > 1) {
+        if (NT > 1) {
             x[NT - 1] = make_uint4(0u, 0u, 0u, 0u);
             ld16_if(x[NT - 1], x1 + U::k_of(i, 0), has1 && U::k_of(i, lane & 3) < left);
             if (U::X_PERM) x[NT - 1] = perm_0415(x[NT - 1]);
@@ -562,7 +575,6 @@ __device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const 
             u.frag(i, m, a, b);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (t > 0 && nt <= t) break;
                 float (&d)[4] = U::GROUPED ? part[m][t] : acc[m][t];
                 mma_16816<ACT>(d, a[0], b[0], a[1], b[1], x[t].x, x[t].y);
                 mma_16816<ACT>(d, a[2], b[2], a[3], b[3], x[t].z, x[t].w);
@@ -574,7 +586,6 @@ __device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const 
                 const float s0 = u.scale(i, m, 0), s1 = u.scale(i, m, 1);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    if (t > 0 && nt <= t) break;
                     acc[m][t][0] = fmaf(s0, part[m][t][0], acc[m][t][0]);
                     acc[m][t][1] = fmaf(s0, part[m][t][1], acc[m][t][1]);
                     acc[m][t][2] = fmaf(s1, part[m][t][2], acc[m][t][2]);
@@ -583,6 +594,12 @@ __device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const 
             }
         }
     }
+}
+template <class U, int ACT, int NT>
+__device__ __forceinline__ void unit_mma(const U& u, const Tokens<U>& x0, const uint16_t* x1, bool has1, int nt,
+                                         int left, int lane, float (&acc)[U::MT][NT][4]) {
+    if (NT == 1 || nt == 1) unit_mma_n<U, ACT, 1, NT>(u, x0, x1, has1, left, lane, acc);
+    else unit_mma_n<U, ACT, NT, NT>(u, x0, x1, has1, left, lane, acc);
 }
 
 }  // namespace moe
