@@ -51,107 +51,122 @@ template <int FMT> struct FewShape {
 constexpr int kFewEntries = MOE_MAX_EXPERTS + kFewPairs / 8;
 
 struct FewPlan {
-    int n;                              // entries: touched experts, ascending, split
-    int te[kFewEntries];                // expert of each
-    int start[kFewEntries + 1];         // first slot of each
-    uint32_t mask[MOE_MAX_EXPERTS];     // by expert id: tokens routed to it
-    int first[MOE_MAX_EXPERTS];         // by expert id: first slot
-    int ids[kFewPairs];
+    int n;                           // entries: touched experts, ascending, split
+    int te[kFewEntries];             // expert of each
+    int start[kFewEntries + 1];      // first slot of each
+    uint32_t mask[MOE_MAX_EXPERTS];  // by expert id: tokens routed to it
+    int first[MOE_MAX_EXPERTS];      // by expert id: first slot
     float slot_w[kFewPairs];
     uint8_t slot_tok[kFewPairs];
-    uint32_t scan[MOE_MAX_EXPERTS / 32];
 };
 
+// [x0, x1): part i of n nearly equal parts of [0, all)
+__device__ __forceinline__ void part_of(int all, int n, int i, int& x0, int& x1) {
+    const int q = all / n, r = all - q * n;
+    x0 = q * i + min(i, r);
+    x1 = x0 + q + (i < r ? 1 : 0);
+}
+
 static __device__ __noinline__ void route_row_nan(const float* lrow, int lane, int E, int k, int renorm, int32_t* ids,
-                                           float* w) {
+                                                  float* w) {
     float v[kPerLane];
 #pragma unroll
     for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < E ? lrow[lane + 32 * j] : 0.0f;
     route_row(v, lane, E, k, renorm, ids, w);
 }
 
-// Everything of the plan but the weights; THREADS threads, all of them here;
-// at most SLOTS slots an entry. `select`: route from the logits (else the ids
-// are there); `publish`: this CTA reports bad ids.
-template <int THREADS, int SLOTS>
+// Everything of the plan but the weights; WARPS warps, all of them here; at
+// most SLOTS slots an entry. A warp takes tokens warp, warp + WARPS, ..., and
+// lane j < k of it the token's pair j: the experts are selected from the
+// logits (`select`) or read. `publish`: this CTA reports bad ids. The plan is
+// on the way of every weight load, so it is short: four barriers, no division.
+template <int WARPS, int SLOTS>
 __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool select, bool publish) {
+    constexpr int ROUNDS = (MOE_MAX_FEW_TOKENS + WARPS - 1) / WARPS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int P = p.T * p.k;
-    static_assert(THREADS >= MOE_MAX_EXPERTS, "one thread per expert");
+    static_assert(WARPS * 32 >= MOE_MAX_EXPERTS, "one thread per expert");
     if (tid < MOE_MAX_EXPERTS) s.mask[tid] = 0;
-    if (select) {
-        for (int t = warp; t < p.T; t += THREADS / 32) {
-            const float* lrow = p.logits + t * p.E;
-            float v[kPerLane], sv;
-            int si;
+    __syncthreads();
+    int ids[ROUNDS];
 #pragma unroll
-            for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < p.E ? __ldg(lrow + lane + 32 * j) : 0.0f;
-            if (!select_row(v, lane, p.E, p.k, sv, si)) {
-                route_row_nan(lrow, lane, p.E, p.k, p.renorm, s.ids + t * p.k, s.slot_w);  // slot_w: scratch here
-                continue;
+    for (int q = 0; q < ROUNDS; ++q) {
+        const int t = warp + q * WARPS;
+        ids[q] = -1;
+        if (t >= p.T) continue;
+        if (select) {
+            const float* lrow = p.logits + t * p.E;
+            float sv;
+            if (!select_row(lrow, lane, p.E, p.k, sv, ids[q])) {
+                // into scratch of the token's own (slot_w is filled later)
+                int32_t* scratch = reinterpret_cast<int32_t*>(s.slot_w) + t * MOE_MAX_TOPK;
+                route_row_nan(lrow, lane, p.E, p.k, p.renorm, scratch, reinterpret_cast<float*>(s.te) + warp * 16);
+                __syncwarp();
+                if (lane < p.k) ids[q] = scratch[lane];
             }
-            if (lane < p.k) s.ids[t * p.k + lane] = si;
+        } else if (lane < p.k) {
+            ids[q] = p.ids[t * p.k + lane];
+            if (publish && (ids[q] < 0 || ids[q] >= p.E)) set_err(p.err, MOE_DEV_ERR_EXPERT_ID);
         }
-    } else {
-        for (int i = tid; i < P; i += THREADS) s.ids[i] = p.ids[i];
+        if (lane >= p.k || ids[q] < 0 || ids[q] >= p.E) ids[q] = -1;
+        else atomicOr(&s.mask[ids[q]], 1u << t);
     }
     __syncthreads();
-    for (int i = tid; i < P; i += THREADS) {
-        const int e = s.ids[i];
-        if (e >= 0 && e < p.E) atomicOr(&s.mask[e], 1u << (i / p.k));
-        else if (publish) set_err(p.err, MOE_DEV_ERR_EXPERT_ID);
-    }
-    __syncthreads();
-    // prefix sums over the experts: entries in the high half, slots in the low
-    uint32_t m = 0, mine = 0, inc = 0;
-    if (tid < MOE_MAX_EXPERTS) {
-        m = s.mask[tid];
-        inc = mine = ((__popc(m) + SLOTS - 1) / SLOTS << 16) + __popc(m);
+    if (warp == 0) {
+        // prefix sums over the experts, eight consecutive ones a lane: entries in the high half, slots in the low
+        constexpr int PER = MOE_MAX_EXPERTS / 32;
+        uint32_t cnt[PER], mine = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            cnt[j] = __popc(s.mask[lane * PER + j]);
+            mine += ((cnt[j] + SLOTS - 1) / SLOTS << 16) + cnt[j];
+        }
+        uint32_t inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
         }
-        if (lane == 31) s.scan[warp] = inc;
-    }
-    __syncthreads();
-    if (tid < MOE_MAX_EXPERTS) {
-        uint32_t before = inc - mine;
-        for (int w = 0; w < warp; ++w) before += s.scan[w];
-        s.first[tid] = before & 0xffffu;
-        for (int j = 0; j < __popc(m); j += SLOTS) {
-            s.te[(before >> 16) + j / SLOTS] = tid;
-            s.start[(before >> 16) + j / SLOTS] = (before & 0xffffu) + j;
+        uint32_t at = inc - mine;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            s.first[lane * PER + j] = at & 0xffffu;
+            for (uint32_t c = 0; c < cnt[j]; c += SLOTS) {
+                s.te[at >> 16] = lane * PER + j;
+                s.start[at >> 16] = at & 0xffffu;
+                at += (1u << 16) + min(cnt[j] - c, static_cast<uint32_t>(SLOTS));
+            }
         }
-        if (tid == MOE_MAX_EXPERTS - 1) {
-            const uint32_t all = before + mine;
-            s.n = all >> 16;
-            s.start[all >> 16] = all & 0xffffu;
+        if (lane == 31) {
+            s.n = inc >> 16;
+            s.start[inc >> 16] = inc & 0xffffu;
         }
     }
     __syncthreads();
-    for (int i = tid; i < P; i += THREADS) {
-        const int e = s.ids[i], t = i / p.k;
-        if (e >= 0 && e < p.E)
-            s.slot_tok[s.first[e] + __popc(s.mask[e] & ((1u << t) - 1u))] = static_cast<uint8_t>(t);
+#pragma unroll
+    for (int q = 0; q < ROUNDS; ++q) {
+        const int t = warp + q * WARPS;
+        if (ids[q] >= 0)
+            s.slot_tok[s.first[ids[q]] + __popc(s.mask[ids[q]] & ((1u << t) - 1u))] = static_cast<uint8_t>(t);
     }
     __syncthreads();
 }
 
-// The slots' weights, from the weights in global memory: an expert that a token
-// names twice gets the sum.
-template <int THREADS> __device__ __forceinline__ void slot_weights(FewPlan& s, const FewParams& p) {
-    const int P = p.T * p.k;
-    for (int i = threadIdx.x; i < P; i += THREADS) {
-        const int e = s.ids[i], t = i / p.k, end = (t + 1) * p.k;
-        if (e < 0 || e >= p.E) continue;
-        bool again = false;
-        for (int j = t * p.k; j < i; ++j) again |= s.ids[j] == e;
-        if (again) continue;
-        float w = p.weights[i];
-        for (int j = i + 1; j < end; ++j)
-            if (s.ids[j] == e) w += p.weights[j];
-        s.slot_w[s.first[e] + __popc(s.mask[e] & ((1u << t) - 1u))] = w;
+// The slots' weights, from the ids and weights in global memory: an expert that
+// a token names twice gets the sum, in the order of its pairs.
+template <int WARPS> __device__ __forceinline__ void slot_weights(FewPlan& s, const FewParams& p) {
+    const int lane = threadIdx.x & 31;
+    for (int t = threadIdx.x >> 5; t < p.T; t += WARPS) {
+        const int e = lane < p.k ? p.ids[t * p.k + lane] : -1;
+        const float w = lane < p.k ? p.weights[t * p.k + lane] : 0.0f;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int j = 0; j < p.k; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            if (same >> j & 1) sum = j == __ffs(same) - 1 ? wj : sum + wj;
+        }
+        if (lane < p.k && e >= 0 && e < p.E && lane == __ffs(same) - 1)
+            s.slot_w[s.first[e] + __popc(s.mask[e] & ((1u << t) - 1u))] = sum;
     }
 }
 
@@ -163,7 +178,7 @@ __device__ __forceinline__ void publish_routing(const FewParams& p, int t, int s
         int si;
 #pragma unroll
         for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < p.E ? __ldg(lrow + lane + 32 * j) : 0.0f;
-        if (select_row(v, lane, p.E, p.k, sv, si))
+        if (select_row(lrow, lane, p.E, p.k, sv, si))
             finish_row(v, lane, p.E, p.k, p.renorm, __shfl_sync(0xffffffffu, sv, 0), sv, si, p.ids + t * p.k,
                        p.weights + t * p.k);
         else
@@ -184,7 +199,7 @@ few_gate_up_kernel(const FewParams p) {
     __shared__ FewPlan s;
     pdl_wait();
     pdl_launch_next();
-    build_plan<(W + 1) * 32, 8 * NT>(s, p, p.logits != nullptr, blockIdx.x == 0);
+    build_plan<W + 1, 8 * NT>(s, p, p.logits != nullptr, blockIdx.x == 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (warp == W) {  // beside the products: the routing outputs, one row per CTA
         if (p.logits) publish_routing(p, blockIdx.x, gridDim.x, lane);
@@ -192,16 +207,21 @@ few_gate_up_kernel(const FewParams p) {
         return;
     }
     const int I = p.I, K = p.H;
-    const int64_t shares = static_cast<int64_t>(s.n) * (I / U::ALIGN);  // row = entry * I + i
-    const int r0 = static_cast<int>(shares * blockIdx.x / gridDim.x) * U::ALIGN;
-    const int r1 = static_cast<int>(shares * (blockIdx.x + 1) / gridDim.x) * U::ALIGN;
+    // The CTA's rows, row = entry * I + i. Where items are many, shares of whole
+    // items: the quantised formats take as long for part of one.
+    const int whole = !FewShape<FMT>::DENSE && I % ROWS == 0 && s.n * (I / ROWS) >= 8 * static_cast<int>(gridDim.x);
+    const int align = whole ? ROWS : U::ALIGN;
+    int r0, r1;
+    part_of(s.n * (I / align), gridDim.x, blockIdx.x, r0, r1);
+    r0 *= align;
+    r1 *= align;
     const int nk = (K + U::SPAN - 1) / U::SPAN;
     // items: up to ROWS consecutive rows of one entry
     const int ti0 = r0 / I, i0 = r0 - ti0 * I, per = (I + ROWS - 1) / ROWS;
     const int f_rows = min(r1 - r0, I - i0), f_items = (f_rows + ROWS - 1) / ROWS;
     const int rest = r1 - r0 - f_rows;
-    const int64_t units = static_cast<int64_t>(f_items + rest / I * per + (rest % I + ROWS - 1) / ROWS) * nk;
-    auto first_unit = [&](int w) { return static_cast<int>(units * w / W); };
+    const int units = (f_items + rest / I * per + (rest % I + ROWS - 1) / ROWS) * nk;
+    auto first_unit = [&](int w) { return units / W * w + min(w, units % W); };
     auto locate = [&](int q, int& ti, int& i) {  // item q of the CTA
         if (q < f_items) {
             ti = ti0;
@@ -419,20 +439,22 @@ few_down_kernel(const FewParams p) {
     // ids it left.
     constexpr bool BESIDE = FewShape<FMT>::RESIDENT > 1;
     if (!BESIDE) pdl_wait();
-    build_plan<W * 32, 8 * NT>(s, p, BESIDE && p.logits != nullptr, false);
+    build_plan<W, 8 * NT>(s, p, BESIDE && p.logits != nullptr, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
-    const int64_t shares = p.H / U::ALIGN;
-    const int n0 = static_cast<int>(shares * blockIdx.x / gridDim.x) * U::ALIGN;
-    const int n1 = static_cast<int>(shares * (blockIdx.x + 1) / gridDim.x) * U::ALIGN;
+    int n0, n1;
+    part_of(p.H / U::ALIGN, gridDim.x, blockIdx.x, n0, n1);
+    n0 *= U::ALIGN;
+    n1 *= U::ALIGN;
     const int ntiles = (n1 - n0 + 15) / 16;
     const int nks = (K + U::SPAN - 1) / U::SPAN;
     float* mine = sums + warp * p.T * 17;
     for (int i = tid; i < W * p.T * 17; i += W * 32) sums[i] = 0.0f;
 
     // A tile's units (entry, contraction step): this warp's share is the same in every tile
-    const int64_t units = static_cast<int64_t>(n) * nks;
-    const int u0 = static_cast<int>(units * warp / W), count = static_cast<int>(units * (warp + 1) / W) - u0;
+    int u0, u1;
+    part_of(n * nks, W, warp, u0, u1);
+    const int count = u1 - u0;
     const int ti_first = u0 / nks, ks_first = u0 - ti_first * nks;
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
 
@@ -491,7 +513,7 @@ few_down_kernel(const FewParams p) {
         advance(l);
     }
     if (BESIDE) pdl_wait();  // h and the routing outputs are complete
-    slot_weights<W * 32>(s, p);
+    slot_weights<W>(s, p);
     {
         Pos q = start;
         for (int d = 0; d < RING - 1; ++d) {

@@ -102,46 +102,53 @@ __device__ __forceinline__ void route_row(const float (&v)[kPerLane], int lane, 
     finish_row(v, lane, E, k, renorm, sel_v[0], sv, si, ids_row, w_row);
 }
 
-// The selection of route_row by integer reductions: lane r < k gets the r-th
-// expert si and its logit sv. Each round takes the largest remaining logit as
-// an order-preserving integer with one warp reduction, and the lowest index
-// that holds it with a second. Returns false, with nothing selected, for a row
-// that holds a NaN: route_row's comparisons are not an order then. (route_row
-// itself took about 8 us of a one-token layer when every CTA ran it: its 16
-// unrolled rounds of shuffles, and the fp64 exponential, which runs on few
-// units per SM.)
-__device__ __forceinline__ bool select_row(const float (&v)[kPerLane], int lane, int E, int k, float& sv, int& si) {
+// The selection of route_row by integer reductions, for E <= 32 PER: lane r < k
+// gets the r-th expert si and its logit sv. Each round takes the largest
+// remaining logit as an order-preserving integer with one warp reduction, and
+// the lowest index that holds it with a second. Returns false, with nothing
+// selected, for a row that holds a NaN: route_row's comparisons are not an
+// order then. (route_row itself took about 8 us of a one-token layer when
+// every CTA ran it: its 16 unrolled rounds of shuffles, and the fp64
+// exponential, which runs on few units per SM.)
+template <int PER>
+__device__ __forceinline__ bool select_row_n(const float* __restrict__ lrow, int lane, int E, int k, float& sv,
+                                             int& si) {
     bool nan = false;
-    uint32_t key[kPerLane];
+    uint32_t key[PER];
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
-        nan |= lane + 32 * j < E && v[j] != v[j];
-        const uint32_t b = __float_as_uint(__fadd_rn(v[j], 0.0f));  // -0 counts as 0
-        key[j] = lane + 32 * j < E ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;  // 0: absent or taken
+    for (int j = 0; j < PER; ++j) {
+        const bool in = lane + 32 * j < E;
+        const float v = in ? __ldg(lrow + lane + 32 * j) : 0.0f;
+        nan |= v != v;
+        const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 counts as 0
+        key[j] = in ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;  // 0: absent or taken
     }
     if (__any_sync(0xffffffffu, nan)) return false;
     sv = 0.0f;
     si = 0;
+#pragma unroll 1
     for (int r = 0; r < k; ++r) {
-        uint32_t bk = 0;
-        int bi = 0;
+        uint32_t bk = key[0];
 #pragma unroll
-        for (int j = 0; j < kPerLane; ++j)
-            if (key[j] > bk) {
-                bk = key[j];
-                bi = lane + 32 * j;
-            }
+        for (int j = 1; j < PER; ++j) bk = max(bk, key[j]);
         const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-        const int at = static_cast<int>(__reduce_min_sync(0xffffffffu, bk == top ? static_cast<uint32_t>(bi) : ~0u));
+        uint32_t mine = ~0u;
+#pragma unroll
+        for (int j = PER - 1; j >= 0; --j)
+            if (key[j] == top) mine = lane + 32 * j;
+        const uint32_t at = __reduce_min_sync(0xffffffffu, mine);
         if (lane == r) {
-            si = at;
+            si = static_cast<int>(at);
             sv = __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
         }
 #pragma unroll
-        for (int j = 0; j < kPerLane; ++j)
+        for (int j = 0; j < PER; ++j)
             if (lane + 32 * j == at) key[j] = 0u;
     }
     return true;
+}
+__device__ __forceinline__ bool select_row(const float* lrow, int lane, int E, int k, float& sv, int& si) {
+    return E <= 128 ? select_row_n<4>(lrow, lane, E, k, sv, si) : select_row_n<kPerLane>(lrow, lane, E, k, sv, si);
 }
 
 }  // namespace moe
