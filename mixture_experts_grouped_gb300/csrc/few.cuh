@@ -18,11 +18,13 @@
 //            finishes an item (16 or 32 such rows, the whole contraction) by
 //            itself; items cut between warps are added once, at the end, in
 //            warp order.
-//   down     columns [n0, n1) of every touched expert, so the weighted sum
-//            over the experts stays inside the CTA: each warp keeps its own
-//            f32 sums per token in shared memory and adds an expert's products,
-//            times the weight, when it leaves that expert; the warps' sums are
-//            added in warp order.
+//   down     a pair of CTAs takes columns [n0, n1) of every touched expert, so
+//            the weighted sum over the experts stays inside the pair: each warp
+//            keeps its own f32 sums per token in shared memory and adds an
+//            expert's products, times the weight, when it leaves that expert;
+//            the warps' sums are added in warp order, and the two CTAs' through
+//            distributed shared memory. (One CTA per column share had 13 rows
+//            of 2048 columns: half of a unit's rows.)
 // No atomics on values: results do not depend on timing. The down kernel is
 // launched early (programmatic dependent launch): its plan and first weight
 // copies need nothing of the gate/up kernel, only the token operand waits.
@@ -45,10 +47,11 @@ template <int FMT> struct FewShape {
     static constexpr bool DENSE = FMT == MOE_W_BF16, GPTQ = FMT == MOE_W_GPTQ_INT4;
     static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
     static constexpr int GU_RING = FMT == MOE_W_FP8_E4M3 ? 5 : 4;
-    static constexpr int DN_RING = DENSE ? 4 : (FMT == MOE_W_FP8_E4M3 ? 5 : 8);
+    static constexpr int DN_RING = 4;
     static constexpr int RESIDENT = DENSE ? 2 : 1;  // CTAs per SM the registers must allow
 };
 constexpr int kFewEntries = MOE_MAX_EXPERTS + kFewPairs / 8;
+constexpr int kFewCols = 33;  // columns of a down tile, and a pad
 
 struct FewPlan {
     int n;                           // entries: touched experts, ascending, split
@@ -403,25 +406,32 @@ few_gate_up_kernel(const FewParams p) {
 
 // ---- down ---------------------------------------------------------------------------
 
-// The end of a 16-column tile: adds the warps' sums in warp order, writes the
-// columns and clears the sums for the next tile.
+// The end of a tile of up to 32 columns: adds the warps' sums in warp order and
+// clears them, then the two CTAs', half of the tile each, and writes it.
 template <int ACT, int W>
-__device__ __noinline__ void few_tile_end(float* sums, uint16_t* out, int T, int H, int n0, int n1) {
+__device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* out, int T, int H, int n0, int n1,
+                                          uint32_t rank) {
     __syncthreads();
-    for (int i = threadIdx.x; i < T * 16; i += W * 32) {
-        const int tok = i >> 4, col = i & 15;
+    for (int i = threadIdx.x; i < T * 32; i += W * 32) {
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            float& part = sums[(w * T + tok) * 17 + col];
+            float& part = sums[w * T * kFewCols + (i >> 5) * kFewCols + (i & 31)];
             v += part;
             part = 0.0f;
         }
-        if (n0 + col < n1)
-            reinterpret_cast<typename Act<ACT>::T*>(out)[static_cast<size_t>(tok) * H + n0 + col] =
+        both[i] = v;
+    }
+    cluster_sync_all();
+    const uint32_t peer = mapa_shared(smem_u32(both), rank ^ 1);
+    for (int i = threadIdx.x + rank * T * 16; i < static_cast<int>(rank + 1) * T * 16; i += W * 32) {
+        const float a = both[i], b = ld_dsmem_f32(peer + 4 * i);
+        const float v = rank == 0 ? a + b : b + a;
+        if (n0 + (i & 31) < n1)
+            reinterpret_cast<typename Act<ACT>::T*>(out)[static_cast<size_t>(i >> 5) * H + n0 + (i & 31)] =
                 Act<ACT>::from_f(v);
     }
-    __syncthreads();
+    cluster_sync_all();  // neither CTA reuses `both` or leaves while the other reads it
 }
 
 template <int FMT, int ACT, int NT>
@@ -429,10 +439,14 @@ __global__ void __launch_bounds__(FewShape<FMT>::DN_WARPS * 32, FewShape<FMT>::R
 few_down_kernel(const FewParams p) {
     using U = Unit<FMT, ACT, false>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT>::DN_RING, W = FewShape<FMT>::DN_WARPS;
+    constexpr int RING = FewShape<FMT>::DN_RING, W = FewShape<FMT>::DN_WARPS, MT = U::MT;
+    static_assert(U::ROWS == 32, "32 columns a tile");
     extern __shared__ uint8_t few_smem[];
-    float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][17]: sums of 16 columns
+    float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][kFewCols]
+    float* both = sums + W * p.T * kFewCols;                                 // [T][32]: this CTA's sums of a tile
     __shared__ FewPlan s;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // Beside the gate/up kernel: only what was complete before that started
     // (logits, or ids given as inputs) and the weights are read before the wait.
     // Otherwise this CTA starts when that kernel is all but done, and takes the
@@ -443,17 +457,17 @@ few_down_kernel(const FewParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
     int n0, n1;
-    part_of(p.H / U::ALIGN, gridDim.x, blockIdx.x, n0, n1);
+    part_of(p.H / U::ALIGN, pairs, pair, n0, n1);
     n0 *= U::ALIGN;
     n1 *= U::ALIGN;
-    const int ntiles = (n1 - n0 + 15) / 16;
+    const int ntiles = (n1 - n0 + 31) / 32;
     const int nks = (K + U::SPAN - 1) / U::SPAN;
-    float* mine = sums + warp * p.T * 17;
-    for (int i = tid; i < W * p.T * 17; i += W * 32) sums[i] = 0.0f;
+    float* mine = sums + warp * p.T * kFewCols;
+    for (int i = tid; i < W * p.T * kFewCols; i += W * 32) sums[i] = 0.0f;
 
-    // A tile's units (entry, contraction step): this warp's share is the same in every tile
+    // A tile's units (entry, contraction step), shared by the pair's warps: this warp's share is the same in every tile
     int u0, u1;
-    part_of(n * nks, W, warp, u0, u1);
+    part_of(n * nks, 2 * W, static_cast<int>(rank) * W + warp, u0, u1);
     const int count = u1 - u0;
     const int ti_first = u0 / nks, ks_first = u0 - ti_first * nks;
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
@@ -492,7 +506,7 @@ few_down_kernel(const FewParams p) {
     auto fetch_w = [&](uint8_t* st, Pos& q) {
         if (enter(q)) {
             const WBase b = expert_base<FMT>(p.down.w, p.down.scales, p.down.zeros, p.H, K, p.down.group_size, s.te[q.ti]);
-            const int a = n0 + 16 * q.tile;
+            const int a = n0 + 32 * q.tile;
             src.aim(b, a, n1 - a, a + 8, n1 - a - 8, q.k, lane);
         }
         if (q.kleft >= U::SPAN) src.load(st, lane);
@@ -527,10 +541,10 @@ few_down_kernel(const FewParams p) {
     }
     __syncthreads();  // the slots' weights, and the sums are zero
 
-    float acc[1][NT][4];
+    float acc[MT][NT][4];
     int stage = 0;
     for (int tile = 0; tile < ntiles; ++tile) {
-        const int a = n0 + 16 * tile;
+        const int a = n0 + 32 * tile;
         int left = count, ti = ti_first, ks = ks_first;
         while (left > 0) {  // one entry's units
             const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = NT > 1 && ns > 8 ? 2 : 1, e = s.te[ti];
@@ -541,16 +555,19 @@ few_down_kernel(const FewParams p) {
             const uint16_t* x1 = has1 ? x0 + static_cast<size_t>(8) * K : x0;
             Tokens<U> x;
             x.clear();
+            float f[MT][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[0][t][0] = acc[0][t][1] = acc[0][t][2] = acc[0][t][3] = 0.0f;
-            const int ra = U::row_a(0, g), rb = U::row_b(g);
-            float f0 = U::SCALE_UP, f1 = U::SCALE_UP;
-            if (U::ROW_SCALE) {
-                const float* sc = static_cast<const float*>(p.down.scales) + static_cast<size_t>(p.H) * e + a;
-                f0 = a + ra < n1 ? __ldg(sc + ra) : 0.0f;
-                f1 = a + rb < n1 ? __ldg(sc + rb) : 0.0f;
+            for (int m = 0; m < MT; ++m) {
+                f[m][0] = f[m][1] = U::SCALE_UP;
+                if (U::ROW_SCALE) {
+                    const float* sc = static_cast<const float*>(p.down.scales) + static_cast<size_t>(p.H) * e + a;
+                    f[m][0] = a + U::row_a(m, g) < n1 ? __ldg(sc + U::row_a(m, g)) : 0.0f;
+                    f[m][1] = a + U::row_b(m, g) < n1 ? __ldg(sc + U::row_b(m, g)) : 0.0f;
+                }
+                if (FMT == MOE_W_NVFP4) f[m][0] = f[m][1] = U::SCALE_UP * __ldg(p.down.scale2 + e);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[m][t][0] = acc[m][t][1] = acc[m][t][2] = acc[m][t][3] = 0.0f;
             }
-            if (FMT == MOE_W_NVFP4) f0 = f1 = U::SCALE_UP * __ldg(p.down.scale2 + e);
             int kleft = K - ks * U::SPAN;
             for (; ks < stop; ++ks) {
                 if (!U::X_RING) x.fetch(x0, has, kleft, lane);
@@ -583,10 +600,14 @@ few_down_kernel(const FewParams p) {
                 for (int q = 0; q < 2; ++q) {
                     const int slot = 8 * t + 2 * c + q;
                     if (slot < ns) {
-                        float* dst = mine + s.slot_tok[s0 + slot] * 17;
+                        float* dst = mine + s.slot_tok[s0 + slot] * kFewCols;
                         const float w = s.slot_w[s0 + slot];
-                        dst[ra] = fmaf(w, f0 * acc[0][t][q], dst[ra]);
-                        dst[rb] = fmaf(w, f1 * acc[0][t][2 + q], dst[rb]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            float &da = dst[U::row_a(m, g)], &db = dst[U::row_b(m, g)];
+                            da = fmaf(w, f[m][0] * acc[m][t][q], da);
+                            db = fmaf(w, f[m][1] * acc[m][t][2 + q], db);
+                        }
                     }
                 }
             }
@@ -594,7 +615,7 @@ few_down_kernel(const FewParams p) {
             ks = 0;
             ++ti;
         }
-        few_tile_end<ACT, W>(sums, p.out, p.T, p.H, a, n1);
+        few_tile_end<ACT, W>(sums, both, p.out, p.T, p.H, a, n1, rank);
     }
 }
 
@@ -606,7 +627,8 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     constexpr int gu_smem =
         F::GU_WARPS * (F::GU_RING * Stage<GU>::BYTES + static_cast<int>(sizeof(float4)) * 2 * GU::MT * NT * 32);
     constexpr int dn_ring = F::DN_WARPS * F::DN_RING * Stage<DN>::BYTES;
-    constexpr int dn_most = dn_ring + static_cast<int>(sizeof(float)) * F::DN_WARPS * (NT == 1 ? 8 : 32) * 17;
+    constexpr int dn_token = static_cast<int>(sizeof(float)) * (F::DN_WARPS * kFewCols + 32);
+    constexpr int dn_most = dn_ring + dn_token * (NT == 1 ? 8 : MOE_MAX_FEW_TOKENS);
     static_assert(gu_smem + sizeof(FewPlan) <= 232448 && dn_most + sizeof(FewPlan) <= 232448, "shared memory");
     static int configured_for = -1;
     int dev = 0;
@@ -619,9 +641,22 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     }
     const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::GU_WARPS + 1) * 32, gu_smem, st, p);
     if (e != cudaSuccess) return e;
-    const int cols = p.H / DN::ALIGN;
-    return launch_pdl(few_down_kernel<FMT, ACT, NT>, sms < cols ? sms : cols, F::DN_WARPS * 32,
-                      dn_ring + sizeof(float) * F::DN_WARPS * p.T * 17, st, p);
+    const int cols = p.H / DN::ALIGN, pairs = sms / 2 < cols ? (sms >= 2 ? sms / 2 : 1) : cols;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(F::DN_WARPS * 32);
+    cfg.dynamicSmemBytes = dn_ring + dn_token * p.T;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, few_down_kernel<FMT, ACT, NT>, p);
 }
 
 // up to 8 tokens: one token tile; more: two, and experts of over 16 tokens are listed twice

@@ -97,12 +97,6 @@ inline size_t rt_smem_bytes(const RtPlan& r) {
     return (static_cast<size_t>(rt_wbuf_floats(r)) + static_cast<size_t>(r.s) * r.tt * r.ep) * sizeof(float);
 }
 
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
 template <int ACT, int EG, int TPL>
 __global__ void __launch_bounds__(kRtThreads, EG == 8 ? 4 : (EG == 16 ? 3 : 2))  // E <= 8: one wave at T = 4096
 router_topk_kernel(const typename Act<ACT>::T* __restrict__ x, const float* __restrict__ wr,

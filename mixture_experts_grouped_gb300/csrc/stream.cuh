@@ -12,8 +12,8 @@
 // g + 8, and the products use them as their (2c, 2c + 1) and (2c + 8, 2c + 9)
 // slots; the token operand takes the same k range of token g.
 //
-// A "unit" is what a warp takes at a time: one or several 16-row tiles x SPAN
-// contraction indices, 1 to 2 KB of weights. Units arrive by cp.async in a
+// A "unit" is what a warp takes at a time: two or four 16-row tiles x SPAN
+// contraction indices, 2 KB of weights. Units arrive by cp.async in a
 // ring of shared-memory stages private to the warp. Each lane copies what it
 // will itself read (only scales cross lanes), so a stage needs no barrier
 // beyond the warp's own, and what is in flight takes no registers. (The same
@@ -102,10 +102,10 @@ __device__ __forceinline__ WBase expert_base(const void* w, const void* sc, cons
 
 // Unit<FMT, ACT, GU>: one format's stage layout and fragments, for the gate/up
 // kernel (GU: set a holds gate rows, set b the up rows of the same columns) or
-// the down kernel (both sets are rows of one 16-row tile).
+// the down kernel (set b holds the rows 8 below those of set a).
 //   MT         16-row tiles per unit; SPAN contraction indices; CHUNKS pieces
 //              of 8 contraction indices a lane holds per row
-//   ROWS       rows per set a and item (GU), rows of a tile (down)
+//   ROWS       rows of a unit, of each set (GU) or in all (down)
 //   ALIGN      first rows are multiples of it
 //   row_a / row_b   which rows lane group g has in tile m (row_b: down only)
 //   BYTES      weights and scales of a unit in a stage
@@ -124,17 +124,17 @@ __device__ __forceinline__ WBase expert_base(const void* w, const void* sc, cons
 // nobody reads.
 template <int FMT, int ACT, bool GU> struct Unit;
 
-// Rows of K contiguous elements of EB bits: per lane and row KT times 16 bytes.
-template <int EB, int MT, int KT> struct RowSrc {
-    static constexpr int STEP = 512 / EB;  // contraction indices of one 16-byte piece of the four lanes
+// Rows of K contiguous elements of EB bits, 16 bytes of each row and lane;
+// tiles DOWN rows apart.
+template <int EB, int MT, int DOWN> struct RowSrc {
     const uint8_t* pa;
     const uint8_t* pb;
-    int na, nb, row8;  // tiles in which the lane's rows exist; bytes from a row to the 8th below it
+    int na, nb, tile;  // tiles in which the lane's rows exist; bytes from tile to tile
     __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
         const int g = lane >> 2, k = k0 + (lane & 3) * (128 / EB);
-        na = (n_a - g + 7) >> 3;
-        nb = (n_b - g + 7) >> 3;
-        row8 = b.K * EB;
+        na = (n_a - g + DOWN - 1) / DOWN;
+        nb = (n_b - g + DOWN - 1) / DOWN;
+        tile = b.K * EB / 8 * DOWN;
         pa = b.w + (static_cast<size_t>(a + g) * b.K + k) * EB / 8;
         pb = b.w + (static_cast<size_t>(bb + g) * b.K + k) * EB / 8;
     }
@@ -142,70 +142,62 @@ template <int EB, int MT, int KT> struct RowSrc {
         uint8_t* d = st + 16 * lane;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            if (m < na)
-#pragma unroll
-                for (int t = 0; t < KT; ++t) cp_async16_row(d + (2 * m * KT + t) * 512, pa + m * row8 + t * 64);
-            if (m < nb)
-#pragma unroll
-                for (int t = 0; t < KT; ++t) cp_async16_row(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + t * 64);
+            if (m < na) cp_async16_row(d + 1024 * m, pa + m * tile);
+            if (m < nb) cp_async16_row(d + 1024 * m + 512, pb + m * tile);
         }
     }
     __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const {  // `left` indices to K's end
         uint8_t* d = st + 16 * lane;
-        for (int t = 0; t < KT; ++t) {
-            const bool in = t * STEP + (lane & 3) * (128 / EB) < left;
-            const int o = in ? t * 64 : -16 * (lane & 3);  // a skipped copy reads nothing: the unit's first piece stands in
-            for (int m = 0; m < MT; ++m) {
-                if (m < na) cp_async16_zfill(d + (2 * m * KT + t) * 512, pa + m * row8 + o, in);
-                if (m < nb) cp_async16_zfill(d + ((2 * m + 1) * KT + t) * 512, pb + m * row8 + o, in);
-            }
+        const bool in = (lane & 3) * (128 / EB) < left;
+        const int o = in ? 0 : -16 * (lane & 3);  // a skipped copy reads nothing: the unit's first piece stands in
+        for (int m = 0; m < MT; ++m) {
+            if (m < na) cp_async16_zfill(d + 1024 * m, pa + m * tile + o, in);
+            if (m < nb) cp_async16_zfill(d + 1024 * m + 512, pb + m * tile + o, in);
         }
     }
     __device__ __forceinline__ void step() {
-        pa += 64 * KT;
-        pb += 64 * KT;
+        pa += 64;
+        pb += 64;
     }
 };
 
 template <int ACT, bool GU> struct Unit<MOE_W_BF16, ACT, GU> {
-    static constexpr int MT = GU ? 2 : 1, KT = GU ? 1 : 2, SPAN = 32 * KT, CHUNKS = KT, BYTES = 2048;
-    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
+    static constexpr int MT = 2, SPAN = 32, CHUNKS = 1, BYTES = 1024 * MT;
+    static constexpr int DOWN = GU ? 8 : 16, ROWS = DOWN * MT, ALIGN = 1;
     static constexpr bool X_RING = true, X_PERM = false, GROUPED = false, ROW_SCALE = false;
     static constexpr float SCALE_UP = 1.0f;
-    struct Src : RowSrc<16, MT, KT> {};
-    uint4 r[MT][2][KT];
-    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
-    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    struct Src : RowSrc<16, MT, DOWN> {};
+    uint4 r[MT][2];
+    static __device__ __forceinline__ int row_a(int m, int g) { return DOWN * m + g; }
+    static __device__ __forceinline__ int row_b(int m, int g) { return DOWN * m + 8 + g; }
     __device__ __forceinline__ void open(const uint8_t* st, int, int, int lane) {
 #pragma unroll
-        for (int q = 0; q < 2 * MT * KT; ++q)
-            r[q / (2 * KT)][q / KT % 2][q % KT] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
+        for (int q = 0; q < 2 * MT; ++q) r[q / 2][q % 2] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
     }
     static __device__ __forceinline__ int k_of(int i, int c) { return 8 * c + 32 * i; }
-    __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        a[0] = r[m][0][i].x; a[1] = r[m][0][i].y; a[2] = r[m][0][i].z; a[3] = r[m][0][i].w;
-        b[0] = r[m][1][i].x; b[1] = r[m][1][i].y; b[2] = r[m][1][i].z; b[3] = r[m][1][i].w;
+    __device__ __forceinline__ void frag(int, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+        a[0] = r[m][0].x; a[1] = r[m][0].y; a[2] = r[m][0].z; a[3] = r[m][0].w;
+        b[0] = r[m][1].x; b[1] = r[m][1].y; b[2] = r[m][1].z; b[3] = r[m][1].w;
     }
     __device__ __forceinline__ float scale(int, int, int) const { return 1.0f; }
 };
 
 template <int ACT, bool GU> struct Unit<MOE_W_FP8_E4M3, ACT, GU> {
-    static constexpr int MT = GU ? 2 : 1, KT = GU ? 1 : 2, SPAN = 64 * KT, CHUNKS = 2 * KT, BYTES = 2048;
-    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
+    static constexpr int MT = 2, SPAN = 64, CHUNKS = 2, BYTES = 1024 * MT;
+    static constexpr int DOWN = GU ? 8 : 16, ROWS = DOWN * MT, ALIGN = 1;
     static constexpr bool X_RING = false, X_PERM = false, GROUPED = false, ROW_SCALE = true;
     static constexpr float SCALE_UP = 1.0f;
-    struct Src : RowSrc<8, MT, KT> {};
-    uint4 r[MT][2][KT];
-    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
-    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    struct Src : RowSrc<8, MT, DOWN> {};
+    uint4 r[MT][2];
+    static __device__ __forceinline__ int row_a(int m, int g) { return DOWN * m + g; }
+    static __device__ __forceinline__ int row_b(int m, int g) { return DOWN * m + 8 + g; }
     __device__ __forceinline__ void open(const uint8_t* st, int, int, int lane) {
 #pragma unroll
-        for (int q = 0; q < 2 * MT * KT; ++q)
-            r[q / (2 * KT)][q / KT % 2][q % KT] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
+        for (int q = 0; q < 2 * MT; ++q) r[q / 2][q % 2] = *reinterpret_cast<const uint4*>(st + 512 * q + 16 * lane);
     }
-    static __device__ __forceinline__ int k_of(int i, int c) { return 16 * c + 8 * (i & 1) + 64 * (i >> 1); }
+    static __device__ __forceinline__ int k_of(int i, int c) { return 16 * c + 8 * i; }
     __device__ __forceinline__ void frag(int i, int m, uint32_t (&a)[4], uint32_t (&b)[4]) const {
-        const uint4 &u = r[m][0][i >> 1], &v = r[m][1][i >> 1];
+        const uint4 &u = r[m][0], &v = r[m][1];
         e4m3x4_to_act<ACT>(i & 1 ? u.z : u.x, a[0], a[1]);
         e4m3x4_to_act<ACT>(i & 1 ? u.w : u.y, a[2], a[3]);
         e4m3x4_to_act<ACT>(i & 1 ? v.z : v.x, b[0], b[1]);
@@ -215,9 +207,8 @@ template <int ACT, bool GU> struct Unit<MOE_W_FP8_E4M3, ACT, GU> {
 };
 
 // NVFP4: the block scales lie along n, one byte each. For each of the unit's 8
-// blocks a stage holds the aligned words around the rows of set a and of set b:
-// WS words a set, 16 WS words in all, two per lane (half of the lanes, where WS
-// is 3).
+// blocks a stage holds the aligned words around the unit's rows: WS words for
+// each of SETS runs of rows (gate and up), three words a lane at most.
 //
 // To bf16, a pair of codes takes two shifts and two logic operations: sign to
 // bit 15, exponent and mantissa to bits 8..6, which is the code's value times
@@ -225,37 +216,37 @@ template <int ACT, bool GU> struct Unit<MOE_W_FP8_E4M3, ACT, GU> {
 // (448 * 2^118 is the most that fits) and the finished sums the other 2^8; the
 // product is exact, as 6 significant bits are.
 template <int ACT, bool GU> struct Unit<MOE_W_NVFP4, ACT, GU> {
-    static constexpr int MT = GU ? 2 : 1, SPAN = 128, CHUNKS = 4;
-    static constexpr int ROWS = 8 * (GU ? MT : 2), ALIGN = 1;
-    static constexpr int WS = GU ? 5 : 3;  // words around 8 MT unaligned bytes
-    static constexpr int SC_AT = 1024 * MT, BYTES = SC_AT + 16 * WS * 4;
+    static constexpr int MT = 2, SPAN = 128, CHUNKS = 4;
+    static constexpr int DOWN = GU ? 8 : 16, ROWS = DOWN * MT, ALIGN = 1;
+    static constexpr int SETS = GU ? 2 : 1, WS = ROWS / 4 + 1;  // words around ROWS unaligned bytes
+    static constexpr int WORDS = 8 * SETS * WS, SC_AT = 1024 * MT, BYTES = SC_AT + WORDS * 4;
     static constexpr bool X_RING = false, X_PERM = ACT == MOE_ACT_BF16, GROUPED = false, ROW_SCALE = false;
     static constexpr float SCALE_UP = ACT == MOE_ACT_BF16 ? 256.0f : 1.0f;
-    static constexpr int PIECES = (16 * WS + 31) / 32;
-    struct Src : RowSrc<4, MT, 1> {
+    static constexpr int PIECES = (WORDS + 31) / 32;
+    struct Src : RowSrc<4, MT, DOWN> {
         const uint8_t* ps[PIECES];
         uint32_t ok;  // bit h: piece h exists
         int row_step;
         __device__ __forceinline__ void aim(const WBase& b, int a, int n_a, int bb, int n_b, int k0, int lane) {
-            RowSrc<4, MT, 1>::aim(b, a, n_a, bb, n_b, k0, lane);
+            RowSrc<4, MT, DOWN>::aim(b, a, n_a, bb, n_b, k0, lane);
             row_step = 8 * b.N;
             ok = 0;
 #pragma unroll
             for (int h = 0; h < PIECES; ++h) {
                 const int p = lane + 32 * h, set = p / (8 * WS), q = p - 8 * WS * set;
                 const int n = ((set ? bb : a) & ~3) + 4 * (q % WS);
-                if (p < 16 * WS && n < b.N) ok |= 1u << h;
+                if (p < WORDS && n < b.N) ok |= 1u << h;
                 ps[h] = b.sc + static_cast<size_t>(k0 / 16 + q / WS) * b.N + n;
             }
         }
         __device__ __forceinline__ void load(uint8_t* st, int lane) const {
-            RowSrc<4, MT, 1>::load(st, lane);
+            RowSrc<4, MT, DOWN>::load(st, lane);
 #pragma unroll
             for (int h = 0; h < PIECES; ++h)
                 if (ok >> h & 1) cp_async4(st + SC_AT + 128 * h + 4 * lane, ps[h]);
         }
         __device__ __forceinline__ void load_tail(uint8_t* st, int left, int lane) const {
-            RowSrc<4, MT, 1>::load_tail(st, left, lane);
+            RowSrc<4, MT, DOWN>::load_tail(st, left, lane);
             for (int h = 0; h < PIECES; ++h) {
                 // a scale past the end meets zero codes, but must not be a NaN
                 const int kb = (lane + 32 * h) % (8 * WS) / WS;
@@ -265,15 +256,15 @@ template <int ACT, bool GU> struct Unit<MOE_W_NVFP4, ACT, GU> {
             }
         }
         __device__ __forceinline__ void step() {
-            RowSrc<4, MT, 1>::step();
+            RowSrc<4, MT, DOWN>::step();
 #pragma unroll
             for (int h = 0; h < PIECES; ++h) ps[h] += row_step;
         }
     };
     uint4 r[MT][2];
     uint32_t s2[MT][2][2];  // the two block scales of the lane's 32 codes, each twice in a word
-    static __device__ __forceinline__ int row_a(int m, int g) { return 8 * m + g; }
-    static __device__ __forceinline__ int row_b(int g) { return 8 + g; }
+    static __device__ __forceinline__ int row_a(int m, int g) { return DOWN * m + g; }
+    static __device__ __forceinline__ int row_b(int m, int g) { return DOWN * m + 8 + g; }
     __device__ __forceinline__ void open(const uint8_t* st, int a, int b, int lane) {
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -281,7 +272,8 @@ template <int ACT, bool GU> struct Unit<MOE_W_NVFP4, ACT, GU> {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 r[m][h] = *reinterpret_cast<const uint4*>(st + 512 * (2 * m + h) + 16 * lane);
-                const uint8_t* s = st + SC_AT + (h * 8 + 2 * c) * WS * 4 + ((h ? b : a) & 3) + 8 * m + g;
+                const uint8_t* s = GU ? st + SC_AT + (h * 8 + 2 * c) * WS * 4 + ((h ? b : a) & 3) + 8 * m + g
+                                      : st + SC_AT + 2 * c * WS * 4 + (a & 3) + 16 * m + 8 * h + g;
                 uint32_t f;
                 asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
                     : "=r"(f)
@@ -328,20 +320,20 @@ template <int ACT, bool GU> struct Unit<MOE_W_NVFP4, ACT, GU> {
     __device__ __forceinline__ float scale(int, int, int) const { return 1.0f; }
 };
 
-// GPTQ: the words of 8 k values lie along n, so a lane copies V neighbouring
-// columns' words at once and they go to V different rows of its fragments.
-//   gate/up  V = 4 (16 bytes): lane group g has columns 4g .. 4g + 3, one in
-//            each of four tiles; an item is 32 columns, a 128-byte line per
-//            k word (with 8 columns an item, DRAM read 3.3 times the weights)
-//   down     V = 2 (8 bytes): columns 2g and 2g + 1 are rows g and g + 8
+// GPTQ: the words of 8 k values lie along n, so a lane copies four neighbouring
+// columns' words at once and they go to four different rows of its fragments:
+//   gate/up  lane group g has columns 4g .. 4g + 3, one in each of four tiles
+//            (32 columns an item, a 128-byte line per k word; with 8 columns an
+//            item, DRAM read 3.3 times the weights)
+//   down     columns 4g .. 4g + 3 are rows g and g + 8 of two tiles
 // The fragments hold the integers q - z (exact), and the group's f16 scale
 // multiplies the f32 sums of each 64 contraction indices (a divisor of every
-// group). Per 64 indices a lane group's V scales and its zero-point word are
+// group). Per 64 indices a lane group's four scales and its zero-point word are
 // copied by one lane each: lane c = 0 / 1 scales of set a / b, 2 / 3 zeros.
 template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
-    static constexpr int V = GU ? 4 : 2, SETS = GU ? 2 : 1, KT = GU ? 1 : 2;  // KT: pieces of 64 indices
-    static constexpr int MT = GU ? 4 : 1, SPAN = 64 * KT, CHUNKS = 2 * KT;
-    static constexpr int ROWS = GU ? 32 : 16, ALIGN = V;
+    static constexpr int V = 4, SETS = GU ? 2 : 1, KT = GU ? 1 : 2;  // KT: pieces of 64 indices
+    static constexpr int MT = GU ? 4 : 2, SPAN = 64 * KT, CHUNKS = 2 * KT;
+    static constexpr int ROWS = 32, ALIGN = V;
     static constexpr int PIECE = 32 * 4 * V;                    // bytes of one k word of all lanes
     static constexpr int SC_AT = 2 * KT * SETS * PIECE;         // then, per 64 indices and set: scales, zeros
     static constexpr int SC_SET = 8 * (2 * V + 4), BYTES = SC_AT + KT * SETS * SC_SET;
@@ -373,12 +365,6 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
             }
             pg += static_cast<size_t>(group) * gstep;
         }
-        static __device__ __forceinline__ void copy(void* d, const uint8_t* s, bool in) {
-            if (V == 4) cp_async16_zfill(d, s, in);
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(d)), "l"(s), "r"(in ? 8 : 0)
-                             : "memory");
-        }
         __device__ __forceinline__ void load_n(uint8_t* st, int left, int lane) {
             uint8_t* d = st + 4 * V * lane;
             const int half = 16 * N;  // 4 k words on
@@ -387,22 +373,22 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
                 const bool in = 64 * t < left;
                 const uint8_t* w = in ? p + 2 * t * half : p;
                 if (va) {
-                    copy(d + 2 * t * PIECE, w, in);
-                    copy(d + (2 * t + 1) * PIECE, w + half, in);
+                    cp_async16_zfill(d + 2 * t * PIECE, w, in);
+                    cp_async16_zfill(d + (2 * t + 1) * PIECE, w + half, in);
                 }
                 if (GU && vb) {
-                    copy(d + 2 * PIECE, w + db, in);
-                    copy(d + 3 * PIECE, w + db + half, in);
+                    cp_async16_zfill(d + 2 * PIECE, w + db, in);
+                    cp_async16_zfill(d + 3 * PIECE, w + db + half, in);
                 }
                 if (vg) {
                     const int g = lane >> 2, c = lane & 3;
                     uint8_t* s = st + SC_AT + (t * SETS + (GU ? c & 1 : 0)) * SC_SET;
-                    if (c >= 2) cp_async4_zfill(s + 16 * V + 4 * g, pg, in);
-                    else if (V == 4)
+                    if (c >= 2)
+                        cp_async4_zfill(s + 16 * V + 4 * g, pg, in);
+                    else
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(s + 8 * g)), "l"(pg),
                                      "r"(in ? 8 : 0)
                                      : "memory");
-                    else cp_async4_zfill(s + 4 * g, pg, in);
                 }
                 // on by 64 indices; not past the end, where the last group stands in for a copy of nothing
                 if (--rest == 0) {
@@ -418,8 +404,8 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
     uint32_t w[KT][2][SETS][V];
     uint32_t z[KT][SETS];  // the V zero points, 4 bits each
     uint2 s[KT][SETS];     // the V scales
-    static __device__ __forceinline__ int row_a(int m, int g) { return GU ? 4 * g + m : 2 * g; }
-    static __device__ __forceinline__ int row_b(int g) { return 2 * g + 1; }
+    static __device__ __forceinline__ int row_a(int m, int g) { return GU ? 4 * g + m : 4 * g + 2 * m; }
+    static __device__ __forceinline__ int row_b(int m, int g) { return 4 * g + 2 * m + 1; }
     __device__ __forceinline__ void open(const uint8_t* st, int a, int b, int lane) {
         const int g = lane >> 2;
 #pragma unroll
@@ -428,22 +414,14 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
             for (int q = 0; q < SETS; ++q) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint8_t* d = st + (2 * (t * SETS + q) + i) * PIECE + 4 * V * lane;
-                    if (V == 4) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(d);
-                        w[t][i][q][0] = u.x;
-                        w[t][i][q][1] = u.y;
-                        w[t][i][q][V - 2] = u.z;
-                        w[t][i][q][V - 1] = u.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(d);
-                        w[t][i][q][0] = u.x;
-                        w[t][i][q][1] = u.y;
-                    }
+                    const uint4 u = *reinterpret_cast<const uint4*>(st + (2 * (t * SETS + q) + i) * PIECE + 16 * lane);
+                    w[t][i][q][0] = u.x;
+                    w[t][i][q][1] = u.y;
+                    w[t][i][q][2] = u.z;
+                    w[t][i][q][3] = u.w;
                 }
                 const uint8_t* sc = st + SC_AT + (t * SETS + q) * SC_SET;
-                if (V == 4) s[t][q] = *reinterpret_cast<const uint2*>(sc + 8 * g);
-                else s[t][q].x = *reinterpret_cast<const uint32_t*>(sc + 4 * g);
+                s[t][q] = *reinterpret_cast<const uint2*>(sc + 8 * g);
                 z[t][q] = *reinterpret_cast<const uint32_t*>(sc + 16 * V + 4 * g) >> (4 * (((q ? b : a) + V * g) & 7));
             }
     }
@@ -480,13 +458,13 @@ template <int ACT, bool GU> struct Unit<MOE_W_GPTQ_INT4, ACT, GU> {
             row(w[t][i & 1][0][m], (z[t][0] >> (4 * m)) & 15u, a);
             row(w[t][i & 1][SETS - 1][m], (z[t][SETS - 1] >> (4 * m)) & 15u, b);
         } else {
-            row(w[t][i & 1][0][0], z[t][0] & 15u, a);
-            row(w[t][i & 1][0][1], (z[t][0] >> 4) & 15u, b);
+            row(w[t][i & 1][0][(2 * m) & 3], (z[t][0] >> (8 * m)) & 15u, a);
+            row(w[t][i & 1][0][(2 * m + 1) & 3], (z[t][0] >> (8 * m + 4)) & 15u, b);
         }
     }
     // of piece i's group: row a (h = 0) or b of tile m
     __device__ __forceinline__ float scale(int i, int m, int h) const {
-        const int t = i >> 1, v = GU ? m : h;
+        const int t = i >> 1, v = GU ? m : 2 * m + h;
         const uint2& u = s[t][GU ? h * (SETS - 1) : 0];
         const uint32_t word = v < 2 ? u.x : u.y;
         return __half2float(__ushort_as_half(static_cast<unsigned short>(v & 1 ? word >> 16 : word & 0xffffu)));
