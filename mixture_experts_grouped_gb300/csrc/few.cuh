@@ -57,10 +57,16 @@ struct FewPlan {
     int n;                           // entries: touched experts, ascending, split
     int te[kFewEntries];             // expert of each
     int start[kFewEntries + 1];      // first slot of each
-    uint32_t mask[MOE_MAX_EXPERTS];  // by expert id: tokens routed to it
-    int first[MOE_MAX_EXPERTS];      // by expert id: first slot
+    uint32_t mask[MOE_MAX_EXPERTS / 8 * 9];  // by expert id (at(id)): tokens routed to it
+    int first[MOE_MAX_EXPERTS / 8 * 9];      // by expert id: first slot
     float slot_w[kFewPairs];
     uint8_t slot_tok[kFewPairs];
+    // eight ids and a pad: the scan reads eight consecutive ones a lane
+    static __device__ __forceinline__ int at(int id) { return id + (id >> 3); }
+    // the slot of token t with expert id
+    __device__ __forceinline__ int slot_of(int id, int t) const {
+        return first[at(id)] + __popc(mask[at(id)] & ((1u << t) - 1u));
+    }
 };
 
 // [x0, x1): part i of n nearly equal parts of [0, all)
@@ -87,40 +93,55 @@ template <int WARPS, int SLOTS>
 __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool select, bool publish) {
     constexpr int ROUNDS = (MOE_MAX_FEW_TOKENS + WARPS - 1) / WARPS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    static_assert(WARPS * 32 >= MOE_MAX_EXPERTS, "one thread per expert");
-    if (tid < MOE_MAX_EXPERTS) s.mask[tid] = 0;
+    constexpr int MASKS = MOE_MAX_EXPERTS / 8 * 9;
+    for (int i = tid; i < MASKS; i += WARPS * 32) s.mask[i] = 0;
     __syncthreads();
     int ids[ROUNDS];
+    const int mine_n = (p.T - warp + WARPS - 1) / WARPS;  // this warp's tokens
+    if (select) {
+        const float* lrow[ROUNDS];
+        float sv[ROUNDS];
+#pragma unroll
+        for (int q = 0; q < ROUNDS; ++q) lrow[q] = p.logits + (warp + q * WARPS) * p.E;
+        uint32_t nan = 0;
+        if (mine_n == 1) {
+            const float* one[1] = {lrow[0]};
+            float v[1];
+            int id[1];
+            nan = select_rows<1>(one, 1, lane, p.E, p.k, v, id);
+            ids[0] = id[0];
+        } else if (mine_n > 1) {
+            nan = select_rows<ROUNDS>(lrow, mine_n, lane, p.E, p.k, sv, ids);
+        }
+        for (; nan; nan &= nan - 1) {
+            const int bad = __ffs(nan) - 1, t = warp + bad * WARPS;
+            // into scratch of the token's and the warp's own (slot_w and te are filled later)
+            int32_t* scratch = reinterpret_cast<int32_t*>(s.slot_w) + t * MOE_MAX_TOPK;
+            route_row_nan(p.logits + t * p.E, lane, p.E, p.k, p.renorm, scratch,
+                          reinterpret_cast<float*>(s.te) + warp * MOE_MAX_TOPK);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < ROUNDS; ++q)
+                if (q == bad && lane < p.k) ids[q] = scratch[lane];
+        }
+    }
 #pragma unroll
     for (int q = 0; q < ROUNDS; ++q) {
         const int t = warp + q * WARPS;
-        ids[q] = -1;
-        if (t >= p.T) continue;
-        if (select) {
-            const float* lrow = p.logits + t * p.E;
-            float sv;
-            if (!select_row(lrow, lane, p.E, p.k, sv, ids[q])) {
-                // into scratch of the token's own (slot_w is filled later)
-                int32_t* scratch = reinterpret_cast<int32_t*>(s.slot_w) + t * MOE_MAX_TOPK;
-                route_row_nan(lrow, lane, p.E, p.k, p.renorm, scratch, reinterpret_cast<float*>(s.te) + warp * 16);
-                __syncwarp();
-                if (lane < p.k) ids[q] = scratch[lane];
-            }
-        } else if (lane < p.k) {
+        if (!select && q < mine_n && lane < p.k) {
             ids[q] = p.ids[t * p.k + lane];
             if (publish && (ids[q] < 0 || ids[q] >= p.E)) set_err(p.err, MOE_DEV_ERR_EXPERT_ID);
         }
-        if (lane >= p.k || ids[q] < 0 || ids[q] >= p.E) ids[q] = -1;
-        else atomicOr(&s.mask[ids[q]], 1u << t);
+        if (q >= mine_n || lane >= p.k || ids[q] < 0 || ids[q] >= p.E) ids[q] = -1;
+        else atomicOr(&s.mask[s.at(ids[q])], 1u << t);
     }
     __syncthreads();
     if (warp == 0) {
         // prefix sums over the experts, eight consecutive ones a lane: entries in the high half, slots in the low
-        constexpr int PER = MOE_MAX_EXPERTS / 32;
-        uint32_t cnt[PER], mine = 0;
+        uint32_t cnt[8], mine = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            cnt[j] = __popc(s.mask[lane * PER + j]);
+        for (int j = 0; j < 8; ++j) {
+            cnt[j] = __popc(s.mask[lane * 9 + j]);
             mine += ((cnt[j] + SLOTS - 1) / SLOTS << 16) + cnt[j];
         }
         uint32_t inc = mine;
@@ -131,10 +152,10 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
         }
         uint32_t at = inc - mine;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            s.first[lane * PER + j] = at & 0xffffu;
+        for (int j = 0; j < 8; ++j) {
+            s.first[lane * 9 + j] = at & 0xffffu;
             for (uint32_t c = 0; c < cnt[j]; c += SLOTS) {
-                s.te[at >> 16] = lane * PER + j;
+                s.te[at >> 16] = lane * 8 + j;
                 s.start[at >> 16] = at & 0xffffu;
                 at += (1u << 16) + min(cnt[j] - c, static_cast<uint32_t>(SLOTS));
             }
@@ -144,13 +165,11 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
             s.start[inc >> 16] = inc & 0xffffu;
         }
     }
+    static_assert(MOE_MAX_EXPERTS == 256, "eight experts a lane");
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < ROUNDS; ++q) {
-        const int t = warp + q * WARPS;
-        if (ids[q] >= 0)
-            s.slot_tok[s.first[ids[q]] + __popc(s.mask[ids[q]] & ((1u << t) - 1u))] = static_cast<uint8_t>(t);
-    }
+    for (int q = 0; q < ROUNDS; ++q)
+        if (ids[q] >= 0) s.slot_tok[s.slot_of(ids[q], warp + q * WARPS)] = static_cast<uint8_t>(warp + q * WARPS);
     __syncthreads();
 }
 
@@ -169,23 +188,23 @@ template <int WARPS> __device__ __forceinline__ void slot_weights(FewPlan& s, co
             if (same >> j & 1) sum = j == __ffs(same) - 1 ? wj : sum + wj;
         }
         if (lane < p.k && e >= 0 && e < p.E && lane == __ffs(same) - 1)
-            s.slot_w[s.first[e] + __popc(s.mask[e] & ((1u << t) - 1u))] = sum;
+            s.slot_w[s.slot_of(e, t)] = sum;
     }
 }
 
 // One warp: ids and weights of the routing outputs' rows t, t + step, ...
 __device__ __forceinline__ void publish_routing(const FewParams& p, int t, int step, int lane) {
     for (; t < p.T; t += step) {
-        const float* lrow = p.logits + t * p.E;
-        float v[kPerLane], sv;
-        int si;
+        const float* lrow[1] = {p.logits + t * p.E};
+        float v[kPerLane], sv[1];
+        int si[1];
 #pragma unroll
-        for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < p.E ? __ldg(lrow + lane + 32 * j) : 0.0f;
-        if (select_row(lrow, lane, p.E, p.k, sv, si))
-            finish_row(v, lane, p.E, p.k, p.renorm, __shfl_sync(0xffffffffu, sv, 0), sv, si, p.ids + t * p.k,
+        for (int j = 0; j < kPerLane; ++j) v[j] = lane + 32 * j < p.E ? __ldg(lrow[0] + lane + 32 * j) : 0.0f;
+        if (select_rows<1>(lrow, 1, lane, p.E, p.k, sv, si) == 0)
+            finish_row(v, lane, p.E, p.k, p.renorm, __shfl_sync(0xffffffffu, sv[0], 0), sv[0], si[0], p.ids + t * p.k,
                        p.weights + t * p.k);
         else
-            route_row_nan(lrow, lane, p.E, p.k, p.renorm, p.ids + t * p.k, p.weights + t * p.k);
+            route_row_nan(lrow[0], lane, p.E, p.k, p.renorm, p.ids + t * p.k, p.weights + t * p.k);
     }
 }
 
@@ -223,15 +242,16 @@ few_gate_up_kernel(const FewParams p) {
     const int ti0 = r0 / I, i0 = r0 - ti0 * I, per = (I + ROWS - 1) / ROWS;
     const int f_rows = min(r1 - r0, I - i0), f_items = (f_rows + ROWS - 1) / ROWS;
     const int rest = r1 - r0 - f_rows;
-    const int units = (f_items + rest / I * per + (rest % I + ROWS - 1) / ROWS) * nk;
+    const int full = rest / I, units = (f_items + full * per + (rest - full * I + ROWS - 1) / ROWS) * nk;
     auto first_unit = [&](int w) { return units / W * w + min(w, units % W); };
     auto locate = [&](int q, int& ti, int& i) {  // item q of the CTA
         if (q < f_items) {
             ti = ti0;
             i = i0 + ROWS * q;
         } else {
-            ti = ti0 + 1 + (q - f_items) / per;
-            i = ROWS * ((q - f_items) % per);
+            const int e = (q - f_items) / per;
+            ti = ti0 + 1 + e;
+            i = ROWS * (q - f_items - e * per);
         }
     };
     auto row_end = [&](int ti) { return min(I, r1 - ti * I); };
@@ -245,10 +265,12 @@ few_gate_up_kernel(const FewParams p) {
     const int u0 = first_unit(warp), u1 = first_unit(warp + 1);
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
 
+    const int q0 = u0 / nk, ks0 = u0 - q0 * nk;  // where the share begins: item, contraction step
+    int ti, i;
+    locate(q0, ti, i);
     // The copies: units left in the warp's share and in the item, contraction
     // indices to its end
-    int l_left = u1 - u0, l_item = 0, l_k = (u0 % nk) * U::SPAN, l_kleft = 0, lti, li;
-    locate(u0 / nk, lti, li);
+    int l_left = u1 - u0, l_item = 0, l_k = ks0 * U::SPAN, l_kleft = 0, lti = ti, li = i;
     typename U::Src src;
     const uint16_t* lx = nullptr;
     bool l_has = false;
@@ -309,8 +331,7 @@ few_gate_up_kernel(const FewParams p) {
     };
 
     float acc[MT][NT][4];
-    int left = u1 - u0, ks = u0 % nk, stage = 0, ti, i;
-    locate(u0 / nk, ti, i);
+    int left = u1 - u0, ks = ks0, stage = 0;
     while (left > 0) {
         const int s0 = s.start[ti], ns = s.start[ti + 1] - s0, nt = NT > 1 && ns > 8 ? 2 : 1;
         const int end = row_end(ti), begin = ks, stop = min(nk, ks + left);
@@ -376,9 +397,9 @@ few_gate_up_kernel(const FewParams p) {
     __syncthreads();
     // The items cut between warps: the first warp that starts inside an item adds
     // its parts in warp order, from the warp before (where the item begins) on.
-    if (warp == 0 || u0 >= units || u0 % nk == 0 || first_unit(warp - 1) > u0 / nk * nk) return;
-    const int q = u0 / nk, q_end = (q + 1) * nk;
-    locate(q, ti, i);
+    if (warp == 0 || u0 >= units || ks0 == 0 || first_unit(warp - 1) > q0 * nk) return;
+    const int q_end = (q0 + 1) * nk;
+    locate(q0, ti, i);
     const int nt = NT > 1 && s.start[ti + 1] - s.start[ti] > 8 ? 2 : 1;
 #pragma unroll
     for (int m = 0; m < MT; ++m)

@@ -102,53 +102,66 @@ __device__ __forceinline__ void route_row(const float (&v)[kPerLane], int lane, 
     finish_row(v, lane, E, k, renorm, sel_v[0], sv, si, ids_row, w_row);
 }
 
-// The selection of route_row by integer reductions, for E <= 32 PER: lane r < k
-// gets the r-th expert si and its logit sv. Each round takes the largest
+// The selection of route_row by integer reductions, of up to ROWS rows at once
+// (their reductions overlap), for E <= 32 PER: lane r < k gets the r-th expert
+// of row q in si[q] and its logit in sv[q]. Each round takes the largest
 // remaining logit as an order-preserving integer with one warp reduction, and
-// the lowest index that holds it with a second. Returns false, with nothing
-// selected, for a row that holds a NaN: route_row's comparisons are not an
-// order then. (route_row itself took about 8 us of a one-token layer when
-// every CTA ran it: its 16 unrolled rounds of shuffles, and the fp64
+// the lowest index that holds it with a second. Returns the rows that hold a
+// NaN, bit by bit: nothing is selected for them (route_row's comparisons are
+// not an order then). (route_row itself took about 8 us of a one-token layer
+// when every CTA ran it: its 16 unrolled rounds of shuffles, and the fp64
 // exponential, which runs on few units per SM.)
-template <int PER>
-__device__ __forceinline__ bool select_row_n(const float* __restrict__ lrow, int lane, int E, int k, float& sv,
-                                             int& si) {
-    bool nan = false;
-    uint32_t key[PER];
+template <int PER, int ROWS>
+__device__ __forceinline__ uint32_t select_rows_n(const float* const (&lrow)[ROWS], int rows, int lane, int E, int k,
+                                                  float (&sv)[ROWS], int (&si)[ROWS]) {
+    uint32_t key[ROWS][PER], nan = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const bool in = lane + 32 * j < E;
-        const float v = in ? __ldg(lrow + lane + 32 * j) : 0.0f;
-        nan |= v != v;
-        const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 counts as 0
-        key[j] = in ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;  // 0: absent or taken
+    for (int q = 0; q < ROWS; ++q) {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const bool in = q < rows && lane + 32 * j < E;
+            const float v = in ? __ldg(lrow[q] + lane + 32 * j) : 0.0f;
+            bad |= v != v;
+            const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));  // -0 counts as 0
+            // 0: absent or taken
+            key[q][j] = in ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;
+        }
+        nan |= static_cast<uint32_t>(bad) << q;
+        sv[q] = 0.0f;
+        si[q] = 0;
     }
-    if (__any_sync(0xffffffffu, nan)) return false;
-    sv = 0.0f;
-    si = 0;
+    nan = __reduce_or_sync(0xffffffffu, nan);
 #pragma unroll 1
     for (int r = 0; r < k; ++r) {
-        uint32_t bk = key[0];
 #pragma unroll
-        for (int j = 1; j < PER; ++j) bk = max(bk, key[j]);
-        const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-        uint32_t mine = ~0u;
+        for (int q = 0; q < ROWS; ++q) {
+            if (q > 0 && q >= rows) break;
+            uint32_t bk = key[q][0];
 #pragma unroll
-        for (int j = PER - 1; j >= 0; --j)
-            if (key[j] == top) mine = lane + 32 * j;
-        const uint32_t at = __reduce_min_sync(0xffffffffu, mine);
-        if (lane == r) {
-            si = static_cast<int>(at);
-            sv = __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
+            for (int j = 1; j < PER; ++j) bk = max(bk, key[q][j]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+            uint32_t mine = ~0u;
+#pragma unroll
+            for (int j = PER - 1; j >= 0; --j)
+                if (key[q][j] == top) mine = lane + 32 * j;
+            const uint32_t at = __reduce_min_sync(0xffffffffu, mine);
+            if (lane == r) {
+                si[q] = static_cast<int>(at);
+                sv[q] = __uint_as_float((top & 0x80000000u) ? top & 0x7fffffffu : ~top);
+            }
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 32 * j == at) key[q][j] = 0u;
         }
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (lane + 32 * j == at) key[j] = 0u;
     }
-    return true;
+    return nan;
 }
-__device__ __forceinline__ bool select_row(const float* lrow, int lane, int E, int k, float& sv, int& si) {
-    return E <= 128 ? select_row_n<4>(lrow, lane, E, k, sv, si) : select_row_n<kPerLane>(lrow, lane, E, k, sv, si);
+template <int ROWS>
+__device__ __forceinline__ uint32_t select_rows(const float* const (&lrow)[ROWS], int rows, int lane, int E, int k,
+                                                float (&sv)[ROWS], int (&si)[ROWS]) {
+    return E <= 128 ? select_rows_n<4, ROWS>(lrow, rows, lane, E, k, sv, si)
+                    : select_rows_n<kPerLane, ROWS>(lrow, rows, lane, E, k, sv, si);
 }
 
 }  // namespace moe

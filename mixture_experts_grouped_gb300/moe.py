@@ -112,11 +112,7 @@ def exported_names():
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or t.__class__ is int else t.data_ptr()
 
 
 _raw_stream = None  # torch's handle of a device's current stream, looked up on first use

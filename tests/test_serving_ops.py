@@ -327,6 +327,28 @@ def test_few_tokens_keeps_non_finite_experts_and_tokens_apart(moe, dev, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(1, 12, 3), (32, 128, 8), (20, 200, 16), (9, 256, 4), (8, 5, 5)])
+def test_few_tokens_routes_like_the_routing_call(moe, dev, T, E, k):
+    """Ties, infinities, signed zeros and NaN among the logits; every softmax form."""
+    layer, x, _, _, _ = few_layer(moe, dev, "bf16", "bf16", T, 8, 8, E, k, 1, renorm=T % 2 == 0)
+    g = gen(T)
+    logits = torch.randint(-3, 4, (T, E), generator=g).float()
+    logits[0, ::3] = -0.0
+    if T > 5:
+        logits[1, 1] = float("inf")
+        logits[2] = float("-inf")
+        logits[3, E // 2] = float("nan")
+        logits[4] = float("nan")
+        logits[5] = 0.0
+    logits = logits.to(dev)
+    layer.forward(x.to(dev), logits)
+    ids, w = torch.empty_like(layer.topk_ids), torch.empty_like(layer.topk_weights)
+    moe.moe_route_topk_softmax(logits, ids, w, T, E, k, layer.renormalize)
+    assert torch.equal(layer.topk_ids, ids)
+    assert torch.equal(layer.topk_weights.view(torch.int32), w.view(torch.int32))
+
+
+@pytest.mark.gpu
 def test_few_tokens_on_a_stream_and_in_a_graph(moe, dev):
     layer, x, logits, gu, down = few_layer(moe, dev, "bf16", "bf16", 4, 512, 256, 16, 4, 2)
     xs, ls = x.to(dev), logits.to(dev)
