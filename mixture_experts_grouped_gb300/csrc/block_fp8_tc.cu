@@ -14,13 +14,15 @@
 //     round trip of a buffer (MMAs, the signal, reading it back, the signal
 //     back) against the two buffers that 512 TMEM columns hold. So a buffer is
 //     read back by many warps at once, 64 columns each, and nothing else
-//     stands in their way: two warps multiply the scales of a block while its
-//     MMAs run and leave them in shared memory. CTA pairs (M = 256) halve the
+//     stands in their way: a warp fetches the scales of a block while its MMAs
+//     run and leaves them in shared memory. A thread needs about 650 clocks to
+//     wait for, issue and commit a block's MMAs, whatever their width, so two
+//     threads issue, a block each in turn (their buffers are independent). CTA pairs (M = 256) halve the
 //     shared-memory traffic but lengthen every signal by a cluster hop, and
 //     measured slower.
 //   * Finished rows leave through a staging area by TMA stores.
-//   * Roles: warp 0 copies (TMA, 128-byte swizzle), warp 1 issues the MMAs,
-//     warps 2 and 3 multiply scales, the others add and store. Every wait is
+//   * Roles: warp 0 copies (TMA, 128-byte swizzle), warps 1 and 2 issue the
+//     MMAs, warp 3 fetches scales, the others add and store. Every wait is
 //     bounded. At BN = 256 the 20 warps' 96 registers are split 32 / 112
 //     between the first four and the others.
 #include "block_fp8.cuh"
@@ -48,7 +50,7 @@ template <int BN> struct TcShape {
 };
 
 struct TcTail {
-    uint64_t full[8], empty[8], tfull[4], tempty[4], mma_done;
+    uint64_t full[8], empty[8], tfull[4], tempty[4], mma_done[2];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -127,10 +129,10 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < S::NBUF; ++i) {
-            mbar_init(&s.tfull[i], 3);  // the MMAs, and the two warps of its scales
+            mbar_init(&s.tfull[i], 2);  // the MMAs, and its scales
             mbar_init(&s.tempty[i], S::EPI_WARPS);
         }
-        mbar_init(&s.mma_done, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s.mma_done[i], 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -177,17 +179,15 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             const long from = issued > S::STAGES ? issued - S::STAGES : 0;
             for (long j = from; j < issued; ++j)
                 mbar_drain(&s.full[j % S::STAGES], static_cast<uint32_t>((j / S::STAGES) & 1), kWaitLimitNs / 8);
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMAs: one accumulation group per block ----------------
+        } else if (warp < 3 && lane == 0) {
+            // ---------------- MMAs: one accumulation group per block, every other block ----------------
             constexpr uint32_t idesc = e4m3_idesc(128, BN);
-            // One thread issues an MMA about as fast as the tensor cores run it, so what
-            // it does between two blocks is a gap in their work: the wait for the next
-            // block's stage stands between this block's MMAs.
-            const int mine = first < n_tiles ? (n_tiles - 1 - first) / step + 1 : 0;
-            const int64_t blocks = static_cast<int64_t>(mine) * p.kb;
-            uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-            bool ok = blocks > 0 && mbar_wait(&s.full[0], 0, wc);
-            for (int64_t i = 0; i < blocks && ok; ++i) {
+            const int64_t mine = first < n_tiles ? (n_tiles - 1 - first) / step + 1 : 0;
+            const int64_t blocks = mine * p.kb;
+            // block i: stage i mod STAGES, buffer i mod NBUF, and their phases
+            uint32_t stage = warp - 1, phase = 0, buf = warp - 1, bphase = 0;
+            bool ok = warp - 1 < blocks && mbar_wait(&s.full[stage], 0, wc);
+            for (int64_t i = warp - 1; i < blocks && ok; i += 2) {
                 if (!mbar_wait(&s.tempty[buf], bphase ^ 1, wc)) break;
                 tc_fence_after();
                 const uint64_t ad = sw128_desc(smem_u32(smem + stage * S::STAGE));
@@ -195,49 +195,56 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                 const uint32_t d = tmem + buf * BN, at = stage;
                 mma_e4m3(d, ad, bd, idesc, 0);
                 mma_e4m3(d, ad + 2, bd + 2, idesc, 1);
-                if (++stage == S::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                if (i + 1 < blocks) ok = mbar_wait(&s.full[stage], phase, wc);
                 mma_e4m3(d, ad + 4, bd + 4, idesc, 1);
                 mma_e4m3(d, ad + 6, bd + 6, idesc, 1);
                 tc_commit(&s.tfull[buf]);
                 tc_commit(&s.empty[at]);
-                if (++buf == S::NBUF) {
-                    buf = 0;
+                stage += 2;
+                if (stage >= S::STAGES) {
+                    stage -= S::STAGES;
+                    phase ^= 1;
+                }
+                buf += 2;
+                if (buf >= S::NBUF) {
+                    buf -= S::NBUF;
                     bphase ^= 1;
                 }
+                if (i + 2 < blocks) ok = mbar_wait(&s.full[stage], phase, wc);
             }
-            tc_commit(&s.mma_done);
-            mbar_drain(&s.mma_done, 0, kWaitLimitNs / 8);
-        } else if (warp >= 2) {
-            // ---------------- scales: 64 rows a warp, two a lane ----------------
+            tc_commit(&s.mma_done[warp - 1]);
+            mbar_drain(&s.mma_done[warp - 1], 0, kWaitLimitNs / 8);
+        } else if (warp == 3) {
+            // ---------------- scales: four rows a lane ----------------
             float* scales = reinterpret_cast<float*>(smem + S::SCALE_AT);
             uint32_t buf = 0, bphase = 0;
             bool ok = true;
             for (int tile = first; tile < n_tiles && ok; tile += step) {
                 const TcTile t = tc_tile<BN>(p, tile);
-                const int r = 64 * (warp - 2) + 2 * lane, m = t.m0 + r;
-                const float* sa0 = p.sa + static_cast<size_t>(min(m, p.M - 1)) * p.kb;
-                const float* sa1 = p.sa + static_cast<size_t>(min(m + 1, p.M - 1)) * p.kb;
-                // lane 0 of the warp: the scale of the tile's first or second 128 columns
-                const float* sb = p.sb + static_cast<size_t>(min(t.n0 + 128 * (warp - 2), p.N - 1) / kQuantGroup) * p.kb;
-                float a0 = __ldg(sa0), a1 = __ldg(sa1), b0 = __ldg(sb);
+                const float* sa[4];
+                float a[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sa[j] = p.sa + static_cast<size_t>(min(t.m0 + 4 * lane + j, p.M - 1)) * p.kb;
+                    a[j] = __ldg(sa[j]);
+                }
+                // lanes 0 and 1: the scales of the tile's first and second 128 columns
+                const float* sb =
+                    p.sb + static_cast<size_t>(min(t.n0 + 128 * (lane & 1), p.N - 1) / kQuantGroup) * p.kb;
+                float b0 = __ldg(sb);
                 for (int b = 0; b < p.kb; ++b) {
-                    const float2 v = make_float2(a0, a1);
+                    const float4 v = make_float4(a[0], a[1], a[2], a[3]);
                     const float vb = b0;
                     const int nb = min(b + 1, p.kb - 1);
-                    a0 = __ldg(sa0 + nb);
-                    a1 = __ldg(sa1 + nb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[j] = __ldg(sa[j] + nb);
                     b0 = __ldg(sb + nb);
                     if (!mbar_wait(&s.tempty[buf], bphase ^ 1, wc)) {
                         ok = false;
                         break;
                     }
                     float* dst = scales + buf * S::SCALES;
-                    *reinterpret_cast<float2*>(dst + r) = v;
-                    if (lane == 0) dst[128 + warp - 2] = vb;
+                    *reinterpret_cast<float4*>(dst + 4 * lane) = v;
+                    if (lane < 2) dst[128 + lane] = vb;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.tfull[buf]);
                     if (++buf == S::NBUF) {
