@@ -23,7 +23,14 @@ namespace moe {
 namespace {
 
 constexpr int kBfThreads = 256, kBfWarps = kBfThreads / 32;
-constexpr int kBfRowsMost = 32;  // rows up to which this form is used
+
+// Which form: up to 8 rows this one; up to 32 (the most it takes) while the
+// weights are small, since its reads of the tokens grow with the rows. Measured
+// here / on tcgen05: 4.9 / 5.9 us at M = 17, N = 2816, K = 2048; 17.3 / 16.3 at
+// M = 16, N = 4096, K = 14336; 34.9 / 28.2 at M = 16, N = 28672, K = 4096.
+inline bool rows_form(int M, int N, int K) {
+    return M <= 8 || (M <= 32 && static_cast<int64_t>(N) * K <= (1 << 24));
+}
 
 // A stage: 4 KB of weights (32 rows x 128), NT tiles of 8 tokens, the tokens'
 // scales, two weight scales. The ring has what fits 200 KB, at most 6 stages.
@@ -249,7 +256,7 @@ extern "C" int moe_block_fp8_gemm(const void* a, const float* a_scales, const vo
                           static_cast<const uint16_t*>(addend), static_cast<uint16_t*>(out), M, N, K,
                           (K + moe::kQuantGroup - 1) / moe::kQuantGroup};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M > moe::kBfRowsMost) return moe::launch_block_fp8_tc(p, act, sms, err_word, st, who);
+    if (!moe::rows_form(M, N, K)) return moe::launch_block_fp8_tc(p, act, sms, err_word, st, who);
     const cudaError_t e = act == MOE_ACT_BF16 ? moe::launch_rows<MOE_ACT_BF16>(p, sms, st)
                                               : moe::launch_rows<MOE_ACT_F16>(p, sms, st);
     if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));

@@ -20,11 +20,15 @@
 //     threads issue, a block each in turn (their buffers are independent). CTA pairs (M = 256) halve the
 //     shared-memory traffic but lengthen every signal by a cluster hop, and
 //     measured slower.
+//   * Too few tiles for the GPU: a cluster of 2 or 4 CTAs per tile, each with a
+//     part of the contraction; each CTA then adds a slice of the columns, in
+//     rank order, from all of them (distributed shared memory).
 //   * Finished rows leave through a staging area by TMA stores.
 //   * Roles: warp 0 copies (TMA, 128-byte swizzle), warps 1 and 2 issue the
 //     MMAs, warp 3 fetches scales, the others add and store. Every wait is
 //     bounded. At BN = 256 the 20 warps' 96 registers are split 32 / 112
-//     between the first four and the others.
+//     between the first four and the others. (A second copying warp, and
+//     scales fetched two blocks ahead, measured 5 to 10% slower.)
 #include "block_fp8.cuh"
 
 namespace moe {
@@ -108,10 +112,11 @@ template <int BN> __device__ __forceinline__ TcTile tc_tile(const BfParams& p, i
     return {(16 * grp + in % rows) * 128, in / rows * BN};
 }
 
-template <int ACT, int BN>
+// PARTS > 1: one tile per cluster of PARTS CTAs; otherwise one CTA walks tiles.
+template <int ACT, int BN, int PARTS>
 __global__ void __launch_bounds__(TcShape<BN>::THREADS, 1)
 block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_o, const BfParams p, int32_t* err, uint64_t wait_ns) {
+                    const __grid_constant__ CUtensorMap tm_o, const BfParams p, int a_rows, int32_t* err, uint64_t wait_ns) {
     using S = TcShape<BN>;
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
@@ -119,7 +124,11 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
     TcTail& s = *reinterpret_cast<TcTail*>(smem + S::TAIL_AT);
     const WaitCtx wc{&s.abort_flag, err, wait_ns};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int first = blockIdx.x, step = gridDim.x;
+    constexpr bool SPLIT = PARTS > 1;
+    const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first = blockIdx.x / PARTS, step = SPLIT ? 1 << 30 : gridDim.x;
+    // this CTA's contraction blocks
+    const int kb0 = p.kb * rank / PARTS, kbs = p.kb * (rank + 1) / PARTS - kb0;
     const int n_tiles = ((p.M + 127) / 128) * ((p.N + BN - 1) / BN);
 
     if (tid == 0) {
@@ -154,17 +163,18 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
         if (BN == 256) regs_dec<32>();  // 4 x 32 + 16 x 112 = 20 x 96
         if (warp == 0 && lane == 0) {
             // ---------------- copies ----------------
+            const uint32_t bytes = a_rows * 128 + BN * 128;
             uint32_t stage = 0, phase = 0;
             long issued = 0;
             bool ok = true;
             for (int tile = first; tile < n_tiles && ok; tile += step) {
                 const TcTile t = tc_tile<BN>(p, tile);
-                for (int b = 0; b < p.kb; ++b) {
+                for (int b = kb0; b < kb0 + kbs; ++b) {
                     if (!mbar_wait(&s.empty[stage], phase ^ 1, wc)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&s.full[stage], S::STAGE);
+                    mbar_arrive_expect_tx(&s.full[stage], bytes);
                     uint8_t* dst = smem + stage * S::STAGE;
                     tma_load_2d(dst, &tm_a, b * 128, t.m0, &s.full[stage]);
                     tma_load_2d(dst + kTcA, &tm_w, b * 128, t.n0, &s.full[stage]);
@@ -179,11 +189,11 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             const long from = issued > S::STAGES ? issued - S::STAGES : 0;
             for (long j = from; j < issued; ++j)
                 mbar_drain(&s.full[j % S::STAGES], static_cast<uint32_t>((j / S::STAGES) & 1), kWaitLimitNs / 8);
-        } else if (warp < 3 && lane == 0) {
+        } else if ((warp == 1 || warp == 2) && lane == 0) {
             // ---------------- MMAs: one accumulation group per block, every other block ----------------
             constexpr uint32_t idesc = e4m3_idesc(128, BN);
             const int64_t mine = first < n_tiles ? (n_tiles - 1 - first) / step + 1 : 0;
-            const int64_t blocks = mine * p.kb;
+            const int64_t blocks = mine * kbs;
             // block i: stage i mod STAGES, buffer i mod NBUF, and their phases
             uint32_t stage = warp - 1, phase = 0, buf = warp - 1, bphase = 0;
             bool ok = warp - 1 < blocks && mbar_wait(&s.full[stage], 0, wc);
@@ -224,17 +234,17 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                 float a[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    sa[j] = p.sa + static_cast<size_t>(min(t.m0 + 4 * lane + j, p.M - 1)) * p.kb;
+                    sa[j] = p.sa + static_cast<size_t>(min(t.m0 + 4 * lane + j, p.M - 1)) * p.kb + kb0;
                     a[j] = __ldg(sa[j]);
                 }
                 // lanes 0 and 1: the scales of the tile's first and second 128 columns
                 const float* sb =
-                    p.sb + static_cast<size_t>(min(t.n0 + 128 * (lane & 1), p.N - 1) / kQuantGroup) * p.kb;
+                    p.sb + static_cast<size_t>(min(t.n0 + 128 * (lane & 1), p.N - 1) / kQuantGroup) * p.kb + kb0;
                 float b0 = __ldg(sb);
-                for (int b = 0; b < p.kb; ++b) {
+                for (int b = 0; b < kbs; ++b) {
                     const float4 v = make_float4(a[0], a[1], a[2], a[3]);
                     const float vb = b0;
-                    const int nb = min(b + 1, p.kb - 1);
+                    const int nb = min(b + 1, kbs - 1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = __ldg(sa[j] + nb);
                     b0 = __ldg(sb + nb);
@@ -268,7 +278,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             uint64_t acc[S::PER / 2];
 #pragma unroll
             for (int j = 0; j < S::PER / 2; ++j) acc[j] = 0;
-            for (int b = 0; b < p.kb; ++b) {
+            for (int b = 0; b < kbs; ++b) {
                 if (!mbar_wait(&s.tfull[buf], bphase, wc)) {
                     ok = false;
                     break;
@@ -295,6 +305,51 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                     buf = 0;
                     bphase ^= 1;
                 }
+            }
+            if (SPLIT) {
+                // the stages are free once every CTA of the cluster is done with its products
+                cluster_sync_all();
+                // 16 bytes (four columns) of every thread, by source CTA and piece of the slice
+                constexpr int SLICE = S::PER / PARTS, PIECES = SLICE / 4, PLANE = S::EPI_WARPS * 32 * 16;
+                uint8_t* sums = smem + ((warp - 4) * 32 + lane) * 16;
+#pragma unroll
+                for (int r = 0; r < PARTS; ++r) {
+                    const uint32_t to = mapa_shared(smem_u32(sums + rank * PIECES * PLANE), r);
+#pragma unroll
+                    for (int j = 0; j < PIECES; ++j)
+                        asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(to + j * PLANE),
+                                     "l"(acc[(r * SLICE + 4 * j) / 2]), "l"(acc[(r * SLICE + 4 * j) / 2 + 1])
+                                     : "memory");
+                }
+                cluster_sync_all();
+                const TcTile t = tc_tile<BN>(p, tile);
+                const int m = t.m0 + 32 * q + lane, n = t.n0 + grp * S::PER + rank * SLICE;
+                if (!ok || m >= p.M) break;
+                const size_t at = static_cast<size_t>(m) * p.N + n;
+#pragma unroll
+                for (int c = 0; c < SLICE; c += 8) {
+                    if (n + c >= p.N) break;
+                    float v[8];
+#pragma unroll
+                    for (int r = 0; r < PARTS; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 f =
+                                *reinterpret_cast<const float4*>(sums + (r * PIECES + c / 4 + h) * PLANE);
+                            v[4 * h] = r ? v[4 * h] + f.x : f.x;
+                            v[4 * h + 1] = r ? v[4 * h + 1] + f.y : f.y;
+                            v[4 * h + 2] = r ? v[4 * h + 2] + f.z : f.z;
+                            v[4 * h + 3] = r ? v[4 * h + 3] + f.w : f.w;
+                        }
+                    if (p.addend) {
+                        float f[8];
+                        unpack8<ACT>(*reinterpret_cast<const uint4*>(p.addend + at + c), f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += f[j];
+                    }
+                    *reinterpret_cast<uint4*>(p.out + at + c) = pack8<ACT>(v);
+                }
+                break;
             }
             if (!ok) break;
             // through the staging area, whose 16-byte pieces lie swizzled by row as the
@@ -337,16 +392,22 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
         if (lane == 0) bulk_wait();
     }
 
+    if (SPLIT && warp < 4) {  // the other warps' two meetings
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, S::COLS);
 }
 
-template <int ACT, int BN>
+template <int ACT, int BN, int PARTS>
 int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
     using S = TcShape<BN>;
-    auto kernel = block_fp8_tc_kernel<ACT, BN>;
+    static_assert(PARTS == 1 || S::EPI_WARPS * 32 * S::PER * 4 <= S::OUT_AT, "a tile's sums fit in the stages");
+    auto kernel = block_fp8_tc_kernel<ACT, BN, PARTS>;
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -356,26 +417,68 @@ int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const c
         configured_for = dev;
     }
     CUtensorMap tm_a, tm_w, tm_o;
-    int rc = make_tmap_2d_u8(&tm_a, p.a, p.M, p.K, 128);
+    // of few rows, no more are copied than there may be (the other TMEM lanes hold sums nobody reads)
+    const int a_rows = p.M >= 128 ? 128 : (p.M + 15) / 16 * 16;
+    int rc = make_tmap_2d_u8(&tm_a, p.a, p.M, p.K, a_rows);
     if (rc == MOE_OK) rc = make_tmap_2d_u8(&tm_w, p.w, p.N, p.K, BN);
     if (rc == MOE_OK) rc = make_tmap_2d_out(&tm_o, p.out, p.M, p.N, 32, 32, ACT);
     if (rc != MOE_OK) return rc;
     const int64_t tiles = static_cast<int64_t>((p.M + 127) / 128) * ((p.N + BN - 1) / BN);
     if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: M=%d x N=%d is too large", who, p.M, p.N);
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), S::THREADS, S::SMEM,
-                                     st, tm_a, tm_w, tm_o, p, err, wait_limit_ns());
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PARTS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(PARTS > 1 ? tiles * PARTS : (tiles < sms ? tiles : sms)));
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = PARTS > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tm_a, tm_w, tm_o, p, a_rows, err, wait_limit_ns());
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     count_launch();
     return check_launch(who);
 }
 
-// The widest tile that still gives every SM one: a wider tile reads less and
-// spends fewer epilogue steps per sum, a narrower one fills more of the GPU.
+// Tile width and split of the contraction, by the time that each choice would
+// take: the waves of CTAs, times the blocks of 128 of each, times what a block
+// costs at that width (measured on a GB300: 260, 310 and 480 ns at 64, 128 and
+// 256 columns), and what a launch costs (2.5 us; 4.5 and 5.5 with the meeting
+// of 2 or 4 CTAs). A wide tile reads less and spends fewer steps per sum, a
+// narrow or split one fills more of the GPU: M = 128, N = 4096, K = 14336
+// takes 16.8 us at 128 x 4 CTAs, 19.5 at 64 x 2, 31 at 64 and 57 at 256.
 template <int ACT> int pick_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
-    const int64_t mt = (p.M + 127) / 128;
-    if (mt * ((p.N + 255) / 256) >= sms) return launch_tc<ACT, 256>(p, sms, err, st, who);
-    if (mt * ((p.N + 127) / 128) >= sms) return launch_tc<ACT, 128>(p, sms, err, st, who);
-    return launch_tc<ACT, 64>(p, sms, err, st, who);
+    static const struct {
+        int bn, parts, block_ns, fixed_ns;
+    } forms[] = {{256, 1, 480, 2500}, {128, 1, 310, 2500}, {64, 1, 260, 2500}, {128, 2, 310, 4500},
+                 {64, 2, 260, 4500},  {128, 4, 310, 5500}, {64, 4, 260, 5500}};
+    int best = 0;
+    int64_t best_ns = INT64_MAX;
+    for (int i = 0; i < 7; ++i) {
+        if (p.kb < forms[i].parts) continue;
+        const int64_t ctas = static_cast<int64_t>((p.M + 127) / 128) * ((p.N + forms[i].bn - 1) / forms[i].bn) *
+                             forms[i].parts;
+        const int64_t blocks = (p.kb + forms[i].parts - 1) / forms[i].parts;
+        const int64_t ns = (ctas + sms - 1) / sms * blocks * forms[i].block_ns + forms[i].fixed_ns;
+        if (ns < best_ns) {
+            best_ns = ns;
+            best = i;
+        }
+    }
+    switch (best) {
+        case 0: return launch_tc<ACT, 256, 1>(p, sms, err, st, who);
+        case 1: return launch_tc<ACT, 128, 1>(p, sms, err, st, who);
+        case 2: return launch_tc<ACT, 64, 1>(p, sms, err, st, who);
+        case 3: return launch_tc<ACT, 128, 2>(p, sms, err, st, who);
+        case 4: return launch_tc<ACT, 64, 2>(p, sms, err, st, who);
+        case 5: return launch_tc<ACT, 128, 4>(p, sms, err, st, who);
+        default: return launch_tc<ACT, 64, 4>(p, sms, err, st, who);
+    }
 }
 
 }  // namespace
