@@ -58,7 +58,7 @@ struct NormRow {
             if (y && i < V) y[i] = pack8<ACT>(v[j]);
             if (q) {
                 // lanes past the row hold NaN or 0 (0 * rstd * 0): they stay out of the maximum
-                const float sc = group_scale(amax_half_warp(i < V ? amax_bits(v[j]) : 0u));
+                const float sc = group_scale(amax_half_warp(i < V ? amax8(v[j]) : 0.0f, 0xffffffffu));
                 if (i < V) {
                     q[i] = e4m3x8(v[j], sc);
                     if ((lane & (kQuantLanes - 1)) == 0) s[i / kQuantLanes] = sc;
@@ -146,39 +146,59 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
 //
 // of a [T, 2I] gate/up product (gate columns, then up). HBM-bound: 4 bytes in
 // and 1 byte out per element of [T, I]. Each thread takes 8 columns, a half
-// warp one group of 128; rows are padded to whole groups in the thread index.
-constexpr int kSiluThreads = 256;
+// warp one group of 128; the groups of all rows are numbered through, so rows
+// of any width fill the blocks.
+constexpr int kSiluThreads = 128;
+constexpr int kSiluItems = 2;  // groups a half warp takes
 
-template <int ACT>
+template <int ACT, typename Index>
 __global__ void __launch_bounds__(kSiluThreads)
 silu_mul_quant_kernel(const uint4* __restrict__ gu, uint2* __restrict__ q, float* __restrict__ s, int T, int I) {
     pdl_wait();
     const int V = I / 8;                                        // vectors per row
-    const int groups = (I + kQuantGroup - 1) / kQuantGroup;
-    const int64_t group = (static_cast<int64_t>(blockIdx.x) * kSiluThreads + threadIdx.x) / kQuantLanes;
-    if (group >= static_cast<int64_t>(T) * groups) return;      // a half warp together
-    const int64_t t = group / groups;
-    const int v = static_cast<int>(group - t * groups) * kQuantLanes + (threadIdx.x & (kQuantLanes - 1));
-    float o[8];
-    uint32_t m = 0;
-    if (v < V) {
-        const uint4* row = gu + t * 2 * V;
-        float g[8], u[8];
-        unpack8<ACT>(__ldg(row + v), g);
-        unpack8<ACT>(__ldg(row + V + v), u);
+    const Index groups = (I + kQuantGroup - 1) / kQuantGroup;
+    const Index all = static_cast<Index>(T) * groups;
+    const int lane = threadIdx.x & (kQuantLanes - 1);
+    uint4 gv[kSiluItems], uv[kSiluItems];
+    Index group[kSiluItems];
+    size_t at[kSiluItems];  // vector of the output; V (of no row) where this lane has none
+    bool in[kSiluItems];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
-        m = amax_bits(o);
+    for (int j = 0; j < kSiluItems; ++j) {
+        group[j] = (static_cast<Index>(blockIdx.x) * kSiluItems + j) * (kSiluThreads / kQuantLanes) +
+                   threadIdx.x / kQuantLanes;
+        const Index t = group[j] / groups;
+        const int v = static_cast<int>(group[j] - t * groups) * kQuantLanes + lane;
+        in[j] = group[j] < all && v < V;
+        at[j] = static_cast<size_t>(t) * V + v;
+        gv[j] = uv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (in[j]) {
+            const uint4* row = gu + at[j] + static_cast<size_t>(t) * V;
+            gv[j] = __ldcs(row);
+            uv[j] = __ldcs(row + V);
+        }
     }
-    // the two halves of a warp may part above: each reduces under its own mask
-    const uint32_t mask = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
-    for (int off = kQuantLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(mask, m, off));
-    if (v < V) {
-        const float sc = group_scale(m);
-        q[t * V + v] = e4m3x8(o, sc);
-        if ((threadIdx.x & (kQuantLanes - 1)) == 0) s[group] = sc;
+    for (int j = 0; j < kSiluItems; ++j) {
+        float g[8], u[8], o[8];
+        unpack8<ACT>(gv[j], g);
+        unpack8<ACT>(uv[j], u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = silu_mul_fast(g[i], u[i]);
+        // a lane past the row or the last group holds zeros, which stay out of the maximum
+        const float sc = group_scale(amax_half_warp(amax8(o), 0xffffffffu));
+        if (in[j]) {
+            q[at[j]] = e4m3x8(o, sc);
+            if (lane == 0) s[group[j]] = sc;
+        }
     }
+}
+
+template <int ACT>
+cudaError_t launch_silu(const uint4* gu, uint2* q, float* s, int T, int I, unsigned blocks, cudaStream_t st) {
+    if (blocks < (1u << 27))  // the group numbers fit in 32 bits: their division is a few instructions, not a hundred
+        return launch_pdl(silu_mul_quant_kernel<ACT, uint32_t>, dim3(blocks), kSiluThreads, 0, st, gu, q, s, T, I);
+    return launch_pdl(silu_mul_quant_kernel<ACT, uint64_t>, dim3(blocks), kSiluThreads, 0, st, gu, q, s, T, I);
 }
 
 }  // namespace
@@ -224,19 +244,15 @@ extern "C" int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, i
     MOE_REQUIRE(moe::aligned16(gate_up) && moe::aligned16(q), "%s: gate_up / q must be 16-byte aligned", who);
     MOE_REQUIRE((reinterpret_cast<uintptr_t>(q_scales) & 3u) == 0, "%s: q_scales must be 4-byte aligned", who);
     const int64_t groups = static_cast<int64_t>(T) * ((I + moe::kQuantGroup - 1) / moe::kQuantGroup);
-    constexpr int kPerBlock = moe::kSiluThreads / moe::kQuantLanes;
+    constexpr int kPerBlock = moe::kSiluItems * moe::kSiluThreads / moe::kQuantLanes;
     const int64_t blocks = (groups + kPerBlock - 1) / kPerBlock;
     if (blocks > 0x7fffffff) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: T=%d x I=%d is too large", who, T, I);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint4* gu = static_cast<const uint4*>(gate_up);
     uint2* qv = static_cast<uint2*>(q);
-    const dim3 grid(static_cast<unsigned>(blocks));
-    const cudaError_t e =
-        act == MOE_ACT_BF16
-            ? moe::launch_pdl(moe::silu_mul_quant_kernel<MOE_ACT_BF16>, grid, moe::kSiluThreads, 0, st, gu, qv,
-                              q_scales, T, I)
-            : moe::launch_pdl(moe::silu_mul_quant_kernel<MOE_ACT_F16>, grid, moe::kSiluThreads, 0, st, gu, qv,
-                              q_scales, T, I);
+    const unsigned grid = static_cast<unsigned>(blocks);
+    const cudaError_t e = act == MOE_ACT_BF16 ? moe::launch_silu<MOE_ACT_BF16>(gu, qv, q_scales, T, I, grid, st)
+                                              : moe::launch_silu<MOE_ACT_F16>(gu, qv, q_scales, T, I, grid, st);
     if (e != cudaSuccess) return moe::fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     moe::count_launch();
     return moe::check_launch(who);

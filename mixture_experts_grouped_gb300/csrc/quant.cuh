@@ -11,23 +11,27 @@ constexpr int kQuantLanes = kQuantGroup / 8;        // lanes of 8 columns per gr
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;        // 2^-126: the scale of an all-zero group, and its reciprocal is finite
 
-// max |v| as the bits of a non-negative float: unsigned order is the order of
-// the magnitudes, and a NaN's bits lie above infinity's, so it wins.
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[8]) {
-    uint32_t m = 0;
+// the larger, or NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+    float m = fabsf(v[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
     return m;
 }
-// the same over the 16 lanes of a half warp (every lane of the warp calls it)
-__device__ __forceinline__ uint32_t amax_half_warp(uint32_t m) {
+// the same over the 16 lanes of a half warp; `mask` names the lanes that call it
+__device__ __forceinline__ float amax_half_warp(float m, uint32_t mask) {
 #pragma unroll
-    for (int off = kQuantLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = kQuantLanes / 2; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, off));
     return m;
 }
 // scale = max(amax / 448, 2^-126); a NaN amax stays NaN
-__device__ __forceinline__ float group_scale(uint32_t bits) {
-    const float s = __fdiv_rn(__uint_as_float(bits), kE4m3Max);
+__device__ __forceinline__ float group_scale(float amax) {
+    const float s = __fdiv_rn(amax, kE4m3Max);
     return s < kMinScale ? kMinScale : s;
 }
 // four codes, the first in the lowest byte; rounds to nearest even, saturates at 448
@@ -50,6 +54,17 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float s) {
     q.x = e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
     q.y = e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r);
     return q;
+}
+
+// silu(g) * u = g / (1 + exp(-g)) * u by the hardware's 2^x and reciprocal, with
+// subnormals flushed: where exp(-g) overflows, the reciprocal of infinity is 0
+// and the product a zero, as in the formula; where it would be subnormal, 1 +
+// it is 1 either way.
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896341f));  // log2(e)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 // eight 16-bit activations <-> f32
