@@ -42,10 +42,11 @@ constexpr int kFewPairs = MOE_MAX_FEW_TOKENS * MOE_MAX_TOPK;
 // 8 warps keep up, and a CTA of each kernel fits an SM, so the down kernel's
 // start hides behind the gate/up kernel's end. The quantised formats are bound
 // by the instructions of their conversion and want all the warps of an SM
-// (GPTQ's wide gate/up items want registers more than warps: 11).
-template <int FMT> struct FewShape {
+// (GPTQ's wide gate/up items with two token tiles want registers more than
+// warps: 11).
+template <int FMT, int NT> struct FewShape {
     static constexpr bool DENSE = FMT == MOE_W_BF16, GPTQ = FMT == MOE_W_GPTQ_INT4;
-    static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
+    static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ && NT > 1 ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
     static constexpr int GU_RING = FMT == MOE_W_FP8_E4M3 ? 5 : 4;
     static constexpr int DN_RING = 4;
     static constexpr int RESIDENT = DENSE ? 2 : 1;  // CTAs per SM the registers must allow
@@ -211,11 +212,11 @@ __device__ __forceinline__ void publish_routing(const FewParams& p, int t, int s
 // ---- gate/up ----------------------------------------------------------------------
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__((FewShape<FMT>::GU_WARPS + 1) * 32, FewShape<FMT>::RESIDENT)
+__global__ void __launch_bounds__((FewShape<FMT, NT>::GU_WARPS + 1) * 32, FewShape<FMT, NT>::RESIDENT)
 few_gate_up_kernel(const FewParams p) {
     using U = Unit<FMT, ACT, true>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT>::GU_RING, W = FewShape<FMT>::GU_WARPS, MT = U::MT, ROWS = U::ROWS;
+    constexpr int RING = FewShape<FMT, NT>::GU_RING, W = FewShape<FMT, NT>::GU_WARPS, MT = U::MT, ROWS = U::ROWS;
     extern __shared__ uint8_t few_smem[];
     float4* cut = reinterpret_cast<float4*>(few_smem + W * RING * S::BYTES);  // [W][2][MT][NT][32]: sums of cut items
     __shared__ FewPlan s;
@@ -231,7 +232,7 @@ few_gate_up_kernel(const FewParams p) {
     const int I = p.I, K = p.H;
     // The CTA's rows, row = entry * I + i. Where items are many, shares of whole
     // items: the quantised formats take as long for part of one.
-    const int whole = !FewShape<FMT>::DENSE && I % ROWS == 0 && s.n * (I / ROWS) >= 8 * static_cast<int>(gridDim.x);
+    const int whole = !FewShape<FMT, NT>::DENSE && I % ROWS == 0 && s.n * (I / ROWS) >= 8 * static_cast<int>(gridDim.x);
     const int align = whole ? ROWS : U::ALIGN;
     int r0, r1;
     part_of(s.n * (I / align), gridDim.x, blockIdx.x, r0, r1);
@@ -456,11 +457,11 @@ __device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* ou
 }
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__(FewShape<FMT>::DN_WARPS * 32, FewShape<FMT>::RESIDENT)
+__global__ void __launch_bounds__(FewShape<FMT, NT>::DN_WARPS * 32, FewShape<FMT, NT>::RESIDENT)
 few_down_kernel(const FewParams p) {
     using U = Unit<FMT, ACT, false>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT>::DN_RING, W = FewShape<FMT>::DN_WARPS, MT = U::MT;
+    constexpr int RING = FewShape<FMT, NT>::DN_RING, W = FewShape<FMT, NT>::DN_WARPS, MT = U::MT;
     static_assert(U::ROWS == 32, "32 columns a tile");
     extern __shared__ uint8_t few_smem[];
     float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][kFewCols]
@@ -472,7 +473,7 @@ few_down_kernel(const FewParams p) {
     // (logits, or ids given as inputs) and the weights are read before the wait.
     // Otherwise this CTA starts when that kernel is all but done, and takes the
     // ids it left.
-    constexpr bool BESIDE = FewShape<FMT>::RESIDENT > 1;
+    constexpr bool BESIDE = FewShape<FMT, NT>::RESIDENT > 1;
     if (!BESIDE) pdl_wait();
     build_plan<W, 8 * NT>(s, p, BESIDE && p.logits != nullptr, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -642,14 +643,14 @@ few_down_kernel(const FewParams p) {
 
 template <int FMT, int ACT, int NT>
 cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
-    using F = FewShape<FMT>;
+    using F = FewShape<FMT, NT>;
     using GU = Unit<FMT, ACT, true>;
     using DN = Unit<FMT, ACT, false>;
     constexpr int gu_smem =
         F::GU_WARPS * (F::GU_RING * Stage<GU>::BYTES + static_cast<int>(sizeof(float4)) * 2 * GU::MT * NT * 32);
     constexpr int dn_ring = F::DN_WARPS * F::DN_RING * Stage<DN>::BYTES;
     constexpr int dn_token = static_cast<int>(sizeof(float)) * (F::DN_WARPS * kFewCols + 32);
-    constexpr int dn_most = dn_ring + dn_token * (NT == 1 ? 8 : MOE_MAX_FEW_TOKENS);
+    constexpr int dn_most = dn_ring + dn_token * MOE_MAX_FEW_TOKENS;
     static_assert(gu_smem + sizeof(FewPlan) <= 232448 && dn_most + sizeof(FewPlan) <= 232448, "shared memory");
     static int configured_for = -1;
     int dev = 0;
@@ -680,10 +681,12 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, few_down_kernel<FMT, ACT, NT>, p);
 }
 
-// up to 8 tokens: one token tile; more: two, and experts of over 16 tokens are listed twice
+// One token tile (8 tokens of an expert at a time) where no expert can have
+// more or few will; otherwise two.
 template <int FMT, int ACT>
 cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t st) {
-    return p.T <= 8 ? launch_few_nt<FMT, ACT, 1>(p, sms, st) : launch_few_nt<FMT, ACT, 2>(p, sms, st);
+    return p.T <= 8 || p.T * p.k <= 4 * p.E ? launch_few_nt<FMT, ACT, 1>(p, sms, st)
+                                            : launch_few_nt<FMT, ACT, 2>(p, sms, st);
 }
 
 }  // namespace moe
