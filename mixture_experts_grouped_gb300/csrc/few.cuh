@@ -140,9 +140,13 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
     if (warp == 0) {
         // prefix sums over the experts, eight consecutive ones a lane: entries in the high half, slots in the low
         uint32_t cnt[8], mine = 0;
+        bool many = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cnt[j] = s.mask[lane * 9 + j];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            cnt[j] = __popc(s.mask[lane * 9 + j]);
+            cnt[j] = __popc(cnt[j]);
+            many |= cnt[j] > SLOTS;
             mine += ((cnt[j] + SLOTS - 1) / SLOTS << 16) + cnt[j];
         }
         uint32_t inc = mine;
@@ -152,13 +156,25 @@ __device__ __forceinline__ void build_plan(FewPlan& s, const FewParams& p, bool 
             if (lane >= off) inc += o;
         }
         uint32_t at = inc - mine;
+        if (!__any_sync(0xffffffffu, many)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s.first[lane * 9 + j] = at & 0xffffu;
-            for (uint32_t c = 0; c < cnt[j]; c += SLOTS) {
-                s.te[at >> 16] = lane * 8 + j;
-                s.start[at >> 16] = at & 0xffffu;
-                at += (1u << 16) + min(cnt[j] - c, static_cast<uint32_t>(SLOTS));
+            for (int j = 0; j < 8; ++j) {
+                s.first[lane * 9 + j] = at & 0xffffu;
+                if (cnt[j]) {
+                    s.te[at >> 16] = lane * 8 + j;
+                    s.start[at >> 16] = at & 0xffffu;
+                    at += (1u << 16) + cnt[j];
+                }
+            }
+        } else {
+            for (int j = 0; j < 8; ++j) {
+                s.first[lane * 9 + j] = at & 0xffffu;
+                const uint32_t n = __popc(s.mask[lane * 9 + j]);
+                for (uint32_t c = 0; c < n; c += SLOTS) {
+                    s.te[at >> 16] = lane * 8 + j;
+                    s.start[at >> 16] = at & 0xffffu;
+                    at += (1u << 16) + min(n - c, static_cast<uint32_t>(SLOTS));
+                }
             }
         }
         if (lane == 31) {
