@@ -11,8 +11,9 @@
 // mask of tokens per expert (T <= 32 bits), the touched experts in ascending
 // order and, per expert, its "slots" (distinct tokens, ascending). An expert
 // with more slots than a unit's product takes (8 or 16) is listed again for
-// the rest, and its weights read again. Each CTA takes an equal share of the weight rows, and each of its warps an equal,
-// contiguous share of the CTA's units (stream.cuh):
+// the rest, and its weights read again. Each CTA takes an equal share of the
+// weight rows, and each of its warps an equal, contiguous share of the CTA's
+// units (stream.cuh):
 //   gate/up  rows (touched expert, i): gate rows and the up rows of the same i
 //            to a unit, so one lane holds both sums of an h element. A warp
 //            finishes an item (16 or 32 such rows, the whole contraction) by
@@ -444,21 +445,21 @@ few_gate_up_kernel(const FewParams p) {
 
 // ---- down ---------------------------------------------------------------------------
 
-// The end of a tile of up to 32 columns: adds the warps' sums in warp order and
-// clears them, then the two CTAs', half of the tile each, and writes it.
+// The end of a tile of up to 32 columns: adds the warps' sums in warp order
+// (clearing them for the next tile, if there is one), then the two CTAs', half
+// of the tile each, and writes it.
 template <int ACT, int W>
 __device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* out, int T, int H, int n0, int n1,
-                                          uint32_t rank) {
+                                          uint32_t rank, bool last) {
     __syncthreads();
     for (int i = threadIdx.x; i < T * 32; i += W * 32) {
+        float* at = sums + (i >> 5) * kFewCols + (i & 31);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            float& part = sums[w * T * kFewCols + (i >> 5) * kFewCols + (i & 31)];
-            v += part;
-            part = 0.0f;
-        }
+        for (int w = 0; w < W; ++w) v += at[w * T * kFewCols];
         both[i] = v;
+        if (!last)
+            for (int w = 0; w < W; ++w) at[w * T * kFewCols] = 0.0f;
     }
     cluster_sync_all();
     const uint32_t peer = mapa_shared(smem_u32(both), rank ^ 1);
@@ -485,13 +486,9 @@ few_down_kernel(const FewParams p) {
     __shared__ FewPlan s;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    // Beside the gate/up kernel: only what was complete before that started
-    // (logits, or ids given as inputs) and the weights are read before the wait.
-    // Otherwise this CTA starts when that kernel is all but done, and takes the
-    // ids it left.
-    constexpr bool BESIDE = FewShape<FMT, NT>::RESIDENT > 1;
-    if (!BESIDE) pdl_wait();
-    build_plan<W, 8 * NT>(s, p, BESIDE && p.logits != nullptr, false);
+    // before the wait: only what was complete before the gate/up kernel started
+    // (logits, or ids given as inputs) and the weights
+    build_plan<W, 8 * NT>(s, p, p.logits != nullptr, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
     int n0, n1;
@@ -564,7 +561,7 @@ few_down_kernel(const FewParams p) {
         fetch_w(ring + d * S::BYTES, l);
         advance(l);
     }
-    if (BESIDE) pdl_wait();  // h and the routing outputs are complete
+    pdl_wait();  // h and the routing outputs are complete
     slot_weights<W>(s, p);
     {
         Pos q = start;
@@ -653,7 +650,7 @@ few_down_kernel(const FewParams p) {
             ks = 0;
             ++ti;
         }
-        few_tile_end<ACT, W>(sums, both, p.out, p.T, p.H, a, n1, rank);
+        few_tile_end<ACT, W>(sums, both, p.out, p.T, p.H, a, n1, rank, tile == ntiles - 1);
     }
 }
 
