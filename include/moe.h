@@ -464,6 +464,7 @@ int moe_add_rmsnorm_quant(const void* x, const void* residual, int32_t act, cons
  *     v[t, i] = g / (1 + exp(-g)) * u,   g = gate_up[t, i], u = gate_up[t, I + i]
  *   gate_up       device act [T, 2 I]
  *   q, q_scales   device uint8 [T, I] and f32 [T, ceil(I / 128)] out
+ * silu(g) of g < -87.3, below 1.1e-36 in magnitude, may count as 0.
  * Requirements: I % 8 == 0; gate_up and q 16-byte aligned.
  */
 int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, int32_t I, void* q,
@@ -480,7 +481,8 @@ int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, int32_t I, v
  *   addend        device act [M, N] or NULL; may be out
  *   out           device act [M, N] out
  *   err_word      device i32 or NULL (MOE_DEV_ERR_TIMEOUT)
- * Requirements: K % 16 == 0, N % 8 == 0, tensors 16-byte aligned.
+ * Requirements: K % 16 == 0, N % 8 == 0, tensors 16-byte aligned; K <= 2^27,
+ * M and N <= 2^30.
  */
 int moe_block_fp8_gemm(const void* a, const float* a_scales, const void* w, const float* w_scales,
                        const void* addend, void* out, int32_t act, int32_t M, int32_t N, int32_t K,

@@ -244,6 +244,8 @@ extern "C" int moe_block_fp8_gemm(const void* a, const float* a_scales, const vo
     MOE_REQUIRE(M >= 0, "%s: M=%d is negative", who, M);
     MOE_REQUIRE(N > 0 && N % 8 == 0, "%s: N=%d must be a positive multiple of 8", who, N);
     MOE_REQUIRE(K > 0 && K % 16 == 0, "%s: K=%d must be a positive multiple of 16", who, K);
+    if (M > (1 << 30) || N > (1 << 30) || K > (1 << 27))
+        return moe::fail(MOE_ERR_UNSUPPORTED, "%s: M=%d, N=%d or K=%d is too large", who, M, N, K);
     if (M == 0) return MOE_OK;
     MOE_REQUIRE(a && a_scales && w && w_scales && out, "%s: NULL pointer", who);
     MOE_REQUIRE(moe::aligned16(a) && moe::aligned16(w) && moe::aligned16(addend) && moe::aligned16(out),

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_block_kernel(const NormParam
 template <int ACT>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
     const int V = p.H / 8;
-    const int blocks = (p.T + kNormWarpRows - 1) / kNormWarpRows;
+    const int blocks = (p.T - 1) / kNormWarpRows + 1;
     if (V <= 32) return launch_pdl(add_rmsnorm_warp_kernel<ACT, 1>, blocks, 32 * kNormWarpRows, 0, st, p);
     if (V <= 64) return launch_pdl(add_rmsnorm_warp_kernel<ACT, 2>, blocks, 32 * kNormWarpRows, 0, st, p);
     const int vpt = V <= 1024 ? 1 : (V <= 2048 ? 2 : 4);

@@ -57,9 +57,9 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float s) {
 }
 
 // silu(g) * u = g / (1 + exp(-g)) * u by the hardware's 2^x and reciprocal, with
-// subnormals flushed: where exp(-g) overflows, the reciprocal of infinity is 0
-// and the product a zero, as in the formula; where it would be subnormal, 1 +
-// it is 1 either way.
+// subnormals flushed: where exp(-g) would be subnormal, 1 + it is 1 either way,
+// and below g = -87.3, where the reciprocal would be (|silu(g)| < 1.1e-36),
+// the product is a zero.
 __device__ __forceinline__ float silu_mul_fast(float g, float u) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504088896341f));  // log2(e)

@@ -194,6 +194,111 @@ def test_gemm_keeps_non_finite_rows_apart_and_repeats_bit_for_bit(moe, dev, M, N
     assert torch.equal(add.view(torch.int16), outs[0].view(torch.int16))
 
 
+# on 152 SMs: tiles of 256 (twice), 128 and 64 columns by one CTA each, then 128 and 64 by two, 128 and 64 by four
+FORMS = [(2000, 4104, 400), (520, 4104, 144), (260, 4104, 144), (130, 264, 400), (520, 1032, 4112), (260, 1032, 2064),
+         (260, 1032, 4112), (40, 520, 2064)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("addend", [False, True])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_gemm_forms_for_many_rows(moe, dev, M, N, K, addend):
+    a, sa, w, sb, add = gemm_inputs(M, N, K, "bf16", addend, M + N)
+    ref, mag = gemm_ref(a, sa, w, sb, add)
+    out = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=dev)
+    moe.moe_block_fp8_gemm(a.to(dev), sa.to(dev), w.to(dev), sb.to(dev), add.to(dev) if addend else None, out, 0, M, N,
+                           K)
+    plain.close(out, ref, "bf16", mag * (K + K / 64 + 8) * plain.F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(40, 512, 8192), (2000, 4096, 1024)])
+def test_gemm_wait_that_runs_out_is_reported(moe, dev, M, N, K):
+    """As in test_gpu_timeout.py: ordinary waits with a limit too short for them, by a cluster and by single CTAs."""
+    a, sa, w, sb, _ = (t.to(dev) if t is not None else None for t in gemm_inputs(M, N, K, "bf16", False, 5))
+    out, err = torch.empty((M, N), dtype=torch.bfloat16, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    moe.moe_block_fp8_gemm(a, sa, w, sb, None, out, 0, M, N, K, err)
+    clean = out.clone()
+    prev = moe.moe_set_wait_limit_ns(300)
+    try:
+        moe.moe_block_fp8_gemm(a, sa, w, sb, None, out, 0, M, N, K, err)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(prev)
+    assert int(err.item()) == moe.MOE_DEV_ERR_TIMEOUT
+    err.zero_()
+    moe.moe_block_fp8_gemm(a, sa, w, sb, None, out, 0, M, N, K, err)
+    assert int(err.item()) == 0 and torch.equal(out.view(torch.int16), clean.view(torch.int16))
+
+
+# ---- offsets past 32 bits --------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_rows_past_32_bits_of_bytes(moe, dev):
+    """The last rows of tensors of more than 2^31 elements equal the same rows run by themselves."""
+    T, H = 140001, 16384
+    x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    x[:3] = 0
+    x[-3:] = torch.randn((3, H), device=dev)
+    w = torch.ones(H, dtype=torch.bfloat16, device=dev)
+
+    def buffers(t, n):
+        return torch.empty((t, n), dtype=torch.uint8, device=dev), torch.empty((t, -(-n // 128)), device=dev)
+    r, y, (q, s) = torch.empty_like(x), torch.empty_like(x), buffers(T, H)
+    moe.moe_add_rmsnorm_quant(x, None, 0, w, 1e-6, T, H, r, y, q, s)
+    r1, y1, (q1, s1) = torch.empty_like(x[:3]), torch.empty_like(x[:3]), buffers(3, H)
+    moe.moe_add_rmsnorm_quant(x[-3:].clone(), None, 0, w, 1e-6, 3, H, r1, y1, q1, s1)
+    for big, one in ((r, r1), (y, y1), (q, q1), (s, s1)):
+        assert torch.equal(big[-3:], one)
+    del r, y, q, s
+    I = H // 2
+    q, s = buffers(T, I)
+    q1, s1 = buffers(3, I)
+    moe.moe_silu_mul_quant(x, 0, T, I, q, s)
+    moe.moe_silu_mul_quant(x[-3:].clone(), 0, 3, I, q1, s1)
+    assert torch.equal(q[-3:], q1) and torch.equal(s[-3:], s1)
+    del x, q, s
+    # an output of more than 2^31 elements, 128 rows of it taken by themselves too
+    K = 256
+    a, sa, w8, sb, _ = (t.to(dev) if t is not None else None for t in gemm_inputs(1, H, K, "bf16", False, 3))
+    T = T // 128 * 128
+    a = torch.randint(0, 0x70, (T, K), dtype=torch.uint8, device=dev)
+    sa = torch.rand((T, 2), device=dev)
+    out, part = torch.empty((T, H), dtype=torch.bfloat16, device=dev), torch.empty((128, H), dtype=torch.bfloat16, device=dev)
+    moe.moe_block_fp8_gemm(a, sa, w8, sb, None, out, 0, T, H, K)
+    moe.moe_block_fp8_gemm(a[-128:].clone(), sa[-128:].clone(), w8, sb, None, part, 0, 128, H, K)
+    # the two may cut the contraction differently: four sums of 64 terms, any order
+    err = (out[-128:].double() - part.double()).abs()
+    mag = (e4m3_abs(a[-128:], sa[-128:])) @ (e4m3_abs(w8, sb.repeat_interleave(128, 0))).T
+    assert torch.all(err <= mag * (2 * (K + 8) * plain.F32) + part.double().abs() * 2 * plain.U["bf16"])
+
+
+def e4m3_abs(codes, scales):
+    return (codes.view(torch.float8_e4m3fn).double() * scales.double().repeat_interleave(128, 1)).abs()
+
+
+@pytest.mark.gpu
+def test_few_tokens_of_experts_past_32_bits_of_bytes(moe, dev):
+    from mixture_experts_grouped_gb300 import ffn
+    from mixture_experts_grouped_gb300 import layer as L
+    T, H, I, E = 2, 2048, 2048, 256
+    gu = torch.empty((E, 2 * I, H), dtype=torch.bfloat16, device=dev)   # 4.3 GB
+    down = torch.empty((E, H, I), dtype=torch.bfloat16, device=dev)
+    g = gen(1)
+    ge, de = weight("bf16", 1, 2 * I, H, 2, g)["w"], weight("bf16", 1, H, I, 1, g)["w"]
+    gu[E - 1], down[E - 1] = ge[0].to(dev), de[0].to(dev)
+    layer = ffn.FewTokensLayer(T, H, I, E, 1, "bf16",
+                               L.DeviceWeight(moe.MoeWeight(0, 0, gu.data_ptr(), None, None, None), [gu]),
+                               L.DeviceWeight(moe.MoeWeight(0, 0, down.data_ptr(), None, None, None), [down]), dev)
+    layer.topk_ids.fill_(E - 1)
+    layer.topk_weights.fill_(0.75)
+    x = torch.randn((T, H), generator=g).bfloat16()
+    out = layer.forward(x.to(dev))
+    ids, w = torch.zeros((T, 1)).int(), torch.full((T, 1), 0.75)
+    ref, slack = plain.few_tokens(x, ids, w, {"w": ge}, {"w": de}, "bf16", "bf16", I, 1)
+    plain.close(out, ref, "bf16", slack)
+
+
 # ---- the layer for a few tokens -------------------------------------------------------
 
 def weight(fmt, e, n, k, groups2, g, group=128):
@@ -478,6 +583,9 @@ def test_misuse_is_refused_before_any_launch(moe, call):
     lambda m: m.moe_add_rmsnorm_quant(16, 16, 0, 16, 1e-6, 4, 32776, 16, 16, 16, 16, 0),
     lambda m: few_args(m, T=33),
     lambda m: few_args(m, H=32768, I=16384),
+    lambda m: m.moe_block_fp8_gemm(16, 16, 16, 16, None, 16, 0, 4, 128, 2 ** 27 + 16, 0, 0),
+    lambda m: m.moe_block_fp8_gemm(16, 16, 16, 16, None, 16, 0, 4, 2 ** 30 + 8, 128, 0, 0),
+    lambda m: m.moe_block_fp8_gemm(16, 16, 16, 16, None, 16, 0, 2 ** 31 - 1, 128, 128, 0, 0),
 ])
 def test_what_is_beyond_the_limits_is_unsupported(moe, call):
     with pytest.raises(moe.MoeError) as ei:
