@@ -19,13 +19,16 @@
 //            finishes an item (16 or 32 such rows, the whole contraction) by
 //            itself; items cut between warps are added once, at the end, in
 //            warp order.
-//   down     a pair of CTAs takes columns [n0, n1) of every touched expert, so
-//            the weighted sum over the experts stays inside the pair: each warp
-//            keeps its own f32 sums per token in shared memory and adds an
-//            expert's products, times the weight, when it leaves that expert;
-//            the warps' sums are added in warp order, and the two CTAs' through
-//            distributed shared memory. (One CTA per column share had 13 rows
-//            of 2048 columns: half of a unit's rows.)
+//   down     a cluster of 2, 4 or 8 CTAs takes columns [n0, n1) of every
+//            touched expert, so the weighted sum over the experts stays inside
+//            the cluster: each warp keeps its own f32 sums per token in shared
+//            memory and adds an expert's products, times the weight, when it
+//            leaves that expert; the warps' sums are added in warp order, and
+//            the CTAs' in rank order through distributed shared memory. A unit
+//            has 32 columns, so narrow layers take larger clusters: T = 16,
+//            H = 256, I = 7000, 8 bf16 experts 29.4 us in clusters of 8, 51.6 in
+//            pairs (4 columns each); at H = 2048 pairs have 27 columns, and one
+//            CTA per column share had 13.
 // No atomics on values: results do not depend on timing. The down kernel is
 // launched early (programmatic dependent launch): its plan and first weight
 // copies need nothing of the gate/up kernel, only the token operand waits.
@@ -54,6 +57,7 @@ template <int FMT, int NT> struct FewShape {
 };
 constexpr int kFewEntries = MOE_MAX_EXPERTS + kFewPairs / 8;
 constexpr int kFewCols = 33;  // columns of a down tile, and a pad
+constexpr int kFewMaxLg = 3, kFewMaxCluster = 1 << kFewMaxLg;  // CTAs that share a down tile, at most
 
 struct FewPlan {
     int n;                           // entries: touched experts, ascending, split
@@ -446,11 +450,11 @@ few_gate_up_kernel(const FewParams p) {
 // ---- down ---------------------------------------------------------------------------
 
 // The end of a tile of up to 32 columns: adds the warps' sums in warp order
-// (clearing them for the next tile, if there is one), then the two CTAs', half
-// of the tile each, and writes it.
+// (clearing them for the next tile, if there is one), then the cluster's CTAs',
+// in rank order, an equal part of the tile each, and writes it.
 template <int ACT, int W>
 __device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* out, int T, int H, int n0, int n1,
-                                          uint32_t rank, bool last) {
+                                          uint32_t rank, int lg, bool last) {
     __syncthreads();
     for (int i = threadIdx.x; i < T * 32; i += W * 32) {
         float* at = sums + (i >> 5) * kFewCols + (i & 31);
@@ -462,20 +466,28 @@ __device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* ou
             for (int w = 0; w < W; ++w) at[w * T * kFewCols] = 0.0f;
     }
     cluster_sync_all();
-    const uint32_t peer = mapa_shared(smem_u32(both), rank ^ 1);
-    for (int i = threadIdx.x + rank * T * 16; i < static_cast<int>(rank + 1) * T * 16; i += W * 32) {
-        const float a = both[i], b = ld_dsmem_f32(peer + 4 * i);
-        const float v = rank == 0 ? a + b : b + a;
+    const int part = T * 32 >> lg, end = (rank + 1) * part;
+    for (int i = rank * part + threadIdx.x; i < end; i += W * 32) {
+        const uint32_t at = smem_u32(both + i);
+        float v = ld_dsmem_f32(mapa_shared(at, 0)) + ld_dsmem_f32(mapa_shared(at, 1));
+        if (lg > 1) {
+            float f[kFewMaxCluster];
+#pragma unroll
+            for (int r = 2; r < kFewMaxCluster; ++r) f[r] = r >> lg ? 0.0f : ld_dsmem_f32(mapa_shared(at, r));
+#pragma unroll
+            for (int r = 2; r < kFewMaxCluster; ++r)
+                if (!(r >> lg)) v += f[r];
+        }
         if (n0 + (i & 31) < n1)
             reinterpret_cast<typename Act<ACT>::T*>(out)[static_cast<size_t>(i >> 5) * H + n0 + (i & 31)] =
                 Act<ACT>::from_f(v);
     }
-    cluster_sync_all();  // neither CTA reuses `both` or leaves while the other reads it
+    cluster_sync_all();  // no CTA reuses `both` or leaves while another reads it
 }
 
 template <int FMT, int ACT, int NT>
 __global__ void __launch_bounds__(FewShape<FMT, NT>::DN_WARPS * 32, FewShape<FMT, NT>::RESIDENT)
-few_down_kernel(const FewParams p) {
+few_down_kernel(const FewParams p, const int lg) {  // clusters of 1 << lg CTAs
     using U = Unit<FMT, ACT, false>;
     using S = Stage<U>;
     constexpr int RING = FewShape<FMT, NT>::DN_RING, W = FewShape<FMT, NT>::DN_WARPS, MT = U::MT;
@@ -485,14 +497,13 @@ few_down_kernel(const FewParams p) {
     float* both = sums + W * p.T * kFewCols;                                 // [T][32]: this CTA's sums of a tile
     __shared__ FewPlan s;
     const uint32_t rank = cluster_ctarank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     // before the wait: only what was complete before the gate/up kernel started
     // (logits, or ids given as inputs) and the weights
     build_plan<W, 8 * NT>(s, p, p.logits != nullptr, false);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int K = p.I, n = s.n;
     int n0, n1;
-    part_of(p.H / U::ALIGN, pairs, pair, n0, n1);
+    part_of(p.H / U::ALIGN, gridDim.x >> lg, blockIdx.x >> lg, n0, n1);
     n0 *= U::ALIGN;
     n1 *= U::ALIGN;
     const int ntiles = (n1 - n0 + 31) / 32;
@@ -500,9 +511,9 @@ few_down_kernel(const FewParams p) {
     float* mine = sums + warp * p.T * kFewCols;
     for (int i = tid; i < W * p.T * kFewCols; i += W * 32) sums[i] = 0.0f;
 
-    // A tile's units (entry, contraction step), shared by the pair's warps: this warp's share is the same in every tile
+    // A tile's units (entry, contraction step), shared by the cluster's warps: this warp's share is the same in every tile
     int u0, u1;
-    part_of(n * nks, 2 * W, static_cast<int>(rank) * W + warp, u0, u1);
+    part_of(n * nks, W << lg, static_cast<int>(rank) * W + warp, u0, u1);
     const int count = u1 - u0;
     const int ti_first = u0 / nks, ks_first = u0 - ti_first * nks;
     uint8_t* ring = few_smem + warp * RING * S::BYTES;
@@ -650,7 +661,7 @@ few_down_kernel(const FewParams p) {
             ks = 0;
             ++ti;
         }
-        few_tile_end<ACT, W>(sums, both, p.out, p.T, p.H, a, n1, rank, tile == ntiles - 1);
+        few_tile_end<ACT, W>(sums, both, p.out, p.T, p.H, a, n1, rank, lg, tile == ntiles - 1);
     }
 }
 
@@ -672,26 +683,53 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
         if (set_smem_limit(reinterpret_cast<const void*>(few_gate_up_kernel<FMT, ACT, NT>), gu_smem) != MOE_OK ||
             set_smem_limit(reinterpret_cast<const void*>(few_down_kernel<FMT, ACT, NT>), dn_most) != MOE_OK)
             return cudaGetLastError();
-        configured_for = dev;
     }
-    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::GU_WARPS + 1) * 32, gu_smem, st, p);
-    if (e != cudaSuccess) return e;
-    const int cols = p.H / DN::ALIGN, pairs = sms / 2 < cols ? (sms >= 2 ? sms / 2 : 1) : cols;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(F::DN_WARPS * 32);
+    cfg.attrs = attr;
+    static int most[kFewMaxLg + 1];  // by lg: clusters that fit the GPU at once, a CTA per SM
+    if (configured_for != dev) {
+        cfg.dynamicSmemBytes = dn_most;
+        cfg.numAttrs = 1;
+        for (int lg = 1; lg <= kFewMaxLg; ++lg) {
+            attr[0].val.clusterDim.x = 1 << lg;
+            cfg.gridDim = dim3(1 << lg);
+            if (cudaOccupancyMaxActiveClusters(&most[lg], few_down_kernel<FMT, ACT, NT>, &cfg) != cudaSuccess)
+                return cudaGetLastError();
+            most[lg] = most[lg] < sms >> lg ? most[lg] : sms >> lg;
+        }
+        configured_for = dev;
+    }
+    // The cluster's size: the fewest units a warp. A tile's end counts as four (about 1.5 us)
+    const int cols = p.H / DN::ALIGN;
+    const int units = (p.T * p.k < p.E ? p.T * p.k : p.E) * ((p.I + DN::SPAN - 1) / DN::SPAN);
+    int best = 1, groups = 1;
+    int64_t least = INT64_MAX;
+    for (int lg = 1; lg <= kFewMaxLg; ++lg) {
+        const int n = most[lg] < cols ? most[lg] : cols, warps = F::DN_WARPS << lg;
+        if (n < 1) break;
+        const int tiles = ((cols + n - 1) / n * DN::ALIGN + 31) / 32;
+        const int64_t steps = static_cast<int64_t>(tiles) * ((units + warps - 1) / warps + 4);
+        if (steps < least) {
+            least = steps;
+            best = lg;
+            groups = n;
+        }
+    }
+    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::GU_WARPS + 1) * 32, gu_smem, st, p);
+    if (e != cudaSuccess) return e;
+    attr[0].val.clusterDim.x = 1 << best;
+    cfg.gridDim = dim3(groups << best);
     cfg.dynamicSmemBytes = dn_ring + dn_token * p.T;
     cfg.stream = st;
-    cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, few_down_kernel<FMT, ACT, NT>, p);
+    return cudaLaunchKernelEx(&cfg, few_down_kernel<FMT, ACT, NT>, p, best);
 }
 
 // One token tile (8 tokens of an expert at a time) where no expert can have
