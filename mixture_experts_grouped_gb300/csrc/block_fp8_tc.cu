@@ -17,9 +17,9 @@
 //     stands in their way: a warp fetches the scales of a block while its MMAs
 //     run and leaves them in shared memory. A thread needs about 650 clocks to
 //     wait for, issue and commit a block's MMAs, whatever their width, so two
-//     threads issue, a block each in turn (their buffers are independent). CTA pairs (M = 256) halve the
-//     shared-memory traffic but lengthen every signal by a cluster hop, and
-//     measured slower.
+//     threads issue, a block each in turn (their buffers are independent).
+//     CTA pairs (M = 256) halve the shared-memory traffic but lengthen every
+//     signal by a cluster hop, and measured slower.
 //   * Too few tiles for the GPU: a cluster of 2 or 4 CTAs per tile, each with a
 //     part of the contraction; each CTA then adds a slice of the columns, in
 //     rank order, from all of them (distributed shared memory).
@@ -446,25 +446,29 @@ int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const c
 }
 
 // Tile width and split of the contraction, by the time that each choice would
-// take: the waves of CTAs, times the blocks of 128 of each, times what a block
+// take: the waves of CTAs, times the blocks of 128 of each at what a block
 // costs at that width (measured on a GB300: 260, 310 and 480 ns at 64, 128 and
-// 256 columns), and what a launch costs (2.5 us; 4.5 and 5.5 with the meeting
-// of 2 or 4 CTAs). A wide tile reads less and spends fewer steps per sum, a
-// narrow or split one fills more of the GPU: M = 128, N = 4096, K = 14336
-// takes 16.8 us at 128 x 4 CTAs, 19.5 at 64 x 2, 31 at 64 and 57 at 256.
+// 256 columns) and what a tile's end holds up the next (0.1, 0.5 and 2.3 us),
+// and what a launch costs (2.5 us; 4.5 and 5.5 with the meeting of 2 or 4
+// CTAs). A wide tile reads less and spends fewer steps per sum, a narrow or
+// split one fills more of the GPU: M = 128, N = 4096, K = 14336 takes 16.8 us
+// at 128 x 4 CTAs, 19.5 at 64 x 2, 31 at 64 and 57 at 256; M = 2048, N = 2816,
+// K = 2048 22.3 at 256, 18.5 at 128, 22.8 at 64. A tile is split only where
+// every CTA runs at once: each wave of clusters begins and ends anew, and those
+// 352 tiles took 36 us at 128 x 2.
 template <int ACT> int pick_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
     static const struct {
-        int bn, parts, block_ns, fixed_ns;
-    } forms[] = {{256, 1, 480, 2500}, {128, 1, 310, 2500}, {64, 1, 260, 2500}, {128, 2, 310, 4500},
-                 {64, 2, 260, 4500},  {128, 4, 310, 5500}, {64, 4, 260, 5500}};
+        int bn, parts, block_ns, tile_ns, fixed_ns;
+    } forms[] = {{256, 1, 480, 2300, 2500}, {128, 1, 310, 500, 2500}, {64, 1, 260, 100, 2500}, {128, 2, 310, 0, 4500},
+                 {64, 2, 260, 0, 4500},     {128, 4, 310, 0, 5500},   {64, 4, 260, 0, 5500}};
     int best = 0;
     int64_t best_ns = INT64_MAX;
     for (int i = 0; i < 7; ++i) {
-        if (p.kb < forms[i].parts) continue;
-        const int64_t ctas = static_cast<int64_t>((p.M + 127) / 128) * ((p.N + forms[i].bn - 1) / forms[i].bn) *
-                             forms[i].parts;
-        const int64_t blocks = (p.kb + forms[i].parts - 1) / forms[i].parts;
-        const int64_t ns = (ctas + sms - 1) / sms * blocks * forms[i].block_ns + forms[i].fixed_ns;
+        const auto& f = forms[i];
+        const int64_t ctas = static_cast<int64_t>((p.M + 127) / 128) * ((p.N + f.bn - 1) / f.bn) * f.parts;
+        if (f.parts > 1 && (p.kb < f.parts || ctas > sms)) continue;
+        const int64_t blocks = (p.kb + f.parts - 1) / f.parts;
+        const int64_t ns = (ctas + sms - 1) / sms * (blocks * f.block_ns + f.tile_ns) + f.fixed_ns;
         if (ns < best_ns) {
             best_ns = ns;
             best = i;

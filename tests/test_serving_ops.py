@@ -194,9 +194,10 @@ def test_gemm_keeps_non_finite_rows_apart_and_repeats_bit_for_bit(moe, dev, M, N
     assert torch.equal(add.view(torch.int16), outs[0].view(torch.int16))
 
 
-# on 152 SMs: tiles of 256 (twice), 128 and 64 columns by one CTA each, then 128 and 64 by two, 128 and 64 by four
+# on 152 SMs: tiles of 128, 64, 128 and 64 columns by one CTA each, 128 and 64 by two CTAs, 128 and 64 by four, and 256
+# columns, one and two tiles to a CTA
 FORMS = [(2000, 4104, 400), (520, 4104, 144), (260, 4104, 144), (130, 264, 400), (520, 1032, 4112), (260, 1032, 2064),
-         (260, 1032, 4112), (40, 520, 2064)]
+         (260, 1032, 4112), (40, 520, 2064), (268, 6712, 2064), (778, 8456, 2064)]
 
 
 @pytest.mark.gpu
@@ -212,7 +213,7 @@ def test_gemm_forms_for_many_rows(moe, dev, M, N, K, addend):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(40, 512, 8192), (2000, 4096, 1024)])
+@pytest.mark.parametrize("M,N,K", [(40, 512, 8192), (2000, 4096, 1024), (300, 7168, 2048)])
 def test_gemm_wait_that_runs_out_is_reported(moe, dev, M, N, K):
     """As in test_gpu_timeout.py: ordinary waits with a limit too short for them, by a cluster and by single CTAs."""
     a, sa, w, sb, _ = (t.to(dev) if t is not None else None for t in gemm_inputs(M, N, K, "bf16", False, 5))
