@@ -732,12 +732,16 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, few_down_kernel<FMT, ACT, NT>, p, best);
 }
 
-// One token tile (8 tokens of an expert at a time) where no expert can have
-// more or few will; otherwise two.
+// Token tiles of 8 a product takes: one, and an expert with more tokens is read
+// again (mostly from L2), or two, where most experts have more than 6. us at one
+// / two, H = 2048, T = 32, k = 8, E = 48 and 32: NVFP4 70 / 73 and 64 / 58, FP8
+// 64 / 69 and 57 / 55, GPTQ 70 / 76 and 64.4 / 63.7. Two never paid for bf16 (90 /
+// 111 at E = 32, 78 / 90 at E = 16).
 template <int FMT, int ACT>
 cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t st) {
-    return p.T <= 8 || p.T * p.k <= 4 * p.E ? launch_few_nt<FMT, ACT, 1>(p, sms, st)
-                                            : launch_few_nt<FMT, ACT, 2>(p, sms, st);
+    if constexpr (FMT != MOE_W_BF16)
+        if (p.T > 8 && p.T * p.k > 6 * p.E) return launch_few_nt<FMT, ACT, 2>(p, sms, st);
+    return launch_few_nt<FMT, ACT, 1>(p, sms, st);
 }
 
 }  // namespace moe

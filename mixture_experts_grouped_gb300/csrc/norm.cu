@@ -14,9 +14,9 @@ namespace {
 // it is normed, y not before it is quantised). HBM-bound: a row is read once
 // into registers (VPT 16-byte vectors a thread), its sum of squares reduced,
 // and every output written from there. A group of 128 columns is half a warp,
-// so its maximum takes four shuffles and no shared memory. Measured: T = 4001,
-// H = 4096, every output: 24.2
-// us, 6.1 TB/s; one row of 2048, 1.6 us, a launch's latency.
+// so its maximum takes four shuffles and no shared memory. Measured: 4001 rows
+// of 4096, every output: 24.2 us, 6.1 TB/s; one row of 2048: 1.6 us, a launch's
+// latency.
 
 template <int ACT, int VPT>
 struct NormRow {
