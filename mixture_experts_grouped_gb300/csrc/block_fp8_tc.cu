@@ -28,7 +28,12 @@
 //     MMAs, warp 3 fetches scales, the others add and store. Every wait is
 //     bounded. At BN = 256 the 20 warps' 96 registers are split 32 / 112
 //     between the first four and the others. (A second copying warp, and
-//     scales fetched two blocks ahead, measured 5 to 10% slower.)
+//     scales fetched two blocks ahead, measured 5 to 10% slower; a second
+//     staging area, in the place of the fourth stage, the same.)
+// Measured: M = 4096, N = 28672, K = 4096 410 us (2.35 PFLOP/s; tensor pipe 49%
+// busy: 480 ns a block of 128 x 256 x 128, of which its MMAs take half, and 2.3 us
+// a tile for the stores); M = 17, N = 4096, K = 14336 16.3 us (8.7 for the bytes:
+// 28 blocks of 310 ns and the meeting of four CTAs).
 #include "block_fp8.cuh"
 
 namespace moe {

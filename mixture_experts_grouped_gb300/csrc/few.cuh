@@ -29,6 +29,13 @@
 //            H = 256, I = 7000, 8 bf16 experts 29.4 us in clusters of 8, 51.6 in
 //            pairs (4 columns each); at H = 2048 pairs have 27 columns, and one
 //            CTA per column share had 13.
+// Measured, us and of the touched weights' time at HBM's rate: bf16, 8 of 128
+// experts of 2048 x 768, one token 23.4 (47%: 4.9 pass before the first weights
+// arrive, about 4 between the kernels and at the end); 8 experts of 4096 x 14336,
+// 7 tokens 410 (88%, HBM); GPTQ, 64 of 2048 x 1408, 16 tokens 82 (41%) and NVFP4,
+// 128 of 2048 x 768, 32 tokens 113 (39%): the conversion keeps 50 and 60% of the
+// issue slots and 45 and 54% of the integer pipe busy over the whole kernels,
+// starts and ends included. (Gate/up on pairs of CTAs too: GPTQ 82.4 -> 85.8.)
 // No atomics on values: results do not depend on timing. The down kernel is
 // launched early (programmatic dependent launch): its plan and first weight
 // copies need nothing of the gate/up kernel, only the token operand waits.
@@ -45,12 +52,13 @@ constexpr int kFewPairs = MOE_MAX_FEW_TOKENS * MOE_MAX_TOPK;
 // Warps per CTA and ring stages per warp. bf16 has next to nothing to convert:
 // 8 warps keep up, and a CTA of each kernel fits an SM, so the down kernel's
 // start hides behind the gate/up kernel's end. The quantised formats are bound
-// by the instructions of their conversion and want all the warps of an SM
-// (GPTQ's wide gate/up items with two token tiles want registers more than
-// warps: 11).
+// by the instructions of their conversion and want all the warps of an SM (us at
+// 15 / 11 warps, T = 32, H = 2048: FP8 110 / 120, NVFP4 111 / 115; GPTQ, T = 16,
+// 84 / 87). GPTQ with two token tiles has 11, which is what shared memory holds.
+// A fifth stage is worth 1% to FP8, and the others have no room for it.
 template <int FMT, int NT> struct FewShape {
     static constexpr bool DENSE = FMT == MOE_W_BF16, GPTQ = FMT == MOE_W_GPTQ_INT4;
-    static constexpr int GU_WARPS = DENSE ? 8 : (GPTQ && NT > 1 ? 11 : 15), DN_WARPS = DENSE ? 8 : 15;
+    static constexpr int WARPS = DENSE ? 8 : (GPTQ && NT > 1 ? 11 : 15);
     static constexpr int GU_RING = FMT == MOE_W_FP8_E4M3 ? 5 : 4;
     static constexpr int DN_RING = 4;
     static constexpr int RESIDENT = DENSE ? 2 : 1;  // CTAs per SM the registers must allow
@@ -233,11 +241,11 @@ __device__ __forceinline__ void publish_routing(const FewParams& p, int t, int s
 // ---- gate/up ----------------------------------------------------------------------
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__((FewShape<FMT, NT>::GU_WARPS + 1) * 32, FewShape<FMT, NT>::RESIDENT)
+__global__ void __launch_bounds__((FewShape<FMT, NT>::WARPS + 1) * 32, FewShape<FMT, NT>::RESIDENT)
 few_gate_up_kernel(const FewParams p) {
     using U = Unit<FMT, ACT, true>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT, NT>::GU_RING, W = FewShape<FMT, NT>::GU_WARPS, MT = U::MT, ROWS = U::ROWS;
+    constexpr int RING = FewShape<FMT, NT>::GU_RING, W = FewShape<FMT, NT>::WARPS, MT = U::MT, ROWS = U::ROWS;
     extern __shared__ uint8_t few_smem[];
     float4* cut = reinterpret_cast<float4*>(few_smem + W * RING * S::BYTES);  // [W][2][MT][NT][32]: sums of cut items
     __shared__ FewPlan s;
@@ -486,11 +494,11 @@ __device__ __noinline__ void few_tile_end(float* sums, float* both, uint16_t* ou
 }
 
 template <int FMT, int ACT, int NT>
-__global__ void __launch_bounds__(FewShape<FMT, NT>::DN_WARPS * 32, FewShape<FMT, NT>::RESIDENT)
+__global__ void __launch_bounds__(FewShape<FMT, NT>::WARPS * 32, FewShape<FMT, NT>::RESIDENT)
 few_down_kernel(const FewParams p, const int lg) {  // clusters of 1 << lg CTAs
     using U = Unit<FMT, ACT, false>;
     using S = Stage<U>;
-    constexpr int RING = FewShape<FMT, NT>::DN_RING, W = FewShape<FMT, NT>::DN_WARPS, MT = U::MT;
+    constexpr int RING = FewShape<FMT, NT>::DN_RING, W = FewShape<FMT, NT>::WARPS, MT = U::MT;
     static_assert(U::ROWS == 32, "32 columns a tile");
     extern __shared__ uint8_t few_smem[];
     float* sums = reinterpret_cast<float*>(few_smem + W * RING * S::BYTES);  // [W][T][kFewCols]
@@ -671,9 +679,9 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     using GU = Unit<FMT, ACT, true>;
     using DN = Unit<FMT, ACT, false>;
     constexpr int gu_smem =
-        F::GU_WARPS * (F::GU_RING * Stage<GU>::BYTES + static_cast<int>(sizeof(float4)) * 2 * GU::MT * NT * 32);
-    constexpr int dn_ring = F::DN_WARPS * F::DN_RING * Stage<DN>::BYTES;
-    constexpr int dn_token = static_cast<int>(sizeof(float)) * (F::DN_WARPS * kFewCols + 32);
+        F::WARPS * (F::GU_RING * Stage<GU>::BYTES + static_cast<int>(sizeof(float4)) * 2 * GU::MT * NT * 32);
+    constexpr int dn_ring = F::WARPS * F::DN_RING * Stage<DN>::BYTES;
+    constexpr int dn_token = static_cast<int>(sizeof(float)) * (F::WARPS * kFewCols + 32);
     constexpr int dn_most = dn_ring + dn_token * MOE_MAX_FEW_TOKENS;
     static_assert(gu_smem + sizeof(FewPlan) <= 232448 && dn_most + sizeof(FewPlan) <= 232448, "shared memory");
     static int configured_for = -1;
@@ -691,7 +699,7 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(F::DN_WARPS * 32);
+    cfg.blockDim = dim3(F::WARPS * 32);
     cfg.attrs = attr;
     static int most[kFewMaxLg + 1];  // by lg: clusters that fit the GPU at once, a CTA per SM
     if (configured_for != dev) {
@@ -712,7 +720,7 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
     int best = 1, groups = 1;
     int64_t least = INT64_MAX;
     for (int lg = 1; lg <= kFewMaxLg; ++lg) {
-        const int n = most[lg] < cols ? most[lg] : cols, warps = F::DN_WARPS << lg;
+        const int n = most[lg] < cols ? most[lg] : cols, warps = F::WARPS << lg;
         if (n < 1) break;
         const int tiles = ((cols + n - 1) / n * DN::ALIGN + 31) / 32;
         const int64_t steps = static_cast<int64_t>(tiles) * ((units + warps - 1) / warps + 4);
@@ -722,7 +730,7 @@ cudaError_t launch_few_nt(const FewParams& p, int sms, cudaStream_t st) {
             groups = n;
         }
     }
-    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::GU_WARPS + 1) * 32, gu_smem, st, p);
+    const cudaError_t e = launch_pdl(few_gate_up_kernel<FMT, ACT, NT>, sms, (F::WARPS + 1) * 32, gu_smem, st, p);
     if (e != cudaSuccess) return e;
     attr[0].val.clusterDim.x = 1 << best;
     cfg.gridDim = dim3(groups << best);
