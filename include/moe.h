@@ -496,7 +496,8 @@ size_t moe_few_tokens_workspace_size(int32_t T, int32_t top_k, int32_t I);
  * kernels (no sort, no gather, no padding):
  *     out[t] = act( sum_j w[t, j] * (h_tj . Wd_e),  e = ids[t, j] )
  *     h_tj[i] = act( silu(x[t] . Wg_e[i]) * (x[t] . Wu_e[i]) )
- * Weights stream from HBM once per touched expert; sums are f32 and the only
+ * Weights stream from HBM once per touched expert (read again, as a rule from
+ * L2, for each further 8 or 16 of its tokens); sums are f32 and the only
  * roundings are h and out (each once).
  *   x             device act [T, H]
  *   logits        device f32 [T, E]: routed as by moe_route_topk_softmax (same
