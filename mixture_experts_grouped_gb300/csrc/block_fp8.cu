@@ -15,9 +15,9 @@
 //     in turn, and the warps' sums added through shared memory in warp order.
 //   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a, read
 //     once per unit for all its 32 weight rows.
-// Measured: M = 1, N = 2816, K = 2048 3.4 us (0.85 of it for the bytes at HBM's
+// Measured: M = 1, N = 2816, K = 2048 3.1 us (0.85 of it for the bytes at HBM's
 // rate: a launch, one round trip to HBM and the sum of the warps make the rest);
-// M = 8, N = 28672, K = 4096 26.9 us, 4.4 TB/s: every 32 rows the warps meet.
+// M = 8, N = 28672, K = 4096 26.0 us, 4.5 TB/s: every 32 rows the warps meet.
 // More rows run on the 5th-generation tensor cores (block_fp8_tc.cu).
 #include "block_fp8.cuh"
 #include "stream.cuh"
@@ -40,6 +40,12 @@ inline bool rows_form(int M, int N, int K) {
 template <int NT> struct BfStage {
     static constexpr int X_AT = 4096, SA_AT = X_AT + 1024 * NT, SB_AT = SA_AT + 32 * NT, BYTES = SB_AT + 16;
     static constexpr int FIT = 204800 / (kBfWarps * BYTES), RING = FIT < 6 ? FIT : 6;
+    // Sums of the warps. One token tile: of all 32 rows, in two areas in turn, one
+    // barrier a tile (M = 1, N = 2816, K = 2048 3.1 us, 3.4 by 16 rows); with more
+    // tokens 16 rows, two barriers (M = 16, N = K = 2048 3.8 us, 4.0 by 32).
+    static constexpr int HALVES = NT == 1 ? 2 : 1, RED = kBfWarps * 512 * NT * HALVES * HALVES;
+    static constexpr int SMEM = kBfWarps * RING * BYTES + RED;
+    static_assert(SMEM <= 232448, "shared memory over the limit");
 };
 
 __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -63,7 +69,7 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
     const int ntiles = (n1 - n0 + 31) / 32;
     const int K = p.K;
     uint8_t* ring = bf_smem + warp * RING * S::BYTES;
-    float4* red = reinterpret_cast<float4*>(bf_smem + kBfWarps * RING * S::BYTES);  // [warps][NT][32], 16 rows' sums
+    float4* red = reinterpret_cast<float4*>(bf_smem + kBfWarps * RING * S::BYTES);  // [areas][halves][warps][NT][32]
 
     // Lane (g, c) copies and uses, of rows g, g + 8, g + 16, g + 24 and of token
     // g of each tile, the 16-byte pieces c and c + 4 of a block's 128 codes.
@@ -185,21 +191,27 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                 }
             }
         }
-        // the tile's contraction is complete: add the warps' sums, 16 rows at a time
+        // the tile's contraction is complete: add the warps' sums, HALVES x 16 rows at a time
+        constexpr int HALVES = S::HALVES;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (first + 16 * h >= n1) break;
+        for (int h0 = 0; h0 < 2; h0 += HALVES) {
+            if (first + 16 * h0 >= n1) break;
+            float4* area = red + (HALVES == 2 ? tile & 1 : 0) * HALVES * kBfWarps * NT * 32;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (t < nt)
-                    red[(warp * NT + t) * 32 + lane] =
-                        make_float4(acc[h][t][0], acc[h][t][1], acc[h][t][2], acc[h][t][3]);
+            for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t < nt)
+                        area[((h * kBfWarps + warp) * NT + t) * 32 + lane] = make_float4(
+                            acc[h0 + h][t][0], acc[h0 + h][t][1], acc[h0 + h][t][2], acc[h0 + h][t][3]);
             __syncthreads();
-            for (int i = tid; i < ms * 16; i += kBfThreads) {
-                const int m = i >> 4, r = i & 15, n = first + 16 * h + r;
-                // row r, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8) + (m & 1)
-                const float* src = reinterpret_cast<const float*>(red + (m >> 3) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) +
-                                   2 * (r >> 3) + (m & 1);
+            for (int i = tid; i < ms * 16 * HALVES; i += kBfThreads) {
+                const int r = i % (16 * HALVES), m = i / (16 * HALVES), h = r >> 4, n = first + 16 * h0 + r;
+                // row r & 15, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8 & 1) + (m & 1)
+                const float* src =
+                    reinterpret_cast<const float*>(area + (h * kBfWarps * NT + (m >> 3)) * 32 + 4 * (r & 7) +
+                                                   ((m & 7) >> 1)) +
+                    2 * ((r >> 3) & 1) + (m & 1);
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kBfWarps; ++w) v += src[w * NT * 128];
@@ -209,14 +221,14 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                     reinterpret_cast<typename Act<ACT>::T*>(p.out)[at] = Act<ACT>::from_f(v);
                 }
             }
-            __syncthreads();
+            if (HALVES == 1) __syncthreads();  // with two areas the next tile's barrier parts a reader and the next writer
         }
     }
 }
 
 template <int ACT, int NT>
 cudaError_t launch_rows_nt(const BfParams& p, dim3 grid, cudaStream_t st) {
-    constexpr int smem = kBfWarps * (BfStage<NT>::RING * BfStage<NT>::BYTES + 512 * NT);
+    constexpr int smem = BfStage<NT>::SMEM;
     static int configured_for = -1;
     int dev = 0;
     cudaGetDevice(&dev);
