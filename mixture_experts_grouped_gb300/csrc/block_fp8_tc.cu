@@ -35,21 +35,22 @@
 // a tile for the stores); M = 17, N = 4096, K = 14336 16.3 us (8.7 for the bytes:
 // 28 blocks of 310 ns and the meeting of four CTAs).
 #include "block_fp8.cuh"
+#include "tc_ring.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kTcA = 128 * 128;  // bytes of a stage's activation rows per CTA
 
-template <int BN> struct TcShape {
+template <int BN, int PARTS> struct TcShape {
     static constexpr int STAGE = kTcA + BN * 128;
-    static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 5 : 6);
-    static constexpr int NBUF = 512 / BN < 4 ? 512 / BN : 4;
+    static constexpr int STAGES = tc_stages(BN, PARTS), NBUF = tc_buffers(BN);
+    static_assert(STAGES % kTcIssuers == 0 && NBUF % kTcIssuers == 0, "every stage and buffer is one issuing thread's");
     static constexpr int COLS = NBUF * BN;             // TMEM columns
     static constexpr int GROUPS = BN == 64 ? 2 : 4;    // warpgroups that read a buffer back
     static constexpr int EPI_WARPS = 4 * GROUPS, THREADS = 128 + 128 * GROUPS;
     static constexpr int PER = BN / GROUPS;            // columns per epilogue warp
-    static constexpr int OUT_BYTES = 32 * 32 * 2;                   // a warp's staging area: 32 x 32 outputs
+    static constexpr int OUT_BYTES = PARTS > 1 ? 0 : 32 * 32 * 2;   // a warp's staging area: 32 x 32 outputs
     static constexpr int OUT_AT = STAGES * STAGE;
     static constexpr int SCALE_AT = OUT_AT + EPI_WARPS * OUT_BYTES; // [NBUF]: 128 row scales, 2 column block scales
     static constexpr int SCALES = 136;                              // floats of a buffer's scales
@@ -59,7 +60,7 @@ template <int BN> struct TcShape {
 };
 
 struct TcTail {
-    uint64_t full[8], empty[8], tfull[4], tempty[4], mma_done[2];
+    uint64_t full[8], empty[8], tfull[4], tempty[4], mma_done[kTcIssuers];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -119,10 +120,10 @@ template <int BN> __device__ __forceinline__ TcTile tc_tile(const BfParams& p, i
 
 // PARTS > 1: one tile per cluster of PARTS CTAs; otherwise one CTA walks tiles.
 template <int ACT, int BN, int PARTS>
-__global__ void __launch_bounds__(TcShape<BN>::THREADS, 1)
+__global__ void __launch_bounds__(TcShape<BN, PARTS>::THREADS, 1)
 block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_o, const BfParams p, int a_rows, int32_t* err, uint64_t wait_ns) {
-    using S = TcShape<BN>;
+    using S = TcShape<BN, PARTS>;
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024_shared(smem_raw);
@@ -146,7 +147,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             mbar_init(&s.tfull[i], 2);  // the MMAs, and its scales
             mbar_init(&s.tempty[i], S::EPI_WARPS);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&s.mma_done[i], 1);
+        for (int i = 0; i < kTcIssuers; ++i) mbar_init(&s.mma_done[i], 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -199,10 +200,11 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             constexpr uint32_t idesc = e4m3_idesc(128, BN);
             const int64_t mine = first < n_tiles ? (n_tiles - 1 - first) / step + 1 : 0;
             const int64_t blocks = mine * kbs;
-            // block i: stage i mod STAGES, buffer i mod NBUF, and their phases
+            // block i: stage i mod STAGES, buffer i mod NBUF, and their phases. Both are this
+            // thread's alone (tc_ring.cuh): a wait by parity needs the phase before to have been seen
             uint32_t stage = warp - 1, phase = 0, buf = warp - 1, bphase = 0;
             bool ok = warp - 1 < blocks && mbar_wait(&s.full[stage], 0, wc);
-            for (int64_t i = warp - 1; i < blocks && ok; i += 2) {
+            for (int64_t i = warp - 1; i < blocks && ok; i += kTcIssuers) {
                 if (!mbar_wait(&s.tempty[buf], bphase ^ 1, wc)) break;
                 tc_fence_after();
                 const uint64_t ad = sw128_desc(smem_u32(smem + stage * S::STAGE));
@@ -214,17 +216,17 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                 mma_e4m3(d, ad + 6, bd + 6, idesc, 1);
                 tc_commit(&s.tfull[buf]);
                 tc_commit(&s.empty[at]);
-                stage += 2;
+                stage += kTcIssuers;
                 if (stage >= S::STAGES) {
                     stage -= S::STAGES;
                     phase ^= 1;
                 }
-                buf += 2;
+                buf += kTcIssuers;
                 if (buf >= S::NBUF) {
                     buf -= S::NBUF;
                     bphase ^= 1;
                 }
-                if (i + 2 < blocks) ok = mbar_wait(&s.full[stage], phase, wc);
+                if (i + kTcIssuers < blocks) ok = mbar_wait(&s.full[stage], phase, wc);
             }
             tc_commit(&s.mma_done[warp - 1]);
             mbar_drain(&s.mma_done[warp - 1], 0, kWaitLimitNs / 8);
@@ -410,7 +412,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
 
 template <int ACT, int BN, int PARTS>
 int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
-    using S = TcShape<BN>;
+    using S = TcShape<BN, PARTS>;
     static_assert(PARTS == 1 || S::EPI_WARPS * 32 * S::PER * 4 <= S::OUT_AT, "a tile's sums fit in the stages");
     auto kernel = block_fp8_tc_kernel<ACT, BN, PARTS>;
     static int configured_for = -1;
@@ -456,9 +458,9 @@ int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const c
 // 256 columns) and what a tile's end holds up the next (0.1, 0.5 and 2.3 us),
 // and what a launch costs (2.5 us; 4.5 and 5.5 with the meeting of 2 or 4
 // CTAs). A wide tile reads less and spends fewer steps per sum, a narrow or
-// split one fills more of the GPU: M = 128, N = 4096, K = 14336 takes 16.8 us
+// split one fills more of the GPU: M = 128, N = 4096, K = 14336 takes 16.6 us
 // at 128 x 4 CTAs, 19.5 at 64 x 2, 31 at 64 and 57 at 256; M = 2048, N = 2816,
-// K = 2048 22.3 at 256, 18.5 at 128, 22.8 at 64. A tile is split only where
+// K = 2048 22.3 at 256, 19.0 at 128, 22.8 at 64. A tile is split only where
 // every CTA runs at once: each wave of clusters begins and ends anew, and those
 // 352 tiles took 36 us at 128 x 2.
 template <int ACT> int pick_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
