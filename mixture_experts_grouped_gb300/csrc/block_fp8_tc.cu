@@ -255,7 +255,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
 #pragma unroll
                     for (int j = 0; j < 4; ++j) a[j] = __ldg(sa[j] + nb);
                     b0 = __ldg(sb + nb);
-                    if (!mbar_wait(&s.tempty[buf], bphase ^ 1, wc)) {
+                    if (!mbar_wait_warp(&s.tempty[buf], bphase ^ 1, wc)) {
                         ok = false;
                         break;
                     }
@@ -286,7 +286,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
 #pragma unroll
             for (int j = 0; j < S::PER / 2; ++j) acc[j] = 0;
             for (int b = 0; b < kbs; ++b) {
-                if (!mbar_wait(&s.tfull[buf], bphase, wc)) {
+                if (!mbar_wait_warp(&s.tfull[buf], bphase, wc)) {
                     ok = false;
                     break;
                 }
@@ -315,6 +315,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
             }
             if (SPLIT) {
                 // the stages are free once every CTA of the cluster is done with its products
+                __syncwarp();
                 cluster_sync_all();
                 // 16 bytes (four columns) of every thread, by source CTA and piece of the slice
                 constexpr int SLICE = S::PER / PARTS, PIECES = SLICE / 4, PLANE = S::EPI_WARPS * 32 * 16;
@@ -328,6 +329,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                                      "l"(acc[(r * SLICE + 4 * j) / 2]), "l"(acc[(r * SLICE + 4 * j) / 2 + 1])
                                      : "memory");
                 }
+                __syncwarp();
                 cluster_sync_all();
                 const TcTile t = tc_tile<BN>(p, tile);
                 const int m = t.m0 + 32 * q + lane, n = t.n0 + grp * S::PER + rank * SLICE;

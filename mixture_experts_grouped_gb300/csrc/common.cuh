@@ -233,6 +233,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
     }
 }
 
+// The same by a whole warp, all 32 lanes here: every lane waits (and so sees the
+// data itself), and the warp goes on only if every lane's wait succeeded. Each
+// lane gives up by its own reading of the barrier, the flag and the clock, and
+// what follows a wait is often warp-wide (TMEM loads, cluster barriers), which
+// lanes that decided differently must not reach apart.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
 // Flags in global memory that one CTA raises for another within a launch.
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {
     int v;

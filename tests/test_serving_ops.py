@@ -232,6 +232,31 @@ def test_gemm_wait_that_runs_out_is_reported(moe, dev, M, N, K):
     assert int(err.item()) == 0 and torch.equal(out.view(torch.int16), clean.view(torch.int16))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("limit_ns", [100, 600, 1500, 4000])
+@pytest.mark.parametrize("M,N,K", [(2000, 4104, 400), (260, 4104, 144), (778, 8456, 2064), (520, 1032, 4112),
+                                   (260, 1032, 2064), (260, 1032, 4112), (40, 520, 2064)])
+def test_gemm_ends_whatever_wait_runs_out(moe, dev, M, N, K, limit_ns):
+    """Every form, with limits that run out at its start, in its middle or not at all: the call ends, a result that
+    is not the clean one is reported, and the next call at the default limit is the clean one."""
+    a, sa, w, sb, add = (t.to(dev) for t in gemm_inputs(M, N, K, "bf16", True, 5))
+    out, err = torch.empty((M, N), dtype=torch.bfloat16, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    moe.moe_block_fp8_gemm(a, sa, w, sb, add, out, 0, M, N, K, err)
+    clean = out.clone()
+    prev = moe.moe_set_wait_limit_ns(limit_ns)
+    try:
+        moe.moe_block_fp8_gemm(a, sa, w, sb, add, out, 0, M, N, K, err)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(prev)
+    code = int(err.item())
+    assert code in (0, moe.MOE_DEV_ERR_TIMEOUT)
+    assert code or torch.equal(out.view(torch.int16), clean.view(torch.int16))
+    err.zero_()
+    moe.moe_block_fp8_gemm(a, sa, w, sb, add, out, 0, M, N, K, err)
+    assert int(err.item()) == 0 and torch.equal(out.view(torch.int16), clean.view(torch.int16))
+
+
 # ---- offsets past 32 bits --------------------------------------------------------------
 
 @pytest.mark.gpu
