@@ -514,7 +514,8 @@ size_t moe_few_tokens_workspace_size(int32_t T, int32_t top_k, int32_t I);
  *   workspace     device, >= moe_few_tokens_workspace_size bytes, 16-byte
  *                 aligned; contents need not be initialised
  * Requirements: those of moe_grouped_gate_up and moe_grouped_down on H, I, E
- * and the formats, and 2 I H < 2^30 weights per expert.
+ * and the formats, one format for both weights, 2 I H < 2^30 weights per
+ * expert, and (min(E, T top_k) + T top_k / 8) I < 2^31 rows that may be touched.
  */
 int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* topk_ids,
                    float* topk_weights, const MoeWeight* w_gate_up, const MoeWeight* w_down,

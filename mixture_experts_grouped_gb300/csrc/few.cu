@@ -67,6 +67,11 @@ extern "C" int moe_few_tokens(const void* x, int32_t act, const float* logits, i
     MOE_REQUIRE(I > 0 && I % 8 == 0, "%s: I=%d must be a positive multiple of 8", who, I);
     if (static_cast<int64_t>(2) * I * H >= (int64_t{1} << 30))
         return moe::fail(MOE_ERR_UNSUPPORTED, "%s: an expert of H=%d x I=%d is too large", who, H, I);
+    // the kernels count rows (entry of the plan, i) in 32 bits: touched experts, and one more entry per 8 of their pairs
+    const int64_t pairs = static_cast<int64_t>(T) * top_k;
+    if (((pairs < E ? pairs : E) + pairs / 8) * I >= (int64_t{1} << 31))
+        return moe::fail(MOE_ERR_UNSUPPORTED, "%s: T=%d x top_k=%d pairs may touch too many rows of I=%d", who, T, top_k,
+                         I);
     int rc = moe::check_weight(w_gate_up, act, 2 * I, H, "gate/up", who);
     if (rc == MOE_OK) rc = moe::check_weight(w_down, act, H, I, "down", who);
     if (rc != MOE_OK) return rc;

@@ -619,6 +619,22 @@ def test_what_is_beyond_the_limits_is_unsupported(moe, call):
     assert ei.value.status == moe.MOE_ERR_UNSUPPORTED and ei.value.message
 
 
+def test_rows_of_the_touched_experts_past_32_bits_are_unsupported(moe):
+    """The kernels count the rows of the experts that a batch may touch (one that more than 8 tokens share counts
+    again) in 32 bits."""
+    nv, bf = moe.MoeWeight(2, 0, 16, 16, None, 16), moe.MoeWeight(0, 0, 16, None, None, None)
+    wide = [dict(gu=nv, down=nv, T=32, k=16, E=256, H=32, I=2 ** 23), dict(gu=bf, down=bf, T=3, k=16, E=64, H=8, I=2 ** 26 - 8),
+            dict(gu=nv, down=nv, T=32, k=16, E=256, H=32, I=6710912)]
+    for kw in wide:
+        with pytest.raises(moe.MoeError) as ei:
+            few_args(moe, **kw, wsb=100)
+        assert ei.value.status == moe.MOE_ERR_UNSUPPORTED and "rows" in ei.value.message
+    # (256 + 64) x 6710880 is below 2^31: the next check is what refuses it
+    with pytest.raises(moe.MoeError) as ei:
+        few_args(moe, gu=nv, down=nv, T=32, k=16, E=256, H=32, I=6710880, wsb=100)
+    assert ei.value.status == moe.MOE_ERR_INVALID and "workspace" in ei.value.message
+
+
 def test_no_rows_is_a_no_op(moe):
     n0 = moe.moe_launch_count()
     moe.moe_add_rmsnorm_quant(None, None, 0, None, 1e-6, 0, 128, None, 16, None, None, 0)
