@@ -475,7 +475,8 @@ int moe_silu_mul_quant(const void* gate_up, int32_t act, int32_t T, int32_t I, v
  *     out[m, n] = act( sum_b a_scales[m, b] * w_scales[n / 128, b]
  *                      * sum_{k in block b} e4m3(a[m, k]) * e4m3(w[n, k])  (+ addend[m, n]) )
  * over the blocks b of 128 contraction indices, f32 accumulation; scales are
- * any f32 values.
+ * any f32 values (a block's two are applied so that only a term that itself
+ * leaves f32's range overflows or is rounded to a subnormal).
  *   a, a_scales   device uint8 [M, K] and f32 [M, ceil(K / 128)]
  *   w, w_scales   device uint8 [N, K] and f32 [ceil(N / 128), ceil(K / 128)]
  *   addend        device act [M, N] or NULL; may be out

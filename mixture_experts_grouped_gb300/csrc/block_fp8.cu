@@ -15,9 +15,14 @@
 //     in turn, and the warps' sums added through shared memory in warp order.
 //   * Tokens sit on the products' 8-wide side: NT tiles of 8 rows of a, read
 //     once per unit for all its 32 weight rows.
+//   * A sum takes its token's scale first, then its rows' (block_fp8.cuh says
+//     where their product would not do). Where a token's scale lies outside
+//     [2^-63, 2^65) and its sums are not zeros, which is only noted on the way,
+//     the warp takes its sums of the tile again with more care. (The note costs 0
+//     to 2%, 4% at M = 1, N = 28672; a vote and a branch in every unit took 7%.)
 // Measured: M = 1, N = 2816, K = 2048 3.1 us (0.85 of it for the bytes at HBM's
 // rate: a launch, one round trip to HBM and the sum of the warps make the rest);
-// M = 8, N = 28672, K = 4096 26.0 us, 4.5 TB/s: every 32 rows the warps meet.
+// M = 8, N = 28672, K = 4096 26.5 us, 4.4 TB/s: every 32 rows the warps meet.
 // More rows run on the 5th-generation tensor cores (block_fp8_tc.cu).
 #include "block_fp8.cuh"
 #include "stream.cuh"
@@ -53,6 +58,65 @@ __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint3
     asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t bits_of(float a, float b) { return __float_as_uint(a) | __float_as_uint(b); }
+// all ones where 2^-63 <= |s| < 2^65 (the exponent's two upper bits differ)
+__device__ __forceinline__ uint32_t ordinary_mask(float s) {
+    const uint32_t u = __float_as_uint(s);
+    return static_cast<uint32_t>(static_cast<int32_t>((u ^ u << 1) << 1) >> 31);
+}
+
+// Sums of one block of 128: 32 weight rows (two halves of 16) x 8 tokens
+__device__ __forceinline__ void block_sums(const uint4 (&w)[4][2], const uint4 (&x)[2], float (&part)[2][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        part[h][0] = part[h][1] = part[h][2] = part[h][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mma_e4m3_16832(part[h], w[2 * h][i].x, w[2 * h + 1][i].x, w[2 * h][i].y, w[2 * h + 1][i].y, x[i].x, x[i].y);
+            mma_e4m3_16832(part[h], w[2 * h][i].z, w[2 * h + 1][i].z, w[2 * h][i].w, w[2 * h + 1][i].w, x[i].z, x[i].w);
+        }
+    }
+}
+
+// One warp's sums of the tile of rows [first, n1), first + 32 at most, again and
+// straight from global memory: for the scales that the kernel's own order of
+// products does not suit (see there), with the care of scale_before.
+template <int NT>
+__device__ __noinline__ void careful_sums(const BfParams& p, int first, int n1, int warp, int lane,
+                                          float (&acc)[2][NT][4]) {
+    const int g = lane >> 2, c = lane & 3, ms = p.M;
+    auto piece = [&](const uint8_t* rows, int row, int end, int k) {
+        return row < end && k < p.K ? *reinterpret_cast<const uint4*>(rows + static_cast<size_t>(row) * p.K + k)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+    };
+    for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < NT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+    for (int b = warp; b < p.kb; b += kBfWarps) {
+        const int k = b * kQuantGroup + 16 * c;
+        uint4 w[4][2];
+        float s[4];
+        for (int r = 0; r < 4; ++r) {
+            const int row = first + 8 * r + g;
+            for (int i = 0; i < 2; ++i) w[r][i] = piece(p.w, row, n1, k + 64 * i);
+            s[r] = p.sb[static_cast<size_t>(min(row, n1 - 1) / kQuantGroup) * p.kb + b];
+        }
+        for (int t = 0; t < NT && 8 * t < ms; ++t) {
+            const uint4 x[2] = {piece(p.a, 8 * t + g, ms, k), piece(p.a, 8 * t + g, ms, k + 64)};
+            float part[2][4];
+            block_sums(w, x, part);
+            for (int q = 0; q < 2; ++q) {
+                const float sm = p.sa[static_cast<size_t>(min(8 * t + 2 * c + q, ms - 1)) * p.kb + b];
+                for (int h = 0; h < 2; ++h)
+                    for (int r = 0; r < 2; ++r) {
+                        float f = sm * s[2 * h + r];
+                        const float v = part[h][2 * r + q] * scale_before(f, sm, s[2 * h + r]);
+                        acc[h][t][2 * r + q] = fmaf(v, f, acc[h][t][2 * r + q]);
+                    }
+            }
+        }
+    }
 }
 
 template <int ACT, int NT>
@@ -139,6 +203,9 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
         }
         cp_async_commit();
     };
+    // no copy brings scales of tokens past the batch; their sums are never read, but must not look odd below
+    if (lane >= ms && lane < 8 * NT)
+        for (int d = 0; d < RING; ++d) *reinterpret_cast<float*>(ring + d * S::BYTES + S::SA_AT + 4 * lane) = 1.0f;
     for (int d = 0; d < RING - 1; ++d) copy_next(d);
     int stage = 0;
     for (int tile = 0; tile < ntiles; ++tile) {
@@ -148,6 +215,7 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
+        uint32_t odd = 0;  // not 0: a token's scale is out of the ordinary where its sums are not zeros
         // which of the two weight scales each of the lane's rows takes
         const int border = (first / kQuantGroup + 1) * kQuantGroup - first;  // rows before the second block
         for (int b = warp; b < p.kb; b += kBfWarps) {
@@ -171,25 +239,32 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                 for (int i = 0; i < 2; ++i)
                     x[i] = 8 * t + g < ms ? *reinterpret_cast<const uint4*>(st + S::X_AT + 1024 * t + 512 * i + 16 * lane)
                                           : make_uint4(0u, 0u, 0u, 0u);
-                // sums of tokens past the batch are never read, so their stale scales do no harm
                 const float2 sm = *reinterpret_cast<const float2*>(st + S::SA_AT + 32 * t + 8 * c);
+                float part[2][4];
+                block_sums(w, x, part);
+                // (sum * token's scale) * rows' scale: each product is exact enough, whatever the rows' scale,
+                // while the token's keeps the first one in the normal range
+                odd |= (bits_of(part[0][0], part[0][2]) | bits_of(part[1][0], part[1][2])) & ~ordinary_mask(sm.x);
+                odd |= (bits_of(part[0][1], part[0][3]) | bits_of(part[1][1], part[1][3])) & ~ordinary_mask(sm.y);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        mma_e4m3_16832(part, w[2 * h][i].x, w[2 * h + 1][i].x, w[2 * h][i].y, w[2 * h + 1][i].y, x[i].x,
-                                       x[i].y);
-                        mma_e4m3_16832(part, w[2 * h][i].z, w[2 * h + 1][i].z, w[2 * h][i].w, w[2 * h + 1][i].w, x[i].z,
-                                       x[i].w);
-                    }
                     const float s0 = 16 * h + g < border ? sb.x : sb.y, s1 = 16 * h + 8 + g < border ? sb.x : sb.y;
-                    acc[h][t][0] = fmaf(sm.x * s0, part[0], acc[h][t][0]);
-                    acc[h][t][1] = fmaf(sm.y * s0, part[1], acc[h][t][1]);
-                    acc[h][t][2] = fmaf(sm.x * s1, part[2], acc[h][t][2]);
-                    acc[h][t][3] = fmaf(sm.y * s1, part[3], acc[h][t][3]);
+                    acc[h][t][0] = fmaf(part[h][0] * sm.x, s0, acc[h][t][0]);
+                    acc[h][t][1] = fmaf(part[h][1] * sm.y, s0, acc[h][t][1]);
+                    acc[h][t][2] = fmaf(part[h][2] * sm.x, s1, acc[h][t][2]);
+                    acc[h][t][3] = fmaf(part[h][3] * sm.y, s1, acc[h][t][3]);
                 }
             }
+        }
+        if (__any_sync(0xffffffffu, odd != 0)) {
+            float again[2][NT][4];  // (acc itself stays in registers)
+            careful_sums<NT>(p, first, n1, warp, lane, again);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[h][t][q] = again[h][t][q];
         }
         // the tile's contraction is complete: add the warps' sums, HALVES x 16 rows at a time
         constexpr int HALVES = S::HALVES;

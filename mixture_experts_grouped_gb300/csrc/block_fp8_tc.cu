@@ -8,8 +8,10 @@
 // 32) into a fresh TMEM buffer, and the epilogue warps read every buffer
 // back, multiply by sa * sb and add to f32 sums in registers. Rows of a are
 // TMEM lanes, so sa is one value per thread and block, and a warp's columns
-// lie in one block of 128 weight rows, so sb is one value per warp. The
-// buffers are a ring: the MMAs of the next blocks run while one is read back.
+// lie in one block of 128 weight rows, so sb is one value per warp. Where a
+// lane's sa * sb lies outside [2^-63, 2^65), the warp multiplies twice
+// (scale_before). The buffers are a ring: the MMAs of the next blocks run while
+// one is read back.
 //   * 128 x BN tiles, BN = 256 when that fills the GPU. What limits it is the
 //     round trip of a buffer (MMAs, the signal, reading it back, the signal
 //     back) against the two buffers that 512 TMEM columns hold. So a buffer is
@@ -30,9 +32,9 @@
 //     between the first four and the others. (A second copying warp, and
 //     scales fetched two blocks ahead, measured 5 to 10% slower; a second
 //     staging area, in the place of the fourth stage, the same.)
-// Measured: M = 4096, N = 28672, K = 4096 410 us (2.35 PFLOP/s; tensor pipe 49%
+// Measured: M = 4096, N = 28672, K = 4096 391 us (2.46 PFLOP/s; tensor pipe 49%
 // busy: 480 ns a block of 128 x 256 x 128, of which its MMAs take half, and 2.3 us
-// a tile for the stores); M = 17, N = 4096, K = 14336 16.3 us (8.7 for the bytes:
+// a tile for the stores); M = 17, N = 4096, K = 14336 16.4 us (8.7 for the bytes:
 // 28 blocks of 310 ns and the meeting of four CTAs).
 #include "block_fp8.cuh"
 #include "tc_ring.cuh"
@@ -291,8 +293,12 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                     break;
                 }
                 tc_fence_after();
-                const float sc = scales[buf * S::SCALES + 32 * q + lane] *
-                                 scales[buf * S::SCALES + 128 + (BN == 256 ? grp / 2 : 0)];
+                const float sa = scales[buf * S::SCALES + 32 * q + lane];
+                const float sb = scales[buf * S::SCALES + 128 + (BN == 256 ? grp / 2 : 0)];
+                float sc = sa * sb;
+                // of the warp, since the branch on it lies between warp-wide TMEM loads
+                const bool odd = __any_sync(0xffffffffu, !scale_ordinary(sc));
+                const float before = odd ? scale_before(sc, sa, sb) : 1.0f;
                 uint64_t s2;
                 asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(sc));
 #pragma unroll
@@ -305,6 +311,9 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.tempty[buf]);
                     }
+                    if (odd)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * before);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], s2, r[2 * j], r[2 * j + 1]);
                 }

@@ -172,6 +172,43 @@ def test_gemm_matches_the_formula(moe, dev, act, addend, M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["huge", "tiny", "subnormal", "far apart", "zero"])
+@pytest.mark.parametrize("M,N,K", [(5, 520, 528), (13, 264, 400), (29, 264, 528), (40, 520, 2064), (260, 4104, 144),
+                                   (260, 1032, 2064), (778, 8456, 400)])
+def test_gemm_takes_any_scales(moe, dev, M, N, K, kind):
+    """Products of two scales that overflow f32, or lose bits below its normal range, while the outputs do not; rows of
+    ordinary scales beside them."""
+    g = gen(M + K)
+    kb, nb = -(-K // 128), -(-N // 128)
+    a = torch.randint(0x60, 0x7F, (M, K), generator=g, dtype=torch.uint8)      # 32 to 448, all positive
+    w = torch.randint(0x60, 0x7F, (N, K), generator=g, dtype=torch.uint8)
+    sa, sb = 1 + torch.rand((M, kb), generator=g), 1 + torch.rand((nb, kb), generator=g)
+    odd = torch.arange(M) % 3 != 1
+    if kind == "huge":                     # products from 1e39; the codes are 0 or the two smallest
+        a, w = (torch.randint(0, 3, t.shape, generator=g, dtype=torch.uint8) for t in (a, w))
+        a[odd, 128:256] = 0                # whole blocks of zeros
+        sa[odd] *= 1e29
+        sb *= 1e10
+    elif kind == "tiny":                   # products about 1e-44, seven times the smallest f32
+        sa[odd] *= 1e-34
+        sb *= 1e-10
+    elif kind == "subnormal":              # one scale below the normal range, the other about 1
+        sa[odd] *= 1e-43
+    elif kind == "far apart":              # the product is ordinary, a sum times the larger scale is not
+        sa[odd] *= 1e37
+        sb *= 1e-30
+    else:
+        sa[odd] = 0
+        sb[:, ::2] = 0
+    ref, mag = gemm_ref(a, sa, w, sb, None)
+    assert ref.abs().max() < 3e38
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    moe.moe_block_fp8_gemm(a.to(dev), sa.to(dev), w.to(dev), sb.to(dev), None, out, 0, M, N, K)
+    # terms and sums below the normal range are rounded to multiples of 2^-149 (a K-th of it for each term)
+    plain.close(out, ref, "bf16", mag * (K + K / 64 + 8) * plain.F32 + (K / 32 + 8) * 2.0 ** -149)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(5, 2048, 1024), (40, 512, 1024), (300, 2048, 1024)])
 def test_gemm_keeps_non_finite_rows_apart_and_repeats_bit_for_bit(moe, dev, M, N, K):
     a, sa, w, sb, add = gemm_inputs(M, N, K, "bf16", True, 7)
