@@ -51,11 +51,21 @@ def quant_buffers(rows: int, cols: int, device):
             torch.empty((rows, g), dtype=torch.float32, device=device))
 
 
+def _require_shape(what: str, t: torch.Tensor, *shape: int) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+
+
 @dataclass
 class BlockFp8Weight:
     """E4M3 codes uint8 [N, K] with f32 scales [ceil(N / 128), ceil(K / 128)]."""
     codes: torch.Tensor
     scales: torch.Tensor
+
+    def require(self, what: str, n: int, k: int) -> None:
+        g = M.MOE_QUANT_GROUP
+        _require_shape(f"{what} weight", self.codes, n, k)
+        _require_shape(f"scales of the {what} weight", self.scales, -(-n // g), -(-k // g))
 
 
 class SharedExpert:
@@ -63,6 +73,8 @@ class SharedExpert:
     SiLU-mul, down product, optionally added to another output."""
 
     def __init__(self, T, H, I, act, w_gate_up: BlockFp8Weight, w_down: BlockFp8Weight, device="cuda"):
+        w_gate_up.require("gate/up", 2 * I, H)
+        w_down.require("down", H, I)
         self.T, self.H, self.I = T, H, I
         self.act_code = M.ACT_CODES[act]
         self.w_gate_up, self.w_down = w_gate_up, w_down
@@ -89,7 +101,9 @@ class FeedForward:
 
     ``forward`` returns (out, r), what the next layer takes. The routed experts
     run as :class:`FewTokensLayer` up to 32 tokens and as
-    :class:`layer.MoeLayer` above; the router weight is f32 [H, E].
+    :class:`layer.MoeLayer` above; the router weight is f32 [H, E]. A shared
+    expert of another T, H or activation type is refused (ValueError). There is
+    no LoRA here: a layer with adapters runs :class:`layer.MoeLayer`'s steps.
     """
 
     def __init__(self, T, H, I, E, k, act, norm_weight, w_router, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight,
@@ -97,6 +111,11 @@ class FeedForward:
                  renormalize: bool = True):
         self.T, self.H, self.E, self.k, self.eps, self.renormalize = T, H, E, k, eps, renormalize
         self.act_code = M.ACT_CODES[act]
+        _require_shape("norm_weight", norm_weight, H)
+        _require_shape("w_router", w_router, H, E)
+        if shared is not None and (shared.T, shared.H, shared.act_code) != (T, H, self.act_code):
+            raise ValueError(f"the shared expert is one of T={shared.T}, H={shared.H}, activation type "
+                             f"{shared.act_code}, the block of T={T}, H={H}, {self.act_code}")
         self.norm_weight, self.w_router, self.shared = norm_weight, w_router, shared
         dt = L.act_dtype(act)
         self.residual = torch.empty((T, H), dtype=dt, device=device)

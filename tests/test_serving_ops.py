@@ -672,6 +672,38 @@ def test_rows_of_the_touched_experts_past_32_bits_are_unsupported(moe):
     assert ei.value.status == moe.MOE_ERR_INVALID and "workspace" in ei.value.message
 
 
+def shared_expert(T, H, I, act="bf16", **kw):
+    from mixture_experts_grouped_gb300 import ffn
+
+    def w8(n, k):
+        return ffn.BlockFp8Weight(torch.zeros((n, k), dtype=torch.uint8), torch.zeros((-(-n // 128), -(-k // 128))))
+    return ffn.SharedExpert(T, H, I, act, kw.get("gu", w8(2 * I, H)), kw.get("down", w8(H, I)), "cpu"), w8
+
+
+def test_blocks_of_unlike_shapes_are_refused(moe):
+    """A shared expert of another T, H or type would read or write past the block's buffers."""
+    from mixture_experts_grouped_gb300 import ffn
+    from mixture_experts_grouped_gb300 import layer as L
+    T, H, I, E, k = 4, 256, 128, 8, 2
+    w = L.DeviceWeight(moe.MoeWeight(0, 0, 16, None, None, None), [])
+
+    def block(shared, norm_weight=torch.zeros(H).bfloat16(), w_router=torch.zeros((H, E))):
+        return ffn.FeedForward(T, H, I, E, k, "bf16", norm_weight, w_router, w, w, shared, device="cpu")
+    good, w8 = shared_expert(T, H, 512)
+    assert block(good).shared is good and block(None).shared is None
+    for other in (shared_expert(T + 1, H, 512)[0], shared_expert(T, H + 128, 512)[0], shared_expert(T, H, 512, "f16")[0]):
+        with pytest.raises(ValueError, match="shared expert"):
+            block(other)
+    with pytest.raises(ValueError, match="norm_weight"):
+        block(good, norm_weight=torch.zeros(H - 8).bfloat16())
+    with pytest.raises(ValueError, match="w_router"):
+        block(good, w_router=torch.zeros((E, H)))
+    for kw in (dict(gu=w8(1016, H)), dict(gu=w8(1024, H - 16)), dict(down=w8(H, 1024)), dict(down=w8(H + 8, 512)),
+               dict(gu=ffn.BlockFp8Weight(w8(1024, H).codes, torch.zeros((8, 1))))):
+        with pytest.raises(ValueError, match="weight"):
+            shared_expert(T, H, 512, **kw)
+
+
 def test_no_rows_is_a_no_op(moe):
     n0 = moe.moe_launch_count()
     moe.moe_add_rmsnorm_quant(None, None, 0, None, 1e-6, 0, 128, None, 16, None, None, 0)
