@@ -35,6 +35,14 @@ class FewTokensLayer:
         self.ws = torch.empty(max(1, self.ws_bytes), dtype=torch.uint8, device=device)
         self.out = torch.empty((T, H), dtype=L.act_dtype(act), device=device)
 
+    @staticmethod
+    def takes(T, H, I, E, k, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight) -> bool:
+        """Whether the call takes a layer that the grouped path takes too: few tokens, weights
+        of one format, and sizes that its row numbers hold."""
+        pairs = T * k
+        return (T <= M.MOE_MAX_FEW_TOKENS and w_gate_up.desc.format == w_down.desc.format and 2 * I * H < 2 ** 30
+                and (min(E, pairs) + pairs // 8) * I < 2 ** 31)
+
     def forward(self, x, logits=None, stream=None):
         """The layer on x [T, H]; returns its output buffer. Without logits the
         routing already in ``topk_ids`` / ``topk_weights`` is used."""
@@ -100,10 +108,11 @@ class FeedForward:
         r = x + residual,  y = norm(r),  out = experts(y) + shared(e4m3(y))
 
     ``forward`` returns (out, r), what the next layer takes. The routed experts
-    run as :class:`FewTokensLayer` up to 32 tokens and as
-    :class:`layer.MoeLayer` above; the router weight is f32 [H, E]. A shared
-    expert of another T, H or activation type is refused (ValueError). There is
-    no LoRA here: a layer with adapters runs :class:`layer.MoeLayer`'s steps.
+    run as :class:`FewTokensLayer` where that takes them (up to 32 tokens,
+    weights of one format) and as :class:`layer.MoeLayer` elsewhere; the router
+    weight is f32 [H, E]. A shared expert of another T, H or activation type is
+    refused (ValueError). There is no LoRA here: a layer with adapters runs
+    :class:`layer.MoeLayer`'s steps.
     """
 
     def __init__(self, T, H, I, E, k, act, norm_weight, w_router, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight,
@@ -122,7 +131,7 @@ class FeedForward:
         self.y = torch.empty((T, H), dtype=dt, device=device)
         self.q, self.q_scales = quant_buffers(T, H, device) if shared is not None else (None, None)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
-        if T <= M.MOE_MAX_FEW_TOKENS:
+        if FewTokensLayer.takes(T, H, I, E, k, w_gate_up, w_down):
             self.experts = FewTokensLayer(T, H, I, E, k, act, w_gate_up, w_down, device, renormalize)
         else:
             self.experts = L.MoeLayer(T, H, I, E, k, bs, act, w_gate_up, w_down, device, renormalize=renormalize)

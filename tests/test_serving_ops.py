@@ -581,6 +581,38 @@ def test_feed_forward_block(moe, dev, T):
     plain.close(out, ref2, act, mag2 * (I + 16) * plain.F32)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 40])
+@pytest.mark.parametrize("fu,fd", [("fp8", "bf16"), ("bf16", "fp8")])
+def test_feed_forward_takes_two_formats_at_any_batch(moe, dev, fu, fd, T):
+    """The grouped path takes gate/up and down weights of different formats, the few-token call does not: such a layer
+    runs at every T."""
+    from mixture_experts_grouped_gb300 import ffn
+    H, I, E, k = 256, 128, 8, 2
+    g = gen(T)
+    gu, down = weight(fu, E, 2 * I, H, 2, g), weight(fd, E, H, I, 1, g)
+    nw, wr = torch.ones(H).bfloat16(), torch.randn((H, E), generator=g) * 0.1
+    block = ffn.FeedForward(T, H, I, E, k, "bf16", nw.to(dev), wr.to(dev), device_weight(moe, gu, fu, dev),
+                            device_weight(moe, down, fd, dev), device=dev)
+    x = torch.randn((T, H), generator=g).bfloat16()
+    out, r = block.forward(x.to(dev))
+    assert torch.equal(r.cpu(), x)
+    ids, wts = block.experts.topk_ids.cpu(), block.experts.topk_weights.cpu()
+    ref, slack, mag = torch.zeros((T, H)).double(), torch.zeros((T, H)).double(), torch.zeros((T, H)).double()
+    for e in range(E):
+        tok, slot = torch.nonzero(ids == e, as_tuple=True)
+        wg, wd = plain.dequant(gu, fu, e), plain.dequant(down, fd, e)
+        # the plain form of one format, on the dequantised (f64) weights
+        yy, ss = plain.few_tokens(block.y.cpu()[tok], torch.zeros((len(tok), 1)).int(), torch.ones((len(tok), 1)),
+                                  {"w": wg[None]}, {"w": wd[None]}, "bf16", "bf16", I, 1)
+        w = wts[tok, slot].double()[:, None]
+        ref.index_add_(0, tok, yy * w)
+        slack.index_add_(0, tok, ss * w)
+        mag.index_add_(0, tok, yy.abs() * w)
+    # the down products are rounded to bf16 too
+    plain.close(out, ref, "bf16", slack * (1 + 2.0 ** -8) + mag * 2.0 ** -8)
+
+
 # ---- refusals (no GPU) -------------------------------------------------------------------
 
 def few_args(m, **kw):
