@@ -19,10 +19,11 @@
 //     where their product would not do). Where a token's scale lies outside
 //     [2^-63, 2^65) and its sums are not zeros, which is only noted on the way,
 //     the warp takes its sums of the tile again with more care. (The note costs 0
-//     to 2%, 4% at M = 1, N = 28672; a vote and a branch in every unit took 7%.)
+//     to 5%, the most at M = 1 and 8, N = 28672; a vote and a branch in every unit
+//     took 7%. Rows of zeros, whose scale is 2^-126, cost nothing.)
 // Measured: M = 1, N = 2816, K = 2048 3.1 us (0.85 of it for the bytes at HBM's
 // rate: a launch, one round trip to HBM and the sum of the warps make the rest);
-// M = 8, N = 28672, K = 4096 26.5 us, 4.4 TB/s: every 32 rows the warps meet.
+// M = 8, N = 28672, K = 4096 27.1 us, 4.4 TB/s: every 32 rows the warps meet.
 // More rows run on the 5th-generation tensor cores (block_fp8_tc.cu).
 #include "block_fp8.cuh"
 #include "stream.cuh"
@@ -60,11 +61,10 @@ __device__ __forceinline__ void mma_e4m3_16832(float (&d)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t bits_of(float a, float b) { return __float_as_uint(a) | __float_as_uint(b); }
-// all ones where 2^-63 <= |s| < 2^65 (the exponent's two upper bits differ)
-__device__ __forceinline__ uint32_t ordinary_mask(float s) {
+// 0 where 2^-63 <= |s| < 2^65 (the exponent's two upper bits differ), else all ones
+__device__ __forceinline__ uint32_t odd_mask(float s) {
     const uint32_t u = __float_as_uint(s);
-    return static_cast<uint32_t>(static_cast<int32_t>((u ^ u << 1) << 1) >> 31);
+    return ~static_cast<uint32_t>(static_cast<int32_t>((u ^ u << 1) << 1) >> 31);
 }
 
 // Sums of one block of 128: 32 weight rows (two halves of 16) x 8 tokens
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[h][t][0] = acc[h][t][1] = acc[h][t][2] = acc[h][t][3] = 0.0f;
-        uint32_t odd = 0;  // not 0: a token's scale is out of the ordinary where its sums are not zeros
+        // of the lane's rows, not 0: a token's scale is out of the ordinary where its sum is not 0
+        uint32_t odd[4] = {0u, 0u, 0u, 0u};
         // which of the two weight scales each of the lane's rows takes
         const int border = (first / kQuantGroup + 1) * kQuantGroup - first;  // rows before the second block
         for (int b = warp; b < p.kb; b += kBfWarps) {
@@ -244,8 +245,12 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                 block_sums(w, x, part);
                 // (sum * token's scale) * rows' scale: each product is exact enough, whatever the rows' scale,
                 // while the token's keeps the first one in the normal range
-                odd |= (bits_of(part[0][0], part[0][2]) | bits_of(part[1][0], part[1][2])) & ~ordinary_mask(sm.x);
-                odd |= (bits_of(part[0][1], part[0][3]) | bits_of(part[1][1], part[1][3])) & ~ordinary_mask(sm.y);
+                const uint32_t mx = odd_mask(sm.x), my = odd_mask(sm.y);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    odd[r] |= __float_as_uint(part[r >> 1][2 * (r & 1)]) & mx;
+                    odd[r] |= __float_as_uint(part[r >> 1][2 * (r & 1) + 1]) & my;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float s0 = 16 * h + g < border ? sb.x : sb.y, s1 = 16 * h + 8 + g < border ? sb.x : sb.y;
@@ -256,7 +261,9 @@ __global__ void __launch_bounds__(kBfThreads, 1) block_fp8_rows_kernel(const BfP
                 }
             }
         }
-        if (__any_sync(0xffffffffu, odd != 0)) {
+        const int left = n1 - first - g;  // (rows past the share hold whatever their stage held)
+        if (__any_sync(0xffffffffu, (left > 0 && odd[0]) || (left > 8 && odd[1]) || (left > 16 && odd[2]) ||
+                                        (left > 24 && odd[3]))) {
             float again[2][NT][4];  // (acc itself stays in registers)
             careful_sums<NT>(p, first, n1, warp, lane, again);
 #pragma unroll

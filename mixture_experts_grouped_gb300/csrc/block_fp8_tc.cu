@@ -10,8 +10,9 @@
 // TMEM lanes, so sa is one value per thread and block, and a warp's columns
 // lie in one block of 128 weight rows, so sb is one value per warp. Where a
 // lane's sa * sb lies outside [2^-63, 2^65), the warp multiplies twice
-// (scale_before). The buffers are a ring: the MMAs of the next blocks run while
-// one is read back.
+// (scale_before; rows of zeros, whose scale is 2^-126, among others: M = 4096,
+// N = 28672, K = 4096 448 us with half the rows zeros, 381 with none). The
+// buffers are a ring: the MMAs of the next blocks run while one is read back.
 //   * 128 x BN tiles, BN = 256 when that fills the GPU. What limits it is the
 //     round trip of a buffer (MMAs, the signal, reading it back, the signal
 //     back) against the two buffers that 512 TMEM columns hold. So a buffer is
@@ -32,7 +33,7 @@
 //     between the first four and the others. (A second copying warp, and
 //     scales fetched two blocks ahead, measured 5 to 10% slower; a second
 //     staging area, in the place of the fourth stage, the same.)
-// Measured: M = 4096, N = 28672, K = 4096 391 us (2.46 PFLOP/s; tensor pipe 49%
+// Measured: M = 4096, N = 28672, K = 4096 381 us (2.52 PFLOP/s; tensor pipe 49%
 // busy: 480 ns a block of 128 x 256 x 128, of which its MMAs take half, and 2.3 us
 // a tile for the stores); M = 17, N = 4096, K = 14336 16.4 us (8.7 for the bytes:
 // 28 blocks of 310 ns and the meeting of four CTAs).
@@ -98,6 +99,14 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t s2, uint32_t a, uin
     asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%2, %3};\n\tfma.rn.f32x2 %0, %1, v, %0;\n\t}"
         : "+l"(acc)
         : "l"(s2), "r"(a), "r"(b));
+}
+
+// (a, b) *= (s, s)
+__device__ __forceinline__ void mul2(uint32_t& a, uint32_t& b, float s) {
+    asm("{\n\t.reg .b64 v, t;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 t, {%2, %2};\n\tmul.rn.f32x2 v, v, t;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "f"(s));
 }
 
 template <int N> __device__ __forceinline__ void regs_inc() {
@@ -313,7 +322,7 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                     }
                     if (odd)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * before);
+                        for (int j = 0; j < 16; ++j) mul2(r[2 * j], r[2 * j + 1], before);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], s2, r[2 * j], r[2 * j + 1]);
                 }
