@@ -231,6 +231,19 @@ def test_gemm_keeps_non_finite_rows_apart_and_repeats_bit_for_bit(moe, dev, M, N
     assert torch.equal(add.view(torch.int16), outs[0].view(torch.int16))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,addend", [("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("M,N,K", [(1, 9736, 1424), (8, 9736, 1424), (16, 8200, 1296), (24, 8200, 2000), (32, 8200, 2000)])
+def test_gemm_of_few_rows_takes_several_tiles(moe, dev, M, N, K, act, addend):
+    """Two 32-row tiles and a part of one to a CTA (152 SMs), every warp with blocks of each, a short last block."""
+    a, sa, w, sb, add = gemm_inputs(M, N, K, act, addend, M + N)
+    ref, mag = gemm_ref(a, sa, w, sb, add)
+    out = torch.full((M, N), float("nan"), dtype=plain.DT[act], device=dev)
+    moe.moe_block_fp8_gemm(a.to(dev), sa.to(dev), w.to(dev), sb.to(dev), add.to(dev) if addend else None, out,
+                           moe.ACT_CODES[act], M, N, K)
+    plain.close(out, ref, act, mag * (K + K / 64 + 8) * plain.F32)
+
+
 # on 152 SMs: tiles of 128, 64, 128 and 64 columns by one CTA each, 128 and 64 by two CTAs, 128 and 64 by four, and 256
 # columns, one and two tiles to a CTA
 FORMS = [(2000, 4104, 400), (520, 4104, 144), (260, 4104, 144), (130, 264, 400), (520, 1032, 4112), (260, 1032, 2064),
@@ -517,6 +530,35 @@ def test_few_tokens_routes_like_the_routing_call(moe, dev, T, E, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,act", [("gptq", "f16"), ("nvfp4", "bf16"), ("fp8", "f16")])
+def test_few_tokens_of_many_rows(moe, dev, fmt, act):
+    """Enough rows that a CTA's share is whole items: 64 experts of 1408 against 152 CTAs."""
+    T, H, I, E, k = 16, 256, 1408, 64, 6
+    layer, x, logits, gu, down = few_layer(moe, dev, fmt, act, T, H, I, E, k, 21)
+    out = layer.forward(x.to(dev), logits.to(dev))
+    ref, slack = plain.few_tokens(x, layer.topk_ids.cpu(), layer.topk_weights.cpu(), gu, down, fmt, act, I, E)
+    plain.close(out, ref, act, slack)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,act", [("bf16", "bf16"), ("fp8", "bf16"), ("nvfp4", "f16"), ("gptq", "f16")])
+def test_few_tokens_of_one_expert_among_many(moe, dev, fmt, act):
+    """All 32 tokens to one expert of 128 (few tokens an expert by the batch's size, so it is listed four times), and
+    the second choice to one of three others."""
+    T, H, I, E, k = 32, 128, 128, 128, 2
+    layer, x, _, gu, down = few_layer(moe, dev, fmt, act, T, H, I, E, k, 22)
+    g = gen(23)
+    ids = torch.stack((torch.full((T,), 77), torch.tensor([3, 76, 127])[torch.randint(0, 3, (T,), generator=g)]), 1).int()
+    w = torch.rand((T, k), generator=g)
+    layer.topk_ids.copy_(ids)
+    layer.topk_weights.copy_(w)
+    out = layer.forward(x.to(dev))
+    assert int(layer.err.item()) == 0
+    ref, slack = plain.few_tokens(x, ids, w, gu, down, fmt, act, I, E)
+    plain.close(out, ref, act, slack)
+
+
+@pytest.mark.gpu
 def test_few_tokens_on_a_stream_and_in_a_graph(moe, dev):
     layer, x, logits, gu, down = few_layer(moe, dev, "bf16", "bf16", 4, 512, 256, 16, 4, 2)
     xs, ls = x.to(dev), logits.to(dev)
@@ -583,8 +625,8 @@ def test_feed_forward_block(moe, dev, T):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [4, 40])
-@pytest.mark.parametrize("fu,fd", [("fp8", "bf16"), ("bf16", "fp8")])
-def test_feed_forward_takes_two_formats_at_any_batch(moe, dev, fu, fd, T):
+@pytest.mark.parametrize("fu,fd", [("fp8", "bf16"), ("bf16", "fp8"), ("fp8", "fp8"), ("nvfp4", "nvfp4"), ("gptq", "gptq")])
+def test_feed_forward_takes_every_format_at_any_batch(moe, dev, fu, fd, T):
     """The grouped path takes gate/up and down weights of different formats, the few-token call does not: such a layer
     runs at every T."""
     from mixture_experts_grouped_gb300 import ffn
