@@ -64,10 +64,11 @@ int make_tmap_5d(CUtensorMap* map, const void* base, int act, const uint64_t (&d
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while the previous kernel in the stream is still finishing (its launch and
-// CTA set-up overlap that kernel's tail). Every kernel of this library starts
-// with pdl_wait(), which blocks until the previous kernel has completed and
-// its writes are visible, so the order of the steps is unchanged. Inside a
-// captured CUDA graph the dependency becomes a programmatic edge.
+// CTA set-up overlap that kernel's tail). Every kernel of this library calls
+// pdl_wait(), which blocks until the previous kernel has completed and its
+// writes are visible, before it reads what that kernel writes, so the order of
+// the steps is unchanged. Inside a captured CUDA graph the dependency becomes
+// a programmatic edge.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args&&... args) {
@@ -103,12 +104,17 @@ __device__ __forceinline__ uint8_t* align1024_shared(uint8_t* base) {
 // Programmatic dependent launch, device side. pdl_wait: block until the
 // kernels this grid depends on have completed and their memory is visible
 // (a no-op for a grid launched without the attribute). Called first in every
-// kernel, by every thread, before any global memory is touched, so a kernel
-// also completes only after its predecessor did. pdl_launch_next: allow the
-// next kernel in the stream to be scheduled now rather than when this one's
-// CTAs have exited. Only the activation gather calls it (the GEMM after it
-// then sets up while the gather runs); triggering early in every kernel
-// measured slower on decode-sized layers (fine-grained T=8 72.7 -> 77 us).
+// kernel but one, by every thread, before any global memory is touched, so a
+// kernel also completes only after its predecessor did. The exception is the
+// few-token layer's down kernel: before its wait it reads the weights and the
+// routing (logits, or ids given as inputs), which it may because the gate/up
+// kernel before it lets it start only after its own wait, when everything
+// before the layer is complete. pdl_launch_next: allow the next kernel in the
+// stream to be scheduled now rather than when this one's CTAs have exited.
+// Called by that gate/up kernel (after its pdl_wait) and by the activation
+// gather (the GEMM after it then sets up while the gather runs); triggering
+// early in every kernel measured slower on decode-sized layers (fine-grained
+// T=8 72.7 -> 77 us).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -250,7 +250,7 @@ few_gate_up_kernel(const FewParams p) {
     float4* cut = reinterpret_cast<float4*>(few_smem + W * RING * S::BYTES);  // [W][2][MT][NT][32]: sums of cut items
     __shared__ FewPlan s;
     pdl_wait();
-    pdl_launch_next();
+    pdl_launch_next();  // not before the wait: the down kernel reads the routing before its own
     build_plan<W + 1, 8 * NT>(s, p, p.logits != nullptr, blockIdx.x == 0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     if (warp == W) {  // beside the products: the routing outputs, one row per CTA
