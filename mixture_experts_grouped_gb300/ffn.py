@@ -102,6 +102,30 @@ class SharedExpert:
         return self.out
 
 
+_WEIGHT_BITS = {M.MOE_W_BF16: 16.0, M.MOE_W_GPTQ_INT4: 4.15, M.MOE_W_NVFP4: 4.5, M.MOE_W_FP8_E4M3: 8.0}
+
+
+def few_tokens_pay(fmt: int, T: int, H: int, I: int, E: int, k: int) -> bool:
+    """Whether the few-token call beats the grouped path on a layer that it takes.
+
+    It saves the grouped path's five launches and its sort, about 20 us; the grouped GEMMs
+    read weights of experts with several tokens faster. So the grouped path pays where the
+    touched weights are many and an expert has many tokens (us, few-token call / grouped):
+    bf16, 8 experts of 4096 x 14336, k = 2: 127 / 134 at T = 1, 214 / 207 at 2, 479 / 435 at
+    16, 754 / 438 at 32; 16 of 4096 x 2048, k = 4: 148 / 146 at T = 12, 165 / 147 at 24; 32
+    of 2048 x 768, k = 8: 70 / 82 at 24, 89 / 83 at 32. FP8, the first layer: 276 / 298 at 16,
+    301 / 299 at 24, 332 / 299 at 32; the second 113 / 116 at 32. GPTQ, the first: 230 / 235
+    at 16, 255 / 236 at 24, 335 / 236 at 32; the second 86 / 93 at 16, 97 / 94 at 24, 119 / 94
+    at 32; the third 57 / 62 at 32. NVFP4, the first 327 / 339 at 32."""
+    per_expert = T * k / E
+    touched = E * (1.0 - (1.0 - k / E) ** T) * 3 * H * I * _WEIGHT_BITS[fmt] / 8  # bytes, expected
+    if fmt == M.MOE_W_BF16:
+        return touched < 1.1e9 and per_expert * touched < 2.3e9
+    if fmt == M.MOE_W_GPTQ_INT4:
+        return per_expert < 6 or per_expert * touched < 1.0e9
+    return per_expert * touched < 6.8e9
+
+
 class FeedForward:
     """The feed-forward half of a decoder layer at one shape:
 
@@ -109,8 +133,8 @@ class FeedForward:
 
     ``forward`` returns (out, r), what the next layer takes. The routed experts
     run as :class:`FewTokensLayer` where that takes them (up to 32 tokens,
-    weights of one format) and as :class:`layer.MoeLayer` elsewhere; the router
-    weight is f32 [H, E]. A shared expert of another T, H or activation type is
+    weights of one format) and is faster (:func:`few_tokens_pay`), and as
+    :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. A shared expert of another T, H or activation type is
     refused (ValueError). There is no LoRA here: a layer with adapters runs
     :class:`layer.MoeLayer`'s steps.
     """
@@ -131,7 +155,8 @@ class FeedForward:
         self.y = torch.empty((T, H), dtype=dt, device=device)
         self.q, self.q_scales = quant_buffers(T, H, device) if shared is not None else (None, None)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
-        if FewTokensLayer.takes(T, H, I, E, k, w_gate_up, w_down):
+        if (FewTokensLayer.takes(T, H, I, E, k, w_gate_up, w_down)
+                and few_tokens_pay(w_gate_up.desc.format, T, H, I, E, k)):
             self.experts = FewTokensLayer(T, H, I, E, k, act, w_gate_up, w_down, device, renormalize)
         else:
             self.experts = L.MoeLayer(T, H, I, E, k, bs, act, w_gate_up, w_down, device, renormalize=renormalize)
