@@ -11,7 +11,7 @@
 // lie in one block of 128 weight rows, so sb is one value per warp. Where a
 // lane's sa * sb lies outside [2^-63, 2^65), the warp multiplies twice
 // (scale_before; rows of zeros, whose scale is 2^-126, among others: M = 4096,
-// N = 28672, K = 4096 448 us with half the rows zeros, 381 with none). The
+// N = 28672, K = 4096 434 us with half the rows zeros, 373 with none). The
 // buffers are a ring: the MMAs of the next blocks run while one is read back.
 //   * 128 x BN tiles, BN = 256 when that fills the GPU. What limits it is the
 //     round trip of a buffer (MMAs, the signal, reading it back, the signal
@@ -33,9 +33,9 @@
 //     between the first four and the others. (A second copying warp, and
 //     scales fetched two blocks ahead, measured 5 to 10% slower; a second
 //     staging area, in the place of the fourth stage, the same.)
-// Measured: M = 4096, N = 28672, K = 4096 381 us (2.52 PFLOP/s; tensor pipe 49%
-// busy: 480 ns a block of 128 x 256 x 128, of which its MMAs take half, and 2.3 us
-// a tile for the stores); M = 17, N = 4096, K = 14336 16.4 us (8.7 for the bytes:
+// Measured: M = 4096, N = 28672, K = 4096 373 us (2.58 PFLOP/s; tensor pipe 49%
+// busy: 465 ns a block of 128 x 256 x 128, of which its MMAs take half, and 1.5 us
+// a tile for the stores); M = 17, N = 4096, K = 14336 16.3 us (8.7 for the bytes:
 // 28 blocks of 310 ns and the meeting of four CTAs).
 #include "block_fp8.cuh"
 #include "tc_ring.cuh"
@@ -47,7 +47,7 @@ constexpr int kTcA = 128 * 128;  // bytes of a stage's activation rows per CTA
 
 template <int BN, int PARTS> struct TcShape {
     static constexpr int STAGE = kTcA + BN * 128;
-    static constexpr int STAGES = tc_stages(BN, PARTS), NBUF = tc_buffers(BN);
+    static constexpr int STAGES = tc_stages(BN), NBUF = tc_buffers(BN);
     static_assert(STAGES % kTcIssuers == 0 && NBUF % kTcIssuers == 0, "every stage and buffer is one issuing thread's");
     static constexpr int COLS = NBUF * BN;             // TMEM columns
     static constexpr int GROUPS = BN == 64 ? 2 : 4;    // warpgroups that read a buffer back
@@ -58,7 +58,7 @@ template <int BN, int PARTS> struct TcShape {
     static constexpr int SCALE_AT = OUT_AT + EPI_WARPS * OUT_BYTES; // [NBUF]: 128 row scales, 2 column block scales
     static constexpr int SCALES = 136;                              // floats of a buffer's scales
     static constexpr int TAIL_AT = SCALE_AT + NBUF * SCALES * 4;
-    static constexpr int SMEM = 1024 + TAIL_AT + 256;
+    static constexpr int SMEM = TAIL_AT + 256;  // (nothing to align by hand: the array is declared aligned)
     static_assert(SMEM <= 232448, "shared memory over the limit");
 };
 
@@ -136,8 +136,12 @@ block_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_const
                     const __grid_constant__ CUtensorMap tm_o, const BfParams p, int a_rows, int32_t* err, uint64_t wait_ns) {
     using S = TcShape<BN, PARTS>;
     pdl_wait();
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align1024_shared(smem_raw);
+    // The array is aligned, so the offset is 0. It is computed all the same: with a base
+    // that the compiler knows, the narrow tiles measured 2 to 5% slower.
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint32_t base;
+    asm("mov.u32 %0, %1;" : "=r"(base) : "r"(smem_u32(smem_raw)));
+    uint8_t* smem = smem_raw + ((1024u - (base & 1023u)) & 1023u);
     TcTail& s = *reinterpret_cast<TcTail*>(smem + S::TAIL_AT);
     const WaitCtx wc{&s.abort_flag, err, wait_ns};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

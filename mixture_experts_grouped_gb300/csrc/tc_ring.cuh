@@ -18,9 +18,9 @@ namespace moe {
 
 constexpr int kTcIssuers = 2;
 
-// by tile width and CTAs per tile: the most that shared memory holds (a tile that
-// is not split has a staging area for its rows besides)
-constexpr int tc_stages(int bn, int parts) { return bn == 256 || (bn == 128 && parts == 1) ? 4 : 6; }
+// By tile width: the most that shared memory holds. (128 columns by one CTA a tile:
+// 390 ns a block with four stages, 310 with six.)
+constexpr int tc_stages(int bn) { return bn == 256 ? 4 : 6; }
 constexpr int tc_buffers(int bn) { return 512 / bn < 4 ? 512 / bn : 4; }
 
 }  // namespace moe
