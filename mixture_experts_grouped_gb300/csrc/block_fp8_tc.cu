@@ -478,20 +478,21 @@ int launch_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const c
 
 // Tile width and split of the contraction, by the time that each choice would
 // take: the waves of CTAs, times the blocks of 128 of each at what a block
-// costs at that width (measured on a GB300: 260, 310 and 480 ns at 64, 128 and
-// 256 columns) and what a tile's end holds up the next (0.1, 0.5 and 2.3 us),
-// and what a launch costs (2.5 us; 4.5 and 5.5 with the meeting of 2 or 4
-// CTAs). A wide tile reads less and spends fewer steps per sum, a narrow or
-// split one fills more of the GPU: M = 128, N = 4096, K = 14336 takes 16.6 us
-// at 128 x 4 CTAs, 19.5 at 64 x 2, 31 at 64 and 57 at 256; M = 2048, N = 2816,
-// K = 2048 22.3 at 256, 19.0 at 128, 22.8 at 64. A tile is split only where
-// every CTA runs at once: each wave of clusters begins and ends anew, and those
-// 352 tiles took 36 us at 128 x 2.
+// costs at that width (260, 315 and 465 ns at 64, 128 and 256 columns) and what
+// a tile's end holds up the next (0.3, 0.7 and 1.5 us), and what a launch costs
+// (2.5 us; 4.5 and 5.5 with the meeting of 2 or 4 CTAs). The costs are fitted to
+// 96 sizes measured on a GB300 at every form: the choice is 0.4% slower than the
+// best form in the mean. A wide tile reads less and spends fewer steps per sum,
+// a narrow or split one fills more of the GPU: M = 128, N = 4096, K = 14336 takes
+// 16.6 us at 128 x 4 CTAs, 19.4 at 64 x 2, 31 at 64 and 56 at 256; M = 2048,
+// N = 2816, K = 2048 20.4 at 256, 19.9 at 128, 24.1 at 64. A tile is split only
+// where every CTA runs at once: each wave of clusters begins and ends anew, and
+// those 352 tiles took 36 us at 128 x 2.
 template <int ACT> int pick_tc(const BfParams& p, int sms, int32_t* err, cudaStream_t st, const char* who) {
     static const struct {
         int bn, parts, block_ns, tile_ns, fixed_ns;
-    } forms[] = {{256, 1, 480, 2300, 2500}, {128, 1, 310, 500, 2500}, {64, 1, 260, 100, 2500}, {128, 2, 310, 0, 4500},
-                 {64, 2, 260, 0, 4500},     {128, 4, 310, 0, 5500},   {64, 4, 260, 0, 5500}};
+    } forms[] = {{256, 1, 465, 1500, 2500}, {128, 1, 315, 700, 2500}, {64, 1, 260, 300, 2500}, {128, 2, 315, 0, 4500},
+                 {64, 2, 260, 0, 4500},     {128, 4, 315, 0, 5500},   {64, 4, 260, 0, 5500}};
     int best = 0;
     int64_t best_ns = INT64_MAX;
     for (int i = 0; i < 7; ++i) {

@@ -174,7 +174,7 @@ def test_gemm_matches_the_formula(moe, dev, act, addend, M, N, K):
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["huge", "tiny", "subnormal", "far apart", "zero"])
 @pytest.mark.parametrize("M,N,K", [(5, 520, 528), (13, 264, 400), (29, 264, 528), (40, 520, 2064), (260, 4104, 144),
-                                   (260, 1032, 2064), (778, 8456, 400)])
+                                   (260, 1032, 2064), (778, 8456, 400), (446, 9752, 400), (513, 7696, 624)])
 def test_gemm_takes_any_scales(moe, dev, M, N, K, kind):
     """Products of two scales that overflow f32, or lose bits below its normal range, while the outputs do not; rows of
     ordinary scales beside them."""
@@ -262,6 +262,22 @@ def test_gemm_forms_for_many_rows(moe, dev, M, N, K, addend):
     plain.close(out, ref, "bf16", mag * (K + K / 64 + 8) * plain.F32)
 
 
+# on 152 SMs: several tiles of 128 columns to a CTA (twice), of 64 columns (twice)
+SEVERAL = [(446, 9752, 400), (257, 12808, 224), (513, 7696, 624), (2487, 928, 224)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("addend", [False, True])
+@pytest.mark.parametrize("M,N,K", SEVERAL)
+def test_gemm_of_several_narrow_tiles(moe, dev, M, N, K, addend):
+    a, sa, w, sb, add = gemm_inputs(M, N, K, "f16", addend, M + N)
+    ref, mag = gemm_ref(a, sa, w, sb, add)
+    out = torch.full((M, N), float("nan"), dtype=torch.float16, device=dev)
+    moe.moe_block_fp8_gemm(a.to(dev), sa.to(dev), w.to(dev), sb.to(dev), add.to(dev) if addend else None, out, 1, M, N,
+                           K)
+    plain.close(out, ref, "f16", mag * (K + K / 64 + 8) * plain.F32)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(40, 512, 8192), (2000, 4096, 1024), (300, 7168, 2048)])
 def test_gemm_wait_that_runs_out_is_reported(moe, dev, M, N, K):
@@ -285,7 +301,8 @@ def test_gemm_wait_that_runs_out_is_reported(moe, dev, M, N, K):
 @pytest.mark.gpu
 @pytest.mark.parametrize("limit_ns", [100, 600, 1500, 4000])
 @pytest.mark.parametrize("M,N,K", [(2000, 4104, 400), (260, 4104, 144), (778, 8456, 2064), (520, 1032, 4112),
-                                   (260, 1032, 2064), (260, 1032, 4112), (40, 520, 2064)])
+                                   (260, 1032, 2064), (260, 1032, 4112), (40, 520, 2064), (446, 9752, 400),
+                                   (513, 7696, 624)])
 def test_gemm_ends_whatever_wait_runs_out(moe, dev, M, N, K, limit_ns):
     """Every form, with limits that run out at its start, in its middle or not at all: the call ends, a result that
     is not the clean one is reported, and the next call at the default limit is the clean one."""
