@@ -33,12 +33,18 @@ namespace {
 
 constexpr int kBfThreads = 256, kBfWarps = kBfThreads / 32;
 
-// Which form: up to 8 rows this one; up to 32 (the most it takes) while the
-// weights are small, since its reads of the tokens grow with the rows. Measured
-// here / on tcgen05: 4.9 / 5.9 us at M = 17, N = 2816, K = 2048; 17.3 / 16.3 at
-// M = 16, N = 4096, K = 14336; 34.9 / 28.2 at M = 16, N = 28672, K = 4096.
+// Which form: up to 8 rows this one; up to 16, and up to 32 (the most it takes),
+// while the weights are small, and for more than 16 rows the contraction short
+// too, since its reads of the tokens grow with both. Measured here / on tcgen05,
+// us: 6.8 / 7.9 at M = 16, N = K = 4096, 12.7 / 10.4 at M = 16, N = 8192, K = 4096;
+// 5.2 / 5.8 at M = 17, N = 2816, K = 2048, 8.0 / 5.9 at M = 17, N = 8192, K = 1408;
+// 5.5 / 5.9 at M = 24, N = 4096, K = 2048, 7.8 / 6.3 at N = 2048, K = 4096; 5.2 / 5.8
+// at M = 32, N = 2816, K = 1408, 6.3 / 5.9 at N = 4096, K = 2048. (M = 8, N = 28672,
+// K = 4096 would take 25.6 there, 27.1 here, and M = 4 25.6 and 23.9.)
 inline bool rows_form(int M, int N, int K) {
-    return M <= 8 || (M <= 32 && static_cast<int64_t>(N) * K <= (1 << 24));
+    const int64_t weights = static_cast<int64_t>(N) * K;
+    if (M <= 16) return M <= 8 || weights <= (1 << 24);
+    return M <= 32 && weights <= (1 << 23) && static_cast<int64_t>(M) * K <= 49152;
 }
 
 // A stage: 4 KB of weights (32 rows x 128), NT tiles of 8 tokens, the tokens'

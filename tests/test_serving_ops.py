@@ -233,7 +233,8 @@ def test_gemm_keeps_non_finite_rows_apart_and_repeats_bit_for_bit(moe, dev, M, N
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("act,addend", [("bf16", True), ("f16", False)])
-@pytest.mark.parametrize("M,N,K", [(1, 9736, 1424), (8, 9736, 1424), (16, 8200, 1296), (24, 8200, 2000), (32, 8200, 2000)])
+@pytest.mark.parametrize("M,N,K", [(1, 9736, 1424), (8, 9736, 1424), (16, 8200, 1296), (24, 8200, 2000), (32, 8200, 2000),
+                                   (24, 5800, 1296), (32, 5800, 1424)])
 def test_gemm_of_few_rows_takes_several_tiles(moe, dev, M, N, K, act, addend):
     """Two 32-row tiles and a part of one to a CTA (152 SMs), every warp with blocks of each, a short last block."""
     a, sa, w, sb, add = gemm_inputs(M, N, K, act, addend, M + N)
