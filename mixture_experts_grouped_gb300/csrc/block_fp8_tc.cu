@@ -33,10 +33,11 @@
 //     between the first four and the others. (A second copying warp, and
 //     scales fetched two blocks ahead, measured 5 to 10% slower; a second
 //     staging area, in the place of the fourth stage, the same.)
-// Measured: M = 4096, N = 28672, K = 4096 373 us (2.58 PFLOP/s; tensor pipe 49%
-// busy: 465 ns a block of 128 x 256 x 128, of which its MMAs take half, and 1.5 us
-// a tile for the stores); M = 17, N = 4096, K = 14336 16.3 us (8.7 for the bytes:
-// 28 blocks of 310 ns and the meeting of four CTAs).
+// Measured: M = 4096, N = 28672, K = 4096 373 us (2.58 PFLOP/s; 415 in long runs,
+// at lower clocks; tensor pipe 55% busy: 465 ns a block of 128 x 256 x 128, of which
+// its MMAs take half, and 1.5 us a tile for the stores); M = 17, N = 4096,
+// K = 14336 16.3 us (8.7 for the bytes: 28 blocks at 5.5 TB/s and the meeting of
+// four CTAs).
 #include "block_fp8.cuh"
 #include "tc_ring.cuh"
 
