@@ -118,7 +118,7 @@ def few_tokens_pay(fmt: int, T: int, H: int, I: int, E: int, k: int) -> bool:
     at 16, 255 / 236 at 24, 335 / 236 at 32; the second 86 / 93 at 16, 97 / 94 at 24, 119 / 94
     at 32; the third 57 / 62 at 32. NVFP4, the first 327 / 339 at 32."""
     per_expert = T * k / E
-    touched = E * (1.0 - (1.0 - k / E) ** T) * 3 * H * I * _WEIGHT_BITS[fmt] / 8  # bytes, expected
+    touched = E * (1.0 - (1.0 - k / E) ** T) * 3 * H * I * _WEIGHT_BITS.get(fmt, 16.0) / 8  # bytes, expected
     if fmt == M.MOE_W_BF16:
         return touched < 1.1e9 and per_expert * touched < 2.3e9
     if fmt == M.MOE_W_GPTQ_INT4:
@@ -134,9 +134,9 @@ class FeedForward:
     ``forward`` returns (out, r), what the next layer takes. The routed experts
     run as :class:`FewTokensLayer` where that takes them (up to 32 tokens,
     weights of one format) and is faster (:func:`few_tokens_pay`), and as
-    :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. A shared expert of another T, H or activation type is
-    refused (ValueError). There is no LoRA here: a layer with adapters runs
-    :class:`layer.MoeLayer`'s steps.
+    :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. A shared
+    expert of another T, H or activation type is refused (ValueError). There is
+    no LoRA here: a layer with adapters runs :class:`layer.MoeLayer`'s steps.
     """
 
     def __init__(self, T, H, I, E, k, act, norm_weight, w_router, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight,
