@@ -11,8 +11,8 @@ Six operators, named by the case's "op":
   glu      SwiGLU of stacked [rows, 2 I] gate/up products
                "out":   h = g s(g) u,  s(g) = 1 / (1 + exp(-g))
                "grad":  d_g = d_h u s(g) (1 + g (1 - s(g))),  d_u = d_h g s(g),  and h again
-  routing  rows to the experts and the gradients of what brings them back: xs[r] = x[token of r],
-           d_y[r] = w_tj d_out[t],  d_w_tj = d_out[t] . y[r],  and from d_w the gradient of the logits
+  routing  rows to the experts and the gradients of what brings them back: xs[row of (t, j)] = x[t],
+           d_y[row] = w_tj d_out[t],  d_w_tj = d_out[t] . y[row],  and from d_w the gradient of the logits
 """
 
 import math
@@ -206,11 +206,8 @@ def prepare(case, seed):
         s["weights"] = (torch.softmax(top, 1) if case["renorm"]
                         else torch.softmax(s["logits"], 1).gather(1, ids)).contiguous()
         order = torch.sort(ids.flatten(), stable=True).indices  # pairs in the experts' order
-        s["pairs"] = order.int()
-        s["row"] = torch.empty_like(s["pairs"])
+        s["row"] = torch.empty(t * k, dtype=torch.int32, device=DEV)
         s["row"][order] = torch.arange(t * k, device=DEV, dtype=torch.int32)
-        s["offsets"] = torch.zeros(e + 1, dtype=torch.int32, device=DEV)
-        s["offsets"][1:] = torch.bincount(ids.flatten(), minlength=e).cumsum(0)
         s["xs"], s["dy"] = empty(t * k, h), empty(t * k, h)
         s["dw"], s["dl"] = empty(t, k, dtype=torch.float32), empty(t, e, dtype=torch.float32)
     return s
@@ -251,7 +248,7 @@ def _run_own(s):
         M.moe_swiglu_backward(s["gu"], s["dh"], act, s["rows"], s["I"], s["dgu"], s["h"])
         return {"gate_up": s["dgu"], "h": s["h"]}
     t, h, k = s["T"], s["H"], s["k"]
-    M.moe_gather_rows(s["x"], act, s["pairs"], s["offsets"], t, k, h, s["E"], t * k, s["xs"], s["err"])
+    M.moe_dispatch(s["x"], act, s["row"], s["xs"], t, h, k, t * k, s["err"])
     M.moe_combine_backward(s["d_out"], s["y"], act, s["row"], s["weights"], s["dy"], s["dw"], t, h, k, t * k, s["err"])
     M.moe_route_backward(s["logits"], s["ids"], s["weights"], s["dw"], s["dl"], t, s["E"], k, s["renorm"], s["err"])
     return {"xs": s["xs"], "dy": s["dy"], "dw": s["dw"], "dl": s["dl"]}
@@ -327,7 +324,8 @@ def _run_plain(s):
         return {"gate_up": torch.cat((dh * u * sg * (1.0 + g * (1.0 - sg)), dh * g * sg), -1).to(act), "h": h}
     t, k = s["T"], s["k"]
     w, ids, row = s["weights"], s["ids"].long(), s["row"].long()
-    token = s["pairs"].long() // k
+    xs = torch.empty_like(s["xs"])
+    xs[row] = s["x"].repeat_interleave(k, 0)
     d_out = s["d_out"].float()
     dw = (d_out[:, None] * s["y"][row].float().unflatten(0, (t, k))).sum(-1)
     dy = torch.empty_like(s["y"])
@@ -339,7 +337,7 @@ def _run_plain(s):
         p = torch.exp(s["logits"] - s["logits"].amax(1, keepdim=True))
         p = p / p.sum(1, keepdim=True)
         dl = p * (torch.zeros_like(p).scatter(1, ids, dw) - mean)
-    return {"xs": s["x"][token], "dy": dy, "dw": dw, "dl": dl}
+    return {"xs": xs, "dy": dy, "dw": dw, "dl": dl}
 
 
 def run(state):
