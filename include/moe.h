@@ -23,6 +23,18 @@
  *   moe_silu_mul_quant       SiLU-mul of a gate/up product, with E4M3 output
  *   moe_few_tokens           the whole layer for at most 32 tokens, two kernels
  *
+ * and, for training the layer, and for dense blocks in 16 bits:
+ *
+ *   moe_ragged_gemm          products grouped by expert over spans of any size, and
+ *                            the gradient of their input
+ *   moe_ragged_wgrad         the gradient of their weight
+ *   moe_dense_gemm           dense product with bias, activation and residual
+ *   moe_bias_act_backward    gradient of its bias and activation
+ *   moe_swiglu               SwiGLU of a gate/up product, moe_swiglu_backward its gradient
+ *   moe_dispatch             token rows to their experts' rows
+ *   moe_combine_backward     gradient of the combine
+ *   moe_route_backward       gradient of the routing
+ *
  * Sources the semantics are restated from (cited per call below):
  *   [lora]    spark_model/layers/ops/moe_lora_grouped.rs (Atlas inference docs)
  *   [ferrum]  ferrum-kernels 0.7.7, src/backend/cuda/moe.rs
@@ -96,6 +108,13 @@ extern "C" {
 /* ---- element types ----------------------------------------------------------- */
 #define MOE_ACT_BF16 0
 #define MOE_ACT_F16 1
+
+/* activation functions of moe_dense_gemm */
+#define MOE_FN_NONE 0      /* z */
+#define MOE_FN_RELU 1      /* max(z, 0) */
+#define MOE_FN_GELU 2      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define MOE_FN_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define MOE_FN_SILU 4      /* z / (1 + exp(-z)) */
 
 #define MOE_W_BF16 0      /* dense weight in the activation type */
 #define MOE_W_GPTQ_INT4 1 /* raw GPTQ 4-bit: qweight / scales / qzeros ([triton]) */
@@ -523,6 +542,146 @@ int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* top
                    int32_t T, int32_t top_k, int32_t H, int32_t I, int32_t E, int32_t renormalize,
                    void* out, int32_t* err_word, void* workspace, size_t workspace_bytes,
                    void* stream);
+
+/* ---- training the layer; dense products in 16 bits ------------------------------- */
+
+/*
+ * The sorted rows of a training step are ragged: group e is the rows
+ * [offsets[e], offsets[e + 1]), of any number, with no padding (align with
+ * block_size 1), offsets[0] >= 0 and offsets[E] <= rows. Rows outside every
+ * group are neither read nor written. Offsets that decrease or leave [0, rows]
+ * set MOE_DEV_ERR_OFFSETS and nothing is computed. With offsets NULL, E must be
+ * 1 and the group is all rows (a dense product). Sums are f32, in an order that
+ * depends on the sizes alone; each output is rounded once.
+ */
+
+/*
+ * Product grouped by expert, rows r of group e:
+ *     transposed == 0:  out[r, n] = act( sum_k a[r, k] * w_e[n, k] )
+ *     transposed != 0:  out[r, k] = act( sum_n a[r, n] * w_e[n, k] )
+ * (the second is the gradient of the first one's input: a is the gradient of
+ * its output).
+ *   a             device act [rows, K], or [rows, N] if transposed
+ *   w             device act [E, N, K]
+ *   offsets       device i32 [E + 1] or NULL
+ *   out           device act [rows, N], or [rows, K] if transposed (not a, not w)
+ *   err_word      device i32 or NULL (MOE_DEV_ERR_OFFSETS, MOE_DEV_ERR_TIMEOUT)
+ * Requirements: N % 8 == 0, K % 8 == 0, 1 <= E <= MOE_MAX_EXPERTS, tensors
+ * 16-byte aligned.
+ */
+int moe_ragged_gemm(const void* a, int32_t act, const void* w, int32_t transposed,
+                    const int32_t* offsets, int32_t rows, int32_t N, int32_t K, int32_t E, void* out,
+                    int32_t* err_word, void* stream);
+
+/*
+ * Gradient of the weight:
+ *     dw_e[n, k] = sum_{r in group e} dy[r, n] * x[r, k]  (+ addend_e[n, k])
+ * An empty group gets zeros (or its addend).
+ *   dy            device act [rows, N]
+ *   x             device act [rows, K]
+ *   addend        device f32 [E, N, K] or NULL; may be dw; with dw_f32 only
+ *   dw            device f32 [E, N, K] if dw_f32, else act [E, N, K], out
+ * The rest as for moe_ragged_gemm.
+ */
+int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, const int32_t* offsets, int32_t rows,
+                     int32_t N, int32_t K, int32_t E, const float* addend, void* dw, int32_t dw_f32,
+                     int32_t* err_word, void* stream);
+
+/*
+ * Dense product with its epilogue:
+ *     z[m, n] = sum_k a[m, k] * w[n, k] + bias[n]
+ *     pre[m, n] = act( z ),   out[m, n] = act( f(z) + residual[m, n] )
+ * f is one of MOE_FN_*, of the unrounded z. f(z) of z < -87.3 may count as 0 for
+ * MOE_FN_SILU.
+ *   a             device act [M, K];  w  device act [N, K]
+ *   bias          device act [N] or NULL
+ *   residual      device act [M, N] or NULL; may be out
+ *   pre           device act [M, N] out or NULL (what the gradient needs)
+ *   out           device act [M, N] out (not a, not w, not pre)
+ *   err_word      device i32 or NULL (MOE_DEV_ERR_TIMEOUT)
+ * Requirements: N % 8 == 0, K % 8 == 0, tensors 16-byte aligned.
+ */
+int moe_dense_gemm(const void* a, int32_t act, const void* w, const void* bias, int32_t fn,
+                   const void* residual, void* pre, void* out, int32_t M, int32_t N, int32_t K,
+                   int32_t* err_word, void* stream);
+
+/*
+ * Gradient of the bias and the activation of moe_dense_gemm:
+ *     dz = d_out * f'(pre),   d_pre[m, n] = act( dz ),   d_bias[n] = sum_m dz[m, n]  (+ d_bias[n])
+ * (f32, dz unrounded, summed in an order that depends on M and N alone). The
+ * gradients of a and w are then moe_ragged_gemm (transposed) and moe_ragged_wgrad of
+ * d_pre, of the residual d_out itself. The derivative of MOE_FN_RELU at 0 is 0.
+ *   d_out         device act [M, N]
+ *   pre           device act [M, N]; may be NULL with MOE_FN_NONE (f' = 1)
+ *   d_pre         device act [M, N] out or NULL; may be d_out or pre
+ *   d_bias        device f32 [N] out or NULL; accumulate != 0 adds to what is there
+ * Requirements: d_pre or d_bias given; N % 8 == 0; tensors 16-byte aligned.
+ */
+int moe_bias_act_backward(const void* d_out, const void* pre, int32_t act, int32_t fn, int32_t M, int32_t N,
+                          void* d_pre, float* d_bias, int32_t accumulate, void* stream);
+
+/*
+ * SwiGLU of a stacked gate/up product, rounded once:
+ *     h[r, i] = g / (1 + exp(-g)) * u,   g = gate_up[r, i], u = gate_up[r, I + i]
+ *   gate_up       device act [rows, 2 I];  h  device act [rows, I] out
+ * silu(g) of g < -87.3 may count as 0. Requirements: I % 8 == 0, 16-byte alignment.
+ */
+int moe_swiglu(const void* gate_up, int32_t act, int32_t rows, int32_t I, void* h, void* stream);
+
+/*
+ * Its gradient, s = 1 / (1 + exp(-g)):
+ *     d_gate_up[r, i] = d_h u s (1 + g (1 - s)),   d_gate_up[r, I + i] = d_h g s
+ *   gate_up       device act [rows, 2 I];  d_h  device act [rows, I]
+ *   d_gate_up     device act [rows, 2 I] out; may be gate_up
+ *   h             device act [rows, I] out or NULL: the forward result again (the
+ *                 same bits as moe_swiglu's), so that it need not be kept; may be d_h
+ */
+int moe_swiglu_backward(const void* gate_up, const void* d_h, int32_t act, int32_t rows, int32_t I,
+                        void* d_gate_up, void* h, void* stream);
+
+/*
+ * Token rows to their experts' rows, the transpose of moe_combine without its
+ * weights: xs[pair_to_row[t * top_k + j]] = x[t]. Pairs with a row < 0 (dropped) write
+ * nothing, nor do rows >= max_rows (which set MOE_DEV_ERR_PAIR_ID). The gradient of x
+ * is moe_combine of the rows' gradients with weights of 1.
+ *   x             device act [T, H];  pair_to_row  device i32 [T * top_k]
+ *   xs            device act [max_rows, H] out (not x)
+ * Requirements: H % 8 == 0, 1 <= top_k <= MOE_MAX_TOPK, 16-byte alignment.
+ */
+int moe_dispatch(const void* x, int32_t act, const int32_t* pair_to_row, void* xs, int32_t T, int32_t H,
+                 int32_t top_k, int32_t max_rows, int32_t* err_word, void* stream);
+
+/*
+ * Gradient of moe_combine, for pairs (t, j) with row r = pair_to_row[t * top_k + j]:
+ *     d_y[r] = act( topk_weights[t, j] * d_out[t] ),   d_weights[t, j] = sum_h d_out[t, h] * y[r, h]
+ * Dropped pairs (r < 0) get d_weights 0 and write no row, as do rows >= max_rows
+ * (which set MOE_DEV_ERR_PAIR_ID).
+ *   d_out         device act [T, H];  y  device act [max_rows, H]
+ *   topk_weights  device f32 [T, top_k]
+ *   d_y           device act [max_rows, H] out; may be y
+ *   d_weights     device f32 [T, top_k] out
+ * Requirements: as for moe_dispatch.
+ */
+int moe_combine_backward(const void* d_out, const void* y, int32_t act, const int32_t* pair_to_row,
+                         const float* topk_weights, void* d_y, float* d_weights, int32_t T, int32_t H,
+                         int32_t top_k, int32_t max_rows, int32_t* err_word, void* stream);
+
+/*
+ * Gradient of moe_route_topk_softmax (ids are taken as constants), with
+ * m = sum_j d_weights[t, j] topk_weights[t, j] and g_e the sum of d_weights over the
+ * slots that name e:
+ *     renormalize != 0:  d_logits[t, e] = sum over the slots j that name e of
+ *                                         topk_weights[t, j] (d_weights[t, j] - m)
+ *     renormalize == 0:  d_logits[t, e] = p_e (g_e - m),  p = softmax(logits[t])
+ * in f32. Ids outside [0, E) take no part and set MOE_DEV_ERR_EXPERT_ID.
+ *   logits        device f32 [T, E]; may be NULL if renormalize
+ *   topk_ids / topk_weights / d_weights   device i32 / f32 / f32 [T, top_k]
+ *   d_logits      device f32 [T, E] out; may be logits
+ * Requirements: those of moe_route_topk_softmax.
+ */
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_weights,
+                       const float* d_weights, float* d_logits, int32_t T, int32_t E, int32_t top_k,
+                       int32_t renormalize, int32_t* err_word, void* stream);
 
 /* ---- host helper ------------------------------------------------------------- */
 

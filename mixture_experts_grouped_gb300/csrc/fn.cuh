@@ -1,0 +1,55 @@
+// The activation functions of the dense product and their derivatives, in f32.
+#pragma once
+
+#include "quant.cuh"
+
+namespace moe {
+
+// 1 / (1 + exp(-z)) by the hardware's 2^x and reciprocal, a few ulp; 0 below
+// z = -87.3 (the reciprocal's flush), 1 at +inf.
+__device__ __forceinline__ float sigmoid_fast(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504088896341f));  // log2(e)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// sqrt(2 / pi) (z + 0.044715 z^3), doubled: (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)),
+// which keeps its relative accuracy where 1 + tanh v cancels
+__device__ __forceinline__ float gelu_tanh_arg2(float z) {
+    return z * fmaf(0.0713548162726f, z * z, 1.59576912160573f);  // 2 sqrt(2 / pi) (0.044715, 1)
+}
+
+// f(z). Functions are chosen per launch, so FN is uniform and the branches cost nothing.
+__device__ __forceinline__ float fn_value(int fn, float z) {
+    switch (fn) {
+        case MOE_FN_RELU: return z < 0.0f ? 0.0f : z;  // (NaN stays)
+        case MOE_FN_GELU: return 0.5f * z * erfcf(z * -0.707106781186547524f);  // erfc: no cancellation for z < 0
+        case MOE_FN_GELU_TANH: return z * sigmoid_fast(gelu_tanh_arg2(z));
+        case MOE_FN_SILU: return z * sigmoid_fast(z);
+        default: return z;
+    }
+}
+
+// f'(z)
+__device__ __forceinline__ float fn_slope(int fn, float z) {
+    switch (fn) {
+        case MOE_FN_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+        case MOE_FN_GELU: {
+            const float c = fminf(fmaxf(z, -40.0f), 40.0f);  // beyond, the density is 0 and must not meet an infinity
+            return fmaf(c * 0.398942280401432678f, __expf(-0.5f * c * c), 0.5f * erfcf(z * -0.707106781186547524f));
+        }
+        case MOE_FN_GELU_TANH: {
+            const float c = fminf(fmaxf(z, -20.0f), 20.0f);  // beyond, s (1 - s) is 0
+            const float s = sigmoid_fast(gelu_tanh_arg2(z));
+            return fmaf(c * s * (1.0f - s), fmaf(0.2140644488178f, c * c, 1.59576912160573f), s);
+        }
+        case MOE_FN_SILU: {
+            const float s = sigmoid_fast(z);
+            return s * fmaf(z, 1.0f - s, 1.0f);
+        }
+        default: return 1.0f;
+    }
+}
+
+}  // namespace moe

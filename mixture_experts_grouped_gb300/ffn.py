@@ -2,8 +2,8 @@
 
 :class:`FewTokensLayer` is the expert layer for at most 32 tokens (buffers and
 one call); :class:`SharedExpert` a dense SwiGLU expert on E4M3 weights with
-block scales; :class:`FeedForward` the feed-forward half of a decoder layer
-from them: residual addition and norm, the routed experts, the shared expert
+block scales, :class:`DenseExpert` the same on 16-bit weights;
+:class:`FeedForward` the feed-forward half of a decoder layer from them: residual addition and norm, the routed experts, the shared expert
 added to them. As in :mod:`layer`, PyTorch only provides device memory and the
 stream, every step runs in libmoe.so, nothing synchronises with the host, and
 buffers are allocated once.
@@ -12,7 +12,7 @@ buffers are allocated once.
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Optional
+from typing import Union
 
 import torch
 
@@ -64,6 +64,11 @@ def _require_shape(what: str, t: torch.Tensor, *shape: int) -> None:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
 
 
+def _require_type(what: str, t: torch.Tensor, dtype: torch.dtype) -> None:
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} is {t.dtype}, {'dense' if t.is_contiguous() else 'strided'}, not dense {dtype}")
+
+
 @dataclass
 class BlockFp8Weight:
     """E4M3 codes uint8 [N, K] with f32 scales [ceil(N / 128), ceil(K / 128)]."""
@@ -102,6 +107,35 @@ class SharedExpert:
         return self.out
 
 
+class DenseExpert:
+    """A dense SwiGLU expert on 16-bit weights (``w_gate_up`` [2 I, H], gate rows first, ``w_down``
+    [H, I], both of the activation type): gate/up product, SwiGLU, down product, optionally added
+    to another output."""
+
+    def __init__(self, T, H, I, act, w_gate_up: torch.Tensor, w_down: torch.Tensor, device="cuda"):
+        _require_shape("gate/up weight", w_gate_up, 2 * I, H)
+        _require_shape("down weight", w_down, H, I)
+        dt = L.act_dtype(act)
+        _require_type("gate/up weight", w_gate_up, dt)
+        _require_type("down weight", w_down, dt)
+        self.T, self.H, self.I = T, H, I
+        self.act_code = M.ACT_CODES[act]
+        self.w_gate_up, self.w_down = w_gate_up, w_down
+        self.gate_up = torch.empty((T, 2 * I), dtype=dt, device=device)
+        self.h = torch.empty((T, I), dtype=dt, device=device)
+        self.out = torch.empty((T, H), dtype=dt, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def forward(self, x, addend=None, stream=None):
+        """The expert on rows [T, H], plus ``addend`` [T, H]; returns its output buffer."""
+        M.moe_dense_gemm(x, self.act_code, self.w_gate_up, None, M.MOE_FN_NONE, None, None, self.gate_up, self.T,
+                         2 * self.I, self.H, self.err, stream)
+        M.moe_swiglu(self.gate_up, self.act_code, self.T, self.I, self.h, stream)
+        M.moe_dense_gemm(self.h, self.act_code, self.w_down, None, M.MOE_FN_NONE, addend, None, self.out, self.T,
+                         self.H, self.I, self.err, stream)
+        return self.out
+
+
 _WEIGHT_BITS = {M.MOE_W_BF16: 16.0, M.MOE_W_GPTQ_INT4: 4.15, M.MOE_W_NVFP4: 4.5, M.MOE_W_FP8_E4M3: 8.0}
 
 
@@ -129,18 +163,19 @@ def few_tokens_pay(fmt: int, T: int, H: int, I: int, E: int, k: int) -> bool:
 class FeedForward:
     """The feed-forward half of a decoder layer at one shape:
 
-        r = x + residual,  y = norm(r),  out = experts(y) + shared(e4m3(y))
+        r = x + residual,  y = norm(r),  out = experts(y) + shared(y)
 
     ``forward`` returns (out, r), what the next layer takes. The routed experts
     run as :class:`FewTokensLayer` where that takes them (up to 32 tokens,
     weights of one format) and is faster (:func:`few_tokens_pay`), and as
-    :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. A shared
-    expert of another T, H or activation type is refused (ValueError). There is
+    :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. The shared
+    expert takes y in E4M3 (:class:`SharedExpert`) or as it is (:class:`DenseExpert`). One
+    of another T, H or activation type is refused (ValueError). There is
     no LoRA here: a layer with adapters runs :class:`layer.MoeLayer`'s steps.
     """
 
     def __init__(self, T, H, I, E, k, act, norm_weight, w_router, w_gate_up: L.DeviceWeight, w_down: L.DeviceWeight,
-                 shared: Optional[SharedExpert] = None, eps: float = 1e-6, bs: int = 16, device="cuda",
+                 shared: Union[SharedExpert, DenseExpert, None] = None, eps: float = 1e-6, bs: int = 16, device="cuda",
                  renormalize: bool = True):
         self.T, self.H, self.E, self.k, self.eps, self.renormalize = T, H, E, k, eps, renormalize
         self.act_code = M.ACT_CODES[act]
@@ -153,7 +188,7 @@ class FeedForward:
         dt = L.act_dtype(act)
         self.residual = torch.empty((T, H), dtype=dt, device=device)
         self.y = torch.empty((T, H), dtype=dt, device=device)
-        self.q, self.q_scales = quant_buffers(T, H, device) if shared is not None else (None, None)
+        self.q, self.q_scales = quant_buffers(T, H, device) if isinstance(shared, SharedExpert) else (None, None)
         self.logits = torch.empty((T, E), dtype=torch.float32, device=device)
         if (FewTokensLayer.takes(T, H, I, E, k, w_gate_up, w_down)
                 and few_tokens_pay(w_gate_up.desc.format, T, H, I, E, k)):
@@ -175,6 +210,8 @@ class FeedForward:
             ex.down(stream)
             ex.combine(stream)
             out = ex.out
-        if self.shared is not None:
+        if isinstance(self.shared, DenseExpert):
+            out = self.shared.forward(self.y, out, stream)
+        elif self.shared is not None:
             out = self.shared.forward(self.q, self.q_scales, out, stream)
         return out, self.residual

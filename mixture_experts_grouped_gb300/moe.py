@@ -24,6 +24,9 @@ MOE_ACT_BF16, MOE_ACT_F16 = 0, 1
 MOE_W_BF16, MOE_W_GPTQ_INT4, MOE_W_NVFP4, MOE_W_FP8_E4M3 = 0, 1, 2, 3
 
 ACT_CODES = {"bf16": MOE_ACT_BF16, "f16": MOE_ACT_F16}
+MOE_FN_NONE, MOE_FN_RELU, MOE_FN_GELU, MOE_FN_GELU_TANH, MOE_FN_SILU = 0, 1, 2, 3, 4
+FN_CODES = {"none": MOE_FN_NONE, "relu": MOE_FN_RELU, "gelu": MOE_FN_GELU, "gelu_tanh": MOE_FN_GELU_TANH,
+            "silu": MOE_FN_SILU}
 WFMT_CODES = {"bf16": MOE_W_BF16, "gptq": MOE_W_GPTQ_INT4, "nvfp4": MOE_W_NVFP4, "fp8": MOE_W_FP8_E4M3}
 
 
@@ -81,6 +84,22 @@ _SIGNATURES = {
     "moe_few_tokens": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, POINTER(MoeWeight),
                                  POINTER(MoeWeight), c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p,
                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_ragged_gemm": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                  c_void_p, c_void_p, c_void_p]),
+    "moe_ragged_wgrad": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p,
+                                   c_void_p, c_int32, c_void_p, c_void_p]),
+    "moe_dense_gemm": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                 c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_bias_act_backward": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                        c_int32, c_void_p]),
+    "moe_swiglu": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_swiglu_backward": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]),
+    "moe_dispatch": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p,
+                               c_void_p]),
+    "moe_combine_backward": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32,
+                                       c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+    "moe_route_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                     c_int32, c_void_p, c_void_p]),
     "moe_validate_group_arrays": (c_int32, [c_char_p, c_int32, POINTER(c_int32), c_int32, POINTER(c_char_p),
                                             POINTER(c_int32), c_int32]),
 }
@@ -280,6 +299,57 @@ def moe_few_tokens(x, act, logits, topk_ids, topk_weights, w_gate_up: MoeWeight,
         _ptr(x), act, _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(w_gate_up),
         ctypes.byref(w_down), T, top_k, H, I, E, 1 if renormalize else 0, _ptr(out), _ptr(err_word),
         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_ragged_gemm(a, act, w, transposed, offsets, rows, N, K, E, out, err_word=None, stream=None):
+    _check("moe_ragged_gemm", lib().moe_ragged_gemm(
+        _ptr(a), act, _ptr(w), 1 if transposed else 0, _ptr(offsets), rows, N, K, E, _ptr(out), _ptr(err_word),
+        _stream(stream)))
+
+
+def moe_ragged_wgrad(dy, x, act, offsets, rows, N, K, E, addend, dw, dw_f32, err_word=None, stream=None):
+    _check("moe_ragged_wgrad", lib().moe_ragged_wgrad(
+        _ptr(dy), _ptr(x), act, _ptr(offsets), rows, N, K, E, _ptr(addend), _ptr(dw), 1 if dw_f32 else 0,
+        _ptr(err_word), _stream(stream)))
+
+
+def moe_dense_gemm(a, act, w, bias, fn, residual, pre, out, M, N, K, err_word=None, stream=None):
+    _check("moe_dense_gemm", lib().moe_dense_gemm(
+        _ptr(a), act, _ptr(w), _ptr(bias), fn, _ptr(residual), _ptr(pre), _ptr(out), M, N, K, _ptr(err_word),
+        _stream(stream)))
+
+
+def moe_bias_act_backward(d_out, pre, act, fn, M, N, d_pre=None, d_bias=None, accumulate=False, stream=None):
+    _check("moe_bias_act_backward", lib().moe_bias_act_backward(
+        _ptr(d_out), _ptr(pre), act, fn, M, N, _ptr(d_pre), _ptr(d_bias), 1 if accumulate else 0, _stream(stream)))
+
+
+def moe_swiglu(gate_up, act, rows, I, h, stream=None):
+    _check("moe_swiglu", lib().moe_swiglu(_ptr(gate_up), act, rows, I, _ptr(h), _stream(stream)))
+
+
+def moe_swiglu_backward(gate_up, d_h, act, rows, I, d_gate_up, h=None, stream=None):
+    _check("moe_swiglu_backward", lib().moe_swiglu_backward(
+        _ptr(gate_up), _ptr(d_h), act, rows, I, _ptr(d_gate_up), _ptr(h), _stream(stream)))
+
+
+def moe_dispatch(x, act, pair_to_row, xs, T, H, top_k, max_rows, err_word=None, stream=None):
+    _check("moe_dispatch", lib().moe_dispatch(
+        _ptr(x), act, _ptr(pair_to_row), _ptr(xs), T, H, top_k, max_rows, _ptr(err_word), _stream(stream)))
+
+
+def moe_combine_backward(d_out, y, act, pair_to_row, topk_weights, d_y, d_weights, T, H, top_k, max_rows,
+                         err_word=None, stream=None):
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        _ptr(d_out), _ptr(y), act, _ptr(pair_to_row), _ptr(topk_weights), _ptr(d_y), _ptr(d_weights), T, H, top_k,
+        max_rows, _ptr(err_word), _stream(stream)))
+
+
+def moe_route_backward(logits, topk_ids, topk_weights, d_weights, d_logits, T, E, top_k, renormalize, err_word=None,
+                       stream=None):
+    _check("moe_route_backward", lib().moe_route_backward(
+        _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(d_weights), _ptr(d_logits), T, E, top_k,
+        1 if renormalize else 0, _ptr(err_word), _stream(stream)))
 
 
 def moe_validate_group_arrays(who: str, num_experts: int, offsets, per_expert) -> None:
