@@ -50,6 +50,10 @@ int make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 // x box_cols (64 or 32), swizzled over the box's 128 or 64 bytes.
 int make_tmap_2d_out(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
                      int act);
+// Encode a dense 3-D tensor map with the 128-byte swizzle: d2 matrices of d1 rows x
+// d0 elements, box 1 x b1 x b0 (b0 elements are 128 bytes); act is MOE_ACT_* or kTmapF32.
+constexpr int kTmapF32 = 100;
+int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1);
 // Encode a plain 3-D tensor map: dims d0 (contiguous) x d1 x d2 elements,
 // byte strides s1 (between d1 steps) and s2 (between d2 steps), box
 // b0 x b1 x b2. Used to fetch two separated halves of a weight tile with one

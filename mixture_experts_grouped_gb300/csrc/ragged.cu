@@ -1,90 +1,12 @@
 // Products grouped by expert over ragged spans, their gradients, and the dense
 // product with its epilogue: entry points.
-#include "fn.cuh"
+#include "ragged.cuh"
 
 namespace moe {
 namespace {
 
-// D[i, j] = sum_k A(i, k) B(j, k), 64 x 64 a block, operands by strides. Plain f32
-// multiply-adds from shared memory.
-struct SimpleParams {
-    const uint16_t *a, *b;
-    const int32_t* offsets;
-    int rows, E, I, J, K;                // I: -1 where i runs over a group's rows; K: -1 where k does
-    int64_t ai, ak, ae, bj, bk, be;      // strides; per expert
-    int64_t oi, oe;                      // output strides (j contiguous)
-    void* out;
-    const float* addend;
-    const uint16_t *bias, *residual;
-    uint16_t* pre;
-    int fn, f32;
-    int32_t* err;
-};
-
-template <int ACT>
-__global__ void __launch_bounds__(256) simple_kernel(const SimpleParams p) {
-    pdl_wait();
-    __shared__ float sa[16][65], sb[16][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    using T = typename Act<ACT>::T;
-    if (p.offsets) {
-        bool bad = p.offsets[0] < 0 || p.offsets[p.E] > p.rows;
-        for (int e = 0; e < p.E; ++e) bad |= p.offsets[e + 1] < p.offsets[e];
-        if (bad) {
-            if (threadIdx.x == 0) set_err(p.err, MOE_DEV_ERR_OFFSETS);
-            return;
-        }
-    }
-    for (int e = blockIdx.z; e < p.E; e += gridDim.z) {
-        const int r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.rows;
-        const int I = p.I < 0 ? r1 - r0 : p.I, K = p.K < 0 ? r1 - r0 : p.K;
-        const int64_t abase = e * p.ae + (p.I < 0 ? r0 * p.ai : r0 * p.ak);
-        const int64_t bbase = e * p.be + (p.K < 0 ? r0 * p.bk : 0);
-        for (int i0 = blockIdx.y * 64; i0 < I; i0 += gridDim.y * 64) {
-            const int j0 = blockIdx.x * 64;
-            float acc[4][4] = {};
-            for (int k0 = 0; k0 < K; k0 += 16) {
-                for (int x = threadIdx.x; x < 1024; x += 256) {
-                    const int kk = x & 15, i = x >> 4;
-                    sa[kk][i] = i0 + i < I && k0 + kk < K
-                                    ? Act<ACT>::to_f(reinterpret_cast<const T*>(p.a)[abase + (i0 + i) * p.ai + (k0 + kk) * p.ak])
-                                    : 0.0f;
-                    sb[kk][i] = j0 + i < p.J && k0 + kk < K
-                                    ? Act<ACT>::to_f(reinterpret_cast<const T*>(p.b)[bbase + (j0 + i) * p.bj + (k0 + kk) * p.bk])
-                                    : 0.0f;
-                }
-                __syncthreads();
-                for (int kk = 0; kk < 16; ++kk)
-                    for (int u = 0; u < 4; ++u)
-                        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(sa[kk][ty * 4 + u], sb[kk][tx * 4 + v], acc[u][v]);
-                __syncthreads();
-            }
-            for (int u = 0; u < 4; ++u)
-                for (int v = 0; v < 4; ++v) {
-                    const int i = i0 + ty * 4 + u, j = j0 + tx * 4 + v;
-                    if (i >= I || j >= p.J) continue;
-                    const int64_t at = e * p.oe + (p.I < 0 ? r0 + i : i) * p.oi + j;
-                    float z = acc[u][v];
-                    if (p.addend) z += p.addend[at];
-                    if (p.bias) z += Act<ACT>::to_f(reinterpret_cast<const T*>(p.bias)[j]);
-                    if (p.pre) reinterpret_cast<T*>(p.pre)[at] = Act<ACT>::from_f(z);
-                    z = fn_value(p.fn, z);
-                    if (p.residual) z += Act<ACT>::to_f(reinterpret_cast<const T*>(p.residual)[at]);
-                    if (p.f32) static_cast<float*>(p.out)[at] = z;
-                    else static_cast<T*>(p.out)[at] = Act<ACT>::from_f(z);
-                }
-        }
-    }
-}
-
-int launch_simple(const SimpleParams& p, int act, int rows_i, void* stream, const char* who) {
-    const dim3 grid((p.J + 63) / 64, rows_i < 64 * 1024 ? (rows_i + 63) / 64 : 1024, p.E);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = act == MOE_ACT_BF16 ? launch_pdl(simple_kernel<MOE_ACT_BF16>, grid, 256, 0, st, p)
-                                              : launch_pdl(simple_kernel<MOE_ACT_F16>, grid, 256, 0, st, p);
-    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
-    count_launch();
-    return check_launch(who);
+int launch_rows(const RaggedArgs& g) {
+    return g.act == MOE_ACT_BF16 ? launch_ragged_rows_bf16(g) : launch_ragged_rows_f16(g);
 }
 
 int check_shapes(const char* who, int act, const int32_t* offsets, int rows, int N, int K, int E) {
@@ -111,24 +33,24 @@ extern "C" int moe_ragged_gemm(const void* a, int32_t act, const void* w, int32_
     MOE_REQUIRE(a && w && out, "%s: NULL pointer", who);
     MOE_REQUIRE(moe::aligned16(a) && moe::aligned16(w) && moe::aligned16(out), "%s: a / w / out must be 16-byte aligned",
                 who);
-    moe::SimpleParams p{};
-    p.a = static_cast<const uint16_t*>(a);
-    p.b = static_cast<const uint16_t*>(w);
-    p.offsets = offsets;
-    p.rows = rows;
-    p.E = E;
-    p.I = -1;
-    p.J = transposed ? K : N;
-    p.K = transposed ? N : K;
-    p.ai = p.K;
-    p.ak = 1;
-    p.bj = transposed ? 1 : K;
-    p.bk = transposed ? K : 1;
-    p.be = static_cast<int64_t>(N) * K;
-    p.oi = p.J;
-    p.out = out;
-    p.err = err_word;
-    return moe::launch_simple(p, act, rows, stream, who);
+    moe::RaggedArgs g{};
+    g.p.offsets = offsets;
+    g.p.rows = rows;
+    g.p.E = E;
+    g.p.J = transposed ? K : N;
+    g.p.C = transposed ? N : K;
+    g.p.out = out;
+    g.p.err = err_word;
+    g.p.wait_ns = moe::wait_limit_ns();
+    g.a = a;
+    g.w = w;
+    g.act = act;
+    g.transposed = transposed;
+    g.N = N;
+    g.K = K;
+    g.st = static_cast<cudaStream_t>(stream);
+    g.who = who;
+    return moe::launch_rows(g);
 }
 
 extern "C" int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, const int32_t* offsets, int32_t rows,
@@ -141,26 +63,25 @@ extern "C" int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, cons
     MOE_REQUIRE(dw && (rows == 0 || (dy && x)), "%s: NULL pointer", who);
     MOE_REQUIRE(moe::aligned16(dy) && moe::aligned16(x) && moe::aligned16(addend) && moe::aligned16(dw),
                 "%s: tensors must be 16-byte aligned", who);
-    moe::SimpleParams p{};
-    p.a = static_cast<const uint16_t*>(dy);
-    p.b = static_cast<const uint16_t*>(x);
-    p.offsets = offsets;
-    p.rows = rows;
-    p.E = E;
-    p.I = N;
-    p.J = K;
-    p.K = -1;
-    p.ai = 1;
-    p.ak = N;
-    p.bj = 1;
-    p.bk = K;
-    p.oi = K;
-    p.oe = static_cast<int64_t>(N) * K;
-    p.out = dw;
-    p.addend = addend;
-    p.f32 = dw_f32;
-    p.err = err_word;
-    return moe::launch_simple(p, act, N, stream, who);
+    moe::RaggedArgs g{};
+    g.p.offsets = offsets;
+    g.p.rows = rows;
+    g.p.E = E;
+    g.p.J = N;
+    g.p.C = K;
+    g.p.out = dw;
+    g.p.addend = addend;
+    g.p.err = err_word;
+    g.p.wait_ns = moe::wait_limit_ns();
+    g.a = dy;
+    g.w = x;
+    g.act = act;
+    g.f32 = dw_f32;
+    g.N = N;
+    g.K = K;
+    g.st = static_cast<cudaStream_t>(stream);
+    g.who = who;
+    return moe::launch_ragged_wgrad(g);
 }
 
 extern "C" int moe_dense_gemm(const void* a, int32_t act, const void* w, const void* bias, int32_t fn,
@@ -175,24 +96,24 @@ extern "C" int moe_dense_gemm(const void* a, int32_t act, const void* w, const v
     MOE_REQUIRE(moe::aligned16(a) && moe::aligned16(w) && moe::aligned16(bias) && moe::aligned16(residual) &&
                     moe::aligned16(pre) && moe::aligned16(out),
                 "%s: tensors must be 16-byte aligned", who);
-    moe::SimpleParams p{};
-    p.a = static_cast<const uint16_t*>(a);
-    p.b = static_cast<const uint16_t*>(w);
-    p.rows = M;
-    p.E = 1;
-    p.I = -1;
-    p.J = N;
-    p.K = K;
-    p.ai = K;
-    p.ak = 1;
-    p.bj = K;
-    p.bk = 1;
-    p.oi = N;
-    p.out = out;
-    p.bias = static_cast<const uint16_t*>(bias);
-    p.residual = static_cast<const uint16_t*>(residual);
-    p.pre = static_cast<uint16_t*>(pre);
-    p.fn = fn;
-    p.err = err_word;
-    return moe::launch_simple(p, act, M, stream, who);
+    moe::RaggedArgs g{};
+    g.p.rows = M;
+    g.p.E = 1;
+    g.p.J = N;
+    g.p.C = K;
+    g.p.out = out;
+    g.p.bias = static_cast<const uint16_t*>(bias);
+    g.p.residual = static_cast<const uint16_t*>(residual);
+    g.p.pre = static_cast<uint16_t*>(pre);
+    g.p.fn = fn;
+    g.p.err = err_word;
+    g.p.wait_ns = moe::wait_limit_ns();
+    g.a = a;
+    g.w = w;
+    g.act = act;
+    g.N = N;
+    g.K = K;
+    g.st = static_cast<cudaStream_t>(stream);
+    g.who = who;
+    return moe::launch_rows(g);
 }
