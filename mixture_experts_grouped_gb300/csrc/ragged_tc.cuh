@@ -12,21 +12,22 @@
 //   transposed copy of the weights is needed.
 // Gradient form (the weight's gradient):
 //     dw_e[n, k] = sum_{r in e} dy[r, n] x[r, k]
-//   Both operands are MN-major, the contraction runs over the group's rows, 64 a block.
-//   A group's last block takes as many MMAs as it has units of 16 rows; the rows of its
-//   last unit that belong to the next group (or to nobody: they may hold infinities) are
-//   set to zeros in shared memory, in both operands, by a warp of each CTA, before the
-//   MMA may read them.
+//   Both operands are MN-major, the contraction runs over the group's rows: whole units of
+//   16, four to a block. The rows that are left, 1 to 15, are a unit of their own: its
+//   other rows belong to the next group or to nobody (they may hold infinities), so a warp
+//   of each CTA has the unit copied into a buffer apart, sets those rows to zeros in both
+//   operands, and then lets the MMA have it. The buffers are two, filled up to two tiles
+//   ahead: in the ring of blocks, where a unit is copied only six blocks before its MMA, the
+//   way from its arrival over the clearing to the other CTA's MMA warp was not hidden and
+//   cost 1.2 us a tile (8 groups of 1024 rows, 4096 x 14336: 668 us, 559 with rows that 16
+//   divides).
 //
-// Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle; a thread takes 90
-// to 190 clocks per copy, and there are up to four a block), warp 1 of the even CTA (the
-// leader) issues the MMAs, warps 2 to 5 are the epilogue, warp 7 clears tails. Two
-// accumulators of 256 TMEM columns let the epilogue of a tile run beside the next one's
-// MMAs. Every wait is bounded.
-//
-// Few tiles with a long contraction: a cluster of PARTS pairs takes one tile, each pair a
-// part of the contraction, and each CTA adds a slice of the tile's rows from all parts in
-// their order (distributed shared memory).
+// Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
+// CTA (the leader) issues the MMAs, warps 2 to 5 are the epilogue, warp 7 makes the tails.
+// Two accumulators of 256 TMEM columns let the epilogue of a tile run beside the next
+// one's MMAs. The issuing warps run their loops whole and elect a lane for the MMAs and
+// copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
+// 14336 x 4096: 271 us, 245 elected). Every wait is bounded.
 #pragma once
 
 #include "ragged.cuh"
@@ -37,36 +38,51 @@ namespace ragged {
 namespace {
 
 enum { ROWS_FWD = 0, ROWS_BACK = 1, WGRAD = 2 };
+// kinds of gradient: 16-bit, f32, f32 with an addend
+enum { G16 = 0, G32 = 1, GADD = 2 };
 
 constexpr int BK = 64;
-constexpr int STAGES = 6;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
 constexpr int STAGE = 2 * OPER;
+constexpr int MAX_STAGES = 6;
 constexpr int THREADS = 256;
-constexpr int SG = 36;                    // row stride (floats) of a warp's staging area: 16-byte reads without conflicts
-constexpr int STG_WARP = 32 * SG * 4;     // rows form: 32 rows x 32 columns f32; gradient form: 32 x 128 bytes
-constexpr int STG_AT = STAGES * STAGE;
+constexpr int SG = 36;  // rows form: row stride (floats) of a warp's staging area, 16-byte reads without conflicts
+constexpr int UNIT = 64 * 16 * 2;             // gradient form: 64 columns of a unit of 16 rows
+constexpr int TBUF = 4 * UNIT, TBUFS = 2;     // a tail of both operands
+constexpr int SLOT = 32 * 128;                // gradient form: 32 rows x 128 bytes of dw
 
 struct Tail {
-    uint64_t full[STAGES], empty[STAGES];
-    uint64_t tloc[STAGES], tready[STAGES];  // gradient form: a tail block's copies of this CTA, and both CTAs' cleared tails
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t tloc[TBUFS], tready[TBUFS], tfree[TBUFS];  // tails: copied (this CTA's), cleared (both CTAs'), used
     uint64_t tfull[2], tempty[2], mma_done;
+    uint64_t slot[4][4];  // addends of a warp's slots
     uint32_t tmem_base;
     int abort_flag, n_tiles, jt;
     int off[MOE_MAX_EXPERTS + 1];
     int tstart[MOE_MAX_EXPERTS + 1];
 };
-constexpr int TAIL_AT = STG_AT + 4 * STG_WARP;
-constexpr int SMEM = 1024 + TAIL_AT + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
-static_assert(SMEM <= 232448, "shared memory over the limit");
-static_assert(STG_AT % 1024 == 0, "the gradient form's staging areas are 1024-byte swizzle atoms");
+
+// Shared memory: the ring of stages, tails, staging areas. The gradient's bound by its own
+// bytes where it has an addend: four slots a warp then keep two loads ahead of the stores,
+// and four stages are left; otherwise two slots and five stages.
+template <int MODE, int KIND> struct Shape {
+    static constexpr int SLOTS = MODE != WGRAD ? 0 : KIND == GADD ? 4 : 2;
+    static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;
+    static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : 32 * SG * 4;
+    static constexpr int TBUF_AT = STAGES * STAGE;
+    static constexpr int STG_AT = TBUF_AT + (MODE == WGRAD ? TBUFS * TBUF : 0);
+    static constexpr int TAIL_AT = STG_AT + 4 * STG_WARP;
+    static constexpr int SMEM = TAIL_AT + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
+    static_assert(SMEM <= 232448, "shared memory over the limit");
+};
 
 // ---- operands -------------------------------------------------------------------------
 // MN-major operand with the 128-byte swizzle, as a TMA box of 64 elements (128 bytes) x 64
 // contraction indices lays it down: 8 contraction indices are 1024 bytes (the stride
 // offset), the next 64 elements are 8192 bytes on (the leading offset).
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(8192u >> 4) << 16 |
+// (A unit's box has 16 indices, so its next 64 elements are 2048 bytes on.)
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t lead = 8192u) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
            static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
 }
 constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;  // instruction descriptor: operand is MN-major
@@ -86,14 +102,22 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src
                  : "memory");
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but this thread's last group have read their shared memory
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// mbar_wait, with an acquire of what the other CTA released to it
+// mbar_wait_warp, with an acquire of what the other CTA released to it
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
-    if (!mbar_wait(bar, parity, w)) return false;
+    if (!mbar_wait_warp(bar, parity, w)) return false;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     return true;
+}
+
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // ---- tiles ------------------------------------------------------------------------------
@@ -247,134 +271,180 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
 // to 2^-9 or 2^-12 anyway and take one.)
 constexpr int CHUNK = 64;  // blocks
 
-__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// Gradient form: lane = row n of dw, columns k. A step is 128 bytes of each row (32 f32 or
+// 64 16-bit values): they are laid into one of the warp's slots, 16-byte pieces swizzled by
+// row, and leave by a TMA store, which leaves out what lies past the weight's edges. An
+// addend comes into the slot by a TMA load two steps before and is added in place.
+template <int KIND> struct Slots {
+    static constexpr int COLS = KIND == G16 ? 64 : 32;
+    static constexpr int N = Shape<WGRAD, KIND>::SLOTS;
+    uint8_t* area;
+    uint64_t* bar;
+    uint32_t used = 0;    // steps done
+    uint32_t loaded = 0;  // steps whose addend was asked for
+    int tile = 0, c = 0;  // the next such step
+};
 
-// Gradient form: lane = row n of dw, columns k. 128 bytes of a row (32 f32 or 64 16-bit
-// values) go to the staging area, 16-byte pieces swizzled by row, and leave by a TMA store,
-// which leaves out what lies past the weight's edges.
-template <int ACT, bool F32>
-__device__ __forceinline__ void wgrad_epilogue(const RaggedParams& p, const CUtensorMap* tm_out, uint32_t ta, uint8_t* stg,
-                                               const Tile& t, int n0, int lane, bool first, bool last) {
-    constexpr int COLS = F32 ? 32 : 64;
-    const int n = n0 + lane;
-    const bool row = n < p.J;
-    const size_t at = (static_cast<size_t>(t.e) * p.J + (row ? n : 0)) * p.C;
-    // what is added: later chunks find there what this thread stored itself
-    const float* add = first ? (p.addend ? p.addend + at : nullptr) : static_cast<const float*>(p.out) + at;
-#pragma unroll 1
-    for (int c = 0; c < p.maxu && t.k0 + c < p.C; c += COLS) {
-        uint4 piece[8];
-#pragma unroll
-        for (int h = 0; h < COLS; h += 32) {
-            uint32_t u[32];
-            float v[32];
-            if (t.rows > 0) {
-                tmem_ld32(ta + c + h, u);
-                if (F32 && add && row) {  // the loads run beside each other
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (t.k0 + c + 4 * q < p.C)
-                            piece[q] = *reinterpret_cast<const uint4*>(add + t.k0 + c + 4 * q);
-                }
-                tmem_ld_wait_regs(u);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-                if (F32 && add && row) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (t.k0 + c + 4 * q < p.C) {
-                            v[4 * q] += __uint_as_float(piece[q].x);
-                            v[4 * q + 1] += __uint_as_float(piece[q].y);
-                            v[4 * q + 2] += __uint_as_float(piece[q].z);
-                            v[4 * q + 3] += __uint_as_float(piece[q].w);
-                        }
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (F32 && add && row && t.k0 + c + 4 * q < p.C)
-                        f = *reinterpret_cast<const float4*>(add + t.k0 + c + 4 * q);
-                    v[4 * q] = f.x;
-                    v[4 * q + 1] = f.y;
-                    v[4 * q + 2] = f.z;
-                    v[4 * q + 3] = f.w;
-                }
-            }
-            if (F32) {
-                if (!last) {
-                    float* own = static_cast<float*>(p.out) + at + t.k0 + c;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (row && t.k0 + c + 4 * q < p.C)
-                            *reinterpret_cast<float4*>(own + 4 * q) =
-                                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                    continue;
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    piece[q] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                          __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    piece[h / 8 + q] = make_uint4(Act<ACT>::pack2(v[8 * q], v[8 * q + 1]),
-                                                  Act<ACT>::pack2(v[8 * q + 2], v[8 * q + 3]),
-                                                  Act<ACT>::pack2(v[8 * q + 4], v[8 * q + 5]),
-                                                  Act<ACT>::pack2(v[8 * q + 6], v[8 * q + 7]));
-            }
-        }
-        if (F32 && !last) continue;
-        if (lane == 0) store_wait_read();  // the area's last store
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(stg + lane * 128 + 16 * (q ^ (lane & 7))) = piece[q];
-        fence_proxy_async_smem();
-        if (F32 && !first) fence_proxy_async_global();  // the store overwrites this thread's earlier ones
-        __syncwarp();
-        if (lane == 0 && n0 < p.J) {
-            store_3d(tm_out, stg, t.k0 + c, n0, t.e);
-            store_commit();
-        }
+__device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(p.maxu, p.C - t.k0); }
+
+// asks for the next step's addend, if there is one (one lane; the slot's last store has been read)
+template <int KIND>
+__device__ __forceinline__ void load_addend(Slots<KIND>& sl, const Tail& s, const RaggedParams& p, const CUtensorMap* tm,
+                                            int n_tiles, int step, int n_off) {
+    if (sl.tile >= n_tiles) return;
+    const Tile t = get_tile<WGRAD>(s, p, sl.tile);
+    const uint32_t i = sl.loaded++ % Slots<KIND>::N;
+    mbar_arrive_expect_tx(sl.bar + i, SLOT);
+    tma_load_3d(sl.area + i * SLOT, tm, t.k0 + sl.c, t.j0 + n_off, t.e, sl.bar + i);
+    sl.c += Slots<KIND>::COLS;
+    if (sl.c >= tile_cols(p, t)) {
+        sl.c = 0;
+        sl.tile += step;
     }
 }
 
+template <int ACT>
+__device__ __forceinline__ uint4 pack_piece(const float* v) {
+    return make_uint4(Act<ACT>::pack2(v[0], v[1]), Act<ACT>::pack2(v[2], v[3]), Act<ACT>::pack2(v[4], v[5]),
+                      Act<ACT>::pack2(v[6], v[7]));
+}
+
+// 32 columns of the accumulator, or zeros of an empty group
+__device__ __forceinline__ void load_sums(uint32_t ta, bool any, float (&v)[32]) {
+    if (any) {
+        uint32_t u[32];
+        tmem_ld32(ta, u);
+        tmem_ld_wait_regs(u);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+    }
+}
+
+// One chunk of a tile. `alone`: the tile's only one. Returns false if a wait gave up.
+template <int ACT, int KIND>
+__device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, const RaggedParams& p,
+                                               const CUtensorMap* tm_out, const CUtensorMap* tm_add, uint32_t ta,
+                                               const Tile& t, int n_off, int lane, bool first, bool alone, int n_tiles,
+                                               int step, const WaitCtx& wc) {
+    constexpr int COLS = Slots<KIND>::COLS, N = Slots<KIND>::N;
+    const int n = t.j0 + n_off + lane, cols = tile_cols(p, t);
+    float* row = static_cast<float*>(p.out) + (static_cast<size_t>(t.e) * p.J + n) * p.C + t.k0;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += COLS) {
+        float v[32];
+        load_sums(ta + c, t.rows > 0, v);
+        if (KIND != G16 && !first) {  // a later chunk: to what this thread stored itself
+            if (n < p.J)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c + 4 * q < cols) {
+                        float4* own = reinterpret_cast<float4*>(row + c + 4 * q);
+                        float4 f = *own;
+                        f.x += v[4 * q];
+                        f.y += v[4 * q + 1];
+                        f.z += v[4 * q + 2];
+                        f.w += v[4 * q + 3];
+                        *own = f;
+                    }
+            continue;
+        }
+        const uint32_t i = sl.used % N;
+        uint8_t* at = sl.area + i * SLOT + lane * 128;
+        if (KIND == GADD) {
+            if (!mbar_wait_warp(sl.bar + i, (sl.used / N) & 1u, wc)) return false;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float4 f = *reinterpret_cast<const float4*>(at + 16 * (q ^ (lane & 7)));
+                v[4 * q] += f.x;
+                v[4 * q + 1] += f.y;
+                v[4 * q + 2] += f.z;
+                v[4 * q + 3] += f.w;
+            }
+        } else if (alone) {
+            if (lane == 0) store_wait_read1();  // the slot's last store: two slots
+            __syncwarp();
+        }
+        ++sl.used;
+        if (KIND != G16 && !alone) {
+            if (n < p.J)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c + 4 * q < cols)
+                        *reinterpret_cast<float4*>(row + c + 4 * q) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else if (KIND == G16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(at + 16 * (q ^ (lane & 7))) = pack_piece<ACT>(v + 8 * q);
+            load_sums(ta + c + 32, t.rows > 0, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(at + 16 * ((4 + q) ^ (lane & 7))) = pack_piece<ACT>(v + 8 * q);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(at + 16 * (q ^ (lane & 7))) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (alone && t.j0 + n_off < p.J) store_3d(tm_out, sl.area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
+            store_commit();  // one group a step, empty or not
+            if (KIND == GADD) {
+                store_wait_read1();  // the step before: its slot is the next but one but one
+                load_addend<KIND>(sl, s, p, tm_add, n_tiles, step, n_off);
+            }
+        }
+    }
+    return true;
+}
+
 // ---- the kernel ---------------------------------------------------------------------------
-// tm_a: the M operand (weights; dy), tm_b: the N operand (rows; x), tm_out: the gradient.
-template <int MODE, int ACT, bool F32, int PARTS>
+// tm_a: the M operand (weights; dy), tm_b: the N operand (rows; x). Gradient form: tm_ta and
+// tm_tb are those in boxes of a unit, tm_out and tm_add the gradient and its addend.
+template <int MODE, int ACT, int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-              const __grid_constant__ CUtensorMap tm_out, const RaggedParams p) {
-    static_assert(PARTS == 1 || MODE != WGRAD, "only the rows form is split");
+              const __grid_constant__ CUtensorMap tm_ta, const __grid_constant__ CUtensorMap tm_tb,
+              const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_add,
+              const RaggedParams p) {
+    using S = Shape<MODE, KIND>;
+    constexpr bool CHUNKED = MODE == WGRAD && KIND != G16;
     pdl_wait();
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = align1024_shared(smem_raw);
-    Tail& s = *reinterpret_cast<Tail*>(smem + TAIL_AT);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Tail& s = *reinterpret_cast<Tail*>(smem + S::TAIL_AT);
     const WaitCtx wc{&s.abort_flag, p.err, p.wait_ns};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
-    const int part = static_cast<int>(crank >> 1);
-    const int first = blockIdx.x / (2 * PARTS), step = gridDim.x / (2 * PARTS);
+    const uint32_t rank = cluster_ctarank();  // 0: leader
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    const int bad = build_tiles<MODE>(s, p);  // identical in every CTA
+    const int bad = build_tiles<MODE>(s, p);  // identical in both CTAs
     if (tid == 0) {
         if (bad && blockIdx.x == 0) set_err(p.err, MOE_DEV_ERR_OFFSETS);
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < TBUFS; ++i) {
             mbar_init(&s.tloc[i], 1);
             mbar_init(&s.tready[i], 2);
+            mbar_init(&s.tfree[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
             mbar_init(&s.tempty[i], 8);  // the pair's epilogue warps
         }
+        for (int i = 0; i < 16; ++i) mbar_init(&s.slot[i >> 2][i & 3], 1);
         mbar_init(&s.mma_done, 1);
         fence_mbar_init();
     }
     __syncthreads();
     const int n_tiles = s.n_tiles;
-    if (first >= n_tiles) return;  // the same in all CTAs of the cluster: nothing allocated yet
+    if (first >= n_tiles) return;  // the same in both CTAs: nothing allocated yet
 
     if (warp == 1) {
         tmem_alloc_pair(&s.tmem_base, 512);
@@ -383,48 +453,43 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     if (tid == 0) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
-        if (MODE == WGRAD) tma_prefetch_desc(&tm_out);
+        if (MODE == WGRAD) {
+            tma_prefetch_desc(&tm_ta);
+            tma_prefetch_desc(&tm_tb);
+            tma_prefetch_desc(&tm_out);
+            tma_prefetch_desc(&tm_add);
+        }
     }
     tc_fence_before();
     cluster_sync_all();  // barriers initialised, TMEM allocated
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    const uint32_t lead_full = mapa_shared(smem_u32(&s.full[0]), lead);
-    const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), lead);
-    const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), lead);
-    const int KBall = (p.C + BK - 1) / BK;
-    const int kb0 = PARTS > 1 ? KBall * part / PARTS : 0;
-    const int kb1 = PARTS > 1 ? KBall * (part + 1) / PARTS : KBall;
-    // this CTA's bytes of a stage
-    const uint32_t b_bytes = MODE == WGRAD ? p.maxu * 64 : p.maxu * 8 * 128;
-    auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows + BK - 1) / BK : kb1 - kb0; };
+    const uint32_t lead_full = mapa_shared(smem_u32(&s.full[0]), 0);
+    const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
+    const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), 0);
+    const int KB = (p.C + BK - 1) / BK;
+    const uint32_t b_bytes = MODE == WGRAD ? p.maxu * 64 : p.maxu * 8 * 128;  // this CTA's, of the N operand
+    // blocks of a tile; of a gradient, those that its whole units of 16 rows fill
+    auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows / 16 + 3) / 4 : KB; };
+    auto chunks_of = [&](const Tile& t) { return CHUNKED ? max(1, (blocks_of(t) + CHUNK - 1) / CHUNK) : 1; };
 
     if (warp == 0 || warp == 6) {
-        if (lane == 0) {
-            // ---------------- copies: warp 0 the M operand, warp 6 the N operand ----------------
-            const bool is_a = warp == 0;
-            uint32_t stage = 0, phase = 0, used = 0, tpar = 0;
-            long issued = 0;
-            bool ok = true;
-            for (int tile = first; tile < n_tiles && ok; tile += step) {
-                const Tile t = get_tile<MODE>(s, p, tile);
-                const int nb = blocks_of(t);
-                for (int b = 0; b < nb; ++b) {
-                    if (!mbar_wait(&s.empty[stage], phase ^ 1, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool tail = MODE == WGRAD && b + 1 == nb && t.rows % 16 != 0;
-                    uint32_t bar = lead_full + stage * 8;
-                    if (tail) {
-                        bar = mapa_shared(smem_u32(&s.tloc[stage]), crank);
-                        if (is_a) mbar_arrive_expect_tx(&s.tloc[stage], OPER + b_bytes);
-                        if (is_a && rank == 0) mbar_arrive(&s.full[stage]);
-                        used |= 1u << stage;
-                        tpar ^= 1u << stage;  // bit: uses so far, mod 2
-                    } else if (is_a && rank == 0) {
-                        mbar_arrive_expect_tx(&s.full[stage], 2 * (OPER + b_bytes));
-                    }
+        // ---------------- copies: warp 0 the M operand, warp 6 the N operand ----------------
+        const bool is_a = warp == 0;
+        uint32_t stage = 0, phase = 0;
+        long issued = 0;
+        bool ok = true;
+        for (int tile = first; tile < n_tiles && ok; tile += step) {
+            const Tile t = get_tile<MODE>(s, p, tile);
+            const int nb = blocks_of(t);
+            for (int b = 0; b < nb; ++b) {
+                if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    if (is_a && rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (OPER + b_bytes));
+                    const uint32_t bar = lead_full + stage * 8;
                     uint8_t* dst = smem + stage * STAGE + (is_a ? 0 : OPER);
                     if (MODE == WGRAD) {
                         const int r = t.m0 + b * BK;
@@ -438,139 +503,160 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                             if (p.maxu == 256) tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
                         }
                     } else {
-                        const int c = (kb0 + b) * BK;
-                        if (is_a) {
-                            const int j = t.j0 + 128 * static_cast<int>(rank);
-                            if (MODE == ROWS_FWD) {
-                                load_3d_pair(dst, &tm_a, c, j, t.e, bar);
-                            } else {
-                                load_3d_pair(dst, &tm_a, j, c, t.e, bar);
-                                load_3d_pair(dst + 8192, &tm_a, j + 64, c, t.e, bar);
-                            }
-                        } else {
+                        const int c = b * BK;
+                        if (!is_a) {
                             // (the box has maxu * 8 rows; the MMA reads n / 2 of them)
                             tma_load_2d_pair(dst, &tm_b, c, t.m0 + static_cast<int>(rank) * (t.n / 2), bar);
+                        } else if (MODE == ROWS_FWD) {
+                            load_3d_pair(dst, &tm_a, c, t.j0 + 128 * static_cast<int>(rank), t.e, bar);
+                        } else {
+                            const int j = t.j0 + 128 * static_cast<int>(rank);
+                            load_3d_pair(dst, &tm_a, j, c, t.e, bar);
+                            load_3d_pair(dst + 8192, &tm_a, j + 64, c, t.e, bar);
                         }
                     }
-                    ++issued;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
                 }
-            }
-            if (is_a) {  // let every copy land before either CTA may exit
-                if (rank == 0) {
-                    const long from = issued > STAGES ? issued - STAGES : 0;
-                    for (long j = from; j < issued; ++j)
-                        mbar_drain(&s.full[j % STAGES], static_cast<uint32_t>((j / STAGES) & 1), kWaitLimitNs / 8);
+                __syncwarp();
+                ++issued;
+                if (++stage == S::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
-                for (int i = 0; i < STAGES; ++i)
-                    if (used >> i & 1u) mbar_drain(&s.tloc[i], (tpar >> i & 1u) ^ 1u, kWaitLimitNs / 8);
             }
         }
+        if (is_a && rank == 0) {  // let every copy land before either CTA may exit
+            const long from = issued > S::STAGES ? issued - S::STAGES : 0;
+            for (long j = from; j < issued; ++j)
+                mbar_drain(&s.full[j % S::STAGES], static_cast<uint32_t>((j / S::STAGES) & 1), kWaitLimitNs / 8);
+        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ---------------- MMAs (leader) ----------------
             const uint32_t major = MODE == WGRAD ? kMajorA | kMajorB : MODE == ROWS_BACK ? kMajorA : 0u;
             constexpr uint32_t STEP_K = 32 >> 4, STEP_MN = 2048 >> 4;  // 16 contraction indices on, in descriptor units
             constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
-            uint32_t stage = 0, phase = 0, tpar = 0;
+            uint32_t stage = 0, phase = 0, tails = 0;
             int local = 0;
             bool ok = true;
             for (int tile = first; tile < n_tiles && ok; tile += step) {
                 const Tile t = get_tile<MODE>(s, p, tile);
-                const int nb = blocks_of(t);
+                const int nb = blocks_of(t), chunks = chunks_of(t);
                 const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
-                uint32_t d = 0;
-                int acc = 0, b0 = 0;  // the accumulator, and the first block that goes there
-                for (int b = 0; b < nb || b == 0; ++b) {
-                    if (b == 0 || (F32 && b % CHUNK == 0)) {
-                        if (b > 0) tc_commit_pair(&s.tfull[acc], static_cast<uint16_t>(3u << lead));
-                        acc = local & 1;
-                        const uint32_t aph = (local >> 1) & 1;
-                        ++local;
-                        if (!mbar_wait(&s.tempty[acc], aph ^ 1, wc)) {
+                for (int ch = 0; ch < chunks && ok; ++ch) {
+                    const int acc = local & 1;
+                    const uint32_t aph = (local >> 1) & 1;
+                    ++local;
+                    if (!mbar_wait_warp(&s.tempty[acc], aph ^ 1, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + acc * 256;
+                    const int b0 = CHUNKED ? ch * CHUNK : 0, b1 = CHUNKED ? min(nb, b0 + CHUNK) : nb;
+                    for (int b = b0; b < b1; ++b) {
+                        if (!mbar_wait_warp(&s.full[stage], phase, wc)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        d = tmem + acc * 256;
-                        b0 = b;
-                        if (nb == 0) break;
-                    }
-                    if (!mbar_wait(&s.full[stage], phase, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    int steps = BK / 16;
-                    if (MODE == WGRAD && b + 1 == nb) {
-                        steps = (t.rows - b * BK + 15) / 16;
-                        if (t.rows % 16 != 0) {  // both CTAs have cleared their tails
-                            if (!wait_cluster(&s.tready[stage], tpar >> stage & 1u, wc)) {
-                                ok = false;
-                                break;
-                            }
-                            tpar ^= 1u << stage;
+                        const uint32_t at = smem_u32(smem + stage * STAGE);
+                        const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
+                        const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
+                        const int steps = MODE == WGRAD ? min(4, t.rows / 16 - 4 * b) : 4;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k)
+                                if (MODE != WGRAD || k < steps)
+                                    tc_mma_pair(d, ad + k * step_a, bd + k * step_b, idesc, b > b0 || k > 0);
+                            tc_commit_pair(&s.empty[stage], 0x3);
+                        }
+                        __syncwarp();
+                        if (++stage == S::STAGES) {
+                            stage = 0;
+                            phase ^= 1;
                         }
                     }
-                    tc_fence_after();
-                    const uint32_t at = smem_u32(smem + stage * STAGE);
-                    const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
-                    const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
-#pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        if (MODE != WGRAD || k < steps)
-                            tc_mma_pair(d, ad + k * step_a, bd + k * step_b, idesc, b > b0 || k > 0);
-                    tc_commit_pair(&s.empty[stage], static_cast<uint16_t>(3u << lead));
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
+                    if (!ok) break;
+                    if (MODE == WGRAD && ch + 1 == chunks && t.rows % 16 != 0) {
+                        const uint32_t tb = tails % TBUFS;
+                        if (!wait_cluster(&s.tready[tb], (tails / TBUFS) & 1u, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        ++tails;
+                        tc_fence_after();
+                        const uint32_t at = smem_u32(smem + S::TBUF_AT + tb * TBUF);
+                        if (elect_one()) {
+                            tc_mma_pair(d, mn_desc(at, UNIT), mn_desc(at + 2 * UNIT, UNIT), idesc, b1 > b0);
+                            tc_commit_pair(&s.tfree[tb], 0x3);
+                        }
+                        __syncwarp();
                     }
+                    if (elect_one()) tc_commit_pair(&s.tfull[acc], 0x3);
+                    __syncwarp();
                 }
-                if (!ok) break;
-                tc_commit_pair(&s.tfull[acc], static_cast<uint16_t>(3u << lead));
             }
-            tc_commit_pair(&s.mma_done, static_cast<uint16_t>(1u << lead));
+            if (elect_one()) tc_commit_pair(&s.mma_done, 0x1);
+            __syncwarp();
             mbar_drain(&s.mma_done, 0, kWaitLimitNs / 8);
         }
-        __syncwarp();
     } else if (warp == 7) {
         if (MODE == WGRAD) {
-            // ---------------- tails: rows of a group's last unit of 16 that are not the group's ----------------
-            uint32_t stage = 0, tpar = 0;
+            // ---------------- tails ----------------
+            uint32_t tails = 0;
             for (int tile = first; tile < n_tiles; tile += step) {
                 const Tile t = get_tile<MODE>(s, p, tile);
-                const int nb = blocks_of(t);
-                if (nb == 0) continue;
-                const uint32_t last = (stage + nb - 1) % STAGES;
-                stage = (stage + nb) % STAGES;
-                if (t.rows % 16 == 0) continue;
-                if (!mbar_wait_warp(&s.tloc[last], tpar >> last & 1u, wc)) break;
-                tpar ^= 1u << last;
-                const int r0 = t.rows - (nb - 1) * BK, r1 = (r0 + 15) / 16 * 16;
-                // row r of each 64-element group is the 128 bytes at 128 r (the swizzle moves bytes within them)
-                uint8_t* base = smem + last * STAGE;
-                const int chunks = 16 + p.maxu / 16;  // 16-byte pieces a row has in both operands
-                for (int i = lane; i < (r1 - r0) * chunks; i += 32) {
-                    const int r = r0 + i / chunks, c = i % chunks;
-                    *reinterpret_cast<uint4*>(base + (c >> 3) * 8192 + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const int left = t.rows % 16;
+                if (left == 0) continue;
+                const uint32_t tb = tails % TBUFS, ph = (tails / TBUFS) & 1u;
+                ++tails;
+                if (!mbar_wait_warp(&s.tfree[tb], ph ^ 1u, wc)) break;
+                uint8_t* buf = smem + S::TBUF_AT + tb * TBUF;
+                if (elect_one()) {
+                    const int r = t.m0 + t.rows - left;
+                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + p.maxu / 2 * static_cast<int>(rank);
+                    mbar_arrive_expect_tx(&s.tloc[tb], p.maxu == 256 ? 4 * UNIT : 3 * UNIT);
+                    tma_load_2d(buf, &tm_ta, n, r, &s.tloc[tb]);
+                    tma_load_2d(buf + UNIT, &tm_ta, n + 64, r, &s.tloc[tb]);
+                    tma_load_2d(buf + 2 * UNIT, &tm_tb, k, r, &s.tloc[tb]);
+                    if (p.maxu == 256) tma_load_2d(buf + 3 * UNIT, &tm_tb, k + 64, r, &s.tloc[tb]);
+                }
+                __syncwarp();
+                if (!mbar_wait_warp(&s.tloc[tb], ph, wc)) {
+                    mbar_drain(&s.tloc[tb], ph, kWaitLimitNs / 8);
+                    break;
+                }
+                // row r of 64 columns is the 128 bytes at 128 r (the swizzle moves bytes within them)
+                for (int i = lane; i < (16 - left) * 32; i += 32) {
+                    const int r = left + (i >> 5), piece = i & 31;
+                    *reinterpret_cast<uint4*>(buf + (piece >> 3) * UNIT + r * 128 + (piece & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(lead_tready + last * 8);
+                if (elect_one()) mbar_arrive_cluster(lead_tready + tb * 8);
+                __syncwarp();
             }
         }
-    } else if (PARTS == 1) {
+    } else {
         // ---------------- epilogue ----------------
         const int q = warp & 3;  // TMEM lane quarter
-        uint8_t* stg = smem + STG_AT + (MODE == WGRAD ? (warp - 2) * 4096 : (warp - 2) * STG_WARP);
+        const int n_off = 128 * static_cast<int>(rank) + 32 * q;
+        uint8_t* stg = smem + S::STG_AT + (warp - 2) * S::STG_WARP;
+        [[maybe_unused]] Slots<MODE == WGRAD ? KIND : G16> sl;
+        if (MODE == WGRAD) {
+            sl.area = stg;
+            sl.bar = s.slot[warp - 2];
+            sl.tile = first;
+            if (KIND == GADD && lane == 0)
+                for (int i = 0; i < 2; ++i) load_addend(sl, s, p, &tm_add, n_tiles, step, n_off);
+        }
         int local = 0;
         bool ok = true;
         for (int tile = first; tile < n_tiles && ok; tile += step) {
             const Tile t = get_tile<MODE>(s, p, tile);
-            const int chunks = F32 ? max(1, (blocks_of(t) + CHUNK - 1) / CHUNK) : 1;
-            for (int ch = 0; ch < chunks; ++ch) {
+            const int chunks = chunks_of(t);
+            for (int ch = 0; ch < chunks && ok; ++ch) {
                 const int acc = local & 1;
                 const uint32_t aph = (local >> 1) & 1;
                 ++local;
@@ -580,9 +666,11 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
                 tc_fence_after();
                 const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-                const int col0 = t.j0 + 128 * static_cast<int>(rank) + 32 * q;
-                if (MODE == WGRAD) wgrad_epilogue<ACT, F32>(p, &tm_out, ta, stg, t, col0, lane, ch == 0, ch + 1 == chunks);
-                else rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, col0, lane);
+                if constexpr (MODE == WGRAD)
+                    ok = wgrad_epilogue<ACT, KIND>(sl, s, p, &tm_out, &tm_add, ta, t, n_off, lane, ch == 0, chunks == 1,
+                                                   n_tiles, step, wc);
+                else
+                    rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, lane);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -591,67 +679,17 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
             }
         }
-        if (MODE == WGRAD && lane == 0) store_wait();
+        if constexpr (MODE == WGRAD) {
+            if (lane == 0) {
+                if (KIND == GADD)  // (only after a wait that gave up are there any)
+                    for (uint32_t i = sl.used; i < sl.loaded; ++i)
+                        mbar_drain(sl.bar + i % Slots<KIND>::N, (i / Slots<KIND>::N) & 1u, kWaitLimitNs / 8);
+                store_wait();
+            }
+        }
     }
 
     __syncwarp();
-    if (PARTS > 1) {
-        // ---------------- a split tile's sums, from all parts ----------------
-        const Tile t = get_tile<MODE>(s, p, first);
-        const bool epi = warp >= 2 && warp < 6;
-        const int q = warp & 3, me = 32 * q + lane;
-        bool ok = true;
-        if (epi) {
-            ok = mbar_wait_warp(&s.tfull[0], 0, wc);
-            tc_fence_after();
-        }
-        __syncwarp();
-        cluster_sync_all();  // every pair's MMAs are complete: the stages are free
-        float* sums = reinterpret_cast<float*>(smem);  // [source part][row of the slice][128 columns]
-        const int per = t.n / PARTS;                   // rows of a slice (n is a multiple of 16)
-        if (epi) {
-            const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-            for (int c = 0; c < t.n; c += 32) {
-                uint32_t u[32];
-                tmem_ld32(ta + c, u);
-                tmem_ld_wait_regs(u);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int dst = (c + j) / per;
-                    if (c + j < t.n) {
-                        const uint32_t to =
-                            mapa_shared(smem_u32(sums + (part * per + c + j - dst * per) * 128 + me), 2 * dst + rank);
-                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(u[j]) : "memory");
-                    }
-                }
-            }
-        }
-        __syncwarp();
-        cluster_sync_all();
-        if (epi && ok) {
-            const int col0 = t.j0 + 128 * static_cast<int>(rank) + 32 * q;
-            const float b = bias_of<ACT>(p, col0 + lane);
-            float* stg = reinterpret_cast<float*>(smem + STG_AT + (warp - 2) * STG_WARP);
-            const int have = min(per, t.rows - part * per);
-#pragma unroll 1
-            for (int c = 0; c < have; c += 32) {
-                float v[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    v[j] = 0.0f;
-                    if (c + j < have) {
-                        v[j] = sums[(c + j) * 128 + me];
-#pragma unroll
-                        for (int r = 1; r < PARTS; ++r) v[j] += sums[(r * per + c + j) * 128 + me];
-                        v[j] += b;
-                    }
-                }
-                store_rows<ACT>(p, v, stg, lane, t.m0 + part * per + c, have - c, col0);
-            }
-        }
-    }
-
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // the leader's MMAs read the peer's shared memory and write its TMEM
@@ -661,66 +699,51 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 
 // ---- launch -----------------------------------------------------------------------------
 
-// clusters of 2 PARTS CTAs that the current device runs at once
-template <typename Kernel> int prepare(Kernel kernel, int parts, int& clusters, const char* who) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * parts;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    const int sms = sm_count();
-    cfg.gridDim = dim3(sms > 0 ? sms / (2 * parts) * (2 * parts) : 2 * parts);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), SMEM);
-    if (rc != MOE_OK) return rc;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
-    if (e != cudaSuccess || clusters <= 0)
-        return fail(MOE_ERR_CUDA, "%s: cannot place clusters of %d CTAs: %s", who, 2 * parts, cudaGetErrorString(e));
-    return MOE_OK;
-}
+struct Maps {
+    CUtensorMap a, b, ta, tb, out, add;
+};
 
-template <int MODE, int ACT, bool F32, int PARTS>
-int launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out, const RaggedParams& p, int64_t tiles,
-           cudaStream_t st, const char* who) {
-    auto kernel = ragged_kernel<MODE, ACT, F32, PARTS>;
-    static int configured_for = -1, clusters = 0;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_for != dev) {
-        int n = 0;
-        const int rc = prepare(kernel, PARTS, n, who);
-        if (rc != MOE_OK) return rc;
-        clusters = n;
-        configured_for = dev;
-    }
-    if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-    if (tiles <= 0) return MOE_OK;
+template <int MODE, int ACT, int KIND>
+int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st, const char* who) {
+    auto kernel = ragged_kernel<MODE, ACT, KIND>;
+    constexpr int smem = Shape<MODE, KIND>::SMEM;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * PARTS;
+    attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    // a split tile is one cluster's; otherwise clusters walk the tiles
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * PARTS * (PARTS > 1 || tiles < clusters ? tiles : clusters)));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.stream = st;
+    cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static int configured_for = -1, max_pairs = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_for != dev) {
+        const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+        if (rc != MOE_OK) return rc;
+        const int sms = sm_count();
+        cfg.gridDim = dim3(sms > 1 ? sms / 2 * 2 : 2);
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess || n <= 0)
+            return fail(MOE_ERR_CUDA, "%s: cannot place pairs of CTAs: %s", who, cudaGetErrorString(e));
+        max_pairs = n;
+        configured_for = dev;
+    }
+    if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < max_pairs ? tiles : max_pairs)));
+    cfg.stream = st;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, b, out, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.ta, m.tb, m.out, m.add, p);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     count_launch();
     return check_launch(who);
 }
 
-// Rows form: tile height and split.
 template <int ACT, int MODE> int rows_form(const RaggedArgs& g) {
     RaggedParams p = g.p;
     // rows a group has, if all have the same
@@ -728,24 +751,14 @@ template <int ACT, int MODE> int rows_form(const RaggedArgs& g) {
     const int units = static_cast<int>((each + 15) / 16 < 16 ? (each + 15) / 16 : 16);
     p.maxu = 1;
     while (p.maxu < units) p.maxu *= 2;
-    int parts = 1;
-    const int64_t jt = (p.J + 255) / 256;
-    if (p.E == 1) {
-        const int64_t tiles = ((p.rows + 15) / 16 + p.maxu - 1) / p.maxu * jt;
-        const int kb = (p.C + BK - 1) / BK;
-        while (parts < 4 && tiles * parts * 2 <= 72 && kb >= 8 * parts) parts *= 2;
-    }
-    CUtensorMap a, b;
-    int rc = make_tmap_3d(&a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64);
-    if (rc == MOE_OK) rc = make_tmap_2d(&b, g.a, p.rows, p.C, p.maxu * 8, g.act);
+    Maps m;
+    int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64);
+    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, p.rows, p.C, p.maxu * 8, g.act);
     if (rc != MOE_OK) return rc;
+    m.ta = m.tb = m.out = m.add = m.b;
     // row tiles at most: one more per group than the rows fill
-    const int64_t tiles = ((p.rows + 16 * p.maxu - 1) / (16 * p.maxu) + (p.E > 1 ? p.E : 0)) * jt;
-    switch (parts) {
-        case 1: return launch<MODE, ACT, false, 1>(a, b, b, p, tiles, g.st, g.who);
-        case 2: return launch<MODE, ACT, false, 2>(a, b, b, p, tiles, g.st, g.who);
-        default: return launch<MODE, ACT, false, 4>(a, b, b, p, tiles, g.st, g.who);
-    }
+    const int64_t tiles = ((p.rows + 16 * p.maxu - 1) / (16 * p.maxu) + (p.E > 1 ? p.E : 0)) * ((p.J + 255) / 256);
+    return launch<MODE, ACT, G16>(m, p, tiles, g.st, g.who);
 }
 
 }  // namespace
