@@ -5,8 +5,78 @@
 namespace moe {
 namespace {
 
+// Which form a product of rows takes.
+//
+// Groups whose sizes only the device knows: CTA pairs, tiles of up to twice a group's mean
+// rows (3066 rows of 64 groups, most of 30 to 60: 71 us with tiles of 96 rows, 72 of 128, 74
+// of 256, whose over-wide boxes bring rows of the next groups along, 80 of 48, which read
+// the fuller groups' weights more than once).
+//
+// One group (a dense product): the form, row tiles and split that a model of their time
+// finds best. Its costs (ns) are fitted to 110 sizes from 1 x 88 x 88 to 4000 x 2048 x 14336
+// measured at every form; the choice is 1.1% slower than the best form in the mean, 15% at
+// worst.
+//   streaming (up to 32 rows): the weights at 5.7 TB/s, or a warp's blocks one after the
+//     other, and 27 ps a byte of the rows, which every CTA reads
+//   split: a launch (and its clusters' meetings), a CTA's blocks, slower where two share an
+//     SM, or the weights at 5.6 TB/s; 26 a row of the tile at its end
+//   pairs: waves of tiles, each its blocks or its epilogue, or the weights at 5 TB/s
+// (us, streaming / split / pairs: 1 x 2816 x 2048 4.8 / 8.2 / 12.8; 32 x 2816 x 2048 9.2 / 8.7 / 13.1; 16 x
+// 14336 x 4096 26.6 / 24.7 / 27.8; 64 x 4096 x 14336 - / 27.6 / 52.6; 333 x 2816 x 2048 - / 13.3 / 14.2; 1333 x 2816 x
+// 2048 - / 23.1 / 19.6.)
+struct RowsPick {
+    RowsForm f;
+    bool streaming;
+};
+RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
+    const int64_t U = (static_cast<int64_t>(p.rows) + 15) / 16, KB = (p.C + 63) / 64;
+    RowsPick best{{1, 0, 0}, false};
+    if (p.offsets) {
+        const int64_t units = ((static_cast<int64_t>(p.rows) + p.E - 1) / p.E + 15) / 16;
+        best.f.maxu = static_cast<int>(units >= 8 ? 16 : 2 * units);
+        return best;
+    }
+    const int64_t J = p.J, bytes = 2 * J * p.C;
+    int64_t best_ns = INT64_MAX;
+    auto ceil = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    auto max = [](int64_t a, int64_t b) { return a > b ? a : b; };
+    auto offer = [&](int64_t ns, const RowsPick& pick) {
+        if (ns < best_ns) {
+            best_ns = ns;
+            best = pick;
+        }
+    };
+    if (p.rows <= 32 && !transposed)
+        offer(2170 + max(bytes / 5700, 250 * ceil(KB, 8)) + 27 * p.rows * (2 * static_cast<int64_t>(p.C)) / 1024,
+              {{0, 0, 0}, true});
+    static const struct {
+        int parts, launch_ns;
+    } splits[] = {{1, 2620}, {2, 4940}, {4, 5410}, {8, 6610}};
+    const int64_t mt = ceil(U, 8), h = ceil(U, mt) * 16, split_tiles = ceil(J, 128) * mt;
+    for (const auto& s : splits) {
+        const int64_t ctas = split_tiles * s.parts;
+        if (s.parts > KB || ctas > 4 * sms) break;
+        const int64_t blocks = ceil(KB, s.parts), load = ctas > sms ? 2 : 1;
+        const int64_t body = blocks * (198 + h * 11 / 10);
+        const int64_t ns = max(max(body, load * blocks * (85 + h * 11 / 10)), bytes / 5600) +
+                           (ceil(ctas, 2 * sms) - 1) * (s.launch_ns + body) + s.launch_ns + 26 * h * load;
+        offer(ns, {{0, static_cast<int>(mt), s.parts}, false});
+    }
+    const int64_t m0 = ceil(U, 16);
+    for (int64_t t = m0; t <= U && t < m0 + 8; ++t) {
+        const int64_t rows = ceil(U, t) * 16, waves = ceil(t * ceil(J, 256), sms / 2);
+        const int64_t ns = 5130 + max(waves * max(KB * (189 + rows * 4 / 10), 1300 + 15 * rows), bytes / 5000) + 15 * rows;
+        offer(ns, {{static_cast<int>(ceil(U, t)), 0, 0}, false});
+    }
+    return best;
+}
+
 int launch_rows(const RaggedArgs& g) {
-    return g.act == MOE_ACT_BF16 ? launch_ragged_rows_bf16(g) : launch_ragged_rows_f16(g);
+    const int sms = sm_count();
+    if (sms < 2) return fail(MOE_ERR_CUDA, "%s: no CUDA device", g.who);
+    const RowsPick pick = pick_rows_form(g.p, g.transposed, sms);
+    if (pick.streaming) return launch_dense_rows(g);
+    return g.act == MOE_ACT_BF16 ? launch_ragged_rows_bf16(g, pick.f) : launch_ragged_rows_f16(g, pick.f);
 }
 
 int check_shapes(const char* who, int act, const int32_t* offsets, int rows, int N, int K, int E) {

@@ -30,8 +30,15 @@ struct RaggedArgs {
     const char* who;
 };
 
-int launch_ragged_rows_bf16(const RaggedArgs& g);
-int launch_ragged_rows_f16(const RaggedArgs& g);
+// How a product of rows runs: on CTA pairs, row tiles of up to maxu units of 16 rows; or, with
+// parts > 0, one group split: row tiles, and CTAs that share a tile's contraction.
+struct RowsForm {
+    int maxu, tiles, parts;
+};
+
+int launch_ragged_rows_bf16(const RaggedArgs& g, const RowsForm& f);
+int launch_ragged_rows_f16(const RaggedArgs& g, const RowsForm& f);
+int launch_dense_rows(const RaggedArgs& g);  // up to 32 rows, one group, not transposed
 int launch_ragged_wgrad(const RaggedArgs& g);
 
 }  // namespace moe

@@ -1,7 +1,12 @@
 // Rows form of the ragged products, fp16.
-#include "ragged_tc.cuh"
+#include "ragged_split.cuh"
 
-int moe::launch_ragged_rows_f16(const RaggedArgs& g) {
-    return g.transposed ? ragged::rows_form<MOE_ACT_F16, ragged::ROWS_BACK>(g)
-                        : ragged::rows_form<MOE_ACT_F16, ragged::ROWS_FWD>(g);
+int moe::launch_ragged_rows_f16(const RaggedArgs& g, const RowsForm& f) {
+    constexpr int ACT = MOE_ACT_F16;
+    if (f.parts) {
+        return g.transposed ? ragged::launch_split<ragged::ROWS_BACK, ACT>(g, f.tiles, f.parts)
+                            : ragged::launch_split<ragged::ROWS_FWD, ACT>(g, f.tiles, f.parts);
+    }
+    return g.transposed ? ragged::launch_rows_form<ragged::ROWS_BACK, ACT>(g, f.maxu)
+                        : ragged::launch_rows_form<ragged::ROWS_FWD, ACT>(g, f.maxu);
 }

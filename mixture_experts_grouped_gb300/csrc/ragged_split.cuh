@@ -1,0 +1,300 @@
+// Dense products of few tiles (ragged products of one group): one 128-column tile to a
+// cluster of CTAs, each with a part of the contraction.
+//
+// With few rows a product is bound by its weights' bytes, and only if every SM streams
+// them: 4096 columns are 16 tiles of the pair form, and 32 SMs drew 2.3 TB/s. Here a tile is
+// 128 output columns (the MMA's M operand, one CTA) by up to 128 rows (its N operand), and
+// up to 8 CTAs share its contraction, two CTAs to an SM. Each then adds a slice of the
+// tile's rows from all parts, in their order, through distributed shared memory, and
+// finishes it. (Clusters of pairs do not fit as well: of 8 CTAs with an SM each, 15 are
+// placed at once.) Every wait is bounded.
+#pragma once
+
+#include "ragged_tc.cuh"
+
+namespace moe {
+namespace ragged {
+namespace {
+
+constexpr int SPLIT_THREADS = 192;
+constexpr int SPLIT_MAX_STAGES = 8;
+constexpr int SPLIT_ROWS = 128;  // most rows of a tile
+constexpr int SPLIT_PARTS = 8;   // most CTAs of a tile
+
+struct SplitTail {
+    uint64_t full[SPLIT_MAX_STAGES], empty[SPLIT_MAX_STAGES], done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct SplitParams {
+    RaggedParams r;
+    int parts, stages;
+    int mt;        // row tiles
+    int box;       // rows of the N operand's boxes: the tallest tile
+    int tmem;      // TMEM columns
+    int tail_at;   // after the stages
+};
+
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    tma_load_3d(dst, map, c0, c1, c2, bar);
+}
+
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int MODE, int ACT>
+__global__ void __launch_bounds__(SPLIT_THREADS)
+split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const SplitParams sp) {
+    pdl_wait();
+    const RaggedParams& p = sp.r;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    SplitTail& s = *reinterpret_cast<SplitTail*>(smem + sp.tail_at);
+    const WaitCtx wc{&s.abort_flag, p.err, p.wait_ns};
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int parts = sp.parts, part = parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / parts;
+    // row tiles fastest: those of a column tile share its weights in L2
+    const int i = tile % sp.mt, j0 = tile / sp.mt * 128;
+    const int U = (p.rows + 15) / 16, u0 = static_cast<int>(static_cast<int64_t>(U) * i / sp.mt),
+              u1 = static_cast<int>(static_cast<int64_t>(U) * (i + 1) / sp.mt);
+    const int m0 = 16 * u0, n = 16 * (u1 - u0), rows = min(p.rows - m0, n);
+    const int KB = (p.C + BK - 1) / BK, kb0 = KB * part / parts, kb1 = KB * (part + 1) / parts;
+    const uint32_t stage_bytes = OPER + sp.box * 128;
+
+    if (tid == 0) {
+        s.abort_flag = 0;
+        for (int q = 0; q < sp.stages; ++q) {
+            mbar_init(&s.full[q], 1);
+            mbar_init(&s.empty[q], 1);
+        }
+        mbar_init(&s.done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&s.tmem_base, sp.tmem);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---------------- copies ----------------
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int b = kb0; b < kb1; ++b) {
+            if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&s.full[stage], stage_bytes);
+                uint8_t* dst = smem + stage * stage_bytes;
+                if (MODE == ROWS_FWD) {
+                    load_3d(dst, &tm_a, b * BK, j0, 0, &s.full[stage]);
+                } else {
+                    load_3d(dst, &tm_a, j0, b * BK, 0, &s.full[stage]);
+                    load_3d(dst + 8192, &tm_a, j0 + 64, b * BK, 0, &s.full[stage]);
+                }
+                tma_load_2d(dst + OPER, &tm_b, b * BK, m0, &s.full[stage]);
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == sp.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        // let every copy land before the stages serve the sums, or the CTA exits
+        for (int j = max(0, issued - sp.stages); j < issued; ++j)
+            mbar_drain(&s.full[j % sp.stages], static_cast<uint32_t>((j / sp.stages) & 1), kWaitLimitNs / 8);
+    } else if (warp == 1) {
+        // ---------------- MMAs ----------------
+        constexpr uint32_t step_a = MODE == ROWS_FWD ? 32 >> 4 : 2048 >> 4;
+        const uint32_t idesc = f16_idesc(ACT, 128, n) | (MODE == ROWS_BACK ? kMajorA : 0u);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int b = kb0; b < kb1; ++b) {
+            if (!mbar_wait_warp(&s.full[stage], phase, wc)) break;
+            tc_fence_after();
+            const uint32_t at = smem_u32(smem + stage * stage_bytes);
+            const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at), bd = sw128_desc(at + OPER);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) tc_mma(tmem, ad + k * step_a, bd + 2 * k, idesc, b > kb0 || k > 0);
+                tc_commit(&s.empty[stage]);
+            }
+            __syncwarp();
+            if (++stage == sp.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (elect_one()) tc_commit(&s.done);
+        __syncwarp();
+        mbar_drain(&s.done, 0, kWaitLimitNs / 8);
+    } else {
+        ok = mbar_wait_warp(&s.done, 0, wc);
+        tc_fence_after();
+    }
+    __syncwarp();
+    const bool epi = warp >= 2;
+    const int q = warp & 3, me = 32 * q + lane;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const float bias = epi ? bias_of<ACT>(p, j0 + me) : 0.0f;
+    // the epilogue's areas lie where the stages were: the sums of all parts, then staging
+    const int sum_bytes = parts > 1 ? parts * ((n / 4 + parts - 1) / parts) * 2048 : 0;  // (slices may differ by 4 rows)
+    float* stg = reinterpret_cast<float*>(smem + sum_bytes + (warp - 2) * (32 * SG * 4));
+    // *abort_flag: a wait gave up here, and what was summed is not whole (the others learn it from err alone)
+    if (parts == 1) {
+        if (epi && ok)
+#pragma unroll 1
+            for (int c = 0; c < rows; c += 32) {
+                uint32_t u[32];
+                float v[32];
+                tmem_ld32(ta + c, u);
+                tmem_ld_wait_regs(u);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]) + bias;
+                store_rows<ACT>(p, v, stg, lane, m0 + c, rows - c, j0 + 32 * q);
+            }
+    } else {
+        cluster_sync_all();  // every CTA's MMAs are complete: the stages are free
+        // part d adds rows 4 f(d) to 4 f(d + 1), f(d) = n / 4 d / parts: four rows of a column are a 16-byte store.
+        // There, [source part][four rows][128 columns][4]
+        float4* sums = reinterpret_cast<float4*>(smem);
+        const int quads = n / 4;
+        if (epi) {
+            int dst = 0, f0 = 0, f1 = quads / parts;
+            while (f1 == f0) f1 = quads * (++dst + 1) / parts;
+            const uint32_t mine = smem_u32(sums + me);
+            uint32_t to = mapa_shared(mine + part * (f1 - f0) * 2048, dst);
+#pragma unroll 1
+            for (int c = 0; c < n; c += 16) {
+                uint32_t u[16];
+                tmem_ld16_wait(ta + c, u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int f = c / 4 + j;
+                    if (f == f1) {
+                        f0 = f1;
+                        while (f1 == f0) f1 = quads * (++dst + 1) / parts;
+                        to = mapa_shared(mine + part * (f1 - f0) * 2048, dst);
+                    }
+                    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (f - f0) * 2048),
+                                 "r"(u[4 * j]), "r"(u[4 * j + 1]), "r"(u[4 * j + 2]), "r"(u[4 * j + 3])
+                                 : "memory");
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (epi && ok) {
+            const int q0 = quads * part / parts, per = quads * (part + 1) / parts - q0;
+            const int have = min(4 * per, rows - 4 * q0);
+#pragma unroll 1
+            for (int c = 0; c < have; c += 32) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (c + 4 * j < have) {
+                        const float4* src = sums + (c / 4 + j) * 128 + me;
+                        f = src[0];
+                        for (int r = 1; r < parts; ++r) {
+                            const float4 x = src[r * per * 128];
+                            f.x += x.x;
+                            f.y += x.y;
+                            f.z += x.z;
+                            f.w += x.w;
+                        }
+                    }
+                    v[4 * j] = f.x + bias;
+                    v[4 * j + 1] = f.y + bias;
+                    v[4 * j + 2] = f.z + bias;
+                    v[4 * j + 3] = f.w + bias;
+                }
+                store_rows<ACT>(p, v, stg, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, sp.tmem);
+}
+
+// Three stages hold the sums (2048 bytes for four rows of each part, the largest slice counting for all) and the
+// staging areas: of 128 rows as of 16.
+constexpr int split_sums(int n) { return SPLIT_PARTS * ((n / 4 + SPLIT_PARTS - 1) / SPLIT_PARTS) * 2048; }
+static_assert(3 * (OPER + SPLIT_ROWS * 128) >= split_sums(SPLIT_ROWS) + 4 * 32 * SG * 4 &&
+                  3 * (OPER + 16 * 128) >= split_sums(16) + 4 * 32 * SG * 4 &&
+                  3 * (OPER + 48 * 128) >= split_sums(48) + 4 * 32 * SG * 4,
+              "the epilogue's areas fit in the stages");
+
+template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int parts) {
+    auto kernel = split_kernel<MODE, ACT>;
+    // of shared memory: two CTAs to an SM, or all where there are fewer CTAs than SMs (clusters of 8 with an SM
+    // each do not fill the GPU: 128 CTAs of 2048 columns take 11.8 us so, two to an SM 7.5)
+    constexpr int all = 229376, half = 114688;
+    const int64_t ctas = static_cast<int64_t>((g.p.J + 127) / 128) * mt * parts;
+    const int most = parts < 8 && ctas * 10 <= sm_count() * 9 ? all : half;
+    static int configured_for = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_for != dev) {
+        const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), all);
+        if (rc != MOE_OK) return rc;
+        configured_for = dev;
+    }
+    SplitParams sp;
+    sp.r = g.p;
+    sp.parts = parts;
+    sp.mt = mt;
+    sp.box = ((g.p.rows + 15) / 16 + mt - 1) / mt * 16;
+    sp.tmem = sp.box <= 32 ? 32 : sp.box <= 64 ? 64 : 128;
+    const int rest = static_cast<int>(sizeof(SplitTail));
+    const int stage = OPER + sp.box * 128;
+    sp.stages = (most - rest) / stage;  // 3 at least
+    if (sp.stages > SPLIT_MAX_STAGES) sp.stages = SPLIT_MAX_STAGES;
+    sp.tail_at = sp.stages * stage;
+    Maps m;
+    int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, 1, 64, MODE == ROWS_FWD ? 128 : 64);
+    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, g.p.rows, g.p.C, sp.box, g.act);
+    if (rc != MOE_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = parts;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((g.p.J + 127) / 128) * mt * parts);
+    cfg.blockDim = dim3(SPLIT_THREADS);
+    cfg.dynamicSmemBytes = sp.tail_at + rest;
+    cfg.stream = g.st;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, sp);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", g.who, cudaGetErrorString(e));
+    count_launch();
+    return check_launch(g.who);
+}
+
+}  // namespace
+}  // namespace ragged
+}  // namespace moe

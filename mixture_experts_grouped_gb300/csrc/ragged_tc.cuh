@@ -64,9 +64,9 @@ struct Tail {
 
 // Shared memory: the ring of stages, tails, staging areas. The gradient's bound by its own
 // bytes where it has an addend: four slots a warp then keep two loads ahead of the stores,
-// and four stages are left; otherwise two slots and five stages.
+// and four stages are left; otherwise three slots and five stages.
 template <int MODE, int KIND> struct Shape {
-    static constexpr int SLOTS = MODE != WGRAD ? 0 : KIND == GADD ? 4 : 2;
+    static constexpr int SLOTS = MODE != WGRAD ? 0 : KIND == GADD ? 4 : 3;
     static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;
     static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : 32 * SG * 4;
     static constexpr int TBUF_AT = STAGES * STAGE;
@@ -102,12 +102,22 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src
                  : "memory");
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// all but this thread's last group have read their shared memory
-__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// all but this thread's last two groups have read their shared memory
+__device__ __forceinline__ void store_wait_read2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // mbar_wait_warp, with an acquire of what the other CTA released to it
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+    const uint32_t a = smem_u32(bar);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
     if (!mbar_wait_warp(bar, parity, w)) return false;
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     return true;
@@ -266,10 +276,26 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
 
 // A tensor core's f32 sums are cut, not rounded, to 24 bits at each step of 16 products:
 // where sums grow steadily, 30000 rows in one accumulator left them 4e-5 short. An f32
-// gradient therefore takes its rows in chunks of 4096 (5e-6), one accumulator each, and
-// the epilogue adds the chunks in f32, through dw itself. (16-bit gradients are rounded
-// to 2^-9 or 2^-12 anyway and take one.)
+// gradient therefore takes its rows in chunks of 4096 (5e-6) and adds the chunks in f32:
+// the first stays in its accumulator, the others come into the second one and are added to
+// it, the last one on its way out. (16-bit gradients are rounded to 2^-9 or 2^-12 anyway.)
 constexpr int CHUNK = 64;  // blocks
+
+// adds the accumulator at tb to the one at ta (this warp's lanes)
+__device__ __forceinline__ void fold(uint32_t ta, uint32_t tb) {
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 32) {
+        uint32_t u[32], v[32];
+        tmem_ld32(ta + c, u);
+        tmem_ld32(tb + c, v);
+        tmem_ld_wait_regs(u);
+        tmem_ld_wait_regs(v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(v[j]));
+        tmem_st32(ta + c, u);
+    }
+    tmem_st_wait();
+}
 
 // Gradient form: lane = row n of dw, columns k. A step is 128 bytes of each row (32 f32 or
 // 64 16-bit values): they are laid into one of the warp's slots, 16-byte pieces swizzled by
@@ -309,48 +335,38 @@ __device__ __forceinline__ uint4 pack_piece(const float* v) {
                       Act<ACT>::pack2(v[6], v[7]));
 }
 
-// 32 columns of the accumulator, or zeros of an empty group
-__device__ __forceinline__ void load_sums(uint32_t ta, bool any, float (&v)[32]) {
-    if (any) {
-        uint32_t u[32];
-        tmem_ld32(ta, u);
-        tmem_ld_wait_regs(u);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-    } else {
+// 32 columns of the sums: none of an empty group, of one accumulator or of two
+__device__ __forceinline__ void load_sums(uint32_t ta, uint32_t tb, int accs, float (&v)[32]) {
+    if (accs == 0) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        return;
+    }
+    uint32_t u[32];
+    tmem_ld32(ta, u);
+    tmem_ld_wait_regs(u);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+    if (accs > 1) {
+        tmem_ld32(tb, u);
+        tmem_ld_wait_regs(u);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(u[j]);
     }
 }
 
-// One chunk of a tile. `alone`: the tile's only one. Returns false if a wait gave up.
+// A tile's sums, in the accumulator at ta and, with accs 2, the one at tb. Returns false if a wait gave up.
 template <int ACT, int KIND>
 __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, const RaggedParams& p,
                                                const CUtensorMap* tm_out, const CUtensorMap* tm_add, uint32_t ta,
-                                               const Tile& t, int n_off, int lane, bool first, bool alone, int n_tiles,
+                                               uint32_t tb, int accs, const Tile& t, int n_off, int lane, int n_tiles,
                                                int step, const WaitCtx& wc) {
     constexpr int COLS = Slots<KIND>::COLS, N = Slots<KIND>::N;
-    const int n = t.j0 + n_off + lane, cols = tile_cols(p, t);
-    float* row = static_cast<float*>(p.out) + (static_cast<size_t>(t.e) * p.J + n) * p.C + t.k0;
+    const int cols = tile_cols(p, t);
 #pragma unroll 1
     for (int c = 0; c < cols; c += COLS) {
         float v[32];
-        load_sums(ta + c, t.rows > 0, v);
-        if (KIND != G16 && !first) {  // a later chunk: to what this thread stored itself
-            if (n < p.J)
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c + 4 * q < cols) {
-                        float4* own = reinterpret_cast<float4*>(row + c + 4 * q);
-                        float4 f = *own;
-                        f.x += v[4 * q];
-                        f.y += v[4 * q + 1];
-                        f.z += v[4 * q + 2];
-                        f.w += v[4 * q + 3];
-                        *own = f;
-                    }
-            continue;
-        }
+        load_sums(ta + c, tb + c, accs, v);
         const uint32_t i = sl.used % N;
         uint8_t* at = sl.area + i * SLOT + lane * 128;
         if (KIND == GADD) {
@@ -363,23 +379,16 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
                 v[4 * q + 2] += f.z;
                 v[4 * q + 3] += f.w;
             }
-        } else if (alone) {
-            if (lane == 0) store_wait_read1();  // the slot's last store: two slots
+        } else {
+            if (lane == 0) store_wait_read2();  // the slot's last store: three slots
             __syncwarp();
         }
         ++sl.used;
-        if (KIND != G16 && !alone) {
-            if (n < p.J)
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c + 4 * q < cols)
-                        *reinterpret_cast<float4*>(row + c + 4 * q) =
-                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else if (KIND == G16) {
+        if (KIND == G16) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<uint4*>(at + 16 * (q ^ (lane & 7))) = pack_piece<ACT>(v + 8 * q);
-            load_sums(ta + c + 32, t.rows > 0, v);
+            load_sums(ta + c + 32, tb + c + 32, accs, v);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<uint4*>(at + 16 * ((4 + q) ^ (lane & 7))) = pack_piece<ACT>(v + 8 * q);
@@ -392,10 +401,10 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (alone && t.j0 + n_off < p.J) store_3d(tm_out, sl.area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
+            if (t.j0 + n_off < p.J) store_3d(tm_out, sl.area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
             store_commit();  // one group a step, empty or not
             if (KIND == GADD) {
-                store_wait_read1();  // the step before: its slot is the next but one but one
+                store_wait_read2();  // the step before the last: the step after the next takes its slot
                 load_addend<KIND>(sl, s, p, tm_add, n_tiles, step, n_off);
             }
         }
@@ -535,21 +544,19 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             const uint32_t major = MODE == WGRAD ? kMajorA | kMajorB : MODE == ROWS_BACK ? kMajorA : 0u;
             constexpr uint32_t STEP_K = 32 >> 4, STEP_MN = 2048 >> 4;  // 16 contraction indices on, in descriptor units
             constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
-            uint32_t stage = 0, phase = 0, tails = 0;
-            int local = 0;
+            uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
             bool ok = true;
             for (int tile = first; tile < n_tiles && ok; tile += step) {
                 const Tile t = get_tile<MODE>(s, p, tile);
                 const int nb = blocks_of(t), chunks = chunks_of(t);
                 const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
                 for (int ch = 0; ch < chunks && ok; ++ch) {
-                    const int acc = local & 1;
-                    const uint32_t aph = (local >> 1) & 1;
-                    ++local;
-                    if (!mbar_wait_warp(&s.tempty[acc], aph ^ 1, wc)) {
+                    const uint32_t acc = ch == 0 ? cur : cur ^ 1u;  // (later chunks: the other one)
+                    if (!mbar_wait_warp(&s.tempty[acc], (uses >> acc & 1u) ^ 1u, wc)) {
                         ok = false;
                         break;
                     }
+                    uses ^= 1u << acc;
                     tc_fence_after();
                     const uint32_t d = tmem + acc * 256;
                     const int b0 = CHUNKED ? ch * CHUNK : 0, b1 = CHUNKED ? min(nb, b0 + CHUNK) : nb;
@@ -595,6 +602,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     if (elect_one()) tc_commit_pair(&s.tfull[acc], 0x3);
                     __syncwarp();
                 }
+                if (chunks == 1) cur ^= 1u;
             }
             if (elect_one()) tc_commit_pair(&s.mma_done, 0x1);
             __syncwarp();
@@ -651,33 +659,47 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             if (KIND == GADD && lane == 0)
                 for (int i = 0; i < 2; ++i) load_addend(sl, s, p, &tm_add, n_tiles, step, n_off);
         }
-        int local = 0;
-        bool ok = true;
-        for (int tile = first; tile < n_tiles && ok; tile += step) {
+        uint32_t cur = 0, uses = 0;
+        auto wait_full = [&](uint32_t acc) {
+            if (!mbar_wait_warp(&s.tfull[acc], uses >> acc & 1u, wc)) return false;
+            uses ^= 1u << acc;
+            tc_fence_after();
+            return true;
+        };
+        auto release = [&](uint32_t acc) {
+            if (lane != 0) return;
+            if (rank == 0) mbar_arrive(&s.tempty[acc]);
+            else mbar_arrive_cluster(lead_tempty + acc * 8);
+        };
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        for (int tile = first; tile < n_tiles; tile += step) {
             const Tile t = get_tile<MODE>(s, p, tile);
             const int chunks = chunks_of(t);
-            for (int ch = 0; ch < chunks && ok; ++ch) {
-                const int acc = local & 1;
-                const uint32_t aph = (local >> 1) & 1;
-                ++local;
-                if (!mbar_wait_warp(&s.tfull[acc], aph, wc)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-                if constexpr (MODE == WGRAD)
-                    ok = wgrad_epilogue<ACT, KIND>(sl, s, p, &tm_out, &tm_add, ta, t, n_off, lane, ch == 0, chunks == 1,
-                                                   n_tiles, step, wc);
-                else
-                    rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, lane);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive(&s.tempty[acc]);
-                    else mbar_arrive_cluster(lead_tempty + acc * 8);
+            if (!wait_full(cur)) break;
+            const uint32_t ta = lanes + cur * 256, tb = lanes + (cur ^ 1u) * 256;
+            bool ok = true;
+            for (int ch = 1; ch < chunks && ok; ++ch) {
+                ok = wait_full(cur ^ 1u);
+                if (ok && ch + 1 < chunks) {
+                    fold(ta, tb);
+                    tc_fence_before();
+                    __syncwarp();
+                    release(cur ^ 1u);
                 }
             }
+            if (!ok) break;
+            if constexpr (MODE == WGRAD) {
+                if (!wgrad_epilogue<ACT, KIND>(sl, s, p, &tm_out, &tm_add, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
+                                               n_off, lane, n_tiles, step, wc))
+                    break;
+            } else {
+                rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, lane);
+            }
+            tc_fence_before();
+            __syncwarp();
+            release(cur);
+            if (chunks > 1) release(cur ^ 1u);
+            else cur ^= 1u;
         }
         if constexpr (MODE == WGRAD) {
             if (lane == 0) {
@@ -744,13 +766,9 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
     return check_launch(who);
 }
 
-template <int ACT, int MODE> int rows_form(const RaggedArgs& g) {
+template <int MODE, int ACT> int launch_rows_form(const RaggedArgs& g, int maxu) {
     RaggedParams p = g.p;
-    // rows a group has, if all have the same
-    const int64_t each = (static_cast<int64_t>(p.rows) + p.E - 1) / p.E;
-    const int units = static_cast<int>((each + 15) / 16 < 16 ? (each + 15) / 16 : 16);
-    p.maxu = 1;
-    while (p.maxu < units) p.maxu *= 2;
+    p.maxu = maxu;
     Maps m;
     int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, p.rows, p.C, p.maxu * 8, g.act);
