@@ -6,12 +6,28 @@
 
 namespace moe {
 
+// x / d of 0 <= x < 2^31 by a multiplication (m = floor(2^(31 + s) / d) + 1, 2^s >= d: the quotient's error
+// stays below x / 2^31 steps of 1 / d)
+struct FastDiv {
+    uint32_t m, s, d;
+    void set(uint32_t div) {
+        d = div;
+        s = 0;
+        while ((1ull << s) < div) ++s;
+        m = static_cast<uint32_t>((1ull << (31 + s)) / div + 1);
+    }
+    __device__ __forceinline__ int div(int x) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * m) >> (31 + s));
+    }
+};
+
 // rows form: out[r, j] over the rows of each group; gradient form: dw_e[n, k]
 struct RaggedParams {
     const int32_t* offsets;  // [E + 1], or NULL: one group of all rows
     int rows, E;
     int J, C;                // rows form: output columns, contraction; gradient form: n, k
-    int maxu;                // rows form: most units of 16 rows a tile has; gradient form: k columns a tile has
+    int maxu;                // rows form: most units of 16 rows a tile has
+    FastDiv kt, per;         // gradient form: tiles of a row of tiles, and of a group
     void* out;
     const uint16_t *bias, *residual;  // rows form
     uint16_t* pre;

@@ -40,18 +40,6 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c
     tma_load_3d(dst, map, c0, c1, c2, bar);
 }
 
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(SPLIT_THREADS)
 split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const SplitParams sp) {
@@ -157,18 +145,18 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const float bias = epi ? bias_of<ACT>(p, j0 + me) : 0.0f;
     // the epilogue's areas lie where the stages were: the sums of all parts, then staging
     const int sum_bytes = parts > 1 ? parts * ((n / 4 + parts - 1) / parts) * 2048 : 0;  // (slices may differ by 4 rows)
-    float* stg = reinterpret_cast<float*>(smem + sum_bytes + (warp - 2) * (32 * SG * 4));
+    float* stg = reinterpret_cast<float*>(smem + sum_bytes + (warp - 2) * (STG_ROWS * SG * 4));
     // *abort_flag: a wait gave up here, and what was summed is not whole (the others learn it from err alone)
     if (parts == 1) {
         if (epi && ok)
 #pragma unroll 1
-            for (int c = 0; c < rows; c += 32) {
-                uint32_t u[32];
-                float v[32];
-                tmem_ld32(ta + c, u);
-                tmem_ld_wait_regs(u);
+            for (int c = 0; c < rows; c += 16) {
+                uint32_t u[16];
+                float v[16];
+                tmem_ld16(ta + c, u);
+                tmem_ld16_wait(u);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]) + bias;
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]) + bias;
                 store_rows<ACT>(p, v, stg, lane, m0 + c, rows - c, j0 + 32 * q);
             }
     } else {
@@ -185,7 +173,8 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 #pragma unroll 1
             for (int c = 0; c < n; c += 16) {
                 uint32_t u[16];
-                tmem_ld16_wait(ta + c, u);
+                tmem_ld16(ta + c, u);
+                tmem_ld16_wait(u);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int f = c / 4 + j;
@@ -206,10 +195,10 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int q0 = quads * part / parts, per = quads * (part + 1) / parts - q0;
             const int have = min(4 * per, rows - 4 * q0);
 #pragma unroll 1
-            for (int c = 0; c < have; c += 32) {
-                float v[32];
+            for (int c = 0; c < have; c += 16) {
+                float v[16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (c + 4 * j < have) {
                         const float4* src = sums + (c / 4 + j) * 128 + me;
@@ -240,9 +229,9 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 // Three stages hold the sums (2048 bytes for four rows of each part, the largest slice counting for all) and the
 // staging areas: of 128 rows as of 16.
 constexpr int split_sums(int n) { return SPLIT_PARTS * ((n / 4 + SPLIT_PARTS - 1) / SPLIT_PARTS) * 2048; }
-static_assert(3 * (OPER + SPLIT_ROWS * 128) >= split_sums(SPLIT_ROWS) + 4 * 32 * SG * 4 &&
-                  3 * (OPER + 16 * 128) >= split_sums(16) + 4 * 32 * SG * 4 &&
-                  3 * (OPER + 48 * 128) >= split_sums(48) + 4 * 32 * SG * 4,
+static_assert(3 * (OPER + SPLIT_ROWS * 128) >= split_sums(SPLIT_ROWS) + 4 * STG_ROWS * SG * 4 &&
+                  3 * (OPER + 16 * 128) >= split_sums(16) + 4 * STG_ROWS * SG * 4 &&
+                  3 * (OPER + 48 * 128) >= split_sums(48) + 4 * STG_ROWS * SG * 4,
               "the epilogue's areas fit in the stages");
 
 template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int parts) {

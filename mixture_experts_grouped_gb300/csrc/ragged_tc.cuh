@@ -23,7 +23,8 @@
 //   divides).
 //
 // Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
-// CTA (the leader) issues the MMAs, warps 2 to 5 are the epilogue, warp 7 makes the tails.
+// CTA (the leader) issues the MMAs, warps 2 to 5 and 8 to 11 are the epilogue, warp 7
+// makes the tails.
 // Two accumulators of 256 TMEM columns let the epilogue of a tile run beside the next
 // one's MMAs. The issuing warps run their loops whole and elect a lane for the MMAs and
 // copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
@@ -45,7 +46,7 @@ constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
 constexpr int STAGE = 2 * OPER;
 constexpr int MAX_STAGES = 6;
-constexpr int THREADS = 256;
+constexpr int STG_ROWS = 16;  // rows form: rows of a warp's staging area
 constexpr int SG = 36;  // rows form: row stride (floats) of a warp's staging area, 16-byte reads without conflicts
 constexpr int UNIT = 64 * 16 * 2;             // gradient form: 64 columns of a unit of 16 rows
 constexpr int TBUF = 4 * UNIT, TBUFS = 2;     // a tail of both operands
@@ -62,16 +63,21 @@ struct Tail {
     int tstart[MOE_MAX_EXPERTS + 1];
 };
 
-// Shared memory: the ring of stages, tails, staging areas. The gradient's bound by its own
-// bytes where it has an addend: four slots a warp then keep two loads ahead of the stores,
-// and four stages are left; otherwise three slots and five stages.
+// Epilogue warps, and shared memory: the ring of stages, tails, staging areas. Eight
+// warps finish a tile, two to a quarter of the TMEM lanes, which take its steps in turn. A
+// gradient with an addend is bound by their bytes: four warps with four slots each, so that
+// two steps' addends are on their way, and four stages. Other gradients have a slot a warp
+// and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four).
 template <int MODE, int KIND> struct Shape {
-    static constexpr int SLOTS = MODE != WGRAD ? 0 : KIND == GADD ? 4 : 3;
+    static constexpr int HALVES = KIND == GADD ? 1 : 2;  // warps to a quarter
+    static constexpr int WARPS = 4 * HALVES;
+    static constexpr int THREADS = 256 + 128 * (HALVES - 1);
+    static constexpr int SLOTS = KIND == GADD ? 4 : 1;
     static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;
-    static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : 32 * SG * 4;
+    static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG_ROWS * SG * 4;
     static constexpr int TBUF_AT = STAGES * STAGE;
     static constexpr int STG_AT = TBUF_AT + (MODE == WGRAD ? TBUFS * TBUF : 0);
-    static constexpr int TAIL_AT = STG_AT + 4 * STG_WARP;
+    static constexpr int TAIL_AT = STG_AT + WARPS * STG_WARP;
     static constexpr int SMEM = TAIL_AT + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
     static_assert(SMEM <= 232448, "shared memory over the limit");
 };
@@ -102,6 +108,7 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src
                  : "memory");
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // all but this thread's last two groups have read their shared memory
 __device__ __forceinline__ void store_wait_read2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
@@ -146,7 +153,7 @@ struct Tile {
 template <int MODE>
 __device__ __forceinline__ int build_tiles(Tail& s, const RaggedParams& p) {
     const int tid = threadIdx.x, lane = tid & 31, E = p.E;
-    for (int i = tid; i <= E; i += THREADS) s.off[i] = p.offsets ? p.offsets[i] : (i ? p.rows : 0);
+    for (int i = tid; i <= E; i += blockDim.x) s.off[i] = p.offsets ? p.offsets[i] : (i ? p.rows : 0);
     const int jt = (p.J + 255) / 256;
     if (tid == 0) {
         s.abort_flag = 0;
@@ -154,11 +161,11 @@ __device__ __forceinline__ int build_tiles(Tail& s, const RaggedParams& p) {
     }
     __syncthreads();
     int bad = 0;
-    for (int i = tid; i < E; i += THREADS) bad |= s.off[i + 1] < s.off[i];
+    for (int i = tid; i < E; i += blockDim.x) bad |= s.off[i + 1] < s.off[i];
     if (tid == 0) bad |= s.off[0] < 0 || s.off[E] > p.rows;
     bad = __syncthreads_or(bad);
     if (MODE == WGRAD) {
-        if (tid == 0) s.n_tiles = bad ? 0 : E * jt * ((p.C + p.maxu - 1) / p.maxu);
+        if (tid == 0) s.n_tiles = bad ? 0 : E * static_cast<int>(p.per.d);
         return bad;
     }
     if (tid < 32) {
@@ -188,14 +195,13 @@ __device__ __forceinline__ int build_tiles(Tail& s, const RaggedParams& p) {
 template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, const RaggedParams& p, int tile) {
     Tile t;
     if (MODE == WGRAD) {
-        const int kt = (p.C + p.maxu - 1) / p.maxu, per = s.jt * kt;
-        t.e = tile / per;
-        const int in = tile - t.e * per, jn = in / kt;
+        t.e = p.per.div(tile);
+        const int in = tile - t.e * static_cast<int>(p.per.d), jn = p.kt.div(in);
         t.j0 = jn * 256;
-        t.k0 = (in - jn * kt) * p.maxu;
+        t.k0 = (in - jn * static_cast<int>(p.kt.d)) * 256;
         t.m0 = s.off[t.e];
         t.rows = s.off[t.e + 1] - t.m0;
-        t.n = p.maxu;
+        t.n = 256;
         return t;
     }
     int lo = 0, hi = p.E - 1;
@@ -207,11 +213,11 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
     t.e = lo;
     const int v = s.off[lo + 1] - s.off[lo], U = (v + 15) / 16, mt = (U + p.maxu - 1) / p.maxu;
     const int local = tile - s.tstart[lo], jn = local / mt, i = local - jn * mt;
-    const int u0 = static_cast<int>(static_cast<int64_t>(U) * i / mt),
-              u1 = static_cast<int>(static_cast<int64_t>(U) * (i + 1) / mt);
+    const int least = U / mt, u0 = i * least + min(i, U - mt * least);  // the first tiles take a unit more
+    const int units = least + (i < U - mt * least);
     t.m0 = s.off[lo] + 16 * u0;
-    t.rows = min(v, 16 * u1) - 16 * u0;
-    t.n = 16 * (u1 - u0);
+    t.rows = min(v - 16 * u0, 16 * units);
+    t.n = 16 * units;
     t.j0 = jn * 256;
     t.k0 = 0;
     return t;
@@ -219,17 +225,17 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
 
 // ---- epilogues --------------------------------------------------------------------------
 
-// Rows form: up to 32 rows x 32 columns z (lane = column, v[i] = row m + i) of a warp to
+// Rows form: up to 16 rows x 32 columns z (lane = column, v[i] = row m + i) of a warp to
 // memory, through its staging area so that they leave as 16-byte pieces of 8 columns; the
 // piece's activation function and residual are applied on the way, in f32.
 template <int ACT>
-__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[32], float* stg, int lane, int m,
+__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[16], float* stg, int lane, int m,
                                            int rows, int col0) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) stg[i * SG + lane] = v[i];
+    for (int i = 0; i < 16; ++i) stg[i * SG + lane] = v[i];
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int r = (i * 32 + lane) >> 2, col = col0 + 8 * (lane & 3);
         if (r >= rows || col >= p.J) continue;
         const float4 lo = *reinterpret_cast<const float4*>(stg + r * SG + 8 * (lane & 3));
@@ -251,6 +257,21 @@ __device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&
     __syncwarp();
 }
 
+// 16 columns of the accumulator
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 template <int ACT>
 __device__ __forceinline__ float bias_of(const RaggedParams& p, int col) {
     if (!p.bias || col >= p.J) return 0.0f;
@@ -259,17 +280,17 @@ __device__ __forceinline__ float bias_of(const RaggedParams& p, int col) {
 
 template <int ACT>
 __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta, float* stg, const Tile& t, int col0,
-                                              int lane) {
+                                              int half, int lane) {
     const float b = bias_of<ACT>(p, col0 + lane);
-    uint32_t nx[32];
-    tmem_ld32(ta, nx);
+    uint32_t nx[16];
+    if (16 * half < t.rows) tmem_ld16(ta + 16 * half, nx);
 #pragma unroll 1
-    for (int c = 0; c < t.rows; c += 32) {
-        float v[32];
-        tmem_ld_wait_regs(nx);
+    for (int c = 16 * half; c < t.rows; c += 32) {
+        float v[16];
+        tmem_ld16_wait(nx);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(nx[j]) + b;
-        if (c + 32 < t.rows) tmem_ld32(ta + c + 32, nx);  // in flight while this one is stored
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(nx[j]) + b;
+        if (c + 32 < t.rows) tmem_ld16(ta + c + 32, nx);  // in flight while this one is stored
         store_rows<ACT>(p, v, stg, lane, t.m0 + c, t.rows - c, col0);
     }
 }
@@ -281,10 +302,10 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
 // it, the last one on its way out. (16-bit gradients are rounded to 2^-9 or 2^-12 anyway.)
 constexpr int CHUNK = 64;  // blocks
 
-// adds the accumulator at tb to the one at ta (this warp's lanes)
-__device__ __forceinline__ void fold(uint32_t ta, uint32_t tb) {
+// adds the accumulator at tb to the one at ta (this warp's lanes and steps of 32 columns)
+template <int STRIDE> __device__ __forceinline__ void fold(uint32_t ta, uint32_t tb, int first) {
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 32) {
+    for (int c = first; c < 256; c += STRIDE) {
         uint32_t u[32], v[32];
         tmem_ld32(ta + c, u);
         tmem_ld32(tb + c, v);
@@ -308,22 +329,23 @@ template <int KIND> struct Slots {
     uint64_t* bar;
     uint32_t used = 0;    // steps done
     uint32_t loaded = 0;  // steps whose addend was asked for
-    int tile = 0, c = 0;  // the next such step
+    int tile = 0, c = 0;  // the next such step, c its column in the tile
+    Tile t;
 };
 
-__device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(p.maxu, p.C - t.k0); }
+__device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(256, p.C - t.k0); }
 
 // asks for the next step's addend, if there is one (one lane; the slot's last store has been read)
 template <int KIND>
 __device__ __forceinline__ void load_addend(Slots<KIND>& sl, const Tail& s, const RaggedParams& p, const CUtensorMap* tm,
                                             int n_tiles, int step, int n_off) {
     if (sl.tile >= n_tiles) return;
-    const Tile t = get_tile<WGRAD>(s, p, sl.tile);
+    if (sl.c == 0) sl.t = get_tile<WGRAD>(s, p, sl.tile);
     const uint32_t i = sl.loaded++ % Slots<KIND>::N;
     mbar_arrive_expect_tx(sl.bar + i, SLOT);
-    tma_load_3d(sl.area + i * SLOT, tm, t.k0 + sl.c, t.j0 + n_off, t.e, sl.bar + i);
+    tma_load_3d(sl.area + i * SLOT, tm, sl.t.k0 + sl.c, sl.t.j0 + n_off, sl.t.e, sl.bar + i);
     sl.c += Slots<KIND>::COLS;
-    if (sl.c >= tile_cols(p, t)) {
+    if (sl.c >= tile_cols(p, sl.t)) {
         sl.c = 0;
         sl.tile += step;
     }
@@ -359,12 +381,12 @@ __device__ __forceinline__ void load_sums(uint32_t ta, uint32_t tb, int accs, fl
 template <int ACT, int KIND>
 __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, const RaggedParams& p,
                                                const CUtensorMap* tm_out, const CUtensorMap* tm_add, uint32_t ta,
-                                               uint32_t tb, int accs, const Tile& t, int n_off, int lane, int n_tiles,
-                                               int step, const WaitCtx& wc) {
-    constexpr int COLS = Slots<KIND>::COLS, N = Slots<KIND>::N;
+                                               uint32_t tb, int accs, const Tile& t, int n_off, int half, int lane,
+                                               int n_tiles, int step, const WaitCtx& wc) {
+    constexpr int COLS = Slots<KIND>::COLS, N = Slots<KIND>::N, HALVES = Shape<WGRAD, KIND>::HALVES;
     const int cols = tile_cols(p, t);
 #pragma unroll 1
-    for (int c = 0; c < cols; c += COLS) {
+    for (int c = half * COLS; c < cols; c += HALVES * COLS) {
         float v[32];
         load_sums(ta + c, tb + c, accs, v);
         const uint32_t i = sl.used % N;
@@ -380,7 +402,7 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
                 v[4 * q + 3] += f.w;
             }
         } else {
-            if (lane == 0) store_wait_read2();  // the slot's last store: three slots
+            if (lane == 0) store_wait_read();  // the slot's last store
             __syncwarp();
         }
         ++sl.used;
@@ -416,7 +438,7 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
 // tm_a: the M operand (weights; dy), tm_b: the N operand (rows; x). Gradient form: tm_ta and
 // tm_tb are those in boxes of a unit, tm_out and tm_add the gradient and its addend.
 template <int MODE, int ACT, int KIND>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Shape<MODE, KIND>::THREADS, 1)
 ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ CUtensorMap tm_ta, const __grid_constant__ CUtensorMap tm_tb,
               const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_add,
@@ -445,7 +467,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.tfull[i], 1);
-            mbar_init(&s.tempty[i], 8);  // the pair's epilogue warps
+            mbar_init(&s.tempty[i], 2 * S::WARPS);  // the pair's epilogue warps
         }
         for (int i = 0; i < 16; ++i) mbar_init(&s.slot[i >> 2][i & 3], 1);
         mbar_init(&s.mma_done, 1);
@@ -477,7 +499,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
     const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), 0);
     const int KB = (p.C + BK - 1) / BK;
-    const uint32_t b_bytes = MODE == WGRAD ? p.maxu * 64 : p.maxu * 8 * 128;  // this CTA's, of the N operand
+    const uint32_t b_bytes = MODE == WGRAD ? OPER : p.maxu * 8 * 128;  // this CTA's, of the N operand
     // blocks of a tile; of a gradient, those that its whole units of 16 rows fill
     auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows / 16 + 3) / 4 : KB; };
     auto chunks_of = [&](const Tile& t) { return CHUNKED ? max(1, (blocks_of(t) + CHUNK - 1) / CHUNK) : 1; };
@@ -507,9 +529,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                             tma_load_2d_pair(dst, &tm_a, n, r, bar);
                             tma_load_2d_pair(dst + 8192, &tm_a, n + 64, r, bar);
                         } else {
-                            const int k = t.k0 + p.maxu / 2 * static_cast<int>(rank);
+                            const int k = t.k0 + 128 * static_cast<int>(rank);
                             tma_load_2d_pair(dst, &tm_b, k, r, bar);
-                            if (p.maxu == 256) tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
+                            tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
                         }
                     } else {
                         const int c = b * BK;
@@ -546,8 +568,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
             uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
             bool ok = true;
+            Tile next = get_tile<MODE>(s, p, first);
             for (int tile = first; tile < n_tiles && ok; tile += step) {
-                const Tile t = get_tile<MODE>(s, p, tile);
+                const Tile t = next;
                 const int nb = blocks_of(t), chunks = chunks_of(t);
                 const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
                 for (int ch = 0; ch < chunks && ok; ++ch) {
@@ -584,6 +607,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                         }
                     }
                     if (!ok) break;
+                    // (found while the MMAs run: it would hold up the next tile's)
+                    if (ch + 1 == chunks && tile + step < n_tiles) next = get_tile<MODE>(s, p, tile + step);
                     if (MODE == WGRAD && ch + 1 == chunks && t.rows % 16 != 0) {
                         const uint32_t tb = tails % TBUFS;
                         if (!wait_cluster(&s.tready[tb], (tails / TBUFS) & 1u, wc)) {
@@ -622,12 +647,12 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 uint8_t* buf = smem + S::TBUF_AT + tb * TBUF;
                 if (elect_one()) {
                     const int r = t.m0 + t.rows - left;
-                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + p.maxu / 2 * static_cast<int>(rank);
-                    mbar_arrive_expect_tx(&s.tloc[tb], p.maxu == 256 ? 4 * UNIT : 3 * UNIT);
+                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + 128 * static_cast<int>(rank);
+                    mbar_arrive_expect_tx(&s.tloc[tb], 4 * UNIT);
                     tma_load_2d(buf, &tm_ta, n, r, &s.tloc[tb]);
                     tma_load_2d(buf + UNIT, &tm_ta, n + 64, r, &s.tloc[tb]);
                     tma_load_2d(buf + 2 * UNIT, &tm_tb, k, r, &s.tloc[tb]);
-                    if (p.maxu == 256) tma_load_2d(buf + 3 * UNIT, &tm_tb, k + 64, r, &s.tloc[tb]);
+                    tma_load_2d(buf + 3 * UNIT, &tm_tb, k + 64, r, &s.tloc[tb]);
                 }
                 __syncwarp();
                 if (!mbar_wait_warp(&s.tloc[tb], ph, wc)) {
@@ -649,12 +674,13 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     } else {
         // ---------------- epilogue ----------------
         const int q = warp & 3;  // TMEM lane quarter
+        const int half = warp >= 8, ew = half ? warp - 4 : warp - 2;  // which of its two warps, and of all
         const int n_off = 128 * static_cast<int>(rank) + 32 * q;
-        uint8_t* stg = smem + S::STG_AT + (warp - 2) * S::STG_WARP;
-        [[maybe_unused]] Slots<MODE == WGRAD ? KIND : G16> sl;
+        uint8_t* stg = smem + S::STG_AT + ew * S::STG_WARP;
+        [[maybe_unused]] Slots<KIND> sl;
         if (MODE == WGRAD) {
             sl.area = stg;
-            sl.bar = s.slot[warp - 2];
+            sl.bar = s.slot[ew];
             sl.tile = first;
             if (KIND == GADD && lane == 0)
                 for (int i = 0; i < 2; ++i) load_addend(sl, s, p, &tm_add, n_tiles, step, n_off);
@@ -681,7 +707,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             for (int ch = 1; ch < chunks && ok; ++ch) {
                 ok = wait_full(cur ^ 1u);
                 if (ok && ch + 1 < chunks) {
-                    fold(ta, tb);
+                    fold<32 * S::HALVES>(ta, tb, 32 * half);
                     tc_fence_before();
                     __syncwarp();
                     release(cur ^ 1u);
@@ -690,10 +716,10 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             if (!ok) break;
             if constexpr (MODE == WGRAD) {
                 if (!wgrad_epilogue<ACT, KIND>(sl, s, p, &tm_out, &tm_add, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
-                                               n_off, lane, n_tiles, step, wc))
+                                               n_off, half, lane, n_tiles, step, wc))
                     break;
             } else {
-                rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, lane);
+                rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, half, lane);
             }
             tc_fence_before();
             __syncwarp();
@@ -737,7 +763,7 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Shape<MODE, KIND>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

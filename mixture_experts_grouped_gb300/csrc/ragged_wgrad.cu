@@ -7,7 +7,11 @@ namespace {
 
 template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
     RaggedParams p = g.p;
-    p.maxu = 256;
+    const int nt = (p.J + 255) / 256, kt = (p.C + 255) / 256;
+    const int64_t tiles = static_cast<int64_t>(p.E) * nt * kt;
+    if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", g.who);
+    p.kt.set(kt);
+    p.per.set(nt * kt);
     Maps m;
     // of no rows, any address serves the maps: no copy is made
     const void* dy = p.rows ? g.a : p.out;
@@ -24,7 +28,6 @@ template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
     if (rc == MOE_OK && KIND == GADD)
         rc = make_tmap_3d(&m.add, const_cast<float*>(p.addend), out, p.C, p.J, p.E, cols, 32);
     if (rc != MOE_OK) return rc;
-    const int64_t tiles = static_cast<int64_t>(p.E) * ((p.J + 255) / 256) * ((p.C + p.maxu - 1) / p.maxu);
     return launch<WGRAD, ACT, KIND>(m, p, tiles, g.st, g.who);
 }
 
