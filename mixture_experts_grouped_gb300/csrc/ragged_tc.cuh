@@ -23,8 +23,8 @@
 //   divides).
 //
 // Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
-// CTA (the leader) issues the MMAs, warps 2 to 5 and 8 to 11 are the epilogue, warp 7
-// makes the tails.
+// CTA (the leader) issues the MMAs, warps 2 to 5 and 8 to 11 are the epilogue (with an
+// addend the latter copy for the former), warp 7 makes the tails.
 // Two accumulators of 256 TMEM columns let the epilogue of a tile run beside the next
 // one's MMAs. The issuing warps run their loops whole and elect a lane for the MMAs and
 // copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
@@ -56,7 +56,7 @@ struct Tail {
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t tloc[TBUFS], tready[TBUFS], tfree[TBUFS];  // tails: copied (this CTA's), cleared (both CTAs'), used
     uint64_t tfull[2], tempty[2], mma_done;
-    uint64_t slot[4][4];  // addends of a warp's slots
+    uint64_t slot[4][4], sdone[4][4];  // a warp's slots: addend there, sums there
     uint32_t tmem_base;
     int abort_flag, n_tiles, jt;
     int off[MOE_MAX_EXPERTS + 1];
@@ -66,12 +66,13 @@ struct Tail {
 // Epilogue warps, and shared memory: the ring of stages, tails, staging areas. Eight
 // warps finish a tile, two to a quarter of the TMEM lanes, which take its steps in turn. A
 // gradient with an addend is bound by their bytes: four warps with four slots each, so that
-// two steps' addends are on their way, and four stages. Other gradients have a slot a warp
+// three steps' addends are on their way, four others that load and store for them, and
+// four stages. Other gradients have a slot a warp
 // and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four).
 template <int MODE, int KIND> struct Shape {
     static constexpr int HALVES = KIND == GADD ? 1 : 2;  // warps to a quarter
     static constexpr int WARPS = 4 * HALVES;
-    static constexpr int THREADS = 256 + 128 * (HALVES - 1);
+    static constexpr int THREADS = 384;
     static constexpr int SLOTS = KIND == GADD ? 4 : 1;
     static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;
     static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG_ROWS * SG * 4;
@@ -109,8 +110,8 @@ __device__ __forceinline__ void store_3d(const CUtensorMap* map, const void* src
 }
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// all but this thread's last two groups have read their shared memory
-__device__ __forceinline__ void store_wait_read2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
+// all but this thread's last group have read their shared memory
+__device__ __forceinline__ void store_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // mbar_wait_warp, with an acquire of what the other CTA released to it
@@ -321,34 +322,68 @@ template <int STRIDE> __device__ __forceinline__ void fold(uint32_t ta, uint32_t
 // Gradient form: lane = row n of dw, columns k. A step is 128 bytes of each row (32 f32 or
 // 64 16-bit values): they are laid into one of the warp's slots, 16-byte pieces swizzled by
 // row, and leave by a TMA store, which leaves out what lies past the weight's edges. An
-// addend comes into the slot by a TMA load two steps before and is added in place.
+// addend comes into the slot by a TMA load three steps before and is added in place.
 template <int KIND> struct Slots {
     static constexpr int COLS = KIND == G16 ? 64 : 32;
     static constexpr int N = Shape<WGRAD, KIND>::SLOTS;
-    uint8_t* area;
-    uint64_t* bar;
-    uint32_t used = 0;    // steps done
-    uint32_t loaded = 0;  // steps whose addend was asked for
-    int tile = 0, c = 0;  // the next such step, c its column in the tile
-    Tile t;
 };
 
 __device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(256, p.C - t.k0); }
 
-// asks for the next step's addend, if there is one (one lane; the slot's last store has been read)
-template <int KIND>
-__device__ __forceinline__ void load_addend(Slots<KIND>& sl, const Tail& s, const RaggedParams& p, const CUtensorMap* tm,
-                                            int n_tiles, int step, int n_off) {
-    if (sl.tile >= n_tiles) return;
-    if (sl.c == 0) sl.t = get_tile<WGRAD>(s, p, sl.tile);
-    const uint32_t i = sl.loaded++ % Slots<KIND>::N;
-    mbar_arrive_expect_tx(sl.bar + i, SLOT);
-    tma_load_3d(sl.area + i * SLOT, tm, sl.t.k0 + sl.c, sl.t.j0 + n_off, sl.t.e, sl.bar + i);
-    sl.c += Slots<KIND>::COLS;
-    if (sl.c >= tile_cols(p, sl.t)) {
-        sl.c = 0;
-        sl.tile += step;
+// With an addend: the copies of one epilogue warp's slots. They are a warp of their own
+// because finding, waiting for and issuing them took as long as the sums (a step 0.9 us,
+// all by one warp).
+__device__ __forceinline__ void copy_slots(Tail& s, const RaggedParams& p, const CUtensorMap* tm_out,
+                                           const CUtensorMap* tm_add, uint8_t* area, int w, int n_off, int n_tiles,
+                                           int first, int step, int lane, const WaitCtx& wc) {
+    constexpr int N = Slots<GADD>::N, COLS = Slots<GADD>::COLS;
+    int ltile = first, lc = 0;  // the next load
+    uint32_t loaded = 0, stored = 0;
+    Tile lt = get_tile<WGRAD>(s, p, first), t = lt;
+    auto load = [&] {
+        if (ltile >= n_tiles) return;
+        const uint32_t i = loaded % N;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&s.slot[w][i], SLOT);
+            tma_load_3d(area + i * SLOT, tm_add, lt.k0 + lc, lt.j0 + n_off, lt.e, &s.slot[w][i]);
+        }
+        __syncwarp();
+        ++loaded;
+        lc += COLS;
+        if (lc >= tile_cols(p, lt)) {
+            lc = 0;
+            ltile += step;
+            if (ltile < n_tiles) lt = get_tile<WGRAD>(s, p, ltile);
+        }
+    };
+    for (int i = 0; i < N - 1; ++i) load();
+    bool ok = true;
+    for (int tile = first; tile < n_tiles && ok; tile += step) {
+        t = get_tile<WGRAD>(s, p, tile);
+        const int cols = tile_cols(p, t);
+        for (int c = 0; c < cols; c += COLS) {
+            const uint32_t i = stored % N;
+            if (!mbar_wait_warp(&s.sdone[w][i], (stored / N) & 1u, wc)) {
+                ok = false;
+                break;
+            }
+            ++stored;
+            if (lane == 0) {
+                if (t.j0 + n_off < p.J) store_3d(tm_out, area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
+                store_commit();       // one group a step, empty or not
+                store_wait_read1();   // the step before has been read: its slot takes the next load
+            }
+            __syncwarp();
+            load();
+        }
     }
+    if (lane == 0) {
+        // (loads that nobody waited for are left only after a wait that gave up)
+        for (uint32_t i = loaded > N ? loaded - N : 0; i < loaded; ++i)
+            mbar_drain(&s.slot[w][i % N], (i / N) & 1u, kWaitLimitNs / 8);
+        store_wait();
+    }
+    __syncwarp();
 }
 
 template <int ACT>
@@ -377,22 +412,22 @@ __device__ __forceinline__ void load_sums(uint32_t ta, uint32_t tb, int accs, fl
     }
 }
 
-// A tile's sums, in the accumulator at ta and, with accs 2, the one at tb. Returns false if a wait gave up.
+// A tile's sums, in the accumulator at ta and, with accs 2, the one at tb. `used` counts the
+// warp's steps. Returns false if a wait gave up.
 template <int ACT, int KIND>
-__device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, const RaggedParams& p,
-                                               const CUtensorMap* tm_out, const CUtensorMap* tm_add, uint32_t ta,
-                                               uint32_t tb, int accs, const Tile& t, int n_off, int half, int lane,
-                                               int n_tiles, int step, const WaitCtx& wc) {
+__device__ __forceinline__ bool wgrad_epilogue(Tail& s, const RaggedParams& p, const CUtensorMap* tm_out, uint8_t* area,
+                                               uint32_t& used, uint32_t ta, uint32_t tb, int accs, const Tile& t, int w,
+                                               int n_off, int half, int lane, const WaitCtx& wc) {
     constexpr int COLS = Slots<KIND>::COLS, N = Slots<KIND>::N, HALVES = Shape<WGRAD, KIND>::HALVES;
     const int cols = tile_cols(p, t);
 #pragma unroll 1
     for (int c = half * COLS; c < cols; c += HALVES * COLS) {
         float v[32];
         load_sums(ta + c, tb + c, accs, v);
-        const uint32_t i = sl.used % N;
-        uint8_t* at = sl.area + i * SLOT + lane * 128;
+        const uint32_t i = used % N;
+        uint8_t* at = area + i * SLOT + lane * 128;
         if (KIND == GADD) {
-            if (!mbar_wait_warp(sl.bar + i, (sl.used / N) & 1u, wc)) return false;
+            if (!mbar_wait_warp(&s.slot[w][i], (used / N) & 1u, wc)) return false;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float4 f = *reinterpret_cast<const float4*>(at + 16 * (q ^ (lane & 7)));
@@ -405,7 +440,7 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
             if (lane == 0) store_wait_read();  // the slot's last store
             __syncwarp();
         }
-        ++sl.used;
+        ++used;
         if (KIND == G16) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -423,11 +458,11 @@ __device__ __forceinline__ bool wgrad_epilogue(Slots<KIND>& sl, const Tail& s, c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (t.j0 + n_off < p.J) store_3d(tm_out, sl.area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
-            store_commit();  // one group a step, empty or not
             if (KIND == GADD) {
-                store_wait_read2();  // the step before the last: the step after the next takes its slot
-                load_addend<KIND>(sl, s, p, tm_add, n_tiles, step, n_off);
+                mbar_arrive(&s.sdone[w][i]);
+            } else if (t.j0 + n_off < p.J) {
+                store_3d(tm_out, area + i * SLOT, t.k0 + c, t.j0 + n_off, t.e);
+                store_commit();
             }
         }
     }
@@ -469,7 +504,10 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             mbar_init(&s.tfull[i], 1);
             mbar_init(&s.tempty[i], 2 * S::WARPS);  // the pair's epilogue warps
         }
-        for (int i = 0; i < 16; ++i) mbar_init(&s.slot[i >> 2][i & 3], 1);
+        for (int i = 0; i < 16; ++i) {
+            mbar_init(&s.slot[i >> 2][i & 3], 1);
+            mbar_init(&s.sdone[i >> 2][i & 3], 1);
+        }
         mbar_init(&s.mma_done, 1);
         fence_mbar_init();
     }
@@ -671,20 +709,20 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 __syncwarp();
             }
         }
+    } else if (MODE == WGRAD && KIND == GADD && warp >= 8) {
+        if constexpr (MODE == WGRAD && KIND == GADD) {
+            // ---------------- copies of addends and gradients, for the epilogue warp of the same quarter ----------------
+            const int q = warp & 3, w = (q + 2) & 3;  // (warps 2 to 5 have quarters 2, 3, 0, 1)
+            copy_slots(s, p, &tm_out, &tm_add, smem + S::STG_AT + w * S::STG_WARP, w,
+                       128 * static_cast<int>(rank) + 32 * q, n_tiles, first, step, lane, wc);
+        }
     } else {
         // ---------------- epilogue ----------------
         const int q = warp & 3;  // TMEM lane quarter
         const int half = warp >= 8, ew = half ? warp - 4 : warp - 2;  // which of its two warps, and of all
         const int n_off = 128 * static_cast<int>(rank) + 32 * q;
         uint8_t* stg = smem + S::STG_AT + ew * S::STG_WARP;
-        [[maybe_unused]] Slots<KIND> sl;
-        if (MODE == WGRAD) {
-            sl.area = stg;
-            sl.bar = s.slot[ew];
-            sl.tile = first;
-            if (KIND == GADD && lane == 0)
-                for (int i = 0; i < 2; ++i) load_addend(sl, s, p, &tm_add, n_tiles, step, n_off);
-        }
+        [[maybe_unused]] uint32_t used = 0;
         uint32_t cur = 0, uses = 0;
         auto wait_full = [&](uint32_t acc) {
             if (!mbar_wait_warp(&s.tfull[acc], uses >> acc & 1u, wc)) return false;
@@ -715,8 +753,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             }
             if (!ok) break;
             if constexpr (MODE == WGRAD) {
-                if (!wgrad_epilogue<ACT, KIND>(sl, s, p, &tm_out, &tm_add, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
-                                               n_off, half, lane, n_tiles, step, wc))
+                if (!wgrad_epilogue<ACT, KIND>(s, p, &tm_out, stg, used, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
+                                               ew, n_off, half, lane, wc))
                     break;
             } else {
                 rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, half, lane);
@@ -727,14 +765,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             if (chunks > 1) release(cur ^ 1u);
             else cur ^= 1u;
         }
-        if constexpr (MODE == WGRAD) {
-            if (lane == 0) {
-                if (KIND == GADD)  // (only after a wait that gave up are there any)
-                    for (uint32_t i = sl.used; i < sl.loaded; ++i)
-                        mbar_drain(sl.bar + i % Slots<KIND>::N, (i / Slots<KIND>::N) & 1u, kWaitLimitNs / 8);
-                store_wait();
-            }
-        }
+        if (MODE == WGRAD && KIND != GADD && lane == 0) store_wait();
     }
 
     __syncwarp();
