@@ -61,39 +61,56 @@ swiglu_backward_kernel(const uint4* gu, const uint4* dh, uint4* dgu, uint4* h, I
 //
 //   dz = d_out f'(pre),   d_bias[n] = sum_m dz[m, n]
 //
-// A CTA takes 64 columns (8 threads across) and every C-th group of 32 rows of a
-// cluster of C CTAs; column sums are added over the CTA's 32 row threads and then over
+// A CTA takes 8 TX columns (TX threads across) and every C-th group of 256 / TX rows of a
+// cluster of C CTAs; column sums are added over the CTA's rows of threads and then over
 // the cluster in rank order (distributed shared memory), so no workspace is needed and
-// the order depends on the sizes alone.
-constexpr int kBiasCols = 64, kBiasRows = 32;
+// the order depends on the sizes alone. TX = 32 where that fills the GPU, since HBM is kinder
+// to 512 bytes of a row than to 128 (4096 x 14336, relu: 59 us, 69 with TX = 8), else 8.
+constexpr int kBiasThreads = 256;
 
-template <int ACT>
-__global__ void __launch_bounds__(256)
-bias_act_backward_kernel(const uint16_t* d_out, const uint16_t* pre, int fn, int M, int N, uint16_t* d_pre,
+template <int ACT, int FN, int TX>
+__global__ void __launch_bounds__(kBiasThreads, 4)  // (with three CTAs an SM, clusters of 8 left SMs empty)
+bias_act_backward_kernel(const uint16_t* d_out, const uint16_t* pre, int M, int N, uint16_t* d_pre,
                          float* d_bias, int accumulate, int C) {
     pdl_wait();
+    constexpr int kBiasCols = 8 * TX, kBiasRows = kBiasThreads / TX;
     __shared__ float part[kBiasRows][kBiasCols];
     __shared__ float total[kBiasCols];
-    const int tid = threadIdx.x, cv = tid & 7, ty = tid >> 3;
+    const int tid = threadIdx.x, cv = tid % TX, ty = tid / TX;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n = blockIdx.x / C * kBiasCols + cv * 8;
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
     if (n < N) {
-#pragma unroll 4
-        for (int m = rank * kBiasRows + ty; m < M; m += C * kBiasRows) {
-            const size_t at = static_cast<size_t>(m) * N + n;
-            float d[8], z[8];
-            unpack8<ACT>(*reinterpret_cast<const uint4*>(d_out + at), d);
-            if (fn != MOE_FN_NONE) {
-                unpack8<ACT>(*reinterpret_cast<const uint4*>(pre + at), z);
+        constexpr int BATCH = 4;  // rows whose loads are in flight together (d_pre may be d_out or pre: the compiler would not)
+        const int stride = C * kBiasRows;
+        for (int m0 = rank * kBiasRows + ty; m0 < M; m0 += BATCH * stride) {
+            uint4 dv[BATCH], zv[BATCH];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] *= fn_slope(fn, z[j]);
+            for (int i = 0; i < BATCH; ++i) {
+                const size_t at = static_cast<size_t>(m0 + i * stride) * N + n;
+                dv[i] = zv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (m0 + i * stride < M) {
+                    dv[i] = *reinterpret_cast<const uint4*>(d_out + at);
+                    if (FN != MOE_FN_NONE) zv[i] = *reinterpret_cast<const uint4*>(pre + at);
+                }
             }
-            if (d_pre) *reinterpret_cast<uint4*>(d_pre + at) = pack8<ACT>(d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += d[j];
+            for (int i = 0; i < BATCH; ++i) {
+                if (m0 + i * stride >= M) break;
+                float d[8], z[8];
+                unpack8<ACT>(dv[i], d);
+                if (FN != MOE_FN_NONE) {
+                    unpack8<ACT>(zv[i], z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] *= fn_slope(FN, z[j]);
+                }
+                if (d_pre)
+                    *reinterpret_cast<uint4*>(d_pre + static_cast<size_t>(m0 + i * stride) * N + n) = pack8<ACT>(d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += d[j];
+            }
         }
     }
     if (!d_bias) return;  // (uniform: no CTA of the cluster waits)
@@ -360,10 +377,12 @@ extern "C" int moe_bias_act_backward(const void* d_out, const void* pre, int32_t
     MOE_REQUIRE(moe::aligned16(d_out) && moe::aligned16(pre) && moe::aligned16(d_pre) && moe::aligned16(d_bias),
                 "%s: tensors must be 16-byte aligned", who);
     if (M == 0 && !d_bias) return MOE_OK;  // (of no rows the bias' gradient is 0, and is written)
-    // of 32-row groups, as many CTAs share a column tile as there are groups, 8 at most
+    // as many CTAs share a column tile as it has groups of rows, 8 at most
+    const bool wide = (static_cast<int64_t>(N) + 255) / 256 * 8 >= 2 * moe::sm_count() && M >= 256;
+    const int rows = wide ? 8 : 32, cols = wide ? 256 : 64;
     int C = 1;
-    while (C < 8 && C * moe::kBiasRows < M) C *= 2;
-    const int64_t blocks = (static_cast<int64_t>(N) + moe::kBiasCols - 1) / moe::kBiasCols * C;
+    while (C < 8 && C * rows < M) C *= 2;
+    const int64_t blocks = (static_cast<int64_t>(N) + cols - 1) / cols * C;
     if (blocks > 0x7fffffff) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: N=%d is too large", who, N);
     return moe::done(who, moe::by_act(act, [&](auto a) {
         cudaLaunchConfig_t cfg = {};
@@ -375,13 +394,24 @@ extern "C" int moe_bias_act_backward(const void* d_out, const void* pre, int32_t
         attr[1].val.clusterDim.y = 1;
         attr[1].val.clusterDim.z = 1;
         cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(moe::kBiasThreads);
         cfg.stream = static_cast<cudaStream_t>(stream);
         cfg.attrs = attr;
         cfg.numAttrs = C > 1 ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, moe::bias_act_backward_kernel<decltype(a)::value>,
-                                  static_cast<const uint16_t*>(d_out), static_cast<const uint16_t*>(pre), fn, M, N,
-                                  static_cast<uint16_t*>(d_pre), d_bias, accumulate, C);
+        constexpr int A = decltype(a)::value;
+        auto run = [&](auto f) {
+            constexpr int F = decltype(f)::value;
+            return cudaLaunchKernelEx(&cfg, wide ? moe::bias_act_backward_kernel<A, F, 32> : moe::bias_act_backward_kernel<A, F, 8>,
+                                      static_cast<const uint16_t*>(d_out), static_cast<const uint16_t*>(pre), M, N,
+                                      static_cast<uint16_t*>(d_pre), d_bias, accumulate, C);
+        };
+        switch (fn) {
+            case MOE_FN_RELU: return run(std::integral_constant<int, MOE_FN_RELU>{});
+            case MOE_FN_GELU: return run(std::integral_constant<int, MOE_FN_GELU>{});
+            case MOE_FN_GELU_TANH: return run(std::integral_constant<int, MOE_FN_GELU_TANH>{});
+            case MOE_FN_SILU: return run(std::integral_constant<int, MOE_FN_SILU>{});
+            default: return run(std::integral_constant<int, MOE_FN_NONE>{});
+        }
     }));
 }
 
