@@ -43,7 +43,6 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(SPLIT_THREADS)
 split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const SplitParams sp) {
-    pdl_wait();
     const RaggedParams& p = sp.r;
     extern __shared__ __align__(1024) uint8_t smem[];
     SplitTail& s = *reinterpret_cast<SplitTail*>(smem + sp.tail_at);
@@ -76,6 +75,8 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
     }
+    pdl_wait();
+    pdl_launch_next();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -328,6 +328,7 @@ __device__ __forceinline__ void copy_slots(Tail& s, const RaggedParams& p, const
                                            const CUtensorMap* tm_add, uint8_t* area, int w, int n_off, int n_tiles,
                                            int first, int step, int lane, const WaitCtx& wc) {
     constexpr int N = Slots<GADD>::N, COLS = Slots<GADD>::COLS;
+    if (first >= n_tiles) return;
     int ltile = first, lc = 0;  // the next load
     uint32_t loaded = 0, stored = 0;
     Tile lt = get_tile<WGRAD>(s, p, first), t = lt;
@@ -471,7 +472,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
               const RaggedParams p) {
     using S = Shape<MODE, KIND>;
     constexpr bool CHUNKED = MODE == WGRAD && KIND != G16;
-    pdl_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
     Tail& s = *reinterpret_cast<Tail*>(smem + S::TAIL_AT);
     const WaitCtx wc{&s.abort_flag, p.err, p.wait_ns};
@@ -479,9 +479,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t rank = cluster_ctarank();  // 0: leader
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
-    const int bad = build_tiles<MODE>(s, p);  // identical in both CTAs
+    // set up while the kernel before this one ends; then its results may be read, and the next one may set up
     if (tid == 0) {
-        if (bad && blockIdx.x == 0) set_err(p.err, MOE_DEV_ERR_OFFSETS);
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
@@ -501,16 +500,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         mbar_init(&s.mma_done, 1);
         fence_mbar_init();
-    }
-    __syncthreads();
-    const int n_tiles = s.n_tiles;
-    if (first >= n_tiles) return;  // the same in both CTAs: nothing allocated yet
-
-    if (warp == 1) {
-        tmem_alloc_pair(&s.tmem_base, 512);
-        tmem_relinquish_pair();
-    }
-    if (tid == 0) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
         if (MODE == WGRAD) {
@@ -520,9 +509,20 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             tma_prefetch_desc(&tm_add);
         }
     }
+    __syncwarp();
+    if (warp == 1) {
+        tmem_alloc_pair(&s.tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();
+    pdl_launch_next();
+    const int bad = build_tiles<MODE>(s, p);  // identical in both CTAs
+    if (tid == 0 && bad && blockIdx.x == 0) set_err(p.err, MOE_DEV_ERR_OFFSETS);
     tc_fence_before();
+    __syncthreads();
     cluster_sync_all();  // barriers initialised, TMEM allocated
     tc_fence_after();
+    const int n_tiles = s.n_tiles;
     const uint32_t tmem = s.tmem_base;
     const uint32_t lead_full = mapa_shared(smem_u32(&s.full[0]), 0);
     const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
@@ -597,7 +597,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
             uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
             bool ok = true;
-            Tile next = get_tile<MODE>(s, p, first);
+            Tile next{};
+            if (first < n_tiles) next = get_tile<MODE>(s, p, first);
             for (int tile = first; tile < n_tiles && ok; tile += step) {
                 const Tile t = next;
                 const int nb = blocks_of(t), chunks = chunks_of(t);
