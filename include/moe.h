@@ -567,7 +567,7 @@ int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* top
  *   out           device act [rows, N], or [rows, K] if transposed (not a, not w)
  *   err_word      device i32 or NULL (MOE_DEV_ERR_OFFSETS, MOE_DEV_ERR_TIMEOUT)
  * Requirements: N % 8 == 0, K % 8 == 0, 1 <= E <= MOE_MAX_EXPERTS, tensors
- * 16-byte aligned.
+ * 16-byte aligned; rows, N and K <= 2^30.
  */
 int moe_ragged_gemm(const void* a, int32_t act, const void* w, int32_t transposed,
                     const int32_t* offsets, int32_t rows, int32_t N, int32_t K, int32_t E, void* out,
@@ -641,9 +641,10 @@ int moe_swiglu_backward(const void* gate_up, const void* d_h, int32_t act, int32
 
 /*
  * Token rows to their experts' rows, the transpose of moe_combine without its
- * weights: xs[pair_to_row[t * top_k + j]] = x[t]. Pairs with a row < 0 (dropped) write
- * nothing, nor do rows >= max_rows (which set MOE_DEV_ERR_PAIR_ID). The gradient of x
- * is moe_combine of the rows' gradients with weights of 1.
+ * weights: xs[pair_to_row[t * top_k + j]] = x[t]. No two pairs have the same row.
+ * Pairs with a row < 0 (dropped) write nothing, nor do rows >= max_rows (which set
+ * MOE_DEV_ERR_PAIR_ID). The gradient of x is moe_combine of the rows' gradients with
+ * weights of 1.
  *   x             device act [T, H];  pair_to_row  device i32 [T * top_k]
  *   xs            device act [max_rows, H] out (not x)
  * Requirements: H % 8 == 0, 1 <= top_k <= MOE_MAX_TOPK, 16-byte alignment.

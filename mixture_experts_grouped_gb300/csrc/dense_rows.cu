@@ -166,14 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(const DenseRows
 
 template <int ACT, int NT> int launch_nt(const DenseRowsParams& p, int sms, const RaggedArgs& g) {
     constexpr int smem = RowsStage<NT>::SMEM;
-    static int configured_for = -1;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_for != dev) {
-        const int rc = set_smem_limit(reinterpret_cast<const void*>(dense_rows_kernel<ACT, NT>), smem);
-        if (rc != MOE_OK) return rc;
-        configured_for = dev;
-    }
+    static PerDevice configured;
+    const int rc = raise_smem_limit(configured, reinterpret_cast<const void*>(dense_rows_kernel<ACT, NT>), smem);
+    if (rc != MOE_OK) return rc;
     const cudaError_t e =
         launch_pdl(dense_rows_kernel<ACT, NT>, dim3(sms < p.N ? sms : p.N), kThreads, smem, g.st, p);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", g.who, cudaGetErrorString(e));

@@ -85,6 +85,8 @@ int check_shapes(const char* who, int act, const int32_t* offsets, int rows, int
     MOE_REQUIRE(N > 0 && N % 8 == 0, "%s: N=%d must be a positive multiple of 8", who, N);
     MOE_REQUIRE(K > 0 && K % 8 == 0, "%s: K=%d must be a positive multiple of 8", who, K);
     MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "%s: E=%d outside [1, %d]", who, E, MOE_MAX_EXPERTS);
+    if (rows > (1 << 30) || N > (1 << 30) || K > (1 << 30))
+        return fail(MOE_ERR_UNSUPPORTED, "%s: %d rows, N=%d or K=%d above 2^30", who, rows, N, K);
     MOE_REQUIRE(offsets || E == 1, "%s: no offsets, but E=%d groups", who, E);
     MOE_REQUIRE((reinterpret_cast<uintptr_t>(offsets) & 3u) == 0, "%s: offsets must be 4-byte aligned", who);
     return MOE_OK;

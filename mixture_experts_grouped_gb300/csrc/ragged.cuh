@@ -52,6 +52,23 @@ struct RowsForm {
     int maxu, tiles, parts;
 };
 
+// What a kernel's first launch on a device found out or set (0: not yet), for launches from any thread.
+struct PerDevice {
+    std::atomic<int> of[64] = {};
+    std::atomic<int>* here() {
+        int dev = 0;
+        return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? &of[dev] : nullptr;
+    }
+};
+// the kernel's limit of dynamic shared memory, raised once a device
+inline int raise_smem_limit(PerDevice& done, const void* kernel, int bytes) {
+    std::atomic<int>* d = done.here();
+    if (d && d->load(std::memory_order_acquire)) return MOE_OK;
+    const int rc = set_smem_limit(kernel, bytes);
+    if (rc == MOE_OK && d) d->store(1, std::memory_order_release);
+    return rc;
+}
+
 int launch_ragged_rows_bf16(const RaggedArgs& g, const RowsForm& f);
 int launch_ragged_rows_f16(const RaggedArgs& g, const RowsForm& f);
 int launch_dense_rows(const RaggedArgs& g);  // up to 32 rows, one group, not transposed

@@ -81,7 +81,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    bool ok = true;
+    bool ok = true;  // (a wait that gave up in another CTA of the cluster shows in the error word alone)
 
     if (warp == 0) {
         // ---------------- copies ----------------
@@ -147,7 +147,6 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     // the epilogue's areas lie where the stages were: the sums of all parts, then staging
     const int sum_bytes = parts > 1 ? parts * ((n / 4 + parts - 1) / parts) * 2048 : 0;  // (slices may differ by 4 rows)
     float* stg = reinterpret_cast<float*>(smem + sum_bytes + (warp - 2) * (STG_ROWS * SG * 4));
-    // *abort_flag: a wait gave up here, and what was summed is not whole (the others learn it from err alone)
     if (parts == 1) {
         if (epi && ok)
 #pragma unroll 1
@@ -242,14 +241,9 @@ template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int p
     constexpr int all = 229376, half = 114688;
     const int64_t ctas = static_cast<int64_t>((g.p.J + 127) / 128) * mt * parts;
     const int most = parts < 8 && ctas * 10 <= sm_count() * 9 ? all : half;
-    static int configured_for = -1;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_for != dev) {
-        const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), all);
-        if (rc != MOE_OK) return rc;
-        configured_for = dev;
-    }
+    static PerDevice configured;
+    int rc = raise_smem_limit(configured, reinterpret_cast<const void*>(kernel), all);
+    if (rc != MOE_OK) return rc;
     SplitParams sp;
     sp.r = g.p;
     sp.parts = parts;
@@ -262,7 +256,7 @@ template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int p
     if (sp.stages > SPLIT_MAX_STAGES) sp.stages = SPLIT_MAX_STAGES;
     sp.tail_at = sp.stages * stage;
     Maps m;
-    int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, 1, 64, MODE == ROWS_FWD ? 128 : 64);
+    rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, 1, 64, MODE == ROWS_FWD ? 128 : 64);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, g.p.rows, g.p.C, sp.box, g.act);
     if (rc != MOE_OK) return rc;
     cudaLaunchConfig_t cfg = {};

@@ -763,6 +763,12 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (s.abort_flag) {
+        // a wait gave up: copies that the other CTA signals, or has signalled here, may still be on their way
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 100000) __nanosleep(1000);
+    }
+    __syncthreads();
     cluster_sync_all();  // the leader's MMAs read the peer's shared memory and write its TMEM
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
@@ -790,20 +796,18 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    static int configured_for = -1, max_pairs = 0;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_for != dev) {
+    static PerDevice pairs;
+    std::atomic<int>* known = pairs.here();
+    int max_pairs = known ? known->load(std::memory_order_acquire) : 0;
+    if (max_pairs == 0) {
         const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
         if (rc != MOE_OK) return rc;
         const int sms = sm_count();
         cfg.gridDim = dim3(sms > 1 ? sms / 2 * 2 : 2);
-        int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        if (e != cudaSuccess || n <= 0)
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&max_pairs, kernel, &cfg);
+        if (e != cudaSuccess || max_pairs <= 0)
             return fail(MOE_ERR_CUDA, "%s: cannot place pairs of CTAs: %s", who, cudaGetErrorString(e));
-        max_pairs = n;
-        configured_for = dev;
+        if (known) known->store(max_pairs, std::memory_order_release);
     }
     if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < max_pairs ? tiles : max_pairs)));

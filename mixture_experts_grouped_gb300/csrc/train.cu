@@ -372,6 +372,7 @@ extern "C" int moe_bias_act_backward(const void* d_out, const void* pre, int32_t
     MOE_REQUIRE(fn >= MOE_FN_NONE && fn <= MOE_FN_SILU, "%s: unknown activation function %d", who, fn);
     MOE_REQUIRE(M >= 0, "%s: M=%d is negative", who, M);
     MOE_REQUIRE(N > 0 && N % 8 == 0, "%s: N=%d must be a positive multiple of 8", who, N);
+    if (M > (1 << 30)) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: M=%d above 2^30", who, M);
     MOE_REQUIRE(d_pre || d_bias, "%s: neither d_pre nor d_bias is given", who);
     MOE_REQUIRE(M == 0 || (d_out && (pre || fn == MOE_FN_NONE)), "%s: NULL pointer", who);
     MOE_REQUIRE(moe::aligned16(d_out) && moe::aligned16(pre) && moe::aligned16(d_pre) && moe::aligned16(d_bias),

@@ -353,6 +353,137 @@ def test_dense_product_of_layers(moe, dev, M, N, K):
     plain.close(out, full.cpu(), act, (fn_error("gelu_tanh", ref, dz) + full.abs() * F32).cpu())
 
 
+# sizes at which products of one group take each of their forms: streaming with 8, 16 and 32 rows and several tiles a
+# CTA, one to eight CTAs to a tile, one and several row tiles, pairs
+FORMS = [(5, 9736, 72), (16, 9736, 136), (30, 9736, 200), (24, 136, 1032), (40, 264, 8192), (150, 520, 4096),
+         (300, 264, 4104), (33, 1000, 1032), (600, 4104, 520), (614, 1648, 4336), (1000, 4096, 1032), (90, 28672, 264)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_products_of_one_group_in_every_form(moe, dev, M, N, K):
+    """Without offsets, and with: the group's size is then known on the device alone."""
+    g = torch.Generator(device=dev).manual_seed(M + N)
+    for act, i in (("bf16", 0), ("f16", 1)):
+        dt = plain.DT[act]
+        w = (torch.randn((N, K), generator=g, device=dev) / math.sqrt(K)).to(dt)
+        for tr in (False, True):
+            a = torch.randn((M, N if tr else K), generator=g, device=dev).to(dt)
+            outs = []
+            for off in (None, torch.tensor([0, M], dtype=torch.int32, device=dev)):
+                for _ in range(2):
+                    out = torch.empty((M, K if tr else N), dtype=dt, device=dev)
+                    moe.moe_ragged_gemm(a, i, w, tr, off, M, N, K, 1, out)
+                    outs.append(out)
+            assert torch.equal(outs[0], outs[1]) and torch.equal(outs[2], outs[3])
+            we = w.double() if tr else w.double().T
+            ref, mag = a.double() @ we, a.double().abs() @ we.abs()
+            for out in outs[::2]:
+                plain.close(out, ref.cpu(), act, sum_slack(mag, N if tr else K).cpu())
+        b, r = torch.randn(N, generator=g, device=dev).to(dt), torch.randn((M, N), generator=g, device=dev).to(dt)
+        a = torch.randn((M, K), generator=g, device=dev).to(dt)
+        z = torch.empty_like(r)
+        out = r.clone()
+        moe.moe_dense_gemm(a, i, w, b, moe.FN_CODES["gelu"], out, z, out, M, N, K)
+        ref = a.double() @ w.double().T + b.double()
+        dz = sum_slack(a.double().abs() @ w.double().abs().T + b.double().abs(), K)
+        plain.close(z, ref.cpu(), act, dz.cpu())
+        full = f64("gelu", ref)[0] + r.double()
+        plain.close(out, full.cpu(), act, (fn_error("gelu", ref, dz) + full.abs() * F32).cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("limit_ns", [1, 100, 1500, 4000])
+@pytest.mark.parametrize("M,N,K", [(40, 264, 8192), (150, 520, 4096), (300, 2056, 328)])
+def test_split_product_ends_whatever_wait_runs_out(moe, dev, M, N, K, limit_ns):
+    """Limits that may run out at its start, in its middle or not at all, with operands that are in no cache: the call
+    ends, a result that is not the clean one is reported, and the next call at the default limit is the clean one."""
+    g = torch.Generator(device=dev).manual_seed(1)
+    a, w = (torch.randn(s, generator=g, device=dev).bfloat16() for s in ((M, K), (N, K)))
+    want, out = (torch.empty((M, N), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    moe.moe_dense_gemm(a, 0, w, None, 0, None, None, want, M, N, K, err)
+    torch.empty(1 << 28, device=dev).zero_()
+    old = moe.moe_set_wait_limit_ns(limit_ns)
+    try:
+        moe.moe_dense_gemm(a, 0, w, None, 0, None, None, out, M, N, K, err)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(old)
+    assert err.item() in (0, moe.MOE_DEV_ERR_TIMEOUT)
+    assert err.item() or torch.equal(out, want)
+    err.zero_()
+    moe.moe_dense_gemm(a, 0, w, None, 0, None, None, out, M, N, K, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.gpu
+def test_tensors_past_32_bits_of_elements(moe, dev):
+    """Rows, weights and gradients whose offsets pass 2^31 elements (4.3 GB each)."""
+    H, R = 8192, 270000
+    g = torch.Generator(device=dev).manual_seed(3)
+    bf = dict(dtype=torch.bfloat16, device=dev)
+
+    def near_rows(got, ref):
+        assert float((got.double() - ref).abs().max()) <= 2 * plain.U["bf16"] * float(ref.abs().max())
+
+    # a product with that many output elements: the last rows
+    a, w = torch.randn((R, 64), generator=g, device=dev).bfloat16(), torch.randn((H, 64), generator=g, device=dev).bfloat16()
+    big = torch.empty((R, H), **bf)
+    moe.moe_dense_gemm(a, 0, w, None, 0, None, None, big, R, H, 64)
+    for lo in (0, 262140, R - 40):
+        near_rows(big[lo:lo + 40], a[lo:lo + 40].double() @ w.double().T)
+    # its rows as the operand of the input's gradient, in two groups, and of the weight's gradient
+    off = torch.tensor([0, 262150, R], dtype=torch.int32, device=dev)
+    ww = torch.stack((w, w.flip(0))).contiguous()
+    back = torch.empty((R, 64), **bf)
+    moe.moe_ragged_gemm(big, 0, ww, True, off, R, H, 64, 2, back)
+    near_rows(back[-40:], big[-40:].double() @ ww[1].double())
+    near_rows(back[262100:262150], big[262100:262150].double() @ ww[0].double())
+    dw = torch.empty((2, H, 64), device=dev)
+    moe.moe_ragged_wgrad(big, a, 0, off, R, H, 64, 2, None, dw, True)
+    ref = big[262150:].double().T @ a[262150:].double()
+    assert float((dw[1].double() - ref).abs().max()) <= 1e-4 * float(ref.abs().max())
+    # SwiGLU of a gate/up product that long, and its gradient
+    h, dgu, dh = torch.empty((R, H // 2), **bf), torch.empty((R, H), **bf), a[:, :8].repeat(1, H // 16)
+    moe.moe_swiglu(big, 0, R, H // 2, h)
+    moe.moe_swiglu_backward(big, dh, 0, R, H // 2, dgu, None)
+    t = big[-3:].double()
+    near_rows(h[-3:], t[:, : H // 2] * torch.sigmoid(t[:, : H // 2]) * t[:, H // 2:])
+    near_rows(dgu[-3:, H // 2:], dh[-3:].double() * t[:, : H // 2] * torch.sigmoid(t[:, : H // 2]))
+    db = torch.empty(H, device=dev)
+    moe.moe_bias_act_backward(big, dgu, 0, 1, R, H, dgu, db)
+    t = torch.where(dgu[-3:] != 0, big[-3:], 0)
+    assert torch.equal(dgu[-3:], t)
+    # rows to such places, and the gradients back from them
+    rows = torch.randperm(R, generator=gen(4))[:64].int()
+    rows[:2] = torch.tensor([R - 1, R - 2])
+    rows = rows.unique().to(dev)[-32:].contiguous()
+    x = torch.randn((16, H), generator=g, device=dev).bfloat16()
+    moe.moe_dispatch(x, 0, rows, big, 16, H, 2, R)
+    assert torch.equal(big[rows.long()], x.repeat_interleave(2, 0))
+    wt, d_w = torch.rand((16, 2), generator=g, device=dev), torch.empty((16, 2), device=dev)
+    moe.moe_combine_backward(x, big, 0, rows, wt, big, d_w, 16, H, 2, R)
+    near_rows(big[rows.long()].unflatten(0, (16, 2)), wt.double()[..., None] * x.double()[:, None])
+    ref = (x.double() ** 2).sum(1, keepdim=True).expand(16, 2)
+    assert torch.allclose(d_w.double(), ref, rtol=1e-5)
+    del big, dgu, dh, h, a, back
+    # a weight that long: 130 experts of 4096 x 4096
+    E, N = 130, 4096
+    w = torch.zeros((E, N, N), **bf)
+    w[-1].normal_(generator=g)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=dev)
+    off[-1] = 20
+    x, out = torch.randn((20, N), generator=g, device=dev).bfloat16(), torch.empty((20, N), **bf)
+    for tr in (False, True):
+        moe.moe_ragged_gemm(x, 0, w, tr, off, 20, N, N, E, out)
+        near_rows(out, x.double() @ (w[-1].double() if tr else w[-1].double().T))
+    moe.moe_ragged_wgrad(x, out, 0, off, 20, N, N, E, None, w, False)
+    near_rows(w[-1], x.double().T @ out.double())
+    assert torch.all(w[:-1:43] == 0)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [2, 20, 150])
 def test_dense_product_keeps_non_finite_values_apart(moe, dev, M):
@@ -761,6 +892,23 @@ def test_calls_on_streams_do_not_disturb_each_other(moe, dev):
 # ---- refusals (no GPU) --------------------------------------------------------------------------------
 
 A = 1 << 20  # an aligned address that no call reaches
+
+
+@pytest.mark.parametrize("call", [
+    lambda m: m.moe_ragged_gemm(A, 0, A, 0, A, (1 << 30) + 1, 64, 64, 2, A, 0, 0),
+    lambda m: m.moe_ragged_wgrad(A, A, 0, A, 4, (1 << 30) + 8, 64, 2, None, A, 1, 0, 0),
+    lambda m: m.moe_ragged_wgrad(A, A, 0, A, 4, 1 << 24, 1 << 24, 2, None, A, 1, 0, 0),     # too many tiles
+    lambda m: m.moe_dense_gemm(A, 0, A, None, 0, None, None, A, 4, 64, (1 << 30) + 8, 0, 0),
+    lambda m: m.moe_bias_act_backward(A, A, 0, 1, (1 << 30) + 1, 64, A, None, 0, 0),
+    lambda m: m.moe_swiglu(A, 0, 1 << 30, 1 << 20, A, 0),
+    lambda m: m.moe_swiglu_backward(A, A, 0, 1 << 30, 1 << 20, A, None, 0),
+])
+def test_what_is_beyond_the_limits_is_unsupported(moe, call):
+    n0 = moe.moe_launch_count()
+    with pytest.raises(moe.MoeError) as e:
+        call(moe)
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED and e.value.message
+    assert moe.moe_launch_count() == n0
 
 
 @pytest.mark.parametrize("call", [
