@@ -45,7 +45,7 @@ enum { G16 = 0, G32 = 1, GADD = 2 };
 constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
 constexpr int STAGE = 2 * OPER;
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 10;
 constexpr int STG_ROWS = 16;  // rows form: rows of a warp's staging area
 constexpr int SG = 36;  // rows form: row stride (floats) of a warp's staging area, 16-byte reads without conflicts
 constexpr int UNIT = 64 * 16 * 2;             // gradient form: 64 columns of a unit of 16 rows
@@ -68,13 +68,15 @@ struct Tail {
 // gradient with an addend is bound by their bytes: four warps with four slots each, so that
 // three steps' addends are on their way, four others that load and store for them, and
 // four stages. Other gradients have a slot a warp
-// and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four).
+// and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four). The rows form
+// has six stages of full height, more of lower ones: a group's few rows leave a tile to its
+// weights' latency, and an SM streams them as fast as it has copies in flight.
 template <int MODE, int KIND> struct Shape {
     static constexpr int HALVES = KIND == GADD ? 1 : 2;  // warps to a quarter
     static constexpr int WARPS = 4 * HALVES;
     static constexpr int THREADS = 384;
     static constexpr int SLOTS = KIND == GADD ? 4 : 1;
-    static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;
+    static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;  // of full height
     static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG_ROWS * SG * 4;
     static constexpr int TBUF_AT = STAGES * STAGE;
     static constexpr int STG_AT = TBUF_AT + (MODE == WGRAD ? TBUFS * TBUF : 0);
@@ -82,6 +84,12 @@ template <int MODE, int KIND> struct Shape {
     static constexpr int SMEM = TAIL_AT + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
     static_assert(SMEM <= 232448, "shared memory over the limit");
 };
+
+// stages that the ring's bytes hold
+template <int MODE, int KIND> __device__ __forceinline__ uint32_t n_stages(uint32_t stage_bytes) {
+    if (MODE == WGRAD) return Shape<MODE, KIND>::STAGES;
+    return min(static_cast<uint32_t>(MAX_STAGES), Shape<MODE, KIND>::STAGES * STAGE / stage_bytes);
+}
 
 // ---- operands -------------------------------------------------------------------------
 // MN-major operand with the 128-byte swizzle, as a TMA box of 64 elements (128 bytes) x 64
@@ -481,7 +489,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 
     // set up while the kernel before this one ends; then its results may be read, and the next one may set up
     if (tid == 0) {
-        for (int i = 0; i < S::STAGES; ++i) {
+        for (int i = 0; i < MAX_STAGES; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
@@ -529,6 +537,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), 0);
     const int KB = (p.C + BK - 1) / BK;
     const uint32_t b_bytes = MODE == WGRAD ? OPER : p.maxu * 8 * 128;  // this CTA's, of the N operand
+    const uint32_t stage_bytes = OPER + b_bytes, stages = n_stages<MODE, KIND>(stage_bytes);
     // blocks of a tile; of a gradient, those that its whole units of 16 rows fill
     auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows / 16 + 3) / 4 : KB; };
     auto chunks_of = [&](const Tile& t) { return CHUNKED ? max(1, (blocks_of(t) + CHUNK - 1) / CHUNK) : 1; };
@@ -550,7 +559,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 if (elect_one()) {
                     if (is_a && rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (OPER + b_bytes));
                     const uint32_t bar = lead_full + stage * 8;
-                    uint8_t* dst = smem + stage * STAGE + (is_a ? 0 : OPER);
+                    uint8_t* dst = smem + stage * stage_bytes + (is_a ? 0 : OPER);
                     if (MODE == WGRAD) {
                         const int r = t.m0 + b * BK;
                         if (is_a) {
@@ -578,16 +587,16 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 }
                 __syncwarp();
                 ++issued;
-                if (++stage == S::STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
         }
         if (is_a && rank == 0) {  // let every copy land before either CTA may exit
-            const long from = issued > S::STAGES ? issued - S::STAGES : 0;
+            const long ring = stages, from = issued > ring ? issued - ring : 0;
             for (long j = from; j < issued; ++j)
-                mbar_drain(&s.full[j % S::STAGES], static_cast<uint32_t>((j / S::STAGES) & 1), kWaitLimitNs / 8);
+                mbar_drain(&s.full[j % ring], static_cast<uint32_t>((j / ring) & 1), kWaitLimitNs / 8);
         }
     } else if (warp == 1) {
         if (rank == 0) {
@@ -619,7 +628,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t at = smem_u32(smem + stage * STAGE);
+                        const uint32_t at = smem_u32(smem + stage * stage_bytes);
                         const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
                         const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
                         const int steps = MODE == WGRAD ? min(4, t.rows / 16 - 4 * b) : 4;
@@ -631,7 +640,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                             tc_commit_pair(&s.empty[stage], 0x3);
                         }
                         __syncwarp();
-                        if (++stage == S::STAGES) {
+                        if (++stage == stages) {
                             stage = 0;
                             phase ^= 1;
                         }
