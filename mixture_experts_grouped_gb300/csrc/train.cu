@@ -231,41 +231,43 @@ route_backward_kernel(const float* logits, const int32_t* __restrict__ ids, cons
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (t >= T) return;
+    constexpr int PER = MOE_MAX_EXPERTS / 32;
+    float p[PER];
     int id = -1;
     float wj = 0.0f, dj = 0.0f;
+    // (every load at once: a row is bound by their latency)
     if (lane < top_k) {
         id = ids[t * top_k + lane];
-        if (id < 0 || id >= E) {
-            set_err(err, MOE_DEV_ERR_EXPERT_ID);
-            id = -1;
-        } else {
-            wj = w[t * top_k + lane];
-            dj = dw[t * top_k + lane];
-        }
+        wj = w[t * top_k + lane];
+        dj = dw[t * top_k + lane];
+    }
+    if (!renorm)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) p[j] = lane + 32 * j < E ? logits[t * E + lane + 32 * j] : -INFINITY;
+    if (lane < top_k && (id < 0 || id >= E)) {
+        set_err(err, MOE_DEV_ERR_EXPERT_ID);
+        id = -1;
+        wj = dj = 0.0f;
     }
     float m = wj * dj;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
-    constexpr int PER = MOE_MAX_EXPERTS / 32;
-    float p[PER];
+    float scale = 1.0f;  // p times it is the softmax
     if (!renorm) {
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            p[j] = lane + 32 * j < E ? logits[t * E + lane + 32 * j] : -INFINITY;
-            top = fmaxf(top, p[j]);
-        }
+        for (int j = 0; j < PER; ++j) top = fmaxf(top, p[j]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
+            if (32 * j >= E) break;
             p[j] = lane + 32 * j < E ? expf(p[j] - top) : 0.0f;
             sum += p[j];
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-#pragma unroll
-        for (int j = 0; j < PER; ++j) p[j] = __fdiv_rn(p[j], sum);
+        scale = __fdiv_rn(1.0f, sum);
     }
     // renormalised: what a slot gives its expert; otherwise the slot's part of g
     const float mine = renorm ? wj * (dj - m) : dj;
@@ -276,12 +278,16 @@ route_backward_kernel(const float* logits, const int32_t* __restrict__ ids, cons
         const int e = __shfl_sync(0xffffffffu, id, s);
         const float v = __shfl_sync(0xffffffffu, mine, s);
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
+        for (int j = 0; j < PER; ++j) {
+            if (32 * j >= E) break;
             if (e == lane + 32 * j) g[j] += v;
+        }
     }
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-        if (lane + 32 * j < E) dl[t * E + lane + 32 * j] = renorm ? g[j] : p[j] * (g[j] - m);
+    for (int j = 0; j < PER; ++j) {
+        if (32 * j >= E) break;
+        if (lane + 32 * j < E) dl[t * E + lane + 32 * j] = renorm ? g[j] : p[j] * scale * (g[j] - m);
+    }
 }
 
 // ---- launches ------------------------------------------------------------------------
