@@ -11,7 +11,9 @@ namespace {
 //   h = g s u,   s = 1 / (1 + exp(-g));   d_u = d_h g s,   d_g = d_h u s (1 + g (1 - s))
 //
 // of [rows, 2 I] gate/up products (gate columns, then up). Each thread takes 16-byte
-// vectors of 8 columns, numbered through over all rows.
+// vectors of 8 columns, numbered through over all rows; the threads that an SM holds keep
+// enough loads in flight. Measured, 8192 x 14336: 100 us forward, 203 back with h given
+// again, both 7.0 TB/s (the copy rate); 64 x 768: 1.4 us, a launch's latency.
 constexpr int kGluThreads = 256;
 
 template <int ACT, typename Index>
@@ -65,7 +67,8 @@ swiglu_backward_kernel(const uint4* gu, const uint4* dh, uint4* dgu, uint4* h, I
 // cluster of C CTAs; column sums are added over the CTA's rows of threads and then over
 // the cluster in rank order (distributed shared memory), so no workspace is needed and
 // the order depends on the sizes alone. TX = 32 where that fills the GPU, since HBM is kinder
-// to 512 bytes of a row than to 128 (4096 x 14336, relu: 59 us, 69 with TX = 8), else 8.
+// to 512 bytes of a row than to 128 (4096 x 14336, relu: 59 us, 69 with TX = 8), else 8 (1333 x
+// 2816: relu 7.6 us, gelu 10, of 3.4 for the bytes). gelu's arithmetic bounds it (83 us).
 constexpr int kBiasThreads = 256;
 
 template <int ACT, int FN, int TX>
@@ -141,7 +144,9 @@ bias_act_backward_kernel(const uint16_t* d_out, const uint16_t* pre, int M, int 
 // ---- rows to the experts, gradient of the combine -----------------------------------
 //
 // A block takes one token and 8 columns a thread at a time: its row is read once and
-// serves the token's K rows, whose accesses are all in flight together.
+// serves the token's K rows, whose accesses are all in flight together. Bound by HBM, at
+// rows in random order: 4096 tokens of 4096 columns, k = 2, 18.7 and 29.7 us, 5.4 and 5.7
+// TB/s; 61 of 2048, k = 8, 3.5 and 3.8 us (row numbers, rows, stores, one after the other).
 template <int K>
 __global__ void __launch_bounds__(256)
 dispatch_kernel(const uint4* x, const int32_t* __restrict__ pair_to_row, uint4* xs, int T, int V, int top_k,
@@ -224,6 +229,7 @@ combine_backward_kernel(const uint4* d_out, const uint4* y, const int32_t* __res
 }
 
 // ---- gradient of the routing: a warp a row -------------------------------------------
+// 61 rows of 128 experts 3.8 us, 4096 of 8 3.7: latency.
 __global__ void __launch_bounds__(128)
 route_backward_kernel(const float* logits, const int32_t* __restrict__ ids, const float* __restrict__ w,
                       const float* __restrict__ dw, float* dl, int T, int E, int top_k, int renorm, int32_t* err) {
