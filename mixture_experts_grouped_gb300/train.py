@@ -19,6 +19,14 @@ from . import moe as M
 from .ffn import _require_shape, _require_type
 
 
+def _require(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> None:
+    """A dense tensor of this type and shape on the current device (the kernels take addresses as they come)."""
+    _require_shape(what, t, *shape)
+    _require_type(what, t, dtype)
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 class MoeTrainLayer:
     """Buffers of one (T, H, I, E, k) shape, a forward and a backward pass:
 
@@ -26,16 +34,17 @@ class MoeTrainLayer:
 
     Weights are 16-bit tensors of the activation type, ``w_gate_up`` [E, 2 I, H]
     (gate rows first) and ``w_down`` [E, H, I]; their gradients ``d_gate_up`` and
-    ``d_down`` are f32. ``backward`` uses what the last ``forward`` left in the
-    buffers, and its logits. It may be called several times for one forward pass."""
+    ``d_down`` are f32, zeros at first. ``backward`` uses what the last ``forward`` left
+    in the buffers, and its logits. It may be called several times for one forward
+    pass. An object runs one pass at a time: calls on several streams share its buffers."""
 
     def __init__(self, T, H, I, E, k, act, w_gate_up: torch.Tensor, w_down: torch.Tensor, device="cuda",
                  renormalize: bool = True):
-        dt = L.act_dtype(act)
-        _require_shape("w_gate_up", w_gate_up, E, 2 * I, H)
-        _require_shape("w_down", w_down, E, H, I)
-        _require_type("w_gate_up", w_gate_up, dt)
-        _require_type("w_down", w_down, dt)
+        dt = self.dtype = L.act_dtype(act)
+        if T < 1:
+            raise ValueError(f"T={T}: a step needs a token")
+        _require("w_gate_up", w_gate_up, dt, E, 2 * I, H)
+        _require("w_down", w_down, dt, E, H, I)
         self.T, self.H, self.I, self.E, self.k, self.P = T, H, I, E, k, T * k
         self.act_code, self.renormalize = M.ACT_CODES[act], renormalize
         self.w_gate_up, self.w_down = w_gate_up, w_down
@@ -62,12 +71,14 @@ class MoeTrainLayer:
         self.out = rows(T, H)
         self.d_y, self.d_h, self.d_gu, self.d_xs, self.d_x = rows(P, H), rows(P, I), rows(P, 2 * I), rows(P, H), rows(T, H)
         self.d_weights, self.d_logits = f32(T, k), f32(T, E)
-        self.d_gate_up, self.d_down = f32(E, 2 * I, H), f32(E, H, I)
+        self.d_gate_up, self.d_down = f32(E, 2 * I, H).zero_(), f32(E, H, I).zero_()
         self.logits = None
 
     def forward(self, x, logits, stream=None):
         """The layer on x [T, H] routed by logits [T, E]; returns its output buffer."""
         T, H, I, E, k, P, act = self.T, self.H, self.I, self.E, self.k, self.P, self.act_code
+        _require("x", x, self.dtype, T, H)
+        _require("logits", logits, torch.float32, T, E)
         self.logits = logits
         M.moe_route_topk_softmax(logits, self.topk_ids, self.topk_weights, T, E, k, self.renormalize, stream)
         M.moe_align_block_size(self.topk_ids, P, E, 1, P, self.sorted_token_ids, self.expert_ids, self.offsets,
@@ -84,6 +95,9 @@ class MoeTrainLayer:
         """Gradients of the last forward pass from its output's, d_out [T, H]: returns (d_x, d_logits);
         the weights' are in ``d_gate_up`` and ``d_down``, added to what is there if ``accumulate``."""
         T, H, I, E, k, P, act = self.T, self.H, self.I, self.E, self.k, self.P, self.act_code
+        if self.logits is None:
+            raise RuntimeError("backward without a forward pass")
+        _require("d_out", d_out, self.dtype, T, H)
         M.moe_combine_backward(d_out, self.y, act, self.pair_to_row, self.topk_weights, self.d_y, self.d_weights, T, H,
                                k, P, self.err, stream)
         M.moe_ragged_gemm(self.d_y, act, self.w_down, True, self.offsets, P, H, I, E, self.d_h, self.err, stream)
@@ -107,15 +121,16 @@ class DenseMlp:
 
     ``w1`` [I, H], ``w2`` [H, I] and the biases (or None) are 16-bit tensors of the
     activation type, ``fn`` a name of ``moe.FN_CODES``. The weights' gradients
-    ``d_w1`` and ``d_w2`` and the biases' ``d_b1`` and ``d_b2`` are f32; the
-    residual's is the output's."""
+    ``d_w1`` and ``d_w2`` and the biases' ``d_b1`` and ``d_b2`` are f32, zeros at first;
+    the residual's is the output's. An object runs one pass at a time."""
 
     def __init__(self, T, H, I, act, fn, w1, b1, w2, b2, device="cuda"):
-        dt = L.act_dtype(act)
+        dt = self.dtype = L.act_dtype(act)
+        if T < 1:
+            raise ValueError(f"T={T}: a step needs a token")
         for name, t, shape in (("w1", w1, (I, H)), ("w2", w2, (H, I)), ("b1", b1, (I,)), ("b2", b2, (H,))):
             if t is not None:
-                _require_shape(name, t, *shape)
-                _require_type(name, t, dt)
+                _require(name, t, dt, *shape)
         self.T, self.H, self.I = T, H, I
         self.act_code, self.fn = M.ACT_CODES[act], M.FN_CODES[fn]
         self.w1, self.b1, self.w2, self.b2 = w1, b1, w2, b2
@@ -127,14 +142,17 @@ class DenseMlp:
             return torch.empty(shape, dtype=torch.float32, device=device)
 
         self.pre, self.h, self.out, self.d_h, self.d_x = rows(I), rows(I), rows(H), rows(I), rows(H)
-        self.d_w1, self.d_w2 = f32(I, H), f32(H, I)
-        self.d_b1 = f32(I) if b1 is not None else None
-        self.d_b2 = f32(H) if b2 is not None else None
+        self.d_w1, self.d_w2 = f32(I, H).zero_(), f32(H, I).zero_()
+        self.d_b1 = f32(I).zero_() if b1 is not None else None
+        self.d_b2 = f32(H).zero_() if b2 is not None else None
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.x = None
 
     def forward(self, x, residual=None, stream=None):
         """The block on x [T, H]; returns its output buffer. x is kept for ``backward``."""
+        _require("x", x, self.dtype, self.T, self.H)
+        if residual is not None:
+            _require("residual", residual, self.dtype, self.T, self.H)
         self.x = x
         M.moe_dense_gemm(x, self.act_code, self.w1, self.b1, self.fn, None, self.pre, self.h, self.T, self.I, self.H,
                          self.err, stream)
@@ -146,6 +164,9 @@ class DenseMlp:
         """Gradients of the last forward pass from its output's, d_out [T, H]: returns d_x; the weights'
         and biases' are in ``d_w1`` .. ``d_b2``, added to what is there if ``accumulate``."""
         T, H, I, act = self.T, self.H, self.I, self.act_code
+        if self.x is None:
+            raise RuntimeError("backward without a forward pass")
+        _require("d_out", d_out, self.dtype, T, H)
         if self.d_b2 is not None:
             M.moe_bias_act_backward(d_out, None, act, M.MOE_FN_NONE, T, H, None, self.d_b2, accumulate,
                                     stream)

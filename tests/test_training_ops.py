@@ -764,6 +764,40 @@ def test_training_step_of_the_layer(moe, dev, T, H, I, E, k, renorm, act):
 
 
 @pytest.mark.gpu
+def test_training_objects_refuse_what_does_not_fit(moe, dev):
+    from mixture_experts_grouped_gb300 import train
+    T, H, I, E, k, bf = 4, 64, 32, 3, 2, dict(dtype=torch.bfloat16, device=dev)
+    w = torch.zeros((E, 2 * I, H), **bf), torch.zeros((E, H, I), **bf)
+    layer = train.MoeTrainLayer(T, H, I, E, k, "bf16", *w)
+    assert torch.all(layer.d_gate_up == 0) and torch.all(layer.d_down == 0)
+    x, logits = torch.zeros((T, H), **bf), torch.zeros((T, E), device=dev)
+    n0 = moe.moe_launch_count()
+    with pytest.raises(RuntimeError):
+        layer.backward(x)
+    for bad_x, bad_l in ((x[:3], logits), (x.half(), logits), (x.T.contiguous().T, logits), (x.cpu(), logits),
+                         (x, logits.double()), (x, logits[:, :2]), (x, logits.cpu())):
+        with pytest.raises(ValueError):
+            layer.forward(bad_x, bad_l)
+    for args in ((0, H, I, E, k, "bf16", *w), (T, H, I, E, k, "f16", *w), (T, H, I, E, k, "bf16", w[0][:, ::2], w[1]),
+                 (T, H, I, E, k, "bf16", w[0].cpu(), w[1])):
+        with pytest.raises(ValueError):
+            train.MoeTrainLayer(*args)
+    m = [torch.zeros(s, **bf) for s in ((I, H), (I,), (H, I), (H,))]
+    block = train.DenseMlp(T, H, I, "bf16", "gelu", *m)
+    with pytest.raises(RuntimeError):
+        block.backward(x)
+    for bad in (dict(x=x[:, ::2]), dict(x=x.cpu()), dict(x=x, residual=x.half())):
+        with pytest.raises(ValueError):
+            block.forward(**bad)
+    with pytest.raises(ValueError):
+        train.DenseMlp(T, H, I, "bf16", "gelu", m[0], m[3], m[2], m[3])
+    assert moe.moe_launch_count() == n0
+    layer.forward(x, logits)
+    with pytest.raises(ValueError):
+        layer.backward(x.float())
+
+
+@pytest.mark.gpu
 def test_training_gradient_against_differences(moe, dev):
     """The loss sum(out * d_out) along the gradient's own direction, by differences of the layer's own outputs."""
     from mixture_experts_grouped_gb300 import train
