@@ -49,6 +49,29 @@ __device__ __forceinline__ float fn_value(int fn, float z) {
     }
 }
 
+// f of eight values: one branch for all, and as little code as that takes
+__device__ __forceinline__ void fn_values(int fn, float (&f)[8]) {
+    switch (fn) {
+        case MOE_FN_RELU:
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = fn_value(MOE_FN_RELU, f[j]);
+            break;
+        case MOE_FN_GELU:
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = fn_value(MOE_FN_GELU, f[j]);
+            break;
+        case MOE_FN_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = fn_value(MOE_FN_GELU_TANH, f[j]);
+            break;
+        case MOE_FN_SILU:
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = fn_value(MOE_FN_SILU, f[j]);
+            break;
+        default: break;
+    }
+}
+
 // f'(z)
 __device__ __forceinline__ float fn_slope(int fn, float z) {
     switch (fn) {

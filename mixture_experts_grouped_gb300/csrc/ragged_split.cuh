@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c
     tma_load_3d(dst, map, c0, c1, c2, bar);
 }
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, int KIND>
 __global__ void __launch_bounds__(SPLIT_THREADS)
 split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const SplitParams sp) {
     const RaggedParams& p = sp.r;
@@ -138,6 +138,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         __syncwarp();
         mbar_drain(&s.done, 0, kWaitLimitNs / 8);
     } else {
+        if constexpr (KIND == FULL) prefetch_residual(p, lane, m0, rows, j0 + 32 * (warp & 3));
         ok = mbar_wait_warp(&s.done, 0, wc);
         tc_fence_after();
     }
@@ -145,7 +146,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const bool epi = warp >= 2;
     const int q = warp & 3, me = 32 * q + lane;
     const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const float bias = epi ? bias_of<ACT>(p, j0 + me) : 0.0f;
+    const float bias = KIND == FULL && epi ? bias_of<ACT>(p, j0 + me) : 0.0f;
     // the epilogue's areas lie where the stages were: the sums of all parts, then staging
     const int sum_bytes = parts > 1 ? parts * ((n / 4 + parts - 1) / parts) * 2048 : 0;  // (slices may differ by 4 rows)
     float* stg = reinterpret_cast<float*>(smem + sum_bytes + (warp - 2) * (STG_ROWS * SG * 4));
@@ -155,11 +156,13 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int c = 0; c < rows; c += 16) {
                 uint32_t u[16];
                 float v[16];
+                Residual res;
+                if (KIND == FULL) res.load(p, lane, m0 + c, rows - c, j0 + 32 * q);
                 tmem_ld16(ta + c, u);
                 tmem_ld16_wait(u);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]) + bias;
-                store_rows<ACT>(p, v, stg, lane, m0 + c, rows - c, j0 + 32 * q);
+                store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + c, rows - c, j0 + 32 * q);
             }
     } else {
         cluster_sync_all();  // every CTA's MMAs are complete: the stages are free
@@ -199,6 +202,8 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 #pragma unroll 1
             for (int c = 0; c < have; c += 16) {
                 float v[16];
+                Residual res;
+                if (KIND == FULL) res.load(p, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -218,7 +223,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     v[4 * j + 2] = f.z + bias;
                     v[4 * j + 3] = f.w + bias;
                 }
-                store_rows<ACT>(p, v, stg, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
+                store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
             }
         }
     }
@@ -236,8 +241,8 @@ static_assert(3 * (OPER + SPLIT_ROWS * 128) >= split_sums(SPLIT_ROWS) + 4 * STG_
                   3 * (OPER + 48 * 128) >= split_sums(48) + 4 * STG_ROWS * SG * 4,
               "the epilogue's areas fit in the stages");
 
-template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int parts) {
-    auto kernel = split_kernel<MODE, ACT>;
+template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g, int mt, int parts) {
+    auto kernel = split_kernel<MODE, ACT, KIND>;
     // of shared memory: two CTAs to an SM, or all where there are fewer CTAs than SMs (clusters of 8 with an SM
     // each do not fill the GPU: 128 CTAs of 2048 columns take 11.8 us so, two to an SM 7.5)
     constexpr int all = 229376, half = 114688;
@@ -279,6 +284,12 @@ template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int p
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", g.who, cudaGetErrorString(e));
     count_launch();
     return check_launch(g.who);
+}
+
+template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int parts) {
+    if (MODE == ROWS_FWD && (g.p.bias || g.p.residual || g.p.pre || g.p.fn != MOE_FN_NONE))
+        return launch_split_kind<ROWS_FWD, ACT, FULL>(g, mt, parts);
+    return launch_split_kind<MODE, ACT, PLAIN>(g, mt, parts);
 }
 
 }  // namespace

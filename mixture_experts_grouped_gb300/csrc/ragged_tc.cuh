@@ -45,8 +45,10 @@ namespace ragged {
 namespace {
 
 enum { ROWS_FWD = 0, ROWS_BACK = 1, WGRAD = 2 };
-// kinds of gradient: 16-bit, f32, f32 with an addend
-enum { G16 = 0, G32 = 1, GADD = 2 };
+// kinds of gradient: 16-bit, f32, f32 with an addend; of the rows form: the product alone, or with bias,
+// activation function, residual and z (their code, jumped over, still cost a plain product's epilogue half its time
+// in instruction fetches)
+enum { G16 = 0, G32 = 1, GADD = 2, PLAIN = 0, FULL = 3 };
 
 constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
@@ -231,32 +233,63 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
 
 // ---- epilogues --------------------------------------------------------------------------
 
+// Rows form: how a warp's 16 rows x 32 columns lie in memory, as 16-byte pieces of 8 columns: lane l has pieces of
+// rows l / 4 and 8 + l / 4.
+struct Piece {
+    int r, col;
+    __device__ __forceinline__ Piece(int i, int lane, int col0) : r(8 * i + (lane >> 2)), col(col0 + 8 * (lane & 3)) {}
+    __device__ __forceinline__ bool in(const RaggedParams& p, int rows) const { return r < rows && col < p.J; }
+    __device__ __forceinline__ size_t at(const RaggedParams& p, int m) const {
+        return static_cast<size_t>(m + r) * p.J + col;
+    }
+};
+struct Residual {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const RaggedParams& p, int lane, int m, int rows, int col0) {
+        if (!p.residual) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Piece c(i, lane, col0);
+            if (c.in(p, rows)) v[i] = *reinterpret_cast<const uint4*>(p.residual + c.at(p, m));
+        }
+    }
+};
+// brings the residual of rows m .. m + rows - 1 into L2, ahead of its use
+__device__ __forceinline__ void prefetch_residual(const RaggedParams& p, int lane, int m, int rows, int col0) {
+    if (!p.residual) return;
+    for (int r = lane >> 1; r < rows; r += 16) {
+        const int col = col0 + 16 * (lane & 1);
+        if (col < p.J)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + static_cast<size_t>(m + r) * p.J + col));
+    }
+}
+
 // Rows form: up to 16 rows x 32 columns z (lane = column, v[i] = row m + i) of a warp to
-// memory, through its staging area so that they leave as 16-byte pieces of 8 columns; the
-// piece's activation function and residual are applied on the way, in f32.
-template <int ACT>
-__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[16], float* stg, int lane, int m,
-                                           int rows, int col0) {
+// memory, through its staging area so that they leave as pieces; the piece's activation
+// function and residual are applied on the way, in f32.
+template <int ACT, int KIND>
+__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[16], const Residual& res, float* stg,
+                                           int lane, int m, int rows, int col0) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) stg[i * SG + lane] = v[i];
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = (i * 32 + lane) >> 2, col = col0 + 8 * (lane & 3);
-        if (r >= rows || col >= p.J) continue;
-        const float4 lo = *reinterpret_cast<const float4*>(stg + r * SG + 8 * (lane & 3));
-        const float4 hi = *reinterpret_cast<const float4*>(stg + r * SG + 8 * (lane & 3) + 4);
+        const Piece c(i, lane, col0);
+        if (!c.in(p, rows)) continue;
+        const float4 lo = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3));
+        const float4 hi = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3) + 4);
         float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const size_t at = static_cast<size_t>(m + r) * p.J + col;
-        if (p.pre) *reinterpret_cast<uint4*>(p.pre + at) = pack8<ACT>(f);
-        if (p.fn != MOE_FN_NONE)
+        const size_t at = c.at(p, m);
+        if (KIND == FULL) {
+            if (p.pre) *reinterpret_cast<uint4*>(p.pre + at) = pack8<ACT>(f);
+            fn_values(p.fn, f);
+            if (p.residual) {
+                float g[8];
+                unpack8<ACT>(res.v[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = fn_value(p.fn, f[j]);
-        if (p.residual) {
-            float g[8];
-            unpack8<ACT>(*reinterpret_cast<const uint4*>(p.residual + at), g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += g[j];
+                for (int j = 0; j < 8; ++j) f[j] += g[j];
+            }
         }
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = pack8<ACT>(f);
     }
@@ -284,20 +317,26 @@ __device__ __forceinline__ float bias_of(const RaggedParams& p, int col) {
     return Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.bias)[col]);
 }
 
-template <int ACT>
+template <int ACT, int KIND>
 __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta, float* stg, const Tile& t, int col0,
                                               int half, int lane) {
-    const float b = bias_of<ACT>(p, col0 + lane);
+    const float b = KIND == FULL ? bias_of<ACT>(p, col0 + lane) : 0.0f;
     uint32_t nx[16];
+    Residual res, res_nx;
     if (16 * half < t.rows) tmem_ld16(ta + 16 * half, nx);
+    if (KIND == FULL) res_nx.load(p, lane, t.m0 + 16 * half, t.rows - 16 * half, col0);
 #pragma unroll 1
     for (int c = 16 * half; c < t.rows; c += 32) {
         float v[16];
         tmem_ld16_wait(nx);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(nx[j]) + b;
+        for (int j = 0; j < 16; ++j) v[j] = KIND == FULL ? __uint_as_float(nx[j]) + b : __uint_as_float(nx[j]);
         if (c + 32 < t.rows) tmem_ld16(ta + c + 32, nx);  // in flight while this one is stored
-        store_rows<ACT>(p, v, stg, lane, t.m0 + c, t.rows - c, col0);
+        if (KIND == FULL) {
+            res = res_nx;
+            res_nx.load(p, lane, t.m0 + c + 32, t.rows - c - 32, col0);
+        }
+        store_rows<ACT, KIND>(p, v, res, stg, lane, t.m0 + c, t.rows - c, col0);
     }
 }
 
@@ -746,6 +785,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         for (int tile = first; tile < n_tiles; tile += step) {
             const Tile t = get_tile<MODE>(s, p, tile);
             const int chunks = chunks_of(t);
+            if constexpr (KIND == FULL) prefetch_residual(p, lane, t.m0, t.rows, t.j0 + n_off);
             if (!wait_full(cur)) break;
             const uint32_t ta = lanes + cur * 256, tb = lanes + (cur ^ 1u) * 256;
             bool ok = true;
@@ -764,7 +804,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                                                ew, n_off, half, lane, wc))
                     break;
             } else {
-                rows_epilogue<ACT>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, half, lane);
+                rows_epilogue<ACT, KIND>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, half, lane);
             }
             tc_fence_before();
             __syncwarp();
@@ -844,7 +884,9 @@ template <int MODE, int ACT> int launch_rows_form(const RaggedArgs& g, int maxu)
     m.ta = m.tb = m.out = m.add = m.b;
     // row tiles at most: one more per group than the rows fill
     const int64_t tiles = ((p.rows + 16 * p.maxu - 1) / (16 * p.maxu) + (p.E > 1 ? p.E : 0)) * ((p.J + 255) / 256);
-    return launch<MODE, ACT, G16>(m, p, tiles, g.st, g.who);
+    if (MODE == ROWS_FWD && (p.bias || p.residual || p.pre || p.fn != MOE_FN_NONE))
+        return launch<ROWS_FWD, ACT, FULL>(m, p, tiles, g.st, g.who);
+    return launch<MODE, ACT, PLAIN>(m, p, tiles, g.st, g.who);
 }
 
 }  // namespace
