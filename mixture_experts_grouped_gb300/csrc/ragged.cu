@@ -1,6 +1,7 @@
 // Products grouped by expert over ragged spans, their gradients, and the dense
 // product with its epilogue: entry points.
 #include "ragged.cuh"
+#include <math.h>
 
 namespace moe {
 namespace {
@@ -10,7 +11,9 @@ namespace {
 // Groups whose sizes only the device knows: CTA pairs, tiles of up to twice a group's mean
 // rows (3066 rows of 64 groups, most of 30 to 60: 71 us with tiles of 96 rows, 72 of 128, 74
 // of 256, whose over-wide boxes bring rows of the next groups along, 80 of 48, which read
-// the fuller groups' weights more than once).
+// the fuller groups' weights more than once); or, of at most 128 rows in all and few tiles,
+// the split form, by the same model with as many groups as rows dealt at random touch (34 rows
+// of 4 groups, 12320 x 840 transposed: pairs 45 us, split 21; 100 rows of 16 groups, 512 x 512: 7.1 and 5.7).
 //
 // One group (a dense product): the form, row tiles and split that a model of their time
 // finds best. Its costs (ns) are fitted to 110 sizes from 1 x 88 x 88 to 4000 x 2048 x 14336
@@ -28,45 +31,80 @@ struct RowsPick {
     RowsForm f;
     bool streaming;
 };
+
+struct Split {
+    int parts, launch_ns;
+};
+constexpr Split kSplits[] = {{1, 2620}, {2, 4940}, {4, 5410}, {8, 6610}};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
 RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
-    const int64_t U = (static_cast<int64_t>(p.rows) + 15) / 16, KB = (p.C + 63) / 64;
+    const int64_t U = ceil_div(p.rows, 16), KB = ceil_div(p.C, 64);
     RowsPick best{{1, 0, 0}, false};
-    if (p.offsets) {
-        const int64_t units = ((static_cast<int64_t>(p.rows) + p.E - 1) / p.E + 15) / 16;
-        best.f.maxu = static_cast<int>(units >= 8 ? 16 : 2 * units);
-        return best;
-    }
-    const int64_t J = p.J, bytes = 2 * J * p.C;
     int64_t best_ns = INT64_MAX;
-    auto ceil = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    auto max = [](int64_t a, int64_t b) { return a > b ? a : b; };
     auto offer = [&](int64_t ns, const RowsPick& pick) {
         if (ns < best_ns) {
             best_ns = ns;
             best = pick;
         }
     };
-    if (p.rows <= 32 && !transposed)
-        offer(2170 + max(bytes / 5700, 250 * ceil(KB, 8)) + 27 * p.rows * (2 * static_cast<int64_t>(p.C)) / 1024,
+    const int64_t J = p.J;
+    // groups that have rows, and the pairs' row tiles of a group, if all have the same
+    int64_t groups = 1, m0 = ceil_div(U, 16), m1 = U < m0 + 7 ? U : m0 + 7;
+    if (p.offsets) {
+        const int64_t units = ceil_div(ceil_div(p.rows, p.E), 16);
+        const int maxu = static_cast<int>(units >= 8 ? 16 : 2 * units);
+        if (p.rows > SPLIT_MAX_ROWS) return {{maxu, 0, 0}, false};
+        groups = static_cast<int64_t>(ceil(p.E * (1.0 - pow(1.0 - 1.0 / p.E, p.rows))));
+        m0 = m1 = 0;
+        offer(5130 + max64(ceil_div(groups * ceil_div(J, 256), sms / 2) * max64(KB * 200, 1500),
+                           2 * J * p.C * groups / 5000) + 240, {{maxu, 0, 0}, false});
+    }
+    const int64_t bytes = 2 * J * p.C * groups;
+    if (p.rows <= 32 && !transposed && !p.offsets)
+        offer(2170 + max64(bytes / 5700, 250 * ceil_div(KB, 8)) + 27 * p.rows * (2 * static_cast<int64_t>(p.C)) / 1024,
               {{0, 0, 0}, true});
-    static const struct {
-        int parts, launch_ns;
-    } splits[] = {{1, 2620}, {2, 4940}, {4, 5410}, {8, 6610}};
-    const int64_t mt = ceil(U, 8), h = ceil(U, mt) * 16, split_tiles = ceil(J, 128) * mt;
-    for (const auto& s : splits) {
-        const int64_t ctas = split_tiles * s.parts;
-        if (s.parts > KB || ctas > 4 * sms) break;
-        const int64_t blocks = ceil(KB, s.parts), load = ctas > sms ? 2 : 1;
+    const int64_t mt = p.offsets ? 1 : ceil_div(U, 8), h = p.offsets ? 16 : ceil_div(U, mt) * 16;
+    for (const auto& s : kSplits) {
+        const int64_t ctas = ceil_div(J, 128) * mt * groups * s.parts;
+        if (s.parts > KB || ceil_div(J, 128) * mt * (p.offsets ? p.E : 1) * s.parts > 4 * sms) break;
+        const int64_t blocks = ceil_div(KB, s.parts), load = ctas > sms ? 2 : 1;
         const int64_t body = blocks * (198 + h * 11 / 10);
-        const int64_t ns = max(max(body, load * blocks * (85 + h * 11 / 10)), bytes / 5600) +
-                           (ceil(ctas, 2 * sms) - 1) * (s.launch_ns + body) + s.launch_ns + 26 * h * load;
+        const int64_t ns = max64(max64(body, load * blocks * (85 + h * 11 / 10)), bytes / 5600) +
+                           (ceil_div(ctas, 2 * sms) - 1) * (s.launch_ns + body) + s.launch_ns + 26 * h * load;
         offer(ns, {{0, static_cast<int>(mt), s.parts}, false});
     }
-    const int64_t m0 = ceil(U, 16);
-    for (int64_t t = m0; t <= U && t < m0 + 8; ++t) {
-        const int64_t rows = ceil(U, t) * 16, waves = ceil(t * ceil(J, 256), sms / 2);
-        const int64_t ns = 5130 + max(waves * max(KB * (189 + rows * 4 / 10), 1300 + 15 * rows), bytes / 5000) + 15 * rows;
-        offer(ns, {{static_cast<int>(ceil(U, t)), 0, 0}, false});
+    for (int64_t t = m0; t <= m1 && t > 0; ++t) {
+        const int64_t rows = ceil_div(U, t) * 16, waves = ceil_div(t * ceil_div(J, 256), sms / 2);
+        const int64_t ns =
+            5130 + max64(waves * max64(KB * (189 + rows * 4 / 10), 1300 + 15 * rows), bytes / 5000) + 15 * rows;
+        offer(ns, {{static_cast<int>(ceil_div(U, t)), 0, 0}, false});
+    }
+    return best;
+}
+
+// Which form the gradient of a weight takes: 0 for CTA pairs; of one group with few tiles, the CTAs that share a
+// tile's rows, by the waves of tiles, their blocks of 64 rows and a launch as above. (us, pairs / split: 4096 rows, 512 x
+// 512 22.5 / 10.7; 2414 rows, 920 x 256 16.0 / 9.5; 30000 rows, 264 x 520 168 / 32; 1024 rows, 1024 x 1024 9.7 / 8.5; 1333 rows,
+// 2816 x 2048 18.6 / 26.4.) The sums of an f32 gradient take no more than 4096 rows each, as in the pairs' chunks.
+int pick_gradient_parts(const RaggedParams& p, bool f32, int sms) {
+    if (p.offsets || p.rows == 0) return 0;
+    const int64_t KB = ceil_div(p.rows, 64);
+    const int64_t waves = ceil_div(ceil_div(p.J, 256) * ceil_div(p.C, 256), sms / 2);
+    int64_t best_ns = 4300 + waves * max64(KB * 290, 1500);
+    int best = 0;
+    const int64_t tiles = ceil_div(p.J, 128) * ceil_div(p.C, 128);
+    for (const auto& s : kSplits) {
+        if (s.parts > KB || tiles * s.parts > 2 * sms) break;
+        const int64_t blocks = ceil_div(KB, s.parts);
+        if (f32 && blocks > 64) continue;
+        const int64_t ns = s.launch_ns + (tiles * s.parts > sms ? 2 : 1) * blocks * 230 + 2500;
+        if (ns < best_ns) {
+            best_ns = ns;
+            best = s.parts;
+        }
     }
     return best;
 }
@@ -153,6 +191,7 @@ extern "C" int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, cons
     g.K = K;
     g.st = static_cast<cudaStream_t>(stream);
     g.who = who;
+    g.parts = moe::pick_gradient_parts(g.p, dw_f32 != 0, moe::sm_count());
     return moe::launch_ragged_wgrad(g);
 }
 

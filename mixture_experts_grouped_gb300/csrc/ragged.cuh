@@ -42,15 +42,17 @@ struct RaggedArgs {
     const void *a, *w;  // rows form: rows, weights [E, .., ..]; gradient form: dy, x
     int act, transposed, f32;
     int N, K;           // the weight's shape
+    int parts;          // gradient form: CTAs that share a tile's contraction; 0: CTA pairs
     cudaStream_t st;
     const char* who;
 };
 
 // How a product of rows runs: on CTA pairs, row tiles of up to maxu units of 16 rows; or, with
-// parts > 0, one group split: row tiles, and CTAs that share a tile's contraction.
+// parts > 0, split: row tiles, and CTAs that share a tile's contraction.
 struct RowsForm {
     int maxu, tiles, parts;
 };
+constexpr int SPLIT_MAX_ROWS = 128;  // most rows of groups that the split form takes
 
 // What a kernel's first launch on a device found out or set (0: not yet), for launches from any thread.
 struct PerDevice {

@@ -1,5 +1,5 @@
-// Dense products of few tiles (ragged products of one group): one 128-column tile to a
-// cluster of CTAs, each with a part of the contraction.
+// Products of few tiles: one 128-column tile to a cluster of CTAs, each with a part of the
+// contraction.
 //
 // With few rows a product is bound by its weights' bytes, and only if every SM streams
 // them: 4096 columns are 16 tiles of the pair form, and 32 SMs drew 2.3 TB/s. Here a tile is
@@ -10,6 +10,12 @@
 // placed at once.) Every wait is bounded. Measured: 37 x 4096 x 14336 26.5 us, 4.5 TB/s (52
 // with pairs); 37 x 2816 x 2048 8.0 us, most of it launch, first copies, and the cluster's two
 // meetings (2.5 us).
+//
+// Groups (with offsets, at most 128 rows in all): a tile for every group and 128 columns;
+// those of empty groups leave at once.
+//
+// Gradient of one group's weight: a tile is 128 rows n by 128 columns k of it, the
+// contraction runs over the rows (past their end the copies bring zeros).
 #pragma once
 
 #include "ragged_tc.cuh"
@@ -21,6 +27,7 @@ namespace {
 constexpr int SPLIT_THREADS = 192;
 constexpr int SPLIT_MAX_STAGES = 8;
 constexpr int SPLIT_ROWS = 128;  // most rows of a tile
+static_assert(SPLIT_MAX_ROWS <= SPLIT_ROWS, "a group is one tile");
 constexpr int SPLIT_PARTS = 8;   // most CTAs of a tile
 
 struct SplitTail {
@@ -32,14 +39,32 @@ struct SplitTail {
 struct SplitParams {
     RaggedParams r;
     int parts, stages;
-    int mt;        // row tiles
-    int box;       // rows of the N operand's boxes: the tallest tile
+    int mt;        // row tiles of one group; gradient: tiles of k
+    int box;       // rows of the N operand's boxes: the tallest tile, or with groups 16, as many boxes as a tile needs
+    int stage;     // bytes of a stage
     int tmem;      // TMEM columns
     int tail_at;   // after the stages
 };
 
 __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
     tma_load_3d(dst, map, c0, c1, c2, bar);
+}
+
+// four columns k .. of row n of one group's weight gradient
+template <int ACT, int KIND>
+__device__ __forceinline__ void store_gradient(const RaggedParams& p, int n, int k, float4 f) {
+    if (n >= p.J || k >= p.C) return;
+    const size_t at = static_cast<size_t>(n) * p.C + k;
+    if (KIND == G16) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+            make_uint2(Act<ACT>::pack2(f.x, f.y), Act<ACT>::pack2(f.z, f.w));
+    } else {
+        if (p.addend) {
+            const float4 a = *reinterpret_cast<const float4*>(p.addend + at);
+            f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
+    }
 }
 
 template <int MODE, int ACT, int KIND>
@@ -52,13 +77,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = sp.parts, part = parts > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int tile = blockIdx.x / parts;
-    // row tiles fastest: those of a column tile share its weights in L2
-    const int i = tile % sp.mt, j0 = tile / sp.mt * 128;
-    const int U = (p.rows + 15) / 16, u0 = static_cast<int>(static_cast<int64_t>(U) * i / sp.mt),
-              u1 = static_cast<int>(static_cast<int64_t>(U) * (i + 1) / sp.mt);
-    const int m0 = 16 * u0, n = 16 * (u1 - u0), rows = min(p.rows - m0, n);
-    const int KB = (p.C + BK - 1) / BK, kb0 = KB * part / parts, kb1 = KB * (part + 1) / parts;
-    const uint32_t stage_bytes = OPER + sp.box * 128;
+    const int KB = ((MODE == WGRAD ? p.rows : p.C) + BK - 1) / BK, kb0 = KB * part / parts, kb1 = KB * (part + 1) / parts;
 
     if (tid == 0) {
         s.abort_flag = 0;
@@ -83,24 +102,62 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
-    bool ok = true;  // (a wait that gave up in another CTA of the cluster shows in the error word alone)
+    // the tile: columns j0 .. (or rows n of a gradient), rows m0 .. (columns k), n of them for the MMA
+    int e = 0, j0, m0, n, rows;
+    if (MODE != WGRAD && p.offsets) {
+        int bad = 0;
+        for (int i = tid; i < p.E; i += SPLIT_THREADS) bad |= p.offsets[i + 1] < p.offsets[i];
+        if (tid == 0) bad |= p.offsets[0] < 0 || p.offsets[p.E] > p.rows;
+        bad = __syncthreads_or(bad);
+        if (bad && tid == 0 && blockIdx.x == 0) set_err(p.err, MOE_DEV_ERR_OFFSETS);
+        const int jt = (p.J + 127) / 128;
+        e = tile / jt;
+        j0 = (tile - e * jt) * 128;
+        m0 = p.offsets[e];
+        rows = bad ? 0 : p.offsets[e + 1] - m0;
+        n = (rows + 15) / 16 * 16;
+    } else {
+        // row tiles fastest: those of a column tile share its weights in L2
+        const int i = tile % sp.mt;
+        j0 = tile / sp.mt * 128;
+        if (MODE == WGRAD) {
+            m0 = 128 * i;
+            n = rows = 128;
+        } else {
+            const int U = (p.rows + 15) / 16, u0 = static_cast<int>(static_cast<int64_t>(U) * i / sp.mt),
+                      u1 = static_cast<int>(static_cast<int64_t>(U) * (i + 1) / sp.mt);
+            m0 = 16 * u0;
+            n = 16 * (u1 - u0);
+            rows = min(p.rows - m0, n);
+        }
+    }
+    const bool any = rows > 0;  // the same in all CTAs of the cluster
+    const int boxes = MODE == WGRAD ? 0 : p.offsets ? n / 16 : 1;
+    const uint32_t bytes = OPER + (MODE == WGRAD ? OPER : boxes * sp.box * 128), stage_bytes = sp.stage;
+    bool ok = any;  // (a wait that gave up in another CTA of the cluster shows in the error word alone)
 
     if (warp == 0) {
         // ---------------- copies ----------------
         int stage = 0, issued = 0;
         uint32_t phase = 0;
-        for (int b = kb0; b < kb1; ++b) {
+        for (int b = kb0; any && b < kb1; ++b) {
             if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) break;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&s.full[stage], stage_bytes);
+                mbar_arrive_expect_tx(&s.full[stage], bytes);
                 uint8_t* dst = smem + stage * stage_bytes;
-                if (MODE == ROWS_FWD) {
-                    load_3d(dst, &tm_a, b * BK, j0, 0, &s.full[stage]);
+                if (MODE == WGRAD) {
+                    tma_load_2d(dst, &tm_a, j0, b * BK, &s.full[stage]);
+                    tma_load_2d(dst + 8192, &tm_a, j0 + 64, b * BK, &s.full[stage]);
+                    tma_load_2d(dst + OPER, &tm_b, m0, b * BK, &s.full[stage]);
+                    tma_load_2d(dst + OPER + 8192, &tm_b, m0 + 64, b * BK, &s.full[stage]);
+                } else if (MODE == ROWS_FWD) {
+                    load_3d(dst, &tm_a, b * BK, j0, e, &s.full[stage]);
                 } else {
-                    load_3d(dst, &tm_a, j0, b * BK, 0, &s.full[stage]);
-                    load_3d(dst + 8192, &tm_a, j0 + 64, b * BK, 0, &s.full[stage]);
+                    load_3d(dst, &tm_a, j0, b * BK, e, &s.full[stage]);
+                    load_3d(dst + 8192, &tm_a, j0 + 64, b * BK, e, &s.full[stage]);
                 }
-                tma_load_2d(dst + OPER, &tm_b, b * BK, m0, &s.full[stage]);
+                for (int i = 0; i < boxes; ++i)
+                    tma_load_2d(dst + OPER + i * 2048, &tm_b, b * BK, m0 + 16 * i, &s.full[stage]);
             }
             __syncwarp();
             ++issued;
@@ -114,18 +171,20 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_drain(&s.full[j % sp.stages], static_cast<uint32_t>((j / sp.stages) & 1), kWaitLimitNs / 8);
     } else if (warp == 1) {
         // ---------------- MMAs ----------------
-        constexpr uint32_t step_a = MODE == ROWS_FWD ? 32 >> 4 : 2048 >> 4;
-        const uint32_t idesc = f16_idesc(ACT, 128, n) | (MODE == ROWS_BACK ? kMajorA : 0u);
+        constexpr uint32_t step_a = MODE == ROWS_FWD ? 32 >> 4 : 2048 >> 4, step_b = MODE == WGRAD ? 2048 >> 4 : 32 >> 4;
+        const uint32_t idesc = f16_idesc(ACT, 128, n) | (MODE == ROWS_FWD ? 0u : kMajorA) | (MODE == WGRAD ? kMajorB : 0u);
         int stage = 0;
         uint32_t phase = 0;
-        for (int b = kb0; b < kb1; ++b) {
+        for (int b = kb0; any && b < kb1; ++b) {
             if (!mbar_wait_warp(&s.full[stage], phase, wc)) break;
             tc_fence_after();
             const uint32_t at = smem_u32(smem + stage * stage_bytes);
-            const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at), bd = sw128_desc(at + OPER);
+            const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
+            const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
             if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k) tc_mma(tmem, ad + k * step_a, bd + 2 * k, idesc, b > kb0 || k > 0);
+                for (int k = 0; k < BK / 16; ++k)
+                    tc_mma(tmem, ad + k * step_a, bd + k * step_b, idesc, b > kb0 || k > 0);
                 tc_commit(&s.empty[stage]);
             }
             __syncwarp();
@@ -139,7 +198,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         mbar_drain(&s.done, 0, kWaitLimitNs / 8);
     } else {
         if constexpr (KIND == FULL) prefetch_residual(p, lane, m0, rows, j0 + 32 * (warp & 3));
-        ok = mbar_wait_warp(&s.done, 0, wc);
+        ok = mbar_wait_warp(&s.done, 0, wc) && any;
         tc_fence_after();
     }
     __syncwarp();
@@ -162,9 +221,15 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 tmem_ld16_wait(u);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]) + bias;
-                store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + c, rows - c, j0 + 32 * q);
+                if constexpr (MODE == WGRAD) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        store_gradient<ACT, KIND>(p, j0 + me, m0 + c + j, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+                } else {
+                    store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + c, rows - c, j0 + 32 * q);
+                }
             }
-    } else {
+    } else if (any) {
         cluster_sync_all();  // every CTA's MMAs are complete: the stages are free
         // part d adds rows 4 f(d) to 4 f(d + 1), f(d) = n / 4 d / parts: four rows of a column are a 16-byte store.
         // There, [source part][four rows][128 columns][4]
@@ -218,12 +283,16 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                             f.w += x.w;
                         }
                     }
+                    if constexpr (MODE == WGRAD) {
+                        if (c + 4 * j < have) store_gradient<ACT, KIND>(p, j0 + me, m0 + 4 * q0 + c + 4 * j, f);
+                    }
                     v[4 * j] = f.x + bias;
                     v[4 * j + 1] = f.y + bias;
                     v[4 * j + 2] = f.z + bias;
                     v[4 * j + 3] = f.w + bias;
                 }
-                store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
+                if constexpr (MODE != WGRAD)
+                    store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
             }
         }
     }
@@ -241,13 +310,13 @@ static_assert(3 * (OPER + SPLIT_ROWS * 128) >= split_sums(SPLIT_ROWS) + 4 * STG_
                   3 * (OPER + 48 * 128) >= split_sums(48) + 4 * STG_ROWS * SG * 4,
               "the epilogue's areas fit in the stages");
 
-template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g, int mt, int parts) {
+// tiles: clusters of the grid; mt as in SplitParams
+template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g, int64_t tiles, int mt, int parts) {
     auto kernel = split_kernel<MODE, ACT, KIND>;
     // of shared memory: two CTAs to an SM, or all where there are fewer CTAs than SMs (clusters of 8 with an SM
     // each do not fill the GPU: 128 CTAs of 2048 columns take 11.8 us so, two to an SM 7.5)
     constexpr int all = 229376, half = 114688;
-    const int64_t ctas = static_cast<int64_t>((g.p.J + 127) / 128) * mt * parts;
-    const int most = parts < 8 && ctas * 10 <= sm_count() * 9 ? all : half;
+    const int most = parts < 8 && tiles * parts * 10 <= sm_count() * 9 ? all : half;
     static PerDevice configured;
     int rc = raise_smem_limit(configured, reinterpret_cast<const void*>(kernel), all);
     if (rc != MOE_OK) return rc;
@@ -255,16 +324,22 @@ template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g
     sp.r = g.p;
     sp.parts = parts;
     sp.mt = mt;
-    sp.box = ((g.p.rows + 15) / 16 + mt - 1) / mt * 16;
-    sp.tmem = sp.box <= 32 ? 32 : sp.box <= 64 ? 64 : 128;
+    const int rows = MODE == WGRAD ? SPLIT_ROWS : ((g.p.rows + 15) / 16 + mt - 1) / mt * 16;  // of the tallest tile
+    sp.box = MODE == WGRAD ? 64 : g.p.offsets ? 16 : rows;
+    sp.tmem = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     const int rest = static_cast<int>(sizeof(SplitTail));
-    const int stage = OPER + sp.box * 128;
-    sp.stages = (most - rest) / stage;  // 3 at least
+    sp.stage = OPER + rows * 128;
+    sp.stages = (most - rest) / sp.stage;  // 3 at least
     if (sp.stages > SPLIT_MAX_STAGES) sp.stages = SPLIT_MAX_STAGES;
-    sp.tail_at = sp.stages * stage;
+    sp.tail_at = sp.stages * sp.stage;
     Maps m;
-    rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, 1, 64, MODE == ROWS_FWD ? 128 : 64);
-    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, g.p.rows, g.p.C, sp.box, g.act);
+    if (MODE == WGRAD) {
+        rc = make_tmap_2d(&m.a, g.a, g.p.rows, g.N, 64, g.act);
+        if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.w, g.p.rows, g.K, 64, g.act);
+    } else {
+        rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, g.p.E, 64, MODE == ROWS_FWD ? 128 : 64);
+        if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, g.p.rows, g.p.C, sp.box, g.act);
+    }
     if (rc != MOE_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -274,7 +349,7 @@ template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g
     attr[1].val.clusterDim.x = parts;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>((g.p.J + 127) / 128) * mt * parts);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * parts));
     cfg.blockDim = dim3(SPLIT_THREADS);
     cfg.dynamicSmemBytes = sp.tail_at + rest;
     cfg.stream = g.st;
@@ -286,10 +361,12 @@ template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g
     return check_launch(g.who);
 }
 
+// row tiles of one group, or every group with a tile
 template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int parts) {
+    const int64_t tiles = static_cast<int64_t>((g.p.J + 127) / 128) * (g.p.offsets ? g.p.E : mt);
     if (MODE == ROWS_FWD && (g.p.bias || g.p.residual || g.p.pre || g.p.fn != MOE_FN_NONE))
-        return launch_split_kind<ROWS_FWD, ACT, FULL>(g, mt, parts);
-    return launch_split_kind<MODE, ACT, PLAIN>(g, mt, parts);
+        return launch_split_kind<ROWS_FWD, ACT, FULL>(g, tiles, mt, parts);
+    return launch_split_kind<MODE, ACT, PLAIN>(g, tiles, mt, parts);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // Gradient form of the ragged products.
-#include "ragged_tc.cuh"
+#include "ragged_split.cuh"
 
 namespace moe {
 namespace ragged {
@@ -32,6 +32,12 @@ template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
 }
 
 template <int ACT> int by_kind(const RaggedArgs& g) {
+    if (g.parts) {
+        const int kt = (g.p.C + 127) / 128;
+        const int64_t tiles = static_cast<int64_t>((g.p.J + 127) / 128) * kt;
+        return g.f32 ? launch_split_kind<WGRAD, ACT, G32>(g, tiles, kt, g.parts)
+                     : launch_split_kind<WGRAD, ACT, G16>(g, tiles, kt, g.parts);
+    }
     if (!g.f32) return gradient_form<ACT, G16>(g);
     return g.p.addend ? gradient_form<ACT, GADD>(g) : gradient_form<ACT, G32>(g);
 }

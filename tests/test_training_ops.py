@@ -261,6 +261,46 @@ def test_weight_gradient_of_layers(moe, dev, rows, E, N, K, f32):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,N,K", [(1, 8, 8), (70, 72, 136), (300, 264, 520), (600, 520, 264), (1000, 1032, 1000),
+                                      (2414, 920, 256), (4097, 512, 520), (9000, 264, 136), (30000, 264, 520),
+                                      (1333, 2816, 2048)])
+def test_weight_gradient_of_one_group_in_every_form(moe, dev, rows, N, K):
+    """Without offsets: pairs, or one to eight CTAs that share a tile's rows; and with, where only pairs do."""
+    g = torch.Generator(device=dev).manual_seed(rows)
+    for act, i in (("bf16", 0), ("f16", 1)):
+        dy, x = (torch.randn((rows, n), generator=g, device=dev).to(plain.DT[act]) for n in (N, K))
+        add = torch.randn((N, K), generator=g, device=dev)
+        ref, mag = dy.double().T @ x.double(), dy.double().abs().T @ x.double().abs()
+        for off in (None, torch.tensor([0, rows], dtype=torch.int32, device=dev)):
+            for f32, addend in ((False, None), (True, None), (True, add), (True, "in place")):
+                outs = []
+                for _ in range(2):
+                    dw = torch.full((N, K), 3.0, dtype=torch.float32 if f32 else plain.DT[act], device=dev)
+                    if addend == "in place":
+                        dw = add.clone()
+                    moe.moe_ragged_wgrad(dy, x, i, off, rows, N, K, 1, dw if addend == "in place" else addend, dw, f32)
+                    outs.append(dw)
+                assert torch.equal(*outs)
+                if f32:
+                    want, m = (ref + add.double(), mag + add.double().abs()) if addend is not None else (ref, mag)
+                    assert torch.all((dw.double() - want).abs() <= sum_slack(m, rows + 1))
+                    assert float((dw.double() - want).norm()) <= (4096 / 16 / 2 + 16) * F32 * float(want.norm())
+                else:
+                    plain.close(dw, ref.cpu(), act, sum_slack(mag, rows).cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("counts,N,K", [([0, 9, 25, 0], 840, 1320), ([2, 1, 0], 72, 4104), ([60, 3, 65], 520, 200),
+                                        ([128], 136, 2056), ([7] * 16, 512, 520), ([1] * 128, 136, 72), ([0] * 4, 72, 72)])
+def test_few_rows_of_groups(moe, dev, counts, N, K, transposed):
+    for j, act in enumerate(("bf16", "f16")):
+        ragged_case(moe, dev, counts, N, K, act, transposed, 7 + j)
+        if sum(counts) <= 100:
+            ragged_case(moe, dev, counts, N, K, act, transposed, 9 + j, lead=5, tail=20)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("off", [[0, 5, 4, 9], [-1, 3, 5, 9], [0, 3, 5, 11], [2 ** 31 - 1, 0, 5, 9], [5, 3, 2, 1]])
 def test_bad_offsets_are_reported_and_compute_nothing(moe, dev, off):
     off = torch.tensor(off, dtype=torch.int32, device=dev)
