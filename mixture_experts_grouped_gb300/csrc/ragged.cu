@@ -90,7 +90,7 @@ RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
 // 512 22.5 / 10.7; 2414 rows, 920 x 256 16.0 / 9.5; 30000 rows, 264 x 520 168 / 32; 1024 rows, 1024 x 1024 9.7 / 8.5; 1333 rows,
 // 2816 x 2048 18.6 / 26.4.) The sums of an f32 gradient take no more than 4096 rows each, as in the pairs' chunks.
 int pick_gradient_parts(const RaggedParams& p, bool f32, int sms) {
-    if (p.offsets || p.rows == 0) return 0;
+    if (p.offsets || p.rows == 0 || sms < 2) return 0;  // (without a device the launch reports it)
     const int64_t KB = ceil_div(p.rows, 64);
     const int64_t waves = ceil_div(ceil_div(p.J, 256) * ceil_div(p.C, 256), sms / 2);
     int64_t best_ns = 4300 + waves * max64(KB * 290, 1500);

@@ -883,7 +883,7 @@ template <int MODE, int ACT> int launch_rows_form(const RaggedArgs& g, int maxu)
     if (rc != MOE_OK) return rc;
     m.ta = m.tb = m.out = m.add = m.b;
     // row tiles at most: one more per group than the rows fill
-    const int64_t tiles = ((p.rows + 16 * p.maxu - 1) / (16 * p.maxu) + (p.E > 1 ? p.E : 0)) * ((p.J + 255) / 256);
+    const int64_t tiles = (static_cast<int64_t>((p.rows + 16 * p.maxu - 1) / (16 * p.maxu)) + (p.E > 1 ? p.E : 0)) * ((p.J + 255) / 256);
     if (MODE == ROWS_FWD && (p.bias || p.residual || p.pre || p.fn != MOE_FN_NONE))
         return launch<ROWS_FWD, ACT, FULL>(m, p, tiles, g.st, g.who);
     return launch<MODE, ACT, PLAIN>(m, p, tiles, g.st, g.who);

@@ -1,6 +1,10 @@
 """Ragged products, the 16-bit dense product and the row operators of a training step against plain
 64-bit forms, their gradients against differences, and their refusals."""
 import math
+import os
+import pathlib
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -1057,6 +1061,32 @@ def test_no_rows_is_a_no_op(moe):
     moe.moe_combine_backward(None, None, 0, None, None, None, None, 0, 64, 2, 0, 0, 0)
     moe.moe_route_backward(None, None, None, None, None, 0, 8, 2, 1, 0, 0)
     assert moe.moe_launch_count() == n0
+
+
+def test_products_without_a_device_fail_with_a_status(moe):
+    calls = """
+import sys
+from mixture_experts_grouped_gb300 import moe as m
+A = 1 << 20
+for call in (lambda: m.moe_ragged_gemm(A, 0, A, 0, A, 4, 64, 64, 2, A, 0, 0),
+             lambda: m.moe_ragged_gemm(A, 0, A, 1, None, 400, 64, 64, 1, A, 0, 0),
+             lambda: m.moe_dense_gemm(A, 0, A, None, 0, None, None, A, 4, 64, 64, 0, 0),
+             lambda: m.moe_ragged_wgrad(A, A, 0, None, 4, 64, 64, 1, None, A, 1, 0, 0),
+             lambda: m.moe_ragged_wgrad(A, A, 0, A, 4, 64, 64, 2, None, A, 0, 0, 0),
+             lambda: m.moe_bias_act_backward(A, A, 0, 1, 4, 64, A, A, 0, 0),
+             lambda: m.moe_swiglu(A, 0, 4, 64, A, 0),
+             lambda: m.moe_dispatch(A, 0, A, A, 4, 64, 2, 8, 0, 0)):
+    try:
+        call()
+    except m.MoeError as e:
+        assert e.status == m.MOE_ERR_CUDA, e
+    else:
+        sys.exit("a call went through")
+"""
+    root = pathlib.Path(__file__).resolve().parents[1]
+    r = subprocess.run([sys.executable, "-c", calls], cwd=root, env={**os.environ, "CUDA_VISIBLE_DEVICES": ""},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr)
 
 
 @pytest.mark.gpu
