@@ -549,8 +549,8 @@ int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* top
  * The sorted rows of a training step are ragged: group e is the rows
  * [offsets[e], offsets[e + 1]), of any number, with no padding (align with
  * block_size 1), offsets[0] >= 0 and offsets[E] <= rows. Rows outside every
- * group are neither read nor written. Offsets that decrease or leave [0, rows]
- * set MOE_DEV_ERR_OFFSETS and nothing is computed. With offsets NULL, E must be
+ * group are left as they are, and what they hold reaches no result. Offsets that
+ * decrease or leave [0, rows] set MOE_DEV_ERR_OFFSETS and nothing is computed. With offsets NULL, E must be
  * 1 and the group is all rows (a dense product). Sums are f32, in an order that
  * depends on the sizes alone; each output is rounded once.
  */
@@ -656,7 +656,7 @@ int moe_dispatch(const void* x, int32_t act, const int32_t* pair_to_row, void* x
  * Gradient of moe_combine, for pairs (t, j) with row r = pair_to_row[t * top_k + j]:
  *     d_y[r] = act( topk_weights[t, j] * d_out[t] ),   d_weights[t, j] = sum_h d_out[t, h] * y[r, h]
  * Dropped pairs (r < 0) get d_weights 0 and write no row, as do rows >= max_rows
- * (which set MOE_DEV_ERR_PAIR_ID).
+ * (which set MOE_DEV_ERR_PAIR_ID). No two pairs have the same row.
  *   d_out         device act [T, H];  y  device act [max_rows, H]
  *   topk_weights  device f32 [T, top_k]
  *   d_y           device act [max_rows, H] out; may be y

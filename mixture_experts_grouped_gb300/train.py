@@ -149,8 +149,10 @@ class DenseMlp:
         self.x = None
 
     def forward(self, x, residual=None, stream=None):
-        """The block on x [T, H]; returns its output buffer. x is kept for ``backward``."""
+        """The block on x [T, H]; returns its output buffer. x is kept for ``backward`` and must not change before it."""
         _require("x", x, self.dtype, self.T, self.H)
+        if x.data_ptr() in (self.out.data_ptr(), self.d_x.data_ptr()):
+            raise ValueError("x is a buffer of the block itself, which a pass overwrites")
         if residual is not None:
             _require("residual", residual, self.dtype, self.T, self.H)
         self.x = x

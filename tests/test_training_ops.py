@@ -463,6 +463,60 @@ def test_split_product_ends_whatever_wait_runs_out(moe, dev, M, N, K, limit_ns):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("limit_ns", [1, 100, 1500, 4000])
+@pytest.mark.parametrize("counts,N,K", [([30, 0, 41, 29], 520, 4096), ([5] * 16, 136, 328)])
+def test_split_groups_end_whatever_wait_runs_out(moe, dev, counts, N, K, limit_ns):
+    """As above, few rows of several groups, both directions; and the gradient of one group's weight, whose tiles
+    the same kernel splits."""
+    rows, E = sum(counts), len(counts)
+    g = torch.Generator(device=dev).manual_seed(2)
+    a, b, w = (torch.randn(s, generator=g, device=dev).bfloat16() for s in ((rows, K), (rows, N), (E, N, K)))
+    dy, x = (torch.randn(s, generator=g, device=dev).bfloat16() for s in ((4096, 264), (4096, 136)))
+    off = offsets_of(counts).to(dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def calls():
+        outs = [torch.empty(s, dtype=torch.bfloat16, device=dev) for s in ((rows, N), (rows, K))]
+        outs.append(torch.zeros((264, 136), device=dev))
+        return outs, (lambda: moe.moe_ragged_gemm(a, 0, w, False, off, rows, N, K, E, outs[0], err),
+                      lambda: moe.moe_ragged_gemm(b, 0, w, True, off, rows, N, K, E, outs[1], err),
+                      lambda: moe.moe_ragged_wgrad(dy, x, 0, None, 4096, 264, 136, 1, None, outs[2], True, err))
+
+    want, run = calls()
+    for f in run:
+        f()
+    outs, run = calls()
+    for i, f in enumerate(run):
+        torch.empty(1 << 28, device=dev).zero_()
+        old = moe.moe_set_wait_limit_ns(limit_ns)
+        try:
+            f()
+            torch.cuda.synchronize()
+        finally:
+            moe.moe_set_wait_limit_ns(old)
+        assert err.item() in (0, moe.MOE_DEV_ERR_TIMEOUT)
+        assert err.item() or torch.equal(outs[i], want[i])
+        err.zero_()
+        f()
+        torch.cuda.synchronize()
+        assert err.item() == 0 and torch.equal(outs[i], want[i])
+
+
+@pytest.mark.gpu
+def test_dense_block_refuses_its_own_buffers(moe, dev):
+    from mixture_experts_grouped_gb300 import train
+    bf = dict(dtype=torch.bfloat16, device=dev)
+    block = train.DenseMlp(4, 64, 32, "bf16", "gelu", torch.zeros((32, 64), **bf), None, torch.zeros((64, 32), **bf), None)
+    x = torch.ones((4, 64), **bf)
+    out = block.forward(x)
+    with pytest.raises(ValueError):
+        block.forward(out)
+    with pytest.raises(ValueError):
+        block.forward(block.backward(x))
+    block.forward(x, residual=out)  # (added in place, each element by the thread that writes it)
+
+
+@pytest.mark.gpu
 def test_tensors_past_32_bits_of_elements(moe, dev):
     """Rows, weights and gradients whose offsets pass 2^31 elements (4.3 GB each)."""
     H, R = 8192, 270000
