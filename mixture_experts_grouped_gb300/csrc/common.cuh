@@ -36,9 +36,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
     } while (0)
 
 // Encode a 2-D bf16/fp16 tensor map: rows x cols (cols contiguous), box
-// box_rows x 64 elements (128 bytes, the 128-byte swizzle span).
+// box_rows x 64 elements (128 bytes, the 128-byte swizzle span). reused: many
+// CTAs read the tensor from L2.
 int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
-                 uint32_t box_rows, int act);
+                 uint32_t box_rows, int act, bool reused = false);
 // Encode a plain (unswizzled) 2-D tensor map of any element type: rows x cols
 // elements of elem_bytes each, box box_rows x box_cols.
 int make_tmap_2d_raw(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t rows,
@@ -53,7 +54,8 @@ int make_tmap_2d_out(CUtensorMap* map, void* base, uint64_t rows, uint64_t cols,
 // Encode a dense 3-D tensor map with the 128-byte swizzle: d2 matrices of d1 rows x
 // d0 elements, box 1 x b1 x b0 (b0 elements are 128 bytes); act is MOE_ACT_* or kTmapF32.
 constexpr int kTmapF32 = 100;
-int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1);
+int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
+                 bool reused = false);
 // Encode a plain 3-D tensor map: dims d0 (contiguous) x d1 x d2 elements,
 // byte strides s1 (between d1 steps) and s2 (between d2 steps), box
 // b0 x b1 x b2. Used to fetch two separated halves of a weight tile with one

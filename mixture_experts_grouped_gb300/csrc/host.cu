@@ -82,8 +82,15 @@ int set_smem_limit(const void* kernel, int bytes) {
     return MOE_OK;
 }
 
+// How far a load of 128 bytes of a row reaches in L2: 256 bytes, which streams from HBM best (64 rows over 128 groups of
+// 1160 x 2056: 49.5 us, 50.8 with 128); 128 for tensors that many CTAs read from L2 where their rows begin between
+// sectors of 32 bytes (3117 x 2048 x 13960: 172 us with 256, 150 with 128; with rows of a multiple of 32 bytes 1% the other way).
+static CUtensorMapL2promotion l2_promotion(uint64_t pitch, bool reused) {
+    return reused && pitch % 32 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+}
+
 int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
-                 int act) {
+                 int act, bool reused) {
     auto fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     if (!aligned16(base)) return fail(MOE_ERR_INVALID, "tensor base address %p is not 16-byte aligned", base);
@@ -95,8 +102,7 @@ int make_tmap_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(map, act == MOE_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                     2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_SWIZZLE_128B, l2_promotion(strides[0], reused), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(MOE_ERR_INVALID, "cuTensorMapEncodeTiled failed (%d) for a %llux%llu tensor", (int)r,
                     (unsigned long long)rows, (unsigned long long)cols);
@@ -181,7 +187,8 @@ int make_tmap_5d(CUtensorMap* map, const void* base, int act, const uint64_t (&d
     return MOE_OK;
 }
 
-int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1) {
+int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
+                 bool reused) {
     auto fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     if (!aligned16(base)) return fail(MOE_ERR_INVALID, "tensor base address %p is not 16-byte aligned", base);
@@ -194,7 +201,7 @@ int make_tmap_3d(CUtensorMap* map, void* base, int act, uint64_t d0, uint64_t d1
                                    : act == MOE_ACT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUresult r = fn(map, dt, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_SWIZZLE_128B, l2_promotion(strides[0], reused), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(MOE_ERR_INVALID, "cuTensorMapEncodeTiled failed (%d) for a %llux%llux%llu tensor", (int)r,
                     (unsigned long long)d0, (unsigned long long)d1, (unsigned long long)d2);

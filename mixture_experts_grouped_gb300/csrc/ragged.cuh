@@ -27,6 +27,7 @@ struct RaggedParams {
     int rows, E;
     int J, C;                // rows form: output columns, contraction; gradient form: n, k
     int maxu;                // rows form: most units of 16 rows a tile has
+    FastDiv units;           // rows form: by maxu
     FastDiv kt, per;         // gradient form: tiles of a row of tiles, and of a group
     void* out;
     const uint16_t *bias, *residual;  // rows form

@@ -30,6 +30,9 @@ constexpr int SPLIT_ROWS = 128;  // most rows of a tile
 static_assert(SPLIT_MAX_ROWS <= SPLIT_ROWS, "a group is one tile");
 constexpr int SPLIT_PARTS = 8;   // most CTAs of a tile
 
+constexpr int STG_ROWS = 16;  // rows of an epilogue warp's staging area
+constexpr int SG = 36;        // and their stride (floats): 16-byte reads without conflicts
+
 struct SplitTail {
     uint64_t full[SPLIT_MAX_STAGES], empty[SPLIT_MAX_STAGES], done;
     uint32_t tmem_base;
@@ -48,6 +51,50 @@ struct SplitParams {
 
 __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
     tma_load_3d(dst, map, c0, c1, c2, bar);
+}
+
+struct Residual {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const RaggedParams& p, int lane, int m, int rows, int col0) {
+        if (!p.residual) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Piece c(i, lane, col0);
+            if (c.in(p, rows)) v[i] = *reinterpret_cast<const uint4*>(p.residual + c.at(p, m));
+        }
+    }
+};
+
+// Up to 16 rows x 32 columns z (lane = column, v[i] = row m + i) of a warp to
+// memory, through its staging area so that they leave as pieces; the piece's activation
+// function and residual are applied on the way, in f32.
+template <int ACT, int KIND>
+__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[16], const Residual& res, float* stg,
+                                           int lane, int m, int rows, int col0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) stg[i * SG + lane] = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Piece c(i, lane, col0);
+        if (!c.in(p, rows)) continue;
+        const float4 lo = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3));
+        const float4 hi = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3) + 4);
+        float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const size_t at = c.at(p, m);
+        if (KIND == FULL) {
+            if (p.pre) *reinterpret_cast<uint4*>(p.pre + at) = pack8<ACT>(f);
+            fn_values(p.fn, f);
+            if (p.residual) {
+                float g[8];
+                unpack8<ACT>(res.v[i], g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] += g[j];
+            }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = pack8<ACT>(f);
+    }
+    __syncwarp();
 }
 
 // four columns k .. of row n of one group's weight gradient

@@ -54,8 +54,7 @@ constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
 constexpr int STAGE = 2 * OPER;
 constexpr int MAX_STAGES = 10;
-constexpr int STG_ROWS = 16;  // rows form: rows of a warp's staging area
-constexpr int SG = 36;  // rows form: row stride (floats) of a warp's staging area, 16-byte reads without conflicts
+constexpr int STG = 32 * 64;  // rows form: a warp's staging area
 constexpr int UNIT = 64 * 16 * 2;             // gradient form: 64 columns of a unit of 16 rows
 constexpr int TBUF = 4 * UNIT, TBUFS = 2;     // a tail of both operands
 constexpr int SLOT = 32 * 128;                // gradient form: 32 rows x 128 bytes of dw
@@ -85,7 +84,7 @@ template <int MODE, int KIND> struct Shape {
     static constexpr int THREADS = 384;
     static constexpr int SLOTS = KIND == GADD ? 4 : 1;
     static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;  // of full height
-    static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG_ROWS * SG * 4;
+    static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG;
     static constexpr int TBUF_AT = STAGES * STAGE;
     static constexpr int STG_AT = TBUF_AT + (MODE == WGRAD ? TBUFS * TBUF : 0);
     static constexpr int TAIL_AT = STG_AT + WARPS * STG_WARP;
@@ -154,6 +153,15 @@ struct Tile {
     int k0;        // gradient form: first k
 };
 
+// x / d of x >= 0, d > 0, by an approximate quotient: off by one below 2^24, by a few above
+__device__ __forceinline__ int quotient(int x, int d) {
+    int q = __float2int_rz(__fdividef(static_cast<float>(x), static_cast<float>(d)));
+    int r = x - q * d;
+    while (r < 0) --q, r += d;
+    while (r >= d) ++q, r -= d;
+    return q;
+}
+
 // Rows form: a group's rows are cut into tiles of nearly equal height, in units of 16 rows
 // and at most maxu of them. Every CTA builds the list from the offsets: the tiles of group
 // e begin at tstart[e], its row tiles fastest, then output columns. Returns whether the
@@ -178,7 +186,7 @@ __device__ __forceinline__ int build_tiles(Tail& s, const RaggedParams& p) {
     }
     if (tid < 32) {
         auto tiles = [&](int e) {
-            return e < E && !bad ? ((s.off[e + 1] - s.off[e] + 15) / 16 + p.maxu - 1) / p.maxu * jt : 0;
+            return e < E && !bad ? p.units.div((s.off[e + 1] - s.off[e] + 15) / 16 + p.maxu - 1) * jt : 0;
         };
         const int per = (E + 31) / 32;
         int loc = 0;
@@ -219,9 +227,9 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
     }
     // (of groups that begin at the same tile all but the last are empty)
     t.e = lo;
-    const int v = s.off[lo + 1] - s.off[lo], U = (v + 15) / 16, mt = (U + p.maxu - 1) / p.maxu;
-    const int local = tile - s.tstart[lo], jn = local / mt, i = local - jn * mt;
-    const int least = U / mt, u0 = i * least + min(i, U - mt * least);  // the first tiles take a unit more
+    const int v = s.off[lo + 1] - s.off[lo], U = (v + 15) / 16, mt = p.units.div(U + p.maxu - 1);
+    const int local = tile - s.tstart[lo], jn = quotient(local, mt), i = local - jn * mt;
+    const int least = quotient(U, mt), u0 = i * least + min(i, U - mt * least);  // the first tiles take a unit more
     const int units = least + (i < U - mt * least);
     t.m0 = s.off[lo] + 16 * u0;
     t.rows = min(v - 16 * u0, 16 * units);
@@ -233,25 +241,14 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
 
 // ---- epilogues --------------------------------------------------------------------------
 
-// Rows form: how a warp's 16 rows x 32 columns lie in memory, as 16-byte pieces of 8 columns: lane l has pieces of
-// rows l / 4 and 8 + l / 4.
+// Rows form: how a warp's rows x 32 columns lie in memory, as 16-byte pieces of 8 columns: lane l has pieces of
+// rows l / 4, 8 + l / 4 and so on.
 struct Piece {
     int r, col;
     __device__ __forceinline__ Piece(int i, int lane, int col0) : r(8 * i + (lane >> 2)), col(col0 + 8 * (lane & 3)) {}
     __device__ __forceinline__ bool in(const RaggedParams& p, int rows) const { return r < rows && col < p.J; }
     __device__ __forceinline__ size_t at(const RaggedParams& p, int m) const {
         return static_cast<size_t>(m + r) * p.J + col;
-    }
-};
-struct Residual {
-    uint4 v[2];
-    __device__ __forceinline__ void load(const RaggedParams& p, int lane, int m, int rows, int col0) {
-        if (!p.residual) return;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const Piece c(i, lane, col0);
-            if (c.in(p, rows)) v[i] = *reinterpret_cast<const uint4*>(p.residual + c.at(p, m));
-        }
     }
 };
 // brings the residual of rows m .. m + rows - 1 into L2, ahead of its use
@@ -262,38 +259,6 @@ __device__ __forceinline__ void prefetch_residual(const RaggedParams& p, int lan
         if (col < p.J)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.residual + static_cast<size_t>(m + r) * p.J + col));
     }
-}
-
-// Rows form: up to 16 rows x 32 columns z (lane = column, v[i] = row m + i) of a warp to
-// memory, through its staging area so that they leave as pieces; the piece's activation
-// function and residual are applied on the way, in f32.
-template <int ACT, int KIND>
-__device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&v)[16], const Residual& res, float* stg,
-                                           int lane, int m, int rows, int col0) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) stg[i * SG + lane] = v[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Piece c(i, lane, col0);
-        if (!c.in(p, rows)) continue;
-        const float4 lo = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3));
-        const float4 hi = *reinterpret_cast<const float4*>(stg + c.r * SG + 8 * (lane & 3) + 4);
-        float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const size_t at = c.at(p, m);
-        if (KIND == FULL) {
-            if (p.pre) *reinterpret_cast<uint4*>(p.pre + at) = pack8<ACT>(f);
-            fn_values(p.fn, f);
-            if (p.residual) {
-                float g[8];
-                unpack8<ACT>(res.v[i], g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += g[j];
-            }
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = pack8<ACT>(f);
-    }
-    __syncwarp();
 }
 
 // 16 columns of the accumulator
@@ -317,26 +282,141 @@ __device__ __forceinline__ float bias_of(const RaggedParams& p, int col) {
     return Act<ACT>::to_f(reinterpret_cast<const typename Act<ACT>::T*>(p.bias)[col]);
 }
 
-template <int ACT, int KIND>
-__device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta, float* stg, const Tile& t, int col0,
-                                              int half, int lane) {
-    const float b = KIND == FULL ? bias_of<ACT>(p, col0 + lane) : 0.0f;
-    uint32_t nx[16];
-    Residual res, res_nx;
-    if (16 * half < t.rows) tmem_ld16(ta + 16 * half, nx);
-    if (KIND == FULL) res_nx.load(p, lane, t.m0 + 16 * half, t.rows - 16 * half, col0);
-#pragma unroll 1
-    for (int c = 16 * half; c < t.rows; c += 32) {
-        float v[16];
-        tmem_ld16_wait(nx);
+// 8 U columns of 16 lanes, as the fragments of 8 x 8 matrices: register 4 u + 2 k + i is lane 8 k + T / 4, column 8 u +
+// 2 (T % 4) + i, T the thread
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+template <int N> __device__ __forceinline__ void tmem_ld_frag_wait(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = KIND == FULL ? __uint_as_float(nx[j]) + b : __uint_as_float(nx[j]);
-        if (c + 32 < t.rows) tmem_ld16(ta + c + 32, nx);  // in flight while this one is stored
-        if (KIND == FULL) {
-            res = res_nx;
-            res_nx.load(p, lane, t.m0 + c + 32, t.rows - c - 32, col0);
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// A warp's staging area: rows of 32 columns in 16 bits; the four 16-byte pieces of a row are swizzled by row pairs, so
+// that neither eight rows of a piece nor the pieces of two rows meet in a bank.
+__device__ __forceinline__ uint32_t piece_at(uint32_t stg, int r, int piece) {
+    return stg + r * 64 + ((piece ^ (r >> 1 & 3)) << 4);
+}
+// fragments (lane j, rows m) to the area, transposed: row m, columns j
+template <int U> __device__ __forceinline__ void stage_frags(uint32_t stg, int lane, const uint32_t (&f)[U][4]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                         piece_at(stg, 8 * u + (lane & 7), lane >> 3)),
+                     "r"(f[u][0]), "r"(f[u][1]), "r"(f[u][2]), "r"(f[u][3])
+                     : "memory");
+}
+// the area's rows to memory: 16-byte pieces, eight rows at a time
+template <int U>
+__device__ __forceinline__ void copy_rows(const RaggedParams& p, uint16_t* out, uint32_t stg, int lane, int m, int rows,
+                                          int col0) {
+    __syncwarp();
+    uint4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "r"(piece_at(stg, 8 * i + (lane >> 2), lane & 3))
+                     : "memory");
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const Piece c(i, lane, col0);
+        if (c.in(p, rows)) *reinterpret_cast<uint4*>(out + c.at(p, m)) = v[i];
+    }
+    __syncwarp();
+}
+
+// Rows form: a warp's 32 columns (TMEM lanes) of a tile, a step of rows at a time, every other step. The sums are read as
+// fragments, finished in f32, rounded, and turned in the staging area. (By one lane a column, with f32 values staged, a
+// plain tile of 256 rows took 2.5 us, now 1.9: 8192 x 8192 x 64 43 us and 33.) A step is 32 rows of a plain product; 16 with
+// bias, function or residual, whose code is twice as long.
+template <int ACT, int KIND>
+__device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta, uint32_t stg, const Tile& t, int col0,
+                                              int half, int lane) {
+    constexpr int U = KIND == FULL ? 2 : 4, STEP = 8 * U;
+    float b[4];  // of lanes 8 j + T / 4
+    if (KIND == FULL)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = bias_of<ACT>(p, col0 + 8 * j + (lane >> 2));
+    uint32_t nx[2][4 * U];
+    uint4 res[U];
+    auto load = [&](int c) {
+        tmem_ld_frag(ta + c, nx[0]);
+        tmem_ld_frag(ta + (16u << 16) + c, nx[1]);
+        if (KIND != FULL || !p.residual) return;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const Piece q(i, lane, col0);
+            if (q.in(p, t.rows - c)) res[i] = *reinterpret_cast<const uint4*>(p.residual + q.at(p, t.m0 + c));
         }
-        store_rows<ACT, KIND>(p, v, res, stg, lane, t.m0 + c, t.rows - c, col0);
+    };
+    if (STEP * half < t.rows) load(STEP * half);
+#pragma unroll 1
+    for (int c = STEP * half; c < t.rows; c += 2 * STEP) {
+        float v[U][8];  // [eight rows][two rows of a lane's four columns]
+        uint32_t f[U][4], r[U][4];
+        tmem_ld_frag_wait(nx[0]);
+        tmem_ld_frag_wait(nx[1]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[u][j] = __uint_as_float(nx[j >> 2][4 * u + (j & 3)]);
+                if (KIND == FULL) v[u][j] += b[j >> 1];
+            }
+        if (KIND == FULL && p.residual) {  // to the area, and back as fragments
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 piece_at(stg, 8 * i + (lane >> 2), lane & 3)),
+                             "r"(res[i].x), "r"(res[i].y), "r"(res[i].z), "r"(res[i].w)
+                             : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[u][0]), "=r"(r[u][1]), "=r"(r[u][2]), "=r"(r[u][3])
+                             : "r"(piece_at(stg, 8 * u + (lane & 7), lane >> 3))
+                             : "memory");
+            __syncwarp();
+        }
+        if (c + 2 * STEP < t.rows) load(c + 2 * STEP);  // in flight while this one is finished
+        auto round_all = [&] {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[u][j] = Act<ACT>::pack2(v[u][2 * j], v[u][2 * j + 1]);
+        };
+        if (KIND == FULL && p.pre) {
+            round_all();
+            stage_frags(stg, lane, f);
+            copy_rows<U>(p, p.pre, stg, lane, t.m0 + c, t.rows - c, col0);
+        }
+        if (KIND == FULL) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                fn_values(p.fn, v[u]);
+                if (!p.residual) continue;
+                float g[8];
+                unpack8<ACT>(make_uint4(r[u][0], r[u][1], r[u][2], r[u][3]), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[u][j] += g[j];
+            }
+        }
+        round_all();
+        stage_frags(stg, lane, f);
+        copy_rows<U>(p, static_cast<uint16_t*>(p.out), stg, lane, t.m0 + c, t.rows - c, col0);
     }
 }
 
@@ -804,7 +884,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                                                ew, n_off, half, lane, wc))
                     break;
             } else {
-                rows_epilogue<ACT, KIND>(p, ta, reinterpret_cast<float*>(stg), t, t.j0 + n_off, half, lane);
+                rows_epilogue<ACT, KIND>(p, ta, smem_u32(stg), t, t.j0 + n_off, half, lane);
             }
             tc_fence_before();
             __syncwarp();
@@ -877,9 +957,11 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
 template <int MODE, int ACT> int launch_rows_form(const RaggedArgs& g, int maxu) {
     RaggedParams p = g.p;
     p.maxu = maxu;
+    p.units.set(maxu);
     Maps m;
-    int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64);
-    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, p.rows, p.C, p.maxu * 8, g.act);
+    const bool reused = p.maxu >= 8;  // tall tiles are bound by what comes from L2, low ones by the weights' way from HBM
+    int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64, reused);
+    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, p.rows, p.C, p.maxu * 8, g.act, reused);
     if (rc != MOE_OK) return rc;
     m.ta = m.tb = m.out = m.add = m.b;
     // row tiles at most: one more per group than the rows fill

@@ -19,8 +19,8 @@ template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
     const uint64_t rows = p.rows ? p.rows : 1;
     const int out = KIND == G16 ? g.act : kTmapF32;
     const uint32_t cols = KIND == G16 ? 64 : 32;
-    int rc = make_tmap_2d(&m.a, dy, rows, p.J, 64, g.act);
-    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, x, rows, p.C, 64, g.act);
+    int rc = make_tmap_2d(&m.a, dy, rows, p.J, 64, g.act, true);
+    if (rc == MOE_OK) rc = make_tmap_2d(&m.b, x, rows, p.C, 64, g.act, true);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.ta, dy, rows, p.J, 16, g.act);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.tb, x, rows, p.C, 16, g.act);
     if (rc == MOE_OK) rc = make_tmap_3d(&m.out, p.out, out, p.C, p.J, p.E, cols, 32);
