@@ -85,25 +85,50 @@ RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
     return best;
 }
 
-// Which form the gradient of a weight takes: 0 for CTA pairs; of one group with few tiles, the CTAs that share a
-// tile's rows, by the waves of tiles, their blocks of 64 rows and a launch as above. (us, pairs / split: 4096 rows, 512 x
-// 512 22.5 / 10.7; 2414 rows, 920 x 256 16.0 / 9.5; 30000 rows, 264 x 520 168 / 32; 1024 rows, 1024 x 1024 9.7 / 8.5; 1333 rows,
-// 2816 x 2048 18.6 / 26.4.) The sums of an f32 gradient take no more than 4096 rows each, as in the pairs' chunks.
-int pick_gradient_parts(const RaggedParams& p, bool f32, int sms) {
-    if (p.offsets || p.rows == 0 || sms < 2) return 0;  // (without a device the launch reports it)
-    const int64_t KB = ceil_div(p.rows, 64);
-    const int64_t waves = ceil_div(ceil_div(p.J, 256) * ceil_div(p.C, 256), sms / 2);
-    int64_t best_ns = 4300 + waves * max64(KB * 290, 1500);
-    int best = 0;
+// Which form the gradient of a weight takes.
+//
+// CTA pairs (parts 0): kt tiles of nearly equal width side by side, of 256 columns at most, and more of them where they
+// fill the waves of tiles better (12288 rows of 64 groups, 2048 x 1408 f32 with addends: five of 256 columns and one of
+// 128 278 us, six alike 254, eight 237; 1333 rows, 2816 x 2048 f32: eight side by side, 88 tiles for 76 pairs, 21.4, thirteen
+// 19.1). A tile takes its blocks of 64 rows, 140 + 0.73 ns a column each, and 0.7 us between tiles (2532 rows of 6 groups, 18736 x 944
+// f32: four side by side 110 us, five 122, six 130), or the way of its bytes, 82 a ns, and if they are 16-bit 0.8 us to pack them. Over many waves a pair's tiles have the average width.
+//
+// Of one group with few tiles, the split form: parts CTAs share a tile's rows; its time as above, more where two of them
+// share an SM, and for addends, which its lanes read 64 bytes at a time. (us, pairs / split, f32: 4000 rows, 512 x 512 18.2 /
+// 10.7; 2000 rows, 2048 x 512 12.3 / 11.6; 100 rows, 1000 x 1000 6.1 / 5.6, with addends 7.5 / 10.3; 30000 rows, 264 x 520
+// 168 / 32; 640 rows, 2048 x 1408 9.0 / 14.0.) The sums of an f32 gradient take no more than 4096 rows each, as in the
+// pairs' chunks.
+struct GradientForm {
+    int parts, kt;
+};
+GradientForm pick_gradient_form(const RaggedParams& p, bool f32, int sms) {
+    const int64_t units = ceil_div(p.C, gradient_unit(f32)), widest = 256 / gradient_unit(f32);
+    const int64_t kt0 = ceil_div(units, widest);
+    GradientForm best{0, static_cast<int>(kt0)};
+    if (p.rows == 0 || sms < 2) return best;  // (without a device the launch reports it)
+    const int64_t KB = ceil_div(ceil_div(p.rows, p.E), 64), rows = ceil_div(p.J, 256) * p.E;
+    const int64_t bytes = f32 ? (p.addend ? 8 : 4) : 2, fixed = f32 ? 0 : 800;
+    int64_t best_ns = INT64_MAX;
+    for (int64_t kt = kt0; kt <= 2 * kt0 && kt <= units; ++kt) {
+        const int64_t waves = ceil_div(rows * kt, sms / 2);
+        const int64_t width = waves > 3 ? p.C / kt : ceil_div(units, kt) * gradient_unit(f32);
+        const int64_t ns = 5100 + waves * max64(KB * (140 + width * 73 / 100) + 700, fixed + bytes * 256 * width / 82);
+        if (ns < best_ns) {
+            best_ns = ns;
+            best.kt = static_cast<int>(kt);
+        }
+    }
+    if (p.offsets) return best;
     const int64_t tiles = ceil_div(p.J, 128) * ceil_div(p.C, 128);
     for (const auto& s : kSplits) {
         if (s.parts > KB || tiles * s.parts > 2 * sms) break;
         const int64_t blocks = ceil_div(KB, s.parts);
         if (f32 && blocks > 64) continue;
-        const int64_t ns = s.launch_ns + (tiles * s.parts > sms ? 2 : 1) * blocks * 230 + 2500;
+        const int64_t ns = s.launch_ns + (tiles * s.parts > sms ? 2000 + blocks * 720 : blocks * 230) +
+                           (s.parts < 8 ? 2500 : 4000) + (p.addend ? 400 + 4600 / s.parts : 0);
         if (ns < best_ns) {
             best_ns = ns;
-            best = s.parts;
+            best.parts = s.parts;
         }
     }
     return best;
@@ -191,7 +216,9 @@ extern "C" int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, cons
     g.K = K;
     g.st = static_cast<cudaStream_t>(stream);
     g.who = who;
-    g.parts = moe::pick_gradient_parts(g.p, dw_f32 != 0, moe::sm_count());
+    const moe::GradientForm form = moe::pick_gradient_form(g.p, dw_f32 != 0, moe::sm_count());
+    g.parts = form.parts;
+    g.kt = form.kt;
     return moe::launch_ragged_wgrad(g);
 }
 

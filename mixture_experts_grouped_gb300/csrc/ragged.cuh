@@ -29,6 +29,8 @@ struct RaggedParams {
     int maxu;                // rows form: most units of 16 rows a tile has
     FastDiv units;           // rows form: by maxu
     FastDiv kt, per;         // gradient form: tiles of a row of tiles, and of a group
+    int kunit, kleast, kmore;  // a row's tiles are kleast units of kunit columns wide, the first kmore one more
+    int turn;                // places by which a pair's tile moves on in each wave of tiles
     void* out;
     const uint16_t *bias, *residual;  // rows form
     uint16_t* pre;
@@ -43,10 +45,14 @@ struct RaggedArgs {
     const void *a, *w;  // rows form: rows, weights [E, .., ..]; gradient form: dy, x
     int act, transposed, f32;
     int N, K;           // the weight's shape
-    int parts;          // gradient form: CTAs that share a tile's contraction; 0: CTA pairs
+    int parts;          // gradient form: CTAs that share a tile's contraction; 0: CTA pairs,
+    int kt;             // with this many tiles side by side
     cudaStream_t st;
     const char* who;
 };
+
+// Columns that the width of a gradient's tile is a multiple of: a store's 128 bytes.
+constexpr int gradient_unit(bool f32) { return f32 ? 32 : 64; }
 
 // How a product of rows runs: on CTA pairs, row tiles of up to maxu units of 16 rows; or, with
 // parts > 0, split: row tiles, and CTAs that share a tile's contraction.

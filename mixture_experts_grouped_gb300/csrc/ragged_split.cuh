@@ -97,19 +97,28 @@ __device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&
     __syncwarp();
 }
 
-// four columns k .. of row n of one group's weight gradient
+// Addends of 16 columns k .. of row n of one group's weight gradient, of those there are. (All at once and ahead of the
+// sums: one after the other, each waited for, an addend cost a tile 8 us.)
+template <int KIND> struct Addends {
+    float4 v[4];
+    __device__ __forceinline__ void load(const RaggedParams& p, int n, int k, int cols) {
+        if (KIND != G32 || !p.addend || n >= p.J) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (4 * j < cols && k + 4 * j < p.C)
+                v[j] = *reinterpret_cast<const float4*>(p.addend + static_cast<size_t>(n) * p.C + k + 4 * j);
+    }
+};
+// four columns k .. of row n
 template <int ACT, int KIND>
-__device__ __forceinline__ void store_gradient(const RaggedParams& p, int n, int k, float4 f) {
+__device__ __forceinline__ void store_gradient(const RaggedParams& p, int n, int k, float4 f, const float4& a) {
     if (n >= p.J || k >= p.C) return;
     const size_t at = static_cast<size_t>(n) * p.C + k;
     if (KIND == G16) {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
             make_uint2(Act<ACT>::pack2(f.x, f.y), Act<ACT>::pack2(f.z, f.w));
     } else {
-        if (p.addend) {
-            const float4 a = *reinterpret_cast<const float4*>(p.addend + at);
-            f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
-        }
+        if (p.addend) f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = f;
     }
 }
@@ -263,7 +272,9 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 uint32_t u[16];
                 float v[16];
                 Residual res;
+                Addends<KIND> add;
                 if (KIND == FULL) res.load(p, lane, m0 + c, rows - c, j0 + 32 * q);
+                if (MODE == WGRAD) add.load(p, j0 + me, m0 + c, 16);
                 tmem_ld16(ta + c, u);
                 tmem_ld16_wait(u);
 #pragma unroll
@@ -271,7 +282,8 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 if constexpr (MODE == WGRAD) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4)
-                        store_gradient<ACT, KIND>(p, j0 + me, m0 + c + j, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+                        store_gradient<ACT, KIND>(p, j0 + me, m0 + c + j, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]),
+                                                  add.v[j / 4]);
                 } else {
                     store_rows<ACT, KIND>(p, v, res, stg, lane, m0 + c, rows - c, j0 + 32 * q);
                 }
@@ -315,7 +327,9 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             for (int c = 0; c < have; c += 16) {
                 float v[16];
                 Residual res;
+                Addends<KIND> add;
                 if (KIND == FULL) res.load(p, lane, m0 + 4 * q0 + c, have - c, j0 + 32 * q);
+                if (MODE == WGRAD) add.load(p, j0 + me, m0 + 4 * q0 + c, have - c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -331,7 +345,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         }
                     }
                     if constexpr (MODE == WGRAD) {
-                        if (c + 4 * j < have) store_gradient<ACT, KIND>(p, j0 + me, m0 + 4 * q0 + c + 4 * j, f);
+                        if (c + 4 * j < have) store_gradient<ACT, KIND>(p, j0 + me, m0 + 4 * q0 + c + 4 * j, f, add.v[j]);
                     }
                     v[4 * j] = f.x + bias;
                     v[4 * j + 1] = f.y + bias;

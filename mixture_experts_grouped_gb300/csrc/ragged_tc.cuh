@@ -37,6 +37,8 @@
 // 184 us, 5.6 TB/s.
 #pragma once
 
+#include <numeric>
+
 #include "ragged.cuh"
 
 namespace moe {
@@ -94,7 +96,6 @@ template <int MODE, int KIND> struct Shape {
 
 // stages that the ring's bytes hold
 template <int MODE, int KIND> __device__ __forceinline__ uint32_t n_stages(uint32_t stage_bytes) {
-    if (MODE == WGRAD) return Shape<MODE, KIND>::STAGES;
     return min(static_cast<uint32_t>(MAX_STAGES), Shape<MODE, KIND>::STAGES * STAGE / stage_bytes);
 }
 
@@ -212,12 +213,12 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
     Tile t;
     if (MODE == WGRAD) {
         t.e = p.per.div(tile);
-        const int in = tile - t.e * static_cast<int>(p.per.d), jn = p.kt.div(in);
+        const int in = tile - t.e * static_cast<int>(p.per.d), jn = p.kt.div(in), kn = in - jn * static_cast<int>(p.kt.d);
         t.j0 = jn * 256;
-        t.k0 = (in - jn * static_cast<int>(p.kt.d)) * 256;
+        t.k0 = (kn * p.kleast + min(kn, p.kmore)) * p.kunit;
         t.m0 = s.off[t.e];
         t.rows = s.off[t.e + 1] - t.m0;
-        t.n = 256;
+        t.n = (p.kleast + (kn < p.kmore)) * p.kunit;
         return t;
     }
     int lo = 0, hi = p.E - 1;
@@ -238,6 +239,23 @@ template <int MODE> __device__ __forceinline__ Tile get_tile(const Tail& s, cons
     t.k0 = 0;
     return t;
 }
+
+// A pair's tiles: one of every wave, `turn` places on in each, so that the narrow tiles at the edges, which come at
+// regular distances, are not all dealt to the same pairs (15421 rows of 133 groups, 3784 x 288 f32 with addends, tiles of
+// 160 and 128 columns side by side: 196 us, 230 without).
+struct Walk {
+    int tile, pos, step, turn;
+    __device__ __forceinline__ explicit Walk(const RaggedParams& p)
+        : tile(blockIdx.x >> 1), pos(tile), step(gridDim.x >> 1), turn(p.turn) {}
+    __device__ __forceinline__ void next() {
+        tile += step + turn;
+        pos += turn;
+        if (pos >= step) {
+            pos -= step;
+            tile -= step;
+        }
+    }
+};
 
 // ---- epilogues --------------------------------------------------------------------------
 
@@ -452,21 +470,22 @@ template <int KIND> struct Slots {
     static constexpr int N = Shape<WGRAD, KIND>::SLOTS;
 };
 
-__device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(256, p.C - t.k0); }
+__device__ __forceinline__ int tile_cols(const RaggedParams& p, const Tile& t) { return min(t.n, p.C - t.k0); }
 
 // With an addend: the copies of one epilogue warp's slots. They are a warp of their own
 // because finding, waiting for and issuing them took as long as the sums (a step 0.9 us,
 // all by one warp).
 __device__ __forceinline__ void copy_slots(Tail& s, const RaggedParams& p, const CUtensorMap* tm_out,
                                            const CUtensorMap* tm_add, uint8_t* area, int w, int n_off, int n_tiles,
-                                           int first, int step, int lane, const WaitCtx& wc) {
+                                           int lane, const WaitCtx& wc) {
     constexpr int N = Slots<GADD>::N, COLS = Slots<GADD>::COLS;
-    if (first >= n_tiles) return;
-    int ltile = first, lc = 0;  // the next load
+    Walk at(p), lat(p);
+    if (at.tile >= n_tiles) return;
+    int lc = 0;  // the next load's column
     uint32_t loaded = 0, stored = 0;
-    Tile lt = get_tile<WGRAD>(s, p, first), t = lt;
+    Tile lt = get_tile<WGRAD>(s, p, lat.tile), t = lt;
     auto load = [&] {
-        if (ltile >= n_tiles) return;
+        if (lat.tile >= n_tiles) return;
         const uint32_t i = loaded % N;
         if (elect_one()) {
             mbar_arrive_expect_tx(&s.slot[w][i], SLOT);
@@ -477,14 +496,14 @@ __device__ __forceinline__ void copy_slots(Tail& s, const RaggedParams& p, const
         lc += COLS;
         if (lc >= tile_cols(p, lt)) {
             lc = 0;
-            ltile += step;
-            if (ltile < n_tiles) lt = get_tile<WGRAD>(s, p, ltile);
+            lat.next();
+            if (lat.tile < n_tiles) lt = get_tile<WGRAD>(s, p, lat.tile);
         }
     };
     for (int i = 0; i < N - 1; ++i) load();
     bool ok = true;
-    for (int tile = first; tile < n_tiles && ok; tile += step) {
-        t = get_tile<WGRAD>(s, p, tile);
+    for (; at.tile < n_tiles && ok; at.next()) {
+        t = get_tile<WGRAD>(s, p, at.tile);
         const int cols = tile_cols(p, t);
         for (int c = 0; c < cols; c += COLS) {
             const uint32_t i = stored % N;
@@ -610,7 +629,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const WaitCtx wc{&s.abort_flag, p.err, p.wait_ns};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();  // 0: leader
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     // set up while the kernel before this one ends; then its results may be read, and the next one may set up
     if (tid == 0) {
@@ -661,7 +679,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
     const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), 0);
     const int KB = (p.C + BK - 1) / BK;
-    const uint32_t b_bytes = MODE == WGRAD ? OPER : p.maxu * 8 * 128;  // this CTA's, of the N operand
+    const bool second = MODE == WGRAD && (p.kleast + (p.kmore > 0)) * p.kunit > 128;  // whether this CTA's share of the N operand is two boxes of 64 columns
+    const uint32_t b_bytes = MODE == WGRAD ? (second ? OPER : OPER / 2) : p.maxu * 8 * 128;  // its bytes
     const uint32_t stage_bytes = OPER + b_bytes, stages = n_stages<MODE, KIND>(stage_bytes);
     // blocks of a tile; of a gradient, those that its whole units of 16 rows fill
     auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows / 16 + 3) / 4 : KB; };
@@ -673,8 +692,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         uint32_t stage = 0, phase = 0;
         long issued = 0;
         bool ok = true;
-        for (int tile = first; tile < n_tiles && ok; tile += step) {
-            const Tile t = get_tile<MODE>(s, p, tile);
+        for (Walk at(p); at.tile < n_tiles && ok; at.next()) {
+            const Tile t = get_tile<MODE>(s, p, at.tile);
             const int nb = blocks_of(t);
             for (int b = 0; b < nb; ++b) {
                 if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) {
@@ -692,9 +711,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                             tma_load_2d_pair(dst, &tm_a, n, r, bar);
                             tma_load_2d_pair(dst + 8192, &tm_a, n + 64, r, bar);
                         } else {
-                            const int k = t.k0 + 128 * static_cast<int>(rank);
+                            const int k = t.k0 + t.n / 2 * static_cast<int>(rank);  // (two boxes may bring more than the share)
                             tma_load_2d_pair(dst, &tm_b, k, r, bar);
-                            tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
+                            if (second) tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
                         }
                     } else {
                         const int c = b * BK;
@@ -732,8 +751,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
             bool ok = true;
             Tile next{};
-            if (first < n_tiles) next = get_tile<MODE>(s, p, first);
-            for (int tile = first; tile < n_tiles && ok; tile += step) {
+            Walk at(p);
+            if (at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
+            while (at.tile < n_tiles && ok) {
                 const Tile t = next;
                 const int nb = blocks_of(t), chunks = chunks_of(t);
                 const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
@@ -771,8 +791,6 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                         }
                     }
                     if (!ok) break;
-                    // (found while the MMAs run: it would hold up the next tile's)
-                    if (ch + 1 == chunks && tile + step < n_tiles) next = get_tile<MODE>(s, p, tile + step);
                     if (MODE == WGRAD && ch + 1 == chunks && t.rows % 16 != 0) {
                         const uint32_t tb = tails % TBUFS;
                         if (!mbar_wait_warp(&s.tready[tb], (tails / TBUFS) & 1u, wc)) {
@@ -791,6 +809,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     if (elect_one()) tc_commit_pair(&s.tfull[acc], 0x3);
                     __syncwarp();
                 }
+                // (found while the MMAs run: it would hold up the next tile's)
+                at.next();
+                if (ok && at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
                 if (chunks == 1) cur ^= 1u;
             }
             if (elect_one()) tc_commit_pair(&s.mma_done, 0x1);
@@ -801,8 +822,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         if (MODE == WGRAD) {
             // ---------------- tails ----------------
             uint32_t tails = 0;
-            for (int tile = first; tile < n_tiles; tile += step) {
-                const Tile t = get_tile<MODE>(s, p, tile);
+            for (Walk at(p); at.tile < n_tiles; at.next()) {
+                const Tile t = get_tile<MODE>(s, p, at.tile);
                 const int left = t.rows % 16;
                 if (left == 0) continue;
                 const uint32_t tb = tails % TBUFS, ph = (tails / TBUFS) & 1u;
@@ -811,7 +832,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 uint8_t* buf = smem + S::TBUF_AT + tb * TBUF;
                 if (elect_one()) {
                     const int r = t.m0 + t.rows - left;
-                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + 128 * static_cast<int>(rank);
+                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + t.n / 2 * static_cast<int>(rank);
                     mbar_arrive_expect_tx(&s.tloc[tb], 4 * UNIT);
                     tma_load_2d(buf, &tm_ta, n, r, &s.tloc[tb]);
                     tma_load_2d(buf + UNIT, &tm_ta, n + 64, r, &s.tloc[tb]);
@@ -840,7 +861,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             // ---------------- copies of addends and gradients, for the epilogue warp of the same quarter ----------------
             const int q = warp & 3, w = (q + 2) & 3;  // (warps 2 to 5 have quarters 2, 3, 0, 1)
             copy_slots(s, p, &tm_out, &tm_add, smem + S::STG_AT + w * S::STG_WARP, w,
-                       128 * static_cast<int>(rank) + 32 * q, n_tiles, first, step, lane, wc);
+                       128 * static_cast<int>(rank) + 32 * q, n_tiles, lane, wc);
         }
     } else {
         // ---------------- epilogue ----------------
@@ -862,8 +883,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             else arrive_remote(lead_tempty + acc * 8);
         };
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        for (int tile = first; tile < n_tiles; tile += step) {
-            const Tile t = get_tile<MODE>(s, p, tile);
+        for (Walk at(p); at.tile < n_tiles; at.next()) {
+            const Tile t = get_tile<MODE>(s, p, at.tile);
             const int chunks = chunks_of(t);
             if constexpr (KIND == FULL) prefetch_residual(p, lane, t.m0, t.rows, t.j0 + n_off);
             if (!wait_full(cur)) break;
@@ -945,10 +966,14 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
         if (known) known->store(max_pairs, std::memory_order_release);
     }
     if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", who);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < max_pairs ? tiles : max_pairs)));
+    const int pairs_used = static_cast<int>(tiles < max_pairs ? tiles : max_pairs);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs_used));
+    RaggedParams q = p;
+    if (MODE == WGRAD)
+        while (q.turn + 1 < pairs_used && std::gcd(static_cast<unsigned>(pairs_used + q.turn), p.per.d) != 1) ++q.turn;
     cfg.stream = st;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.ta, m.tb, m.out, m.add, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.ta, m.tb, m.out, m.add, q);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: launch failed: %s", who, cudaGetErrorString(e));
     count_launch();
     return check_launch(who);

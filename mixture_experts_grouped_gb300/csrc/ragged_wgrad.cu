@@ -7,7 +7,11 @@ namespace {
 
 template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
     RaggedParams p = g.p;
-    const int nt = (p.J + 255) / 256, kt = (p.C + 255) / 256;
+    const int nt = (p.J + 255) / 256, kt = g.kt;
+    p.kunit = gradient_unit(g.f32);
+    const int units = (p.C + p.kunit - 1) / p.kunit;
+    p.kleast = units / kt;
+    p.kmore = units % kt;
     const int64_t tiles = static_cast<int64_t>(p.E) * nt * kt;
     if (tiles > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", g.who);
     p.kt.set(kt);
