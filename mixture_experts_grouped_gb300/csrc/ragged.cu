@@ -109,7 +109,7 @@ GradientForm pick_gradient_form(const RaggedParams& p, bool f32, int sms) {
     const int64_t KB = ceil_div(ceil_div(p.rows, p.E), 64), rows = ceil_div(p.J, 256) * p.E;
     const int64_t bytes = f32 ? (p.addend ? 8 : 4) : 2, fixed = f32 ? 0 : 800;
     int64_t best_ns = INT64_MAX;
-    for (int64_t kt = kt0; kt <= 2 * kt0 && kt <= units; ++kt) {
+    for (int64_t kt = kt0; kt <= 2 * kt0 && kt <= kt0 + 12 && kt <= units; ++kt) {
         const int64_t waves = ceil_div(rows * kt, sms / 2);
         const int64_t width = waves > 3 ? p.C / kt : ceil_div(units, kt) * gradient_unit(f32);
         const int64_t ns = 5100 + waves * max64(KB * (140 + width * 73 / 100) + 700, fixed + bytes * 256 * width / 82);

@@ -12,8 +12,8 @@
 //   transposed copy of the weights is needed.
 // Gradient form (the weight's gradient):
 //     dw_e[n, k] = sum_{r in e} dy[r, n] x[r, k]
-//   Both operands are MN-major, the contraction runs over the group's rows: whole units of
-//   16, four to a block. The rows that are left, 1 to 15, are a unit of their own: its
+//   A tile is 256 rows n by up to 256 columns k. Both operands are MN-major, the contraction
+//   runs over the group's rows: whole units of 16, four to a block. The rows that are left, 1 to 15, are a unit of their own: its
 //   other rows belong to the next group or to nobody (they may hold infinities), so a warp
 //   of each CTA has the unit copied into a buffer apart, sets those rows to zeros in both
 //   operands, and then lets the MMA have it. The buffers are two, filled up to two tiles
@@ -30,10 +30,10 @@
 // copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
 // 14336 x 4096: 271 us, 245 elected). Every wait is bounded.
 //
-// Measured: 8192 rows of 8 groups, 28672 x 4096 1000 us, 1.92 PFLOP/s (1203 under the power cap of
+// Measured: 8192 rows of 8 groups, 28672 x 4096 1014 us, 1.9 PFLOP/s (1203 under the power cap of
 // long runs); its transposed form the same; 64 rows of 50 touched groups, 1536 x 2048 55 us, 5.7
-// TB/s. Gradients: 8192 rows of 8 groups, 4096 x 14336 bf16 550 us, 1.75 PFLOP/s; 12288 rows of 64
-// groups, 2048 x 1408 f32 with addends 276 us, 5.65 TB/s; 32768 rows of 128 groups, 1536 x 2048 bf16
+// TB/s. Gradients: 8192 rows of 8 groups, 4096 x 14336 bf16 545 us, 1.76 PFLOP/s; 12288 rows of 64
+// groups, 2048 x 1408 f32 with addends 239 us, 6.5 TB/s; 32768 rows of 128 groups, 1536 x 2048 bf16
 // 184 us, 5.6 TB/s.
 #pragma once
 
@@ -969,7 +969,7 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
     const int pairs_used = static_cast<int>(tiles < max_pairs ? tiles : max_pairs);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs_used));
     RaggedParams q = p;
-    if (MODE == WGRAD)
+    if (MODE == WGRAD && tiles > max_pairs)
         while (q.turn + 1 < pairs_used && std::gcd(static_cast<unsigned>(pairs_used + q.turn), p.per.d) != 1) ++q.turn;
     cfg.stream = st;
     cfg.numAttrs = 2;

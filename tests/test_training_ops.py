@@ -305,6 +305,14 @@ def test_few_rows_of_groups(moe, dev, counts, N, K, transposed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("f32,addend", [(True, None), (True, "in place"), (False, None)])
+@pytest.mark.parametrize("counts,N,K", [([30, 0, 65, 2, 17], 2056, 1416), ([5, 21] * 20, 520, 296), ([100, 1], 4104, 1000),
+                                        ([19] * 64, 776, 328), ([140, 9, 70], 136, 8200)])
+def test_weight_gradient_of_uneven_tiles_over_many_waves(moe, dev, counts, N, K, f32, addend):
+    wgrad_case(moe, dev, counts, N, K, "bf16" if N % 16 else "f16", f32, addend, N, lead=3, tail=4)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("off", [[0, 5, 4, 9], [-1, 3, 5, 9], [0, 3, 5, 11], [2 ** 31 - 1, 0, 5, 9], [5, 3, 2, 1]])
 def test_bad_offsets_are_reported_and_compute_nothing(moe, dev, off):
     off = torch.tensor(off, dtype=torch.int32, device=dev)
