@@ -13,14 +13,14 @@
 // Gradient form (the weight's gradient):
 //     dw_e[n, k] = sum_{r in e} dy[r, n] x[r, k]
 //   A tile is 256 rows n by up to 256 columns k. Both operands are MN-major, the contraction
-//   runs over the group's rows: whole units of 16, four to a block. The rows that are left, 1 to 15, are a unit of their own: its
-//   other rows belong to the next group or to nobody (they may hold infinities), so a warp
-//   of each CTA has the unit copied into a buffer apart, sets those rows to zeros in both
-//   operands, and then lets the MMA have it. The buffers are two, filled up to two tiles
-//   ahead: in the ring of blocks, where a unit is copied only six blocks before its MMA, the
-//   way from its arrival over the clearing to the other CTA's MMA warp was not hidden and
-//   cost 1.2 us a tile (8 groups of 1024 rows, 4096 x 14336: 668 us, 559 with rows that 16
-//   divides).
+//   runs over the group's rows: whole units of 16, four to a block. The rows that are left,
+//   1 to 15, are a unit of their own: its other rows belong to the next group or to nobody
+//   (they may hold infinities), so a warp of each CTA has the unit copied into a buffer
+//   apart, sets those rows to zeros in both operands, and then lets the MMA have it. The
+//   buffers are two, filled up to two tiles ahead: in the ring of blocks, where a unit is
+//   copied only six blocks before its MMA, the way from its arrival over the clearing to
+//   the other CTA's MMA warp was not hidden and cost 1.2 us a tile (8 groups of 1024 rows,
+//   4096 x 14336: 668 us, 559 with rows that 16 divides).
 //
 // Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
 // CTA (the leader) issues the MMAs, warps 2 to 5 and 8 to 11 are the epilogue (with an
