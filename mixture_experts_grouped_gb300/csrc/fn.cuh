@@ -72,7 +72,7 @@ __device__ __forceinline__ void fn_values(int fn, float (&f)[8]) {
     }
 }
 
-// f'(z)
+// f'(z), at an infinity its limit: a z that is finite in f32 may be stored as one in 16 bits. NaN stays.
 __device__ __forceinline__ float fn_slope(int fn, float z) {
     switch (fn) {
         case MOE_FN_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
@@ -88,7 +88,8 @@ __device__ __forceinline__ float fn_slope(int fn, float z) {
         }
         case MOE_FN_SILU: {
             const float s = sigmoid_fast(z);
-            return s * fmaf(z, 1.0f - s, 1.0f);
+            const float c = fminf(fmaxf(z, -100.0f), 100.0f);  // beyond, s (1 - s) is 0
+            return s * fmaf(c, 1.0f - s, 1.0f);
         }
         default: return 1.0f;
     }

@@ -1,0 +1,48 @@
+"""The training operators at the edges of what they take: infinities, tails, long sums, outputs in place of inputs,
+tensors of other devices, and an object's own buffers as its inputs."""
+import math
+
+import pytest
+import torch
+
+import plain
+from test_training_ops import FNS, dev, moe  # noqa: F401
+
+
+
+
+# ---- infinities ------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("fn", FNS[1:])
+def test_slopes_of_infinite_values_are_their_limits(moe, dev, fn, act):
+    """0 at -inf and 1 at +inf, in every column of a vector, and in the bias' sums."""
+    z = torch.tensor([-math.inf, math.inf] * 8, dtype=plain.DT[act], device=dev).repeat(40, 1)
+    d = torch.full_like(z, 0.75)
+    dz, db = torch.empty_like(z), torch.empty(16, device=dev)
+    moe.moe_bias_act_backward(d, z, moe.ACT_CODES[act], moe.FN_CODES[fn], 40, 16, dz, db)
+    assert torch.all(dz[:, ::2] == 0) and torch.all(dz[:, 1::2] == 0.75)
+    assert torch.all(db[::2] == 0) and torch.all(db[1::2] == 30.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", FNS[1:])
+@pytest.mark.parametrize("M", [1, 40, 200])
+def test_gradient_through_a_pre_that_overflows_f16(moe, dev, fn, M):
+    """z = +-76800 is finite in f32, where its function is taken, and infinite in the f16 that the gradient reads."""
+    N, K = 72, 64
+    a, w = torch.zeros((M, K), dtype=torch.float16), torch.zeros((N, K), dtype=torch.float16)
+    a[:, 0], w[:, 0] = 256.0, 1.0
+    w[3, 0], w[5, 0] = -300.0, 300.0
+    out, pre = (torch.empty((M, N), dtype=torch.float16, device=dev) for _ in range(2))
+    code = moe.FN_CODES[fn]
+    moe.moe_dense_gemm(a.to(dev), 1, w.to(dev), None, code, None, pre, out, M, N, K)
+    assert torch.all(pre[:, 3] == -math.inf) and torch.all(pre[:, 5] == math.inf)
+    assert torch.all(out[:, 3] == 0) and torch.all(out[:, 5] == math.inf)
+    d = torch.full((M, N), 0.5, dtype=torch.float16, device=dev)
+    dz, db = torch.empty_like(d), torch.empty(N, device=dev)
+    moe.moe_bias_act_backward(d, pre, 1, code, M, N, dz, db)
+    want = torch.full((M, N), 0.5, dtype=torch.float16, device=dev)  # slopes at 256 are 1
+    want[:, 3] = 0
+    assert torch.equal(dz, want) and torch.equal(db, want.float().sum(0))
