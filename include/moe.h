@@ -610,7 +610,8 @@ int moe_dense_gemm(const void* a, int32_t act, const void* w, const void* bias, 
  *     dz = d_out * f'(pre),   d_pre[m, n] = act( dz ),   d_bias[n] = sum_m dz[m, n]  (+ d_bias[n])
  * (f32, dz unrounded, summed in an order that depends on M and N alone). The
  * gradients of a and w are then moe_ragged_gemm (transposed) and moe_ragged_wgrad of
- * d_pre, of the residual d_out itself. The derivative of MOE_FN_RELU at 0 is 0.
+ * d_pre, of the residual d_out itself. The derivative of MOE_FN_RELU at 0 is 0; at an infinite
+ * pre (a z that its type does not hold) a derivative is its limit.
  *   d_out         device act [M, N]
  *   pre           device act [M, N]; may be NULL with MOE_FN_NONE (f' = 1)
  *   d_pre         device act [M, N] out or NULL; may be d_out or pre
@@ -624,7 +625,8 @@ int moe_bias_act_backward(const void* d_out, const void* pre, int32_t act, int32
  * SwiGLU of a stacked gate/up product, rounded once:
  *     h[r, i] = g / (1 + exp(-g)) * u,   g = gate_up[r, i], u = gate_up[r, I + i]
  *   gate_up       device act [rows, 2 I];  h  device act [rows, I] out
- * silu(g) of g < -87.3 may count as 0. Requirements: I % 8 == 0, 16-byte alignment.
+ * silu(g) of g < -87.3 may count as 0, and of g = -inf is 0. Requirements: I % 8 == 0, 16-byte
+ * alignment.
  */
 int moe_swiglu(const void* gate_up, int32_t act, int32_t rows, int32_t I, void* h, void* stream);
 
@@ -635,6 +637,7 @@ int moe_swiglu(const void* gate_up, int32_t act, int32_t rows, int32_t I, void* 
  *   d_gate_up     device act [rows, 2 I] out; may be gate_up
  *   h             device act [rows, I] out or NULL: the forward result again (the
  *                 same bits as moe_swiglu's), so that it need not be kept; may be d_h
+ * At infinite g, silu and its slope are their limits.
  */
 int moe_swiglu_backward(const void* gate_up, const void* d_h, int32_t act, int32_t rows, int32_t I,
                         void* d_gate_up, void* h, void* stream);

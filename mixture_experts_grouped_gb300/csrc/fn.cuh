@@ -14,6 +14,14 @@ __device__ __forceinline__ float sigmoid_fast(float z) {
     return r;
 }
 
+// g s and its slope, of s = sigmoid_fast(g). A gate stored in 16 bits may have overflowed: an infinite one has its limits,
+// 0 and 0 at -inf, inf and 1 at +inf (g s alone and g (1 - s) would be NaN). A NaN is in s, and stays.
+__device__ __forceinline__ float silu_part(float g, float s) { return fmaxf(g, -3.402823466e38f) * s; }
+__device__ __forceinline__ float silu_slope(float g, float s) {
+    const float c = fminf(fmaxf(g, -100.0f), 100.0f);  // beyond, s (1 - s) is 0
+    return s * fmaf(c, 1.0f - s, 1.0f);
+}
+
 // sqrt(2 / pi) (z + 0.044715 z^3), doubled: (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)),
 // which keeps its relative accuracy where 1 + tanh v cancels
 __device__ __forceinline__ float gelu_tanh_arg2(float z) {
@@ -86,11 +94,7 @@ __device__ __forceinline__ float fn_slope(int fn, float z) {
             const float s = sigmoid_fast(gelu_tanh_arg2(z));
             return fmaf(c * s * (1.0f - s), fmaf(0.2140644488178f, c * c, 1.59576912160573f), s);
         }
-        case MOE_FN_SILU: {
-            const float s = sigmoid_fast(z);
-            const float c = fminf(fmaxf(z, -100.0f), 100.0f);  // beyond, s (1 - s) is 0
-            return s * fmaf(c, 1.0f - s, 1.0f);
-        }
+        case MOE_FN_SILU: return silu_slope(z, sigmoid_fast(z));
         default: return 1.0f;
     }
 }

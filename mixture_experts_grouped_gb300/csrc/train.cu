@@ -29,7 +29,7 @@ swiglu_kernel(const uint4* __restrict__ gu, uint4* __restrict__ h, Index vectors
     unpack8<ACT>(gv, g);
     unpack8<ACT>(uv, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = silu_mul_fast(g[j], u[j]);
+    for (int j = 0; j < 8; ++j) o[j] = silu_part(g[j], sigmoid_fast(g[j])) * u[j];
     h[i] = pack8<ACT>(o);
 }
 
@@ -49,10 +49,10 @@ swiglu_backward_kernel(const uint4* gu, const uint4* dh, uint4* dgu, uint4* h, I
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float s = sigmoid_fast(g[j]);
-        const float f = g[j] * s;
+        const float f = silu_part(g[j], s);
         o[j] = f * u[j];
         du[j] = d[j] * f;
-        dg[j] = d[j] * u[j] * (s * fmaf(g[j], 1.0f - s, 1.0f));
+        dg[j] = d[j] * u[j] * silu_slope(g[j], s);
     }
     dgu[at] = pack8<ACT>(dg);
     dgu[at + V] = pack8<ACT>(du);

@@ -46,3 +46,21 @@ def test_gradient_through_a_pre_that_overflows_f16(moe, dev, fn, M):
     want = torch.full((M, N), 0.5, dtype=torch.float16, device=dev)  # slopes at 256 are 1
     want[:, 3] = 0
     assert torch.equal(dz, want) and torch.equal(db, want.float().sum(0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_swiglu_of_infinite_gates_is_its_limit(moe, dev, act):
+    """A gate that overflowed to -inf gives 0 and has no gradient, one of +inf has the slope 1; a NaN stays."""
+    rows, I, dt = 3, 24, plain.DT[act]
+    g = torch.tensor([-math.inf, math.inf, math.nan, 1.0], dtype=dt, device=dev).repeat(rows, I // 4)
+    u, dh = torch.full((rows, I), 2.0, dtype=dt, device=dev), torch.full((rows, I), 0.5, dtype=dt, device=dev)
+    gu = torch.cat((g, u), 1).contiguous()
+    h, h2, dgu = torch.empty_like(u), torch.empty_like(u), torch.empty_like(gu)
+    moe.moe_swiglu(gu, moe.ACT_CODES[act], rows, I, h)
+    moe.moe_swiglu_backward(gu, dh, moe.ACT_CODES[act], rows, I, dgu, h2)
+    assert torch.equal(h.view(torch.int16), h2.view(torch.int16))
+    dg, du = dgu[:, :I], dgu[:, I:]
+    assert torch.all(h[:, ::4] == 0) and torch.all(h[:, 1::4] == math.inf) and torch.isnan(h[:, 2::4]).all()
+    assert torch.all(dg[:, ::4] == 0) and torch.all(dg[:, 1::4] == 1.0) and torch.isnan(dg[:, 2::4]).all()
+    assert torch.all(du[:, ::4] == 0) and torch.all(du[:, 1::4] == math.inf) and torch.isnan(du[:, 2::4]).all()
