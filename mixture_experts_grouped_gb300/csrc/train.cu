@@ -107,7 +107,7 @@ bias_act_backward_kernel(const uint16_t* d_out, const uint16_t* pre, int M, int 
                 if (FN != MOE_FN_NONE) {
                     unpack8<ACT>(zv[i], z);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) d[j] *= fn_slope(FN, z[j]);
+                    for (int j = 0; j < 8; ++j) d[j] = __fmul_rn(d[j], fn_slope(FN, z[j]));  // (not fused with the sum)
                 }
                 if (d_pre)
                     *reinterpret_cast<uint4*>(d_pre + static_cast<size_t>(m0 + i * stride) * N + n) = pack8<ACT>(d);

@@ -6,9 +6,9 @@ import pytest
 import torch
 
 import plain
-from test_training_ops import FNS, dev, moe  # noqa: F401
+from test_training_ops import FNS, dev, f64, moe  # noqa: F401
 
-
+F32 = plain.F32
 
 
 # ---- infinities ------------------------------------------------------------------------------------
@@ -64,3 +64,31 @@ def test_swiglu_of_infinite_gates_is_its_limit(moe, dev, act):
     assert torch.all(h[:, ::4] == 0) and torch.all(h[:, 1::4] == math.inf) and torch.isnan(h[:, 2::4]).all()
     assert torch.all(dg[:, ::4] == 0) and torch.all(dg[:, 1::4] == 1.0) and torch.isnan(dg[:, 2::4]).all()
     assert torch.all(du[:, ::4] == 0) and torch.all(du[:, 1::4] == math.inf) and torch.isnan(du[:, 2::4]).all()
+
+
+# ---- outputs in place of inputs ---------------------------------------------------------------------
+
+# one row, the narrow form with one and several batches of rows a thread, the wide form (whose columns fill the GPU)
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("M,N", [(1, 8), (33, 200), (5000, 72), (1333, 264), (300, 9736), (1100, 16384)])
+def test_bias_and_activation_gradient_in_place(moe, dev, M, N, fn, act):
+    """d_pre in the place of d_out, and in that of pre, has the bits that it has in a tensor of its own, and so has
+    d_bias; without d_pre too."""
+    g = torch.Generator(device=dev).manual_seed(M)
+    d, z = (torch.randn((M, N), generator=g, device=dev).to(plain.DT[act]) for _ in range(2))
+    codes = moe.ACT_CODES[act], moe.FN_CODES[fn]
+    dz, db = torch.empty_like(d), torch.empty(N, device=dev)
+    moe.moe_bias_act_backward(d, z, *codes, M, N, dz, db)
+    ref = d.double() * f64(fn, z.double())[1]
+    assert torch.all((dz.double() - ref).abs()
+                     <= ref.abs() * plain.U[act] + d.double().abs() * 64 * F32 + plain.TINY[act])
+    for place in ("d_out", "pre", "none"):
+        di, zi, db2 = d.clone(), z.clone(), torch.empty(N, device=dev)
+        into = {"d_out": di, "pre": zi, "none": None}[place]
+        moe.moe_bias_act_backward(di, zi, *codes, M, N, into, db2)
+        assert torch.equal(db2, db), place
+        assert into is None or torch.equal(into, dz), place
+        assert place == "d_out" or torch.equal(di, d)
+        assert place == "pre" or torch.equal(zi, z)
