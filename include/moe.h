@@ -591,8 +591,8 @@ int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, const int32_t* 
  * Dense product with its epilogue:
  *     z[m, n] = sum_k a[m, k] * w[n, k] + bias[n]
  *     pre[m, n] = act( z ),   out[m, n] = act( f(z) + residual[m, n] )
- * f is one of MOE_FN_*, of the unrounded z. f(z) of z < -87.3 may count as 0 for
- * MOE_FN_SILU.
+ * f is one of MOE_FN_*, of the unrounded z, to a few parts in 10^6 of its value; that of z < -13 may
+ * count as 0 for MOE_FN_GELU (|f| < 1e-37), of z < -87.3 for MOE_FN_SILU.
  *   a             device act [M, K];  w  device act [N, K]
  *   bias          device act [N] or NULL
  *   residual      device act [M, N] or NULL; may be out

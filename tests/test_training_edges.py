@@ -92,3 +92,38 @@ def test_bias_and_activation_gradient_in_place(moe, dev, M, N, fn, act):
         assert into is None or torch.equal(into, dz), place
         assert place == "d_out" or torch.equal(di, d)
         assert place == "pre" or torch.equal(zi, z)
+
+
+# ---- the tail of gelu -------------------------------------------------------------------------------
+
+def gelu_part(z):
+    """The part of itself by which the normal distribution of z may be off: 9e-7 of its polynomial; 24 half steps of
+    its evaluation, and of the hardware's 2^x and reciprocal; and the roundings of the exponent z^2 / 2, of two half
+    steps of itself at most."""
+    return 9e-7 + (24 + z * z) * F32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_gelu_keeps_its_relative_accuracy_in_the_tail(moe, dev, act):
+    """To where the density leaves f32's normal range (-13): a half step of the type beside gelu_part, value and slope."""
+    z = torch.cat([torch.linspace(-13, 0, 3001), torch.linspace(0, 9, 1001), -torch.logspace(-6, 0, 1002)])
+    z = z.to(plain.DT[act])[: 5000]
+    n = len(z)
+    a = torch.zeros((1, 8), dtype=z.dtype)
+    a[0, 0] = 1
+    w = torch.zeros((n, 8), dtype=z.dtype)
+    w[:, 0] = z
+    out = torch.empty((1, n), dtype=z.dtype, device=dev)
+    moe.moe_dense_gemm(a.to(dev), moe.ACT_CODES[act], w.to(dev), None, moe.MOE_FN_GELU, None, None, out, 1, n, 8)
+    z = z.double()
+    cdf, density = torch.exp(torch.special.log_ndtr(z)), torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    part = gelu_part(z)
+    plain.close(out[0], z * cdf, act, z.abs() * cdf * part)
+    one = torch.ones((1, n), dtype=plain.DT[act], device=dev)
+    moe.moe_bias_act_backward(one, z[None].to(plain.DT[act]).to(dev), moe.ACT_CODES[act], moe.MOE_FN_GELU, 1, n, out)
+    plain.close(out[0], cdf + z * density, act, (cdf + z.abs() * density) * part)
+    # and in f32, as the bias' gradient: one row, each column its own sum
+    db = torch.empty(n, device=dev)
+    moe.moe_bias_act_backward(one, z[None].to(plain.DT[act]).to(dev), moe.ACT_CODES[act], moe.MOE_FN_GELU, 1, n, None, db)
+    assert torch.all((db.cpu().double() - (cdf + z * density)).abs() <= (cdf + z.abs() * density) * part + 1e-38)
