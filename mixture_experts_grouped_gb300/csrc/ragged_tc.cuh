@@ -47,10 +47,12 @@ namespace ragged {
 namespace {
 
 enum { ROWS_FWD = 0, ROWS_BACK = 1, WGRAD = 2 };
-// kinds of gradient: 16-bit, f32, f32 with an addend; of the rows form: the product alone, or with bias,
+// kinds of gradient: 16-bit, f32, f32 with an addend, 16-bit of more rows than a chunk (whose loop would cost the others
+// 1%); of the rows form: the product alone, or with bias,
 // activation function, residual and z (their code, jumped over, still cost a plain product's epilogue half its time
 // in instruction fetches)
-enum { G16 = 0, G32 = 1, GADD = 2, PLAIN = 0, FULL = 3 };
+enum { G16 = 0, G32 = 1, GADD = 2, G16LONG = 4, PLAIN = 0, FULL = 3 };
+constexpr bool in_16_bits(int kind) { return kind == G16 || kind == G16LONG; }
 
 constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
@@ -438,25 +440,28 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
     }
 }
 
-// A tensor core's f32 sums are cut, not rounded, to 24 bits at each step of 16 products:
-// where sums grow steadily, 30000 rows in one accumulator left them 4e-5 short. An f32
-// gradient therefore takes its rows in chunks of 4096 (5e-6) and adds the chunks in f32:
-// the first stays in its accumulator, the others come into the second one and are added to
-// it, the last one on its way out. (16-bit gradients are rounded to 2^-9 or 2^-12 anyway.)
-constexpr int CHUNK = 64;  // blocks
+// A tensor core's f32 sums are cut, not rounded, at each step of 16 products: of n products
+// of one sign, a sum comes out up to n 2^-27 short (measured, as a part of it: 4096 rows
+// 2.6e-5, 30000 1.9e-4). A gradient therefore takes its rows in chunks (gradient_chunk) and
+// adds the chunks in f32: the first stays in its accumulator, the others come into the second
+// one and are added to it, the last one on its way out.
 
-// adds the accumulator at tb to the one at ta (this warp's lanes and steps of 32 columns)
-template <int STRIDE> __device__ __forceinline__ void fold(uint32_t ta, uint32_t tb, int first) {
+// adds the accumulator at tb to the one at ta: the columns that this warp will store, COLS of
+// every HALVES * COLS
+template <int COLS, int HALVES> __device__ __forceinline__ void fold(uint32_t ta, uint32_t tb, int half) {
 #pragma unroll 1
-    for (int c = first; c < 256; c += STRIDE) {
-        uint32_t u[32], v[32];
-        tmem_ld32(ta + c, u);
-        tmem_ld32(tb + c, v);
-        tmem_ld_wait_regs(u);
-        tmem_ld_wait_regs(v);
+    for (int c = half * COLS; c < 256; c += HALVES * COLS) {
+#pragma unroll 1
+        for (int i = c; i < c + COLS; i += 32) {
+            uint32_t u[32], v[32];
+            tmem_ld32(ta + i, u);
+            tmem_ld32(tb + i, v);
+            tmem_ld_wait_regs(u);
+            tmem_ld_wait_regs(v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(v[j]));
-        tmem_st32(ta + c, u);
+            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(__uint_as_float(u[j]) + __uint_as_float(v[j]));
+            tmem_st32(ta + i, u);
+        }
     }
     tmem_st_wait();
 }
@@ -466,7 +471,7 @@ template <int STRIDE> __device__ __forceinline__ void fold(uint32_t ta, uint32_t
 // row, and leave by a TMA store, which leaves out what lies past the weight's edges. An
 // addend comes into the slot by a TMA load three steps before and is added in place.
 template <int KIND> struct Slots {
-    static constexpr int COLS = KIND == G16 ? 64 : 32;
+    static constexpr int COLS = in_16_bits(KIND) ? 64 : 32;
     static constexpr int N = Shape<WGRAD, KIND>::SLOTS;
 };
 
@@ -585,7 +590,7 @@ __device__ __forceinline__ bool wgrad_epilogue(Tail& s, const RaggedParams& p, c
             __syncwarp();
         }
         ++used;
-        if (KIND == G16) {
+        if (in_16_bits(KIND)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 *reinterpret_cast<uint4*>(at + 16 * (q ^ (lane & 7))) = pack_piece<ACT>(v + 8 * q);
@@ -624,6 +629,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
               const RaggedParams p) {
     using S = Shape<MODE, KIND>;
     constexpr bool CHUNKED = MODE == WGRAD && KIND != G16;
+    constexpr int CHUNK = gradient_chunk(!in_16_bits(KIND), ACT);
     extern __shared__ __align__(1024) uint8_t smem[];
     Tail& s = *reinterpret_cast<Tail*>(smem + S::TAIL_AT);
     const WaitCtx wc{&s.abort_flag, p.err, p.wait_ns};
@@ -890,13 +896,15 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             if (!wait_full(cur)) break;
             const uint32_t ta = lanes + cur * 256, tb = lanes + (cur ^ 1u) * 256;
             bool ok = true;
-            for (int ch = 1; ch < chunks && ok; ++ch) {
-                ok = wait_full(cur ^ 1u);
-                if (ok && ch + 1 < chunks) {
-                    fold<32 * S::HALVES>(ta, tb, 32 * half);
-                    tc_fence_before();
-                    __syncwarp();
-                    release(cur ^ 1u);
+            if constexpr (CHUNKED) {
+                for (int ch = 1; ch < chunks && ok; ++ch) {
+                    ok = wait_full(cur ^ 1u);
+                    if (ok && ch + 1 < chunks) {
+                        fold<Slots<KIND>::COLS, S::HALVES>(ta, tb, half);
+                        tc_fence_before();
+                        __syncwarp();
+                        release(cur ^ 1u);
+                    }
                 }
             }
             if (!ok) break;

@@ -21,8 +21,8 @@ template <int ACT, int KIND> int gradient_form(const RaggedArgs& g) {
     const void* dy = p.rows ? g.a : p.out;
     const void* x = p.rows ? g.w : p.out;
     const uint64_t rows = p.rows ? p.rows : 1;
-    const int out = KIND == G16 ? g.act : kTmapF32;
-    const uint32_t cols = KIND == G16 ? 64 : 32;
+    const int out = in_16_bits(KIND) ? g.act : kTmapF32;
+    const uint32_t cols = in_16_bits(KIND) ? 64 : 32;
     int rc = make_tmap_2d(&m.a, dy, rows, p.J, 64, g.act, true);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.b, x, rows, p.C, 64, g.act, true);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.ta, dy, rows, p.J, 16, g.act);
@@ -42,7 +42,8 @@ template <int ACT> int by_kind(const RaggedArgs& g) {
         return g.f32 ? launch_split_kind<WGRAD, ACT, G32>(g, tiles, kt, g.parts)
                      : launch_split_kind<WGRAD, ACT, G16>(g, tiles, kt, g.parts);
     }
-    if (!g.f32) return gradient_form<ACT, G16>(g);
+    if (!g.f32)
+        return g.p.rows > 64 * gradient_chunk(false, ACT) ? gradient_form<ACT, G16LONG>(g) : gradient_form<ACT, G16>(g);
     return g.p.addend ? gradient_form<ACT, GADD>(g) : gradient_form<ACT, G32>(g);
 }
 

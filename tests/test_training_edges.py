@@ -127,3 +127,38 @@ def test_gelu_keeps_its_relative_accuracy_in_the_tail(moe, dev, act):
     db = torch.empty(n, device=dev)
     moe.moe_bias_act_backward(one, z[None].to(plain.DT[act]).to(dev), moe.ACT_CODES[act], moe.MOE_FN_GELU, 1, n, None, db)
     assert torch.all((db.cpu().double() - (cdf + z * density)).abs() <= (cdf + z.abs() * density) * part + 1e-38)
+
+
+# ---- long sums --------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,rows,chunk", [("f16", 1200000, 16384), ("bf16", 4000000, 131072)])
+@pytest.mark.parametrize("N,K,counts", [(64, 72, None), (72, 64, "one"), (136, 264, "few")])
+def test_weight_gradient_in_16_bits_of_very_many_rows(moe, dev, act, rows, chunk, N, K, counts):
+    """Sums of one sign, of which n rows in one accumulator come out up to n 2^-27 short: a chunk loses a quarter of
+    the output's half step. Columns of many scales, so that the rounding of the outputs has no common sign."""
+    if counts == "few":
+        rows //= 4
+    g = torch.Generator(device=dev).manual_seed(N)
+    dt = plain.DT[act]
+    dy, x = (torch.empty((rows, n), dtype=dt, device=dev).uniform_(0.05, 0.15, generator=g) for n in (N, K))
+    dy *= torch.empty(N, dtype=dt, device=dev).uniform_(0.5, 2.0, generator=g)
+    split = {None: None, "one": [0, rows], "few": [0, 77, 77, rows // 5, rows - 3, rows - 3]}[counts]
+    off = torch.tensor(split, dtype=torch.int32, device=dev) if split else None
+    E = len(split) - 1 if split else 1
+    dw, again = (torch.empty((E, N, K), dtype=dt, device=dev) for _ in range(2))
+    for o in (dw, again):
+        moe.moe_ragged_wgrad(dy, x, moe.ACT_CODES[act], off, rows, N, K, E, None, o, False)
+    assert torch.equal(dw, again)
+    bounds = split or [0, rows]
+    for e in range(E):
+        ref = torch.zeros((N, K), dtype=torch.float64, device=dev)
+        for lo in range(bounds[e], bounds[e + 1], 1 << 19):
+            hi = min(lo + (1 << 19), bounds[e + 1])
+            ref += dy[lo:hi].double().T @ x[lo:hi].double()
+        n = bounds[e + 1] - bounds[e]
+        lost = min(chunk, n) * 2.0 ** -27 + (n // chunk + 16) * F32  # and the sum of the chunks
+        plain.close(dw[e], ref.cpu(), act, ref.cpu() * lost)
+        if n > chunk:  # the rounding's mean over N K outputs: six of its deviations, U / sqrt(3 N K) each
+            mean = float(((dw[e].double() - ref) / ref).mean())
+            assert abs(mean) <= lost + 6 * plain.U[act] / math.sqrt(3 * N * K)
