@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import plain
-from test_training_ops import FNS, dev, f64, moe  # noqa: F401
+from test_training_ops import FNS, dev, f64, moe, offsets_of  # noqa: F401
 
 F32 = plain.F32
 
@@ -162,3 +162,54 @@ def test_weight_gradient_in_16_bits_of_very_many_rows(moe, dev, act, rows, chunk
         if n > chunk:  # the rounding's mean over N K outputs: six of its deviations, U / sqrt(3 N K) each
             mean = float(((dw[e].double() - ref) / ref).mean())
             assert abs(mean) <= lost + 6 * plain.U[act] / math.sqrt(3 * N * K)
+
+
+# ---- waits that run out -----------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("limit_ns", [1, 300])
+@pytest.mark.parametrize("call", ["dense", "groups", "transposed", "gradient"])
+def test_split_form_reports_a_wait_that_runs_out(moe, dev, call, limit_ns):
+    """Contractions so long that the wait for a tile's last product (45 us and more) outlasts any first look at its
+    barrier, with a limit far below: the call ends, the status is there, and the next call is the clean one."""
+    g = torch.Generator(device=dev).manual_seed(1)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def randn16(*shape):
+        return torch.randn(shape, generator=g, device=dev).bfloat16()
+
+    if call == "dense":
+        M, N, K = 40, 264, 131072
+        a, w = randn16(M, K), randn16(N, K)
+
+        def run(out):
+            moe.moe_dense_gemm(a, 0, w, None, 0, None, None, out, M, N, K, err)
+        shape = M, N
+    elif call == "gradient":
+        rows, N, K = 100000, 264, 136
+        a, w = randn16(rows, N), randn16(rows, K)
+
+        def run(out):
+            moe.moe_ragged_wgrad(a, w, 0, None, rows, N, K, 1, None, out, False, err)
+        shape = N, K
+    else:
+        tr, counts = call == "transposed", [30, 0, 41, 29]
+        N, K = (65536, 520) if tr else (520, 65536)
+        a, w, off = randn16(100, N if tr else K), randn16(4, N, K), offsets_of(counts).to(dev)
+
+        def run(out):
+            moe.moe_ragged_gemm(a, 0, w, tr, off, 100, N, K, 4, out, err)
+        shape = 100, K if tr else N
+    want, out = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    run(want)
+    assert err.item() == 0
+    old = moe.moe_set_wait_limit_ns(limit_ns)
+    try:
+        run(out)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_limit_ns(old)
+    assert err.item() == moe.MOE_DEV_ERR_TIMEOUT
+    err.zero_()
+    run(out)
+    assert err.item() == 0 and torch.equal(out, want)
