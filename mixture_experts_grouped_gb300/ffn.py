@@ -69,6 +69,28 @@ def _require_type(what: str, t: torch.Tensor, dtype: torch.dtype) -> None:
         raise ValueError(f"{what} is {t.dtype}, {'dense' if t.is_contiguous() else 'strided'}, not dense {dtype}")
 
 
+def _cuda_device(device) -> torch.device:
+    """The device of an object's buffers, by its number (that of "cuda" is the current one)."""
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"device {d}: the kernels run on a CUDA device")
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+
+
+def _require(what: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype, *shape: int) -> None:
+    """A dense tensor of this type and shape on the object's device (the kernels take addresses as they come)."""
+    _require_shape(what, t, *shape)
+    _require_type(what, t, dtype)
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+def _require_current(device: torch.device) -> None:
+    """A call launches on the current device, which must be the one that the object's buffers are on."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the buffers are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 @dataclass
 class BlockFp8Weight:
     """E4M3 codes uint8 [N, K] with f32 scales [ceil(N / 128), ceil(K / 128)]."""

@@ -7,7 +7,8 @@ provides device memory and the stream, every step runs in libmoe.so, nothing
 synchronises with the host and buffers are allocated once, so a forward and a
 backward pass can be captured in a CUDA graph. There is no autograd here:
 ``backward`` is called with the output's gradient and writes the gradients
-into buffers of the object.
+into buffers of the object. Weights and inputs are on the object's device, and a
+pass runs while that is the current one; anything else is refused (ValueError).
 """
 
 from __future__ import annotations
@@ -16,15 +17,7 @@ import torch
 
 from . import layer as L
 from . import moe as M
-from .ffn import _require_shape, _require_type
-
-
-def _require(what: str, t: torch.Tensor, dtype: torch.dtype, *shape: int) -> None:
-    """A dense tensor of this type and shape on the current device (the kernels take addresses as they come)."""
-    _require_shape(what, t, *shape)
-    _require_type(what, t, dtype)
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+from .ffn import _cuda_device, _require, _require_current
 
 
 class MoeTrainLayer:
@@ -43,8 +36,9 @@ class MoeTrainLayer:
         dt = self.dtype = L.act_dtype(act)
         if T < 1:
             raise ValueError(f"T={T}: a step needs a token")
-        _require("w_gate_up", w_gate_up, dt, E, 2 * I, H)
-        _require("w_down", w_down, dt, E, H, I)
+        device = self.device = _cuda_device(device)
+        _require("w_gate_up", w_gate_up, device, dt, E, 2 * I, H)
+        _require("w_down", w_down, device, dt, E, H, I)
         self.T, self.H, self.I, self.E, self.k, self.P = T, H, I, E, k, T * k
         self.act_code, self.renormalize = M.ACT_CODES[act], renormalize
         self.w_gate_up, self.w_down = w_gate_up, w_down
@@ -77,8 +71,9 @@ class MoeTrainLayer:
     def forward(self, x, logits, stream=None):
         """The layer on x [T, H] routed by logits [T, E]; returns its output buffer."""
         T, H, I, E, k, P, act = self.T, self.H, self.I, self.E, self.k, self.P, self.act_code
-        _require("x", x, self.dtype, T, H)
-        _require("logits", logits, torch.float32, T, E)
+        _require_current(self.device)
+        _require("x", x, self.device, self.dtype, T, H)
+        _require("logits", logits, self.device, torch.float32, T, E)
         self.logits = logits
         M.moe_route_topk_softmax(logits, self.topk_ids, self.topk_weights, T, E, k, self.renormalize, stream)
         M.moe_align_block_size(self.topk_ids, P, E, 1, P, self.sorted_token_ids, self.expert_ids, self.offsets,
@@ -97,7 +92,8 @@ class MoeTrainLayer:
         T, H, I, E, k, P, act = self.T, self.H, self.I, self.E, self.k, self.P, self.act_code
         if self.logits is None:
             raise RuntimeError("backward without a forward pass")
-        _require("d_out", d_out, self.dtype, T, H)
+        _require_current(self.device)
+        _require("d_out", d_out, self.device, self.dtype, T, H)
         M.moe_combine_backward(d_out, self.y, act, self.pair_to_row, self.topk_weights, self.d_y, self.d_weights, T, H,
                                k, P, self.err, stream)
         M.moe_ragged_gemm(self.d_y, act, self.w_down, True, self.offsets, P, H, I, E, self.d_h, self.err, stream)
@@ -128,9 +124,10 @@ class DenseMlp:
         dt = self.dtype = L.act_dtype(act)
         if T < 1:
             raise ValueError(f"T={T}: a step needs a token")
+        device = self.device = _cuda_device(device)
         for name, t, shape in (("w1", w1, (I, H)), ("w2", w2, (H, I)), ("b1", b1, (I,)), ("b2", b2, (H,))):
             if t is not None:
-                _require(name, t, dt, *shape)
+                _require(name, t, device, dt, *shape)
         self.T, self.H, self.I = T, H, I
         self.act_code, self.fn = M.ACT_CODES[act], M.FN_CODES[fn]
         self.w1, self.b1, self.w2, self.b2 = w1, b1, w2, b2
@@ -150,11 +147,12 @@ class DenseMlp:
 
     def forward(self, x, residual=None, stream=None):
         """The block on x [T, H]; returns its output buffer. x is kept for ``backward`` and must not change before it."""
-        _require("x", x, self.dtype, self.T, self.H)
+        _require_current(self.device)
+        _require("x", x, self.device, self.dtype, self.T, self.H)
         if x.data_ptr() in (self.out.data_ptr(), self.d_x.data_ptr()):
             raise ValueError("x is a buffer of the block itself, which a pass overwrites")
         if residual is not None:
-            _require("residual", residual, self.dtype, self.T, self.H)
+            _require("residual", residual, self.device, self.dtype, self.T, self.H)
         self.x = x
         M.moe_dense_gemm(x, self.act_code, self.w1, self.b1, self.fn, None, self.pre, self.h, self.T, self.I, self.H,
                          self.err, stream)
@@ -168,7 +166,8 @@ class DenseMlp:
         T, H, I, act = self.T, self.H, self.I, self.act_code
         if self.x is None:
             raise RuntimeError("backward without a forward pass")
-        _require("d_out", d_out, self.dtype, T, H)
+        _require_current(self.device)
+        _require("d_out", d_out, self.device, self.dtype, T, H)
         if self.d_b2 is not None:
             M.moe_bias_act_backward(d_out, None, act, M.MOE_FN_NONE, T, H, None, self.d_b2, accumulate,
                                     stream)

@@ -1,6 +1,7 @@
 """The training operators at the edges of what they take: infinities, tails, long sums, outputs in place of inputs,
 tensors of other devices, and an object's own buffers as its inputs."""
 import math
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -213,3 +214,62 @@ def test_split_form_reports_a_wait_that_runs_out(moe, dev, call, limit_ns):
     err.zero_()
     run(out)
     assert err.item() == 0 and torch.equal(out, want)
+
+
+# ---- devices ----------------------------------------------------------------------------------------
+
+def test_tensors_and_devices_have_to_fit_the_object(monkeypatch):
+    """The checks themselves, with stand-ins for tensors and for the current device."""
+    from mixture_experts_grouped_gb300 import ffn
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        ffn._cuda_device("cpu")
+    here = ffn._cuda_device("cuda")
+    assert here == torch.device("cuda:1") and ffn._cuda_device("cuda:0") == torch.device("cuda:0")
+    ffn._require_current(here)
+    with pytest.raises(ValueError):
+        ffn._require_current(torch.device("cuda:0"))
+
+    def tensor(device="cuda:1", dtype=torch.float16, shape=(4, 8), dense=True):
+        return SimpleNamespace(device=torch.device(device), dtype=dtype, shape=shape, is_contiguous=lambda: dense)
+
+    ffn._require("x", tensor(), here, torch.float16, 4, 8)
+    for bad in (tensor("cuda:0"), tensor("cpu"), tensor(dtype=torch.bfloat16), tensor(shape=(4, 7)), tensor(dense=False)):
+        with pytest.raises(ValueError):
+            ffn._require("x", bad, here, torch.float16, 4, 8)
+
+
+def training_objects(dev, device):
+    from mixture_experts_grouped_gb300 import train
+    T, H, I, E, k, bf = 4, 64, 32, 3, 2, dict(dtype=torch.bfloat16, device=dev)
+    layer = train.MoeTrainLayer(T, H, I, E, k, "bf16", torch.zeros((E, 2 * I, H), **bf), torch.zeros((E, H, I), **bf),
+                                device)
+    block = train.DenseMlp(T, H, I, "bf16", "gelu", *(torch.zeros(s, **bf) for s in ((I, H), (I,), (H, I), (H,))),
+                           device)
+    return layer, block, torch.zeros((T, H), **bf), torch.zeros((T, E), device=dev)
+
+
+def test_training_objects_need_a_cuda_device():
+    from mixture_experts_grouped_gb300 import train
+    w = torch.zeros((3, 64, 64)), torch.zeros((3, 64, 32))
+    with pytest.raises(ValueError):
+        train.MoeTrainLayer(4, 64, 32, 3, 2, "bf16", *w, device="cpu")
+    with pytest.raises(ValueError):
+        train.DenseMlp(4, 64, 32, "bf16", "gelu", w[0], None, w[1], None, device="cpu")
+
+
+@pytest.mark.gpu
+def test_training_objects_run_on_their_own_device_alone(moe, dev, monkeypatch):
+    layer, block, x, logits = training_objects(dev, "cuda")
+    layer.forward(x, logits)
+    block.forward(x)
+    n0 = moe.moe_launch_count()
+    for device in ("cpu", "cuda:1"):  # buffers apart from the weights
+        with pytest.raises(ValueError):
+            training_objects(dev, device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: layer.forward(x, logits), lambda: layer.backward(x), lambda: block.forward(x),
+                 lambda: block.backward(x)):
+        with pytest.raises(ValueError):
+            call()
+    assert moe.moe_launch_count() == n0
