@@ -79,10 +79,11 @@ def _cuda_device(device) -> torch.device:
 
 def _require(what: str, t: torch.Tensor, device: torch.device, dtype: torch.dtype, *shape: int) -> None:
     """A dense tensor of this type and shape on the object's device (the kernels take addresses as they come)."""
+    if t.dtype == dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return
     _require_shape(what, t, *shape)
     _require_type(what, t, dtype)
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    raise ValueError(f"{what} is on {t.device}, not on {device}")
 
 
 def _require_current(device: torch.device) -> None:
@@ -135,11 +136,10 @@ class DenseExpert:
     to another output."""
 
     def __init__(self, T, H, I, act, w_gate_up: torch.Tensor, w_down: torch.Tensor, device="cuda"):
-        _require_shape("gate/up weight", w_gate_up, 2 * I, H)
-        _require_shape("down weight", w_down, H, I)
-        dt = L.act_dtype(act)
-        _require_type("gate/up weight", w_gate_up, dt)
-        _require_type("down weight", w_down, dt)
+        dt = self.dtype = L.act_dtype(act)
+        device = self.device = _cuda_device(device)
+        _require("gate/up weight", w_gate_up, device, dt, 2 * I, H)
+        _require("down weight", w_down, device, dt, H, I)
         self.T, self.H, self.I = T, H, I
         self.act_code = M.ACT_CODES[act]
         self.w_gate_up, self.w_down = w_gate_up, w_down
@@ -149,7 +149,15 @@ class DenseExpert:
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
 
     def forward(self, x, addend=None, stream=None):
-        """The expert on rows [T, H], plus ``addend`` [T, H]; returns its output buffer."""
+        """The expert on rows [T, H], plus ``addend`` [T, H]; returns its output buffer. Rows and addend of another
+        type, shape, stride or device are refused (ValueError)."""
+        _require_current(self.device)
+        _require("x", x, self.device, self.dtype, self.T, self.H)
+        if addend is not None:
+            _require("addend", addend, self.device, self.dtype, self.T, self.H)
+        return self._run(x, addend, stream)
+
+    def _run(self, x, addend, stream):
         M.moe_dense_gemm(x, self.act_code, self.w_gate_up, None, M.MOE_FN_NONE, None, None, self.gate_up, self.T,
                          2 * self.I, self.H, self.err, stream)
         M.moe_swiglu(self.gate_up, self.act_code, self.T, self.I, self.h, stream)
@@ -192,7 +200,7 @@ class FeedForward:
     weights of one format) and is faster (:func:`few_tokens_pay`), and as
     :class:`layer.MoeLayer` elsewhere; the router weight is f32 [H, E]. The shared
     expert takes y in E4M3 (:class:`SharedExpert`) or as it is (:class:`DenseExpert`). One
-    of another T, H or activation type is refused (ValueError). There is
+    of another T, H or activation type is refused (ValueError), a :class:`DenseExpert` of another device too. There is
     no LoRA here: a layer with adapters runs :class:`layer.MoeLayer`'s steps.
     """
 
@@ -206,6 +214,8 @@ class FeedForward:
         if shared is not None and (shared.T, shared.H, shared.act_code) != (T, H, self.act_code):
             raise ValueError(f"the shared expert is one of T={shared.T}, H={shared.H}, activation type "
                              f"{shared.act_code}, the block of T={T}, H={H}, {self.act_code}")
+        if isinstance(shared, DenseExpert) and shared.device != _cuda_device(device):
+            raise ValueError(f"the shared expert is on {shared.device}, the block on {device}")
         self.norm_weight, self.w_router, self.shared = norm_weight, w_router, shared
         dt = L.act_dtype(act)
         self.residual = torch.empty((T, H), dtype=dt, device=device)
@@ -233,7 +243,7 @@ class FeedForward:
             ex.combine(stream)
             out = ex.out
         if isinstance(self.shared, DenseExpert):
-            out = self.shared.forward(self.y, out, stream)
+            out = self.shared._run(self.y, out, stream)  # (the block's own buffers: they fit)
         elif self.shared is not None:
             out = self.shared.forward(self.q, self.q_scales, out, stream)
         return out, self.residual

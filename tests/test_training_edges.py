@@ -273,3 +273,35 @@ def test_training_objects_run_on_their_own_device_alone(moe, dev, monkeypatch):
         with pytest.raises(ValueError):
             call()
     assert moe.moe_launch_count() == n0
+
+
+@pytest.mark.gpu
+def test_dense_expert_refuses_what_does_not_fit(moe, dev, monkeypatch):
+    from mixture_experts_grouped_gb300 import ffn
+    from mixture_experts_grouped_gb300 import layer as L
+    T, H, I, bf = 4, 64, 32, dict(dtype=torch.bfloat16, device=dev)
+    w = torch.zeros((2 * I, H), **bf), torch.zeros((H, I), **bf)
+    expert = ffn.DenseExpert(T, H, I, "bf16", *w)
+    x = torch.ones((T, H), **bf)
+    assert torch.equal(expert.forward(x, x), x)
+    n0 = moe.moe_launch_count()
+    for bad in (x[:3], x[:, :32], x.half(), x.float(), x.T.contiguous().T, x.cpu()):
+        for args in ((bad,), (bad, x), (x, bad)):
+            with pytest.raises(ValueError):
+                expert.forward(*args)
+    for bad in ((w[0].cpu(), w[1]), (w[0], w[1].half()), (w[1], w[0])):
+        with pytest.raises(ValueError):
+            ffn.DenseExpert(T, H, I, "bf16", *bad)
+    for device in ("cpu", "cuda:1"):
+        with pytest.raises(ValueError):
+            ffn.DenseExpert(T, H, I, "bf16", *w, device=device)
+    desc = [L.DeviceWeight(moe.MoeWeight(moe.MOE_W_BF16, 0, t.data_ptr(), None, None, None), [t])
+            for t in (torch.zeros((3, 2 * I, H), **bf), torch.zeros((3, H, I), **bf))]
+    norm, router = torch.ones(H, **bf), torch.zeros((H, 3), device=dev)
+    for device in ("cpu", "cuda:1"):
+        with pytest.raises(ValueError):
+            ffn.FeedForward(T, H, I, 3, 2, "bf16", norm, router, *desc, expert, device=device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        expert.forward(x)
+    assert moe.moe_launch_count() == n0
