@@ -92,6 +92,27 @@ def _require_current(device: torch.device) -> None:
         raise ValueError(f"the buffers are on {device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
+class _Buffers:
+    """Where the named buffers of an object lie, to tell inputs that a pass would overwrite before it is done with
+    them: not by their first address alone, since a view of a buffer may begin in its middle."""
+
+    def __init__(self, owner, *names: str):
+        self.at = {n: self._extent(getattr(owner, n)) for n in names if getattr(owner, n) is not None}
+
+    @staticmethod
+    def _extent(t: torch.Tensor):
+        return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+    def refuse(self, what: str, t: torch.Tensor, among=None, in_place: str = "") -> None:
+        """ValueError if t, an input of the pass, shares memory with a buffer (of those named); with ``in_place`` it may
+        be exactly that one."""
+        lo, hi = self._extent(t)
+        for name in among or self.at:
+            first, last = self.at.get(name, (0, 0))
+            if lo < last and first < hi and not (name == in_place and (lo, hi) == (first, last)):
+                raise ValueError(f"{what} lies in the object's own buffer {name}, which the pass overwrites")
+
+
 @dataclass
 class BlockFp8Weight:
     """E4M3 codes uint8 [N, K] with f32 scales [ceil(N / 128), ceil(K / 128)]."""
@@ -147,14 +168,18 @@ class DenseExpert:
         self.h = torch.empty((T, I), dtype=dt, device=device)
         self.out = torch.empty((T, H), dtype=dt, device=device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
+        self._own = _Buffers(self, "gate_up", "h", "out", "err")
 
     def forward(self, x, addend=None, stream=None):
         """The expert on rows [T, H], plus ``addend`` [T, H]; returns its output buffer. Rows and addend of another
-        type, shape, stride or device are refused (ValueError)."""
+        type, shape, stride or device are refused (ValueError), and such as the pass overwrites before it has read
+        them; the output buffer itself may be the addend."""
         _require_current(self.device)
         _require("x", x, self.device, self.dtype, self.T, self.H)
+        self._own.refuse("x", x, ("gate_up", "err"))
         if addend is not None:
             _require("addend", addend, self.device, self.dtype, self.T, self.H)
+            self._own.refuse("addend", addend, in_place="out")
         return self._run(x, addend, stream)
 
     def _run(self, x, addend, stream):

@@ -17,7 +17,7 @@ import torch
 
 from . import layer as L
 from . import moe as M
-from .ffn import _cuda_device, _require, _require_current
+from .ffn import _Buffers, _cuda_device, _require, _require_current
 
 
 class MoeTrainLayer:
@@ -67,13 +67,22 @@ class MoeTrainLayer:
         self.d_weights, self.d_logits = f32(T, k), f32(T, E)
         self.d_gate_up, self.d_down = f32(E, 2 * I, H).zero_(), f32(E, H, I).zero_()
         self.logits = None
+        self._own = _Buffers(self, "topk_ids", "topk_weights", "sorted_token_ids", "expert_ids", "pair_to_row", "offsets",
+                             "total", "align_ws", "err", "ones", "xs", "gate_up", "h", "y", "out", "d_y", "d_h", "d_gu",
+                             "d_xs", "d_x", "d_weights", "d_logits", "d_gate_up", "d_down")
+        self._before_x = ("topk_ids", "topk_weights", "sorted_token_ids", "expert_ids", "pair_to_row", "offsets", "total",
+                          "align_ws", "err", "xs")  # written before x has been read, or while it is
 
     def forward(self, x, logits, stream=None):
-        """The layer on x [T, H] routed by logits [T, E]; returns its output buffer."""
+        """The layer on x [T, H] routed by logits [T, E]; returns its output buffer. logits is kept for ``backward``, must
+        not change before it and is no buffer of the layer; x may be one that the pass has read by the time it writes
+        it, like an earlier output."""
         T, H, I, E, k, P, act = self.T, self.H, self.I, self.E, self.k, self.P, self.act_code
         _require_current(self.device)
         _require("x", x, self.device, self.dtype, T, H)
         _require("logits", logits, self.device, torch.float32, T, E)
+        self._own.refuse("x", x, self._before_x)
+        self._own.refuse("logits", logits)
         self.logits = logits
         M.moe_route_topk_softmax(logits, self.topk_ids, self.topk_weights, T, E, k, self.renormalize, stream)
         M.moe_align_block_size(self.topk_ids, P, E, 1, P, self.sorted_token_ids, self.expert_ids, self.offsets,
@@ -94,6 +103,7 @@ class MoeTrainLayer:
             raise RuntimeError("backward without a forward pass")
         _require_current(self.device)
         _require("d_out", d_out, self.device, self.dtype, T, H)
+        self._own.refuse("d_out", d_out, ("d_y", "d_weights", "err"))
         M.moe_combine_backward(d_out, self.y, act, self.pair_to_row, self.topk_weights, self.d_y, self.d_weights, T, H,
                                k, P, self.err, stream)
         M.moe_ragged_gemm(self.d_y, act, self.w_down, True, self.offsets, P, H, I, E, self.d_h, self.err, stream)
@@ -144,15 +154,17 @@ class DenseMlp:
         self.d_b2 = f32(H).zero_() if b2 is not None else None
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         self.x = None
+        self._own = _Buffers(self, "pre", "h", "out", "d_h", "d_x", "d_w1", "d_w2", "d_b1", "d_b2", "err")
 
     def forward(self, x, residual=None, stream=None):
-        """The block on x [T, H]; returns its output buffer. x is kept for ``backward`` and must not change before it."""
+        """The block on x [T, H]; returns its output buffer. x is kept for ``backward``, must not change before it
+        and is no buffer of the block; the residual may be the output buffer itself."""
         _require_current(self.device)
         _require("x", x, self.device, self.dtype, self.T, self.H)
-        if x.data_ptr() in (self.out.data_ptr(), self.d_x.data_ptr()):
-            raise ValueError("x is a buffer of the block itself, which a pass overwrites")
+        self._own.refuse("x", x)
         if residual is not None:
             _require("residual", residual, self.device, self.dtype, self.T, self.H)
+            self._own.refuse("residual", residual, ("pre", "h", "out", "err"), in_place="out")
         self.x = x
         M.moe_dense_gemm(x, self.act_code, self.w1, self.b1, self.fn, None, self.pre, self.h, self.T, self.I, self.H,
                          self.err, stream)
@@ -168,6 +180,7 @@ class DenseMlp:
             raise RuntimeError("backward without a forward pass")
         _require_current(self.device)
         _require("d_out", d_out, self.device, self.dtype, T, H)
+        self._own.refuse("d_out", d_out, ("d_b2", "d_w2", "d_h", "err"))
         if self.d_b2 is not None:
             M.moe_bias_act_backward(d_out, None, act, M.MOE_FN_NONE, T, H, None, self.d_b2, accumulate,
                                     stream)

@@ -305,3 +305,97 @@ def test_dense_expert_refuses_what_does_not_fit(moe, dev, monkeypatch):
     with pytest.raises(ValueError):
         expert.forward(x)
     assert moe.moe_launch_count() == n0
+
+
+# ---- an object's own buffers as its inputs -----------------------------------------------------------
+
+def test_buffers_that_an_input_must_not_share():
+    from mixture_experts_grouped_gb300 import ffn
+    pool = torch.zeros(64)
+    own = ffn._Buffers(SimpleNamespace(a=pool[:16], b=pool[16:32], none=None), "a", "b", "none")
+    own.refuse("x", pool[32:])
+    own.refuse("x", pool[:16], ("b",))
+    own.refuse("x", pool[16:32], in_place="b")
+    own.refuse("x", torch.zeros(0))
+    for bad in (pool[:16], pool[15:16], pool[8:24], pool[31:40], pool):
+        with pytest.raises(ValueError):
+            own.refuse("x", bad)
+    for bad in (pool[16:24], pool[20:32], pool[24:40], pool[8:24]):  # not exactly b
+        with pytest.raises(ValueError):
+            own.refuse("x", bad, ("b",), in_place="b")
+
+
+@pytest.mark.gpu
+def test_dense_block_refuses_every_buffer_that_it_overwrites(moe, dev):
+    from mixture_experts_grouped_gb300 import train
+    T, H, bf = 8, 64, dict(dtype=torch.bfloat16, device=dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    w = [torch.randn(s, generator=g, device=dev).bfloat16() / 8 for s in ((H, H), (H,), (H, H), (H,))]
+    block = train.DenseMlp(T, H, H, "bf16", "gelu", *w)  # H = I: every buffer has x's shape
+    x = torch.randn((T, H), generator=g, device=dev).bfloat16()
+    out = block.forward(x).clone()
+    dx = block.backward(x).clone()
+    n0 = moe.moe_launch_count()
+    whole = {n: getattr(block, n) for n in ("pre", "h", "out", "d_h", "d_x")}
+    whole["d_w1"] = block.d_w1.view(torch.bfloat16).flatten()[16: 16 + T * H].view(T, H)  # within
+    for t in whole.values():
+        with pytest.raises(ValueError):
+            block.forward(t)
+    for n in ("pre", "h"):
+        with pytest.raises(ValueError):
+            block.forward(x, residual=whole[n])
+    with pytest.raises(ValueError):
+        block.backward(whole["d_h"])
+    assert moe.moe_launch_count() == n0
+    # what a pass has read before it writes it: the last output added in place, gradients that are outputs
+    added = block.forward(x, residual=x).clone()
+    assert torch.equal(block.forward(x, residual=block.d_x.copy_(x)), added)
+    assert torch.equal(block.forward(x, residual=block.out.copy_(x)), added)
+    assert torch.equal(block.forward(x), out)
+    assert torch.equal(block.backward(block.d_x.copy_(x)), dx)
+
+
+@pytest.mark.gpu
+def test_expert_layer_refuses_every_buffer_that_it_overwrites(moe, dev):
+    from mixture_experts_grouped_gb300 import train
+    T, H, E = 8, 64, 2
+    g = torch.Generator(device=dev).manual_seed(2)
+    w = [torch.randn(s, generator=g, device=dev).bfloat16() / 8 for s in ((E, 2 * H, H), (E, H, H))]
+    layer = train.MoeTrainLayer(T, H, H, E, 1, "bf16", *w, renormalize=False)  # one expert a token: rows are tokens
+    both = train.MoeTrainLayer(T, H, H, E, E, "bf16", *w)                      # all: weights have the logits' shape
+    x = torch.randn((T, H), generator=g, device=dev).bfloat16()
+    logits = torch.randn((T, E), generator=g, device=dev)
+    out = layer.forward(x, logits).clone()
+    dx, dl = (t.clone() for t in layer.backward(x))
+    n0 = moe.moe_launch_count()
+    for call in (lambda: layer.forward(layer.xs, logits), lambda: layer.forward(x, layer.d_logits),
+                 lambda: both.forward(x, both.topk_weights), lambda: both.forward(x, both.d_weights),
+                 lambda: layer.backward(layer.d_y),
+                 lambda: layer.forward(x, layer.d_down.flatten()[3: 3 + T * E].view(T, E))):
+        with pytest.raises(ValueError):
+            call()
+    assert moe.moe_launch_count() == n0
+    # what a pass has read before it writes it
+    assert torch.equal(layer.forward(layer.out.copy_(x), logits), out)
+    assert torch.equal(layer.forward(layer.d_x.copy_(x), logits), out)
+    assert all(torch.equal(a, b) for a, b in zip(layer.backward(layer.d_x.copy_(x)), (dx, dl)))
+
+
+@pytest.mark.gpu
+def test_dense_expert_refuses_every_buffer_that_it_overwrites(moe, dev):
+    from mixture_experts_grouped_gb300 import ffn
+    T, H = 8, 64
+    g = torch.Generator(device=dev).manual_seed(3)
+    w = [torch.randn(s, generator=g, device=dev).bfloat16() / 8 for s in ((2 * H, H), (H, H))]
+    expert = ffn.DenseExpert(T, H, H, "bf16", *w)
+    x = torch.randn((T, H), generator=g, device=dev).bfloat16()
+    out = expert.forward(x, x).clone()
+    n0 = moe.moe_launch_count()
+    within = expert.gate_up.flatten()[8: 8 + T * H].view(T, H)
+    for args in ((within,), (x, within), (x, expert.h)):
+        with pytest.raises(ValueError):
+            expert.forward(*args)
+    assert moe.moe_launch_count() == n0
+    assert torch.equal(expert.forward(x, expert.out.copy_(x)), out)
+    assert torch.equal(expert.forward(expert.out.copy_(x), x), out)
+    assert torch.equal(expert.forward(expert.h.copy_(x), x), out)
