@@ -83,7 +83,7 @@ class MoeTrainLayer:
         _require("logits", logits, self.device, torch.float32, T, E)
         self._own.refuse("x", x, self._before_x)
         self._own.refuse("logits", logits)
-        self.logits = logits
+        self.logits = None  # (until the pass is complete: a call of it may be refused)
         M.moe_route_topk_softmax(logits, self.topk_ids, self.topk_weights, T, E, k, self.renormalize, stream)
         M.moe_align_block_size(self.topk_ids, P, E, 1, P, self.sorted_token_ids, self.expert_ids, self.offsets,
                                self.total, self.pair_to_row, self.err, self.align_ws, self.align_ws_bytes, stream)
@@ -93,6 +93,7 @@ class MoeTrainLayer:
         M.moe_swiglu(self.gate_up, act, P, I, self.h, stream)
         M.moe_ragged_gemm(self.h, act, self.w_down, False, self.offsets, P, H, I, E, self.y, self.err, stream)
         M.moe_combine(self.y, act, self.pair_to_row, self.topk_weights, self.out, T, H, k, P, self.err, stream)
+        self.logits = logits
         return self.out
 
     def backward(self, d_out, accumulate: bool = False, stream=None):
@@ -165,11 +166,12 @@ class DenseMlp:
         if residual is not None:
             _require("residual", residual, self.device, self.dtype, self.T, self.H)
             self._own.refuse("residual", residual, ("pre", "h", "out", "err"), in_place="out")
-        self.x = x
+        self.x = None  # (until the pass is complete)
         M.moe_dense_gemm(x, self.act_code, self.w1, self.b1, self.fn, None, self.pre, self.h, self.T, self.I, self.H,
                          self.err, stream)
         M.moe_dense_gemm(self.h, self.act_code, self.w2, self.b2, M.MOE_FN_NONE, residual, None, self.out, self.T,
                          self.H, self.I, self.err, stream)
+        self.x = x
         return self.out
 
     def backward(self, d_out, accumulate: bool = False, stream=None):

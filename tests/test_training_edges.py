@@ -399,3 +399,22 @@ def test_dense_expert_refuses_every_buffer_that_it_overwrites(moe, dev):
     assert torch.equal(expert.forward(x, expert.out.copy_(x)), out)
     assert torch.equal(expert.forward(expert.out.copy_(x), x), out)
     assert torch.equal(expert.forward(expert.h.copy_(x), x), out)
+
+
+@pytest.mark.gpu
+def test_a_pass_that_was_refused_midway_has_no_backward_pass(moe, dev):
+    """E above the routing's limit: the layer's first call refuses it, and what is left in the buffers is no forward
+    pass."""
+    from mixture_experts_grouped_gb300 import train
+    T, H, I, E, k, bf = 4, 64, 32, moe.MOE_MAX_EXPERTS + 1, 2, dict(dtype=torch.bfloat16, device=dev)
+    layer = train.MoeTrainLayer(T, H, I, E, k, "bf16", torch.zeros((E, 2 * I, H), **bf), torch.zeros((E, H, I), **bf))
+    x, logits = torch.zeros((T, H), **bf), torch.zeros((T, E), device=dev)
+    with pytest.raises(moe.MoeError):
+        layer.forward(x, logits)
+    with pytest.raises(RuntimeError, match="without a forward pass"):
+        layer.backward(x)
+    block = train.DenseMlp(T, 60, I, "bf16", "gelu", torch.zeros((I, 60), **bf), None, torch.zeros((60, I), **bf), None)
+    with pytest.raises(moe.MoeError):
+        block.forward(torch.zeros((T, 60), **bf))
+    with pytest.raises(RuntimeError, match="without a forward pass"):
+        block.backward(torch.zeros((T, 60), **bf))
