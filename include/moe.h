@@ -555,7 +555,7 @@ int moe_few_tokens(const void* x, int32_t act, const float* logits, int32_t* top
  * depends on the sizes alone; each output is rounded once. A tensor core cuts its
  * running sums rather than round them: n products may come out n 2^-27 of the sum of
  * their magnitudes short. n is the contraction (N or K) of a product; of a weight gradient
- * it is at most 4096 rows for f32, 16384 for f16 and 131072 for bf16, whose sums are then
+ * it is at most 640 rows for f32, 16384 for f16 and 131072 for bf16, whose sums are then
  * added in f32.
  */
 

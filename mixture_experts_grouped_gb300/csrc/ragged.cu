@@ -96,11 +96,11 @@ RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
 // Of one group with few tiles, the split form: parts CTAs share a tile's rows; its time as above, more where two of them
 // share an SM, and for addends, which its lanes read 64 bytes at a time. (us, pairs / split, f32: 4000 rows, 512 x 512 18.2 /
 // 10.7; 2000 rows, 2048 x 512 12.3 / 11.6; 100 rows, 1000 x 1000 6.1 / 5.6, with addends 7.5 / 10.3; 30000 rows, 264 x 520
-// 168 / 32; 640 rows, 2048 x 1408 9.0 / 14.0.) A part takes no more rows than a chunk of the pairs' form.
+// 168 / 32; 640 rows, 2048 x 1408 9.0 / 14.0.)
 struct GradientForm {
     int parts, kt;
 };
-GradientForm pick_gradient_form(const RaggedParams& p, bool f32, int act, int sms) {
+GradientForm pick_gradient_form(const RaggedParams& p, bool f32, int sms) {
     const int64_t units = ceil_div(p.C, gradient_unit(f32)), widest = 256 / gradient_unit(f32);
     const int64_t kt0 = ceil_div(units, widest);
     GradientForm best{0, static_cast<int>(kt0)};
@@ -122,7 +122,6 @@ GradientForm pick_gradient_form(const RaggedParams& p, bool f32, int act, int sm
     for (const auto& s : kSplits) {
         if (s.parts > KB || tiles * s.parts > 2 * sms) break;
         const int64_t blocks = ceil_div(KB, s.parts);
-        if (blocks > gradient_chunk(f32, act)) continue;
         const int64_t ns = s.launch_ns + (tiles * s.parts > sms ? 2000 + blocks * 720 : blocks * 230) +
                            (s.parts < 8 ? 2500 : 4000) + (p.addend ? 400 + 4600 / s.parts : 0);
         if (ns < best_ns) {
@@ -215,7 +214,7 @@ extern "C" int moe_ragged_wgrad(const void* dy, const void* x, int32_t act, cons
     g.K = K;
     g.st = static_cast<cudaStream_t>(stream);
     g.who = who;
-    const moe::GradientForm form = moe::pick_gradient_form(g.p, dw_f32 != 0, act, moe::sm_count());
+    const moe::GradientForm form = moe::pick_gradient_form(g.p, dw_f32 != 0, moe::sm_count());
     g.parts = form.parts;
     g.kt = form.kt;
     return moe::launch_ragged_wgrad(g);

@@ -35,6 +35,7 @@ constexpr int SG = 36;        // and their stride (floats): 16-byte reads withou
 
 struct SplitTail {
     uint64_t full[SPLIT_MAX_STAGES], empty[SPLIT_MAX_STAGES], done;
+    uint64_t sums[2], taken[2];  // a chunk's sums there, and read
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -102,7 +103,7 @@ __device__ __forceinline__ void store_rows(const RaggedParams& p, const float (&
 template <int KIND> struct Addends {
     float4 v[4];
     __device__ __forceinline__ void load(const RaggedParams& p, int n, int k, int cols) {
-        if (KIND != G32 || !p.addend || n >= p.J) return;
+        if (in_16_bits(KIND) || !p.addend || n >= p.J) return;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (4 * j < cols && k + 4 * j < p.C)
@@ -114,7 +115,7 @@ template <int ACT, int KIND>
 __device__ __forceinline__ void store_gradient(const RaggedParams& p, int n, int k, float4 f, const float4& a) {
     if (n >= p.J || k >= p.C) return;
     const size_t at = static_cast<size_t>(n) * p.C + k;
-    if (KIND == G16) {
+    if (in_16_bits(KIND)) {
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
             make_uint2(Act<ACT>::pack2(f.x, f.y), Act<ACT>::pack2(f.z, f.w));
     } else {
@@ -124,7 +125,7 @@ __device__ __forceinline__ void store_gradient(const RaggedParams& p, int n, int
 }
 
 template <int MODE, int ACT, int KIND>
-__global__ void __launch_bounds__(SPLIT_THREADS)
+__global__ void __launch_bounds__(SPLIT_THREADS, KIND == G16LONG || KIND == G32LONG ? 2 : 1)  // (two CTAs to an SM)
 split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const SplitParams sp) {
     const RaggedParams& p = sp.r;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -142,6 +143,10 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_init(&s.empty[q], 1);
         }
         mbar_init(&s.done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.sums[i], 1);
+            mbar_init(&s.taken[i], 4);  // the epilogue's warps
+        }
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -190,6 +195,9 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const bool any = rows > 0;  // the same in all CTAs of the cluster
     const int boxes = MODE == WGRAD ? 0 : p.offsets ? n / 16 : 1;
     const uint32_t bytes = OPER + (MODE == WGRAD ? OPER : boxes * sp.box * 128), stage_bytes = sp.stage;
+    // the rows of a long part of a gradient come in chunks (see gradient_chunk)
+    constexpr bool CHUNKED = KIND == G16LONG || KIND == G32LONG;
+    constexpr int CHUNK = gradient_chunk(!in_16_bits(KIND), ACT);
     bool ok = any;  // (a wait that gave up in another CTA of the cluster shows in the error word alone)
 
     if (warp == 0) {
@@ -232,6 +240,21 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         int stage = 0;
         uint32_t phase = 0;
         for (int b = kb0; any && b < kb1; ++b) {
+            uint32_t acc = tmem;
+            bool more = b > kb0;  // adds to what the accumulator holds
+            if constexpr (CHUNKED) {  // the two accumulators in turn
+                const int ch = (b - kb0) / CHUNK, in = (b - kb0) - ch * CHUNK;
+                if (in == 0 && ch > 0) {
+                    if (elect_one()) tc_commit(&s.sums[(ch - 1) & 1]);
+                    __syncwarp();
+                    if (ch > 1) {
+                        if (!mbar_wait_warp(&s.taken[ch & 1], ((ch >> 1) - 1) & 1, wc)) break;
+                        tc_fence_after();
+                    }
+                }
+                acc += (ch & 1) * 128;
+                more = in > 0;
+            }
             if (!mbar_wait_warp(&s.full[stage], phase, wc)) break;
             tc_fence_after();
             const uint32_t at = smem_u32(smem + stage * stage_bytes);
@@ -240,7 +263,7 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k)
-                    tc_mma(tmem, ad + k * step_a, bd + k * step_b, idesc, b > kb0 || k > 0);
+                    tc_mma(acc, ad + k * step_a, bd + k * step_b, idesc, more || k > 0);
                 tc_commit(&s.empty[stage]);
             }
             __syncwarp();
@@ -254,8 +277,40 @@ split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         mbar_drain(&s.done, 0, kWaitLimitNs / 8);
     } else {
         if constexpr (KIND == FULL) prefetch_residual(p, lane, m0, rows, j0 + 32 * (warp & 3));
-        ok = mbar_wait_warp(&s.done, 0, wc) && any;
-        tc_fence_after();
+        if constexpr (CHUNKED) {
+            // the chunks' sums, added up in registers and laid into the first accumulator
+            const int chunks = (kb1 - kb0 + CHUNK - 1) / CHUNK;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            uint32_t v[8][16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[i][j] = 0u;
+            for (int ch = 0; ch < chunks; ++ch) {
+                const bool last = ch + 1 == chunks;
+                ok = mbar_wait_warp(last ? &s.done : &s.sums[ch & 1], last ? 0 : ch >> 1 & 1, wc);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t u[16];
+                    tmem_ld16(lanes + (ch & 1) * 128 + 16 * i, u);
+                    tmem_ld16_wait(u);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[i][j] = __float_as_uint(__uint_as_float(v[i][j]) + __uint_as_float(u[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && !last) mbar_arrive(&s.taken[ch & 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tmem_st16(lanes + 16 * i, v[i]);
+            tmem_st_wait();
+        } else {
+            ok = mbar_wait_warp(&s.done, 0, wc) && any;
+            tc_fence_after();
+        }
     }
     __syncwarp();
     const bool epi = warp >= 2;
@@ -388,6 +443,7 @@ template <int MODE, int ACT, int KIND> int launch_split_kind(const RaggedArgs& g
     const int rows = MODE == WGRAD ? SPLIT_ROWS : ((g.p.rows + 15) / 16 + mt - 1) / mt * 16;  // of the tallest tile
     sp.box = MODE == WGRAD ? 64 : g.p.offsets ? 16 : rows;
     sp.tmem = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    if (KIND == G16LONG || KIND == G32LONG) sp.tmem = 256;  // two accumulators
     const int rest = static_cast<int>(sizeof(SplitTail));
     sp.stage = OPER + rows * 128;
     sp.stages = (most - rest) / sp.stage;  // 3 at least

@@ -22,9 +22,9 @@
 //   the other CTA's MMA warp was not hidden and cost 1.2 us a tile (8 groups of 1024 rows,
 //   4096 x 14336: 668 us, 559 with rows that 16 divides).
 //
-// Roles: warps 0 and 6 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
-// CTA (the leader) issues the MMAs, warps 2 to 5 and 8 to 11 are the epilogue (with an
-// addend the latter copy for the former), warp 7 makes the tails.
+// Roles: warps 0 and 2 copy the two operands (TMA, 128-byte swizzle), warp 1 of the even
+// CTA (the leader) issues the MMAs, warp 3 makes the tails, warps 4 to 11 are the epilogue
+// (GADD: the latter four copy for the former).
 // Two accumulators of 256 TMEM columns let the epilogue of a tile run beside the next
 // one's MMAs. The issuing warps run their loops whole and elect a lane for the MMAs and
 // copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
@@ -47,12 +47,13 @@ namespace ragged {
 namespace {
 
 enum { ROWS_FWD = 0, ROWS_BACK = 1, WGRAD = 2 };
-// kinds of gradient: 16-bit, f32, f32 with an addend, 16-bit of more rows than a chunk (whose loop would cost the others
-// 1%); of the rows form: the product alone, or with bias,
-// activation function, residual and z (their code, jumped over, still cost a plain product's epilogue half its time
-// in instruction fetches)
-enum { G16 = 0, G32 = 1, GADD = 2, G16LONG = 4, PLAIN = 0, FULL = 3 };
+// kinds of gradient: 16-bit, f32, f32 with addends that come by TMA (GADD) or by loads (G32ADD; ragged_wgrad.cu has the
+// choice), and those whose chunks' loop would cost the others time or registers: 16-bit of more rows than a chunk, and
+// (split form alone) f32; of the rows form: the product alone, or with bias, activation function, residual and z (their
+// code, jumped over, still cost a plain product's epilogue half its time in instruction fetches)
+enum { G16 = 0, G32 = 1, GADD = 2, G16LONG = 4, G32LONG = 5, G32ADD = 6, PLAIN = 0, FULL = 3 };
 constexpr bool in_16_bits(int kind) { return kind == G16 || kind == G16LONG; }
+constexpr bool in_registers(int kind) { return kind == G32 || kind == G32ADD; }  // (see RowSums)
 
 constexpr int BK = 64;
 constexpr int OPER = 128 * BK * 2;  // bytes of a CTA's share of an operand per stage
@@ -78,14 +79,17 @@ struct Tail {
 // warps finish a tile, two to a quarter of the TMEM lanes, which take its steps in turn. A
 // gradient with an addend is bound by their bytes: four warps with four slots each, so that
 // three steps' addends are on their way, four others that load and store for them, and
-// four stages. Other gradients have a slot a warp
-// and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four). The rows form
+// four stages. Other gradients have a slot a warp and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four). The rows form
 // has six stages of full height, more of lower ones: a group's few rows leave a tile to its
 // weights' latency, and an SM streams them as fast as it has copies in flight.
 template <int MODE, int KIND> struct Shape {
     static constexpr int HALVES = KIND == GADD ? 1 : 2;  // warps to a quarter
     static constexpr int WARPS = 4 * HALVES;
     static constexpr int THREADS = 384;
+    // kinds that keep a tile's sums in registers: those of the first four warps' threads, and of the epilogue's; together
+    // no more than the launch's
+    static constexpr int REGS_ROLES = 72, REGS_SUMS = 216, REGS_LAUNCH = 168;
+    static_assert(128 * REGS_ROLES + 256 * REGS_SUMS <= THREADS * REGS_LAUNCH, "more registers than the launch has");
     static constexpr int SLOTS = KIND == GADD ? 4 : 1;
     static constexpr int STAGES = MODE != WGRAD ? 6 : KIND == GADD ? 4 : 5;  // of full height
     static constexpr int STG_WARP = MODE == WGRAD ? SLOTS * SLOT : STG;
@@ -296,6 +300,15 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 template <int ACT>
 __device__ __forceinline__ float bias_of(const RaggedParams& p, int col) {
     if (!p.bias || col >= p.J) return 0.0f;
@@ -442,9 +455,12 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
 
 // A tensor core's f32 sums are cut, not rounded, at each step of 16 products: of n products
 // of one sign, a sum comes out up to n 2^-27 short (measured, as a part of it: 4096 rows
-// 2.6e-5, 30000 1.9e-4). A gradient therefore takes its rows in chunks (gradient_chunk) and
-// adds the chunks in f32: the first stays in its accumulator, the others come into the second
-// one and are added to it, the last one on its way out.
+// 2.6e-5, 30000 1.9e-4), and of n products of random signs n 1.2e-9. A gradient therefore
+// takes its rows in chunks (gradient_chunk) and adds the chunks in f32. G32: the chunks take
+// the accumulators in turn, and the epilogue adds them up in registers, 128 a lane, beside the
+// next chunk's MMAs. GADD, whose
+// groups are short, and G16LONG: the first chunk stays in its accumulator, the others come into the
+// second one and are added to it, the last one on its way out.
 
 // adds the accumulator at tb to the one at ta: the columns that this warp will store, COLS of
 // every HALVES * COLS
@@ -618,6 +634,96 @@ __device__ __forceinline__ bool wgrad_epilogue(Tail& s, const RaggedParams& p, c
     return true;
 }
 
+// ---- G32: sums in registers ----------------------------------------------------------------
+// Lane = row n of dw; a warp has every other 32 columns of a tile.
+struct RowSums {
+    uint32_t v[4][32];
+    // adds 32 columns of an accumulator
+    __device__ __forceinline__ void add(int i, uint32_t ta) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t u[16];
+            tmem_ld16(ta + 16 * h, u);
+            tmem_ld16_wait(u);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[i][16 * h + j] = __float_as_uint(__uint_as_float(v[i][16 * h + j]) + __uint_as_float(u[j]));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[i][j] = 0u;
+    }
+};
+// brings the lane's addends into L2, ahead of their use
+__device__ __forceinline__ void prefetch_addend(const RaggedParams& p, const Tile& t, int row, int first, int cols) {
+    if (t.j0 + row >= p.J) return;
+    const float* at = p.addend + (static_cast<size_t>(t.e) * p.J + t.j0 + row) * p.C + t.k0;
+    for (int c = first; c < cols; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
+}
+// A warp's sums, and its addends, through its slot to dw (which may hold the addends). The addends are read 128 bytes of a
+// row to eight lanes, a step ahead, and meet the sums in the slot: read by the lane that adds them, they took the L1 1.1 us a
+// step of the CTA's warps (16384 rows of 8 groups, 4096 x 3584: 395 us).
+struct Addend {
+    float4 f[8];  // of rows 4 q + lane / 8
+    __device__ __forceinline__ void load(const float* at, int C, int rows, int cols, int lane) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r = 4 * q + (lane >> 3), c = 4 * (lane & 7);
+            f[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < rows && c < cols) f[q] = *reinterpret_cast<const float4*>(at + static_cast<size_t>(r) * C + c);
+        }
+    }
+};
+template <int KIND>
+__device__ __forceinline__ void store_sums(const RaggedParams& p, const CUtensorMap* tm_out, uint8_t* slot, RowSums& s,
+                                           uint32_t ta, const Tile& t, int n_off, int half, int cols, int lane) {
+    const int n = t.j0 + n_off;
+    const float* from = p.addend + (static_cast<size_t>(t.e) * p.J + n) * p.C + t.k0;
+    // (G32ADD always has them. Where the compiler knows, it issues the next step's loads too late: 8192 rows of 8 groups, 4096 x
+    // 3584, 231 us and 222)
+    const bool add = KIND == G32ADD && p.addend;
+    Addend a;
+    if (add) a.load(from + 32 * half, p.C, p.J - n, cols - 32 * half, lane);
+    uint8_t* at = slot + lane * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = 32 * half + 64 * i;
+        if (c >= cols) break;
+        if (KIND == G32 && t.rows > 0) s.add(i, ta + 64 * i);
+        if (lane == 0) store_wait_read();  // the slot's last store
+        __syncwarp();
+        if (add) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int r = 4 * q + (lane >> 3);
+                *reinterpret_cast<float4*>(slot + r * 128 + 16 * ((lane ^ r) & 7)) = a.f[q];
+            }
+            __syncwarp();
+            a.load(from + c + 64, p.C, p.J - n, cols - c - 64, lane);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float4* piece = reinterpret_cast<float4*>(at + 16 * (q ^ (lane & 7)));
+            float4 f = make_float4(__uint_as_float(s.v[i][4 * q]), __uint_as_float(s.v[i][4 * q + 1]),
+                                   __uint_as_float(s.v[i][4 * q + 2]), __uint_as_float(s.v[i][4 * q + 3]));
+            if (add) {
+                const float4 g = *piece;
+                f = make_float4(f.x + g.x, f.y + g.y, f.z + g.z, f.w + g.w);
+            }
+            *piece = f;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && n < p.J) {
+            store_3d(tm_out, slot, t.k0 + c, n, t.e);
+            store_commit();
+        }
+    }
+}
+
 // ---- the kernel ---------------------------------------------------------------------------
 // tm_a: the M operand (weights; dy), tm_b: the N operand (rows; x). Gradient form: tm_ta and
 // tm_tb are those in boxes of a unit, tm_out and tm_add the gradient and its addend.
@@ -628,7 +734,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_add,
               const RaggedParams p) {
     using S = Shape<MODE, KIND>;
-    constexpr bool CHUNKED = MODE == WGRAD && KIND != G16;
+    constexpr bool RING = MODE == WGRAD && in_registers(KIND), CHUNKED = MODE == WGRAD && KIND != G16;
     constexpr int CHUNK = gradient_chunk(!in_16_bits(KIND), ACT);
     extern __shared__ __align__(1024) uint8_t smem[];
     Tail& s = *reinterpret_cast<Tail*>(smem + S::TAIL_AT);
@@ -692,187 +798,193 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     auto blocks_of = [&](const Tile& t) { return MODE == WGRAD ? (t.rows / 16 + 3) / 4 : KB; };
     auto chunks_of = [&](const Tile& t) { return CHUNKED ? max(1, (blocks_of(t) + CHUNK - 1) / CHUNK) : 1; };
 
-    if (warp == 0 || warp == 6) {
-        // ---------------- copies: warp 0 the M operand, warp 6 the N operand ----------------
-        const bool is_a = warp == 0;
-        uint32_t stage = 0, phase = 0;
-        long issued = 0;
-        bool ok = true;
-        for (Walk at(p); at.tile < n_tiles && ok; at.next()) {
-            const Tile t = get_tile<MODE>(s, p, at.tile);
-            const int nb = blocks_of(t);
-            for (int b = 0; b < nb; ++b) {
-                if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    if (is_a && rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (OPER + b_bytes));
-                    const uint32_t bar = lead_full + stage * 8;
-                    uint8_t* dst = smem + stage * stage_bytes + (is_a ? 0 : OPER);
-                    if (MODE == WGRAD) {
-                        const int r = t.m0 + b * BK;
-                        if (is_a) {
-                            const int n = t.j0 + 128 * static_cast<int>(rank);
-                            tma_load_2d_pair(dst, &tm_a, n, r, bar);
-                            tma_load_2d_pair(dst + 8192, &tm_a, n + 64, r, bar);
-                        } else {
-                            const int k = t.k0 + t.n / 2 * static_cast<int>(rank);  // (two boxes may bring more than the share)
-                            tma_load_2d_pair(dst, &tm_b, k, r, bar);
-                            if (second) tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
-                        }
-                    } else {
-                        const int c = b * BK;
-                        if (!is_a) {
-                            // (the box has maxu * 8 rows; the MMA reads n / 2 of them)
-                            tma_load_2d_pair(dst, &tm_b, c, t.m0 + static_cast<int>(rank) * (t.n / 2), bar);
-                        } else if (MODE == ROWS_FWD) {
-                            load_3d_pair(dst, &tm_a, c, t.j0 + 128 * static_cast<int>(rank), t.e, bar);
-                        } else {
-                            const int j = t.j0 + 128 * static_cast<int>(rank);
-                            load_3d_pair(dst, &tm_a, j, c, t.e, bar);
-                            load_3d_pair(dst + 8192, &tm_a, j + 64, c, t.e, bar);
-                        }
-                    }
-                }
-                __syncwarp();
-                ++issued;
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (is_a && rank == 0) {  // let every copy land before either CTA may exit
-            const long ring = stages, from = issued > ring ? issued - ring : 0;
-            for (long j = from; j < issued; ++j)
-                mbar_drain(&s.full[j % ring], static_cast<uint32_t>((j / ring) & 1), kWaitLimitNs / 8);
-        }
-    } else if (warp == 1) {
-        if (rank == 0) {
-            // ---------------- MMAs (leader) ----------------
-            const uint32_t major = MODE == WGRAD ? kMajorA | kMajorB : MODE == ROWS_BACK ? kMajorA : 0u;
-            constexpr uint32_t STEP_K = 32 >> 4, STEP_MN = 2048 >> 4;  // 16 contraction indices on, in descriptor units
-            constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
-            uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
+    if (warp < 4) {
+        if constexpr (RING) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::REGS_ROLES));
+        if (warp == 0 || warp == 2) {
+            // ---------------- copies: warp 0 the M operand, warp 2 the N operand ----------------
+            const bool is_a = warp == 0;
+            uint32_t stage = 0, phase = 0;
+            long issued = 0;
             bool ok = true;
-            Tile next{};
-            Walk at(p);
-            if (at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
-            while (at.tile < n_tiles && ok) {
-                const Tile t = next;
-                const int nb = blocks_of(t), chunks = chunks_of(t);
-                const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
-                for (int ch = 0; ch < chunks && ok; ++ch) {
-                    const uint32_t acc = ch == 0 ? cur : cur ^ 1u;  // (later chunks: the other one)
-                    if (!mbar_wait_warp(&s.tempty[acc], (uses >> acc & 1u) ^ 1u, wc)) {
+            for (Walk at(p); at.tile < n_tiles && ok; at.next()) {
+                const Tile t = get_tile<MODE>(s, p, at.tile);
+                const int nb = blocks_of(t);
+                for (int b = 0; b < nb; ++b) {
+                    if (!mbar_wait_warp(&s.empty[stage], phase ^ 1, wc)) {
                         ok = false;
                         break;
                     }
-                    uses ^= 1u << acc;
-                    tc_fence_after();
-                    const uint32_t d = tmem + acc * 256;
-                    const int b0 = CHUNKED ? ch * CHUNK : 0, b1 = CHUNKED ? min(nb, b0 + CHUNK) : nb;
-                    for (int b = b0; b < b1; ++b) {
-                        if (!mbar_wait_warp(&s.full[stage], phase, wc)) {
+                    if (elect_one()) {
+                        if (is_a && rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (OPER + b_bytes));
+                        const uint32_t bar = lead_full + stage * 8;
+                        uint8_t* dst = smem + stage * stage_bytes + (is_a ? 0 : OPER);
+                        if (MODE == WGRAD) {
+                            const int r = t.m0 + b * BK;
+                            if (is_a) {
+                                const int n = t.j0 + 128 * static_cast<int>(rank);
+                                tma_load_2d_pair(dst, &tm_a, n, r, bar);
+                                tma_load_2d_pair(dst + 8192, &tm_a, n + 64, r, bar);
+                            } else {
+                                // (two boxes may bring more than the share)
+                                const int k = t.k0 + t.n / 2 * static_cast<int>(rank);
+                                tma_load_2d_pair(dst, &tm_b, k, r, bar);
+                                if (second) tma_load_2d_pair(dst + 8192, &tm_b, k + 64, r, bar);
+                            }
+                        } else {
+                            const int c = b * BK;
+                            if (!is_a) {
+                                // (the box has maxu * 8 rows; the MMA reads n / 2 of them)
+                                tma_load_2d_pair(dst, &tm_b, c, t.m0 + static_cast<int>(rank) * (t.n / 2), bar);
+                            } else if (MODE == ROWS_FWD) {
+                                load_3d_pair(dst, &tm_a, c, t.j0 + 128 * static_cast<int>(rank), t.e, bar);
+                            } else {
+                                const int j = t.j0 + 128 * static_cast<int>(rank);
+                                load_3d_pair(dst, &tm_a, j, c, t.e, bar);
+                                load_3d_pair(dst + 8192, &tm_a, j + 64, c, t.e, bar);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (is_a && rank == 0) {  // let every copy land before either CTA may exit
+                const long ring = stages, from = issued > ring ? issued - ring : 0;
+                for (long j = from; j < issued; ++j)
+                    mbar_drain(&s.full[j % ring], static_cast<uint32_t>((j / ring) & 1), kWaitLimitNs / 8);
+            }
+        } else if (warp == 1) {
+            if (rank == 0) {
+                // ---------------- MMAs (leader) ----------------
+                const uint32_t major = MODE == WGRAD ? kMajorA | kMajorB : MODE == ROWS_BACK ? kMajorA : 0u;
+                constexpr uint32_t STEP_K = 32 >> 4, STEP_MN = 2048 >> 4;  // 16 contraction indices on, in descriptor units
+                constexpr uint32_t step_a = MODE == ROWS_FWD ? STEP_K : STEP_MN, step_b = MODE == WGRAD ? STEP_MN : STEP_K;
+                uint32_t stage = 0, phase = 0, tails = 0, cur = 0, uses = 0;  // uses: bit a, uses of accumulator a, mod 2
+                bool ok = true;
+                Tile next{};
+                Walk at(p);
+                if (at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
+                while (at.tile < n_tiles && ok) {
+                    const Tile t = next;
+                    const int nb = blocks_of(t), chunks = chunks_of(t);
+                    const uint32_t idesc = f16_idesc(ACT, 256, t.n) | major;
+                    for (int ch = 0; ch < chunks && ok; ++ch) {
+                        const uint32_t acc = RING || ch == 0 ? cur : cur ^ 1u;  // (later chunks: the other one)
+                        if (!mbar_wait_warp(&s.tempty[acc], (uses >> acc & 1u) ^ 1u, wc)) {
                             ok = false;
                             break;
                         }
+                        uses ^= 1u << acc;
                         tc_fence_after();
-                        const uint32_t at = smem_u32(smem + stage * stage_bytes);
-                        const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
-                        const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
-                        const int steps = MODE == WGRAD ? min(4, t.rows / 16 - 4 * b) : 4;
-                        if (elect_one()) {
+                        const uint32_t d = tmem + acc * 256;
+                        const int b0 = CHUNKED ? ch * CHUNK : 0, b1 = CHUNKED ? min(nb, b0 + CHUNK) : nb;
+                        for (int b = b0; b < b1; ++b) {
+                            if (!mbar_wait_warp(&s.full[stage], phase, wc)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t at = smem_u32(smem + stage * stage_bytes);
+                            const uint64_t ad = MODE == ROWS_FWD ? sw128_desc(at) : mn_desc(at);
+                            const uint64_t bd = MODE == WGRAD ? mn_desc(at + OPER) : sw128_desc(at + OPER);
+                            const int steps = MODE == WGRAD ? min(4, t.rows / 16 - 4 * b) : 4;
+                            if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < BK / 16; ++k)
-                                if (MODE != WGRAD || k < steps)
-                                    tc_mma_pair(d, ad + k * step_a, bd + k * step_b, idesc, b > b0 || k > 0);
-                            tc_commit_pair(&s.empty[stage], 0x3);
+                                for (int k = 0; k < BK / 16; ++k)
+                                    if (MODE != WGRAD || k < steps)
+                                        tc_mma_pair(d, ad + k * step_a, bd + k * step_b, idesc, b > b0 || k > 0);
+                                tc_commit_pair(&s.empty[stage], 0x3);
+                            }
+                            __syncwarp();
+                            if (++stage == stages) {
+                                stage = 0;
+                                phase ^= 1;
+                            }
                         }
+                        if (!ok) break;
+                        if (MODE == WGRAD && ch + 1 == chunks && t.rows % 16 != 0) {
+                            const uint32_t tb = tails % TBUFS;
+                            if (!mbar_wait_warp(&s.tready[tb], (tails / TBUFS) & 1u, wc)) {
+                                ok = false;
+                                break;
+                            }
+                            ++tails;
+                            tc_fence_after();
+                            const uint32_t at = smem_u32(smem + S::TBUF_AT + tb * TBUF);
+                            if (elect_one()) {
+                                tc_mma_pair(d, mn_desc(at, UNIT), mn_desc(at + 2 * UNIT, UNIT), idesc, b1 > b0);
+                                tc_commit_pair(&s.tfree[tb], 0x3);
+                            }
+                            __syncwarp();
+                        }
+                        if (elect_one()) tc_commit_pair(&s.tfull[acc], 0x3);
                         __syncwarp();
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                        if (RING) cur ^= 1u;
                     }
-                    if (!ok) break;
-                    if (MODE == WGRAD && ch + 1 == chunks && t.rows % 16 != 0) {
-                        const uint32_t tb = tails % TBUFS;
-                        if (!mbar_wait_warp(&s.tready[tb], (tails / TBUFS) & 1u, wc)) {
-                            ok = false;
-                            break;
-                        }
-                        ++tails;
-                        tc_fence_after();
-                        const uint32_t at = smem_u32(smem + S::TBUF_AT + tb * TBUF);
-                        if (elect_one()) {
-                            tc_mma_pair(d, mn_desc(at, UNIT), mn_desc(at + 2 * UNIT, UNIT), idesc, b1 > b0);
-                            tc_commit_pair(&s.tfree[tb], 0x3);
-                        }
-                        __syncwarp();
+                    // (found while the MMAs run: it would hold up the next tile's)
+                    at.next();
+                    if (ok && at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
+                    if (!RING && chunks == 1) cur ^= 1u;
+                }
+                if (elect_one()) tc_commit_pair(&s.mma_done, 0x1);
+                __syncwarp();
+                mbar_drain(&s.mma_done, 0, kWaitLimitNs / 8);
+            }
+        } else if (warp == 3) {
+            if (MODE == WGRAD) {
+                // ---------------- tails ----------------
+                uint32_t tails = 0;
+                for (Walk at(p); at.tile < n_tiles; at.next()) {
+                    const Tile t = get_tile<MODE>(s, p, at.tile);
+                    const int left = t.rows % 16;
+                    if (left == 0) continue;
+                    const uint32_t tb = tails % TBUFS, ph = (tails / TBUFS) & 1u;
+                    ++tails;
+                    if (!mbar_wait_warp(&s.tfree[tb], ph ^ 1u, wc)) break;
+                    uint8_t* buf = smem + S::TBUF_AT + tb * TBUF;
+                    if (elect_one()) {
+                        const int r = t.m0 + t.rows - left;
+                        const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + t.n / 2 * static_cast<int>(rank);
+                        mbar_arrive_expect_tx(&s.tloc[tb], 4 * UNIT);
+                        tma_load_2d(buf, &tm_ta, n, r, &s.tloc[tb]);
+                        tma_load_2d(buf + UNIT, &tm_ta, n + 64, r, &s.tloc[tb]);
+                        tma_load_2d(buf + 2 * UNIT, &tm_tb, k, r, &s.tloc[tb]);
+                        tma_load_2d(buf + 3 * UNIT, &tm_tb, k + 64, r, &s.tloc[tb]);
                     }
-                    if (elect_one()) tc_commit_pair(&s.tfull[acc], 0x3);
+                    __syncwarp();
+                    if (!mbar_wait_warp(&s.tloc[tb], ph, wc)) {
+                        mbar_drain(&s.tloc[tb], ph, kWaitLimitNs / 8);
+                        break;
+                    }
+                    // row r of 64 columns is the 128 bytes at 128 r (the swizzle moves bytes within them)
+                    for (int i = lane; i < (16 - left) * 32; i += 32) {
+                        const int r = left + (i >> 5), piece = i & 31;
+                        *reinterpret_cast<uint4*>(buf + (piece >> 3) * UNIT + r * 128 + (piece & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) arrive_remote(lead_tready + tb * 8);
                     __syncwarp();
                 }
-                // (found while the MMAs run: it would hold up the next tile's)
-                at.next();
-                if (ok && at.tile < n_tiles) next = get_tile<MODE>(s, p, at.tile);
-                if (chunks == 1) cur ^= 1u;
-            }
-            if (elect_one()) tc_commit_pair(&s.mma_done, 0x1);
-            __syncwarp();
-            mbar_drain(&s.mma_done, 0, kWaitLimitNs / 8);
-        }
-    } else if (warp == 7) {
-        if (MODE == WGRAD) {
-            // ---------------- tails ----------------
-            uint32_t tails = 0;
-            for (Walk at(p); at.tile < n_tiles; at.next()) {
-                const Tile t = get_tile<MODE>(s, p, at.tile);
-                const int left = t.rows % 16;
-                if (left == 0) continue;
-                const uint32_t tb = tails % TBUFS, ph = (tails / TBUFS) & 1u;
-                ++tails;
-                if (!mbar_wait_warp(&s.tfree[tb], ph ^ 1u, wc)) break;
-                uint8_t* buf = smem + S::TBUF_AT + tb * TBUF;
-                if (elect_one()) {
-                    const int r = t.m0 + t.rows - left;
-                    const int n = t.j0 + 128 * static_cast<int>(rank), k = t.k0 + t.n / 2 * static_cast<int>(rank);
-                    mbar_arrive_expect_tx(&s.tloc[tb], 4 * UNIT);
-                    tma_load_2d(buf, &tm_ta, n, r, &s.tloc[tb]);
-                    tma_load_2d(buf + UNIT, &tm_ta, n + 64, r, &s.tloc[tb]);
-                    tma_load_2d(buf + 2 * UNIT, &tm_tb, k, r, &s.tloc[tb]);
-                    tma_load_2d(buf + 3 * UNIT, &tm_tb, k + 64, r, &s.tloc[tb]);
-                }
-                __syncwarp();
-                if (!mbar_wait_warp(&s.tloc[tb], ph, wc)) {
-                    mbar_drain(&s.tloc[tb], ph, kWaitLimitNs / 8);
-                    break;
-                }
-                // row r of 64 columns is the 128 bytes at 128 r (the swizzle moves bytes within them)
-                for (int i = lane; i < (16 - left) * 32; i += 32) {
-                    const int r = left + (i >> 5), piece = i & 31;
-                    *reinterpret_cast<uint4*>(buf + (piece >> 3) * UNIT + r * 128 + (piece & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (elect_one()) arrive_remote(lead_tready + tb * 8);
-                __syncwarp();
             }
         }
     } else if (MODE == WGRAD && KIND == GADD && warp >= 8) {
         if constexpr (MODE == WGRAD && KIND == GADD) {
             // ---------------- copies of addends and gradients, for the epilogue warp of the same quarter ----------------
-            const int q = warp & 3, w = (q + 2) & 3;  // (warps 2 to 5 have quarters 2, 3, 0, 1)
-            copy_slots(s, p, &tm_out, &tm_add, smem + S::STG_AT + w * S::STG_WARP, w,
+            const int q = warp & 3;
+            copy_slots(s, p, &tm_out, &tm_add, smem + S::STG_AT + q * S::STG_WARP, q,
                        128 * static_cast<int>(rank) + 32 * q, n_tiles, lane, wc);
         }
     } else {
         // ---------------- epilogue ----------------
+        if constexpr (RING) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::REGS_SUMS));
         const int q = warp & 3;  // TMEM lane quarter
-        const int half = warp >= 8, ew = half ? warp - 4 : warp - 2;  // which of its two warps, and of all
+        const int half = warp >= 8, ew = warp - 4;  // which of its two warps, and of all
         const int n_off = 128 * static_cast<int>(rank) + 32 * q;
         uint8_t* stg = smem + S::STG_AT + ew * S::STG_WARP;
         [[maybe_unused]] uint32_t used = 0;
@@ -889,37 +1001,69 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             else arrive_remote(lead_tempty + acc * 8);
         };
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        for (Walk at(p); at.tile < n_tiles; at.next()) {
-            const Tile t = get_tile<MODE>(s, p, at.tile);
-            const int chunks = chunks_of(t);
-            if constexpr (KIND == FULL) prefetch_residual(p, lane, t.m0, t.rows, t.j0 + n_off);
-            if (!wait_full(cur)) break;
-            const uint32_t ta = lanes + cur * 256, tb = lanes + (cur ^ 1u) * 256;
-            bool ok = true;
-            if constexpr (CHUNKED) {
-                for (int ch = 1; ch < chunks && ok; ++ch) {
-                    ok = wait_full(cur ^ 1u);
-                    if (ok && ch + 1 < chunks) {
-                        fold<Slots<KIND>::COLS, S::HALVES>(ta, tb, half);
-                        tc_fence_before();
-                        __syncwarp();
-                        release(cur ^ 1u);
+        if constexpr (RING) {
+            for (Walk at(p); at.tile < n_tiles; at.next()) {
+                const Tile t = get_tile<MODE>(s, p, at.tile);
+                const int chunks = chunks_of(t), cols = tile_cols(p, t);
+                if constexpr (KIND == G32ADD) prefetch_addend(p, t, n_off + lane, 32 * half, cols);
+                RowSums v;
+                v.clear();
+                auto next = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    release(cur);
+                    cur ^= 1u;
+                };
+                // (without addends the last chunk is added step by step beside the stores: 8192 rows of 8 groups, 4096 x
+                // 3584, 170 us and 174; with them that would hold its accumulator too long, 284 us and 222)
+                const int early = KIND == G32ADD ? chunks : chunks - 1;
+                bool ok = true;
+                for (int ch = 0; ch < early; ++ch) {
+                    ok = wait_full(cur);
+                    if (!ok) break;
+                    if (t.rows > 0)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v.add(i, lanes + cur * 256 + 32 * half + 64 * i);  // (past the tile's too)
+                    next();
+                }
+                if (KIND == G32) ok = ok && wait_full(cur);
+                if (!ok) break;
+                store_sums<KIND>(p, &tm_out, stg, v, lanes + cur * 256 + 32 * half, t, n_off, half, cols, lane);
+                if (KIND == G32) next();
+            }
+        } else {
+            for (Walk at(p); at.tile < n_tiles; at.next()) {
+                const Tile t = get_tile<MODE>(s, p, at.tile);
+                const int chunks = chunks_of(t);
+                if constexpr (KIND == FULL) prefetch_residual(p, lane, t.m0, t.rows, t.j0 + n_off);
+                if (!wait_full(cur)) break;
+                const uint32_t ta = lanes + cur * 256, tb = lanes + (cur ^ 1u) * 256;
+                bool ok = true;
+                if constexpr (CHUNKED) {
+                    for (int ch = 1; ch < chunks && ok; ++ch) {
+                        ok = wait_full(cur ^ 1u);
+                        if (ok && ch + 1 < chunks) {
+                            fold<Slots<KIND>::COLS, S::HALVES>(ta, tb, half);
+                            tc_fence_before();
+                            __syncwarp();
+                            release(cur ^ 1u);
+                        }
                     }
                 }
+                if (!ok) break;
+                if constexpr (MODE == WGRAD) {
+                    if (!wgrad_epilogue<ACT, KIND>(s, p, &tm_out, stg, used, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
+                                                   ew, n_off, half, lane, wc))
+                        break;
+                } else {
+                    rows_epilogue<ACT, KIND>(p, ta, smem_u32(stg), t, t.j0 + n_off, half, lane);
+                }
+                tc_fence_before();
+                __syncwarp();
+                release(cur);
+                if (chunks > 1) release(cur ^ 1u);
+                else cur ^= 1u;
             }
-            if (!ok) break;
-            if constexpr (MODE == WGRAD) {
-                if (!wgrad_epilogue<ACT, KIND>(s, p, &tm_out, stg, used, ta, tb, t.rows == 0 ? 0 : chunks > 1 ? 2 : 1, t,
-                                               ew, n_off, half, lane, wc))
-                    break;
-            } else {
-                rows_epilogue<ACT, KIND>(p, ta, smem_u32(stg), t, t.j0 + n_off, half, lane);
-            }
-            tc_fence_before();
-            __syncwarp();
-            release(cur);
-            if (chunks > 1) release(cur ^ 1u);
-            else cur ^= 1u;
         }
         if (MODE == WGRAD && KIND != GADD && lane == 0) store_wait();
     }
@@ -966,6 +1110,12 @@ int launch(const Maps& m, const RaggedParams& p, int64_t tiles, cudaStream_t st,
     if (max_pairs == 0) {
         const int rc = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
         if (rc != MOE_OK) return rc;
+        if (MODE == WGRAD && in_registers(KIND)) {  // (a larger share than the launch's would be waited for without end)
+            cudaFuncAttributes fa;
+            const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+            if (e != cudaSuccess || fa.numRegs < Shape<MODE, KIND>::REGS_LAUNCH)
+                return fail(MOE_ERR_CUDA, "%s: the kernel was built with too few registers", who);
+        }
         const int sms = sm_count();
         cfg.gridDim = dim3(sms > 1 ? sms / 2 * 2 : 2);
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&max_pairs, kernel, &cfg);

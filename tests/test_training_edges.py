@@ -165,19 +165,78 @@ def test_weight_gradient_in_16_bits_of_very_many_rows(moe, dev, act, rows, chunk
             assert abs(mean) <= lost + 6 * plain.U[act] / math.sqrt(3 * N * K)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("addend", [None, "apart", "in place"])
+@pytest.mark.parametrize("rows,N,K,counts", [
+    (600, 264, 136, None), (5000, 264, 520, None), (4200, 136, 72, None), (30000, 520, 264, None),
+    (200000, 136, 264, None), (4100, 1032, 1000, None), (9000, 2816, 2048, None),
+    (641, 72, 136, "one"), (5000, 520, 264, "one"), (12000, 512, 520, "few"), (40000, 264, 1032, "few"),
+    (9000, 136, 72, "many"), (70000, 520, 1416, "many")])
+def test_f32_gradients_are_as_good_as_sums_in_f32(moe, dev, act, addend, rows, N, K, counts):
+    """Rows of random signs, as gradients are: off by 1e-6 of their 2-norm at most however many rows, which is what a
+    plain f32 product of 4096 rows has. (640 rows in one accumulator, 40 steps of 16: measured 8.0e-7 in f16 and 6.0e-7 in
+    bf16. The chunks are added in f32.)"""
+    g = torch.Generator(device=dev).manual_seed(rows + N)
+    dt = plain.DT[act]
+    dy, x = (torch.randn((rows, n), generator=g, device=dev).to(dt) for n in (N, K))
+    split = {None: None, "one": [0, rows], "few": [5, 5, rows // 3, rows // 3 + 511, rows - 2],
+             "many": list(range(0, rows + 1, rows // 40))[:41]}[counts]
+    off = torch.tensor(split, dtype=torch.int32, device=dev) if split else None
+    bounds = split or [0, rows]
+    E = len(bounds) - 1
+    add = torch.randn((E, N, K), generator=g, device=dev) if addend else None
+    outs = []
+    for _ in range(2):
+        dw = add.clone() if addend == "in place" else torch.full((E, N, K), 7.0, device=dev)
+        moe.moe_ragged_wgrad(dy, x, moe.ACT_CODES[act], off, rows, N, K, E, dw if addend == "in place" else add, dw, True)
+        outs.append(dw)
+    assert torch.equal(*outs)
+    for e in range(E):
+        at = slice(bounds[e], bounds[e + 1])
+        ref = torch.zeros((N, K), dtype=torch.float64, device=dev)
+        for lo in range(bounds[e], bounds[e + 1], 1 << 17):
+            hi = min(lo + (1 << 17), bounds[e + 1])
+            ref += dy[lo:hi].double().T @ x[lo:hi].double()
+        size = float(ref.norm())
+        if addend:
+            ref += add[e].double()
+        assert float((outs[0][e].double() - ref).norm()) <= 1e-6 * size + F32 * float(ref.norm()), (e, at)
+        if bounds[e] == bounds[e + 1]:
+            assert torch.equal(outs[0][e].double(), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,N,K,one", [(3000, 264, 520, False), (3000, 264, 520, True), (100000, 136, 72, False),
+                                          (40000, 520, 264, True)])
+def test_f32_gradients_of_one_sign(moe, dev, act, rows, N, K, one):
+    """640 rows in one accumulator come out 640 2^-27 = 4.8e-6 short at most; the chunks are added in f32."""
+    g = torch.Generator(device=dev).manual_seed(N)
+    dy, x = (torch.empty((rows, n), dtype=plain.DT[act], device=dev).uniform_(0.05, 0.15, generator=g) for n in (N, K))
+    off = torch.tensor([0, rows], dtype=torch.int32, device=dev) if one else None
+    dw = torch.empty((N, K), device=dev)
+    moe.moe_ragged_wgrad(dy, x, moe.ACT_CODES[act], off, rows, N, K, 1, None, dw, True)
+    ref = dy.double().T @ x.double()
+    assert torch.all((dw.double() - ref).abs() <= ref * (640 * 2.0 ** -27 + (rows / 640 + 8) * F32))
+
+
 # ---- waits that run out -----------------------------------------------------------------------------
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("limit_ns", [1, 300])
-@pytest.mark.parametrize("call", ["dense", "groups", "transposed", "gradient"])
+@pytest.mark.parametrize("call", ["dense", "groups", "transposed", "gradient", "gradient in chunks"])
 def test_split_form_reports_a_wait_that_runs_out(moe, dev, call, limit_ns):
     """Contractions so long that the wait for a tile's last product (45 us and more) outlasts any first look at its
     barrier, with a limit far below: the call ends, the status is there, and the next call is the clean one."""
     g = torch.Generator(device=dev).manual_seed(1)
     err = torch.zeros(1, dtype=torch.int32, device=dev)
 
+    chunks = call == "gradient in chunks"  # f16: of 16384 rows each, 60 us (those of an f32 gradient are too short)
+    dtype = torch.float16 if chunks else torch.bfloat16
+
     def randn16(*shape):
-        return torch.randn(shape, generator=g, device=dev).bfloat16()
+        return torch.randn(shape, generator=g, device=dev).to(dtype)
 
     if call == "dense":
         M, N, K = 40, 264, 131072
@@ -186,12 +245,12 @@ def test_split_form_reports_a_wait_that_runs_out(moe, dev, call, limit_ns):
         def run(out):
             moe.moe_dense_gemm(a, 0, w, None, 0, None, None, out, M, N, K, err)
         shape = M, N
-    elif call == "gradient":
-        rows, N, K = 100000, 264, 136
+    elif call.startswith("gradient"):
+        rows, N, K = 300000 if chunks else 100000, 264, 136
         a, w = randn16(rows, N), randn16(rows, K)
 
         def run(out):
-            moe.moe_ragged_wgrad(a, w, 0, None, rows, N, K, 1, None, out, False, err)
+            moe.moe_ragged_wgrad(a, w, 1 if chunks else 0, None, rows, N, K, 1, None, out, False, err)
         shape = N, K
     else:
         tr, counts = call == "transposed", [30, 0, 41, 29]
@@ -201,7 +260,7 @@ def test_split_form_reports_a_wait_that_runs_out(moe, dev, call, limit_ns):
         def run(out):
             moe.moe_ragged_gemm(a, 0, w, tr, off, 100, N, K, 4, out, err)
         shape = 100, K if tr else N
-    want, out = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    want, out = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
     run(want)
     assert err.item() == 0
     old = moe.moe_set_wait_limit_ns(limit_ns)
