@@ -109,18 +109,21 @@ __device__ __forceinline__ uint8_t* align1024_shared(uint8_t* base) {
 
 // Programmatic dependent launch, device side. pdl_wait: block until the
 // kernels this grid depends on have completed and their memory is visible
-// (a no-op for a grid launched without the attribute). Called first in every
-// kernel but one, by every thread, before any global memory is touched, so a
-// kernel also completes only after its predecessor did. The exception is the
+// (a no-op for a grid launched without the attribute). Called in every kernel
+// but one by every thread before any global memory is touched (first, or after
+// barriers and tensor memory are set up), so a kernel also completes only
+// after its predecessor did. The exception is the
 // few-token layer's down kernel: before its wait it reads the weights and the
 // routing (logits, or ids given as inputs), which it may because the gate/up
 // kernel before it lets it start only after its own wait, when everything
 // before the layer is complete. pdl_launch_next: allow the next kernel in the
 // stream to be scheduled now rather than when this one's CTAs have exited.
-// Called by that gate/up kernel (after its pdl_wait) and by the activation
-// gather (the GEMM after it then sets up while the gather runs); triggering
-// early in every kernel measured slower on decode-sized layers (fine-grained
-// T=8 72.7 -> 77 us).
+// Called, always after pdl_wait, by that gate/up kernel, by the activation
+// gather (the GEMM after it then sets up while the gather runs) and by the
+// ragged and split products (ragged_tc.cuh, ragged_split.cuh), whatever kernel
+// comes next: what a kernel reads before its own wait may therefore still be
+// written by the one before it. Triggering early in every kernel measured
+// slower on decode-sized layers (fine-grained T=8 72.7 -> 77 us).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_rows_kernel(const DenseRows
             const int r = i & 31, m = i >> 5, n = first + r, h = r >> 4;
             if (n >= n1) continue;
             // row r & 15, column m & 7 of token tile m / 8: lane 4 (r & 7) + (m & 7) / 2, element 2 (r / 8 & 1) + (m & 1)
-            const float* src = red + ((h * NT + (m >> 3)) * 32 + 4 * (r & 7) + ((m & 7) >> 1)) * 4 + 2 * ((r >> 3) & 1) + (m & 1);
+            const int at_lane = 4 * (r & 7) + ((m & 7) >> 1), elem = 2 * ((r >> 3) & 1) + (m & 1);
+            const float* src = red + ((h * NT + (m >> 3)) * 32 + at_lane) * 4 + elem;
             float z = 0.0f;
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) z += src[q * 2 * NT * 128];

@@ -82,9 +82,10 @@ int set_smem_limit(const void* kernel, int bytes) {
     return MOE_OK;
 }
 
-// How far a load of 128 bytes of a row reaches in L2: 256 bytes, which streams from HBM best (64 rows over 128 groups of
-// 1160 x 2056: 49.5 us, 50.8 with 128); 128 for tensors that many CTAs read from L2 where their rows begin between
-// sectors of 32 bytes (3117 x 2048 x 13960: 172 us with 256, 150 with 128; with rows of a multiple of 32 bytes 1% the other way).
+// How far a load of 128 bytes of a row reaches in L2: 256 bytes, which streams from HBM best
+// (64 rows over 128 groups of 1160 x 2056: 49.5 us, 50.8 with 128); 128 for tensors that many
+// CTAs read from L2 where their rows begin between sectors of 32 bytes (3117 x 2048 x 13960:
+// 172 us with 256, 150 with 128; with rows of a multiple of 32 bytes 1% the other way).
 static CUtensorMapL2promotion l2_promotion(uint64_t pitch, bool reused) {
     return reused && pitch % 32 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
 }

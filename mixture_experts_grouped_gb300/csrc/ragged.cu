@@ -16,9 +16,14 @@ namespace {
 // of 4 groups, 12320 x 840 transposed: pairs 45 us, split 21; 100 rows of 16 groups, 512 x 512: 7.1 and 5.7).
 //
 // One group (a dense product): the form, row tiles and split that a model of their time
-// finds best. Its costs (ns) are fitted to 110 sizes from 1 x 88 x 88 to 4000 x 2048 x 14336
-// measured at every form; the choice is 1.1% slower than the best form in the mean, 15% at
-// worst.
+// finds best. Its costs (ns) were fitted to 110 sizes from 1 x 88 x 88 to 4000 x 2048 x 14336
+// at an earlier state of the kernels, whose epilogues have become faster since, and it knows
+// nothing of bias, function, residual and z. Against the best of all forms, on 70 random sizes
+// that the fit did not see: half of the choices lose 0.1% or less, the mean 6%. It loses most
+// at streaming's rows with contractions below 600, for whose tile ends it has no term (14
+// sizes: 13% in the mean; 17 x 27104 x 120 12.0 us, split 6.5; 32 x 28672 x 64 15.0 and 4.3), with
+// full epilogues (6 sizes: 17%, 37% at worst), and at single sizes (2676 x 1712 x 13448: pairs of
+// 16 units 182 us, of 10 130); transposed products lose 1%.
 //   streaming (up to 32 rows): the weights at 5.7 TB/s, or a warp's blocks one after the
 //     other, and 27 ps a byte of the rows, which every CTA reads
 //   split: a launch (and its clusters' meetings), a CTA's blocks, slower where two share an
@@ -87,16 +92,20 @@ RowsPick pick_rows_form(const RaggedParams& p, bool transposed, int sms) {
 
 // Which form the gradient of a weight takes.
 //
-// CTA pairs (parts 0): kt tiles of nearly equal width side by side, of 256 columns at most, and more of them where they
-// fill the waves of tiles better (12288 rows of 64 groups, 2048 x 1408 f32 with addends: five of 256 columns and one of
-// 128 278 us, six alike 254, eight 237; 1333 rows, 2816 x 2048 f32: eight side by side, 88 tiles for 76 pairs, 21.4, thirteen
-// 19.1). A tile takes its blocks of 64 rows, 140 + 0.73 ns a column each, and 0.7 us between tiles (2532 rows of 6 groups, 18736 x 944
-// f32: four side by side 110 us, five 122, six 130), or the way of its bytes, 82 a ns, and if they are 16-bit 0.8 us to pack them. Over many waves a pair's tiles have the average width.
+// CTA pairs (parts 0): kt tiles of nearly equal width side by side, of 256 columns at most, and
+// more of them where they fill the waves of tiles better (12288 rows of 64 groups, 2048 x 1408
+// f32 with addends: five of 256 columns and one of 128 278 us, six alike 254, eight 237; 1333
+// rows, 2816 x 2048 f32: eight side by side, 88 tiles for 76 pairs, 21.4, thirteen 19.1, both
+// before the sums' chunks). A tile takes its blocks of 64 rows, 140 + 0.73 ns a column each,
+// and 0.7 us between tiles (2532 rows of 6 groups, 18736 x 944 f32: four side by side 110 us,
+// five 122, six 130), or the way of its bytes, 82 a ns, and if they are 16-bit 0.8 us to pack
+// them. Over many waves a pair's tiles have the average width.
 //
-// Of one group with few tiles, the split form: parts CTAs share a tile's rows; its time as above, more where two of them
-// share an SM, and for addends, which its lanes read 64 bytes at a time. (us, pairs / split, f32: 4000 rows, 512 x 512 18.2 /
-// 10.7; 2000 rows, 2048 x 512 12.3 / 11.6; 100 rows, 1000 x 1000 6.1 / 5.6, with addends 7.5 / 10.3; 30000 rows, 264 x 520
-// 168 / 32; 640 rows, 2048 x 1408 9.0 / 14.0.)
+// Of one group with few tiles, the split form: parts CTAs share a tile's rows; its time as
+// above, more where two of them share an SM, and for addends, which its lanes read 64 bytes at
+// a time. (us, pairs / split, f32: 4000 rows, 512 x 512 20.4 / 12.0; 2000 rows, 2048 x 512 13.5 /
+// 12.7; 100 rows, 1000 x 1000 6.2 / 5.5; 30000 rows, 264 x 520 151 / 33; with the forms' models
+// the other way, 640 rows, 2048 x 1408 9.4 / 14.0, 100 rows, 1000 x 1000 with addends 7.8 / 10.3.)
 struct GradientForm {
     int parts, kt;
 };

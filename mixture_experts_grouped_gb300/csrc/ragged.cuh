@@ -54,10 +54,11 @@ struct RaggedArgs {
 // Columns that the width of a gradient's tile is a multiple of: a store's 128 bytes.
 constexpr int gradient_unit(bool f32) { return f32 ? 32 : 64; }
 
-// Most blocks of 64 rows that one accumulator of a gradient sums, since a tensor core's sums of n rows may come out n 2^-27
-// short (ragged_tc.cuh). For f32 640 rows: of random signs 8e-7 of their 2-norm in f16 and 6e-7 in bf16, as good as a plain
-// f32 product; 4096 rows 5e-6. For 16 bits as many as lose a quarter of the output's half step (2^-13 of 2^-11 in f16, 2^-10 of
-// 2^-8 in bf16); without that, 1.2 million rows of one sign came out 0.8% short.
+// Most blocks of 64 rows that one accumulator of a gradient sums, since a tensor core's sums
+// of n rows may come out n 2^-27 short (ragged_tc.cuh). For f32 640 rows: of random signs they
+// are off by 8e-7 of their 2-norm in f16 and 6e-7 in bf16, as good as a plain f32 product; 4096
+// rows by 5e-6. For 16 bits as many as lose a quarter of the output's half step (2^-13 of 2^-11
+// in f16, 2^-10 of 2^-8 in bf16); without that, 1.2 million rows of one sign came out 0.8% short.
 constexpr int gradient_chunk(bool f32, int act) { return f32 ? 10 : act == MOE_ACT_F16 ? 256 : 2048; }
 
 // How a product of rows runs: on CTA pairs, row tiles of up to maxu units of 16 rows; or, with

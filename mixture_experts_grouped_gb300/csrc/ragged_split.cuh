@@ -486,6 +486,14 @@ template <int MODE, int ACT> int launch_split(const RaggedArgs& g, int mt, int p
     return launch_split_kind<MODE, ACT, PLAIN>(g, tiles, mt, parts);
 }
 
+// A product of rows in the form that was chosen for it.
+template <int ACT> int launch_rows_act(const RaggedArgs& g, const RowsForm& f) {
+    if (f.parts)
+        return g.transposed ? launch_split<ROWS_BACK, ACT>(g, f.tiles, f.parts)
+                            : launch_split<ROWS_FWD, ACT>(g, f.tiles, f.parts);
+    return g.transposed ? launch_rows_form<ROWS_BACK, ACT>(g, f.maxu) : launch_rows_form<ROWS_FWD, ACT>(g, f.maxu);
+}
+
 }  // namespace
 }  // namespace ragged
 }  // namespace moe

@@ -30,11 +30,11 @@
 // copies: by a lane that a branch on the lane number singled out, each took longer (4096 x
 // 14336 x 4096: 271 us, 245 elected). Every wait is bounded.
 //
-// Measured: 8192 rows of 8 groups, 28672 x 4096 1014 us, 1.9 PFLOP/s (1203 under the power cap of
-// long runs); its transposed form the same; 64 rows of 50 touched groups, 1536 x 2048 55 us, 5.7
-// TB/s. Gradients: 8192 rows of 8 groups, 4096 x 14336 bf16 545 us, 1.76 PFLOP/s; 12288 rows of 64
-// groups, 2048 x 1408 f32 with addends 239 us, 6.5 TB/s; 32768 rows of 128 groups, 1536 x 2048 bf16
-// 184 us, 5.6 TB/s.
+// Measured: 8192 rows of 8 groups, 28672 x 4096 1014 to 1066 us, 1.8 to 1.9 PFLOP/s (1166 to 1224
+// under the power cap of long runs); its transposed form the same; 64 rows of 50 touched
+// groups, 1536 x 2048 55 us, 5.7 TB/s. Gradients: 8192 rows of 8 groups, 4096 x 14336 bf16 545 us,
+// 1.76 PFLOP/s; 12288 rows of 64 groups, 2048 x 1408 f32 with addends 234 us, 6.6 TB/s; 32768 rows
+// of 128 groups, 1536 x 2048 bf16 184 us, 5.6 TB/s.
 #pragma once
 
 #include <numeric>
@@ -663,9 +663,10 @@ __device__ __forceinline__ void prefetch_addend(const RaggedParams& p, const Til
     const float* at = p.addend + (static_cast<size_t>(t.e) * p.J + t.j0 + row) * p.C + t.k0;
     for (int c = first; c < cols; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
 }
-// A warp's sums, and its addends, through its slot to dw (which may hold the addends). The addends are read 128 bytes of a
-// row to eight lanes, a step ahead, and meet the sums in the slot: read by the lane that adds them, they took the L1 1.1 us a
-// step of the CTA's warps (16384 rows of 8 groups, 4096 x 3584: 395 us).
+// A warp's sums, and its addends, through its slot to dw (which may hold the addends). The
+// addends are read 128 bytes of a row to eight lanes, a step ahead, and meet the sums in the
+// slot: read by the lane that adds them, they took the L1 1.1 us a step of the CTA's warps
+// (16384 rows of 8 groups, 4096 x 3584: 395 us, so 346).
 struct Addend {
     float4 f[8];  // of rows 4 q + lane / 8
     __device__ __forceinline__ void load(const float* at, int C, int rows, int cols, int lane) {
@@ -682,8 +683,8 @@ __device__ __forceinline__ void store_sums(const RaggedParams& p, const CUtensor
                                            uint32_t ta, const Tile& t, int n_off, int half, int cols, int lane) {
     const int n = t.j0 + n_off;
     const float* from = p.addend + (static_cast<size_t>(t.e) * p.J + n) * p.C + t.k0;
-    // (G32ADD always has them. Where the compiler knows, it issues the next step's loads too late: 8192 rows of 8 groups, 4096 x
-    // 3584, 231 us and 222)
+    // (G32ADD always has them. Where the compiler knows, it issues the next step's loads too
+    // late: 8192 rows of 8 groups, 4096 x 3584, 231 us and 222)
     const bool add = KIND == G32ADD && p.addend;
     Addend a;
     if (add) a.load(from + 32 * half, p.C, p.J - n, cols - 32 * half, lane);
@@ -791,7 +792,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t lead_tempty = mapa_shared(smem_u32(&s.tempty[0]), 0);
     const uint32_t lead_tready = mapa_shared(smem_u32(&s.tready[0]), 0);
     const int KB = (p.C + BK - 1) / BK;
-    const bool second = MODE == WGRAD && (p.kleast + (p.kmore > 0)) * p.kunit > 128;  // whether this CTA's share of the N operand is two boxes of 64 columns
+    // whether this CTA's share of the N operand is two boxes of 64 columns
+    const bool second = MODE == WGRAD && (p.kleast + (p.kmore > 0)) * p.kunit > 128;
     const uint32_t b_bytes = MODE == WGRAD ? (second ? OPER : OPER / 2) : p.maxu * 8 * 128;  // its bytes
     const uint32_t stage_bytes = OPER + b_bytes, stages = n_stages<MODE, KIND>(stage_bytes);
     // blocks of a tile; of a gradient, those that its whole units of 16 rows fill
@@ -1014,8 +1016,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     release(cur);
                     cur ^= 1u;
                 };
-                // (without addends the last chunk is added step by step beside the stores: 8192 rows of 8 groups, 4096 x
-                // 3584, 170 us and 174; with them that would hold its accumulator too long, 284 us and 222)
+                // (without addends the last chunk is added step by step beside the stores: 8192
+                // rows of 8 groups, 4096 x 3584, 170 us and 174; with them that would hold its
+                // accumulator too long, 284 us and 222)
                 const int early = KIND == G32ADD ? chunks : chunks - 1;
                 bool ok = true;
                 for (int ch = 0; ch < early; ++ch) {
@@ -1023,7 +1026,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     if (!ok) break;
                     if (t.rows > 0)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v.add(i, lanes + cur * 256 + 32 * half + 64 * i);  // (past the tile's too)
+                        for (int i = 0; i < 4; ++i)  // (past the tile's columns too)
+                            v.add(i, lanes + cur * 256 + 32 * half + 64 * i);
                     next();
                 }
                 if (KIND == G32) ok = ok && wait_full(cur);
@@ -1142,13 +1146,15 @@ template <int MODE, int ACT> int launch_rows_form(const RaggedArgs& g, int maxu)
     p.maxu = maxu;
     p.units.set(maxu);
     Maps m;
-    const bool reused = p.maxu >= 8;  // tall tiles are bound by what comes from L2, low ones by the weights' way from HBM
+    // tall tiles are bound by what comes from L2, low ones by the weights' way from HBM
+    const bool reused = p.maxu >= 8;
     int rc = make_tmap_3d(&m.a, const_cast<void*>(g.w), g.act, g.K, g.N, p.E, 64, MODE == ROWS_FWD ? 128 : 64, reused);
     if (rc == MOE_OK) rc = make_tmap_2d(&m.b, g.a, p.rows, p.C, p.maxu * 8, g.act, reused);
     if (rc != MOE_OK) return rc;
     m.ta = m.tb = m.out = m.add = m.b;
     // row tiles at most: one more per group than the rows fill
-    const int64_t tiles = (static_cast<int64_t>((p.rows + 16 * p.maxu - 1) / (16 * p.maxu)) + (p.E > 1 ? p.E : 0)) * ((p.J + 255) / 256);
+    const int64_t row_tiles = (p.rows + 16 * p.maxu - 1) / (16 * p.maxu) + (p.E > 1 ? p.E : 0);
+    const int64_t tiles = row_tiles * ((p.J + 255) / 256);
     if (MODE == ROWS_FWD && (p.bias || p.residual || p.pre || p.fn != MOE_FN_NONE))
         return launch<ROWS_FWD, ACT, FULL>(m, p, tiles, g.st, g.who);
     return launch<MODE, ACT, PLAIN>(m, p, tiles, g.st, g.who);

@@ -49,10 +49,11 @@ template <int ACT> int by_kind(const RaggedArgs& g) {
     if (!g.f32)
         return g.p.rows > 64 * gradient_chunk(false, ACT) ? gradient_form<ACT, G16LONG>(g) : gradient_form<ACT, G16>(g);
     if (!g.p.addend) return gradient_form<ACT, G32>(g);
-    // Addends by TMA, by warps of their own, where groups are short and the gradient is bound by its bytes: 12288 rows of 64
-    // groups, 2048 x 1408, 234 us (282 by the adding warps' loads); 512 rows of one, 4096 x 4096, 32 (36). Above, where a group
-    // has several chunks, which that form adds in tensor memory at a pair's standstill, by loads: 700 rows of one 38 (43),
-    // 8192 of 8, 4096 x 3584, 222 (277).
+    // Addends come by TMA, through warps of their own, where groups are short and the gradient is
+    // bound by its bytes: 12288 rows of 64 groups, 2048 x 1408, 234 us (282 by the adding warps'
+    // loads); 512 rows of one, 4096 x 4096, 32 (36). Above, where a group has several chunks, which
+    // that form adds in tensor memory while the pair's MMAs stand still, by loads: 700 rows of one 38
+    // (43), 8192 of 8, 4096 x 3584, 222 (277).
     return g.p.rows <= 576 * static_cast<int64_t>(g.p.E) ? gradient_form<ACT, GADD>(g) : gradient_form<ACT, G32ADD>(g);
 }
 

@@ -68,7 +68,9 @@ swiglu_backward_kernel(const uint4* gu, const uint4* dh, uint4* dgu, uint4* h, I
 // the cluster in rank order (distributed shared memory), so no workspace is needed and
 // the order depends on the sizes alone. TX = 32 where that fills the GPU, since HBM is kinder
 // to 512 bytes of a row than to 128 (4096 x 14336, relu: 59 us, 69 with TX = 8), else 8 (1333 x
-// 2816: relu 7.6 us, gelu 10, of 3.4 for the bytes). gelu's arithmetic bounds it (83 us).
+// 2816: relu 7.6 us, gelu 10, of 3.4 for the bytes). gelu takes 29 instructions an element where
+// relu takes 13 (4096 x 14336: 83 us, issue slots 67% busy, and 41): with some 21 warps an SM
+// its arithmetic and its loads overlap in part only.
 constexpr int kBiasThreads = 256;
 
 template <int ACT, int FN, int TX>
@@ -86,7 +88,8 @@ bias_act_backward_kernel(const uint16_t* d_out, const uint16_t* pre, int M, int 
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
     if (n < N) {
-        constexpr int BATCH = 4;  // rows whose loads are in flight together (d_pre may be d_out or pre: the compiler would not)
+        // rows whose loads are in flight together (d_pre may be d_out or pre: the compiler would not)
+        constexpr int BATCH = 4;
         const int stride = C * kBiasRows;
         for (int m0 = rank * kBiasRows + ty; m0 < M; m0 += BATCH * stride) {
             uint4 dv[BATCH], zv[BATCH];
@@ -414,7 +417,9 @@ extern "C" int moe_bias_act_backward(const void* d_out, const void* pre, int32_t
         constexpr int A = decltype(a)::value;
         auto run = [&](auto f) {
             constexpr int F = decltype(f)::value;
-            return cudaLaunchKernelEx(&cfg, wide ? moe::bias_act_backward_kernel<A, F, 32> : moe::bias_act_backward_kernel<A, F, 8>,
+            return cudaLaunchKernelEx(&cfg,
+                                      wide ? moe::bias_act_backward_kernel<A, F, 32>
+                                           : moe::bias_act_backward_kernel<A, F, 8>,
                                       static_cast<const uint16_t*>(d_out), static_cast<const uint16_t*>(pre), M, N,
                                       static_cast<uint16_t*>(d_pre), d_bias, accumulate, C);
         };
