@@ -172,7 +172,7 @@ def test_weight_gradient_in_16_bits_of_very_many_rows(moe, dev, act, rows, chunk
     (600, 264, 136, None), (5000, 264, 520, None), (4200, 136, 72, None), (30000, 520, 264, None),
     (200000, 136, 264, None), (4100, 1032, 1000, None), (9000, 2816, 2048, None),
     (641, 72, 136, "one"), (5000, 520, 264, "one"), (12000, 512, 520, "few"), (40000, 264, 1032, "few"),
-    (9000, 136, 72, "many"), (70000, 520, 1416, "many")])
+    (9000, 136, 72, "many"), (70000, 520, 1416, "many"), (4100, 264, 520, "uneven"), (9000, 72, 1032, "uneven")])
 def test_f32_gradients_are_as_good_as_sums_in_f32(moe, dev, act, addend, rows, N, K, counts):
     """Rows of random signs, as gradients are: off by 1e-6 of their 2-norm at most however many rows, which is what a
     plain f32 product of 4096 rows has. (640 rows in one accumulator, 40 steps of 16: measured 8.0e-7 in f16 and 6.0e-7 in
@@ -181,7 +181,8 @@ def test_f32_gradients_are_as_good_as_sums_in_f32(moe, dev, act, addend, rows, N
     dt = plain.DT[act]
     dy, x = (torch.randn((rows, n), generator=g, device=dev).to(dt) for n in (N, K))
     split = {None: None, "one": [0, rows], "few": [5, 5, rows // 3, rows // 3 + 511, rows - 2],
-             "many": list(range(0, rows + 1, rows // 40))[:41]}[counts]
+             "many": list(range(0, rows + 1, rows // 40))[:41],
+             "uneven": [0, rows - 90] + list(range(rows - 89, rows - 69)) + [rows]}[counts]  # one long group, many short
     off = torch.tensor(split, dtype=torch.int32, device=dev) if split else None
     bounds = split or [0, rows]
     E = len(bounds) - 1
