@@ -79,9 +79,10 @@ struct Tail {
 // warps finish a tile, two to a quarter of the TMEM lanes, which take its steps in turn. A
 // gradient with an addend is bound by their bytes: four warps with four slots each, so that
 // three steps' addends are on their way, four others that load and store for them, and
-// four stages. Other gradients have a slot a warp and five stages (8192 rows, 8 groups, 4096 x 14336: 557 us, 631 with four). The rows form
-// has six stages of full height, more of lower ones: a group's few rows leave a tile to its
-// weights' latency, and an SM streams them as fast as it has copies in flight.
+// four stages. Other gradients have a slot a warp and five stages (8192 rows, 8 groups, 4096 x
+// 14336: 557 us, 631 with four). The rows form has six stages of full height, more of lower
+// ones: a group's few rows leave a tile to its weights' latency, and an SM streams them as
+// fast as it has copies in flight.
 template <int MODE, int KIND> struct Shape {
     static constexpr int HALVES = KIND == GADD ? 1 : 2;  // warps to a quarter
     static constexpr int WARPS = 4 * HALVES;
@@ -456,11 +457,12 @@ __device__ __forceinline__ void rows_epilogue(const RaggedParams& p, uint32_t ta
 // A tensor core's f32 sums are cut, not rounded, at each step of 16 products: of n products
 // of one sign, a sum comes out up to n 2^-27 short (measured, as a part of it: 4096 rows
 // 2.6e-5, 30000 1.9e-4), and of n products of random signs n 1.2e-9. A gradient therefore
-// takes its rows in chunks (gradient_chunk) and adds the chunks in f32. G32: the chunks take
-// the accumulators in turn, and the epilogue adds them up in registers, 128 a lane, beside the
-// next chunk's MMAs. GADD, whose
-// groups are short, and G16LONG: the first chunk stays in its accumulator, the others come into the
-// second one and are added to it, the last one on its way out.
+// takes its rows in chunks (gradient_chunk) and adds the chunks in f32. G32 and G32ADD: the
+// chunks take the accumulators in turn, and the epilogue adds them up in registers, 128 a
+// lane, beside the next chunk's MMAs (16384 rows of 8 groups, 4096 x 3584 f32: 282 us, 275 with
+// 4096 rows in one accumulator; 1333 rows, 2816 x 2048: 20.0 and 19.0). GADD, whose groups are
+// short, and G16LONG: the first chunk stays in its accumulator, the others come into the second
+// one and are added to it, the last one on its way out.
 
 // adds the accumulator at tb to the one at ta: the columns that this warp will store, COLS of
 // every HALVES * COLS
@@ -634,7 +636,7 @@ __device__ __forceinline__ bool wgrad_epilogue(Tail& s, const RaggedParams& p, c
     return true;
 }
 
-// ---- G32: sums in registers ----------------------------------------------------------------
+// ---- G32, G32ADD: sums in registers ----------------------------------------------------------------
 // Lane = row n of dw; a warp has every other 32 columns of a tile.
 struct RowSums {
     uint32_t v[4][32];

@@ -3,10 +3,11 @@
 :class:`FewTokensLayer` is the expert layer for at most 32 tokens (buffers and
 one call); :class:`SharedExpert` a dense SwiGLU expert on E4M3 weights with
 block scales, :class:`DenseExpert` the same on 16-bit weights;
-:class:`FeedForward` the feed-forward half of a decoder layer from them: residual
-addition and norm, the routed experts, the shared expert added to them. As in :mod:`layer`, PyTorch only provides device memory and the
-stream, every step runs in libmoe.so, nothing synchronises with the host, and
-buffers are allocated once.
+:class:`FeedForward` the feed-forward half of a decoder layer from them:
+residual addition and norm, the routed experts, the shared expert added to
+them. As in :mod:`layer`, PyTorch only provides device memory and the stream,
+every step runs in libmoe.so, nothing synchronises with the host, and buffers
+are allocated once.
 """
 
 from __future__ import annotations
