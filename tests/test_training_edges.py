@@ -222,6 +222,32 @@ def test_f32_gradients_of_one_sign(moe, dev, act, rows, N, K, one):
     assert torch.all((dw.double() - ref).abs() <= ref * (640 * 2.0 ** -27 + (rows / 640 + 8) * F32))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act,f32,rows", [("bf16", True, 640), ("f16", True, 1280), ("bf16", True, 5120),
+                                          ("f16", False, 16384), ("f16", False, 131072), ("bf16", False, 131072)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_gradients_around_a_chunk(moe, dev, act, f32, rows, grouped):
+    """One row, a few and a unit of 16 less and more than a whole number of chunks, of one group in the split form and
+    of two in the pairs'."""
+    N, K, dt, code = 136, 72, plain.DT[act], moe.ACT_CODES[act]
+    g = torch.Generator(device=dev).manual_seed(rows)
+    dy, x = (torch.randn((rows + 40, n), generator=g, device=dev).to(dt) for n in (N, K))
+    dy[rows + 17:], x[rows + 17:] = math.nan, math.inf  # no group's
+    for n in (rows - 17, rows - 16, rows - 1, rows, rows + 1, rows + 16, rows + 17):
+        off = torch.tensor([0, n, n], dtype=torch.int32, device=dev) if grouped else None
+        E = 2 if grouped else 1
+        dw = torch.full((E, N, K), 7.0, dtype=torch.float32 if f32 else dt, device=dev)
+        moe.moe_ragged_wgrad(dy, x, code, off, rows + 40 if grouped else n, N, K, E, None, dw, f32)
+        d, xe = dy[:n].double(), x[:n].double()
+        ref, mag = d.T @ xe, d.abs().T @ xe.abs()
+        lost = mag * (min(n, 640 if f32 else 16384 if act == "f16" else 131072) * 2.0 ** -27 + 300 * F32)
+        if f32:
+            assert torch.all((dw[0].double() - ref).abs() <= lost), n
+        else:
+            plain.close(dw[0], ref.cpu(), act, lost.cpu())
+        assert not grouped or torch.all(dw[1] == 0)
+
+
 # ---- waits that run out -----------------------------------------------------------------------------
 
 @pytest.mark.gpu
